@@ -68,7 +68,9 @@ typedef enum {
   USP_ERR_BAD_POSITIONS = 6, /* device: a negative position id */
   USP_ERR_TIMEOUT = 7,       /* device: a bounded wait inside a kernel gave up */
   USP_ERR_CUDA = 8,          /* a CUDA runtime/driver call or launch failed */
-  USP_ERR_WORKSPACE = 9      /* workspace pointer null/misaligned or smaller than required */
+  USP_ERR_WORKSPACE = 9,     /* workspace pointer null/misaligned or smaller than required */
+  USP_ERR_BAD_MODS = 10      /* device: a bucket id outside [0, n_buckets), a negative prefix length, or
+                                fewer prefix lengths than documents */
 } usp_status;
 
 /* Static, human-readable name of a status code.  Never NULL. */
@@ -383,6 +385,98 @@ int usp_attn_bwd_dkdv(const usp_attn_params* params, const void* q, const void* 
 int usp_attn_bwd_dq(const usp_attn_params* params, const void* q, const void* k, const void* v,
                     const float* lse, const void* dO, void* dq, const void* ws, size_t ws_bytes,
                     int32_t* dev_status, usp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention with modified scores: usp_attn_fwd / usp_attn_bwd with a tanh cap,
+ * a bias by distance and a prefix mask.  For global query head h, token t, key
+ * u of t's document [a, b):
+ *     x = softmax_scale q_t.k_u - slopes[h] |t - u|
+ *         + rel_bias[h][buckets[clamp(t - u, -R, R) + R]]          R = max_distance
+ *     z = softcap tanh(x / softcap)   (z = x without a cap: the cap bounds the biased score)
+ * and the softmax runs over z and the head's sink logit (which is not capped).
+ * Visible keys: those of usp_attn_fwd, and with prefix_lens also every key u of
+ * the first prefix_lens[d] tokens of t's document d, whatever its order
+ * (t - u <= window_left still holds with a window).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  float softcap;               /* 0: none; else 2^-10 .. 2^10.  The absolute error of z is about
+                                  2.5e-7 softcap (fp32 tanh by one exponential and a reciprocal). */
+  const float* slopes;         /* device fp32 [Hq] (global heads), or NULL: no linear bias */
+  const float* rel_bias;       /* device fp32 [Hq][n_buckets], or NULL: no learned bias.  -inf hides keys
+                                  (only without a cap); a row that then sees nothing has O = 0, LSE = -inf */
+  const int32_t* buckets;      /* device int32 [2*max_distance + 1]: the bucket of distance t - u at index
+                                  t - u + max_distance; farther distances take the ends' buckets */
+  int n_buckets;               /* 1 .. 4097 */
+  int max_distance;            /* 1 .. 2048 */
+  int rel_bias_grad;           /* 1: the backward collects the gradient of rel_bias (a larger workspace) */
+  const int32_t* prefix_lens;  /* device int32 [n_prefix], one per document in cu_seqlens order, or NULL; more
+                                  than the document's length means all of it.  Needs causal = 1. */
+  int n_prefix;                /* at least the number of documents */
+} usp_score_mods;
+
+/* Host helper: a bucket map for usp_score_mods.buckets, into HOST memory
+ * int32 [2*max_distance + 1].  With n = |t - u| and K = n_buckets (half of them
+ * when bidirectional): distances n < K/2 have a bucket each, farther ones
+ *     K/2 + floor( (K - K/2) ln(n / (K/2)) / ln(max_distance / (K/2)) ),
+ * at most K - 1.  bidirectional: keys after the query (t - u < 0) take the upper
+ * half of the buckets; otherwise they take bucket 0 (they are masked in a causal
+ * model; with a prefix use a bidirectional map).
+ * Errors: USP_ERR_INVALID_ARG (null, K < 2, odd n_buckets when bidirectional,
+ * max_distance <= K/2), USP_ERR_UNSUPPORTED (max_distance > 2048, n_buckets > 4097). */
+int usp_rel_buckets_log(int n_buckets, int max_distance, int bidirectional, int32_t* buckets);
+
+/* Forward.  q, k, v, o, lse, dev_status and params as usp_attn_fwd (every
+ * io_layout; ring <= 1).
+ * dev_status may also get USP_ERR_BAD_MODS (the outputs are then unspecified).
+ * Every element of q, k and v must be finite, hidden keys' too: a tile's products
+ * take all its keys, hidden ones with weight 0.
+ * Errors: as usp_attn_fwd, and USP_ERR_INVALID_ARG (mods NULL, a softcap that is
+ * negative, infinite or NaN, fields of an absent rel_bias or prefix_lens that are
+ * not zero, a prefix without causal order), USP_ERR_UNSUPPORTED (softcap,
+ * max_distance or n_buckets outside their ranges, ring > 1). */
+int usp_attn_mod_fwd(const usp_attn_params* params, const usp_score_mods* mods, const void* q, const void* k,
+                     const void* v, void* o, float* lse, int32_t* dev_status, usp_stream_t stream);
+
+/* Workspace of the backward: the statistics of usp_attn_bwd, with rel_bias the
+ * bias rows by distance, and with rel_bias_grad partial sums of the scores'
+ * gradient by distance (8 (2R + 1) bytes per head and 32 tokens).  The fast form
+ * adds the stored dS blocks, as usp_attn_bwd_fast_workspace_bytes does; with a
+ * prefix or without causal order they cover every pair of a key tile and a query
+ * slice of a row.  0: invalid arguments, or (fast) S not a multiple of 128. */
+size_t usp_attn_mod_bwd_workspace_bytes(const usp_attn_params* params, const usp_score_mods* mods);
+size_t usp_attn_mod_bwd_fast_workspace_bytes(const usp_attn_params* params, const usp_score_mods* mods);
+
+/* Gradients of usp_attn_mod_fwd for the loss sum(O * dO): with P_tu = exp(z_tu - LSE_t)
+ *     dX_tu = P_tu (dO_t . v_u - D_t) (1 - tanh^2(x_tu / softcap))
+ *     dQ_t = scale sum_u dX_tu k_u,  dK_u = scale sum_t dX_tu q_t,  dV_u = sum_t P_tu dO_t
+ *     drel_bias[h][b] = sum of dX_tu over the pairs whose distance has bucket b
+ * and dsinks as in usp_attn_bwd.  slopes get no gradient.  D_t = dO_t . O_t is
+ * taken from the bf16 o, or, where a gradient in fp32 would show its rounding
+ * (rel_bias_grad, or dsinks with sinks), as sum_u P_tu (dO_t . v_u) in fp32 by a
+ * pass of its own over the scores.  drel_bias: fp32 [Hq][n_buckets], given exactly when mods->rel_bias_grad.
+ * Deterministic.  A workspace belongs to one call at a time: backward calls that
+ * may overlap (other streams, graphs launched at once) need one each.
+ * Errors: as usp_attn_mod_fwd and usp_attn_bwd. */
+int usp_attn_mod_bwd(const usp_attn_params* params, const usp_score_mods* mods, const void* q, const void* k,
+                     const void* v, const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                     float* dsinks, float* drel_bias, void* ws, size_t ws_bytes, int32_t* dev_status,
+                     usp_stream_t stream);
+
+/* Its phases, as those of usp_attn_bwd: the preprocess first (statistics, bias
+ * rows, cleared partial sums), then dK/dV, then dQ; head groups for the dK/dV
+ * and dQ passes with USP_IO_SEQ as there.  usp_attn_mod_bwd_rel_bias reduces the partial
+ * sums once the dK/dV passes of all heads are done. */
+int usp_attn_mod_bwd_preprocess(const usp_attn_params* params, const usp_score_mods* mods, const void* q,
+                                const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                                float* dsinks, void* ws, size_t ws_bytes, int32_t* dev_status, usp_stream_t stream);
+int usp_attn_mod_bwd_dkdv(const usp_attn_params* params, const usp_score_mods* mods, const void* q, const void* k,
+                          const void* v, const void* dO, void* dk, void* dv, const void* ws, size_t ws_bytes,
+                          int32_t* dev_status, usp_stream_t stream);
+int usp_attn_mod_bwd_dq(const usp_attn_params* params, const usp_score_mods* mods, const void* q, const void* k,
+                        const void* v, const void* dO, void* dq, const void* ws, size_t ws_bytes, int32_t* dev_status,
+                        usp_stream_t stream);
+int usp_attn_mod_bwd_rel_bias(const usp_attn_params* params, const usp_score_mods* mods, float* drel_bias, void* ws,
+                              size_t ws_bytes, usp_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -27,6 +27,7 @@ USP_ERR_BAD_POSITIONS = 6
 USP_ERR_TIMEOUT = 7
 USP_ERR_CUDA = 8
 USP_ERR_WORKSPACE = 9
+USP_ERR_BAD_MODS = 10
 
 EXPORTED = [
     "usp_status_string", "usp_version",
@@ -39,6 +40,9 @@ EXPORTED = [
     "usp_ring_fwd_merge", "usp_ring_grad_accumulate", "usp_attn_bwd_fast_workspace_bytes",
     "usp_a2a_pack_seq_to_head", "usp_a2a_unpack_seq_to_head", "usp_a2a_pack_head_to_seq",
     "usp_a2a_unpack_head_to_seq",
+    "usp_rel_buckets_log", "usp_attn_mod_fwd", "usp_attn_mod_bwd_workspace_bytes",
+    "usp_attn_mod_bwd_fast_workspace_bytes", "usp_attn_mod_bwd", "usp_attn_mod_bwd_preprocess",
+    "usp_attn_mod_bwd_dkdv", "usp_attn_mod_bwd_dq", "usp_attn_mod_bwd_rel_bias",
 ]
 
 USP_RING_FIRST = 1
@@ -61,6 +65,16 @@ class AttnParams(ctypes.Structure):
         ("io_layout", ctypes.c_int), ("ring", ctypes.c_int), ("ring_step", ctypes.c_int),
         ("head_first", ctypes.c_int), ("head_count", ctypes.c_int),
     ]
+
+
+class ScoreModsStruct(ctypes.Structure):
+    """usp_score_mods (include/usp.h).  ``tensors`` keeps what its pointers point at."""
+    _fields_ = [
+        ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("rel_bias", ctypes.c_void_p),
+        ("buckets", ctypes.c_void_p), ("n_buckets", ctypes.c_int), ("max_distance", ctypes.c_int),
+        ("rel_bias_grad", ctypes.c_int), ("prefix_lens", ctypes.c_void_p), ("n_prefix", ctypes.c_int),
+    ]
+    tensors = ()
 
 
 USP_IO_HEAD = 0
@@ -108,6 +122,20 @@ def load() -> ctypes.CDLL:
     for name in ("usp_a2a_pack_seq_to_head", "usp_a2a_unpack_seq_to_head", "usp_a2a_pack_head_to_seq",
                  "usp_a2a_unpack_head_to_seq"):
         getattr(L, name).argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, vp]
+    prm, mods = ctypes.POINTER(AttnParams), ctypes.POINTER(ScoreModsStruct)
+    L.usp_rel_buckets_log.argtypes = [i32, i32, i32, vp]
+    L.usp_attn_mod_fwd.argtypes = [prm, mods] + [vp] * 7
+    for name in ("usp_attn_mod_bwd_workspace_bytes", "usp_attn_mod_bwd_fast_workspace_bytes"):
+        getattr(L, name).restype = sz
+        getattr(L, name).argtypes = [prm, mods]
+    L.usp_attn_mod_bwd.argtypes = [prm, mods] + [vp] * 12 + [sz, vp, vp]
+    L.usp_attn_mod_bwd_preprocess.argtypes = [prm, mods] + [vp] * 8 + [sz, vp, vp]
+    L.usp_attn_mod_bwd_dkdv.argtypes = [prm, mods] + [vp] * 7 + [sz, vp, vp]
+    L.usp_attn_mod_bwd_dq.argtypes = [prm, mods] + [vp] * 6 + [sz, vp, vp]
+    L.usp_attn_mod_bwd_rel_bias.argtypes = [prm, mods, vp, vp, sz, vp]
+    for name in ("usp_rel_buckets_log", "usp_attn_mod_fwd", "usp_attn_mod_bwd", "usp_attn_mod_bwd_preprocess",
+                 "usp_attn_mod_bwd_dkdv", "usp_attn_mod_bwd_dq", "usp_attn_mod_bwd_rel_bias"):
+        getattr(L, name).restype = i32
     for name in ("usp_relayout_fwd", "usp_relayout_bwd", "usp_relayout_fwd_qkv",
                  "usp_cu_seqlens_from_position_ids", "usp_cu_seqlens_from_position_ids_noalloc",
                  "usp_attn_fwd", "usp_attn_bwd",
@@ -299,3 +327,128 @@ def usp_a2a_pack_head_to_seq(x_head, send, B, S_local, H, D, P, stream=None):
 
 def usp_a2a_unpack_head_to_seq(recv, x_local, B, S_local, H, D, P, stream=None):
     _a2a("usp_a2a_unpack_head_to_seq", recv, x_local, B, S_local, H, D, P, stream)
+
+
+# -- attention with modified scores ------------------------------------------
+def usp_rel_buckets_log(n_buckets: int, max_distance: int, bidirectional: bool) -> torch.Tensor:
+    """The bucket of every distance -max_distance..max_distance (int32 host tensor, for ``score_mods``): near
+    distances one bucket each, farther ones in buckets of geometrically growing width."""
+    out = torch.empty((2 * int(max_distance) + 1 if max_distance > 0 else 1,), dtype=torch.int32)
+    _check(load().usp_rel_buckets_log(int(n_buckets), int(max_distance), 1 if bidirectional else 0,
+                                      ctypes.c_void_p(out.data_ptr())), "usp_rel_buckets_log")
+    return out
+
+
+def score_mods(Hq, softcap=0.0, slopes=None, rel_bias=None, buckets=None, rel_bias_grad=False,
+               prefix_lens=None) -> ScoreModsStruct:
+    """usp_score_mods from tensors: slopes fp32 [Hq], rel_bias fp32 [Hq][n_buckets] with buckets int32
+    [2*max_distance + 1], prefix_lens int32 [documents]."""
+    sl, rb = _dev(slopes, "slopes", torch.float32), _dev(rel_bias, "rel_bias", torch.float32)
+    bk, pl = _dev(buckets, "buckets", torch.int32), _dev(prefix_lens, "prefix_lens", torch.int32)
+    if slopes is not None and slopes.numel() != Hq:
+        raise ValueError(f"slopes must hold one value per query head ({Hq}), got {slopes.numel()}")
+    if (rel_bias is None) != (buckets is None):
+        raise ValueError("rel_bias and buckets come together")
+    if rel_bias is not None:
+        if rel_bias.dim() != 2 or rel_bias.shape[0] != Hq or rel_bias.shape[1] < 1:
+            raise ValueError(f"rel_bias must be [{Hq}][n_buckets], got {tuple(rel_bias.shape)}")
+        if buckets.dim() != 1 or buckets.numel() < 3 or buckets.numel() % 2 != 1:
+            raise ValueError("buckets must be [2*max_distance + 1] with max_distance >= 1")
+    elif rel_bias_grad:
+        raise ValueError("rel_bias_grad needs a rel_bias")
+    if prefix_lens is not None and (prefix_lens.dim() != 1 or prefix_lens.numel() < 1):
+        raise ValueError("prefix_lens must be [documents]")
+    m = ScoreModsStruct(float(softcap), sl, rb, bk, 0 if rel_bias is None else rel_bias.shape[1],
+                        0 if buckets is None else (buckets.numel() - 1) // 2, 1 if rel_bias_grad else 0, pl,
+                        0 if prefix_lens is None else prefix_lens.numel())
+    m.tensors = tuple(t for t in (slopes, rel_bias, buckets, prefix_lens) if t is not None)
+    return m
+
+
+class _Call:
+    """The tensors of one call: their sizes against the parameters, one device, that device's stream."""
+
+    def __init__(self, prm: AttnParams, mods: ScoreModsStruct, stream):
+        self.prm, self.mods, self.stream, self.device = prm, mods, stream, None
+        P, tok = max(prm.P, 1), prm.B * prm.S
+        hk = prm.Hkv // P if prm.Hkv >= P else 1
+        kv_head = prm.io_layout != USP_IO_SEQ
+        self.sizes = {"q": tok * prm.Hq * prm.D, "kv": (P * hk if kv_head else prm.Hkv) * tok * prm.D,
+                      "lse": tok * prm.Hq, "heads": prm.Hq, "rel": prm.Hq * mods.n_buckets, None: None}
+        for t in mods.tensors:
+            self._on(t, "mods")
+
+    def _on(self, t, name):
+        if self.device is None:
+            self.device = t.device
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, other tensors of the call on {self.device}")
+
+    def __call__(self, t, name, dtype, size):
+        ptr = _dev(t, name, dtype)
+        if t is not None:
+            self._on(t, name)
+            if size is not None and t.numel() != self.sizes[size]:
+                raise ValueError(f"{name} has {t.numel()} elements, the parameters need {self.sizes[size]}")
+        return ptr
+
+    def run(self, where, *args):
+        with torch.cuda.device(self.device):
+            stream = _stream(torch.cuda.current_stream(self.device) if self.stream is None else self.stream)
+            _check(getattr(load(), where)(ctypes.byref(self.prm), ctypes.byref(self.mods), *args, stream), where)
+
+
+_BF, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def usp_attn_mod_fwd(params: AttnParams, mods: ScoreModsStruct, q, k, v, o, lse, dev_status=None, stream=None):
+    c = _Call(params, mods, stream)
+    c.run("usp_attn_mod_fwd", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"), c(o, "o", _BF, "q"),
+          c(lse, "lse", _F32, "lse"), c(dev_status, "dev_status", _I32, None))
+
+
+def usp_attn_mod_bwd_workspace_bytes(params: AttnParams, mods: ScoreModsStruct) -> int:
+    return int(load().usp_attn_mod_bwd_workspace_bytes(ctypes.byref(params), ctypes.byref(mods)))
+
+
+def usp_attn_mod_bwd_fast_workspace_bytes(params: AttnParams, mods: ScoreModsStruct) -> int:
+    return int(load().usp_attn_mod_bwd_fast_workspace_bytes(ctypes.byref(params), ctypes.byref(mods)))
+
+
+def usp_attn_mod_bwd(params: AttnParams, mods: ScoreModsStruct, q, k, v, o, lse, dO, dq, dk, dv, dsinks, drel_bias,
+                     ws, dev_status=None, stream=None):
+    c = _Call(params, mods, stream)
+    c.run("usp_attn_mod_bwd", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"), c(o, "o", _BF, "q"),
+          c(lse, "lse", _F32, "lse"), c(dO, "dO", _BF, "q"), c(dq, "dq", _BF, "q"),
+          c(dk, "dk", _BF, "kv"), c(dv, "dv", _BF, "kv"), c(dsinks, "dsinks", _F32, "heads"),
+          c(drel_bias, "drel_bias", _F32, "rel"), c(ws, "ws", None, None), ws.numel() * ws.element_size(),
+          c(dev_status, "dev_status", _I32, None))
+
+
+def usp_attn_mod_bwd_preprocess(params: AttnParams, mods: ScoreModsStruct, q, k, v, o, lse, dO, dsinks, ws,
+                                dev_status=None, stream=None):
+    c = _Call(params, mods, stream)
+    c.run("usp_attn_mod_bwd_preprocess", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"),
+          c(o, "o", _BF, "q"), c(lse, "lse", _F32, "lse"), c(dO, "dO", _BF, "q"), c(dsinks, "dsinks", _F32, "heads"), c(ws, "ws", None, None),
+          ws.numel() * ws.element_size(), c(dev_status, "dev_status", _I32, None))
+
+
+def usp_attn_mod_bwd_dkdv(params: AttnParams, mods: ScoreModsStruct, q, k, v, dO, dk, dv, ws, dev_status=None,
+                          stream=None):
+    c = _Call(params, mods, stream)
+    c.run("usp_attn_mod_bwd_dkdv", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"),
+          c(dO, "dO", _BF, "q"), c(dk, "dk", _BF, "kv"), c(dv, "dv", _BF, "kv"), c(ws, "ws", None, None),
+          ws.numel() * ws.element_size(), c(dev_status, "dev_status", _I32, None))
+
+
+def usp_attn_mod_bwd_dq(params: AttnParams, mods: ScoreModsStruct, q, k, v, dO, dq, ws, dev_status=None, stream=None):
+    c = _Call(params, mods, stream)
+    c.run("usp_attn_mod_bwd_dq", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"),
+          c(dO, "dO", _BF, "q"), c(dq, "dq", _BF, "q"), c(ws, "ws", None, None), ws.numel() * ws.element_size(),
+          c(dev_status, "dev_status", _I32, None))
+
+
+def usp_attn_mod_bwd_rel_bias(params: AttnParams, mods: ScoreModsStruct, drel_bias, ws, stream=None):
+    c = _Call(params, mods, stream)
+    c.run("usp_attn_mod_bwd_rel_bias", c(drel_bias, "drel_bias", _F32, "rel"), c(ws, "ws", None, None),
+          ws.numel() * ws.element_size())

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "usp_attn_common.cuh"
+#include "usp_attn_mods.cuh"
 #include "usp_internal.h"
 
 namespace usp {
@@ -202,6 +203,53 @@ int check_attn_params(const usp_attn_params* p) {
   return USP_OK;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes and layouts of an attention call with modified scores; `q` gets the
+// parameters with a window that spans whole rows taken for none.
+int check_mod_params(const usp_attn_params* p, const usp_score_mods* m, usp_attn_params& q) {
+  int rc = check_attn_params(p);
+  if (rc != USP_OK) return rc;
+  if (m == nullptr) return USP_ERR_INVALID_ARG;
+  if (!(m->softcap >= 0.f) || isinf(m->softcap)) return USP_ERR_INVALID_ARG;
+  if (m->softcap != 0.f && (m->softcap < 0x1p-10f || m->softcap > 0x1p10f)) return USP_ERR_UNSUPPORTED;
+  if (m->rel_bias != nullptr) {
+    if (m->buckets == nullptr || m->n_buckets < 1 || m->max_distance < 1) return USP_ERR_INVALID_ARG;
+    if (m->rel_bias_grad != 0 && m->rel_bias_grad != 1) return USP_ERR_INVALID_ARG;
+    if (m->max_distance > kMaxBiasDistance || m->n_buckets > 2 * kMaxBiasDistance + 1) return USP_ERR_UNSUPPORTED;
+  } else if (m->buckets != nullptr || m->n_buckets != 0 || m->max_distance != 0 || m->rel_bias_grad != 0) {
+    return USP_ERR_INVALID_ARG;
+  }
+  if (m->prefix_lens != nullptr ? m->n_prefix < 1 || p->causal == 0 : m->n_prefix != 0) return USP_ERR_INVALID_ARG;
+  if (!aligned4(m->slopes) || !aligned4(m->rel_bias) || !aligned4(m->buckets) || !aligned4(m->prefix_lens))
+    return USP_ERR_ALIGNMENT;
+  if (p->ring > 1) return USP_ERR_UNSUPPORTED;
+  q = *p;
+  if (q.window_left >= q.S) q.window_left = -1;
+  return USP_OK;
+}
+
+// The same for the phases of the backward, with their workspace.
+int check_mod_bwd(const usp_attn_params* p, const usp_score_mods* m, usp_attn_params& q, bool groups, const void* ws,
+                  size_t ws_bytes) {
+  int rc = check_mod_params(p, m, q);
+  if (rc != USP_OK) return rc;
+  if (!groups && p->head_count != 0) return USP_ERR_INVALID_ARG;  // head groups are for the dK/dV and dQ passes
+  if (p->io_layout == USP_IO_SEQ_KV_HEAD) return USP_ERR_UNSUPPORTED;  // a forward-only layout
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < attn_mod_bwd_ws_bytes(q, *m))
+    return USP_ERR_WORKSPACE;
+  return USP_OK;
+}
+
+template <class... T>
+bool any_null(const T*... p) {
+  return (... || (p == nullptr));
+}
+template <class... T>
+bool all_aligned16(const T*... p) {
+  return (... && aligned16(p));
+}
+
 }  // namespace
 
 extern "C" {
@@ -218,6 +266,7 @@ const char* usp_status_string(int s) {
     case USP_ERR_TIMEOUT: return "USP_ERR_TIMEOUT: a bounded wait inside a kernel gave up";
     case USP_ERR_CUDA: return "USP_ERR_CUDA: CUDA call or launch failed";
     case USP_ERR_WORKSPACE: return "USP_ERR_WORKSPACE: workspace missing, misaligned or too small";
+    case USP_ERR_BAD_MODS: return "USP_ERR_BAD_MODS: bucket id out of range, negative or missing prefix length";
     default: return "USP_ERR_UNKNOWN";
   }
 }
@@ -463,6 +512,117 @@ int usp_ring_grad_accumulate(const void* g_step, float* g_acc, void* g_out, size
   if (!aligned16(g_step) || (g_acc && !aligned16(g_acc)) || (g_out && !aligned16(g_out))) return USP_ERR_ALIGNMENT;
   if (n / 8 >= (1ull << 32)) return USP_ERR_UNSUPPORTED;
   return launch_ring_grad_accumulate(g_step, g_acc, g_out, n, flags, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---- attention with modified scores
+
+int usp_rel_buckets_log(int n_buckets, int max_distance, int bidirectional, int32_t* buckets) {
+  if (buckets == nullptr || (bidirectional != 0 && bidirectional != 1)) return USP_ERR_INVALID_ARG;
+  const int half = bidirectional ? n_buckets / 2 : n_buckets, exact = half / 2;
+  if (n_buckets < 2 || (bidirectional && n_buckets % 2 != 0) || half < 2 || max_distance <= exact)
+    return USP_ERR_INVALID_ARG;
+  if (max_distance > kMaxBiasDistance || n_buckets > 2 * kMaxBiasDistance + 1) return USP_ERR_UNSUPPORTED;
+  const double range = log(static_cast<double>(max_distance) / exact);
+  for (int d = -max_distance; d <= max_distance; ++d) {
+    const int n = d < 0 ? -d : d;
+    int b = n;
+    if (n >= exact) {
+      // the small term puts a distance that meets a border exactly into the upper bucket
+      b = exact + static_cast<int>(log(static_cast<double>(n) / exact) / range * (half - exact) + 1e-9);
+      if (b > half - 1) b = half - 1;
+    }
+    buckets[d + max_distance] = d >= 0 ? b : bidirectional ? b + half : 0;
+  }
+  return USP_OK;
+}
+
+int usp_attn_mod_fwd(const usp_attn_params* params, const usp_score_mods* mods, const void* q, const void* k,
+                     const void* v, void* o, float* lse, int32_t* dev_status, usp_stream_t stream) {
+  usp_attn_params prm;
+  int rc = check_mod_params(params, mods, prm);
+  if (rc != USP_OK) return rc;
+  if (params->head_count != 0) return USP_ERR_INVALID_ARG;  // head groups are for the dK/dV and dQ passes
+  if (any_null(q, k, v, o, lse)) return USP_ERR_INVALID_ARG;
+  if (!all_aligned16(q, k, v, o, lse)) return USP_ERR_ALIGNMENT;
+  return launch_attn_mod_fwd(prm, *mods, q, k, v, o, lse, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t usp_attn_mod_bwd_workspace_bytes(const usp_attn_params* params, const usp_score_mods* mods) {
+  usp_attn_params prm;
+  return check_mod_params(params, mods, prm) != USP_OK ? 0 : attn_mod_bwd_ws_bytes(prm, *mods);
+}
+
+size_t usp_attn_mod_bwd_fast_workspace_bytes(const usp_attn_params* params, const usp_score_mods* mods) {
+  usp_attn_params prm;
+  return check_mod_params(params, mods, prm) != USP_OK ? 0 : attn_mod_bwd_fast_ws_bytes(prm, *mods);
+}
+
+int usp_attn_mod_bwd_preprocess(const usp_attn_params* params, const usp_score_mods* mods, const void* q,
+                                const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                                float* dsinks, void* ws, size_t ws_bytes, int32_t* dev_status, usp_stream_t stream) {
+  usp_attn_params prm;
+  int rc = check_mod_bwd(params, mods, prm, false, ws, ws_bytes);
+  if (rc != USP_OK) return rc;
+  if (any_null(q, k, v, o, lse, dO)) return USP_ERR_INVALID_ARG;
+  if (!all_aligned16(q, k, v, o, lse, dO)) return USP_ERR_ALIGNMENT;
+  return launch_attn_mod_bwd_preprocess(prm, *mods, q, k, v, o, lse, dO, prm.sinks ? dsinks : nullptr, ws, dev_status,
+                                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+int usp_attn_mod_bwd_dkdv(const usp_attn_params* params, const usp_score_mods* mods, const void* q, const void* k,
+                          const void* v, const void* dO, void* dk, void* dv, const void* ws, size_t ws_bytes,
+                          int32_t* dev_status, usp_stream_t stream) {
+  usp_attn_params prm;
+  int rc = check_mod_bwd(params, mods, prm, true, ws, ws_bytes);
+  if (rc != USP_OK) return rc;
+  if (any_null(q, k, v, dO, dk, dv)) return USP_ERR_INVALID_ARG;
+  if (!all_aligned16(q, k, v, dO, dk, dv)) return USP_ERR_ALIGNMENT;
+  return launch_attn_mod_bwd_dkdv(prm, *mods, q, k, v, dO, dk, dv, ws, ws_bytes, dev_status,
+                                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+int usp_attn_mod_bwd_dq(const usp_attn_params* params, const usp_score_mods* mods, const void* q, const void* k,
+                        const void* v, const void* dO, void* dq, const void* ws, size_t ws_bytes, int32_t* dev_status,
+                        usp_stream_t stream) {
+  usp_attn_params prm;
+  int rc = check_mod_bwd(params, mods, prm, true, ws, ws_bytes);
+  if (rc != USP_OK) return rc;
+  if (any_null(q, k, v, dO, dq)) return USP_ERR_INVALID_ARG;
+  if (!all_aligned16(q, k, v, dO, dq)) return USP_ERR_ALIGNMENT;
+  return launch_attn_mod_bwd_dq(prm, *mods, q, k, v, dO, dq, ws, ws_bytes, dev_status,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+int usp_attn_mod_bwd_rel_bias(const usp_attn_params* params, const usp_score_mods* mods, float* drel_bias, void* ws,
+                              size_t ws_bytes, usp_stream_t stream) {
+  usp_attn_params prm;
+  int rc = check_mod_bwd(params, mods, prm, false, ws, ws_bytes);
+  if (rc != USP_OK) return rc;
+  if (drel_bias == nullptr || mods->rel_bias == nullptr || !mods->rel_bias_grad) return USP_ERR_INVALID_ARG;
+  if (!aligned4(drel_bias)) return USP_ERR_ALIGNMENT;
+  return launch_attn_mod_bwd_rel_bias(prm, *mods, drel_bias, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int usp_attn_mod_bwd(const usp_attn_params* params, const usp_score_mods* mods, const void* q, const void* k,
+                     const void* v, const void* o, const float* lse, const void* dO, void* dq, void* dk,
+                     void* dv, float* dsinks, float* drel_bias, void* ws, size_t ws_bytes, int32_t* dev_status, usp_stream_t stream) {
+  // every phase's checks before the first launch
+  usp_attn_params prm;
+  int rc = check_mod_bwd(params, mods, prm, false, ws, ws_bytes);
+  if (rc != USP_OK) return rc;
+  if (any_null(q, k, v, o, lse, dO, dq, dk, dv)) return USP_ERR_INVALID_ARG;
+  if (!all_aligned16(q, k, v, o, lse, dO, dq, dk, dv)) return USP_ERR_ALIGNMENT;
+  const bool rel = mods->rel_bias != nullptr && mods->rel_bias_grad;
+  if (rel != (drel_bias != nullptr)) return USP_ERR_INVALID_ARG;
+  if (!aligned4(drel_bias)) return USP_ERR_ALIGNMENT;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if ((rc = launch_attn_mod_bwd_preprocess(prm, *mods, q, k, v, o, lse, dO, prm.sinks ? dsinks : nullptr, ws,
+                                           dev_status, st)) != USP_OK)
+    return rc;
+  if ((rc = launch_attn_mod_bwd_dkdv(prm, *mods, q, k, v, dO, dk, dv, ws, ws_bytes, dev_status, st)) != USP_OK)
+    return rc;
+  if (rel && (rc = launch_attn_mod_bwd_rel_bias(prm, *mods, drel_bias, ws, st)) != USP_OK) return rc;
+  return launch_attn_mod_bwd_dq(prm, *mods, q, k, v, dO, dq, ws, ws_bytes, dev_status, st);
 }
 
 }  // extern "C"

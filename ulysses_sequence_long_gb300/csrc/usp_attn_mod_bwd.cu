@@ -1,0 +1,441 @@
+// usp_attn_mod_bwd.cu — the backward with modified scores: the kernels of
+// usp_attn_bwd.cuh with the steps of usp_attn_mods.cuh compiled in, the rows of
+// the bias by distance, and the reduction of the table's gradient.
+//
+// Workspace: the statistics of the plain backward | the bias rows by distance
+// [Hq][tab_len(R)] | partial sums of dX by distance [Hq][n_kb][2][2R+1] (one row
+// for each head, 32-key block and half of a query slice; the dK/dV pass writes
+// them) | their sums over key blocks [Hq][splits][2R+1] | the stored dS blocks.
+#include "usp_attn_bwd.cuh"
+
+namespace usp {
+
+Mods make_mods(const usp_score_mods& m);
+
+namespace bwd {
+
+// --------------------------------------------------------------- delta
+// The row statistics with D_t = sum_u P_tu (dO_t . v_u) summed in fp32 over the
+// scores themselves (D_t = dO_t . O_t by the definition of O).  O reaches the
+// backward as bf16 and from P rounded to bf16, each good to 2^-9: invisible in
+// bf16 gradients, but the fp32 gradients of the sinks and of the bias table sum
+// over all tokens and would carry it (relative error 1e-3 measured; with this
+// pass under 1e-5).  It costs two of the five products of the backward.
+//
+// CTA = (query head, 128 rows), as the dQ pass: Q and dO in TMEM as A operands,
+// 128-key tiles of K and V through a shared-memory ring, no output tile.  S has
+// two TMEM buffers, so S_{n+1} is issued while the compute warps turn S_n into
+// P_n; dP_{n+1} follows once they have read dP_n.
+// TMEM: S [0,128) and [128,256), dP [256,384), Q [384, 384+D/2), dO [.., 384+D).
+struct BarsD {
+  uint64_t qd_ready;
+  uint64_t k_full[8], v_full[8], kv_empty[8];
+  uint64_t s_full[2], s_free[2], dp_full, dp_free, mma_done;
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kDeltaRed = 512;  // byte offset of the row sums of group 1 after the barriers
+static_assert(sizeof(BarsD) <= kDeltaRed && kDeltaRed + kBM * 4 <= 1024, "delta barrier block");
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    delta_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs p,
+                 const __nv_bfloat16* __restrict__ q_in, const __nv_bfloat16* __restrict__ do_in,
+                 const float* __restrict__ lse, float* __restrict__ stats, int bsp, int n_tiles, Mods mods) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  BarsD* bars = reinterpret_cast<BarsD*>(smem + C::B_BAR);
+  float* red = reinterpret_cast<float*>(smem + C::B_BAR + kDeltaRed);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const int qt = n_tiles - 1 - static_cast<int>(blockIdx.x) / p.Hq;
+  const int hg = static_cast<int>(blockIdx.x) % p.Hq;
+  const int r = hg / p.hq, j = hg % p.hq;
+  const HeadRef qh = q_head_ref(p, r, j), kvh = kv_head_ref(p, r, j / p.G);
+  const int t0 = qt * kBM;
+
+  const int n_docs = checked_docs(p);
+  if (n_docs == 0) return;
+  int lo, hi;
+  key_range(p, mods, n_docs, t0, min(t0 + kBM, p.BS) - 1, lo, hi);
+  if (p.seq_io) lo &= ~(kBN - 1);  // key tiles inside one rank's shard
+  const int n_kv = hi > lo ? (hi - lo + kBN - 1) / kBN : 0;
+
+  if (tid == 0) {
+    mbar_init(&bars->qd_ready, 8);
+    for (int s = 0; s < C::KST; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->kv_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->s_free[b], 8);
+    }
+    mbar_init(&bars->dp_full, 1);
+    mbar_init(&bars->dp_free, 8);
+    mbar_init(&bars->mma_done, 1);
+    bars->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&bars->tmem, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  volatile int* abort = &bars->abort;
+  const uint32_t sbase = smem_u32(smem);
+  constexpr uint32_t T_DP = 256, T_Q = 384, T_DO = T_Q + D / 2;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tmap(&tk);
+      prefetch_tmap(&tv);
+      int issued = 0;
+      for (int n = 0; n < n_kv; ++n) {
+        const int s = n % C::KST;
+        if (n >= C::KST && !mbar_wait(&bars->kv_empty[s], ((n / C::KST) - 1) & 1, abort, p.status)) break;
+        const int kv0 = lo + n * kBN;
+        mbar_arrive_expect_tx(&bars->k_full[s], C::TILE);
+        for (int c = 0; c < C::NCH; ++c)
+          tma_load_rows(smem + C::B_K + s * C::TILE + c * kAtomBytes, &tk, &bars->k_full[s], p, c, kvh, kv0);
+        mbar_arrive_expect_tx(&bars->v_full[s], C::TILE);
+        for (int c = 0; c < C::NCH; ++c)
+          tma_load_rows(smem + C::B_V + s * C::TILE + c * kAtomBytes, &tv, &bars->v_full[s], p, c, kvh, kv0);
+        issued = n + 1;
+      }
+      // never leave the CTA with copies still landing in its shared memory
+      for (int n = max(0, issued - C::KST); n < issued; ++n) {
+        mbar_wait(&bars->k_full[n % C::KST], (n / C::KST) & 1, abort, p.status);
+        mbar_wait(&bars->v_full[n % C::KST], (n / C::KST) & 1, abort, p.status);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16(kBM, kBN, false, false);  // [128 rows x 128 keys], K = D
+      auto issue_s = [&](int n) -> bool {
+        const int s = n % C::KST, b = n & 1;
+        if (!mbar_wait(&bars->k_full[s], (n / C::KST) & 1, abort, p.status)) return false;
+        if (n >= 2 && !mbar_wait(&bars->s_free[b], ((n >> 1) - 1) & 1, abort, p.status)) return false;
+        tc_fence_after();
+        const uint32_t ka = sbase + C::B_K + s * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ts(tmem + b * kBN, tmem + T_Q + kk * 8, kmajor_desc(ka, kAtomBytes, kk), id_s, kk > 0);
+        mma_commit(&bars->s_full[b]);
+        return true;
+      };
+      auto issue_dp = [&](int n) -> bool {
+        const int s = n % C::KST;
+        if (!mbar_wait(&bars->v_full[s], (n / C::KST) & 1, abort, p.status)) return false;
+        if (n >= 1 && !mbar_wait(&bars->dp_free, (n - 1) & 1, abort, p.status)) return false;
+        tc_fence_after();
+        const uint32_t va = sbase + C::B_V + s * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ts(tmem + T_DP, tmem + T_DO + kk * 8, kmajor_desc(va, kAtomBytes, kk), id_s, kk > 0);
+        mma_commit(&bars->dp_full);
+        mma_commit(&bars->kv_empty[s]);  // S_n was issued before: K_n and V_n are read
+        return true;
+      };
+      bool ok = mbar_wait(&bars->qd_ready, 0, abort, p.status);
+      if (ok && n_kv > 0) ok = issue_s(0);
+      for (int n = 0; n < n_kv && ok; ++n) {
+        if (n + 1 < n_kv) ok = issue_s(n + 1);
+        if (ok) ok = issue_dp(n);
+      }
+      mma_commit(&bars->mma_done);
+      mbar_wait(&bars->mma_done, 0, abort, p.status);
+    }
+  } else {
+    // ------------------------------------------------------------ compute
+    const int grp = warp >> 2;  // key columns [64*grp, 64*grp + 64) of every tile
+    const int row = (warp & 3) * 32 + lane;
+    const int t = t0 + row;
+    const bool row_ok = t < p.BS;
+    const uint32_t lb = tmem + ((static_cast<uint32_t>(warp & 3) * 32) << 16);
+    {
+      const size_t off = row_offset(p, qh, p.hq, p.Hq, row_ok ? t : 0, D);
+      row_to_tmem<D>(lb + (grp == 0 ? T_Q : T_DO), (grp == 0 ? q_in : do_in) + off, row_ok);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->qd_ready);
+    }
+    int a = 0, b = 0, pe = 0;
+    float nlse2 = -INFINITY;
+    if (row_ok) {
+      doc_bounds(p, mods, n_docs, t, a, b, pe);
+      const float l = __ldg(lse + stat_index(p, r, j, t));
+      nlse2 = l == -INFINITY ? l : l * -kLog2e;  // (the statistics' plane 0, see preprocess_kernel)
+    }
+    int vlo, vhi;  // the row's visible keys
+    visible_keys(mods, t, a, b, pe, p.causal, p.window_left, row_ok, vlo, vhi);
+    const float* tab =
+        mods.table != nullptr ? mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad : nullptr;
+    const float slope2 = mods.slopes != nullptr ? __ldg(mods.slopes + hg) * kLog2E : 0.f;
+    uint64_t acc2[4] = {0, 0, 0, 0};  // 8 independent partial sums, two per register
+    bool ok = true;
+    for (int n = 0; n < n_kv && ok; ++n) {
+      const int k0 = lo + n * kBN + grp * 64;  // first key of this group's columns
+      if (!(ok = mbar_wait(&bars->s_full[n & 1], (n >> 1) & 1, abort, p.status))) break;
+      tc_fence_after();
+      float x[64];
+      tmem_ld_cols<64>(lb + (n & 1) * kBN + grp * 64, x);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->s_free[n & 1]);
+      const int d0 = t - k0, dw = d0 - lane;
+      Affine f = add_bias<64, -1>(x, tab, mods.R, slope2, d0, dw - 63, dw + 31, p.scale_log2);
+      if (mods.cap > 0.f) {
+        cap_scores(x, f, mods.cap);
+        f = {mods.cap * kLog2E, 0.f};
+      }
+      const int c_lo = vlo - k0, c_hi = vhi - k0;
+      if (!(c_lo <= 0 && c_hi >= 63)) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (c < c_lo || c > c_hi) x[c] = -INFINITY;
+      }
+      const uint64_t sc2 = f2_pack(f.sc, f.sc), nl2 = f2_pack(nlse2 + f.off, nlse2 + f.off);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        const float2 e = f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sc2, nl2));
+        x[c] = ex2(e.x);
+        x[c + 1] = ex2(e.y);
+      }
+      if (!(ok = mbar_wait(&bars->dp_full, n & 1, abort, p.status))) break;
+      tc_fence_after();
+      float dp[64];
+      tmem_ld_cols<64>(lb + T_DP + grp * 64, dp);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->dp_free);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2)
+        acc2[(c >> 1) & 3] = f2_fma(f2_pack(x[c], x[c + 1]), f2_pack(dp[c], dp[c + 1]), acc2[(c >> 1) & 3]);
+    }
+    const float2 s01 = f2_unpack(f2_add(acc2[0], acc2[1])), s23 = f2_unpack(f2_add(acc2[2], acc2[3]));
+    const float sum = (s01.x + s01.y) + (s23.x + s23.y);
+    // the two key halves of a row meet; every compute warp comes here, also after a wait that gave up
+    if (grp == 1) red[row] = sum;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (grp == 0 && row_ok) {
+      stats[plane_index(bsp, p.hq, r, j, 0, t)] = nlse2;
+      stats[plane_index(bsp, p.hq, r, j, 1, t)] = sum + red[row];
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace bwd
+
+namespace {
+
+template <int D>
+int run_delta(const AttnArgs& a, const Mods& m, const void* q, const void* k, const void* v, const void* dO,
+              const float* lse, float* stats, cudaStream_t st) {
+  using C = bwd::Cfg<D>;
+  CUtensorMap tk, tv;
+  int rc;
+  if ((rc = make_rows_tmap(&tk, k, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
+  if ((rc = make_rows_tmap(&tv, v, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
+  if (cudaFuncSetAttribute(bwd::delta_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::B_SMEM) != cudaSuccess)
+    return USP_ERR_CUDA;
+  const int n_tiles = (a.BS + kBM - 1) / kBM;
+  bwd::delta_kernel<D><<<static_cast<unsigned>(n_tiles) * a.Hq, bwd::kThreads, C::B_SMEM, st>>>(
+      tk, tv, a, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(dO), lse, stats,
+      stats_row_pitch(a.BS), n_tiles, m);
+  return check_launch();
+}
+
+constexpr int kRelThreads = 256;
+constexpr int kRelRows = 64;    // partial rows that one block of the first reduction sums
+constexpr int kRelSplits = 64;  // most blocks per head
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct Layout {
+  size_t table, partial, sums, ds, total;  // byte offsets; total without the stored dS
+  int n_kb, n_rows, splits;
+};
+
+Layout mod_layout(const usp_attn_params& p, const usp_score_mods& m) {
+  Layout L{};
+  L.table = L.partial = L.sums = attn_bwd_ws_bytes(p);
+  L.n_kb = (p.B * p.S + 31) / 32;
+  L.n_rows = 2 * L.n_kb;
+  L.splits = (L.n_rows + kRelRows - 1) / kRelRows;
+  if (L.splits > kRelSplits) L.splits = kRelSplits;
+  size_t end = L.table;
+  if (m.rel_bias != nullptr) {
+    const size_t row = 2 * static_cast<size_t>(m.max_distance) + 1;
+    end = L.partial = end + up256(sizeof(float) * p.Hq * tab_len(m.max_distance));
+    if (m.rel_bias_grad) {
+      end = L.sums = end + up256(sizeof(float) * p.Hq * static_cast<size_t>(L.n_rows) * row);
+      end += up256(sizeof(float) * p.Hq * static_cast<size_t>(L.splits) * row);
+    }
+  }
+  L.ds = L.total = end;
+  return L;
+}
+
+// A prefix, or no causal order, lets a key be seen by earlier rows: the stored
+// dS then takes every (key tile, query slice) pair.
+bool every_slice(const usp_attn_params& p, const usp_score_mods& m) { return !p.causal || m.prefix_lens != nullptr; }
+
+size_t mod_ds_bytes(const usp_attn_params& p, const usp_score_mods& m) {
+  bwd::DsGeom g;
+  long long n;
+  return ds_geom(p, g, n, every_slice(p, m)) ? static_cast<size_t>(n) * kBN * bwd::kSL * 2 : 0;
+}
+
+// Rows by distance in the log2 domain; one block per head.
+__global__ void __launch_bounds__(kRelThreads) rel_expand_kernel(Mods m, float* __restrict__ table, int32_t* status) {
+  const int n = tab_len(m.R);
+  for (int e = threadIdx.x; e < n; e += kRelThreads)
+    table[static_cast<size_t>(blockIdx.x) * n + e] = table_entry(m, blockIdx.x, e, status);
+}
+
+// Sums a split's partial rows of a head: thread = distance, rows in order.
+__global__ void __launch_bounds__(kRelThreads)
+    rel_sum_kernel(const float* __restrict__ partial, float* __restrict__ sums, int n_rows, int per, int row) {
+  const int h = blockIdx.x, s = blockIdx.y;
+  const int r0 = s * per, r1 = min(n_rows, r0 + per);
+  const float* src = partial + static_cast<size_t>(h) * n_rows * row;
+  for (int c = threadIdx.x; c < row; c += kRelThreads) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    int r = r0;
+    for (; r + 4 <= r1; r += 4)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] += __ldg(src + static_cast<size_t>(r + e) * row + c);
+    for (; r < r1; ++r) acc[0] += __ldg(src + static_cast<size_t>(r) * row + c);
+    sums[(static_cast<size_t>(h) * gridDim.y + s) * row + c] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+  }
+}
+
+// The splits' sums of a head, then its buckets: thread = bucket, distances in
+// order (no atomics: the result does not depend on the schedule).
+__global__ void __launch_bounds__(kRelThreads)
+    rel_bucket_kernel(Mods m, const float* __restrict__ sums, float* __restrict__ drel, int splits) {
+  extern __shared__ float by_dist[];
+  const int h = blockIdx.x, row = 2 * m.R + 1;
+  const float* src = sums + static_cast<size_t>(h) * splits * row;
+  for (int c = threadIdx.x; c < row; c += kRelThreads) {
+    float acc = 0.f;
+    for (int s = 0; s < splits; ++s) acc += __ldg(src + static_cast<size_t>(s) * row + c);
+    by_dist[c] = acc;
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < m.n_buckets; b += kRelThreads) {
+    float acc = 0.f;
+    for (int c = 0; c < row; ++c)
+      if (min(max(__ldg(m.buckets + c), 0), m.n_buckets - 1) == b) acc += by_dist[c];
+    drel[static_cast<size_t>(h) * m.n_buckets + b] = acc;
+  }
+}
+
+Mods bwd_mods(const usp_attn_params& p, const usp_score_mods& sm, const void* ws) {
+  Mods m = make_mods(sm);
+  const Layout L = mod_layout(p, sm);
+  uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(ws));
+  m.n_kb = L.n_kb;
+  if (sm.rel_bias != nullptr) {
+    m.table = reinterpret_cast<const float*>(base + L.table);
+    if (sm.rel_bias_grad) m.partial = reinterpret_cast<float*>(base + L.partial);
+  }
+  return m;
+}
+
+// The stored-dS region of the workspace, or null when it does not hold one.
+void* mod_ds_region(const usp_attn_params& p, const usp_score_mods& m, const void* ws, size_t ws_bytes,
+                    bwd::DsGeom& g, long long& n) {
+  const size_t need = mod_ds_bytes(p, m), at = mod_layout(p, m).ds;
+  if (need == 0 || ws_bytes < at + need || !ds_geom(p, g, n, every_slice(p, m))) return nullptr;
+  return static_cast<uint8_t*>(const_cast<void*>(ws)) + at;
+}
+
+}  // namespace
+
+size_t attn_mod_bwd_ws_bytes(const usp_attn_params& p, const usp_score_mods& m) { return mod_layout(p, m).total; }
+
+size_t attn_mod_bwd_fast_ws_bytes(const usp_attn_params& p, const usp_score_mods& m) {
+  const size_t ds = mod_ds_bytes(p, m);
+  return ds == 0 ? 0 : mod_layout(p, m).total + ds;
+}
+
+int launch_attn_mod_bwd_preprocess(const usp_attn_params& p, const usp_score_mods& sm, const void* q, const void* k,
+                                   const void* v, const void* o, const float* lse, const void* dO, float* dsinks,
+                                   void* ws, int32_t* status, cudaStream_t st) {
+  const Mods m = bwd_mods(p, sm, ws);
+  if (sm.rel_bias != nullptr) {
+    const Layout L = mod_layout(p, sm);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    rel_expand_kernel<<<p.Hq, kRelThreads, 0, st>>>(m, reinterpret_cast<float*>(base + L.table), status);
+    if (check_launch() != USP_OK) return USP_ERR_CUDA;
+    // distances that no chunk reaches stay at zero
+    if (sm.rel_bias_grad && cudaMemsetAsync(base + L.partial, 0, L.sums - L.partial, st) != cudaSuccess)
+      return USP_ERR_CUDA;
+  }
+  const bool exact_delta = dsinks != nullptr || m.partial != nullptr;  // a gradient in fp32 hangs on D
+  if (!exact_delta) return run_preprocess(p, o, lse, dO, nullptr, ws, status, st);
+  const AttnArgs a = make_args(p, status);
+  float* stats = static_cast<float*>(ws);
+  const int rc = p.D == 128 ? run_delta<128>(a, m, q, k, v, dO, lse, stats, st)
+                            : run_delta<64>(a, m, q, k, v, dO, lse, stats, st);
+  if (rc != USP_OK || dsinks == nullptr) return rc;
+  bwd::dsink_kernel<<<a.P * a.hq, 256, 0, st>>>(stats, dsinks, a, stats_row_pitch(a.BS));
+  return check_launch();
+}
+
+int launch_attn_mod_bwd_dkdv(const usp_attn_params& p, const usp_score_mods& sm, const void* q, const void* k,
+                             const void* v, const void* dO, void* dk, void* dv, const void* ws, size_t ws_bytes,
+                             int32_t* status, cudaStream_t st) {
+  const AttnArgs a = make_args(p, status);
+  const Mods m = bwd_mods(p, sm, ws);
+  const float* stats = static_cast<const float*>(ws);
+  bwd::DsGeom g{};
+  long long nb = 0;
+  void* ds = mod_ds_region(p, sm, ws, ws_bytes, g, nb);
+  if (p.D == 128) return run_grad_pass<128>(false, a, m, q, k, v, dO, nullptr, dk, dv, stats, ds, g, nb, st);
+  return run_grad_pass<64>(false, a, m, q, k, v, dO, nullptr, dk, dv, stats, ds, g, nb, st);
+}
+
+int launch_attn_mod_bwd_dq(const usp_attn_params& p, const usp_score_mods& sm, const void* q, const void* k,
+                           const void* v, const void* dO, void* dq, const void* ws, size_t ws_bytes, int32_t* status,
+                           cudaStream_t st) {
+  const AttnArgs a = make_args(p, status);
+  const Mods m = bwd_mods(p, sm, ws);
+  const float* stats = static_cast<const float*>(ws);
+  bwd::DsGeom g{};
+  long long nb = 0;
+  void* ds = mod_ds_region(p, sm, ws, ws_bytes, g, nb);
+  if (p.D == 128) return run_grad_pass<128>(true, a, m, q, k, v, dO, dq, nullptr, nullptr, stats, ds, g, nb, st);
+  return run_grad_pass<64>(true, a, m, q, k, v, dO, dq, nullptr, nullptr, stats, ds, g, nb, st);
+}
+
+int launch_attn_mod_bwd_rel_bias(const usp_attn_params& p, const usp_score_mods& sm, float* drel_bias, void* ws,
+                                 cudaStream_t st) {
+  const Layout L = mod_layout(p, sm);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  const int row = 2 * sm.max_distance + 1, per = (L.n_rows + L.splits - 1) / L.splits;
+  float* sums = reinterpret_cast<float*>(base + L.sums);
+  rel_sum_kernel<<<dim3(p.Hq, L.splits), kRelThreads, 0, st>>>(reinterpret_cast<const float*>(base + L.partial), sums,
+                                                               L.n_rows, per, row);
+  if (check_launch() != USP_OK) return USP_ERR_CUDA;
+  rel_bucket_kernel<<<p.Hq, kRelThreads, row * sizeof(float), st>>>(make_mods(sm), sums, drel_bias, L.splits);
+  return check_launch();
+}
+
+}  // namespace usp

@@ -1,0 +1,30 @@
+// usp_attn_mod_fwd.cu — the launch of the attention forward with modified
+// scores (the kernel of usp_attn_fwd.cuh with the steps of usp_attn_mods.cuh
+// compiled in).
+#include "usp_attn_fwd.cuh"
+
+namespace usp {
+
+Mods make_mods(const usp_score_mods& m) {
+  Mods x{};
+  x.cap = m.softcap;
+  x.slopes = m.slopes;
+  x.rel_bias = m.rel_bias;
+  x.buckets = m.buckets;
+  x.n_buckets = m.n_buckets;
+  x.R = m.rel_bias != nullptr ? m.max_distance : 0;
+  x.prefix = m.prefix_lens;
+  x.n_prefix = m.n_prefix;
+  return x;
+}
+
+int launch_attn_mod_fwd(const usp_attn_params& prm, const usp_score_mods& sm, const void* q, const void* k,
+                        const void* v, void* o, float* lse, int32_t* status, cudaStream_t st) {
+  const AttnArgs a = make_fwd_args(prm, status);
+  const Mods m = make_mods(sm);
+  const int tab_bytes = m.rel_bias != nullptr ? tab_len(m.R) * static_cast<int>(sizeof(float)) : 0;
+  if (prm.D == 128) return run_fwd<128>(a, m, tab_bytes, q, k, v, o, lse, st);
+  return run_fwd<64>(a, m, tab_bytes, q, k, v, o, lse, st);
+}
+
+}  // namespace usp

@@ -72,4 +72,21 @@ int launch_attn_bwd_dkdv(const usp_attn_params& p, const void* q, const void* k,
 int launch_attn_bwd_dq(const usp_attn_params& p, const void* q, const void* k, const void* v, const float* lse,
                        const void* dO, void* dq, const void* ws, size_t ws_bytes, int32_t* status, cudaStream_t st);
 
+// Attention with modified scores (usp_attn_mod_*).
+int launch_attn_mod_fwd(const usp_attn_params& p, const usp_score_mods& m, const void* q, const void* k, const void* v,
+                        void* o, float* lse, int32_t* status, cudaStream_t st);
+size_t attn_mod_bwd_ws_bytes(const usp_attn_params& p, const usp_score_mods& m);
+size_t attn_mod_bwd_fast_ws_bytes(const usp_attn_params& p, const usp_score_mods& m);  // 0: no stored-dS path
+int launch_attn_mod_bwd_preprocess(const usp_attn_params& p, const usp_score_mods& m, const void* q, const void* k,
+                                   const void* v, const void* o, const float* lse, const void* dO, float* dsinks,
+                                   void* ws, int32_t* status, cudaStream_t st);
+int launch_attn_mod_bwd_dkdv(const usp_attn_params& p, const usp_score_mods& m, const void* q, const void* k,
+                             const void* v, const void* dO, void* dk, void* dv, const void* ws, size_t ws_bytes,
+                             int32_t* status, cudaStream_t st);
+int launch_attn_mod_bwd_dq(const usp_attn_params& p, const usp_score_mods& m, const void* q, const void* k,
+                           const void* v, const void* dO, void* dq, const void* ws, size_t ws_bytes, int32_t* status,
+                           cudaStream_t st);
+int launch_attn_mod_bwd_rel_bias(const usp_attn_params& p, const usp_score_mods& m, float* drel_bias, void* ws,
+                                 cudaStream_t st);
+
 }  // namespace usp

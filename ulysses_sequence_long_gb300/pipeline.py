@@ -32,7 +32,7 @@ the library's kernels.
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 from typing import Optional
 
 import torch
@@ -67,8 +67,40 @@ class Shape:
         return (self.S // self.P) % 128 == 0
 
 
+@dataclass
+class ScoreMods:
+    """What modifies the scores of a layer (``usp_score_mods``): a tanh cap, a
+    linear bias by distance (slopes fp32 ``[Hq]``), a learned bias by distance
+    bucket (rel_bias fp32 ``[Hq][n_buckets]``, buckets int32
+    ``[2*max_distance + 1]``, e.g. ``rel_buckets_log``), and a prefix mask
+    (prefix_lens int32, one per document).  Heads are the layer's global ones.
+    The layer reads the tensors at every call, so a table updated in place is
+    the one the next call uses."""
+    softcap: float = 0.0
+    slopes: Optional[torch.Tensor] = None
+    rel_bias: Optional[torch.Tensor] = None
+    buckets: Optional[torch.Tensor] = None
+    prefix_lens: Optional[torch.Tensor] = None
+    rel_bias_grad: bool = True   # the backward gives the table's gradient
+
+    def struct(self, Hq: int, with_backward: bool = True) -> B_.ScoreModsStruct:
+        return B_.score_mods(Hq, self.softcap, self.slopes, self.rel_bias, self.buckets,
+                             with_backward and self.rel_bias is not None and self.rel_bias_grad, self.prefix_lens)
+
+    def for_heads(self, first: int, count: int) -> "ScoreMods":
+        """The same for the query heads [first, first + count): one rank's slice."""
+        cut = lambda t: None if t is None else t[first:first + count].contiguous()
+        return replace(self, slopes=cut(self.slopes), rel_bias=cut(self.rel_bias))
+
+
+def rel_buckets_log(n_buckets: int, max_distance: int, bidirectional: bool, device="cuda") -> torch.Tensor:
+    """A bucket map for ``ScoreMods.buckets`` on ``device`` (``usp_rel_buckets_log``)."""
+    return B_.usp_rel_buckets_log(n_buckets, max_distance, bidirectional).to(device)
+
+
 def plan_backward(prm: B_.AttnParams, free_bytes: int, stored_ds: Optional[bool] = None, Hkv: int = 0,
-                  groups_ok: bool = False, group_size: Optional[int] = None):
+                  groups_ok: bool = False, group_size: Optional[int] = None,
+                  mods: Optional[B_.ScoreModsStruct] = None):
     """(workspace bytes, stored dS?, key/value head groups) of the backward
     calls for ``free_bytes`` of free device memory (host arithmetic only).
 
@@ -79,13 +111,19 @@ def plan_backward(prm: B_.AttnParams, free_bytes: int, stored_ds: Optional[bool]
     that fits (the passes then run group by group over the same workspace);
     True insists on it (ValueError if the shape has none).  ``group_size``
     forces groups of that many key/value heads.  A group is (first key/value
-    head, count); [(0, 0)] means all heads in one pass."""
+    head, count); [(0, 0)] means all heads in one pass.  ``mods``: the layer's
+    modified scores, if any."""
+    def fast_bytes(prm):
+        if mods is not None:
+            return B_.usp_attn_mod_bwd_fast_workspace_bytes(prm, mods)
+        return B_.usp_attn_bwd_fast_workspace_bytes(prm)
+
     def with_group(c):
         prm_c = B_.AttnParams(*[getattr(prm, f) for f, _ in prm._fields_])
         prm_c.head_first, prm_c.head_count = 0, c
-        return B_.usp_attn_bwd_fast_workspace_bytes(prm_c)
+        return fast_bytes(prm_c)
 
-    fast = B_.usp_attn_bwd_fast_workspace_bytes(prm)
+    fast = fast_bytes(prm)
     groups = [(0, 0)]
     if group_size is not None:
         if not groups_ok or stored_ds is False:
@@ -105,25 +143,35 @@ def plan_backward(prm: B_.AttnParams, free_bytes: int, stored_ds: Optional[bool]
                     break
     if stored_ds and fast == 0:
         raise ValueError("this shape has no stored-dS backward (it needs a causal mask and S % 128 == 0)")
-    n = fast if stored_ds else B_.usp_attn_bwd_workspace_bytes(prm)
+    if stored_ds:
+        n = fast
+    elif mods is not None:
+        n = B_.usp_attn_mod_bwd_workspace_bytes(prm, mods)
+    else:
+        n = B_.usp_attn_bwd_workspace_bytes(prm)
     return n, bool(stored_ds), groups
 
 
 def backward_workspace(prm: B_.AttnParams, device, stored_ds: Optional[bool] = None, Hkv: int = 0,
-                       groups_ok: bool = False, group_size: Optional[int] = None):
+                       groups_ok: bool = False, group_size: Optional[int] = None,
+                       mods: Optional[B_.ScoreModsStruct] = None):
     """The workspace tensor of the backward calls on ``device``, with the
     choices of ``plan_backward`` for the device's free memory."""
     free = torch.cuda.mem_get_info(device)[0] if stored_ds is None and group_size is None else 0
-    n, stored_ds, groups = plan_backward(prm, free, stored_ds, Hkv, groups_ok, group_size)
+    n, stored_ds, groups = plan_backward(prm, free, stored_ds, Hkv, groups_ok, group_size, mods)
     return torch.empty((max(n, 256),), dtype=torch.uint8, device=device), stored_ds, groups
 
 
 class UlyssesAttention:
-    """Buffers and calls for one shape on one device."""
+    """Buffers and calls for one shape on one device.  With ``mods`` the scores
+    are modified (``ScoreMods``): the same calls, and ``drel_bias`` after a
+    backward."""
 
     def __init__(self, shape: Shape, device="cuda", with_backward: bool = True, fused: Optional[bool] = None,
-                 stored_ds: Optional[bool] = None, ds_group_size: Optional[int] = None):
+                 stored_ds: Optional[bool] = None, ds_group_size: Optional[int] = None,
+                 mods: Optional[ScoreMods] = None):
         s = self.shape = shape
+        self._mods = None if mods is None else mods.struct(s.Hq, with_backward)
         self.stored_ds = stored_ds
         self.ds_group_size = ds_group_size
         self.fused = shape.can_fuse if fused is None else bool(fused)
@@ -158,6 +206,8 @@ class UlyssesAttention:
             self.dk_seq = torch.empty(seq_kv, dtype=bf, device=dev)
             self.dv_seq = torch.empty(seq_kv, dtype=bf, device=dev)
             self.dsinks = torch.zeros((s.Hq,), dtype=torch.float32, device=dev)
+            if self._mods is not None and self._mods.rel_bias_grad:
+                self.drel_bias = torch.zeros((s.Hq, self._mods.n_buckets), dtype=torch.float32, device=dev)
         self._bwd_ws = None
         self.ds_groups = [(0, 0)]
         self._inputs = None  # the forward's q/k/v as the attention kernels read them
@@ -173,7 +223,7 @@ class UlyssesAttention:
         if self._bwd_ws is None:
             self._bwd_ws, self.stored_ds, self.ds_groups = backward_workspace(
                 prm, self.lse.device, self.stored_ds, self.shape.Hkv, groups_ok=self.fused,
-                group_size=self.ds_group_size)
+                group_size=self.ds_group_size, mods=self._mods)
         return self._bwd_ws
 
     # -- steps ---------------------------------------------------------------
@@ -196,7 +246,12 @@ class UlyssesAttention:
 
     def attention(self, sinks=None, stream=None):
         q, k, v = self._inputs
-        if self.fused:
+        if self._mods is not None:
+            prm = self.params(sinks, B_.USP_IO_SEQ_KV_HEAD if self.fused else None)
+            kv = (self.k_head, self.v_head) if self.fused else (k, v)
+            B_.usp_attn_mod_fwd(prm, self._mods, q, *kv, self.o_seq if self.fused else self.o_head, self.lse,
+                                self.status, stream)
+        elif self.fused:
             B_.usp_attn_fwd(self.params(sinks, B_.USP_IO_SEQ_KV_HEAD), q, self.k_head, self.v_head, self.o_seq,
                             self.lse, self.status, stream)
         else:
@@ -234,22 +289,40 @@ class UlyssesAttention:
             B_.usp_relayout_fwd(do_seq, self.do_head, s.B, s.S, s.Hq, s.D, s.P, stream)
             do, o, dq, dk, dv = self.do_head, self.o_head, self.dq_head, self.dk_head, self.dv_head
         mark(1)
-        B_.usp_attn_bwd_preprocess(prm, o, self.lse, do, self.dsinks if sinks is not None else None, ws,
-                                   self.status, stream)
+        dsinks = self.dsinks if sinks is not None else None
+        mods = self._mods
+        if mods is not None:
+            def dkdv(prm):
+                B_.usp_attn_mod_bwd_dkdv(prm, mods, q, k, v, do, dk, dv, ws, self.status, stream)
+
+            def dq_pass(prm):
+                B_.usp_attn_mod_bwd_dq(prm, mods, q, k, v, do, dq, ws, self.status, stream)
+
+            B_.usp_attn_mod_bwd_preprocess(prm, mods, q, k, v, o, self.lse, do, dsinks, ws, self.status, stream)
+        else:
+            def dkdv(prm):
+                B_.usp_attn_bwd_dkdv(prm, q, k, v, self.lse, do, dk, dv, ws, self.status, stream)
+
+            def dq_pass(prm):
+                B_.usp_attn_bwd_dq(prm, q, k, v, self.lse, do, dq, ws, self.status, stream)
+
+            B_.usp_attn_bwd_preprocess(prm, o, self.lse, do, dsinks, ws, self.status, stream)
         mark(2)
         if len(self.ds_groups) == 1:
-            B_.usp_attn_bwd_dkdv(prm, q, k, v, self.lse, do, dk, dv, ws, self.status, stream)
+            dkdv(prm)
             mark(3)
-            B_.usp_attn_bwd_dq(prm, q, k, v, self.lse, do, dq, ws, self.status, stream)
+            dq_pass(prm)
         else:  # stored dS a key/value head group at a time (both passes per group)
             gmark = group_marks or (lambda g, i: None)
             for gi, grp in enumerate(self.ds_groups):
                 prm_g = self.params(None, group=grp)
-                B_.usp_attn_bwd_dkdv(prm_g, q, k, v, self.lse, do, dk, dv, ws, self.status, stream)
+                dkdv(prm_g)
                 gmark(gi, 0)
-                B_.usp_attn_bwd_dq(prm_g, q, k, v, self.lse, do, dq, ws, self.status, stream)
+                dq_pass(prm_g)
                 gmark(gi, 1)
             mark(3)
+        if mods is not None and mods.rel_bias_grad:
+            B_.usp_attn_mod_bwd_rel_bias(prm, mods, self.drel_bias, ws, stream)
         mark(4)
         if not self.fused:
             B_.usp_relayout_bwd(self.dq_head, self.dq_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
@@ -260,7 +333,8 @@ class UlyssesAttention:
 
     def backward(self, do_seq, sinks=None, stream=None):
         """dO shards in; dQ/dK/dV shards out (``self.dq_seq`` ...), dsinks.
-        In explicit mode this is the single ``usp_attn_bwd`` call."""
+        In explicit mode this is the single ``usp_attn_bwd`` (or
+        ``usp_attn_mod_bwd``) call."""
         if self.fused:
             return self.backward_phases(do_seq, sinks, stream)
         s = self.shape
@@ -268,8 +342,14 @@ class UlyssesAttention:
         ws = self._ws(prm)
         q, k, v = self._inputs
         B_.usp_relayout_fwd(do_seq, self.do_head, s.B, s.S, s.Hq, s.D, s.P, stream)
-        B_.usp_attn_bwd(prm, q, k, v, self.o_head, self.lse, self.do_head, self.dq_head, self.dk_head,
-                        self.dv_head, self.dsinks if sinks is not None else None, ws, self.status, stream)
+        dsinks = self.dsinks if sinks is not None else None
+        if self._mods is not None:
+            B_.usp_attn_mod_bwd(prm, self._mods, q, k, v, self.o_head, self.lse, self.do_head, self.dq_head,
+                                self.dk_head, self.dv_head, dsinks, self.drel_bias if self._mods.rel_bias_grad else None,
+                                ws, self.status, stream)
+        else:
+            B_.usp_attn_bwd(prm, q, k, v, self.o_head, self.lse, self.do_head, self.dq_head, self.dk_head,
+                            self.dv_head, dsinks, ws, self.status, stream)
         B_.usp_relayout_bwd(self.dq_head, self.dq_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
         B_.usp_relayout_bwd(self.dk_head, self.dk_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
         B_.usp_relayout_bwd(self.dv_head, self.dv_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
