@@ -619,8 +619,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       [[maybe_unused]] float slope2 = 0.f;
       if constexpr (M::on) {
         const int hg = hg0 + i / n_q;
-        if (mods.table != nullptr) tab = mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad;
-        if (mods.slopes != nullptr) slope2 = __ldg(mods.slopes + hg) * kLog2E;
+        if constexpr (M::bias_on) {
+          if (mods.table != nullptr) tab = mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad;
+          if (mods.slopes != nullptr) slope2 = __ldg(mods.slopes + hg) * kLog2E;
+        }
       }
 #pragma unroll
       for (int c = 0; c < NCK; ++c) {
@@ -639,16 +641,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t xs2 = sc2;
         if constexpr (M::on) {
           const int d0 = q0 + 32 * c - u, dw = q0 + 32 * c - uw;
-          Affine f = add_bias<32, 1>(x, tab, mods.R, slope2, d0, dw - 31, dw + 31, p.scale_log2);
-          if (mods.cap > 0.f) {
+          Affine f{p.scale_log2, 0.f};
+          if constexpr (M::bias_on) f = add_bias<32, 1>(x, tab, mods.R, slope2, d0, dw - 31, dw + 31, p.scale_log2);
+          if constexpr (M::cap_on) {
             cap_scores(x, f, mods.cap);
             cap_slope(x, gf);
             f = {mods.cap * kLog2E, 0.f};
           }
-          if (f.off != 0.f) {
+          if constexpr (M::bias_on && !M::cap_on) {
+            if (f.off != 0.f) {
+              const uint64_t a2 = f2_pack(f.sc, f.sc), o2 = f2_pack(f.off, f.off);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e], f.sc, f.off);
-            f.sc = 1.f;
+              for (int e = 0; e < 32; e += 2) {
+                const float2 y = f2_unpack(f2_fma(f2_pack(x[e], x[e + 1]), a2, o2));
+                x[e] = y.x;
+                x[e + 1] = y.y;
+              }
+              f.sc = 1.f;
+            }
           }
           xs2 = f2_pack(f.sc, f.sc);
         }
@@ -669,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_packed<16>(lb + T_S + gc + 16 * c, pr[c]);
         if constexpr (M::on) {
-          if (mods.cap > 0.f) {
+          if constexpr (M::cap_on) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) pr[c][e] *= gf[e];
           }
@@ -709,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 16; ++e) pk[c][e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
         tmem_st16(lb + T_DP + gc + 16 * c, pk[c]);
-        if constexpr (M::on) {
+        if constexpr (bias_on<M>) {
           if (mods.partial != nullptr) {
             // The table's gradient sums dX along diagonals (t - u = const).
             // Chunks wholly beyond R add to one sum per key; in the others a
@@ -760,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->ds_full);
-      if constexpr (M::on) {
+      if constexpr (bias_on<M>) {
         if (mods.partial != nullptr && i % n_q == n_q - 1) {  // the head's last slice: its sums beyond R
           float fl = far_lo, fh = far_hi;
 #pragma unroll
@@ -990,8 +1000,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     [[maybe_unused]] const float* tab = nullptr;  // Mods: the head's bias row and slope
     [[maybe_unused]] float slope2 = 0.f;
     if constexpr (M::on) {
-      if (mods.table != nullptr) tab = mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad;
-      if (mods.slopes != nullptr) slope2 = __ldg(mods.slopes + hg) * kLog2E;
+      if constexpr (M::bias_on) {
+        if (mods.table != nullptr) tab = mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad;
+        if (mods.slopes != nullptr) slope2 = __ldg(mods.slopes + hg) * kLog2E;
+      }
     }
     const uint32_t s_col = T_S + grp * 64, dp_col = T_DP + grp * 64;
     bool ok = true;
@@ -1007,8 +1019,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       Affine f{p.scale_log2, 0.f};
       if constexpr (M::on) {
         const int d0 = t - k0, dw = d0 - lane;
-        f = add_bias<64, -1>(x, tab, mods.R, slope2, d0, dw - 63, dw + 31, p.scale_log2);
-        if (mods.cap > 0.f) {
+        if constexpr (M::bias_on) f = add_bias<64, -1>(x, tab, mods.R, slope2, d0, dw - 63, dw + 31, p.scale_log2);
+        if constexpr (M::cap_on) {
           cap_scores(x, f, mods.cap);
           cap_slope(x, gf);
           f = {mods.cap * kLog2E, 0.f};
@@ -1031,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if constexpr (M::on) {
-        if (mods.cap > 0.f) {
+        if constexpr (M::cap_on) {
 #pragma unroll
           for (int c = 0; c < 64; ++c) pr[c] *= gf[c];
         }
@@ -1406,6 +1418,18 @@ static inline int run_preprocess(const usp_attn_params& prm, const void* o, cons
   return USP_OK;
 }
 
+// The dQ pass over stored dS meets the mask's extent alone, not the scores.
+template <class M>
+struct DsMods {
+  using type = M;
+};
+template <bool CAP, bool BIAS>
+struct DsMods<Mods<CAP, BIAS>> {
+  using type = Mods<false, false>;
+};
+static inline NoMods ds_mods(const NoMods& m) { return m; }
+static inline Mods<false, false> ds_mods(const ModArgs& m) { return {m}; }
+
 template <int D, class M>
 static int run_grad_pass(bool dq_pass, const AttnArgs& a, const M& mods, const void* q, const void* k, const void* v,
                          const void* dO, void* dq, void* dk, void* dv, const float* stats, void* ds,
@@ -1419,16 +1443,18 @@ static int run_grad_pass(bool dq_pass, const AttnArgs& a, const M& mods, const v
   if (dq_pass && ds != nullptr) {
     // dQ = dS K from the blocks the dK/dV pass stored
     using CD = bwd::CfgDs<D>;
+    using MD = typename DsMods<M>::type;
+    const MD dmods = ds_mods(mods);
     CUtensorMap tk, tds, tdq;
     if ((rc = make_rows_tmap(&tk, k, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
     if ((rc = make_ds_tmap(&tds, ds, ds_blocks)) != USP_OK) return rc;
     if ((rc = make_rows_tmap(&tdq, dq, a, a.hq, a.Hq, D, kBM)) != USP_OK) return rc;
-    if (cudaFuncSetAttribute(bwd::dq_ds_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, CD::SMEM) !=
+    if (cudaFuncSetAttribute(bwd::dq_ds_kernel<D, MD>, cudaFuncAttributeMaxDynamicSharedMemorySize, CD::SMEM) !=
         cudaSuccess)
       return USP_ERR_CUDA;
     const int n_units = g.n_tiles * a.n_qh;
     const int grid = n_units < device_sm_count() ? n_units : device_sm_count();  // persistent: one CTA per SM
-    bwd::dq_ds_kernel<D, M><<<grid, bwd::kDsThreads, CD::SMEM, st>>>(tk, tds, tdq, a, g, n_units, mods);
+    bwd::dq_ds_kernel<D, MD><<<grid, bwd::kDsThreads, CD::SMEM, st>>>(tk, tds, tdq, a, g, n_units, dmods);
     return check_launch();
   }
   if (!dq_pass) {

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
     fence_barrier_init();
   }
   if constexpr (M::on) {
-    if (mods.rel_bias != nullptr)
+    if (M::bias_on && mods.rel_bias != nullptr)
       for (int e = tid; e < tab_len(mods.R); e += C::THREADS)
         reinterpret_cast<float*>(smem + C::OFF_TAB)[e] = table_entry(mods, r * p.hq + j, e, p.status);
   }
@@ -348,9 +348,9 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
     [[maybe_unused]] const float* tab = nullptr;
     if constexpr (M::on) {
       visible_keys(mods, t, a, b, pe, p.causal, p.window_left, row_ok, mvlo, mvhi);
-      if (mods.slopes != nullptr) slope2 = __ldg(mods.slopes + gh) * kLog2E;
-      if (mods.rel_bias != nullptr) tab = reinterpret_cast<const float*>(smem + C::OFF_TAB) + mods.R + kTabPad;
-      fixed_ref = mods.cap > 0.f && mods.cap * kLog2E <= kFixedRefCap2;
+      if (M::bias_on && mods.slopes != nullptr) slope2 = __ldg(mods.slopes + gh) * kLog2E;
+      if (M::bias_on && mods.rel_bias != nullptr) tab = reinterpret_cast<const float*>(smem + C::OFF_TAB) + mods.R + kTabPad;
+      fixed_ref = M::cap_on && mods.cap * kLog2E <= kFixedRefCap2;
       if (fixed_ref) {
         const float ref = fmaxf(m, 0.f);  // m is the sink's logit or -inf
         l = ex2(m - ref);
@@ -373,8 +373,9 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
       [[maybe_unused]] float off = 0.f;
       if constexpr (M::on) {
         const int d0 = t - kv0, dw = d0 - lane;  // distance of column 0; the warp's first row's
-        Affine f = add_bias<kBN, -1>(s, tab, mods.R, slope2, d0, dw - (kBN - 1), dw + 31, sc);
-        if (mods.cap > 0.f) {
+        Affine f{sc, 0.f};
+        if constexpr (M::bias_on) f = add_bias<kBN, -1>(s, tab, mods.R, slope2, d0, dw - (kBN - 1), dw + 31, sc);
+        if constexpr (M::cap_on) {
           cap_scores(s, f, mods.cap);
           f = {mods.cap * kLog2E, 0.f};
         }
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
       }
       float alpha = 1.f;
       bool rescale = false;
-      if (!M::on || !fixed_ref) {
+      if (!fixed_ref) {
         // row max as 8 independent chains
         float mx8[8];
 #pragma unroll

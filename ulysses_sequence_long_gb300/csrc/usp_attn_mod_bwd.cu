@@ -10,7 +10,7 @@
 
 namespace usp {
 
-Mods make_mods(const usp_score_mods& m);
+ModArgs make_mods(const usp_score_mods& m);
 
 namespace bwd {
 
@@ -37,11 +37,11 @@ struct BarsD {
 constexpr int kDeltaRed = 512;  // byte offset of the row sums of group 1 after the barriers
 static_assert(sizeof(BarsD) <= kDeltaRed && kDeltaRed + kBM * 4 <= 1024, "delta barrier block");
 
-template <int D>
+template <int D, class M>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs p,
                  const __nv_bfloat16* __restrict__ q_in, const __nv_bfloat16* __restrict__ do_in,
-                 const float* __restrict__ lse, float* __restrict__ stats, int bsp, int n_tiles, Mods mods) {
+                 const float* __restrict__ lse, float* __restrict__ stats, int bsp, int n_tiles, M mods) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -191,8 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->s_free[n & 1]);
       const int d0 = t - k0, dw = d0 - lane;
-      Affine f = add_bias<64, -1>(x, tab, mods.R, slope2, d0, dw - 63, dw + 31, p.scale_log2);
-      if (mods.cap > 0.f) {
+      Affine f{p.scale_log2, 0.f};
+      if constexpr (M::bias_on) f = add_bias<64, -1>(x, tab, mods.R, slope2, d0, dw - 63, dw + 31, p.scale_log2);
+      if constexpr (M::cap_on) {
         cap_scores(x, f, mods.cap);
         f = {mods.cap * kLog2E, 0.f};
       }
@@ -243,18 +244,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
-template <int D>
-int run_delta(const AttnArgs& a, const Mods& m, const void* q, const void* k, const void* v, const void* dO,
+template <int D, class M>
+int run_delta(const AttnArgs& a, const M& m, const void* q, const void* k, const void* v, const void* dO,
               const float* lse, float* stats, cudaStream_t st) {
   using C = bwd::Cfg<D>;
   CUtensorMap tk, tv;
   int rc;
   if ((rc = make_rows_tmap(&tk, k, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
   if ((rc = make_rows_tmap(&tv, v, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
-  if (cudaFuncSetAttribute(bwd::delta_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::B_SMEM) != cudaSuccess)
+  if (cudaFuncSetAttribute(bwd::delta_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::B_SMEM) != cudaSuccess)
     return USP_ERR_CUDA;
   const int n_tiles = (a.BS + kBM - 1) / kBM;
-  bwd::delta_kernel<D><<<static_cast<unsigned>(n_tiles) * a.Hq, bwd::kThreads, C::B_SMEM, st>>>(
+  bwd::delta_kernel<D, M><<<static_cast<unsigned>(n_tiles) * a.Hq, bwd::kThreads, C::B_SMEM, st>>>(
       tk, tv, a, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(dO), lse, stats,
       stats_row_pitch(a.BS), n_tiles, m);
   return check_launch();
@@ -302,7 +303,7 @@ size_t mod_ds_bytes(const usp_attn_params& p, const usp_score_mods& m) {
 }
 
 // Rows by distance in the log2 domain; one block per head.
-__global__ void __launch_bounds__(kRelThreads) rel_expand_kernel(Mods m, float* __restrict__ table, int32_t* status) {
+__global__ void __launch_bounds__(kRelThreads) rel_expand_kernel(ModArgs m, float* __restrict__ table, int32_t* status) {
   const int n = tab_len(m.R);
   for (int e = threadIdx.x; e < n; e += kRelThreads)
     table[static_cast<size_t>(blockIdx.x) * n + e] = table_entry(m, blockIdx.x, e, status);
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kRelThreads)
 // The splits' sums of a head, then its buckets: thread = bucket, distances in
 // order (no atomics: the result does not depend on the schedule).
 __global__ void __launch_bounds__(kRelThreads)
-    rel_bucket_kernel(Mods m, const float* __restrict__ sums, float* __restrict__ drel, int splits) {
+    rel_bucket_kernel(ModArgs m, const float* __restrict__ sums, float* __restrict__ drel, int splits) {
   extern __shared__ float by_dist[];
   const int h = blockIdx.x, row = 2 * m.R + 1;
   const float* src = sums + static_cast<size_t>(h) * splits * row;
@@ -346,8 +347,8 @@ __global__ void __launch_bounds__(kRelThreads)
   }
 }
 
-Mods bwd_mods(const usp_attn_params& p, const usp_score_mods& sm, const void* ws) {
-  Mods m = make_mods(sm);
+ModArgs bwd_mods(const usp_attn_params& p, const usp_score_mods& sm, const void* ws) {
+  ModArgs m = make_mods(sm);
   const Layout L = mod_layout(p, sm);
   uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(ws));
   m.n_kb = L.n_kb;
@@ -378,7 +379,7 @@ size_t attn_mod_bwd_fast_ws_bytes(const usp_attn_params& p, const usp_score_mods
 int launch_attn_mod_bwd_preprocess(const usp_attn_params& p, const usp_score_mods& sm, const void* q, const void* k,
                                    const void* v, const void* o, const float* lse, const void* dO, float* dsinks,
                                    void* ws, int32_t* status, cudaStream_t st) {
-  const Mods m = bwd_mods(p, sm, ws);
+  const ModArgs m = bwd_mods(p, sm, ws);
   if (sm.rel_bias != nullptr) {
     const Layout L = mod_layout(p, sm);
     uint8_t* base = static_cast<uint8_t*>(ws);
@@ -392,8 +393,10 @@ int launch_attn_mod_bwd_preprocess(const usp_attn_params& p, const usp_score_mod
   if (!exact_delta) return run_preprocess(p, o, lse, dO, nullptr, ws, status, st);
   const AttnArgs a = make_args(p, status);
   float* stats = static_cast<float*>(ws);
-  const int rc = p.D == 128 ? run_delta<128>(a, m, q, k, v, dO, lse, stats, st)
-                            : run_delta<64>(a, m, q, k, v, dO, lse, stats, st);
+  const int rc = with_mods(m, [&](const auto& mods) {
+    return p.D == 128 ? run_delta<128>(a, mods, q, k, v, dO, lse, stats, st)
+                      : run_delta<64>(a, mods, q, k, v, dO, lse, stats, st);
+  });
   if (rc != USP_OK || dsinks == nullptr) return rc;
   bwd::dsink_kernel<<<a.P * a.hq, 256, 0, st>>>(stats, dsinks, a, stats_row_pitch(a.BS));
   return check_launch();
@@ -403,26 +406,30 @@ int launch_attn_mod_bwd_dkdv(const usp_attn_params& p, const usp_score_mods& sm,
                              const void* v, const void* dO, void* dk, void* dv, const void* ws, size_t ws_bytes,
                              int32_t* status, cudaStream_t st) {
   const AttnArgs a = make_args(p, status);
-  const Mods m = bwd_mods(p, sm, ws);
+  const ModArgs m = bwd_mods(p, sm, ws);
   const float* stats = static_cast<const float*>(ws);
   bwd::DsGeom g{};
   long long nb = 0;
   void* ds = mod_ds_region(p, sm, ws, ws_bytes, g, nb);
-  if (p.D == 128) return run_grad_pass<128>(false, a, m, q, k, v, dO, nullptr, dk, dv, stats, ds, g, nb, st);
-  return run_grad_pass<64>(false, a, m, q, k, v, dO, nullptr, dk, dv, stats, ds, g, nb, st);
+  return with_mods(m, [&](const auto& mods) {
+    return p.D == 128 ? run_grad_pass<128>(false, a, mods, q, k, v, dO, nullptr, dk, dv, stats, ds, g, nb, st)
+                      : run_grad_pass<64>(false, a, mods, q, k, v, dO, nullptr, dk, dv, stats, ds, g, nb, st);
+  });
 }
 
 int launch_attn_mod_bwd_dq(const usp_attn_params& p, const usp_score_mods& sm, const void* q, const void* k,
                            const void* v, const void* dO, void* dq, const void* ws, size_t ws_bytes, int32_t* status,
                            cudaStream_t st) {
   const AttnArgs a = make_args(p, status);
-  const Mods m = bwd_mods(p, sm, ws);
+  const ModArgs m = bwd_mods(p, sm, ws);
   const float* stats = static_cast<const float*>(ws);
   bwd::DsGeom g{};
   long long nb = 0;
   void* ds = mod_ds_region(p, sm, ws, ws_bytes, g, nb);
-  if (p.D == 128) return run_grad_pass<128>(true, a, m, q, k, v, dO, dq, nullptr, nullptr, stats, ds, g, nb, st);
-  return run_grad_pass<64>(true, a, m, q, k, v, dO, dq, nullptr, nullptr, stats, ds, g, nb, st);
+  return with_mods(m, [&](const auto& mods) {
+    return p.D == 128 ? run_grad_pass<128>(true, a, mods, q, k, v, dO, dq, nullptr, nullptr, stats, ds, g, nb, st)
+                      : run_grad_pass<64>(true, a, mods, q, k, v, dO, dq, nullptr, nullptr, stats, ds, g, nb, st);
+  });
 }
 
 int launch_attn_mod_bwd_rel_bias(const usp_attn_params& p, const usp_score_mods& sm, float* drel_bias, void* ws,

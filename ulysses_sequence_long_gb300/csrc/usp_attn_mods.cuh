@@ -33,8 +33,7 @@ struct NoMods {
   static constexpr bool on = false;
 };
 
-struct Mods {
-  static constexpr bool on = true;
+struct ModArgs {
   float cap;               // softcap, 0: none
   const float* slopes;     // global [Hq] or null
   const float* rel_bias;   // global [Hq][n_buckets] or null
@@ -49,21 +48,44 @@ struct Mods {
   int n_kb;  // 32-key blocks of the rank-local tokens
 };
 
+// The compiled combinations: a kernel that tests for the cap and the biases at
+// run time keeps their registers alive, and the ones at the 168-register limit
+// then spill (prefixes cost a few instructions per tile and are tested for).
+template <bool CAP, bool BIAS>
+struct Mods : ModArgs {
+  static constexpr bool on = true;
+  static constexpr bool cap_on = CAP;
+  static constexpr bool bias_on = BIAS;
+};
+
+template <class M>
+constexpr bool bias_on = false;
+template <bool CAP, bool BIAS>
+constexpr bool bias_on<Mods<CAP, BIAS>> = BIAS;
+
+// f(M{}) with the combination that `m` needs.
+template <class F>
+auto with_mods(const ModArgs& m, F f) {
+  const bool bias = m.slopes != nullptr || m.rel_bias != nullptr;
+  if (m.cap > 0.f) return bias ? f(Mods<true, true>{m}) : f(Mods<true, false>{m});
+  return bias ? f(Mods<false, true>{m}) : f(Mods<false, false>{m});
+}
+
 // Bucket of distance index i, clamped into the table; an id outside it is reported.
-__device__ __forceinline__ int checked_bucket(const Mods& m, int i, int32_t* status) {
+__device__ __forceinline__ int checked_bucket(const ModArgs& m, int i, int32_t* status) {
   const int b = __ldg(m.buckets + i);
   if (b < 0 || b >= m.n_buckets) set_status(status, USP_ERR_BAD_MODS);
   return min(max(b, 0), m.n_buckets - 1);
 }
 
 // Entry e (of tab_len(R)) of head h's row by distance, in the log2 domain.
-__device__ __forceinline__ float table_entry(const Mods& m, int h, int e, int32_t* status) {
+__device__ __forceinline__ float table_entry(const ModArgs& m, int h, int e, int32_t* status) {
   const int d = min(max(e - (m.R + kTabPad), -m.R), m.R);
   return __ldg(m.rel_bias + static_cast<size_t>(h) * m.n_buckets + checked_bucket(m, d + m.R, status)) * kLog2E;
 }
 
 // One past the last prefix token of document d = [a, b).
-__device__ __forceinline__ int prefix_end(const Mods& m, int d, int a, int b, int32_t* status) {
+__device__ __forceinline__ int prefix_end(const ModArgs& m, int d, int a, int b, int32_t* status) {
   if (m.prefix == nullptr) return a;
   if (d >= m.n_prefix) {
     set_status(status, USP_ERR_BAD_MODS);
@@ -79,7 +101,7 @@ __device__ __forceinline__ void doc_bounds(const AttnArgs& p, const NoMods&, int
   doc_bounds(p.cu, n, p.BS, t, a, b);
   pe = a;
 }
-__device__ __forceinline__ void doc_bounds(const AttnArgs& p, const Mods& m, int n, int t, int& a, int& b, int& pe) {
+__device__ __forceinline__ void doc_bounds(const AttnArgs& p, const ModArgs& m, int n, int t, int& a, int& b, int& pe) {
   const int d = find_doc(p.cu, n, t);
   a = max(0, min(__ldg(p.cu + d), t));
   b = min(p.BS, max(__ldg(p.cu + d + 1), t + 1));
