@@ -439,7 +439,7 @@ int usp_attn_mod_fwd(const usp_attn_params* params, const usp_score_mods* mods, 
 
 /* Workspace of the backward: the statistics of usp_attn_bwd, with rel_bias the
  * bias rows by distance, and with rel_bias_grad partial sums of the scores'
- * gradient by distance (8 (2R + 1) bytes per head and 32 tokens).  The fast form
+ * gradient by distance (16 (2R + 1) bytes per head and 32 tokens).  The fast form
  * adds the stored dS blocks, as usp_attn_bwd_fast_workspace_bytes does; with a
  * prefix or without causal order they cover every pair of a key tile and a query
  * slice of a row.  0: invalid arguments, or (fast) S not a multiple of 128. */
@@ -463,7 +463,7 @@ int usp_attn_mod_bwd(const usp_attn_params* params, const usp_score_mods* mods, 
                      usp_stream_t stream);
 
 /* Its phases, as those of usp_attn_bwd: the preprocess first (statistics, bias
- * rows, cleared partial sums), then dK/dV, then dQ; head groups for the dK/dV
+ * rows), then dK/dV, then dQ; head groups for the dK/dV
  * and dQ passes with USP_IO_SEQ as there.  usp_attn_mod_bwd_rel_bias reduces the partial
  * sums once the dK/dV passes of all heads are done. */
 int usp_attn_mod_bwd_preprocess(const usp_attn_params* params, const usp_score_mods* mods, const void* q,

@@ -190,7 +190,7 @@ def test_workspace_sizes(lib):
     rel = dict(rel=16, buckets=16, nb=8, R=16)
     rows = up(4 * 4 * (2 * (16 + 160) + 1))
     assert n(_params(), _mods(**rel))[0] == stats + rows
-    part = up(4 * 4 * 16 * 33) + up(4 * 4 * 1 * 33)                       # 8 blocks of 32 keys, 2 halves; 1 split
+    part = up(4 * 4 * 32 * 33) + up(4 * 4 * 1 * 33)                       # 8 blocks of 32 keys, 4 quarters; 1 split
     assert n(_params(), _mods(**rel, grad=1))[0] == stats + rows + part
 
 

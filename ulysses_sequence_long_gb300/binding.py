@@ -157,9 +157,25 @@ def _check(rc: int, where: str) -> None:
         raise UspError(rc, where)
 
 
+class Buffer:
+    """A tensor that was checked once and whose owner keeps it: the calls take it for the tensor and do not look
+    at it again (a layer's own buffers, at every step of a model)."""
+    __slots__ = ("tensor", "ptr", "nbytes")
+
+    def __init__(self, tensor: torch.Tensor, name: str = "buffer", dtype=None):
+        self.ptr = _dev(tensor, name, dtype)
+        self.tensor, self.nbytes = tensor, tensor.numel() * tensor.element_size()
+
+
+def _nbytes(t) -> int:
+    return t.nbytes if type(t) is Buffer else t.numel() * t.element_size()
+
+
 def _dev(t: Optional[torch.Tensor], name: str, dtype=None):
     if t is None:
         return None
+    if type(t) is Buffer:
+        return t.ptr
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if not t.is_contiguous():
@@ -203,7 +219,7 @@ def usp_cu_seqlens_from_position_ids(pos, B, S, P, cu_seqlens, n_docs, max_len, 
     _check(load().usp_cu_seqlens_from_position_ids(
         _dev(pos, "pos", torch.int32), B, S, P, _dev(cu_seqlens, "cu_seqlens", torch.int32),
         _dev(n_docs, "n_docs", torch.int32), _dev(max_len, "max_len", torch.int32), _dev(ws, "ws"),
-        ws.numel() * ws.element_size(), _dev(dev_status, "dev_status", torch.int32), _stream(stream)),
+        _nbytes(ws), _dev(dev_status, "dev_status", torch.int32), _stream(stream)),
         "usp_cu_seqlens_from_position_ids")
 
 
@@ -365,37 +381,53 @@ def score_mods(Hq, softcap=0.0, slopes=None, rel_bias=None, buckets=None, rel_bi
     return m
 
 
+def _mod_sizes(prm: AttnParams, mods: ScoreModsStruct) -> dict:
+    """Elements that the parameters ask of each tensor."""
+    P, tok = max(prm.P, 1), prm.B * prm.S
+    hk = prm.Hkv // P if prm.Hkv >= P else 1
+    kv = (prm.Hkv if prm.io_layout == USP_IO_SEQ else P * hk) * tok * prm.D
+    return {"q": tok * prm.Hq * prm.D, "kv": kv, "lse": tok * prm.Hq, "heads": prm.Hq, "rel": prm.Hq * mods.n_buckets,
+            None: None}
+
+
 class _Call:
     """The tensors of one call: their sizes against the parameters, one device, that device's stream."""
 
     def __init__(self, prm: AttnParams, mods: ScoreModsStruct, stream):
         self.prm, self.mods, self.stream, self.device = prm, mods, stream, None
-        P, tok = max(prm.P, 1), prm.B * prm.S
-        hk = prm.Hkv // P if prm.Hkv >= P else 1
-        kv_head = prm.io_layout != USP_IO_SEQ
-        self.sizes = {"q": tok * prm.Hq * prm.D, "kv": (P * hk if kv_head else prm.Hkv) * tok * prm.D,
-                      "lse": tok * prm.Hq, "heads": prm.Hq, "rel": prm.Hq * mods.n_buckets, None: None}
+        self.sizes = _mod_sizes(prm, mods)
         for t in mods.tensors:
             self._on(t, "mods")
 
     def _on(self, t, name):
         if self.device is None:
             self.device = t.device
-        if t.device != self.device:
+        elif t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, other tensors of the call on {self.device}")
 
     def __call__(self, t, name, dtype, size):
+        if t is None:
+            return None
+        if type(t) is Buffer:
+            if self.device is None:
+                self.device = t.tensor.device
+            return t.ptr
         ptr = _dev(t, name, dtype)
-        if t is not None:
-            self._on(t, name)
-            if size is not None and t.numel() != self.sizes[size]:
-                raise ValueError(f"{name} has {t.numel()} elements, the parameters need {self.sizes[size]}")
+        self._on(t, name)
+        if size is not None and t.numel() != self.sizes[size]:
+            raise ValueError(f"{name} has {t.numel()} elements, the parameters need {self.sizes[size]}")
         return ptr
 
     def run(self, where, *args):
-        with torch.cuda.device(self.device):
-            stream = _stream(torch.cuda.current_stream(self.device) if self.stream is None else self.stream)
-            _check(getattr(load(), where)(ctypes.byref(self.prm), ctypes.byref(self.mods), *args, stream), where)
+        if torch.cuda.current_device() == self.device.index:
+            self._launch(where, args)
+        else:
+            with torch.cuda.device(self.device):
+                self._launch(where, args)
+
+    def _launch(self, where, args):
+        stream = _stream(torch.cuda.current_stream(self.device) if self.stream is None else self.stream)
+        _check(getattr(load(), where)(ctypes.byref(self.prm), ctypes.byref(self.mods), *args, stream), where)
 
 
 _BF, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
@@ -421,7 +453,7 @@ def usp_attn_mod_bwd(params: AttnParams, mods: ScoreModsStruct, q, k, v, o, lse,
     c.run("usp_attn_mod_bwd", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"), c(o, "o", _BF, "q"),
           c(lse, "lse", _F32, "lse"), c(dO, "dO", _BF, "q"), c(dq, "dq", _BF, "q"),
           c(dk, "dk", _BF, "kv"), c(dv, "dv", _BF, "kv"), c(dsinks, "dsinks", _F32, "heads"),
-          c(drel_bias, "drel_bias", _F32, "rel"), c(ws, "ws", None, None), ws.numel() * ws.element_size(),
+          c(drel_bias, "drel_bias", _F32, "rel"), c(ws, "ws", None, None), _nbytes(ws),
           c(dev_status, "dev_status", _I32, None))
 
 
@@ -430,7 +462,7 @@ def usp_attn_mod_bwd_preprocess(params: AttnParams, mods: ScoreModsStruct, q, k,
     c = _Call(params, mods, stream)
     c.run("usp_attn_mod_bwd_preprocess", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"),
           c(o, "o", _BF, "q"), c(lse, "lse", _F32, "lse"), c(dO, "dO", _BF, "q"), c(dsinks, "dsinks", _F32, "heads"), c(ws, "ws", None, None),
-          ws.numel() * ws.element_size(), c(dev_status, "dev_status", _I32, None))
+          _nbytes(ws), c(dev_status, "dev_status", _I32, None))
 
 
 def usp_attn_mod_bwd_dkdv(params: AttnParams, mods: ScoreModsStruct, q, k, v, dO, dk, dv, ws, dev_status=None,
@@ -438,17 +470,17 @@ def usp_attn_mod_bwd_dkdv(params: AttnParams, mods: ScoreModsStruct, q, k, v, dO
     c = _Call(params, mods, stream)
     c.run("usp_attn_mod_bwd_dkdv", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"),
           c(dO, "dO", _BF, "q"), c(dk, "dk", _BF, "kv"), c(dv, "dv", _BF, "kv"), c(ws, "ws", None, None),
-          ws.numel() * ws.element_size(), c(dev_status, "dev_status", _I32, None))
+          _nbytes(ws), c(dev_status, "dev_status", _I32, None))
 
 
 def usp_attn_mod_bwd_dq(params: AttnParams, mods: ScoreModsStruct, q, k, v, dO, dq, ws, dev_status=None, stream=None):
     c = _Call(params, mods, stream)
     c.run("usp_attn_mod_bwd_dq", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"),
-          c(dO, "dO", _BF, "q"), c(dq, "dq", _BF, "q"), c(ws, "ws", None, None), ws.numel() * ws.element_size(),
+          c(dO, "dO", _BF, "q"), c(dq, "dq", _BF, "q"), c(ws, "ws", None, None), _nbytes(ws),
           c(dev_status, "dev_status", _I32, None))
 
 
 def usp_attn_mod_bwd_rel_bias(params: AttnParams, mods: ScoreModsStruct, drel_bias, ws, stream=None):
     c = _Call(params, mods, stream)
     c.run("usp_attn_mod_bwd_rel_bias", c(drel_bias, "drel_bias", _F32, "rel"), c(ws, "ws", None, None),
-          ws.numel() * ws.element_size())
+          _nbytes(ws))

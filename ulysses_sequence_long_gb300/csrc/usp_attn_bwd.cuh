@@ -370,13 +370,30 @@ struct Grads {
 // slice i:  [P^T_i] dV_i, S^T_{i+1}  [dS^T_i] dK_i, dP^T_{i+1}  (brackets: the
 // compute warps' hand-offs), so the tensor core works on the next slice's
 // scores while the compute warps turn the current one into P^T and dS^T.
+//
+// With a bias four groups of four warps share a slice's columns (32 each): the
+// bias and its table's gradient lengthen a warp's chain from S^T to P^T and from
+// dP^T to dS^T, which the tensor core waits for, and half the columns halve it
+// (8192 packed tokens, D = 128: learned bias 361 -> 302 us, slopes 352 -> 295 us).
+// Without one the chain is short enough that the fewer registers of 16 warps cost
+// as much as they gain (prefix 209 us with two groups, 214 with four; a cap 356
+// and 348, but a cap over short windows at D = 64 96 and 104).
+template <class M>
+struct Team {
+  static constexpr int NG = bias_on<M> ? kModGroups : 2;
+  static constexpr int THREADS = 128 * NG + 64;
+  static constexpr int WP = 4 * NG;  // producer warp (the MMA warp is WP + 1)
+};
+
 template <int D, class M>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Team<M>::THREADS, 1)
     dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                 const __grid_constant__ CUtensorMap tst, const __grid_constant__ CUtensorMap tds_st,
                 const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs p,
                 Grads g, M mods) {
   using C = Cfg<D>;
+  using T = Team<M>;
+  constexpr int GQ = C::SL / T::NG;  // queries of a group
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -439,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&bars->st_full, 1);
     mbar_init(&bars->dpt_full, 1);
-    mbar_init(&bars->p_full, 8);
-    mbar_init(&bars->ds_full, 8);
+    mbar_init(&bars->p_full, 4 * T::NG);
+    mbar_init(&bars->ds_full, 4 * T::NG);
     mbar_init(&bars->fin, 1);
     mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
@@ -459,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t T_S = 0, T_DP = C::SL, T_DV = 2 * C::SL, T_DK = T_DV + D, T_K = T_DK + D, T_V = T_K + D / 2;
   static_assert(C::KV_SMEM ? T_K <= 512 : T_V + D / 2 <= 512, "TMEM columns");
 
-  if (warp == 8) {
+  if (warp == T::WP) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       prefetch_tmap(&tq);
@@ -496,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&bars->do_full[i % C::NST], (i / C::NST) & 1, abort, p.status);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == T::WP + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_bf16(kBN, C::SL, false, false);  // [128 keys x SL queries], K = D
@@ -515,11 +532,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t k_s = sbase + C::A_KV, v_s = k_s + C::NCH * kAtomBytes;
       auto q_slot = [&](int i) { return sbase + C::A_Q + (i % C::NST) * C::SLICE; };
       auto do_slot = [&](int i) { return sbase + C::A_DO + (i % C::NST) * C::SLICE; };
-      // A operand columns of a packed slice: compute group g packs its SL/2
-      // queries into the SL/4 columns at g*SL/2 (K step kk: 16 queries, 8 columns)
+      // A operand columns of a packed slice: compute group g packs its GQ
+      // queries into the GQ/2 columns at g*GQ (K step kk: 16 queries, 8 columns)
       auto acol = [](int kk) -> uint32_t {
-        constexpr int per = C::SL / 32;  // K steps per group
-        return static_cast<uint32_t>((kk / per) * (C::SL / 2) + (kk % per) * 8);
+        constexpr int per = GQ / 16;  // K steps per group
+        return static_cast<uint32_t>((kk / per) * GQ + (kk % per) * 8);
       };
       bool ok = n_it == 0 || mbar_wait(&bars->kv_ready, 0, abort, p.status);
       if (ok && n_it > 0 && (ok = mbar_wait(&bars->q_full[0], 0, abort, p.status))) {
@@ -568,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ compute
-    const int grp = warp >> 2;                      // query columns [grp*SL/2, (grp+1)*SL/2) of each slice
+    const int grp = warp >> 2;                      // query columns [grp*GQ, (grp+1)*GQ) of each slice
     const int krow = (warp & 3) * 32 + lane;        // TMEM lane = key row
     const int u = u0 + krow;
     const bool key_ok = u < p.BS;
@@ -581,18 +598,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lb = tmem + ((static_cast<uint32_t>(warp & 3) * 32) << 16);
     if constexpr (!C::KV_SMEM) {
       // K (group 0) or V (group 1) row of this key into TMEM
-      const size_t off = row_offset(p, kvh, p.hk, p.Hkv, key_ok ? u : 0, D);
-      row_to_tmem<D>(lb + (grp == 0 ? T_K : T_V), (grp == 0 ? g.k : g.v) + off, key_ok);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->kv_ready);
+      if (grp < 2) {
+        const size_t off = row_offset(p, kvh, p.hk, p.Hkv, key_ok ? u : 0, D);
+        row_to_tmem<D>(lb + (grp == 0 ? T_K : T_V), (grp == 0 ? g.k : g.v) + off, key_ok);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->kv_ready);
+      }
     }
-    // The group's SL/2 query columns of a slice, in 32-column chunks.  Packed
+    // The group's GQ query columns of a slice, in 32-column chunks.  Packed
     // P^T (dS^T) of chunk c goes to the group's columns gc + 16c, over fp32
     // columns the group has already read.
-    constexpr int NCK = C::SL / 64;
-    const int gc = grp * (C::SL / 2);
-    uint8_t* stg = smem + C::A_DS + warp * C::STG;  // this warp's dS staging buffer
+    constexpr int NCK = GQ / 32;
+    const int gc = grp * GQ;
+    uint8_t* stg = smem + C::A_DS + warp * (32 * GQ * 2);  // this warp's dS staging buffer
     bool ok = true, staged = false;
     [[maybe_unused]] const int uw = u0 + (warp & 3) * 32;  // the warp's first key
     [[maybe_unused]] float far_lo = 0.f, far_hi = 0.f;     // the head's dX at distances <= -R, >= R (this key)
@@ -620,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (M::on) {
         const int hg = hg0 + i / n_q;
         if constexpr (M::bias_on) {
+
           if (mods.table != nullptr) tab = mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad;
           if (mods.slopes != nullptr) slope2 = __ldg(mods.slopes + hg) * kLog2E;
         }
@@ -751,8 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 done = lane == 0 ? r1 : r2;
                 run = (lane == 0 ? 0.f : r1) + x[e];
               }
-              float* row = mods.partial + (static_cast<size_t>(hg0 + i / n_q) * mods.n_kb + (uw >> 5)) * 2 * (2 * mods.R + 1) +
-                           grp * (2 * mods.R + 1) + mods.R;
+              float* row = rel_row(mods, hg0 + i / n_q, uw, grp) + mods.R;
               auto put = [&](int d, float v) {
                 if (d >= mods.R) far_hi += v;
                 else if (d <= -mods.R) far_lo += v;
@@ -779,8 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fh += __shfl_xor_sync(0xffffffffu, fh, o);
           }
           if (lane == 0 && uw < p.BS) {
-            float* row = mods.partial + (static_cast<size_t>(hg0 + i / n_q) * mods.n_kb + (uw >> 5)) * 2 * (2 * mods.R + 1) +
-                         grp * (2 * mods.R + 1);
+            float* row = rel_row(mods, hg0 + i / n_q, uw, grp);
             row[0] = fl;
             row[2 * mods.R] = fh;
           }
@@ -788,26 +806,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (store_ds) {
-        // The warp's [32 key rows][64 query columns] part of the dS^T block
-        // (head, row, kt, qs): staged in shared memory in the 128-byte swizzle
-        // (16-byte chunk e of row r at r*128 + (e ^ r%8)*16: every store
-        // instruction is conflict-free) and written by one TMA store.
+        // The warp's [32 key rows][GQ query columns] part of the dS^T block
+        // (head, row, kt, qs): staged in shared memory in the map's swizzle (128
+        // bytes: 16-byte chunk e of row r at r*128 + (e ^ r%8)*16; 64 bytes with
+        // 32 columns: r*64 + (e ^ (r/2)%4)*16; every store instruction is
+        // conflict-free) and written by one TMA store.
         const int hg = hg0 + i / n_q;
-        const int qs = (qlo - ds_row0) / kSL + (i % n_q) * (C::SL / kSL) + grp;
+        const int qs = (qlo - ds_row0) / kSL + (i % n_q) * (C::SL / kSL) + gc / kSL;
         const int rel = qs - g.dsg.first * ds_kt;
         if (rel >= 0 && rel < ds_cnt) {
           const long long blk = (static_cast<long long>(hg - p.hq0) * p.B + ds_rowb) * g.dsg.per_row + ds_off0 + rel;
           if (staged && lane == 0) bulk_wait_group_read<0>();  // the previous store has read the buffer
           __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(stg + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+          for (int e = 0; e < GQ / 8; ++e)
+            *reinterpret_cast<uint4*>(stg + lane * (2 * GQ) +
+                                      ((e ^ (GQ == 64 ? lane & 7 : (lane >> 1) & 3)) << 4)) =
                 make_uint4(pk[e / 4][4 * (e % 4)], pk[e / 4][4 * (e % 4) + 1], pk[e / 4][4 * (e % 4) + 2],
                            pk[e / 4][4 * (e % 4) + 3]);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&tds_st, stg, 0, (warp & 3) * 32, static_cast<int>(blk));
+            tma_store_3d(&tds_st, stg, gc % kSL, (warp & 3) * 32, static_cast<int>(blk));
             bulk_commit_group();
           }
           staged = true;
@@ -817,13 +837,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && n_it > 0 && (ok = mbar_wait(&bars->fin, 0, abort, p.status))) {
       tc_fence_after();
       const size_t off = row_offset(p, kvh, p.hk, p.Hkv, key_ok ? u : 0, D);
-      if (grp == 0)
-        store_row<D>(lb + T_DV, g.dv + off, 1.f, key_ok);
+      constexpr int DC = 2 * D / T::NG;  // columns of a group: the first half of the groups stores dV, the others dK
+      const int d0 = grp % (T::NG / 2) * DC;
+      if (grp < T::NG / 2)
+        store_row<DC>(lb + T_DV + d0, g.dv + off + d0, 1.f, key_ok);
       else
-        store_row<D>(lb + T_DK, g.dk + off, p.scale, key_ok);
+        store_row<DC>(lb + T_DK + d0, g.dk + off + d0, p.scale, key_ok);
     } else if (ok && n_it == 0 && key_ok) {
-      __nv_bfloat16* dst = (grp == 0 ? g.dv : g.dk) + row_offset(p, kvh, p.hk, p.Hkv, u, D);
-      for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(dst + e) = make_uint4(0, 0, 0, 0);
+      constexpr int DC = 2 * D / T::NG;
+      __nv_bfloat16* dst = (grp < T::NG / 2 ? g.dv : g.dk) + row_offset(p, kvh, p.hk, p.Hkv, u, D) + grp % (T::NG / 2) * DC;
+      for (int e = 0; e < DC; e += 8) *reinterpret_cast<uint4*>(dst + e) = make_uint4(0, 0, 0, 0);
     }
     if (staged && lane == 0) bulk_wait_group_all();  // the dS stores are complete before the CTA ends
   }
@@ -1467,7 +1490,7 @@ static int run_grad_pass(bool dq_pass, const AttnArgs& a, const M& mods, const v
     memset(&tds_st, 0, sizeof(tds_st));  // unused unless dS is stored
     memset(&tk, 0, sizeof(tk));          // unused unless K, V are shared-memory tiles
     memset(&tv, 0, sizeof(tv));
-    if (ds != nullptr && (rc = make_ds_store_tmap(&tds_st, ds, ds_blocks)) != USP_OK) return rc;
+    if (ds != nullptr && (rc = make_ds_store_tmap(&tds_st, ds, ds_blocks, C::SL / bwd::Team<M>::NG)) != USP_OK) return rc;
     if (C::KV_SMEM) {
       if ((rc = make_rows_tmap(&tk, k, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
       if ((rc = make_rows_tmap(&tv, v, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
@@ -1476,7 +1499,7 @@ static int run_grad_pass(bool dq_pass, const AttnArgs& a, const M& mods, const v
         cudaSuccess)
       return USP_ERR_CUDA;
     const unsigned grid = static_cast<unsigned>(g.n_tiles) * (a.seq_io ? a.n_kvh : a.P * a.hk);
-    bwd::dkdv_kernel<D, M><<<grid, bwd::kThreads, C::A_SMEM, st>>>(tq, tdo, tst, tds_st, tk, tv, a, g, mods);
+    bwd::dkdv_kernel<D, M><<<grid, bwd::Team<M>::THREADS, C::A_SMEM, st>>>(tq, tdo, tst, tds_st, tk, tv, a, g, mods);
   } else {
     // 128-key tiles of K and V stream past TMEM-resident Q, dO
     CUtensorMap tk, tv;

@@ -257,7 +257,7 @@ int run_fwd_window(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& 
                    float* lse, cudaStream_t st);
 
 int make_ds_tmap(CUtensorMap* m, const void* base, long long n_blocks);
-int make_ds_store_tmap(CUtensorMap* m, void* base, long long n_blocks);
+int make_ds_store_tmap(CUtensorMap* m, void* base, long long n_blocks, int cols);
 
 // Tensor map of the backward's planar statistics, fp32 [P*hq][2][pitch]: dims
 // {BS, 2, P*hq}, box {box_rows, 2, 1} (box_rows tokens of both planes of one

@@ -3,8 +3,8 @@
 // the bias by distance, and the reduction of the table's gradient.
 //
 // Workspace: the statistics of the plain backward | the bias rows by distance
-// [Hq][tab_len(R)] | partial sums of dX by distance [Hq][n_kb][2][2R+1] (one row
-// for each head, 32-key block and half of a query slice; the dK/dV pass writes
+// [Hq][tab_len(R)] | partial sums of dX by distance [Hq][n_kb][4][2R+1] (one row
+// for each head, 32-key block and quarter of a query slice; the dK/dV pass writes
 // them) | their sums over key blocks [Hq][splits][2R+1] | the stored dS blocks.
 #include "usp_attn_bwd.cuh"
 
@@ -276,7 +276,7 @@ Layout mod_layout(const usp_attn_params& p, const usp_score_mods& m) {
   Layout L{};
   L.table = L.partial = L.sums = attn_bwd_ws_bytes(p);
   L.n_kb = (p.B * p.S + 31) / 32;
-  L.n_rows = 2 * L.n_kb;
+  L.n_rows = kModGroups * L.n_kb;
   L.splits = (L.n_rows + kRelRows - 1) / kRelRows;
   if (L.splits > kRelSplits) L.splits = kRelSplits;
   size_t end = L.table;
@@ -302,11 +302,18 @@ size_t mod_ds_bytes(const usp_attn_params& p, const usp_score_mods& m) {
   return ds_geom(p, g, n, every_slice(p, m)) ? static_cast<size_t>(n) * kBN * bwd::kSL * 2 : 0;
 }
 
-// Rows by distance in the log2 domain; one block per head.
-__global__ void __launch_bounds__(kRelThreads) rel_expand_kernel(ModArgs m, float* __restrict__ table, int32_t* status) {
-  const int n = tab_len(m.R);
-  for (int e = threadIdx.x; e < n; e += kRelThreads)
-    table[static_cast<size_t>(blockIdx.x) * n + e] = table_entry(m, blockIdx.x, e, status);
+// Rows by distance in the log2 domain (the first block of a head), and cleared
+// partial sums (every block).
+__global__ void __launch_bounds__(kRelThreads)
+    rel_expand_kernel(ModArgs m, float* __restrict__ table, float4* __restrict__ clear, size_t n_clear, int32_t* status) {
+  const int n = tab_len(m.R), h = blockIdx.x;
+  if (blockIdx.y == 0)
+    for (int e = threadIdx.x; e < n; e += kRelThreads)
+      table[static_cast<size_t>(h) * n + e] = table_entry(m, h, e, status);
+  // the partial sums: distances that no chunk reaches stay at zero
+  const size_t step = static_cast<size_t>(gridDim.x) * gridDim.y * kRelThreads;
+  for (size_t i = (static_cast<size_t>(blockIdx.y) * gridDim.x + h) * kRelThreads + threadIdx.x; i < n_clear; i += step)
+    clear[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 // Sums a split's partial rows of a head: thread = distance, rows in order.
@@ -326,24 +333,30 @@ __global__ void __launch_bounds__(kRelThreads)
   }
 }
 
-// The splits' sums of a head, then its buckets: thread = bucket, distances in
-// order (no atomics: the result does not depend on the schedule).
+// The splits' sums of a head, then its buckets: a warp takes a bucket at a time,
+// its lanes the distances, joined by a fixed tree (no atomics: the result does
+// not depend on the schedule).
 __global__ void __launch_bounds__(kRelThreads)
     rel_bucket_kernel(ModArgs m, const float* __restrict__ sums, float* __restrict__ drel, int splits) {
   extern __shared__ float by_dist[];
-  const int h = blockIdx.x, row = 2 * m.R + 1;
+  const int h = blockIdx.x, row = 2 * m.R + 1, lane = threadIdx.x & 31;
+  int* bucket = reinterpret_cast<int*>(by_dist + row);
   const float* src = sums + static_cast<size_t>(h) * splits * row;
   for (int c = threadIdx.x; c < row; c += kRelThreads) {
     float acc = 0.f;
+#pragma unroll 4
     for (int s = 0; s < splits; ++s) acc += __ldg(src + static_cast<size_t>(s) * row + c);
     by_dist[c] = acc;
+    bucket[c] = min(max(__ldg(m.buckets + c), 0), m.n_buckets - 1);
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < m.n_buckets; b += kRelThreads) {
+  for (int b = threadIdx.x >> 5; b < m.n_buckets; b += kRelThreads / 32) {
     float acc = 0.f;
-    for (int c = 0; c < row; ++c)
-      if (min(max(__ldg(m.buckets + c), 0), m.n_buckets - 1) == b) acc += by_dist[c];
-    drel[static_cast<size_t>(h) * m.n_buckets + b] = acc;
+    for (int c = lane; c < row; c += 32)
+      if (bucket[c] == b) acc += by_dist[c];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (lane == 0) drel[static_cast<size_t>(h) * m.n_buckets + b] = acc;
   }
 }
 
@@ -383,11 +396,11 @@ int launch_attn_mod_bwd_preprocess(const usp_attn_params& p, const usp_score_mod
   if (sm.rel_bias != nullptr) {
     const Layout L = mod_layout(p, sm);
     uint8_t* base = static_cast<uint8_t*>(ws);
-    rel_expand_kernel<<<p.Hq, kRelThreads, 0, st>>>(m, reinterpret_cast<float*>(base + L.table), status);
+    const size_t n_clear = sm.rel_bias_grad ? (L.sums - L.partial) / sizeof(float4) : 0;
+    const int per_head = n_clear > 0 ? (4 * device_sm_count() + p.Hq - 1) / p.Hq : 1;
+    rel_expand_kernel<<<dim3(p.Hq, per_head), kRelThreads, 0, st>>>(
+        m, reinterpret_cast<float*>(base + L.table), reinterpret_cast<float4*>(base + L.partial), n_clear, status);
     if (check_launch() != USP_OK) return USP_ERR_CUDA;
-    // distances that no chunk reaches stay at zero
-    if (sm.rel_bias_grad && cudaMemsetAsync(base + L.partial, 0, L.sums - L.partial, st) != cudaSuccess)
-      return USP_ERR_CUDA;
   }
   const bool exact_delta = dsinks != nullptr || m.partial != nullptr;  // a gradient in fp32 hangs on D
   if (!exact_delta) return run_preprocess(p, o, lse, dO, nullptr, ws, status, st);
@@ -441,7 +454,7 @@ int launch_attn_mod_bwd_rel_bias(const usp_attn_params& p, const usp_score_mods&
   rel_sum_kernel<<<dim3(p.Hq, L.splits), kRelThreads, 0, st>>>(reinterpret_cast<const float*>(base + L.partial), sums,
                                                                L.n_rows, per, row);
   if (check_launch() != USP_OK) return USP_ERR_CUDA;
-  rel_bucket_kernel<<<p.Hq, kRelThreads, row * sizeof(float), st>>>(make_mods(sm), sums, drel_bias, L.splits);
+  rel_bucket_kernel<<<p.Hq, kRelThreads, row * (sizeof(float) + sizeof(int)), st>>>(make_mods(sm), sums, drel_bias, L.splits);
   return check_launch();
 }
 

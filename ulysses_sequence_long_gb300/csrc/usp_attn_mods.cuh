@@ -42,7 +42,7 @@ struct ModArgs {
   const int32_t* prefix;   // [n_prefix] or null
   int n_prefix;
   // backward: the expanded rows [Hq][tab_len(R)] (log2 domain), and the partial
-  // sums of dX by distance [Hq][n_kb][2][2R+1] (null: the table's gradient is not asked for)
+  // sums of dX by distance [Hq][n_kb][4][2R+1] (null: the table's gradient is not asked for)
   const float* table;
   float* partial;
   int n_kb;  // 32-key blocks of the rank-local tokens
@@ -69,6 +69,13 @@ auto with_mods(const ModArgs& m, F f) {
   const bool bias = m.slopes != nullptr || m.rel_bias != nullptr;
   if (m.cap > 0.f) return bias ? f(Mods<true, true>{m}) : f(Mods<true, false>{m});
   return bias ? f(Mods<false, true>{m}) : f(Mods<false, false>{m});
+}
+
+// The partial sums (distance -R at 0) of head hg over the 32 keys from `uw` and
+// query group `grp` of the dK/dV pass.
+constexpr int kModGroups = 4;
+__device__ __forceinline__ float* rel_row(const ModArgs& m, int hg, int uw, int grp) {
+  return m.partial + ((static_cast<size_t>(hg) * m.n_kb + (uw >> 5)) * kModGroups + grp) * (2 * m.R + 1);
 }
 
 // Bucket of distance index i, clamped into the table; an id outside it is reported.

@@ -40,6 +40,11 @@ import torch
 from . import binding as B_
 
 
+# Layers with modified scores: up to this many tokens the forward reads k and v from their shards (see
+# UlyssesAttention).  TOKENS_NOTE
+KV_IN_PLACE_TOKENS = 2048
+
+
 @dataclass
 class Shape:
     B: int
@@ -211,9 +216,29 @@ class UlyssesAttention:
         self._bwd_ws = None
         self.ds_groups = [(0, 0)]
         self._inputs = None  # the forward's q/k/v as the attention kernels read them
+        if self._mods is not None:
+            # One rank's shards are its head layout, byte for byte: nothing to exchange.
+            self._one_rank = P == 1
+            # Few tokens: the forward reads k and v from the shards too.  Two launches fewer; the rows strided
+            # over all key/value heads cost a long sequence, which re-reads every tile many times, 12%.
+            self._kv_in_place = self.fused and Bb * S <= KV_IN_PLACE_TOKENS
+            self._own = {n: B_.Buffer(t, n) for n, t in vars(self).items() if isinstance(t, torch.Tensor)}
+            self._prm = {}
 
     def params(self, sinks: Optional[torch.Tensor], io: Optional[int] = None, group=(0, 0)) -> B_.AttnParams:
         s = self.shape
+        if self._mods is not None:   # built once for each layout and group; only the sinks change
+            if io is None:
+                io = B_.USP_IO_SEQ if self.fused else B_.USP_IO_HEAD
+            prm = self._prm.get((io, group))
+            if prm is None:
+                prm = self._prm[io, group] = B_.attn_params(
+                    s.B, s.S, s.Hq, s.Hkv, s.D, s.P, self.cu_seqlens, self.n_docs, s.causal, s.window_left,
+                    s.softmax_scale, None, io, head_first=group[0], head_count=group[1])
+            if sinks is not None and sinks.numel() != s.Hq:
+                raise ValueError(f"sinks must hold one logit per query head ({s.Hq}), got {sinks.numel()}")
+            prm.sinks = B_._dev(sinks, "sinks", torch.float32)
+            return prm
         if io is None:
             io = B_.USP_IO_SEQ if self.fused else B_.USP_IO_HEAD
         return B_.attn_params(s.B, s.S, s.Hq, s.Hkv, s.D, s.P, self.cu_seqlens, self.n_docs, s.causal,
@@ -224,11 +249,31 @@ class UlyssesAttention:
             self._bwd_ws, self.stored_ds, self.ds_groups = backward_workspace(
                 prm, self.lse.device, self.stored_ds, self.shape.Hkv, groups_ok=self.fused,
                 group_size=self.ds_group_size, mods=self._mods)
+            if self._mods is not None:
+                self._own["ws"] = B_.Buffer(self._bwd_ws, "ws")
         return self._bwd_ws
+
+    def _handle(self, stream):
+        """The CUDA stream of a whole pass, looked up once."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.lse.device)
+        return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+    def _check_shards(self, t, name, H):
+        s = self.shape
+        B_._dev(t, name, torch.bfloat16)
+        if t.numel() != s.B * s.S * H * s.D or t.device != self.lse.device:
+            raise ValueError(f"{name} must be the shards [{s.P}][{s.B}][{s.S // s.P}][{H}][{s.D}] on {self.lse.device}")
 
     # -- steps ---------------------------------------------------------------
     def exchange_qkv(self, q_seq, k_seq, v_seq, stream=None):
         s = self.shape
+        if self._mods is not None:
+            for t, name, H in ((q_seq, "q", s.Hq), (k_seq, "k", s.Hkv), (v_seq, "v", s.Hkv)):
+                self._check_shards(t, name, H)
+            if self._one_rank or self._kv_in_place:
+                self._inputs = (q_seq, k_seq, v_seq)
+                return
         if self.fused:
             # q stays in its shards; k and v go to head layout for the forward
             B_.usp_relayout_fwd(k_seq, self.k_head, s.B, s.S, s.Hkv, s.D, s.P, stream)
@@ -241,16 +286,30 @@ class UlyssesAttention:
 
     def boundaries(self, pos_shards, stream=None):
         s = self.shape
+        if self._mods is not None:
+            if pos_shards.numel() != s.B * s.S:
+                raise ValueError(f"position ids must cover {s.B} x {s.S} tokens, got {pos_shards.numel()}")
+            o = self._own
+            B_.usp_cu_seqlens_from_position_ids(pos_shards, s.B, s.S, s.P, o["cu_seqlens"], o["n_docs"], o["max_len"],
+                                                o["scan_ws"], o["status"], stream)
+            return
         B_.usp_cu_seqlens_from_position_ids(pos_shards, s.B, s.S, s.P, self.cu_seqlens, self.n_docs,
                                             self.max_len, self.scan_ws, self.status, stream)
 
     def attention(self, sinks=None, stream=None):
         q, k, v = self._inputs
         if self._mods is not None:
-            prm = self.params(sinks, B_.USP_IO_SEQ_KV_HEAD if self.fused else None)
-            kv = (self.k_head, self.v_head) if self.fused else (k, v)
-            B_.usp_attn_mod_fwd(prm, self._mods, q, *kv, self.o_seq if self.fused else self.o_head, self.lse,
-                                self.status, stream)
+            own = self._own
+            o = own["o_seq" if self.fused or self._one_rank else "o_head"]
+            if self._one_rank:
+                io = B_.USP_IO_HEAD
+            elif self._kv_in_place:
+                io = B_.USP_IO_SEQ
+            elif self.fused:
+                io, k, v = B_.USP_IO_SEQ_KV_HEAD, own["k_head"], own["v_head"]
+            else:
+                io, q, k, v = B_.USP_IO_HEAD, own["q_head"], own["k_head"], own["v_head"]
+            B_.usp_attn_mod_fwd(self.params(sinks, io), self._mods, q, k, v, o, own["lse"], own["status"], stream)
         elif self.fused:
             B_.usp_attn_fwd(self.params(sinks, B_.USP_IO_SEQ_KV_HEAD), q, self.k_head, self.v_head, self.o_seq,
                             self.lse, self.status, stream)
@@ -259,11 +318,15 @@ class UlyssesAttention:
 
     def exchange_out(self, stream=None):
         s = self.shape
+        if self._mods is not None and self._one_rank:
+            return
         if not self.fused:
             B_.usp_relayout_bwd(self.o_head, self.o_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
 
     def forward(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None):
         """Sequence shards in, sequence shards out (``self.o_seq``)."""
+        if self._mods is not None:
+            stream = self._handle(stream)
         self.exchange_qkv(q_seq, k_seq, v_seq, stream)
         self.boundaries(pos_shards, stream)
         self.attention(sinks, stream)
@@ -278,6 +341,8 @@ class UlyssesAttention:
         after the last group and `group_marks(g, 0)` / `group_marks(g, 1)`
         after group g's dK/dV and dQ passes."""
         s = self.shape
+        if self._mods is not None:
+            return self._mod_backward(do_seq, sinks, self._handle(stream), marks, group_marks)
         prm = self.params(sinks)
         ws = self._ws(prm)
         mark = marks or (lambda i: None)
@@ -289,42 +354,72 @@ class UlyssesAttention:
             B_.usp_relayout_fwd(do_seq, self.do_head, s.B, s.S, s.Hq, s.D, s.P, stream)
             do, o, dq, dk, dv = self.do_head, self.o_head, self.dq_head, self.dk_head, self.dv_head
         mark(1)
-        dsinks = self.dsinks if sinks is not None else None
-        mods = self._mods
-        if mods is not None:
-            def dkdv(prm):
-                B_.usp_attn_mod_bwd_dkdv(prm, mods, q, k, v, do, dk, dv, ws, self.status, stream)
-
-            def dq_pass(prm):
-                B_.usp_attn_mod_bwd_dq(prm, mods, q, k, v, do, dq, ws, self.status, stream)
-
-            B_.usp_attn_mod_bwd_preprocess(prm, mods, q, k, v, o, self.lse, do, dsinks, ws, self.status, stream)
-        else:
-            def dkdv(prm):
-                B_.usp_attn_bwd_dkdv(prm, q, k, v, self.lse, do, dk, dv, ws, self.status, stream)
-
-            def dq_pass(prm):
-                B_.usp_attn_bwd_dq(prm, q, k, v, self.lse, do, dq, ws, self.status, stream)
-
-            B_.usp_attn_bwd_preprocess(prm, o, self.lse, do, dsinks, ws, self.status, stream)
+        B_.usp_attn_bwd_preprocess(prm, o, self.lse, do, self.dsinks if sinks is not None else None, ws,
+                                   self.status, stream)
         mark(2)
         if len(self.ds_groups) == 1:
-            dkdv(prm)
+            B_.usp_attn_bwd_dkdv(prm, q, k, v, self.lse, do, dk, dv, ws, self.status, stream)
             mark(3)
-            dq_pass(prm)
+            B_.usp_attn_bwd_dq(prm, q, k, v, self.lse, do, dq, ws, self.status, stream)
         else:  # stored dS a key/value head group at a time (both passes per group)
             gmark = group_marks or (lambda g, i: None)
             for gi, grp in enumerate(self.ds_groups):
                 prm_g = self.params(None, group=grp)
-                dkdv(prm_g)
+                B_.usp_attn_bwd_dkdv(prm_g, q, k, v, self.lse, do, dk, dv, ws, self.status, stream)
                 gmark(gi, 0)
-                dq_pass(prm_g)
+                B_.usp_attn_bwd_dq(prm_g, q, k, v, self.lse, do, dq, ws, self.status, stream)
                 gmark(gi, 1)
             mark(3)
-        if mods is not None and mods.rel_bias_grad:
-            B_.usp_attn_mod_bwd_rel_bias(prm, mods, self.drel_bias, ws, stream)
         mark(4)
         if not self.fused:
+            B_.usp_relayout_bwd(self.dq_head, self.dq_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
+            B_.usp_relayout_bwd(self.dk_head, self.dk_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
+            B_.usp_relayout_bwd(self.dv_head, self.dv_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
+        mark(5)
+        return self.dq_seq, self.dk_seq, self.dv_seq
+
+    def _mod_backward(self, do_seq, sinks, stream, marks, group_marks):
+        """``backward_phases`` with modified scores: one library call where no one asks for its phases and
+        the stored dS holds every head."""
+        s, own, mods = self.shape, self._own, self._mods
+        prm = self.params(sinks)
+        self._ws(prm)
+        ws = own["ws"]
+        mark = marks or (lambda i: None)
+        in_place = self.fused or self._one_rank      # the tensors of the call are the shards
+        lay = "_seq" if in_place else "_head"
+        q, k, v = self._inputs if in_place else (own["q_head"], own["k_head"], own["v_head"])
+        o, dq, dk, dv = (own[n + lay] for n in ("o", "dq", "dk", "dv"))
+        lse, status = own["lse"], own["status"]
+        dsinks = own["dsinks"] if sinks is not None else None
+        drel = own["drel_bias"] if mods.rel_bias_grad else None
+        self._check_shards(do_seq, "do", s.Hq)
+        mark(0)
+        do = do_seq
+        if not in_place:
+            B_.usp_relayout_fwd(do_seq, self.do_head, s.B, s.S, s.Hq, s.D, s.P, stream)
+            do = own["do_head"]
+        mark(1)
+        if marks is None and len(self.ds_groups) == 1:
+            B_.usp_attn_mod_bwd(prm, mods, q, k, v, o, lse, do, dq, dk, dv, dsinks, drel, ws, status, stream)
+        else:
+            gmark = group_marks or (lambda g, i: None)
+            B_.usp_attn_mod_bwd_preprocess(prm, mods, q, k, v, o, lse, do, dsinks, ws, status, stream)
+            mark(2)
+            one = len(self.ds_groups) == 1
+            for gi, grp in enumerate(self.ds_groups):
+                prm_g = prm if one else self.params(None, group=grp)
+                B_.usp_attn_mod_bwd_dkdv(prm_g, mods, q, k, v, do, dk, dv, ws, status, stream)
+                mark(3) if one else gmark(gi, 0)
+                B_.usp_attn_mod_bwd_dq(prm_g, mods, q, k, v, do, dq, ws, status, stream)
+                if not one:
+                    gmark(gi, 1)
+            if not one:
+                mark(3)
+            if drel is not None:
+                B_.usp_attn_mod_bwd_rel_bias(prm, mods, drel, ws, stream)
+        mark(4)
+        if not in_place:
             B_.usp_relayout_bwd(self.dq_head, self.dq_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
             B_.usp_relayout_bwd(self.dk_head, self.dk_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
             B_.usp_relayout_bwd(self.dv_head, self.dv_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
@@ -335,21 +430,15 @@ class UlyssesAttention:
         """dO shards in; dQ/dK/dV shards out (``self.dq_seq`` ...), dsinks.
         In explicit mode this is the single ``usp_attn_bwd`` (or
         ``usp_attn_mod_bwd``) call."""
-        if self.fused:
+        if self.fused or self._mods is not None:
             return self.backward_phases(do_seq, sinks, stream)
         s = self.shape
         prm = self.params(sinks)
         ws = self._ws(prm)
         q, k, v = self._inputs
         B_.usp_relayout_fwd(do_seq, self.do_head, s.B, s.S, s.Hq, s.D, s.P, stream)
-        dsinks = self.dsinks if sinks is not None else None
-        if self._mods is not None:
-            B_.usp_attn_mod_bwd(prm, self._mods, q, k, v, self.o_head, self.lse, self.do_head, self.dq_head,
-                                self.dk_head, self.dv_head, dsinks, self.drel_bias if self._mods.rel_bias_grad else None,
-                                ws, self.status, stream)
-        else:
-            B_.usp_attn_bwd(prm, q, k, v, self.o_head, self.lse, self.do_head, self.dq_head, self.dk_head,
-                            self.dv_head, dsinks, ws, self.status, stream)
+        B_.usp_attn_bwd(prm, q, k, v, self.o_head, self.lse, self.do_head, self.dq_head, self.dk_head,
+                        self.dv_head, self.dsinks if sinks is not None else None, ws, self.status, stream)
         B_.usp_relayout_bwd(self.dq_head, self.dq_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
         B_.usp_relayout_bwd(self.dk_head, self.dk_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
         B_.usp_relayout_bwd(self.dv_head, self.dv_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
