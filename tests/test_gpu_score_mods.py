@@ -196,8 +196,9 @@ def test_parity(c, fused, stored_ds):
 
 
 def test_without_mods_equals_the_plain_attention():
-    """No cap, bias or prefix: the same sums as the plain kernels from the same layout (in the fused one a short
-    layer reads k and v from the shards, whose key tiles start elsewhere)."""
+    """No cap, bias or prefix: the plain attention.  The row sums join in another order (half a row at a time):
+    the LSE differs by the roundings of at most 512 positive terms added in chains of at most 128, under 128 half
+    steps of the sum, 128 2^-24 = 7.6e-6 of its logarithm, and a rounding of the result (below 8: 2.4e-7)."""
     from ulysses_sequence_long_gb300.pipeline import Shape, UlyssesAttention
     c = next(x for x in CASES if x.w.name == "none")
     t, pos, kw = _inputs(c)
@@ -207,7 +208,7 @@ def test_without_mods_equals_the_plain_attention():
     plain = UlyssesAttention(Shape(w.B, w.S, w.Hq, w.Hkv, w.D, w.P), fused=False)
     plain.forward(d["q"], d["k"], d["v"], torch.from_numpy(pos).cuda(), sinks)
     torch.cuda.synchronize()
-    assert torch.equal(plain.lse, ua.lse)
+    assert (plain.lse - ua.lse).abs().max().item() <= 8e-6
     assert_close("o", _np(ua.o_seq), _np(plain.o_seq))
 
 

@@ -20,7 +20,7 @@ size_t attn_bwd_ds_bytes(const usp_attn_params& p) {
 // 1. D = rowsum(dO * O) and -LSE*log2e into the workspace, then the sink gradients.
 int launch_attn_bwd_preprocess(const usp_attn_params& prm, const void* o, const float* lse, const void* dO,
                                float* dsinks, void* ws, int32_t* status, cudaStream_t st) {
-  return run_preprocess(prm, o, lse, dO, dsinks, ws, status, st);
+  return run_preprocess(prm, NoMods{}, o, lse, dO, dsinks, ws, status, st);
 }
 
 // The stored-dS region of the workspace (after the statistics), or null when

@@ -76,10 +76,10 @@ __device__ __forceinline__ size_t plane_index(int bsp, int hq, int r, int j, int
 // one contiguous run.
 constexpr int kPreTok = 32;  // the most tokens of a chunk
 
-template <int D>
+template <int D, class M>
 __global__ void __launch_bounds__(256) preprocess_kernel(const uint4* __restrict__ o, const uint4* __restrict__ dO,
                                                          const float* __restrict__ lse, float* __restrict__ stats,
-                                                         AttnArgs p, int bsp, int n_chunks, int tok) {
+                                                         AttnArgs p, int bsp, int n_chunks, int tok, M mods) {
   constexpr int LPR = D / 8;           // 16-byte lanes per row
   // passes whose loads are issued before any of them is reduced, so that
   // enough bytes are in flight (D = 64 rows are short; D = 128 keeps one)
@@ -139,7 +139,11 @@ __global__ void __launch_bounds__(256) preprocess_kernel(const uint4* __restrict
         const int r = p.seq_io ? h / p.hq : r0, j = p.seq_io ? h - r * p.hq : h, t = t0 + k;
         // a row that sees nothing (LSE = -inf) keeps -inf, so that its weights are 2^-inf = 0
         const float l = __ldg(lse + stat_index(p, r, j, t));
-        stats[plane_index(bsp, p.hq, r, j, 0, t)] = l == -INFINITY ? l : l * -kLog2e;
+        float nl = l == -INFINITY ? l : l * -kLog2e;
+        if constexpr (bias_on<M>) {
+          if (mods.slopes != nullptr) nl -= slope_of_row(mods, __ldg(mods.slopes + r * p.hq + j) * kLog2E, t);
+        }
+        stats[plane_index(bsp, p.hq, r, j, 0, t)] = nl;
         stats[plane_index(bsp, p.hq, r, j, 1, t)] = dsum[idx];
       }
     }
@@ -354,6 +358,7 @@ struct Grads {
   int n_tiles;         // 128-token tiles per rank
   __nv_bfloat16* ds;   // stored dS blocks, or null (the dQ pass recomputes S and dP)
   DsGeom dsg;
+  int split;           // modified scores: CTAs of a cluster that share a key tile's query heads (dK/dV; else 1)
 };
 
 // --------------------------------------------------------------- dK / dV
@@ -385,7 +390,8 @@ struct Team {
   static constexpr int WP = 4 * NG;  // producer warp (the MMA warp is WP + 1)
 };
 
-template <int D, class M>
+// SPLIT: a key tile's query heads are shared by the g.split CTAs of a cluster.
+template <int D, class M, bool SPLIT>
 __global__ void __launch_bounds__(Team<M>::THREADS, 1)
     dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                 const __grid_constant__ CUtensorMap tst, const __grid_constant__ CUtensorMap tds_st,
@@ -409,11 +415,15 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
   // summed by the exchange back), in seq-layout the global head, whose
   // gradient sums the whole group of Hq/Hkv query heads over the ranks.
   const int per = p.seq_io ? p.n_kvh : p.P * p.hk;
-  const int kt = static_cast<int>(blockIdx.x) / per;
-  const int unit = static_cast<int>(blockIdx.x) % per;
+  const int split = SPLIT ? g.split : 1, part = SPLIT ? static_cast<int>(blockIdx.x) % split : 0;
+  const int cta = static_cast<int>(blockIdx.x) / split;
+  const int kt = cta / per;
+  const int unit = cta % per;
   const HeadRef kvh = p.seq_io ? HeadRef{0, 0, p.kvh0 + unit} : kv_head_ref(p, unit / p.hk, unit % p.hk);
-  const int n_heads = p.seq_io ? p.Hq / p.Hkv : p.G;
-  const int hg0 = p.seq_io ? (p.kvh0 + unit) * n_heads : kvh.r * p.hq + kvh.j * p.G;  // first query head (global)
+  const int n_group = p.seq_io ? p.Hq / p.Hkv : p.G;
+  const int n_heads = n_group / split;  // of this CTA
+  const int hg0 = (p.seq_io ? (p.kvh0 + unit) * n_group : kvh.r * p.hq + kvh.j * p.G) +
+                  part * n_heads;  // first query head (global)
   const int u0 = kt * kBN;
 
   const int n_docs = checked_docs(p);
@@ -438,7 +448,7 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
     qlo &= ~(kBM - 1);
     qhi = (qhi + kBM - 1) & ~(kBM - 1);
   } else {
-    qlo &= p.seq_io ? ~(C::SL - 1) : ~3;
+    qlo &= p.seq_io ? ~(C::SL - 1) : M::on ? ~31 : ~3;  // Mods: see slope_of_row
   }
   const int n_q = qhi > qlo ? (qhi - qlo + C::SL - 1) / C::SL : 0;
   const int n_it = n_heads * n_q;
@@ -662,14 +672,16 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
         if constexpr (M::on) {
           const int d0 = q0 + 32 * c - u, dw = q0 + 32 * c - uw;
           Affine f{p.scale_log2, 0.f};
-          if constexpr (M::bias_on) f = add_bias<32, 1>(x, tab, mods.R, slope2, d0, dw - 31, dw + 31, p.scale_log2);
+          if constexpr (M::bias_on)
+            f = add_bias_of_key(x, tab, mods.R, slope2, !M::cap_on, d0, dw - 31, dw + 31, mods.later_hidden,
+                                p.scale_log2);
           if constexpr (M::cap_on) {
-            cap_scores(x, f, mods.cap);
-            cap_slope(x, gf);
-            f = {mods.cap * kLog2E, 0.f};
+            const float k = cap_scores<false>(x, f, mods.cap, M::bias_on);
+            cap_slope(x, gf, k);
+            f = {k * mods.cap * kLog2E, 0.f};
           }
           if constexpr (M::bias_on && !M::cap_on) {
-            if (f.off != 0.f) {
+            if (slope2 != 0.f || f.off != 0.f) {  // (uniform: without a slope the offset is a table's end)
               const uint64_t a2 = f2_pack(f.sc, f.sc), o2 = f2_pack(f.off, f.off);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
@@ -834,23 +846,65 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
         }
       }
     }
+    constexpr int DC = 2 * D / T::NG;  // columns of a group: the first half of the groups stores dV, the others dK
+    const bool is_dv = grp < T::NG / 2;
+    const int d0 = grp % (T::NG / 2) * DC;
     if (ok && n_it > 0 && (ok = mbar_wait(&bars->fin, 0, abort, p.status))) {
       tc_fence_after();
       const size_t off = row_offset(p, kvh, p.hk, p.Hkv, key_ok ? u : 0, D);
-      constexpr int DC = 2 * D / T::NG;  // columns of a group: the first half of the groups stores dV, the others dK
-      const int d0 = grp % (T::NG / 2) * DC;
-      if (grp < T::NG / 2)
-        store_row<DC>(lb + T_DV + d0, g.dv + off + d0, 1.f, key_ok);
-      else
-        store_row<DC>(lb + T_DK + d0, g.dk + off + d0, p.scale, key_ok);
+      const uint32_t acc = lb + (is_dv ? T_DV : T_DK) + d0;
+      if constexpr (!SPLIT) {
+        store_row<DC>(acc, (is_dv ? g.dv : g.dk) + off + d0, is_dv ? 1.f : p.scale, key_ok);
+      } else {
+        // this CTA's sums, fp32, over the slices' shared memory (every copy into it
+        // has landed and every product has read it); see the tail of the kernel
+        float4* row = reinterpret_cast<float4*>(smem + C::A_Q + (is_dv ? 0 : kBN * D * 4) + krow * D * 4);
+#pragma unroll 1
+        for (int c = 0; c < DC / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(acc + c * 32, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            row[((d0 + c * 32) / 4 + e) ^ (krow & 7)] =
+                make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
+                            __uint_as_float(v[4 * e + 3]));
+        }
+      }
     } else if (ok && n_it == 0 && key_ok) {
-      constexpr int DC = 2 * D / T::NG;
-      __nv_bfloat16* dst = (grp < T::NG / 2 ? g.dv : g.dk) + row_offset(p, kvh, p.hk, p.Hkv, u, D) + grp % (T::NG / 2) * DC;
+      __nv_bfloat16* dst = (is_dv ? g.dv : g.dk) + row_offset(p, kvh, p.hk, p.Hkv, u, D) + d0;
       for (int e = 0; e < DC; e += 8) *reinterpret_cast<uint4*>(dst + e) = make_uint4(0, 0, 0, 0);
     }
     if (staged && lane == 0) bulk_wait_group_all();  // the dS stores are complete before the CTA ends
   }
 
+  if constexpr (SPLIT) {
+    // A key tile's query heads shared by a cluster: each CTA adds up the cluster's
+    // sums of its share of the rows, in the CTAs' order, and stores them.
+    if (n_it > 0) {
+      cluster_sync();
+      if (warp < T::WP) {
+        const int rows = kBN / split;
+        for (int i = tid; i < 2 * rows * (D / 4); i += 4 * T::NG * 32) {
+          const int c = i % (D / 4), rr = i / (D / 4), is_dk = rr / rows, row = part * rows + rr % rows;
+          const uint32_t at = sbase + C::A_Q + is_dk * (kBN * D * 4) + row * D * 4 + ((c ^ (row & 7)) << 4);
+          float4 sum = ld_cluster(at, 0);
+          for (int o = 1; o < split; ++o) {
+            const float4 x = ld_cluster(at, o);
+            sum.x += x.x;
+            sum.y += x.y;
+            sum.z += x.z;
+            sum.w += x.w;
+          }
+          const float mul = is_dk ? p.scale : 1.f;
+          if (u0 + row < p.BS)
+            *reinterpret_cast<uint2*>((is_dk ? g.dk : g.dv) + row_offset(p, kvh, p.hk, p.Hkv, u0 + row, D) + 4 * c) =
+                make_uint2(pack_bf16x2(sum.x * mul, sum.y * mul), pack_bf16x2(sum.z * mul, sum.w * mul));
+        }
+      }
+      cluster_sync();  // the sums stay in place until every CTA has read them
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -1014,6 +1068,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (row_ok) {
       doc_bounds(p, mods, n_docs, t, a, b, pe);
       nlse2 = __ldg(g.stats + plane_index(g.bsp, p.hq, r, j, 0, t));
+      if constexpr (bias_on<M>) {
+        if (mods.slopes != nullptr) nlse2 += slope_of_row(mods, __ldg(mods.slopes + hg) * kLog2E, t);
+      }
       dvt = __ldg(g.stats + plane_index(g.bsp, p.hq, r, j, 1, t));
     }
     a = max(a, rk0);  // a ring step: one key/value super-chunk only
@@ -1042,11 +1099,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       Affine f{p.scale_log2, 0.f};
       if constexpr (M::on) {
         const int d0 = t - k0, dw = d0 - lane;
-        if constexpr (M::bias_on) f = add_bias<64, -1>(x, tab, mods.R, slope2, d0, dw - 63, dw + 31, p.scale_log2);
+        if constexpr (M::bias_on)
+          f = add_bias(x, tab, mods.R, slope2, nullptr, d0, dw - 63, dw + 31, mods.later_hidden, p.scale_log2);
         if constexpr (M::cap_on) {
-          cap_scores(x, f, mods.cap);
-          cap_slope(x, gf);
-          f = {mods.cap * kLog2E, 0.f};
+          const float k = cap_scores<false>(x, f, mods.cap, M::bias_on);
+          cap_slope(x, gf, k);
+          f = {k * mods.cap * kLog2E, 0.f};
         }
       }
       if (!(c_lo <= 0 && c_hi >= 63)) {
@@ -1415,8 +1473,9 @@ static inline AttnArgs make_args(const usp_attn_params& prm, int32_t* status) {
 }
 
 // D = rowsum(dO * O) and -LSE*log2e into the workspace, then the sink gradients.
-static inline int run_preprocess(const usp_attn_params& prm, const void* o, const float* lse, const void* dO,
-                                 float* dsinks, void* ws, int32_t* status, cudaStream_t st) {
+template <class M>
+static int run_preprocess(const usp_attn_params& prm, const M& mods, const void* o, const float* lse, const void* dO,
+                          float* dsinks, void* ws, int32_t* status, cudaStream_t st) {
   const AttnArgs a = make_args(prm, status);
   float* stats = static_cast<float*>(ws);
   const int bsp = stats_row_pitch(a.BS);
@@ -1428,11 +1487,11 @@ static inline int run_preprocess(const usp_attn_params& prm, const void* o, cons
   const int n_chunks = chunks_of(tok);
   const int smem = Hb * tok * static_cast<int>(sizeof(float));
   int grid = n_chunks < device_sm_count() * 8 ? n_chunks : device_sm_count() * 8;
-  auto kern = prm.D == 128 ? bwd::preprocess_kernel<128> : bwd::preprocess_kernel<64>;
+  auto kern = prm.D == 128 ? bwd::preprocess_kernel<128, M> : bwd::preprocess_kernel<64, M>;
   if (smem > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return USP_ERR_CUDA;
   kern<<<grid, 256, smem, st>>>(static_cast<const uint4*>(o), static_cast<const uint4*>(dO), lse, stats, a, bsp,
-                                n_chunks, tok);
+                                n_chunks, tok, mods);
   if (check_launch() != USP_OK) return USP_ERR_CUDA;
   if (dsinks != nullptr && a.sinks != nullptr) {
     bwd::dsink_kernel<<<a.P * a.hq, 256, 0, st>>>(stats, dsinks, a, bsp);
@@ -1461,7 +1520,7 @@ static int run_grad_pass(bool dq_pass, const AttnArgs& a, const M& mods, const v
   bwd::Grads g{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
                static_cast<const __nv_bfloat16*>(v), static_cast<const __nv_bfloat16*>(dO),
                static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv),
-               stats, stats_row_pitch(a.BS), (a.BS + kBM - 1) / kBM, static_cast<__nv_bfloat16*>(ds), dsg};
+               stats, stats_row_pitch(a.BS), (a.BS + kBM - 1) / kBM, static_cast<__nv_bfloat16*>(ds), dsg, 1};
   int rc;
   if (dq_pass && ds != nullptr) {
     // dQ = dS K from the blocks the dK/dV pass stored
@@ -1495,11 +1554,34 @@ static int run_grad_pass(bool dq_pass, const AttnArgs& a, const M& mods, const v
       if ((rc = make_rows_tmap(&tk, k, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
       if ((rc = make_rows_tmap(&tv, v, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
     }
-    if (cudaFuncSetAttribute(bwd::dkdv_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::A_SMEM) !=
-        cudaSuccess)
-      return USP_ERR_CUDA;
     const unsigned grid = static_cast<unsigned>(g.n_tiles) * (a.seq_io ? a.n_kvh : a.P * a.hk);
-    bwd::dkdv_kernel<D, M><<<grid, bwd::Team<M>::THREADS, C::A_SMEM, st>>>(tq, tdo, tst, tds_st, tk, tv, a, g, mods);
+    if constexpr (M::on) {
+      // Few key tiles and heads: split a group's query heads over a cluster while twice the CTAs still fit the
+      // GPU twice (2048 tokens, 4 key/value heads of 4 query heads, D = 128: 64 CTAs 219 us, 256 CTAs 90 us)
+      const int group = a.seq_io ? a.Hq / a.Hkv : a.G;
+      while (g.split < 8 && group % (2 * g.split) == 0 && grid * 2 * g.split <= 2u * device_sm_count()) g.split *= 2;
+      if (g.split > 1) {
+        auto kern = bwd::dkdv_kernel<D, M, true>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::A_SMEM) != cudaSuccess)
+          return USP_ERR_CUDA;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim = {static_cast<unsigned>(g.split), 1, 1};
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(grid * g.split);
+        cfg.blockDim = dim3(bwd::Team<M>::THREADS);
+        cfg.dynamicSmemBytes = C::A_SMEM;
+        cfg.stream = st;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, tq, tdo, tst, tds_st, tk, tv, a, g, mods) == cudaSuccess ? USP_OK
+                                                                                                        : USP_ERR_CUDA;
+      }
+    }
+    auto kern = bwd::dkdv_kernel<D, M, false>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::A_SMEM) != cudaSuccess)
+      return USP_ERR_CUDA;
+    kern<<<grid, bwd::Team<M>::THREADS, C::A_SMEM, st>>>(tq, tdo, tst, tds_st, tk, tv, a, g, mods);
   } else {
     // 128-key tiles of K and V stream past TMEM-resident Q, dO
     CUtensorMap tk, tv;

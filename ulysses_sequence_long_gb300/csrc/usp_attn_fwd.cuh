@@ -52,10 +52,13 @@ constexpr int kRel = 8;
 // core, 512 TMEM columns, one CTA per SM) or 1 (one softmax warpgroup; at
 // D = 64 its 192 TMEM columns and 82 KB of shared memory let two CTAs share
 // an SM, which then overlap each other's latencies).
-template <int D, int NQT>
+// NH softmax warpgroups per Q tile: 1 (a thread takes a whole row) or, with
+// modified scores, 2 (a thread takes half of a row's keys; the halves meet in the
+// row's maximum and sum through shared memory).
+template <int D, int NQT, int NH = 1>
 struct Cfg {
-  static constexpr int THREADS = 128 * NQT + 64;      // softmax warpgroups, producer warp, MMA warp
-  static constexpr int WP = 4 * NQT;                  // producer warp (the MMA warp is WP + 1)
+  static constexpr int THREADS = 128 * NQT * NH + 64;  // softmax warpgroups, producer warp, MMA warp
+  static constexpr int WP = 4 * NQT * NH;              // producer warp (the MMA warp is WP + 1)
   static constexpr int CTAS = (NQT == 1 && D == 64) ? 2 : 1;  // CTAs per SM
   static constexpr uint32_t TCOLS = NQT == 2 ? 512 : 256;     // TMEM columns allocated
   static constexpr int NCH = D / 64;                  // 64-wide column atoms per row
@@ -66,8 +69,11 @@ struct Cfg {
   static constexpr int OFF_K = OFF_Q + NQT * TILE;
   static constexpr int OFF_V = OFF_K + ST * TILE;
   static constexpr int OFF_BAR = OFF_V + ST * TILE;
-  static constexpr int SMEM = OFF_BAR + 1024 + 1024;  // barriers + alignment slack
-  static constexpr int OFF_TAB = OFF_BAR + 1024;      // Mods: the head's bias row by distance (SMEM grows by it)
+  static constexpr int XBYTES = NH == 2 ? 2 * NQT * 2 * kBM * 4 : 0;  // [2 buffers][tile][half][row] floats
+  static constexpr int OFF_RAMP = OFF_BAR + 512;      // Mods: slope times column (128 floats)
+  static constexpr int OFF_X = OFF_BAR + 1024;        // NH = 2: what the halves of a row exchange
+  static constexpr int OFF_TAB = OFF_X + XBYTES;      // Mods: the head's bias row by distance (SMEM grows by it)
+  static constexpr int SMEM = OFF_BAR + 1024 + XBYTES + 1024;  // barriers, exchange, alignment slack
   static constexpr uint32_t T_O = 128 * NQT;          // first O column (S_q at 128q)
 };
 
@@ -77,6 +83,7 @@ struct Bars {
   uint64_t p_full[2];
   uint64_t o_final[2];
   uint64_t mma_done;
+  uint64_t x_full[2];  // NH = 2: both halves of the tile's rows have written their exchange values
   // Four stages (KV_ONE): kv_full[s] = K and V of the tile in stage s
   // landed (V has time to land before S, so PV needs no wait of its own).
   // Two stages: K_0 signals k_first, and kv_full[m % 2] = V_m and K_{m+1}
@@ -90,17 +97,25 @@ struct Bars {
   int abort;
 };
 
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
 struct Out {
   __nv_bfloat16* o;
   float* lse;
   int nqb;  // query blocks (NQT tiles of 128 rows) per (rank, head)
 };
 
+// Halves of a row's keys (see Cfg).  With modified scores a row's chain from S to P
+// is longer, and 8 softmax warps do not hide it (SPLITNOTE).
+template <class M>
+constexpr int kHalves = M::on ? 2 : 1;
+
 template <int D, int NQT, class M>
-__global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
+__global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>::CTAS)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, AttnArgs p, Out out, M mods) {
-  using C = Cfg<D, NQT>;
+  constexpr int NH = kHalves<M>, NC = kBN / NH;  // columns of a thread
+  using C = Cfg<D, NQT, NH>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
@@ -147,8 +162,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
     // no key to see (a ring step whose block lies after these rows): O = 0 and
     // LSE = the sink logit alone, or -inf
     if (warp < C::WP) {
-      const int q = warp >> 2, t = t0 + q * kBM + (tid & 127);
-      if (tile_ok[q] && t < p.BS) {
+      const int q = (warp >> 2) / NH, t = t0 + q * kBM + (tid & 127);
+      if (tile_ok[q] && t < p.BS && (warp >> 2) % NH == 0) {
         uint4* dst = reinterpret_cast<uint4*>(out.o + row_offset(p, qh, p.hq, p.Hq, t, D));
         for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0, 0, 0, 0);
         const int bb = t / p.S, ss = t - bb * p.S;
@@ -163,7 +178,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
     for (int q = 0; q < NQT; ++q) {
       mbar_init(&bars->q_full[q], 1);
       mbar_init(&bars->s_full[q], 1);
-      mbar_init(&bars->p_full[q], 4);
+      mbar_init(&bars->p_full[q], 4 * NH);
+      mbar_init(&bars->x_full[q], 4 * NH);
       mbar_init(&bars->o_final[q], 1);
     }
     mbar_init(&bars->mma_done, 1);
@@ -177,6 +193,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
     fence_barrier_init();
   }
   if constexpr (M::on) {
+    if (M::bias_on && mods.slopes != nullptr && tid < kBN)
+      reinterpret_cast<float*>(smem + C::OFF_RAMP)[tid] = __ldg(mods.slopes + r * p.hq + j) * kLog2E * static_cast<float>(tid);
     if (M::bias_on && mods.rel_bias != nullptr)
       for (int e = tid; e < tab_len(mods.R); e += C::THREADS)
         reinterpret_cast<float*>(smem + C::OFF_TAB)[e] = table_entry(mods, r * p.hq + j, e, p.status);
@@ -276,8 +294,9 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
       auto issue_pv = [&](int q, int st, bool acc) {
         const uint64_t vd = sdesc_sw128(sbase + C::OFF_V + st * C::TILE, kAtomBytes, 1024);
 #pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          mma_ts(tmem + C::T_O + q * D, tmem + q * kBN + kk * 8, sdesc_add(vd, kk * 16 * 128), idesc_o,
+        for (int kk = 0; kk < kBN / 16; ++kk)  // P of half h sits in columns NC h .. NC h + NC / 2
+          mma_ts(tmem + C::T_O + q * D, tmem + q * kBN + kk / (8 / NH) * NC + kk % (8 / NH) * 8,
+                 sdesc_add(vd, kk * 16 * 128), idesc_o,
                  (acc || kk > 0) ? 1u : 0u);
       };
       if (ok) ok = C::KV_ONE ? mbar_wait(&bars->kv_full[0], 0, abort, p.status)
@@ -322,7 +341,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int q = warp >> 2;            // which Q tile
+    const int q = (warp >> 2) / NH;     // which Q tile
+    const int half = (warp >> 2) % NH;  // which half of a row's keys
     const int row = tid & 127;          // TMEM lane = row of the tile
     const int t = t0 + q * kBM + row;   // rank-local token
     const bool row_ok = t < p.BS;
@@ -337,7 +357,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
     float m = -INFINITY, l = 0.f;
     if (p.sinks != nullptr) {
       m = __ldg(p.sinks + gh) * 1.4426950408889634f;
-      l = 1.f;
+      l = half == 0 ? 1.f : 0.f;  // the sink counts once
     }
     // Mods: the row's visible keys, its bias row and slope, and whether the
     // cap bounds the scores tightly enough for a fixed reference of the softmax
@@ -346,6 +366,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
     [[maybe_unused]] bool fixed_ref = false;
     [[maybe_unused]] float slope2 = 0.f;
     [[maybe_unused]] const float* tab = nullptr;
+    [[maybe_unused]] const float* ramp = reinterpret_cast<const float*>(smem + C::OFF_RAMP);
     if constexpr (M::on) {
       visible_keys(mods, t, a, b, pe, p.causal, p.window_left, row_ok, mvlo, mvhi);
       if (M::bias_on && mods.slopes != nullptr) slope2 = __ldg(mods.slopes + gh) * kLog2E;
@@ -353,38 +374,53 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
       fixed_ref = M::cap_on && mods.cap * kLog2E <= kFixedRefCap2;
       if (fixed_ref) {
         const float ref = fmaxf(m, 0.f);  // m is the sink's logit or -inf
-        l = ex2(m - ref);
+        l = half == 0 ? ex2(m - ref) : 0.f;
         m = ref;
       }
     }
+    // NH = 2: `give` hands this half's value of the row to the other half and returns
+    // the other's.  Two buffers in turn: a thread writes a buffer again only after the
+    // next exchange, to which the other half comes after reading it.
+    [[maybe_unused]] uint32_t xn = 0;
+    [[maybe_unused]] auto exchange = [&](float mine, float& other) -> bool {
+      float* x = reinterpret_cast<float*>(smem + C::OFF_X) + ((xn & 1) * NQT + q) * 2 * kBM;
+      x[half * kBM + row] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->x_full[q]);
+      if (!mbar_wait(&bars->x_full[q], xn & 1, abort, p.status)) return false;
+      other = x[(half ^ 1) * kBM + row];
+      ++xn;
+      return true;
+    };
     bool ok = tile_ok[q];
     for (int n = 0; n < n_kv && ok; ++n) {
       if (!(ok = mbar_wait(&bars->s_full[q], n & 1, abort, p.status))) break;
       tc_fence_after();
-      uint32_t sr[kBN / 32][32];
+      uint32_t sr[NC / 32][32];
 #pragma unroll
-      for (int c = 0; c < kBN / 32; ++c) tmem_ld32(s_tm + c * 32, sr[c]);
+      for (int c = 0; c < NC / 32; ++c) tmem_ld32(s_tm + half * NC + c * 32, sr[c]);
       tmem_wait_ld();
-      float s[kBN];
+      float s[NC];
 #pragma unroll
-      for (int c = 0; c < kBN; ++c) s[c] = __uint_as_float(sr[c >> 5][c & 31]);
-      const int kv0 = lo + n * kBN;
+      for (int c = 0; c < NC; ++c) s[c] = __uint_as_float(sr[c >> 5][c & 31]);
+      const int kv0 = lo + n * kBN + half * NC;  // the thread's first key
       float sc = p.scale_log2;  // a score's factor into the log2 domain
       [[maybe_unused]] float off = 0.f;
       if constexpr (M::on) {
         const int d0 = t - kv0, dw = d0 - lane;  // distance of column 0; the warp's first row's
         Affine f{sc, 0.f};
-        if constexpr (M::bias_on) f = add_bias<kBN, -1>(s, tab, mods.R, slope2, d0, dw - (kBN - 1), dw + 31, sc);
+        if constexpr (M::bias_on)
+          f = add_bias(s, tab, mods.R, slope2, ramp, d0, dw - (NC - 1), dw + 31, mods.later_hidden, sc);
         if constexpr (M::cap_on) {
-          cap_scores(s, f, mods.cap);
-          f = {mods.cap * kLog2E, 0.f};
+          const float k = cap_scores<true>(s, f, mods.cap, M::bias_on);
+          f = {k * mods.cap * kLog2E, 0.f};
         }
         sc = f.sc;
         off = f.off;
         const int c_lo = mvlo - kv0, c_hi = mvhi - kv0;
-        if (!(c_lo <= 0 && c_hi >= kBN - 1)) {
+        if (!(c_lo <= 0 && c_hi >= NC - 1)) {
 #pragma unroll
-          for (int c = 0; c < kBN; ++c)
+          for (int c = 0; c < NC; ++c)
             if (c < c_lo || c > c_hi) s[c] = -INFINITY;
         }
       } else {
@@ -396,7 +432,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
           visible_keys(t, a, b, p.causal, p.window_left, row_ok, vlo, vhi);
           const int c_lo = vlo - kv0, c_hi = vhi - kv0;
 #pragma unroll
-          for (int c = 0; c < kBN; ++c)
+          for (int c = 0; c < NC; ++c)
             if (c < c_lo || c > c_hi) s[c] = -INFINITY;
         }
       }
@@ -408,12 +444,17 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
 #pragma unroll
         for (int e = 0; e < 8; ++e) mx8[e] = s[e];
 #pragma unroll
-        for (int c = 8; c < kBN; c += 8)
+        for (int c = 8; c < NC; c += 8)
 #pragma unroll
           for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(mx8[e], s[c + e]);
         const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-        const float m_tile = M::on ? fmaf(mx, sc, off) : mx * sc;  // -inf stays -inf
+        float m_tile = M::on ? fmaf(mx, sc, off) : mx * sc;  // -inf stays -inf
+        if constexpr (NH == 2) {
+          float other;
+          if (!(ok = exchange(m_tile, other))) break;
+          m_tile = fmaxf(m_tile, other);
+        }
         const float m_new = fmaxf(m, m_tile);
         const bool need = m_new > m + 8.f;
         rescale = __any_sync(0xffffffffu, need);
@@ -427,17 +468,18 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
       uint64_t rs2[4] = {0, 0, 0, 0};  // 8 independent partial sums, two per register
       const float nm = M::on ? off - m_use : -m_use;
       const uint64_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(nm, nm);
+      constexpr int PC = NC == kBN ? 64 : 32;  // columns packed and stored as soon as they are done
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {  // each 64-column half is packed and stored as soon as it is done
-        uint32_t pk[32];
+      for (int h = 0; h < NC / PC; ++h) {
+        uint32_t pk[PC / 2];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 e = f2_unpack(f2_fma(f2_pack(s[64 * h + 2 * c], s[64 * h + 2 * c + 1]), sc2, nm2));
+        for (int c = 0; c < PC / 2; ++c) {
+          const float2 e = f2_unpack(f2_fma(f2_pack(s[PC * h + 2 * c], s[PC * h + 2 * c + 1]), sc2, nm2));
           const float p0 = ex2(e.x), p1 = ex2(e.y);
           rs2[c & 3] = f2_add(rs2[c & 3], f2_pack(p0, p1));
           pk[c] = pack_bf16x2(p0, p1);
         }
-        tmem_st32(s_tm + 32 * h, pk);
+        tmem_st(s_tm + half * NC + PC / 2 * h, pk);
       }
       const float2 r01 = f2_unpack(f2_add(rs2[0], rs2[1])), r23 = f2_unpack(f2_add(rs2[2], rs2[3]));
       l += (r01.x + r01.y) + (r23.x + r23.y);
@@ -446,7 +488,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
       // after it), and PV of this tile waits for this warp's arrival below.
       if (rescale && n > 0) {
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = half * (D / 32 / NH); c < (half + 1) * (D / 32 / NH); ++c) {
           uint32_t ov[32];
           tmem_ld32(o_tm + c * 32, ov);
           tmem_wait_ld();
@@ -460,13 +502,17 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->p_full[q]);
     }
+    if constexpr (NH == 2) {
+      float other = 0.f;
+      if (ok && (ok = exchange(l, other))) l = half == 0 ? l + other : other + l;
+    }
     // ---- epilogue: O /= l, bf16 out; LSE = ln(sum) including the sink
     if (ok && (ok = mbar_wait(&bars->o_final[q], 0, abort, p.status))) {
       tc_fence_after();
       const float inv_l = l > 0.f ? 1.f / l : 0.f;
       __nv_bfloat16* orow = out.o + row_offset(p, qh, p.hq, p.Hq, row_ok ? t : 0, D);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = half * (D / 32 / NH); c < (half + 1) * (D / 32 / NH); ++c) {
         uint32_t ov[32];
         tmem_ld32(o_tm + c * 32, ov);
         tmem_wait_ld();
@@ -480,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
           for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pkd[4 * e], pkd[4 * e + 1], pkd[4 * e + 2], pkd[4 * e + 3]);
         }
       }
-      if (row_ok) {
+      if (row_ok && half == 0) {
         const int bb = t / p.S, ss = t - bb * p.S;
         out.lse[(static_cast<size_t>(r * p.B + bb) * p.hq + j) * p.S + ss] =
             l > 0.f || (M::on && l != l) ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -502,7 +548,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, Cfg<D, NQT>::CTAS)
 template <int D, int NQT, class M>
 static int run_fwd(const AttnArgs& a, const M& mods, int tab_bytes, const CUtensorMap& tq, const CUtensorMap& tk,
                    const CUtensorMap& tv, void* o, float* lse, cudaStream_t st) {
-  using C = fwd::Cfg<D, NQT>;
+  using C = fwd::Cfg<D, NQT, fwd::kHalves<M>>;
   fwd::Out out{static_cast<__nv_bfloat16*>(o), lse, (a.BS + NQT * kBM - 1) / (NQT * kBM)};
   auto kern = fwd::attn_fwd_kernel<D, NQT, M>;
   const int smem = C::SMEM + tab_bytes;

@@ -10,7 +10,7 @@
 
 namespace usp {
 
-ModArgs make_mods(const usp_score_mods& m);
+ModArgs make_mods(const usp_attn_params& p, const usp_score_mods& m);
 
 namespace bwd {
 
@@ -192,10 +192,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bars->s_free[n & 1]);
       const int d0 = t - k0, dw = d0 - lane;
       Affine f{p.scale_log2, 0.f};
-      if constexpr (M::bias_on) f = add_bias<64, -1>(x, tab, mods.R, slope2, d0, dw - 63, dw + 31, p.scale_log2);
+      if constexpr (M::bias_on)
+        f = add_bias(x, tab, mods.R, slope2, nullptr, d0, dw - 63, dw + 31, mods.later_hidden, p.scale_log2);
       if constexpr (M::cap_on) {
-        cap_scores(x, f, mods.cap);
-        f = {mods.cap * kLog2E, 0.f};
+        const float k = cap_scores<false>(x, f, mods.cap, M::bias_on);
+        f = {k * mods.cap * kLog2E, 0.f};
       }
       const int c_lo = vlo - k0, c_hi = vhi - k0;
       if (!(c_lo <= 0 && c_hi >= 63)) {
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (grp == 1) red[row] = sum;
     asm volatile("bar.sync 1, 256;" ::: "memory");
     if (grp == 0 && row_ok) {
-      stats[plane_index(bsp, p.hq, r, j, 0, t)] = nlse2;
+      stats[plane_index(bsp, p.hq, r, j, 0, t)] = nlse2 - slope_of_row(mods, slope2, t);
       stats[plane_index(bsp, p.hq, r, j, 1, t)] = sum + red[row];
     }
   }
@@ -262,8 +263,9 @@ int run_delta(const AttnArgs& a, const M& m, const void* q, const void* k, const
 }
 
 constexpr int kRelThreads = 256;
-constexpr int kRelRows = 64;    // partial rows that one block of the first reduction sums
+constexpr int kRelRows = 32;    // partial rows that one block of the first reduction sums
 constexpr int kRelSplits = 64;  // most blocks per head
+constexpr int kRelAhead = 16;   // rows whose loads a thread has in flight
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -316,20 +318,24 @@ __global__ void __launch_bounds__(kRelThreads)
     clear[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-// Sums a split's partial rows of a head: thread = distance, rows in order.
-__global__ void __launch_bounds__(kRelThreads)
+// Sums a split's partial rows of a head: thread = distance, kRelAhead rows in
+// flight, joined in a fixed order.
+__global__ void __launch_bounds__(1024)
     rel_sum_kernel(const float* __restrict__ partial, float* __restrict__ sums, int n_rows, int per, int row) {
   const int h = blockIdx.x, s = blockIdx.y;
   const int r0 = s * per, r1 = min(n_rows, r0 + per);
   const float* src = partial + static_cast<size_t>(h) * n_rows * row;
-  for (int c = threadIdx.x; c < row; c += kRelThreads) {
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    int r = r0;
-    for (; r + 4 <= r1; r += 4)
+  for (int c = threadIdx.x; c < row; c += blockDim.x) {
+    float acc[kRelAhead] = {};
+    for (int r = r0; r < r1; r += kRelAhead)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] += __ldg(src + static_cast<size_t>(r + e) * row + c);
-    for (; r < r1; ++r) acc[0] += __ldg(src + static_cast<size_t>(r) * row + c);
-    sums[(static_cast<size_t>(h) * gridDim.y + s) * row + c] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      for (int e = 0; e < kRelAhead; ++e)
+        if (r + e < r1) acc[e] += __ldg(src + static_cast<size_t>(r + e) * row + c);
+#pragma unroll
+    for (int o = kRelAhead / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int e = 0; e < o; ++e) acc[e] += acc[e + o];
+    sums[(static_cast<size_t>(h) * gridDim.y + s) * row + c] = acc[0];
   }
 }
 
@@ -360,8 +366,33 @@ __global__ void __launch_bounds__(kRelThreads)
   }
 }
 
+// dsink_h = -sum_t exp(sink_h - LSE_t) D_t: one block per head, fixed-order tree.
+constexpr int kSinkThreads = 512;
+__global__ void __launch_bounds__(kSinkThreads)
+    mod_dsink_kernel(const float* __restrict__ stats, const float* __restrict__ lse, float* __restrict__ dsinks,
+                     AttnArgs p, int bsp) {
+  __shared__ float red[kSinkThreads];
+  const int r = blockIdx.x / p.hq, j = blockIdx.x % p.hq;
+  const float z2 = __ldg(p.sinks + blockIdx.x) * kLog2E;
+  const float* dd = stats + bwd::plane_index(bsp, p.hq, r, j, 1, 0);
+  float acc = 0.f;
+  for (int b = 0; b < p.B; ++b) {
+    const float* l = lse + (static_cast<size_t>(r * p.B + b) * p.hq + j) * p.S;
+#pragma unroll 4
+    for (int s = threadIdx.x; s < p.S; s += kSinkThreads)
+      acc -= ex2(fmaf(-kLog2E, __ldg(l + s), z2)) * __ldg(dd + b * p.S + s);
+  }
+  red[threadIdx.x] = acc;
+  __syncthreads();
+  for (int s = kSinkThreads / 2; s > 0; s >>= 1) {
+    if (threadIdx.x < s) red[threadIdx.x] += red[threadIdx.x + s];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) dsinks[blockIdx.x] = red[0];
+}
+
 ModArgs bwd_mods(const usp_attn_params& p, const usp_score_mods& sm, const void* ws) {
-  ModArgs m = make_mods(sm);
+  ModArgs m = make_mods(p, sm);
   const Layout L = mod_layout(p, sm);
   uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(ws));
   m.n_kb = L.n_kb;
@@ -403,7 +434,8 @@ int launch_attn_mod_bwd_preprocess(const usp_attn_params& p, const usp_score_mod
     if (check_launch() != USP_OK) return USP_ERR_CUDA;
   }
   const bool exact_delta = dsinks != nullptr || m.partial != nullptr;  // a gradient in fp32 hangs on D
-  if (!exact_delta) return run_preprocess(p, o, lse, dO, nullptr, ws, status, st);
+  if (!exact_delta)
+    return with_mods(m, [&](const auto& mods) { return run_preprocess(p, mods, o, lse, dO, nullptr, ws, status, st); });
   const AttnArgs a = make_args(p, status);
   float* stats = static_cast<float*>(ws);
   const int rc = with_mods(m, [&](const auto& mods) {
@@ -411,7 +443,7 @@ int launch_attn_mod_bwd_preprocess(const usp_attn_params& p, const usp_score_mod
                       : run_delta<64>(a, mods, q, k, v, dO, lse, stats, st);
   });
   if (rc != USP_OK || dsinks == nullptr) return rc;
-  bwd::dsink_kernel<<<a.P * a.hq, 256, 0, st>>>(stats, dsinks, a, stats_row_pitch(a.BS));
+  mod_dsink_kernel<<<a.Hq, kSinkThreads, 0, st>>>(stats, lse, dsinks, a, stats_row_pitch(a.BS));
   return check_launch();
 }
 
@@ -451,10 +483,11 @@ int launch_attn_mod_bwd_rel_bias(const usp_attn_params& p, const usp_score_mods&
   uint8_t* base = static_cast<uint8_t*>(ws);
   const int row = 2 * sm.max_distance + 1, per = (L.n_rows + L.splits - 1) / L.splits;
   float* sums = reinterpret_cast<float*>(base + L.sums);
-  rel_sum_kernel<<<dim3(p.Hq, L.splits), kRelThreads, 0, st>>>(reinterpret_cast<const float*>(base + L.partial), sums,
+  const int threads = row < 1024 ? (row + 31) / 32 * 32 : 1024;
+  rel_sum_kernel<<<dim3(p.Hq, L.splits), threads, 0, st>>>(reinterpret_cast<const float*>(base + L.partial), sums,
                                                                L.n_rows, per, row);
   if (check_launch() != USP_OK) return USP_ERR_CUDA;
-  rel_bucket_kernel<<<p.Hq, kRelThreads, row * (sizeof(float) + sizeof(int)), st>>>(make_mods(sm), sums, drel_bias, L.splits);
+  rel_bucket_kernel<<<p.Hq, kRelThreads, row * (sizeof(float) + sizeof(int)), st>>>(make_mods(p, sm), sums, drel_bias, L.splits);
   return check_launch();
 }
 

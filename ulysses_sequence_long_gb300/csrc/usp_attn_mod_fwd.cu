@@ -5,8 +5,9 @@
 
 namespace usp {
 
-ModArgs make_mods(const usp_score_mods& m) {
+ModArgs make_mods(const usp_attn_params& p, const usp_score_mods& m) {
   ModArgs x{};
+  x.later_hidden = p.causal && m.prefix_lens == nullptr;
   x.cap = m.softcap;
   x.slopes = m.slopes;
   x.rel_bias = m.rel_bias;
@@ -21,7 +22,7 @@ ModArgs make_mods(const usp_score_mods& m) {
 int launch_attn_mod_fwd(const usp_attn_params& prm, const usp_score_mods& sm, const void* q, const void* k,
                         const void* v, void* o, float* lse, int32_t* status, cudaStream_t st) {
   const AttnArgs a = make_fwd_args(prm, status);
-  const ModArgs m = make_mods(sm);
+  const ModArgs m = make_mods(prm, sm);
   const int tab_bytes = m.rel_bias != nullptr ? tab_len(m.R) * static_cast<int>(sizeof(float)) : 0;
   return with_mods(m, [&](const auto& mods) {
     return prm.D == 128 ? run_fwd<128>(a, mods, tab_bytes, q, k, v, o, lse, st)

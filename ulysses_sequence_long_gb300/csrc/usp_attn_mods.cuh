@@ -39,6 +39,7 @@ struct ModArgs {
   const float* rel_bias;   // global [Hq][n_buckets] or null
   const int32_t* buckets;  // [2R+1]
   int n_buckets, R;
+  bool later_hidden;       // causal without a prefix: no row sees a key after it
   const int32_t* prefix;   // [n_prefix] or null
   int n_prefix;
   // backward: the expanded rows [Hq][tab_len(R)] (log2 domain), and the partial
@@ -170,15 +171,16 @@ struct Affine {
   float sc, off;
 };
 
-// Adds the biases to N raw scores of one row (STEP = -1: column c is the key
-// at distance d0 - c) or one key (STEP = +1: column c is the query at distance
-// d0 + c), d0 = t - u of column 0.  [dmin, dmax] are the distances that the
-// whole warp meets in the block (warp-uniform).  `row` points at distance 0 of
-// the head's table (null: none).  Distances all beyond R cost nothing per
-// element: their bias is one value and goes into `off`.
-template <int N, int STEP>
-__device__ __forceinline__ Affine add_bias(float (&x)[N], const float* row, int R, float slope2, int d0, int dmin,
-                                           int dmax, float scale_log2) {
+// Adds the biases to N raw scores of one row: column c is the key at distance
+// d0 - c.  [dmin, dmax] are the distances that the whole warp meets in the block
+// (warp-uniform).  `row` points at distance 0 of the head's table (null: none).
+// Distances all beyond R cost nothing per element: their bias is one value and
+// goes into `off`.  `later_hidden`: keys after the query are masked anyway, so
+// their slope may have either sign.  `ramp`: slope2 * c for every column in shared
+// memory, or null (computed here).
+template <int N>
+__device__ __forceinline__ Affine add_bias(float (&x)[N], const float* row, int R, float slope2, const float* ramp,
+                                           int d0, int dmin, int dmax, bool later_hidden, float scale_log2) {
   Affine f{scale_log2, 0.f};
   if (row != nullptr) {
     if (dmin >= R || dmax <= -R) {
@@ -186,41 +188,107 @@ __device__ __forceinline__ Affine add_bias(float (&x)[N], const float* row, int 
     } else {
       const float* at = row + d0;
 #pragma unroll
-      for (int c = 0; c < N; ++c) x[c] = fmaf(x[c], f.sc, at[STEP * c]);
+      for (int c = 0; c < N; ++c) x[c] = fmaf(x[c], f.sc, at[-c]);
       f.sc = 1.f;
     }
   }
   if (slope2 != 0.f) {
     const float d0f = static_cast<float>(d0);
-    if (dmin >= 0 || dmax <= 0) {
-      // one side of the diagonal: -slope |d0 + STEP c| = -slope |d0| + k c
-      const float k = dmin >= 0 ? -STEP * slope2 : STEP * slope2;
-      const uint64_t sc2 = f2_pack(f.sc, f.sc), k2 = f2_pack(k, k);
+    if (dmin >= 0 || later_hidden) {
+      // -slope (d0 - c) = -slope d0 + slope c
+      const uint64_t sc2 = f2_pack(f.sc, f.sc), k2 = f2_pack(slope2, slope2);
 #pragma unroll
-      for (int c = 0; c < N; c += 2) {
-        const float2 y = f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sc2,
-                                          f2_mul(f2_pack(static_cast<float>(c), static_cast<float>(c + 1)), k2)));
+      for (int c = 0; c < N; c += 4) {
+        uint64_t a2, b2;
+        if (ramp != nullptr) {
+          const float4 r4 = *reinterpret_cast<const float4*>(ramp + c);
+          a2 = f2_pack(r4.x, r4.y);
+          b2 = f2_pack(r4.z, r4.w);
+        } else {
+          a2 = f2_mul(f2_pack(static_cast<float>(c), static_cast<float>(c + 1)), k2);
+          b2 = f2_mul(f2_pack(static_cast<float>(c + 2), static_cast<float>(c + 3)), k2);
+        }
+        const float2 y = f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sc2, a2));
+        const float2 z = f2_unpack(f2_fma(f2_pack(x[c + 2], x[c + 3]), sc2, b2));
         x[c] = y.x;
         x[c + 1] = y.y;
+        x[c + 2] = z.x;
+        x[c + 3] = z.y;
       }
-      f.off -= slope2 * fabsf(d0f);
+      f.off -= slope2 * d0f;
     } else {
 #pragma unroll
-      for (int c = 0; c < N; ++c) x[c] = fmaf(x[c], f.sc, -slope2 * fabsf(d0f + static_cast<float>(STEP * c)));
+      for (int c = 0; c < N; ++c) x[c] = fmaf(x[c], f.sc, -slope2 * fabsf(d0f - static_cast<float>(c)));
     }
     f.sc = 1.f;
   }
   return f;
 }
 
-// tanh(y) / y on |y| <= 1 as a polynomial in t = y^2, degree 6, fitted by
-// interpolation at Chebyshev nodes: the absolute error of y q(y^2) evaluated in
-// fp32 is at most 1.3e-7 (the fit's own is 3.7e-8).  An absolute error of c
-// times that in the score is below what fp32 leaves of a score of that size,
-// which the fp32 gradients of rel_bias and the sinks need.  (One exponential and a
-// reciprocal per score, tanh = 1 - 2 / (1 + e^(2y)), costs an absolute 2e-7 at
-// y = 0 already.)
+// The dK/dV pass reads a row's -LSE log2e for 32 queries at a time, the same for
+// every key: without a cap (which takes the biased score) a row's part of the
+// slope's bias goes there, slope2 (t & 31), so that a key adds one value per block
+// of 32 queries (which start at multiples of 32).  Within 32 queries the values stay
+// small enough for fp32 not to lose the LSE.
+template <class M>
+__device__ __forceinline__ float slope_of_row(const M& m, float slope2, int t) {
+  if constexpr (bias_on<M>) {
+    if constexpr (!M::cap_on) return slope2 * static_cast<float>(t & 31);
+  }
+  return 0.f;
+}
+
+// The biases of 32 raw scores of one key: column c is the query at distance d0 + c;
+// `in_stats`: its -slope2 c comes with its statistics (above).  As add_bias otherwise.
+__device__ __forceinline__ Affine add_bias_of_key(float (&x)[32], const float* row, int R, float slope2, bool in_stats,
+                                                  int d0, int dmin, int dmax, bool later_hidden, float scale_log2) {
+  Affine f{scale_log2, 0.f};
+  if (row != nullptr) {
+    if (dmin >= R || dmax <= -R) {
+      f.off = row[dmin >= R ? R : -R];
+    } else {
+      const float* at = row + d0;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) x[c] = fmaf(x[c], f.sc, at[c]);
+      f.sc = 1.f;
+    }
+  }
+  if (slope2 != 0.f) {
+    const float d0f = static_cast<float>(d0);
+    if (in_stats) {
+      f.off -= slope2 * d0f;  // -slope (d0 + c) = -slope d0 - slope c
+      if (dmin < 0 && !later_hidden) {
+        // queries before the key: -slope |d| = -slope d + 2 slope min(d, 0)
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          x[c] = fmaf(x[c], f.sc, 2.f * slope2 * fminf(d0f + static_cast<float>(c), 0.f));
+        f.sc = 1.f;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) x[c] = fmaf(x[c], f.sc, -slope2 * fabsf(d0f + static_cast<float>(c)));
+      f.sc = 1.f;
+    }
+  }
+  return f;
+}
+
+// tanh(y) / y as a polynomial q in t = y^2 (own fits by interpolation at Chebyshev
+// nodes): degree 2 for |y| <= 1/4, 4 for |y| <= 1/2, 6 for |y| <= 1.  The absolute
+// error of y q(y^2) evaluated in fp32 is at most 1.2e-7 in each range; c times that
+// is below what fp32 leaves of a score of that size, which the fp32 gradients of
+// rel_bias and the sinks need.  (One exponential and a reciprocal per score, tanh =
+// 1 - 2 / (1 + e^(2y)), costs an absolute 2e-7 at y = 0 already.)
+template <int DEG>
 __host__ __device__ constexpr float tanh_q(int i) {
+  static_assert(DEG == 2 || DEG == 4 || DEG == 6, "");
+  if (DEG == 2) return i == 0 ? 0.999999583f : i == 1 ? -0.333218962f : 0.128414333f;
+  if (DEG == 4)
+    return i == 0   ? 1.f
+           : i == 1 ? -0.333330691f
+           : i == 2 ? 0.13324751f
+           : i == 3 ? -0.0529842377f
+                    : 0.0171313453f;
   return i == 0   ? 0.99999994f
          : i == 1 ? -0.333328277f
          : i == 2 ? 0.133250758f
@@ -231,60 +299,89 @@ __host__ __device__ constexpr float tanh_q(int i) {
 }
 
 // tanh of any y: the polynomial inside |y| <= 1, outside 1 - 2 e / (1 + e) with
-// e = e^(-2|y|) <= 0.14, whose absolute error is under 1e-7.  Keeps NaN.
-__device__ __forceinline__ float tanh_any(float y) {
+// e = e^(-2|y|) <= 0.14, whose absolute error is under 1e-7.  Keeps NaN.  Not
+// inlined: unrolled over a block's scores it would push the loops that do run out of
+// the instruction cache.
+static __device__ __noinline__ float tanh_any(float y) {
   const float t = y * y;
-  float q = tanh_q(6);
+  float q = tanh_q<6>(6);
 #pragma unroll
-  for (int i = 5; i >= 0; --i) q = fmaf(q, t, tanh_q(i));
+  for (int i = 5; i >= 0; --i) q = fmaf(q, t, tanh_q<6>(i));
   const float e = ex2(-2.f * kLog2E * fabsf(y));
   const float big = fmaf(-2.f * e, rcp(1.f + e), 1.f);
   return fabsf(y) <= 1.f ? y * q : copysignf(big, y);
 }
 
-// x -> tanh(x2 ln2 / cap) in place, where x2 = x f.sc + f.off: the capped score
-// is then cap log2e times that.  The warp takes the polynomial alone, two scores
-// per instruction, unless one of its scores is beyond |y| = 1.
-template <int N>
-__device__ __forceinline__ void cap_scores(float (&x)[N], Affine f, float cap) {
-  const float k = 0.6931471805599453f / cap;
-  const uint64_t k2 = f2_pack(f.sc * k, f.sc * k), o2 = f2_pack(f.off * k, f.off * k);
-  float top[4] = {0.f, 0.f, 0.f, 0.f};
+// x -> tanh(k x) / k by the polynomial of degree DEG in (k x)^2: the powers of k
+// go into its coefficients, so k costs no multiplication per score.
+template <int DEG, int N>
+__device__ __forceinline__ void tanh_poly(float (&x)[N], float k) {
+  uint64_t q2[DEG + 1];
+  float kp = 1.f;
+#pragma unroll
+  for (int i = 0; i <= DEG; ++i) {
+    q2[i] = f2_pack(tanh_q<DEG>(i) * kp, tanh_q<DEG>(i) * kp);
+    kp *= k * k;
+  }
 #pragma unroll
   for (int c = 0; c < N; c += 2) {
-    const float2 y = f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), k2, o2));
-    x[c] = y.x;
-    x[c + 1] = y.y;
-    top[(c >> 1) & 3] = fmax3(top[(c >> 1) & 3], fabsf(y.x), fabsf(y.y));
-  }
-  // (the max skips a NaN, which the polynomial keeps)
-  if (!__any_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > 1.f)) {
-    uint64_t q2[7];
+    const uint64_t y = f2_pack(x[c], x[c + 1]), t = f2_mul(y, y);
+    uint64_t q = f2_fma(q2[DEG], t, q2[DEG - 1]);
 #pragma unroll
-    for (int i = 0; i < 7; ++i) q2[i] = f2_pack(tanh_q(i), tanh_q(i));
-#pragma unroll
-    for (int c = 0; c < N; c += 2) {
-      const uint64_t y = f2_pack(x[c], x[c + 1]), t = f2_mul(y, y);
-      uint64_t q = f2_fma(q2[6], t, q2[5]);
-#pragma unroll
-      for (int i = 4; i >= 0; --i) q = f2_fma(q, t, q2[i]);
-      const float2 z = f2_unpack(f2_mul(y, q));
-      x[c] = z.x;
-      x[c + 1] = z.y;
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < N; ++c) x[c] = tanh_any(x[c]);
+    for (int i = DEG - 2; i >= 0; --i) q = f2_fma(q, t, q2[i]);
+    const float2 z = f2_unpack(f2_mul(y, q));
+    x[c] = z.x;
+    x[c + 1] = z.y;
   }
 }
 
-// g = 1 - tanh^2, the cap's derivative, from the tanh.
+// x -> w = tanh(y) / k in place, y = x2 ln2 / cap, x2 = x f.sc + f.off, and returns
+// k: the capped score in the log2 domain is then w k cap log2e, and tanh is w k.
+// The kernels are bound by the packed fp32 operations of a score, so a warp takes
+// the shortest polynomial that its largest |y| allows (forward, 8192 packed
+// tokens, D = 128, cap 30: CAPNOTE).
+template <bool TIERS, int N>
+__device__ __forceinline__ float cap_scores(float (&x)[N], Affine f, float cap, bool biased) {
+  float k = f.sc * (0.6931471805599453f / cap);
+  if (biased || k < 0x1p-9f) {
+    // to y itself: the offset of a bias, or a k whose powers would leave fp32
+    const float ko = f.off * (0.6931471805599453f / cap);
+    const uint64_t k2 = f2_pack(k, k), o2 = f2_pack(ko, ko);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+      const float2 y = f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), k2, o2));
+      x[c] = y.x;
+      x[c + 1] = y.y;
+    }
+    k = 1.f;
+  }
+  float top4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < N; c += 2) top4[(c >> 1) & 3] = fmax3(top4[(c >> 1) & 3], fabsf(x[c]), fabsf(x[c + 1]));
+  // (the max skips a NaN, which every path keeps)
+  const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * k;
+  if (TIERS && !__any_sync(0xffffffffu, top > 0.25f)) {
+    tanh_poly<2>(x, k);
+  } else if (TIERS && !__any_sync(0xffffffffu, top > 0.5f)) {
+    tanh_poly<4>(x, k);
+  } else if (!__any_sync(0xffffffffu, top > 1.f)) {
+    tanh_poly<6>(x, k);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c) x[c] = tanh_any(x[c] * k);
+    k = 1.f;
+  }
+  return k;
+}
+
+// g = 1 - tanh^2, the cap's derivative, from cap_scores' w and k.
 template <int N>
-__device__ __forceinline__ void cap_slope(const float (&th)[N], float (&g)[N]) {
+__device__ __forceinline__ void cap_slope(const float (&w)[N], float (&g)[N], float k) {
+  const uint64_t mk2 = f2_pack(-k * k, -k * k), one = f2_pack(1.f, 1.f);
 #pragma unroll
   for (int c = 0; c < N; c += 2) {
-    const uint64_t y = f2_pack(th[c], th[c + 1]);
-    const float2 z = f2_unpack(f2_fma(f2_mul(y, f2_pack(-1.f, -1.f)), y, f2_pack(1.f, 1.f)));
+    const uint64_t y = f2_pack(w[c], w[c + 1]);
+    const float2 z = f2_unpack(f2_fma(f2_mul(y, mk2), y, one));
     g[c] = z.x;
     g[c + 1] = z.y;
   }
