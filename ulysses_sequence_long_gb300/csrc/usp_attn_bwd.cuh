@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
       [[maybe_unused]] float slope2 = 0.f;
       if constexpr (M::on) {
         const int hg = hg0 + i / n_q;
-        if constexpr (M::bias_on) {
+        if constexpr (bias_on<M>) {
 
           if (mods.table != nullptr) tab = mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad;
           if (mods.slopes != nullptr) slope2 = __ldg(mods.slopes + hg) * kLog2E;
@@ -667,20 +667,20 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
         // only chunks that straddle a document, diagonal or window edge pay
         // for the per-element mask (hidden scores become -inf, so exp2 gives 0)
         const int c_lo = vlo - (q0 + 32 * c), c_hi = vhi - (q0 + 32 * c);
-        [[maybe_unused]] float gf[M::on ? 32 : 1];  // the cap's derivative
+        [[maybe_unused]] float gf[cap_on<M> ? 32 : 1];  // the cap's derivative
         uint64_t xs2 = sc2;
         if constexpr (M::on) {
           const int d0 = q0 + 32 * c - u, dw = q0 + 32 * c - uw;
           Affine f{p.scale_log2, 0.f};
-          if constexpr (M::bias_on)
-            f = add_bias_of_key(x, tab, mods.R, slope2, !M::cap_on, d0, dw - 31, dw + 31, mods.later_hidden,
+          if constexpr (bias_on<M>)
+            f = add_bias_of_key(x, tab, mods.R, slope2, !cap_on<M>, d0, dw - 31, dw + 31, mods.later_hidden,
                                 p.scale_log2);
-          if constexpr (M::cap_on) {
-            const float k = cap_scores<false>(x, f, mods.cap, M::bias_on);
-            cap_slope(x, gf, k);
-            f = {k * mods.cap * kLog2E, 0.f};
+          if constexpr (cap_on<M>) {
+            cap_scores<false, bias_on<M>>(x, f, mods.cap, true);
+            cap_slope(x, gf);
+            f = {mods.cap * kLog2E, 0.f};
           }
-          if constexpr (M::bias_on && !M::cap_on) {
+          if constexpr (bias_on<M> && !cap_on<M>) {
             if (slope2 != 0.f || f.off != 0.f) {  // (uniform: without a slope the offset is a table's end)
               const uint64_t a2 = f2_pack(f.sc, f.sc), o2 = f2_pack(f.off, f.off);
 #pragma unroll
@@ -710,12 +710,7 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
           pr[c][4 * c4 + 3] = ex2(e1.y);
         }
         tmem_st_packed<16>(lb + T_S + gc + 16 * c, pr[c]);
-        if constexpr (M::on) {
-          if constexpr (M::cap_on) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) pr[c][e] *= gf[e];
-          }
-        }
+        if constexpr (cap_on<M>) f2_scale(pr[c], gf);
       }
       tc_fence_before();
       __syncwarp();
@@ -1080,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     [[maybe_unused]] const float* tab = nullptr;  // Mods: the head's bias row and slope
     [[maybe_unused]] float slope2 = 0.f;
     if constexpr (M::on) {
-      if constexpr (M::bias_on) {
+      if constexpr (bias_on<M>) {
         if (mods.table != nullptr) tab = mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad;
         if (mods.slopes != nullptr) slope2 = __ldg(mods.slopes + hg) * kLog2E;
       }
@@ -1095,16 +1090,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       float x[64];
       tmem_ld_cols<64>(lb + s_col, x);
       const int c_lo = vlo - k0, c_hi = vhi - k0;
-      [[maybe_unused]] float gf[M::on ? 64 : 1];  // the cap's derivative
+      [[maybe_unused]] float gf[cap_on<M> ? 64 : 1];  // the cap's derivative
       Affine f{p.scale_log2, 0.f};
       if constexpr (M::on) {
         const int d0 = t - k0, dw = d0 - lane;
-        if constexpr (M::bias_on)
+        if constexpr (bias_on<M>)
           f = add_bias(x, tab, mods.R, slope2, nullptr, d0, dw - 63, dw + 31, mods.later_hidden, p.scale_log2);
-        if constexpr (M::cap_on) {
-          const float k = cap_scores<false>(x, f, mods.cap, M::bias_on);
-          cap_slope(x, gf, k);
-          f = {k * mods.cap * kLog2E, 0.f};
+        if constexpr (cap_on<M>) {
+          cap_scores<false, true>(x, f, mods.cap, true);
+          cap_slope(x, gf);
+          f = {mods.cap * kLog2E, 0.f};
         }
       }
       if (!(c_lo <= 0 && c_hi >= 63)) {
@@ -1124,10 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if constexpr (M::on) {
-        if constexpr (M::cap_on) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) pr[c] *= gf[c];
-        }
+        if constexpr (cap_on<M>) f2_scale(pr, gf);
       }
       if (!(ok = mbar_wait(&bars->dp_full, ph, abort, p.status))) break;
       tc_fence_after();

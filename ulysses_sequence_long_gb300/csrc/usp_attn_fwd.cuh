@@ -33,6 +33,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "usp_attn_common.cuh"
 #include "usp_attn_mods.cuh"
@@ -105,15 +106,20 @@ struct Out {
   int nqb;  // query blocks (NQT tiles of 128 rows) per (rank, head)
 };
 
-// Halves of a row's keys (see Cfg).  With modified scores a row's chain from S to P
-// is longer, and 8 softmax warps do not hide it (SPLITNOTE).
+// Halves of a row's keys (see Cfg).  A cap lengthens a row's chain from S to P, and 8
+// softmax warps do not hide it (8192 packed tokens, D = 128: 225 us with whole rows,
+// 208 with halves).  Without one the exchange of the row's maximum costs more than
+// the shorter chain gains (prefix 123 and 127 us, slopes 211 and 219).
 template <class M>
-constexpr int kHalves = M::on ? 2 : 1;
+constexpr int kHalves = 1;
+template <bool BIAS>
+constexpr int kHalves<Mods<true, BIAS>> = 2;
 
 template <int D, int NQT, class M>
 __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>::CTAS)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                    const __grid_constant__ CUtensorMap tv, AttnArgs p, Out out, M mods) {
+                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to, AttnArgs p, Out out,
+                    M mods) {
   constexpr int NH = kHalves<M>, NC = kBN / NH;  // columns of a thread
   using C = Cfg<D, NQT, NH>;
   extern __shared__ uint8_t smem_raw[];
@@ -130,19 +136,72 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
   const HeadRef qh = q_head_ref(p, r, j), kvh = kv_head_ref(p, r, j / p.G);
   const int t0 = qb * NQT * kBM;
 
-  const int n_docs = checked_docs(p);
-  if (n_docs == 0) return;
-
   bool tile_ok[NQT];
-  int lo = 0x7FFFFFFF, hi = 0;
-  for (int q = 0; q < NQT; ++q) {
-    int first = t0 + q * kBM;
-    tile_ok[q] = first < p.BS;
-    if (tile_ok[q]) {
-      int last = min(first + kBM, p.BS) - 1, l0, h0;
-      key_range(p, mods, n_docs, first, last, l0, h0);
-      lo = min(lo, l0);
-      hi = max(hi, h0);
+  for (int q = 0; q < NQT; ++q) tile_ok[q] = t0 + q * kBM < p.BS;
+  volatile int* abort = &bars->abort;
+  auto init_bars = [&] {
+    for (int q = 0; q < NQT; ++q) {
+      mbar_init(&bars->q_full[q], 1);
+      mbar_init(&bars->s_full[q], 1);
+      mbar_init(&bars->p_full[q], 4 * NH);
+      mbar_init(&bars->x_full[q], 4 * NH);
+      mbar_init(&bars->o_final[q], 1);
+    }
+    mbar_init(&bars->mma_done, 1);
+    for (int j = 0; j < kRel; ++j) mbar_init(&bars->rel[j], 1);
+    mbar_init(&bars->k_first, 1);
+    for (int s = 0; s < C::ST; ++s) mbar_init(&bars->kv_full[s], 1);
+    bars->abort = 0;
+    fence_barrier_init();
+  };
+  auto load_q = [&] {
+    prefetch_tmap(&tq);
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+    for (int q = 0; q < NQT; ++q) {
+      if (!tile_ok[q]) continue;
+      mbar_arrive_expect_tx(&bars->q_full[q], C::TILE);
+      for (int c = 0; c < C::NCH; ++c)
+        tma_load_rows(smem + C::OFF_Q + q * C::TILE + c * kAtomBytes, &tq, &bars->q_full[q], p, c, qh, t0 + q * kBM);
+    }
+  };
+  // Mods: Q, which waits for nothing, is on its way before the documents are looked
+  // up, and the first K before the CTA has its TMEM; by the producer itself.
+  const bool is_producer = warp == C::WP && lane == 0;
+  if constexpr (M::on) {
+    if (is_producer) {
+      init_bars();
+      load_q();
+    }
+  }
+  auto leave_early = [&] {  // never with copies still landing
+    if constexpr (M::on) {
+      if (is_producer)
+        for (int q = 0; q < NQT; ++q)
+          if (tile_ok[q]) mbar_wait(&bars->q_full[q], 0, abort, p.status);
+    }
+  };
+
+  int n_docs, lo = 0x7FFFFFFF, hi = 0;
+  [[maybe_unused]] TileDocs docs;
+  if constexpr (M::on) {
+    const int last = min(t0 + NQT * kBM, p.BS) - 1;
+    if (!checked_tile_docs(p, mods, t0, last, n_docs, docs)) {
+      leave_early();
+      return;
+    }
+    key_range(p, mods, docs, t0, last, lo, hi);
+  } else {
+    n_docs = checked_docs(p);
+    if (n_docs == 0) return;
+    for (int q = 0; q < NQT; ++q) {
+      int first = t0 + q * kBM;
+      if (tile_ok[q]) {
+        int last = min(first + kBM, p.BS) - 1, l0, h0;
+        key_range(p, n_docs, first, last, l0, h0);
+        lo = min(lo, l0);
+        hi = max(hi, h0);
+      }
     }
   }
   // Ring x Ulysses step: only the key/value super-chunk held at this step (the
@@ -171,31 +230,34 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
             p.sinks != nullptr ? __ldg(p.sinks + r * p.hq + j) : -INFINITY;
       }
     }
+    leave_early();
     return;
   }
 
-  if (tid == 0) {
-    for (int q = 0; q < NQT; ++q) {
-      mbar_init(&bars->q_full[q], 1);
-      mbar_init(&bars->s_full[q], 1);
-      mbar_init(&bars->p_full[q], 4 * NH);
-      mbar_init(&bars->x_full[q], 4 * NH);
-      mbar_init(&bars->o_final[q], 1);
+  auto load = [&](int kv, int n, uint64_t* full) {  // K (kv 0) or V tile n into its stage
+    uint8_t* dst = smem + (kv == 0 ? C::OFF_K : C::OFF_V) + (n % C::ST) * C::TILE;
+    for (int c = 0; c < C::NCH; ++c)
+      tma_load_rows(dst + c * kAtomBytes, kv == 0 ? &tk : &tv, full, p, c, kvh, lo + n * kBN, p.kv_seq_io != 0);
+  };
+  auto load_first = [&] {
+    if constexpr (C::KV_ONE) {
+      mbar_arrive_expect_tx(&bars->kv_full[0], 2 * C::TILE);
+      load(0, 0, &bars->kv_full[0]);
+      load(1, 0, &bars->kv_full[0]);
+    } else {
+      mbar_arrive_expect_tx(&bars->k_first, C::TILE);
+      load(0, 0, &bars->k_first);
     }
-    mbar_init(&bars->mma_done, 1);
-    for (int j = 0; j < kRel; ++j) mbar_init(&bars->rel[j], 1);
-    mbar_init(&bars->k_first, 1);
-    for (int s = 0; s < C::ST; ++s) {
-      mbar_init(&bars->kv_full[s], 1);
-
-    }
-    bars->abort = 0;
-    fence_barrier_init();
+  };
+  if constexpr (M::on) {
+    if (is_producer) load_first();
+  } else if (tid == 0) {
+    init_bars();
   }
   if constexpr (M::on) {
-    if (M::bias_on && mods.slopes != nullptr && tid < kBN)
+    if (bias_on<M> && mods.slopes != nullptr && tid < kBN)
       reinterpret_cast<float*>(smem + C::OFF_RAMP)[tid] = __ldg(mods.slopes + r * p.hq + j) * kLog2E * static_cast<float>(tid);
-    if (M::bias_on && mods.rel_bias != nullptr)
+    if (bias_on<M> && mods.rel_bias != nullptr)
       for (int e = tid; e < tab_len(mods.R); e += C::THREADS)
         reinterpret_cast<float*>(smem + C::OFF_TAB)[e] = table_entry(mods, r * p.hq + j, e, p.status);
   }
@@ -207,31 +269,21 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
-  volatile int* abort = &bars->abort;
   const uint32_t sbase = smem_u32(smem);
 
   if (warp == C::WP) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      prefetch_tmap(&tq);
-      prefetch_tmap(&tk);
-      prefetch_tmap(&tv);
-      for (int q = 0; q < NQT; ++q) {
-        if (!tile_ok[q]) continue;
-        mbar_arrive_expect_tx(&bars->q_full[q], C::TILE);
-        for (int c = 0; c < C::NCH; ++c)
-          tma_load_rows(smem + C::OFF_Q + q * C::TILE + c * kAtomBytes, &tq, &bars->q_full[q], p, c, qh, t0 + q * kBM);
+      if constexpr (!M::on) {
+        load_q();
+        load_first();
       }
-      auto load = [&](int kv, int n, uint64_t* full) {  // K (kv 0) or V tile n into its stage
-        uint8_t* dst = smem + (kv == 0 ? C::OFF_K : C::OFF_V) + (n % C::ST) * C::TILE;
-        for (int c = 0; c < C::NCH; ++c)
-          tma_load_rows(dst + c * kAtomBytes, kv == 0 ? &tk : &tv, full, p, c, kvh, lo + n * kBN, p.kv_seq_io != 0);
-      };
       int issued = 0;  // KV_ONE: tiles whose K and V loads were issued; else V_m (with K_{m+1}) groups
       if constexpr (C::KV_ONE) {
         // K_n and V_n once their stage is free: K_n replaces K_{n-ST} (free
         // after release n-ST), V_n replaces V_{n-ST} (release n-ST+1)
-        for (int n = 0; n < n_kv; ++n) {
+        issued = 1;
+        for (int n = 1; n < n_kv; ++n) {
           const int st = n % C::ST;
           bool ok_n = true;
           for (int kv = 0; kv < 2 && ok_n; ++kv) {
@@ -249,8 +301,6 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
         // K_0 alone; then V_m with K_{m+1}: V_m replaces V_{m-2} (free after
         // PV_{m-2}), K_{m+1} replaces K_{m-1} (free after S_{m-1}), both by
         // release m-1
-        mbar_arrive_expect_tx(&bars->k_first, C::TILE);
-        load(0, 0, &bars->k_first);
         for (int m = 0; m < n_kv; ++m) {
           if (m >= 1 && !mbar_wait(&bars->rel[(m - 1) % kRel], ((m - 1) / kRel) & 1, abort, p.status)) break;
           const bool k_next = m + 1 < n_kv;
@@ -350,7 +400,11 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
     const uint32_t s_tm = lane_base + q * kBN;
     const uint32_t o_tm = lane_base + C::T_O + q * D;
     int a = 0, b = 0, pe = 0;
-    if (row_ok) doc_bounds(p, mods, n_docs, t, a, b, pe);
+    if constexpr (M::on) {
+      if (row_ok) doc_bounds(p, mods, docs, t, a, b, pe);
+    } else {
+      if (row_ok) doc_bounds(p, mods, n_docs, t, a, b, pe);
+    }
     a = max(a, rk0);  // a ring step sees one key/value super-chunk
     b = min(b, rk1);
     const int gh = r * p.hq + j;  // global query head: the sink slice of this rank
@@ -369,9 +423,9 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
     [[maybe_unused]] const float* ramp = reinterpret_cast<const float*>(smem + C::OFF_RAMP);
     if constexpr (M::on) {
       visible_keys(mods, t, a, b, pe, p.causal, p.window_left, row_ok, mvlo, mvhi);
-      if (M::bias_on && mods.slopes != nullptr) slope2 = __ldg(mods.slopes + gh) * kLog2E;
-      if (M::bias_on && mods.rel_bias != nullptr) tab = reinterpret_cast<const float*>(smem + C::OFF_TAB) + mods.R + kTabPad;
-      fixed_ref = M::cap_on && mods.cap * kLog2E <= kFixedRefCap2;
+      if (bias_on<M> && mods.slopes != nullptr) slope2 = __ldg(mods.slopes + gh) * kLog2E;
+      if (bias_on<M> && mods.rel_bias != nullptr) tab = reinterpret_cast<const float*>(smem + C::OFF_TAB) + mods.R + kTabPad;
+      fixed_ref = cap_on<M> && mods.cap * kLog2E <= kFixedRefCap2;
       if (fixed_ref) {
         const float ref = fmaxf(m, 0.f);  // m is the sink's logit or -inf
         l = half == 0 ? ex2(m - ref) : 0.f;
@@ -409,10 +463,10 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
       if constexpr (M::on) {
         const int d0 = t - kv0, dw = d0 - lane;  // distance of column 0; the warp's first row's
         Affine f{sc, 0.f};
-        if constexpr (M::bias_on)
+        if constexpr (bias_on<M>)
           f = add_bias(s, tab, mods.R, slope2, ramp, d0, dw - (NC - 1), dw + 31, mods.later_hidden, sc);
-        if constexpr (M::cap_on) {
-          const float k = cap_scores<true>(s, f, mods.cap, M::bias_on);
+        if constexpr (cap_on<M>) {
+          const float k = cap_scores<true, true>(s, f, mods.cap, bias_on<M>);
           f = {k * mods.cap * kLog2E, 0.f};
         }
         sc = f.sc;
@@ -506,24 +560,65 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
       float other = 0.f;
       if (ok && (ok = exchange(l, other))) l = half == 0 ? l + other : other + l;
     }
+    [[maybe_unused]] bool stored = false;
     // ---- epilogue: O /= l, bf16 out; LSE = ln(sum) including the sink
     if (ok && (ok = mbar_wait(&bars->o_final[q], 0, abort, p.status))) {
       tc_fence_after();
       const float inv_l = l > 0.f ? 1.f / l : 0.f;
-      __nv_bfloat16* orow = out.o + row_offset(p, qh, p.hq, p.Hq, row_ok ? t : 0, D);
+      if constexpr (M::on) {
+        // The warp's 32 rows go through its part of the Q tile (every S has read it),
+        // 64 columns at a time in the swizzle of the tensor map (16-byte chunk e of row
+        // r at r*128 + (e ^ r%8)*16), and out by TMA: stores of whole rows by their
+        // threads touch a sector per 16 bytes and kept a CTA 2 us longer on its SM.
+        // Halves: of a 128-wide row one atom each, of a 64-wide one the first has it all.
+        constexpr int ATOMS = D / 64;
+        const int c0 = NH == 2 && ATOMS == 2 ? half : 0, c1 = NH == 2 ? (ATOMS == 2 ? half + 1 : 1 - half) : ATOMS;
+        if (c0 < c1) {
 #pragma unroll 1
-      for (int c = half * (D / 32 / NH); c < (half + 1) * (D / 32 / NH); ++c) {
-        uint32_t ov[32];
-        tmem_ld32(o_tm + c * 32, ov);
-        tmem_wait_ld();
-        uint32_t pkd[16];
+          for (int c = c0; c < c1; ++c) {
+            uint8_t* stage = smem + C::OFF_Q + q * C::TILE + c * kAtomBytes + (row & ~31) * 128;
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          pkd[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * inv_l, __uint_as_float(ov[2 * e + 1]) * inv_l);
-        if (row_ok) {
-          uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+            for (int h = 0; h < 2; ++h) {
+              uint32_t ov[32];
+              tmem_ld32(o_tm + c * 64 + h * 32, ov);
+              tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pkd[4 * e], pkd[4 * e + 1], pkd[4 * e + 2], pkd[4 * e + 3]);
+              for (int e = 0; e < 4; ++e) {
+                uint4 pk;
+                pk.x = pack_bf16x2(__uint_as_float(ov[8 * e]) * inv_l, __uint_as_float(ov[8 * e + 1]) * inv_l);
+                pk.y = pack_bf16x2(__uint_as_float(ov[8 * e + 2]) * inv_l, __uint_as_float(ov[8 * e + 3]) * inv_l);
+                pk.z = pack_bf16x2(__uint_as_float(ov[8 * e + 4]) * inv_l, __uint_as_float(ov[8 * e + 5]) * inv_l);
+                pk.w = pack_bf16x2(__uint_as_float(ov[8 * e + 6]) * inv_l, __uint_as_float(ov[8 * e + 7]) * inv_l);
+                *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * h + e) ^ (lane & 7)) << 4)) = pk;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int tw = t - lane;  // the warp's first row; rows past the tensor's end are dropped by the copy
+          if (lane == 0 && tw < p.BS) {
+            for (int c = c0; c < c1; ++c)
+              tma_store_rows(&to, smem + C::OFF_Q + q * C::TILE + c * kAtomBytes + (row & ~31) * 128, p, c, qh, tw);
+            bulk_commit_group();
+            stored = true;
+          }
+        }
+      } else {
+        __nv_bfloat16* orow = out.o + row_offset(p, qh, p.hq, p.Hq, row_ok ? t : 0, D);
+#pragma unroll 1
+        for (int c = half * (D / 32 / NH); c < (half + 1) * (D / 32 / NH); ++c) {
+          uint32_t ov[32];
+          tmem_ld32(o_tm + c * 32, ov);
+          tmem_wait_ld();
+          uint32_t pkd[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            pkd[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * inv_l, __uint_as_float(ov[2 * e + 1]) * inv_l);
+          if (row_ok) {
+            uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pkd[4 * e], pkd[4 * e + 1], pkd[4 * e + 2], pkd[4 * e + 3]);
+          }
         }
       }
       if (row_ok && half == 0) {
@@ -532,6 +627,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
             l > 0.f || (M::on && l != l) ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
       }
     }
+    if (stored) bulk_wait_group_all();  // the O stores are complete before the CTA ends
   }
 
   tc_fence_before();
@@ -555,7 +651,13 @@ static int run_fwd(const AttnArgs& a, const M& mods, int tab_bytes, const CUtens
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return USP_ERR_CUDA;
   const unsigned grid = static_cast<unsigned>(out.nqb) * a.P * a.hq;
-  kern<<<grid, C::THREADS, smem, st>>>(tq, tk, tv, a, out, mods);
+  CUtensorMap to;
+  memset(&to, 0, sizeof(to));  // used with modified scores alone
+  if constexpr (M::on) {
+    const int rc = make_rows_tmap(&to, o, a, a.hq, a.Hq, D, 32);
+    if (rc != USP_OK) return rc;
+  }
+  kern<<<grid, C::THREADS, smem, st>>>(tq, tk, tv, to, a, out, mods);
   return check_launch();
 }
 

@@ -22,56 +22,95 @@ namespace bwd {
 // over all tokens and would carry it (relative error 1e-3 measured; with this
 // pass under 1e-5).  It costs two of the five products of the backward.
 //
-// CTA = (query head, 128 rows), as the dQ pass: Q and dO in TMEM as A operands,
-// 128-key tiles of K and V through a shared-memory ring, no output tile.  S has
-// two TMEM buffers, so S_{n+1} is issued while the compute warps turn S_n into
-// P_n; dP_{n+1} follows once they have read dP_n.
-// TMEM: S [0,128) and [128,256), dP [256,384), Q [384, 384+D/2), dO [.., 384+D).
+// Persistent: one CTA per SM walks units (query head, 128 rows), late rows first,
+// u = blockIdx.x, + gridDim.x, ...  A CTA per unit spent as long on its set-up
+// (barriers, TMEM, first loads) and tear-down as on its tiles: DELTANOTE.
+// Q and dO tiles and a ring of 128-key tiles of K and V come by TMA and run on from
+// unit to unit; S has two TMEM buffers, so S_{n+1} is issued while the compute warps
+// turn S_n into P_n, behind dP_n, which takes dP's one buffer once they have read
+// dP_{n-1}.  The tile counter n runs over all of the CTA's units.
+// TMEM: S [0,128) and [128,256), dP [256,384).
+template <int D>
+struct CfgD {
+  static constexpr int NCH = D / 64;
+  static constexpr int TILE = NCH * kBN * 128;       // 128-row bf16 tile
+  static constexpr int QST = D == 128 ? 1 : 2;       // buffers of (Q, dO)
+  static constexpr int KST = D == 128 ? 3 : 5;       // buffers of K; S runs a tile ahead of dP
+  static constexpr int VST = D == 128 ? 2 : 4;       // buffers of V
+  static constexpr int OFF_Q = 0;                    // per buffer: Q, then dO
+  static constexpr int OFF_K = OFF_Q + QST * 2 * TILE;
+  static constexpr int OFF_V = OFF_K + KST * TILE;
+  static constexpr int OFF_BAR = OFF_V + VST * TILE;
+  static constexpr int OFF_RED = OFF_BAR + 512;      // [2][128] floats
+  static constexpr int SMEM = OFF_RED + 1024 + 1024;
+};
+static_assert(CfgD<128>::SMEM <= kMaxDynSmem && CfgD<64>::SMEM <= kMaxDynSmem, "delta shared memory");
+
 struct BarsD {
-  uint64_t qd_ready;
-  uint64_t k_full[8], v_full[8], kv_empty[8];
-  uint64_t s_full[2], s_free[2], dp_full, dp_free, mma_done;
+  uint64_t qd_full[2], qd_free[2];
+  uint64_t k_full[5], k_free[5], v_full[4], v_free[4];
+  uint64_t s_full[2], s_free[2], dp_full, dp_free;
+  uint64_t red_full[2];  // the second group's row sums of a unit (two in turn) are in shared memory
+  uint64_t mma_done;
   uint32_t tmem;
   int abort;
 };
-constexpr int kDeltaRed = 512;  // byte offset of the row sums of group 1 after the barriers
-static_assert(sizeof(BarsD) <= kDeltaRed && kDeltaRed + kBM * 4 <= 1024, "delta barrier block");
+static_assert(sizeof(BarsD) <= 512, "delta barrier block");
+
+struct DeltaUnit {
+  int r, j, hg, t0, lo, n_kv;
+  TileDocs docs;
+};
+
+// (by a whole warp)
+template <class M>
+__device__ __forceinline__ DeltaUnit delta_unit(const AttnArgs& p, const M& mods, int n_docs, int n_tiles, int u) {
+  DeltaUnit w;
+  w.hg = u % p.Hq;
+  w.r = w.hg / p.hq;
+  w.j = w.hg % p.hq;
+  w.t0 = (n_tiles - 1 - u / p.Hq) * kBM;
+  const int last = min(w.t0 + kBM, p.BS) - 1;
+  int hi;
+  w.docs = tile_docs(p, mods, n_docs, w.t0, last);
+  key_range(p, mods, w.docs, w.t0, last, w.lo, hi);
+  if (p.seq_io) w.lo &= ~(kBN - 1);  // key tiles inside one rank's shard
+  w.n_kv = hi > w.lo ? (hi - w.lo + kBN - 1) / kBN : 0;
+  return w;
+}
 
 template <int D, class M>
 __global__ void __launch_bounds__(kThreads, 1)
-    delta_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs p,
-                 const __nv_bfloat16* __restrict__ q_in, const __nv_bfloat16* __restrict__ do_in,
+    delta_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
+                 const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs p,
                  const float* __restrict__ lse, float* __restrict__ stats, int bsp, int n_tiles, M mods) {
-  using C = Cfg<D>;
+  using C = CfgD<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  BarsD* bars = reinterpret_cast<BarsD*>(smem + C::B_BAR);
-  float* red = reinterpret_cast<float*>(smem + C::B_BAR + kDeltaRed);
+  BarsD* bars = reinterpret_cast<BarsD*>(smem + C::OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-  const int qt = n_tiles - 1 - static_cast<int>(blockIdx.x) / p.Hq;
-  const int hg = static_cast<int>(blockIdx.x) % p.Hq;
-  const int r = hg / p.hq, j = hg % p.hq;
-  const HeadRef qh = q_head_ref(p, r, j), kvh = kv_head_ref(p, r, j / p.G);
-  const int t0 = qt * kBM;
 
   const int n_docs = checked_docs(p);
   if (n_docs == 0) return;
-  int lo, hi;
-  key_range(p, mods, n_docs, t0, min(t0 + kBM, p.BS) - 1, lo, hi);
-  if (p.seq_io) lo &= ~(kBN - 1);  // key tiles inside one rank's shard
-  const int n_kv = hi > lo ? (hi - lo + kBN - 1) / kBN : 0;
+  const int n_units = n_tiles * p.Hq;
 
   if (tid == 0) {
-    mbar_init(&bars->qd_ready, 8);
+    for (int s = 0; s < C::QST; ++s) {
+      mbar_init(&bars->qd_full[s], 1);
+      mbar_init(&bars->qd_free[s], 1);
+    }
     for (int s = 0; s < C::KST; ++s) {
       mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_free[s], 1);
+    }
+    for (int s = 0; s < C::VST; ++s) {
       mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->kv_empty[s], 1);
+      mbar_init(&bars->v_free[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->s_full[b], 1);
       mbar_init(&bars->s_free[b], 8);
+      mbar_init(&bars->red_full[b], 4);
     }
     mbar_init(&bars->dp_full, 1);
     mbar_init(&bars->dp_free, 8);
@@ -89,67 +128,113 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars->tmem;
   volatile int* abort = &bars->abort;
   const uint32_t sbase = smem_u32(smem);
-  constexpr uint32_t T_DP = 256, T_Q = 384, T_DO = T_Q + D / 2;
+  constexpr uint32_t T_DP = 256;
 
+  // The producer's and the MMA issuer's warps walk the units as a whole (delta_unit);
+  // their first lanes act.
   if (warp == 8) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
+      prefetch_tmap(&tq);
+      prefetch_tmap(&tdo);
       prefetch_tmap(&tk);
       prefetch_tmap(&tv);
-      int issued = 0;
-      for (int n = 0; n < n_kv; ++n) {
-        const int s = n % C::KST;
-        if (n >= C::KST && !mbar_wait(&bars->kv_empty[s], ((n / C::KST) - 1) & 1, abort, p.status)) break;
-        const int kv0 = lo + n * kBN;
-        mbar_arrive_expect_tx(&bars->k_full[s], C::TILE);
-        for (int c = 0; c < C::NCH; ++c)
-          tma_load_rows(smem + C::B_K + s * C::TILE + c * kAtomBytes, &tk, &bars->k_full[s], p, c, kvh, kv0);
-        mbar_arrive_expect_tx(&bars->v_full[s], C::TILE);
-        for (int c = 0; c < C::NCH; ++c)
-          tma_load_rows(smem + C::B_V + s * C::TILE + c * kAtomBytes, &tv, &bars->v_full[s], p, c, kvh, kv0);
-        issued = n + 1;
+    }
+    int n = 0, k = 0;  // tiles and units whose loads were issued
+    int vn = 0;        // (a K without its V, where a wait gave up between them)
+    bool ok = true;
+    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+      const DeltaUnit w = delta_unit(p, mods, n_docs, n_tiles, u);
+      if (w.n_kv == 0) continue;
+      if (lane == 0) {
+        const HeadRef qh = q_head_ref(p, w.r, w.j), kvh = kv_head_ref(p, w.r, w.j / p.G);
+        for (int i = 0; i < w.n_kv && ok; ++i) {
+          const int s = n % C::KST;
+          if (n >= C::KST && !(ok = mbar_wait(&bars->k_free[s], ((n / C::KST) - 1) & 1, abort, p.status))) break;
+          mbar_arrive_expect_tx(&bars->k_full[s], C::TILE);
+          for (int c = 0; c < C::NCH; ++c)
+            tma_load_rows(smem + C::OFF_K + s * C::TILE + c * kAtomBytes, &tk, &bars->k_full[s], p, c, kvh,
+                          w.lo + i * kBN);
+          ++n;
+          if (i == 0) {  // the unit's Q and dO, after its first keys: their buffer may still be read
+            const int b = k % C::QST;
+            if (k >= C::QST && !(ok = mbar_wait(&bars->qd_free[b], ((k / C::QST) - 1) & 1, abort, p.status))) break;
+            uint8_t* qd = smem + C::OFF_Q + b * 2 * C::TILE;
+            mbar_arrive_expect_tx(&bars->qd_full[b], 2 * C::TILE);
+            for (int c = 0; c < C::NCH; ++c) {
+              tma_load_rows(qd + c * kAtomBytes, &tq, &bars->qd_full[b], p, c, qh, w.t0);
+              tma_load_rows(qd + C::TILE + c * kAtomBytes, &tdo, &bars->qd_full[b], p, c, qh, w.t0);
+            }
+            ++k;
+          }
+          const int v = vn % C::VST;
+          if (vn >= C::VST && !(ok = mbar_wait(&bars->v_free[v], ((vn / C::VST) - 1) & 1, abort, p.status))) break;
+          mbar_arrive_expect_tx(&bars->v_full[v], C::TILE);
+          for (int c = 0; c < C::NCH; ++c)
+            tma_load_rows(smem + C::OFF_V + v * C::TILE + c * kAtomBytes, &tv, &bars->v_full[v], p, c, kvh,
+                          w.lo + i * kBN);
+          ++vn;
+        }
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {
       // never leave the CTA with copies still landing in its shared memory
-      for (int n = max(0, issued - C::KST); n < issued; ++n) {
-        mbar_wait(&bars->k_full[n % C::KST], (n / C::KST) & 1, abort, p.status);
-        mbar_wait(&bars->v_full[n % C::KST], (n / C::KST) & 1, abort, p.status);
-      }
+      for (int i = max(0, n - C::KST); i < n; ++i)
+        mbar_wait(&bars->k_full[i % C::KST], (i / C::KST) & 1, abort, p.status);
+      for (int i = max(0, vn - C::VST); i < vn; ++i)
+        mbar_wait(&bars->v_full[i % C::VST], (i / C::VST) & 1, abort, p.status);
+      for (int i = max(0, k - C::QST); i < k; ++i)
+        mbar_wait(&bars->qd_full[i % C::QST], (i / C::QST) & 1, abort, p.status);
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16(kBM, kBN, false, false);  // [128 rows x 128 keys], K = D
-      auto issue_s = [&](int n) -> bool {
-        const int s = n % C::KST, b = n & 1;
-        if (!mbar_wait(&bars->k_full[s], (n / C::KST) & 1, abort, p.status)) return false;
-        if (n >= 2 && !mbar_wait(&bars->s_free[b], ((n >> 1) - 1) & 1, abort, p.status)) return false;
-        tc_fence_after();
-        const uint32_t ka = sbase + C::B_K + s * C::TILE;
+    constexpr uint32_t idesc = idesc_bf16(kBM, kBN, false, false);  // [128 rows x 128 keys], K = D
+    auto issue = [&](uint32_t t_out, uint32_t a, uint32_t b) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ts(tmem + b * kBN, tmem + T_Q + kk * 8, kmajor_desc(ka, kAtomBytes, kk), id_s, kk > 0);
-        mma_commit(&bars->s_full[b]);
-        return true;
-      };
-      auto issue_dp = [&](int n) -> bool {
-        const int s = n % C::KST;
-        if (!mbar_wait(&bars->v_full[s], (n / C::KST) & 1, abort, p.status)) return false;
-        if (n >= 1 && !mbar_wait(&bars->dp_free, (n - 1) & 1, abort, p.status)) return false;
-        tc_fence_after();
-        const uint32_t va = sbase + C::B_V + s * C::TILE;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ts(tmem + T_DP, tmem + T_DO + kk * 8, kmajor_desc(va, kAtomBytes, kk), id_s, kk > 0);
-        mma_commit(&bars->dp_full);
-        mma_commit(&bars->kv_empty[s]);  // S_n was issued before: K_n and V_n are read
-        return true;
-      };
-      bool ok = mbar_wait(&bars->qd_ready, 0, abort, p.status);
-      if (ok && n_kv > 0) ok = issue_s(0);
-      for (int n = 0; n < n_kv && ok; ++n) {
-        if (n + 1 < n_kv) ok = issue_s(n + 1);
-        if (ok) ok = issue_dp(n);
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ss(tmem + t_out, kmajor_desc(a, kAtomBytes, kk), kmajor_desc(b, kAtomBytes, kk), idesc, kk > 0);
+    };
+    auto issue_s = [&](int n, uint32_t q_at) -> bool {
+      const int s = n % C::KST, b = n & 1;
+      if (!mbar_wait(&bars->k_full[s], (n / C::KST) & 1, abort, p.status)) return false;
+      if (n >= 2 && !mbar_wait(&bars->s_free[b], ((n >> 1) - 1) & 1, abort, p.status)) return false;
+      tc_fence_after();
+      issue(b * kBN, q_at, sbase + C::OFF_K + s * C::TILE);
+      mma_commit(&bars->s_full[b]);
+      mma_commit(&bars->k_free[s]);
+      return true;
+    };
+    auto issue_dp = [&](int n, uint32_t do_at) -> bool {
+      const int s = n % C::VST;
+      if (!mbar_wait(&bars->v_full[s], (n / C::VST) & 1, abort, p.status)) return false;
+      if (n >= 1 && !mbar_wait(&bars->dp_free, (n - 1) & 1, abort, p.status)) return false;
+      tc_fence_after();
+      issue(T_DP, do_at, sbase + C::OFF_V + s * C::TILE);
+      mma_commit(&bars->dp_full);
+      mma_commit(&bars->v_free[s]);
+      return true;
+    };
+    int n = 0, k = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+      const DeltaUnit w = delta_unit(p, mods, n_docs, n_tiles, u);
+      if (w.n_kv == 0) continue;
+      const int b = k % C::QST;
+      if (lane == 0 && (ok = mbar_wait(&bars->qd_full[b], (k / C::QST) & 1, abort, p.status))) {
+        const uint32_t q_at = sbase + C::OFF_Q + b * 2 * C::TILE, do_at = q_at + C::TILE;
+        ok = issue_s(n, q_at);
+        // dP_n before S_{n+1}: the compute warps come to dP_n first
+        for (int i = 0; i < w.n_kv && ok; ++i, ++n) {
+          ok = issue_dp(n, do_at);
+          if (ok && i + 1 < w.n_kv) ok = issue_s(n + 1, q_at);
+        }
+        if (ok) mma_commit(&bars->qd_free[b]);
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ++k;
+    }
+    if (lane == 0) {
       mma_commit(&bars->mma_done);
       mbar_wait(&bars->mma_done, 0, abort, p.status);
     }
@@ -157,79 +242,104 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ compute
     const int grp = warp >> 2;  // key columns [64*grp, 64*grp + 64) of every tile
     const int row = (warp & 3) * 32 + lane;
-    const int t = t0 + row;
-    const bool row_ok = t < p.BS;
     const uint32_t lb = tmem + ((static_cast<uint32_t>(warp & 3) * 32) << 16);
-    {
-      const size_t off = row_offset(p, qh, p.hq, p.Hq, row_ok ? t : 0, D);
-      row_to_tmem<D>(lb + (grp == 0 ? T_Q : T_DO), (grp == 0 ? q_in : do_in) + off, row_ok);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->qd_ready);
-    }
-    int a = 0, b = 0, pe = 0;
-    float nlse2 = -INFINITY;
-    if (row_ok) {
-      doc_bounds(p, mods, n_docs, t, a, b, pe);
-      const float l = __ldg(lse + stat_index(p, r, j, t));
-      nlse2 = l == -INFINITY ? l : l * -kLog2e;  // (the statistics' plane 0, see preprocess_kernel)
-    }
-    int vlo, vhi;  // the row's visible keys
-    visible_keys(mods, t, a, b, pe, p.causal, p.window_left, row_ok, vlo, vhi);
-    const float* tab =
-        mods.table != nullptr ? mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad : nullptr;
-    const float slope2 = mods.slopes != nullptr ? __ldg(mods.slopes + hg) * kLog2E : 0.f;
-    uint64_t acc2[4] = {0, 0, 0, 0};  // 8 independent partial sums, two per register
+    float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
+    // What a unit needs of its geometry; the next unit's is looked up under the first
+    // tile of the current one, whose dP is not there yet.
+    struct Row {
+      int lo, n_kv, vlo, vhi;
+      float lse;
+    };
+    auto row_of = [&](int u) -> Row {
+      Row x{0, 0, 1, 0, 0.f};
+      if (u >= n_units) return x;
+      const DeltaUnit w = delta_unit(p, mods, n_docs, n_tiles, u);
+      const int t = w.t0 + row;
+      const bool row_ok = t < p.BS;
+      if (row_ok) x.lse = __ldg(lse + stat_index(p, w.r, w.j, t));
+      int a = 0, b = 0, pe = 0;
+      if (row_ok) doc_bounds(p, mods, w.docs, t, a, b, pe);
+      visible_keys(mods, t, a, b, pe, p.causal, p.window_left, row_ok, x.vlo, x.vhi);
+      x.lo = w.lo;
+      x.n_kv = w.n_kv;
+      return x;
+    };
+    Row next = row_of(blockIdx.x);
+    int n = 0, k = 0;
     bool ok = true;
-    for (int n = 0; n < n_kv && ok; ++n) {
-      const int k0 = lo + n * kBN + grp * 64;  // first key of this group's columns
-      if (!(ok = mbar_wait(&bars->s_full[n & 1], (n >> 1) & 1, abort, p.status))) break;
-      tc_fence_after();
-      float x[64];
-      tmem_ld_cols<64>(lb + (n & 1) * kBN + grp * 64, x);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->s_free[n & 1]);
-      const int d0 = t - k0, dw = d0 - lane;
-      Affine f{p.scale_log2, 0.f};
-      if constexpr (M::bias_on)
-        f = add_bias(x, tab, mods.R, slope2, nullptr, d0, dw - 63, dw + 31, mods.later_hidden, p.scale_log2);
-      if constexpr (M::cap_on) {
-        const float k = cap_scores<false>(x, f, mods.cap, M::bias_on);
-        f = {k * mods.cap * kLog2E, 0.f};
+    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+      const Row w = next;
+      const int hg = u % p.Hq, t = (n_tiles - 1 - u / p.Hq) * kBM + row;
+      const float nlse2 = w.lse == -INFINITY || t >= p.BS ? -INFINITY : w.lse * -kLog2e;  // (as in preprocess_kernel)
+      const float* tab =
+          mods.table != nullptr ? mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad : nullptr;
+      const float slope2 = mods.slopes != nullptr ? __ldg(mods.slopes + hg) * kLog2E : 0.f;
+      if (w.n_kv == 0) {
+        next = row_of(u + static_cast<int>(gridDim.x));
+        continue;
       }
-      const int c_lo = vlo - k0, c_hi = vhi - k0;
-      if (!(c_lo <= 0 && c_hi >= 63)) {
+      uint64_t acc2[4] = {0, 0, 0, 0};  // 8 independent partial sums, two per register
+      for (int i = 0; i < w.n_kv && ok; ++i, ++n) {
+        const int k0 = w.lo + i * kBN + grp * 64;  // first key of this group's columns
+        if (!(ok = mbar_wait(&bars->s_full[n & 1], (n >> 1) & 1, abort, p.status))) break;
+        tc_fence_after();
+        float x[64];
+        tmem_ld_cols<64>(lb + (n & 1) * kBN + grp * 64, x);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->s_free[n & 1]);
+        const int d0 = t - k0, dw = d0 - lane;
+        Affine f{p.scale_log2, 0.f};
+        if constexpr (bias_on<M>)
+          f = add_bias(x, tab, mods.R, slope2, nullptr, d0, dw - 63, dw + 31, mods.later_hidden, p.scale_log2);
+        if constexpr (cap_on<M>) {
+          cap_scores<false, true>(x, f, mods.cap, true);
+          f = {mods.cap * kLog2E, 0.f};
+        }
+        const int c_lo = w.vlo - k0, c_hi = w.vhi - k0;
+        if (!(c_lo <= 0 && c_hi >= 63)) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (c < c_lo || c > c_hi) x[c] = -INFINITY;
+          for (int c = 0; c < 64; ++c)
+            if (c < c_lo || c > c_hi) x[c] = -INFINITY;
+        }
+        const uint64_t sc2 = f2_pack(f.sc, f.sc), nl2 = f2_pack(nlse2 + f.off, nlse2 + f.off);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float2 e = f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sc2, nl2));
+          x[c] = ex2(e.x);
+          x[c + 1] = ex2(e.y);
+        }
+        if (i == 0) next = row_of(u + static_cast<int>(gridDim.x));
+        if (!(ok = mbar_wait(&bars->dp_full, n & 1, abort, p.status))) break;
+        tc_fence_after();
+        float dp[64];
+        tmem_ld_cols<64>(lb + T_DP + grp * 64, dp);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->dp_free);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2)
+          acc2[(c >> 1) & 3] = f2_fma(f2_pack(x[c], x[c + 1]), f2_pack(dp[c], dp[c + 1]), acc2[(c >> 1) & 3]);
       }
-      const uint64_t sc2 = f2_pack(f.sc, f.sc), nl2 = f2_pack(nlse2 + f.off, nlse2 + f.off);
-#pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        const float2 e = f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sc2, nl2));
-        x[c] = ex2(e.x);
-        x[c + 1] = ex2(e.y);
+      if (!ok) break;
+      const float2 s01 = f2_unpack(f2_add(acc2[0], acc2[1])), s23 = f2_unpack(f2_add(acc2[2], acc2[3]));
+      const float sum = (s01.x + s01.y) + (s23.x + s23.y);
+      // The two key halves of a row meet.  The second group writes a buffer again two
+      // units later, for which it has waited for a dP that the first group's reading of
+      // the unit between released: the first group has read this one by then.
+      if (grp == 1) {
+        red[(k & 1) * kBM + row] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->red_full[k & 1]);
+      } else {
+        if (!(ok = mbar_wait(&bars->red_full[k & 1], (k >> 1) & 1, abort, p.status))) break;
+        if (t < p.BS) {
+          float* plane = stats + plane_index(bsp, p.hq, hg / p.hq, hg % p.hq, 0, t);
+          plane[0] = nlse2 - slope_of_row(mods, slope2, t);
+          plane[bsp] = sum + red[(k & 1) * kBM + row];
+        }
       }
-      if (!(ok = mbar_wait(&bars->dp_full, n & 1, abort, p.status))) break;
-      tc_fence_after();
-      float dp[64];
-      tmem_ld_cols<64>(lb + T_DP + grp * 64, dp);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->dp_free);
-#pragma unroll
-      for (int c = 0; c < 64; c += 2)
-        acc2[(c >> 1) & 3] = f2_fma(f2_pack(x[c], x[c + 1]), f2_pack(dp[c], dp[c + 1]), acc2[(c >> 1) & 3]);
-    }
-    const float2 s01 = f2_unpack(f2_add(acc2[0], acc2[1])), s23 = f2_unpack(f2_add(acc2[2], acc2[3]));
-    const float sum = (s01.x + s01.y) + (s23.x + s23.y);
-    // the two key halves of a row meet; every compute warp comes here, also after a wait that gave up
-    if (grp == 1) red[row] = sum;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (grp == 0 && row_ok) {
-      stats[plane_index(bsp, p.hq, r, j, 0, t)] = nlse2 - slope_of_row(mods, slope2, t);
-      stats[plane_index(bsp, p.hq, r, j, 1, t)] = sum + red[row];
+      ++k;
     }
   }
 
@@ -248,17 +358,20 @@ namespace {
 template <int D, class M>
 int run_delta(const AttnArgs& a, const M& m, const void* q, const void* k, const void* v, const void* dO,
               const float* lse, float* stats, cudaStream_t st) {
-  using C = bwd::Cfg<D>;
-  CUtensorMap tk, tv;
+  using C = bwd::CfgD<D>;
+  CUtensorMap tq, tdo, tk, tv;
   int rc;
+  if ((rc = make_rows_tmap(&tq, q, a, a.hq, a.Hq, D, kBM)) != USP_OK) return rc;
+  if ((rc = make_rows_tmap(&tdo, dO, a, a.hq, a.Hq, D, kBM)) != USP_OK) return rc;
   if ((rc = make_rows_tmap(&tk, k, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
   if ((rc = make_rows_tmap(&tv, v, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
-  if (cudaFuncSetAttribute(bwd::delta_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::B_SMEM) != cudaSuccess)
+  auto kern = bwd::delta_kernel<D, M>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return USP_ERR_CUDA;
   const int n_tiles = (a.BS + kBM - 1) / kBM;
-  bwd::delta_kernel<D, M><<<static_cast<unsigned>(n_tiles) * a.Hq, bwd::kThreads, C::B_SMEM, st>>>(
-      tk, tv, a, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(dO), lse, stats,
-      stats_row_pitch(a.BS), n_tiles, m);
+  const long long units = static_cast<long long>(n_tiles) * a.Hq;
+  const int grid = units < device_sm_count() ? static_cast<int>(units) : device_sm_count();
+  kern<<<grid, bwd::kThreads, C::SMEM, st>>>(tq, tdo, tk, tv, a, lse, stats, stats_row_pitch(a.BS), n_tiles, m);
   return check_launch();
 }
 

@@ -55,14 +55,16 @@ struct ModArgs {
 template <bool CAP, bool BIAS>
 struct Mods : ModArgs {
   static constexpr bool on = true;
-  static constexpr bool cap_on = CAP;
-  static constexpr bool bias_on = BIAS;
 };
 
 template <class M>
 constexpr bool bias_on = false;
 template <bool CAP, bool BIAS>
 constexpr bool bias_on<Mods<CAP, BIAS>> = BIAS;
+template <class M>
+constexpr bool cap_on = false;
+template <bool CAP, bool BIAS>
+constexpr bool cap_on<Mods<CAP, BIAS>> = CAP;
 
 // f(M{}) with the combination that `m` needs.
 template <class F>
@@ -166,6 +168,113 @@ __device__ __forceinline__ void query_range(const AttnArgs& p, const M& m, int n
   }
 }
 
+// find_doc by a whole warp, for one token: 32 boundaries are looked at at once
+// instead of one after the other.
+__device__ __forceinline__ int find_doc_warp(const int32_t* __restrict__ cu, int n, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const unsigned at_or_before = __ballot_sync(0xffffffffu, at < hi && __ldg(cu + at) <= t) | 1u;  // (cu[lo] <= t)
+    lo += (31 - __clz(at_or_before)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// The documents of a tile's first and last token, found by a whole warp.
+struct TileDocs {
+  int d0, a0, b0, pe0, d1, a1, b1, pe1;
+};
+template <class M>
+__device__ __forceinline__ TileDocs tile_docs(const AttnArgs& p, const M& m, int n, int first, int last) {
+  TileDocs w;
+  w.d0 = find_doc_warp(p.cu, n, first);
+  w.a0 = max(0, min(__ldg(p.cu + w.d0), first));
+  w.b0 = min(p.BS, max(__ldg(p.cu + w.d0 + 1), first + 1));
+  w.pe0 = prefix_end(m, w.d0, w.a0, w.b0, p.status);
+  w.d1 = w.d0;
+  w.a1 = w.a0;
+  w.b1 = w.b0;
+  w.pe1 = w.pe0;
+  if (last >= w.b0) {
+    w.d1 = find_doc_warp(p.cu, n, last);
+    w.a1 = max(0, min(__ldg(p.cu + w.d1), last));
+    w.b1 = min(p.BS, max(__ldg(p.cu + w.d1 + 1), last + 1));
+    w.pe1 = prefix_end(m, w.d1, w.a1, w.b1, p.status);
+  }
+  return w;
+}
+
+// checked_docs and tile_docs together, their loads in flight at the same time:
+// false (the status recorded) when cu_seqlens cannot describe the sequence.  The
+// lookups stay inside cu_seqlens whatever it holds, since 1 <= n <= B*S.
+template <class M>
+__device__ __forceinline__ bool checked_tile_docs(const AttnArgs& p, const M& m, int first, int last, int& n,
+                                                  TileDocs& w) {
+  n = __ldg(p.n_docs);
+  bool ok = n >= 1 && n <= p.BS;
+  if (ok) {
+    const int c0 = __ldg(p.cu), cn = __ldg(p.cu + n);
+    w = tile_docs(p, m, n, first, last);
+    ok = c0 == 0 && cn == p.BS;
+  }
+  if (!ok) {
+    if (threadIdx.x == 0) set_status(p.status, USP_ERR_BAD_SEQLENS);
+    return false;
+  }
+  if (blockIdx.x == 0) {
+    for (int d = threadIdx.x; d < n; d += blockDim.x)
+      if (__ldg(p.cu + d + 1) <= __ldg(p.cu + d)) set_status(p.status, USP_ERR_BAD_SEQLENS);
+  }
+  return true;
+}
+
+// doc_bounds of a token of the tile.
+template <class M>
+__device__ __forceinline__ void doc_bounds(const AttnArgs& p, const M& m, const TileDocs& w, int t, int& a, int& b,
+                                           int& pe) {
+  a = w.a0;
+  b = w.b0;
+  pe = w.pe0;
+  if (t >= w.a1) {
+    a = w.a1;
+    b = w.b1;
+    pe = w.pe1;
+  } else if (t >= w.b0) {  // a document inside the tile
+    int lo = w.d0 + 1, hi = w.d1;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.cu + mid) <= t) lo = mid; else hi = mid;
+    }
+    a = max(0, min(__ldg(p.cu + lo), t));
+    b = min(p.BS, max(__ldg(p.cu + lo + 1), t + 1));
+    pe = prefix_end(m, lo, a, b, p.status);
+  }
+}
+
+// key_range / query_range of the tile.
+template <class M>
+__device__ __forceinline__ void key_range(const AttnArgs& p, const M&, const TileDocs& w, int first, int last, int& lo,
+                                          int& hi) {
+  lo = w.a0;
+  hi = p.causal ? max(last + 1, w.pe1) : w.b1;
+  if (p.window_left >= 0) {
+    lo = max(lo, first - p.window_left);
+    if (!p.causal) hi = min(hi, last + p.window_left + 1);
+  }
+}
+template <class M>
+__device__ __forceinline__ void query_range(const AttnArgs& p, const M&, const TileDocs& w, int first, int last,
+                                            int& lo, int& hi) {
+  lo = !p.causal || first < w.pe0 ? w.a0 : first;
+  hi = w.b1;
+  if (p.window_left >= 0) {
+    hi = min(hi, last + p.window_left + 1);
+    if (!p.causal) lo = max(lo, first - p.window_left);
+  }
+}
+
 // What a block of scores still has to go through: x2 = x * sc + off.
 struct Affine {
   float sc, off;
@@ -233,7 +342,7 @@ __device__ __forceinline__ Affine add_bias(float (&x)[N], const float* row, int 
 template <class M>
 __device__ __forceinline__ float slope_of_row(const M& m, float slope2, int t) {
   if constexpr (bias_on<M>) {
-    if constexpr (!M::cap_on) return slope2 * static_cast<float>(t & 31);
+    if constexpr (!cap_on<M>) return slope2 * static_cast<float>(t & 31);
   }
   return 0.f;
 }
@@ -299,10 +408,8 @@ __host__ __device__ constexpr float tanh_q(int i) {
 }
 
 // tanh of any y: the polynomial inside |y| <= 1, outside 1 - 2 e / (1 + e) with
-// e = e^(-2|y|) <= 0.14, whose absolute error is under 1e-7.  Keeps NaN.  Not
-// inlined: unrolled over a block's scores it would push the loops that do run out of
-// the instruction cache.
-static __device__ __noinline__ float tanh_any(float y) {
+// e = e^(-2|y|) <= 0.14, whose absolute error is under 1e-7.  Keeps NaN.
+__device__ __forceinline__ float tanh_any(float y) {
   const float t = y * y;
   float q = tanh_q<6>(6);
 #pragma unroll
@@ -311,6 +418,10 @@ static __device__ __noinline__ float tanh_any(float y) {
   const float big = fmaf(-2.f * e, rcp(1.f + e), 1.f);
   return fabsf(y) <= 1.f ? y * q : copysignf(big, y);
 }
+
+// The same as a call: unrolled over a block's scores the rare path is several times
+// the size of the loops that do run.
+static __device__ __noinline__ float tanh_any_call(float y) { return tanh_any(y); }
 
 // x -> tanh(k x) / k by the polynomial of degree DEG in (k x)^2: the powers of k
 // go into its coefficients, so k costs no multiplication per score.
@@ -340,10 +451,10 @@ __device__ __forceinline__ void tanh_poly(float (&x)[N], float k) {
 // The kernels are bound by the packed fp32 operations of a score, so a warp takes
 // the shortest polynomial that its largest |y| allows (forward, 8192 packed
 // tokens, D = 128, cap 30: CAPNOTE).
-template <bool TIERS, int N>
+template <bool TIERS, bool CALL, int N>
 __device__ __forceinline__ float cap_scores(float (&x)[N], Affine f, float cap, bool biased) {
   float k = f.sc * (0.6931471805599453f / cap);
-  if (biased || k < 0x1p-9f) {
+  if (!TIERS || biased || k < 0x1p-9f) {
     // to y itself: the offset of a bias, or a k whose powers would leave fp32
     const float ko = f.off * (0.6931471805599453f / cap);
     const uint64_t k2 = f2_pack(k, k), o2 = f2_pack(ko, ko);
@@ -368,22 +479,33 @@ __device__ __forceinline__ float cap_scores(float (&x)[N], Affine f, float cap, 
     tanh_poly<6>(x, k);
   } else {
 #pragma unroll
-    for (int c = 0; c < N; ++c) x[c] = tanh_any(x[c] * k);
+    for (int c = 0; c < N; ++c) x[c] = CALL ? tanh_any_call(x[c] * k) : tanh_any(x[c] * k);
     k = 1.f;
   }
   return k;
 }
 
-// g = 1 - tanh^2, the cap's derivative, from cap_scores' w and k.
+// g = 1 - tanh^2, the cap's derivative, from the tanh.
 template <int N>
-__device__ __forceinline__ void cap_slope(const float (&w)[N], float (&g)[N], float k) {
-  const uint64_t mk2 = f2_pack(-k * k, -k * k), one = f2_pack(1.f, 1.f);
+__device__ __forceinline__ void cap_slope(const float (&th)[N], float (&g)[N]) {
+  const uint64_t minus = f2_pack(-1.f, -1.f), one = f2_pack(1.f, 1.f);
 #pragma unroll
   for (int c = 0; c < N; c += 2) {
-    const uint64_t y = f2_pack(w[c], w[c + 1]);
-    const float2 z = f2_unpack(f2_fma(f2_mul(y, mk2), y, one));
+    const uint64_t y = f2_pack(th[c], th[c + 1]);
+    const float2 z = f2_unpack(f2_fma(f2_mul(y, minus), y, one));
     g[c] = z.x;
     g[c + 1] = z.y;
+  }
+}
+
+// p *= g
+template <int N>
+__device__ __forceinline__ void f2_scale(float (&p)[N], const float (&g)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const float2 z = f2_unpack(f2_mul(f2_pack(p[c], p[c + 1]), f2_pack(g[c], g[c + 1])));
+    p[c] = z.x;
+    p[c + 1] = z.y;
   }
 }
 
