@@ -419,9 +419,38 @@ __device__ __forceinline__ float tanh_any(float y) {
   return fabsf(y) <= 1.f ? y * q : copysignf(big, y);
 }
 
-// The same as a call: unrolled over a block's scores the rare path is several times
-// the size of the loops that do run.
-static __device__ __noinline__ float tanh_any_call(float y) { return tanh_any(y); }
+// x -> tanh(k x) for scores of which some lie beyond the cap.  Rare, and unrolled
+// over a block several times the size of the code that does run, so a loop over the
+// block: through TMEM, whose columns [tmem, tmem + N) are this warp's to write.
+template <int N>
+__device__ __forceinline__ void tanh_rare(float (&x)[N], float k, uint32_t tmem) {
+#pragma unroll
+  for (int c = 0; c < N; c += 32) {
+    uint32_t v[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(x[c + e]);
+    tmem_st32(tmem + c, v);
+  }
+  tmem_wait_st();
+#pragma unroll 1
+  for (int c = 0; c < N; c += 4) {
+    uint32_t v[4];
+    tmem_ld4(tmem + c, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(tanh_any(__uint_as_float(v[e]) * k));
+    tmem_st4(tmem + c, v);
+    tmem_wait_st();
+  }
+#pragma unroll
+  for (int c = 0; c < N; c += 32) {
+    uint32_t v[32];
+    tmem_ld32(tmem + c, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[c + e] = __uint_as_float(v[e]);
+  }
+}
 
 // x -> tanh(k x) / k by the polynomial of degree DEG in (k x)^2: the powers of k
 // go into its coefficients, so k costs no multiplication per score.
@@ -450,11 +479,12 @@ __device__ __forceinline__ void tanh_poly(float (&x)[N], float k) {
 // k: the capped score in the log2 domain is then w k cap log2e, and tanh is w k.
 // The kernels are bound by the packed fp32 operations of a score, so a warp takes
 // the shortest polynomial that its largest |y| allows (forward, 8192 packed
-// tokens, D = 128, cap 30: CAPNOTE).
-template <bool TIERS, bool CALL, int N>
-__device__ __forceinline__ float cap_scores(float (&x)[N], Affine f, float cap, bool biased) {
+// tokens, D = 128, cap 30: 225 us, and 241 with degree 6 alone).
+// `tmem`: N columns of this warp's lanes, free to write.
+template <int TIERS, int N>
+__device__ __forceinline__ float cap_scores(float (&x)[N], Affine f, float cap, bool biased, uint32_t tmem) {
   float k = f.sc * (0.6931471805599453f / cap);
-  if (!TIERS || biased || k < 0x1p-9f) {
+  if (TIERS != 3 || biased || k < 0x1p-9f) {
     // to y itself: the offset of a bias, or a k whose powers would leave fp32
     const float ko = f.off * (0.6931471805599453f / cap);
     const uint64_t k2 = f2_pack(k, k), o2 = f2_pack(ko, ko);
@@ -471,15 +501,14 @@ __device__ __forceinline__ float cap_scores(float (&x)[N], Affine f, float cap, 
   for (int c = 0; c < N; c += 2) top4[(c >> 1) & 3] = fmax3(top4[(c >> 1) & 3], fabsf(x[c]), fabsf(x[c + 1]));
   // (the max skips a NaN, which every path keeps)
   const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * k;
-  if (TIERS && !__any_sync(0xffffffffu, top > 0.25f)) {
+  if (TIERS > 1 && !__any_sync(0xffffffffu, top > 0.25f)) {
     tanh_poly<2>(x, k);
-  } else if (TIERS && !__any_sync(0xffffffffu, top > 0.5f)) {
+  } else if (TIERS > 2 && !__any_sync(0xffffffffu, top > 0.5f)) {
     tanh_poly<4>(x, k);
   } else if (!__any_sync(0xffffffffu, top > 1.f)) {
     tanh_poly<6>(x, k);
   } else {
-#pragma unroll
-    for (int c = 0; c < N; ++c) x[c] = CALL ? tanh_any_call(x[c] * k) : tanh_any(x[c] * k);
+    tanh_rare(x, k, tmem);
     k = 1.f;
   }
   return k;

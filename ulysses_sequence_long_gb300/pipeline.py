@@ -41,7 +41,7 @@ from . import binding as B_
 
 
 # Layers with modified scores: up to this many tokens the forward reads k and v from their shards (see
-# UlyssesAttention).  TOKENS_NOTE
+# UlyssesAttention).  
 KV_IN_PLACE_TOKENS = 2048
 
 
