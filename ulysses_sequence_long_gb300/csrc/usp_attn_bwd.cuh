@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(256) preprocess_kernel(const uint4* __restrict
   const int Hb = p.seq_io ? p.P * p.hq : p.hq;
   const int tid = threadIdx.x, lane_row = tid % LPR;
   const int nct = (p.BS + tok - 1) / tok;  // head-layout chunks per rank
+  if constexpr (M::on) grid_wait();
   for (int c = blockIdx.x; c < n_chunks; c += gridDim.x) {
     // chunk -> first token t0 (rank-local, b*S + s), its rank (head-layout) and
     // the element offset of its first row
@@ -403,6 +404,7 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if constexpr (M::on) grid_wait();
   if (static_cast<int>(smem - smem_raw) > C::A_SMEM - C::A_NEED) {  // the launch's bytes cannot hold the layout
     if (tid == 0) set_status(p.status, USP_ERR_CUDA);
     return;
@@ -936,6 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const HeadRef qh = q_head_ref(p, r, j), kvh = kv_head_ref(p, r, j / p.G);
   const int t0 = qt * kBM;
 
+  if constexpr (M::on) grid_wait();
   const int n_docs = checked_docs(p);
   if (n_docs == 0) return;
   int lo, hi;
@@ -1239,6 +1242,7 @@ __global__ void __launch_bounds__(kDsThreads, 1)
   BarsDs* bars = reinterpret_cast<BarsDs*>(smem + C::BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  if constexpr (M::on) grid_wait();
   const int n_docs = checked_docs(p);
   if (n_docs == 0) return;
 
@@ -1484,6 +1488,9 @@ static int run_preprocess(const usp_attn_params& prm, const M& mods, const void*
   auto kern = prm.D == 128 ? bwd::preprocess_kernel<128, M> : bwd::preprocess_kernel<64, M>;
   if (smem > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return USP_ERR_CUDA;
+  if constexpr (M::on)
+    return launch_chained(kern, grid, 256, smem, 1, st, static_cast<const uint4*>(o), static_cast<const uint4*>(dO),
+                          lse, stats, a, bsp, n_chunks, tok, mods);
   kern<<<grid, 256, smem, st>>>(static_cast<const uint4*>(o), static_cast<const uint4*>(dO), lse, stats, a, bsp,
                                 n_chunks, tok, mods);
   if (check_launch() != USP_OK) return USP_ERR_CUDA;
@@ -1530,6 +1537,9 @@ static int run_grad_pass(bool dq_pass, const AttnArgs& a, const M& mods, const v
       return USP_ERR_CUDA;
     const int n_units = g.n_tiles * a.n_qh;
     const int grid = n_units < device_sm_count() ? n_units : device_sm_count();  // persistent: one CTA per SM
+    if constexpr (M::on)
+      return launch_chained(bwd::dq_ds_kernel<D, MD>, grid, bwd::kDsThreads, CD::SMEM, 1, st, tk, tds, tdq, a, g,
+                            n_units, dmods);
     bwd::dq_ds_kernel<D, MD><<<grid, bwd::kDsThreads, CD::SMEM, st>>>(tk, tds, tdq, a, g, n_units, dmods);
     return check_launch();
   }
@@ -1558,23 +1568,16 @@ static int run_grad_pass(bool dq_pass, const AttnArgs& a, const M& mods, const v
         auto kern = bwd::dkdv_kernel<D, M, true>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::A_SMEM) != cudaSuccess)
           return USP_ERR_CUDA;
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim = {static_cast<unsigned>(g.split), 1, 1};
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(grid * g.split);
-        cfg.blockDim = dim3(bwd::Team<M>::THREADS);
-        cfg.dynamicSmemBytes = C::A_SMEM;
-        cfg.stream = st;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, kern, tq, tdo, tst, tds_st, tk, tv, a, g, mods) == cudaSuccess ? USP_OK
-                                                                                                        : USP_ERR_CUDA;
+        return launch_chained(kern, grid * g.split, bwd::Team<M>::THREADS, C::A_SMEM, g.split, st, tq, tdo, tst, tds_st,
+                              tk, tv, a, g, mods);
       }
     }
     auto kern = bwd::dkdv_kernel<D, M, false>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::A_SMEM) != cudaSuccess)
       return USP_ERR_CUDA;
+    if constexpr (M::on)
+      return launch_chained(kern, grid, bwd::Team<M>::THREADS, C::A_SMEM, 1, st, tq, tdo, tst, tds_st, tk, tv, a, g,
+                            mods);
     kern<<<grid, bwd::Team<M>::THREADS, C::A_SMEM, st>>>(tq, tdo, tst, tds_st, tk, tv, a, g, mods);
   } else {
     // 128-key tiles of K and V stream past TMEM-resident Q, dO
@@ -1583,7 +1586,10 @@ static int run_grad_pass(bool dq_pass, const AttnArgs& a, const M& mods, const v
     if ((rc = make_rows_tmap(&tv, v, a, a.hk, a.Hkv, D, kBN)) != USP_OK) return rc;
     if (cudaFuncSetAttribute(bwd::dq_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::B_SMEM) != cudaSuccess)
       return USP_ERR_CUDA;
-    bwd::dq_kernel<D, M><<<static_cast<unsigned>(g.n_tiles) * a.n_qh, bwd::kThreads, C::B_SMEM, st>>>(tk, tv, a, g, mods);
+    const unsigned grid = static_cast<unsigned>(g.n_tiles) * a.n_qh;
+    if constexpr (M::on)
+      return launch_chained(bwd::dq_kernel<D, M>, grid, bwd::kThreads, C::B_SMEM, 1, st, tk, tv, a, g, mods);
+    bwd::dq_kernel<D, M><<<grid, bwd::kThreads, C::B_SMEM, st>>>(tk, tv, a, g, mods);
   }
   return check_launch();
 }

@@ -169,8 +169,9 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
   // up, and the first K before the CTA has its TMEM; by the producer itself.
   const bool is_producer = warp == C::WP && lane == 0;
   if constexpr (M::on) {
+    if (is_producer) init_bars();
+    grid_wait();
     if (is_producer) {
-      init_bars();
       load_q();
     }
   }
@@ -656,6 +657,7 @@ static int run_fwd(const AttnArgs& a, const M& mods, int tab_bytes, const CUtens
   if constexpr (M::on) {
     const int rc = make_rows_tmap(&to, o, a, a.hq, a.Hq, D, 32);
     if (rc != USP_OK) return rc;
+    return launch_chained(kern, grid, C::THREADS, smem, 1, st, tq, tk, tv, to, a, out, mods);
   }
   kern<<<grid, C::THREADS, smem, st>>>(tq, tk, tv, to, a, out, mods);
   return check_launch();

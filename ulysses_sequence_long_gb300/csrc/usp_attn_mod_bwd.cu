@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   BarsD* bars = reinterpret_cast<BarsD*>(smem + C::OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  grid_wait();
   const int n_docs = checked_docs(p);
   if (n_docs == 0) return;
   const int n_units = n_tiles * p.Hq;
@@ -372,8 +373,8 @@ int run_delta(const AttnArgs& a, const M& m, const void* q, const void* k, const
   const int n_tiles = (a.BS + kBM - 1) / kBM;
   const long long units = static_cast<long long>(n_tiles) * a.Hq;
   const int grid = units < device_sm_count() ? static_cast<int>(units) : device_sm_count();
-  kern<<<grid, bwd::kThreads, C::SMEM, st>>>(tq, tdo, tk, tv, a, lse, stats, stats_row_pitch(a.BS), n_tiles, m);
-  return check_launch();
+  return launch_chained(kern, grid, bwd::kThreads, C::SMEM, 1, st, tq, tdo, tk, tv, a, lse, stats,
+                        stats_row_pitch(a.BS), n_tiles, m);
 }
 
 constexpr int kRelThreads = 256;
@@ -423,6 +424,7 @@ size_t mod_ds_bytes(const usp_attn_params& p, const usp_score_mods& m) {
 __global__ void __launch_bounds__(kRelThreads)
     rel_expand_kernel(ModArgs m, float* __restrict__ table, float4* __restrict__ clear, size_t n_clear, int32_t* status) {
   const int n = tab_len(m.R), h = blockIdx.x;
+  grid_wait();
   if (blockIdx.y == 0)
     for (int e = threadIdx.x; e < n; e += kRelThreads)
       table[static_cast<size_t>(h) * n + e] = table_entry(m, h, e, status);
@@ -437,6 +439,7 @@ __global__ void __launch_bounds__(kRelThreads)
 __global__ void __launch_bounds__(1024)
     rel_sum_kernel(const float* __restrict__ partial, float* __restrict__ sums, int n_rows, int per, int row) {
   const int h = blockIdx.x, s = blockIdx.y;
+  grid_wait();
   const int r0 = s * per, r1 = min(n_rows, r0 + per);
   const float* src = partial + static_cast<size_t>(h) * n_rows * row;
   for (int c = threadIdx.x; c < row; c += blockDim.x) {
@@ -462,6 +465,7 @@ __global__ void __launch_bounds__(kRelThreads)
   const int h = blockIdx.x, row = 2 * m.R + 1, lane = threadIdx.x & 31;
   int* bucket = reinterpret_cast<int*>(by_dist + row);
   const float* src = sums + static_cast<size_t>(h) * splits * row;
+  grid_wait();
   for (int c = threadIdx.x; c < row; c += kRelThreads) {
     float acc = 0.f;
 #pragma unroll 4
@@ -487,6 +491,7 @@ __global__ void __launch_bounds__(kSinkThreads)
                      AttnArgs p, int bsp) {
   __shared__ float red[kSinkThreads];
   const int r = blockIdx.x / p.hq, j = blockIdx.x % p.hq;
+  grid_wait();
   const float z2 = __ldg(p.sinks + blockIdx.x) * kLog2E;
   const float* dd = stats + bwd::plane_index(bsp, p.hq, r, j, 1, 0);
   float acc = 0.f;
@@ -543,9 +548,10 @@ int launch_attn_mod_bwd_preprocess(const usp_attn_params& p, const usp_score_mod
     uint8_t* base = static_cast<uint8_t*>(ws);
     const size_t n_clear = sm.rel_bias_grad ? (L.sums - L.partial) / sizeof(float4) : 0;
     const int per_head = n_clear > 0 ? (4 * device_sm_count() + p.Hq - 1) / p.Hq : 1;
-    rel_expand_kernel<<<dim3(p.Hq, per_head), kRelThreads, 0, st>>>(
-        m, reinterpret_cast<float*>(base + L.table), reinterpret_cast<float4*>(base + L.partial), n_clear, status);
-    if (check_launch() != USP_OK) return USP_ERR_CUDA;
+    const int rc = launch_chained(rel_expand_kernel, dim3(p.Hq, per_head), kRelThreads, 0, 1, st, m,
+                                  reinterpret_cast<float*>(base + L.table),
+                                  reinterpret_cast<float4*>(base + L.partial), n_clear, status);
+    if (rc != USP_OK) return rc;
   }
   const bool exact_delta = dsinks != nullptr || m.partial != nullptr;  // a gradient in fp32 hangs on D
   if (!exact_delta)
@@ -557,8 +563,7 @@ int launch_attn_mod_bwd_preprocess(const usp_attn_params& p, const usp_score_mod
                       : run_delta<64>(a, mods, q, k, v, dO, lse, stats, st);
   });
   if (rc != USP_OK || dsinks == nullptr) return rc;
-  mod_dsink_kernel<<<a.Hq, kSinkThreads, 0, st>>>(stats, lse, dsinks, a, stats_row_pitch(a.BS));
-  return check_launch();
+  return launch_chained(mod_dsink_kernel, a.Hq, kSinkThreads, 0, 1, st, stats, lse, dsinks, a, stats_row_pitch(a.BS));
 }
 
 int launch_attn_mod_bwd_dkdv(const usp_attn_params& p, const usp_score_mods& sm, const void* q, const void* k,
@@ -598,11 +603,11 @@ int launch_attn_mod_bwd_rel_bias(const usp_attn_params& p, const usp_score_mods&
   const int row = 2 * sm.max_distance + 1, per = (L.n_rows + L.splits - 1) / L.splits;
   float* sums = reinterpret_cast<float*>(base + L.sums);
   const int threads = row < 1024 ? (row + 31) / 32 * 32 : 1024;
-  rel_sum_kernel<<<dim3(p.Hq, L.splits), threads, 0, st>>>(reinterpret_cast<const float*>(base + L.partial), sums,
-                                                               L.n_rows, per, row);
-  if (check_launch() != USP_OK) return USP_ERR_CUDA;
-  rel_bucket_kernel<<<p.Hq, kRelThreads, row * (sizeof(float) + sizeof(int)), st>>>(make_mods(p, sm), sums, drel_bias, L.splits);
-  return check_launch();
+  const int rc = launch_chained(rel_sum_kernel, dim3(p.Hq, L.splits), threads, 0, 1, st,
+                                reinterpret_cast<const float*>(base + L.partial), sums, L.n_rows, per, row);
+  if (rc != USP_OK) return rc;
+  return launch_chained(rel_bucket_kernel, p.Hq, kRelThreads, row * static_cast<int>(sizeof(float) + sizeof(int)), 1,
+                        st, make_mods(p, sm), sums, drel_bias, L.splits);
 }
 
 }  // namespace usp

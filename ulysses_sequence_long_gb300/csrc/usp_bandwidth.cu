@@ -85,6 +85,7 @@ __device__ __forceinline__ void relayout_body(const int4* __restrict__ src, int4
 template <bool kToHead>
 __global__ void __launch_bounds__(kRelayoutThreads) relayout_kernel(const int4* __restrict__ src,
                                                                     int4* __restrict__ dst, RelayoutGeom g) {
+  grid_wait();
   relayout_body<kToHead>(src, dst, g, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
 }
 
@@ -94,6 +95,7 @@ __global__ void __launch_bounds__(kRelayoutThreads) relayout_kernel(const int4* 
 __global__ void __launch_bounds__(kRelayoutThreads) relayout_reduce_kernel(const int4* __restrict__ src,
                                                                            int4* __restrict__ dst, RelayoutGeom g) {
   const uint32_t stride = gridDim.x * blockDim.x;
+  grid_wait();
   for (uint32_t v = blockIdx.x * blockDim.x + threadIdx.x; v < g.n_vec; v += stride) {
     const uint32_t run = g.run_vec.div(v);
     const uint32_t k = v - run * g.run_vec.d;
@@ -126,6 +128,7 @@ struct Relayout3 {
 };
 
 __global__ void __launch_bounds__(kRelayoutThreads) relayout_qkv_kernel(Relayout3 a) {
+  grid_wait();
   int t = blockIdx.x < a.block_end[0] ? 0 : (blockIdx.x < a.block_end[1] ? 1 : 2);
   uint32_t b0 = t == 0 ? 0 : a.block_end[t - 1];
   uint32_t nb = a.block_end[t] - b0;
@@ -172,12 +175,10 @@ int launch_relayout(const void* src, void* dst, int B, int S, int H, int D, int 
   if (g.n_vec == 0) return USP_OK;
   int grid = relayout_grid(g.n_vec);
   if (!to_head && g.rep_u > 1)
-    relayout_reduce_kernel<<<grid, kRelayoutThreads, 0, st>>>(static_cast<const int4*>(src), static_cast<int4*>(dst), g);
-  else if (to_head)
-    relayout_kernel<true><<<grid, kRelayoutThreads, 0, st>>>(static_cast<const int4*>(src), static_cast<int4*>(dst), g);
-  else
-    relayout_kernel<false><<<grid, kRelayoutThreads, 0, st>>>(static_cast<const int4*>(src), static_cast<int4*>(dst), g);
-  return check_launch();
+    return launch_chained(relayout_reduce_kernel, grid, kRelayoutThreads, 0, 1, st, static_cast<const int4*>(src),
+                          static_cast<int4*>(dst), g);
+  return launch_chained(to_head ? relayout_kernel<true> : relayout_kernel<false>, grid, kRelayoutThreads, 0, 1, st,
+                        static_cast<const int4*>(src), static_cast<int4*>(dst), g);
 }
 
 int launch_relayout_qkv(const void* const src[3], void* const dst[3], const int H[3], int B, int S, int D, int Ps,
@@ -200,8 +201,7 @@ int launch_relayout_qkv(const void* const src[3], void* const dst[3], const int 
     acc += nb;
     a.block_end[t] = acc;
   }
-  relayout_qkv_kernel<<<acc, kRelayoutThreads, 0, st>>>(a);
-  return check_launch();
+  return launch_chained(relayout_qkv_kernel, acc, kRelayoutThreads, 0, 1, st, a);
 }
 
 // ============================================================== cu_seqlens
@@ -389,6 +389,7 @@ __device__ __forceinline__ uint32_t warp_flags(const int32_t* __restrict__ pos, 
 }
 
 __global__ void scan_init_kernel(ScanWs ws, int nblk, int32_t* max_len) {
+  grid_wait();
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < nblk; i += gridDim.x * blockDim.x) ws.state[i] = 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *ws.ticket = 0;
@@ -451,6 +452,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const int32_t* __
   __shared__ int sh_bid, sh_pre_cnt, sh_pre_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool single = g.nblk == 1;
+  grid_wait();
   if (tid == 0) {
     sh_bid = single ? 0 : static_cast<int>(atomicAdd(ws.ticket, 1u));
     if (single) *max_len = 0;  // (the reset kernel does this when there are several blocks)
@@ -594,9 +596,9 @@ int launch_cu_seqlens(const int32_t* pos, int B, int S, int P, int32_t* cu, int3
           cudaSuccess)
     return USP_ERR_CUDA;
   // (one block needs no ticket and no block states: no reset kernel)
-  if (g.nblk > 1) scan_init_kernel<<<1, 256, 0, st>>>(w, g.nblk, max_len);
-  scan_kernel<<<g.nblk, kScanThreads, smem, st>>>(pos, g, w, cu, n_docs, max_len, status);
-  return check_launch();
+  if (g.nblk > 1 && launch_chained(scan_init_kernel, 1, 256, 0, 1, st, w, g.nblk, max_len) != USP_OK) return USP_ERR_CUDA;
+  return launch_chained(scan_kernel, g.nblk, kScanThreads, static_cast<int>(smem), 1, st, pos, g, w, cu, n_docs, max_len,
+                        status);
 }
 
 }  // namespace usp

@@ -16,6 +16,31 @@ int device_sm_count();
 // Records a CUDA error of the last launch as USP_ERR_CUDA.
 int check_launch();
 
+// A launch that is set up while the kernel before it in the stream ends (programmatic
+// dependent launch: the kernel calls grid_wait first), in clusters of `cluster` CTAs.
+// It hides a launch's 1.5 to 2 us when a stream runs kernel by kernel: a training step of
+// 256 tokens 77 -> 60 us, of 4096 tokens 296 -> 285.  Letting the next kernel start before
+// this one's last CTAs have ended was slower: its CTAs crowd onto the SMs that come free
+// first (8192 tokens: 720 -> 754 us).
+template <class... KA, class... A>
+inline int launch_chained(void (*kern)(KA...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st,
+                          A&&... args) {
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, kern, static_cast<A&&>(args)...);
+  return check_launch();
+}
+
 // Exact unsigned 32-bit division by a runtime constant (multiply-high and
 // shift, Granlund & Montgomery 1994, "Division by invariant integers using
 // multiplication", round-up variant).

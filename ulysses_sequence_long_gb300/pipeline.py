@@ -40,9 +40,12 @@ import torch
 from . import binding as B_
 
 
-# Layers with modified scores: up to this many tokens the forward reads k and v from their shards (see
-# UlyssesAttention).  
-KV_IN_PLACE_TOKENS = 2048
+# Layers with modified scores: up to this many tokens the forward reads k and v from their shards instead of
+# moving them to head layout first.  Two launches fewer, but the rows of a key tile lie a whole token's
+# key/value heads apart and are read again by every query tile.  Forward on 8 ranks, microseconds in place /
+# moved: 32 heads over 8, D 128: 31.3 / 34.9 at 1024 tokens, 55.4 / 59.4 at 2048, 157.9 / 158.2 at 4096,
+# 508 / 506 at 8192, 1838 / 1806 at 16384; 64 heads over 8, D 64: 248 / 256 at 4096.
+KV_IN_PLACE_TOKENS = 4096
 
 
 @dataclass
@@ -219,8 +222,7 @@ class UlyssesAttention:
         if self._mods is not None:
             # One rank's shards are its head layout, byte for byte: nothing to exchange.
             self._one_rank = P == 1
-            # Few tokens: the forward reads k and v from the shards too.  Two launches fewer; the rows strided
-            # over all key/value heads cost a long sequence, which re-reads every tile many times, 12%.
+            # Few tokens: the forward reads k and v from the shards too.
             self._kv_in_place = self.fused and Bb * S <= KV_IN_PLACE_TOKENS
             self._own = {n: B_.Buffer(t, n) for n, t in vars(self).items() if isinstance(t, torch.Tensor)}
             self._prm = {}
