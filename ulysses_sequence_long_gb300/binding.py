@@ -68,13 +68,15 @@ class AttnParams(ctypes.Structure):
 
 
 class ScoreModsStruct(ctypes.Structure):
-    """usp_score_mods (include/usp.h).  ``tensors`` keeps what its pointers point at."""
+    """usp_score_mods (include/usp.h).  ``tensors`` keeps what its pointers point at, all on ``device`` (None when
+    there is no tensor)."""
     _fields_ = [
         ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("rel_bias", ctypes.c_void_p),
         ("buckets", ctypes.c_void_p), ("n_buckets", ctypes.c_int), ("max_distance", ctypes.c_int),
         ("rel_bias_grad", ctypes.c_int), ("prefix_lens", ctypes.c_void_p), ("n_prefix", ctypes.c_int),
     ]
     tensors = ()
+    device = None
 
 
 USP_IO_HEAD = 0
@@ -160,15 +162,17 @@ def _check(rc: int, where: str) -> None:
 class Buffer:
     """A tensor that was checked once and whose owner keeps it: the calls take it for the tensor and do not look
     at it again (a layer's own buffers, at every step of a model)."""
-    __slots__ = ("tensor", "ptr", "nbytes")
+    __slots__ = ("tensor", "ptr")
 
     def __init__(self, tensor: torch.Tensor, name: str = "buffer", dtype=None):
         self.ptr = _dev(tensor, name, dtype)
-        self.tensor, self.nbytes = tensor, tensor.numel() * tensor.element_size()
+        self.tensor = tensor
 
 
 def _nbytes(t) -> int:
-    return t.nbytes if type(t) is Buffer else t.numel() * t.element_size()
+    if type(t) is Buffer:
+        t = t.tensor
+    return t.numel() * t.element_size()
 
 
 def _dev(t: Optional[torch.Tensor], name: str, dtype=None):
@@ -378,6 +382,11 @@ def score_mods(Hq, softcap=0.0, slopes=None, rel_bias=None, buckets=None, rel_bi
                         0 if buckets is None else (buckets.numel() - 1) // 2, 1 if rel_bias_grad else 0, pl,
                         0 if prefix_lens is None else prefix_lens.numel())
     m.tensors = tuple(t for t in (slopes, rel_bias, buckets, prefix_lens) if t is not None)
+    for t in m.tensors:
+        if m.device is None:
+            m.device = t.device
+        elif t.device != m.device:
+            raise ValueError(f"the tensors of the score modifications are on {m.device} and {t.device}")
     return m
 
 
@@ -393,17 +402,10 @@ def _mod_sizes(prm: AttnParams, mods: ScoreModsStruct) -> dict:
 class _Call:
     """The tensors of one call: their sizes against the parameters, one device, that device's stream."""
 
-    def __init__(self, prm: AttnParams, mods: ScoreModsStruct, stream):
-        self.prm, self.mods, self.stream, self.device = prm, mods, stream, None
-        self.sizes = _mod_sizes(prm, mods)
-        for t in mods.tensors:
-            self._on(t, "mods")
+    __slots__ = ("prm", "mods", "stream", "device", "sizes")
 
-    def _on(self, t, name):
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, other tensors of the call on {self.device}")
+    def __init__(self, prm: AttnParams, mods: ScoreModsStruct, stream):
+        self.prm, self.mods, self.stream, self.device, self.sizes = prm, mods, stream, mods.device, None
 
     def __call__(self, t, name, dtype, size):
         if t is None:
@@ -413,9 +415,15 @@ class _Call:
                 self.device = t.tensor.device
             return t.ptr
         ptr = _dev(t, name, dtype)
-        self._on(t, name)
-        if size is not None and t.numel() != self.sizes[size]:
-            raise ValueError(f"{name} has {t.numel()} elements, the parameters need {self.sizes[size]}")
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, other tensors of the call on {self.device}")
+        if size is not None:
+            if self.sizes is None:
+                self.sizes = _mod_sizes(self.prm, self.mods)
+            if t.numel() != self.sizes[size]:
+                raise ValueError(f"{name} has {t.numel()} elements, the parameters need {self.sizes[size]}")
         return ptr
 
     def run(self, where, *args):

@@ -380,7 +380,13 @@ int run_delta(const AttnArgs& a, const M& m, const void* q, const void* k, const
 constexpr int kRelThreads = 256;
 constexpr int kRelRows = 32;    // partial rows that one block of the first reduction sums
 constexpr int kRelSplits = 64;  // most blocks per head
+constexpr int kRelDirect = 96;  // rows that the second reduction takes by itself: 32 rows of 257 in 4.7 us, 8.5 with the
+                                // first before it (8192 tokens: 16 us both; blocks that join by a ticket: 26)
 constexpr int kRelAhead = 16;   // rows whose loads a thread has in flight
+
+// Threads of a block for each distance of a row, and how many such teams 1024 hold.
+__host__ __device__ constexpr int rel_width(int row) { return row < 1024 ? (row + 31) / 32 * 32 : 1024; }
+__host__ __device__ constexpr int rel_teams(int row) { return 1024 / rel_width(row); }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -394,7 +400,7 @@ Layout mod_layout(const usp_attn_params& p, const usp_score_mods& m) {
   L.table = L.partial = L.sums = attn_bwd_ws_bytes(p);
   L.n_kb = (p.B * p.S + 31) / 32;
   L.n_rows = kModGroups * L.n_kb;
-  L.splits = (L.n_rows + kRelRows - 1) / kRelRows;
+  L.splits = L.n_rows <= kRelDirect ? 1 : (L.n_rows + kRelRows - 1) / kRelRows;
   if (L.splits > kRelSplits) L.splits = kRelSplits;
   size_t end = L.table;
   if (m.rel_bias != nullptr) {
@@ -402,7 +408,7 @@ Layout mod_layout(const usp_attn_params& p, const usp_score_mods& m) {
     end = L.partial = end + up256(sizeof(float) * p.Hq * tab_len(m.max_distance));
     if (m.rel_bias_grad) {
       end = L.sums = end + up256(sizeof(float) * p.Hq * static_cast<size_t>(L.n_rows) * row);
-      end += up256(sizeof(float) * p.Hq * static_cast<size_t>(L.splits) * row);
+      if (L.splits > 1) end += up256(sizeof(float) * p.Hq * static_cast<size_t>(L.splits) * row);
     }
   }
   L.ds = L.total = end;
@@ -434,50 +440,56 @@ __global__ void __launch_bounds__(kRelThreads)
     clear[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-// Sums a split's partial rows of a head: thread = distance, kRelAhead rows in
-// flight, joined in a fixed order.
-__global__ void __launch_bounds__(1024)
-    rel_sum_kernel(const float* __restrict__ partial, float* __restrict__ sums, int n_rows, int per, int row) {
-  const int h = blockIdx.x, s = blockIdx.y;
-  grid_wait();
-  const int r0 = s * per, r1 = min(n_rows, r0 + per);
-  const float* src = partial + static_cast<size_t>(h) * n_rows * row;
-  for (int c = threadIdx.x; c < row; c += blockDim.x) {
-    float acc[kRelAhead] = {};
-    for (int r = r0; r < r1; r += kRelAhead)
+// One column of rows [r0, r1), kRelAhead of them in flight (the last again past the
+// end: a load behind a branch would wait for the one before), joined in a fixed order.
+__device__ __forceinline__ float rel_column(const float* __restrict__ src, int r0, int r1, int step, int row) {
+  float acc = 0.f;
+  for (int r = r0; r < r1; r += step) {
+    float x[kRelAhead];
 #pragma unroll
-      for (int e = 0; e < kRelAhead; ++e)
-        if (r + e < r1) acc[e] += __ldg(src + static_cast<size_t>(r + e) * row + c);
+    for (int e = 0; e < kRelAhead; ++e) x[e] = __ldg(src + static_cast<size_t>(min(r + e, r1 - 1)) * row);
+#pragma unroll
+    for (int e = 0; e < kRelAhead; ++e) x[e] = r + e < r1 ? x[e] : 0.f;
 #pragma unroll
     for (int o = kRelAhead / 2; o > 0; o >>= 1)
 #pragma unroll
-      for (int e = 0; e < o; ++e) acc[e] += acc[e + o];
-    sums[(static_cast<size_t>(h) * gridDim.y + s) * row + c] = acc[0];
+      for (int e = 0; e < o; ++e) x[e] += x[e + o];
+    acc += x[0];
   }
+  return acc;
 }
 
-// The splits' sums of a head, then its buckets: a warp takes a bucket at a time,
-// its lanes the distances, joined by a fixed tree (no atomics: the result does
-// not depend on the schedule).
-__global__ void __launch_bounds__(kRelThreads)
-    rel_bucket_kernel(ModArgs m, const float* __restrict__ sums, float* __restrict__ drel, int splits) {
-  extern __shared__ float by_dist[];
-  const int h = blockIdx.x, row = 2 * m.R + 1, lane = threadIdx.x & 31;
-  int* bucket = reinterpret_cast<int*>(by_dist + row);
-  const float* src = sums + static_cast<size_t>(h) * splits * row;
+// Many rows: a split's partial rows of a head become one, thread = distance.
+__global__ void __launch_bounds__(1024, 1)
+    rel_sum_kernel(const float* __restrict__ partial, float* __restrict__ sums, int n_rows, int per, int row) {
+  const int h = blockIdx.x, s = blockIdx.y;
   grid_wait();
-  for (int c = threadIdx.x; c < row; c += kRelThreads) {
-    float acc = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) acc += __ldg(src + static_cast<size_t>(s) * row + c);
-    by_dist[c] = acc;
-    bucket[c] = min(max(__ldg(m.buckets + c), 0), m.n_buckets - 1);
-  }
+  const float* src = partial + static_cast<size_t>(h) * n_rows * row;
+  for (int c = threadIdx.x; c < row; c += blockDim.x)
+    sums[(static_cast<size_t>(h) * gridDim.y + s) * row + c] =
+        rel_column(src + c, s * per, min(n_rows, (s + 1) * per), kRelAhead, row);
+}
+
+// A head's rows, teams of threads in turn over them, then its buckets: a warp takes a
+// bucket at a time, its lanes the distances, joined by a fixed tree (no atomics: the
+// result does not depend on the schedule).
+__global__ void __launch_bounds__(1024, 1)
+    rel_grad_kernel(ModArgs m, const float* __restrict__ rows, float* __restrict__ drel, int n_rows, int row) {
+  extern __shared__ float by_dist[];  // [teams][row]
+  const int teams = rel_teams(row), width = blockDim.x / teams, team = threadIdx.x / width;
+  int* bucket = reinterpret_cast<int*>(by_dist + teams * row);
+  const int h = blockIdx.x, lane = threadIdx.x & 31;
+  grid_wait();
+  const float* src = rows + static_cast<size_t>(h) * n_rows * row;
+  for (int c = threadIdx.x - team * width; c < row; c += width)
+    by_dist[team * row + c] = rel_column(src + c, team * kRelAhead, n_rows, teams * kRelAhead, row);
+  for (int c = threadIdx.x; c < row; c += blockDim.x) bucket[c] = min(max(__ldg(m.buckets + c), 0), m.n_buckets - 1);
   __syncthreads();
-  for (int b = threadIdx.x >> 5; b < m.n_buckets; b += kRelThreads / 32) {
+  for (int b = threadIdx.x >> 5; b < m.n_buckets; b += blockDim.x / 32) {
     float acc = 0.f;
     for (int c = lane; c < row; c += 32)
-      if (bucket[c] == b) acc += by_dist[c];
+      if (bucket[c] == b)
+        for (int e = 0; e < teams; ++e) acc += by_dist[e * row + c];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
     if (lane == 0) drel[static_cast<size_t>(h) * m.n_buckets + b] = acc;
@@ -600,14 +612,20 @@ int launch_attn_mod_bwd_rel_bias(const usp_attn_params& p, const usp_score_mods&
                                  cudaStream_t st) {
   const Layout L = mod_layout(p, sm);
   uint8_t* base = static_cast<uint8_t*>(ws);
-  const int row = 2 * sm.max_distance + 1, per = (L.n_rows + L.splits - 1) / L.splits;
-  float* sums = reinterpret_cast<float*>(base + L.sums);
-  const int threads = row < 1024 ? (row + 31) / 32 * 32 : 1024;
-  const int rc = launch_chained(rel_sum_kernel, dim3(p.Hq, L.splits), threads, 0, 1, st,
-                                reinterpret_cast<const float*>(base + L.partial), sums, L.n_rows, per, row);
-  if (rc != USP_OK) return rc;
-  return launch_chained(rel_bucket_kernel, p.Hq, kRelThreads, row * static_cast<int>(sizeof(float) + sizeof(int)), 1,
-                        st, make_mods(p, sm), sums, drel_bias, L.splits);
+  const int row = 2 * sm.max_distance + 1, width = rel_width(row), teams = rel_teams(row);
+  const float* rows = reinterpret_cast<const float*>(base + L.partial);
+  int n_rows = L.n_rows;
+  if (L.splits > 1) {
+    float* sums = reinterpret_cast<float*>(base + L.sums);
+    const int per = (L.n_rows + L.splits - 1) / L.splits;
+    const int rc = launch_chained(rel_sum_kernel, dim3(p.Hq, L.splits), width, 0, 1, st, rows, sums, n_rows, per, row);
+    if (rc != USP_OK) return rc;
+    rows = sums;
+    n_rows = L.splits;
+  }
+  const int smem = row * (teams * static_cast<int>(sizeof(float)) + static_cast<int>(sizeof(int)));
+  return launch_chained(rel_grad_kernel, p.Hq, teams * width, smem, 1, st, make_mods(p, sm), rows, drel_bias, n_rows,
+                        row);
 }
 
 }  // namespace usp

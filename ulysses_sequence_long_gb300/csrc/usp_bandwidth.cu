@@ -225,9 +225,9 @@ int launch_relayout_qkv(const void* const src[3], void* const dst[3], const int 
 //      and it writes its starts into cu_seqlens.  A document's length is
 //      taken where it ends (the next start, or B*S after the last start).
 // Flags beyond the shared-memory budget (ranges longer than kScanSmemWords *
-// 32 positions) are recomputed from the positions in step 3.  With several
-// blocks a small kernel before it resets the block states; a sequence of at
-// most one block's range (every workload here) takes the one launch alone.
+// 32 positions) are recomputed from the positions in step 3.  A small kernel
+// before it resets the block states.  A sequence of at most one block's range
+// takes the one launch of scan_small_kernel instead.
 constexpr int kScanThreads = 1024;
 constexpr int kScanItems = 32;                                 // positions per thread and step: one flag word
 constexpr int kScanStep = kScanThreads * kScanItems;           // positions per block and step
@@ -236,7 +236,7 @@ static_assert(kScanChunk % kScanStep == 0, "ranges are whole steps");
 
 struct ScanGeom {
   int B, S, P, Sl, total;
-  int nblk;   // blocks in the grid (1: no ticket, no block states, no reset kernel)
+  int nblk;   // blocks in the grid
   int range;  // positions per block (a multiple of kScanStep)
   int vec;    // 1: each thread's 32 positions are one aligned, contiguous run
 };
@@ -451,12 +451,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const int32_t* __
   __shared__ int sh[72];
   __shared__ int sh_bid, sh_pre_cnt, sh_pre_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool single = g.nblk == 1;
   grid_wait();
-  if (tid == 0) {
-    sh_bid = single ? 0 : static_cast<int>(atomicAdd(ws.ticket, 1u));
-    if (single) *max_len = 0;  // (the reset kernel does this when there are several blocks)
-  }
+  if (tid == 0) sh_bid = static_cast<int>(atomicAdd(ws.ticket, 1u));
   __syncthreads();
   const int bid = sh_bid;
   const int lo = bid * g.range;                                  // first position of this block's range
@@ -489,15 +485,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const int32_t* __
   if (neg) set_status(status, USP_ERR_BAD_POSITIONS);
   int ex_c, ex_l, b_cnt, b_last;
   block_scan2(cnt, last, ex_c, ex_l, b_cnt, b_last, sh);
-  if (tid == 0 && !single) st_state(ws.state + bid, scan_state(1, b_cnt, b_last));
+  if (tid == 0) st_state(ws.state + bid, scan_state(1, b_cnt, b_last));
 
   // 2. prefix: the aggregates of every block before this one
-  if (warp == 0 && single) {
-    if (lane == 0) {
-      sh_pre_cnt = 0;
-      sh_pre_last = -1;
-    }
-  } else if (warp == 0) {
+  if (warp == 0) {
     int pre_cnt = 0, pre_last = -1;
     const uint64_t t0 = global_ns();
     for (int j0 = 0; j0 < bid; j0 += 32) {
@@ -569,12 +560,101 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const int32_t* __
   if (lane == 0 && local_max) atomicMax(max_len, local_max);
 }
 
+// A sequence of at most kScanChunk positions: one block, a word of 32 flags by a
+// ballot of 32 lanes' positions (kSmallAhead words' loads in flight per warp), then
+// a thread per word.  A call is one chain of latencies: few barriers, and little
+// code, which a kernel this short reads for the first time as it runs it
+// (256 tokens: 2.6 us, 7.0 by scan_kernel's one block; 3 rows of 1000 on 8 ranks: 2.7 and
+// 10.4; 8192 tokens: 4.2 and 8.4).
+constexpr int kSmallAhead = 8;
+__global__ void __launch_bounds__(kScanThreads, 1)
+    scan_small_kernel(const int32_t* __restrict__ pos, int total, int B, int P, FastDiv S, FastDiv Sl,
+                      int32_t* __restrict__ cu, int32_t* n_docs, int32_t* max_len, int32_t* status) {
+  __shared__ uint32_t words[kScanThreads];
+  __shared__ int sh_cnt[32], sh_last[32], sh_max[32];
+  constexpr uint32_t kAll = 0xffffffffu;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int n_words = (total + 31) / 32;  // <= blockDim.x
+  const bool gathered = P == 1 || B == 1;  // the shards already sit in gathered order
+  grid_wait();
+  bool negative = false;
+  for (int w0 = warp * kSmallAhead; w0 < n_words; w0 += warps * kSmallAhead) {
+    int v[kSmallAhead], s[kSmallAhead];
+#pragma unroll
+    for (int e = 0; e < kSmallAhead; ++e) {
+      const uint32_t gi = (w0 + e) * 32 + lane, b = S.div(gi);
+      s[e] = gi - b * S.d;
+      v[e] = 1;
+      if (gi < total) {
+        const uint32_t r = Sl.div(s[e]);
+        v[e] = __ldg(pos + (gathered ? gi : (r * B + b) * Sl.d + (s[e] - r * Sl.d)));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kSmallAhead; ++e) {
+      const bool in = (w0 + e) * 32 + lane < total;
+      negative |= v[e] < 0;
+      const uint32_t word = __ballot_sync(kAll, in && (v[e] == 0 || s[e] == 0));
+      if (lane == e && w0 + e < n_words) words[w0 + e] = word;
+    }
+  }
+  if (negative) set_status(status, USP_ERR_BAD_POSITIONS);
+  __syncthreads();
+
+  uint32_t w = tid < n_words ? words[tid] : 0u;
+  int cnt = __popc(w), last = w ? tid * 32 + 31 - __clz(w) : -1;
+  const int own = cnt;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int c = __shfl_up_sync(kAll, cnt, o), l = __shfl_up_sync(kAll, last, o);
+    if (lane >= o) {
+      cnt += c;
+      last = max(last, l);
+    }
+  }
+  if (lane == 31) {
+    sh_cnt[warp] = cnt;
+    sh_last[warp] = last;
+  }
+  __syncthreads();
+  const int before_c = lane < warp ? sh_cnt[lane] : 0, before_l = lane < warp ? sh_last[lane] : -1;
+  int off = __reduce_add_sync(kAll, before_c) + cnt - own;
+  const int up = __shfl_up_sync(kAll, last, 1);
+  int prev = max(__reduce_max_sync(kAll, before_l), lane > 0 ? up : -1);
+  int longest = 0;
+  while (w) {
+    const int gi = tid * 32 + __ffs(w) - 1;
+    w &= w - 1;
+    cu[off++] = gi;
+    if (prev >= 0) longest = max(longest, gi - prev);
+    prev = gi;
+  }
+  if (tid == static_cast<int>(blockDim.x) - 1) {  // every start lies in its words or before: the last document ends at B*S
+    *n_docs = off;
+    cu[off] = total;
+    longest = max(longest, total - prev);
+  }
+  longest = __reduce_max_sync(kAll, longest);
+  if (lane == 0) sh_max[warp] = longest;
+  __syncthreads();
+  if (warp == 0) {
+    longest = __reduce_max_sync(kAll, lane < warps ? sh_max[lane] : 0);
+    if (lane == 0) *max_len = longest;
+  }
+}
+
 size_t cu_seqlens_ws_bytes(int B, int S) {
   return cu_seqlens_ws_bytes_for(static_cast<long long>(B) * S);
 }
 
 int launch_cu_seqlens(const int32_t* pos, int B, int S, int P, int32_t* cu, int32_t* n_docs, int32_t* max_len,
                       int32_t* ws, int32_t* status, cudaStream_t st) {
+  if (static_cast<long long>(B) * S <= kScanChunk) {
+    // a thread per word, and a warp for every kSmallAhead words
+    const int threads = std::min(kScanThreads, std::max(32, (B * S / kSmallAhead + 31) / 32 * 32));
+    return launch_chained(scan_small_kernel, 1, threads, 0, 1, st, pos, B * S, B, P, FastDiv(S), FastDiv(S / P), cu,
+                          n_docs, max_len, status);
+  }
   ScanGeom g{B, S, P, S / P, B * S, 0, 0, 0};
   // as many blocks as SMs (at most one per kScanChunk positions, the
   // workspace's state count); each block's range a whole number of steps
@@ -595,8 +675,7 @@ int launch_cu_seqlens(const int32_t* pos, int B, int S, int P, int32_t* cu, int3
       cudaFuncSetAttribute(scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
           cudaSuccess)
     return USP_ERR_CUDA;
-  // (one block needs no ticket and no block states: no reset kernel)
-  if (g.nblk > 1 && launch_chained(scan_init_kernel, 1, 256, 0, 1, st, w, g.nblk, max_len) != USP_OK) return USP_ERR_CUDA;
+  if (launch_chained(scan_init_kernel, 1, 256, 0, 1, st, w, g.nblk, max_len) != USP_OK) return USP_ERR_CUDA;
   return launch_chained(scan_kernel, g.nblk, kScanThreads, static_cast<int>(smem), 1, st, pos, g, w, cu, n_docs, max_len,
                         status);
 }

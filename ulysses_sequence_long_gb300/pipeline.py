@@ -220,6 +220,8 @@ class UlyssesAttention:
         self.ds_groups = [(0, 0)]
         self._inputs = None  # the forward's q/k/v as the attention kernels read them
         if self._mods is not None:
+            if self._mods.device not in (None, self.lse.device):
+                raise ValueError(f"the score modifications are on {self._mods.device}, the layer on {self.lse.device}")
             # One rank's shards are its head layout, byte for byte: nothing to exchange.
             self._one_rank = P == 1
             # Few tokens: the forward reads k and v from the shards too.
@@ -237,9 +239,10 @@ class UlyssesAttention:
                 prm = self._prm[io, group] = B_.attn_params(
                     s.B, s.S, s.Hq, s.Hkv, s.D, s.P, self.cu_seqlens, self.n_docs, s.causal, s.window_left,
                     s.softmax_scale, None, io, head_first=group[0], head_count=group[1])
-            if sinks is not None and sinks.numel() != s.Hq:
-                raise ValueError(f"sinks must hold one logit per query head ({s.Hq}), got {sinks.numel()}")
             prm.sinks = B_._dev(sinks, "sinks", torch.float32)
+            if sinks is not None and (sinks.numel() != s.Hq or sinks.device != self.lse.device):
+                raise ValueError(f"sinks must hold one logit per query head ({s.Hq}) on {self.lse.device}, "
+                                 f"got {sinks.numel()} on {sinks.device}")
             return prm
         if io is None:
             io = B_.USP_IO_SEQ if self.fused else B_.USP_IO_HEAD
@@ -258,29 +261,30 @@ class UlyssesAttention:
     def _handle(self, stream):
         """The CUDA stream of a whole pass, looked up once."""
         if stream is None:
-            stream = torch.cuda.current_stream(self.lse.device)
+            return torch._C._cuda_getCurrentRawStream(self.lse.device.index)
         return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
-    def _check_shards(self, t, name, H):
+    def _shards(self, t, name, H):
         s = self.shape
-        B_._dev(t, name, torch.bfloat16)
+        shards = B_.Buffer(t, name, torch.bfloat16)
         if t.numel() != s.B * s.S * H * s.D or t.device != self.lse.device:
             raise ValueError(f"{name} must be the shards [{s.P}][{s.B}][{s.S // s.P}][{H}][{s.D}] on {self.lse.device}")
+        return shards
 
     # -- steps ---------------------------------------------------------------
     def exchange_qkv(self, q_seq, k_seq, v_seq, stream=None):
         s = self.shape
         if self._mods is not None:
-            for t, name, H in ((q_seq, "q", s.Hq), (k_seq, "k", s.Hkv), (v_seq, "v", s.Hkv)):
-                self._check_shards(t, name, H)
+            self._inputs = (self._shards(q_seq, "q", s.Hq), self._shards(k_seq, "k", s.Hkv),
+                            self._shards(v_seq, "v", s.Hkv))
             if self._one_rank or self._kv_in_place:
-                self._inputs = (q_seq, k_seq, v_seq)
                 return
         if self.fused:
             # q stays in its shards; k and v go to head layout for the forward
             B_.usp_relayout_fwd(k_seq, self.k_head, s.B, s.S, s.Hkv, s.D, s.P, stream)
             B_.usp_relayout_fwd(v_seq, self.v_head, s.B, s.S, s.Hkv, s.D, s.P, stream)
-            self._inputs = (q_seq, k_seq, v_seq)
+            if self._mods is None:
+                self._inputs = (q_seq, k_seq, v_seq)
             return
         B_.usp_relayout_fwd_qkv(q_seq, k_seq, v_seq, self.q_head, self.k_head, self.v_head,
                                 s.B, s.S, s.Hq, s.Hkv, s.D, s.P, stream)
@@ -289,8 +293,9 @@ class UlyssesAttention:
     def boundaries(self, pos_shards, stream=None):
         s = self.shape
         if self._mods is not None:
-            if pos_shards.numel() != s.B * s.S:
-                raise ValueError(f"position ids must cover {s.B} x {s.S} tokens, got {pos_shards.numel()}")
+            if pos_shards.numel() != s.B * s.S or pos_shards.device != self.lse.device:
+                raise ValueError(f"position ids must cover {s.B} x {s.S} tokens on {self.lse.device}, "
+                                 f"got {pos_shards.numel()} on {pos_shards.device}")
             o = self._own
             B_.usp_cu_seqlens_from_position_ids(pos_shards, s.B, s.S, s.P, o["cu_seqlens"], o["n_docs"], o["max_len"],
                                                 o["scan_ws"], o["status"], stream)
@@ -328,6 +333,9 @@ class UlyssesAttention:
     def forward(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None):
         """Sequence shards in, sequence shards out (``self.o_seq``)."""
         if self._mods is not None:
+            if torch.cuda.current_device() != self.lse.device.index:
+                with torch.cuda.device(self.lse.device):
+                    return self.forward(q_seq, k_seq, v_seq, pos_shards, sinks, stream)
             stream = self._handle(stream)
         self.exchange_qkv(q_seq, k_seq, v_seq, stream)
         self.boundaries(pos_shards, stream)
@@ -395,9 +403,8 @@ class UlyssesAttention:
         lse, status = own["lse"], own["status"]
         dsinks = own["dsinks"] if sinks is not None else None
         drel = own["drel_bias"] if mods.rel_bias_grad else None
-        self._check_shards(do_seq, "do", s.Hq)
+        do = self._shards(do_seq, "do", s.Hq)
         mark(0)
-        do = do_seq
         if not in_place:
             B_.usp_relayout_fwd(do_seq, self.do_head, s.B, s.S, s.Hq, s.D, s.P, stream)
             do = own["do_head"]
@@ -432,6 +439,10 @@ class UlyssesAttention:
         """dO shards in; dQ/dK/dV shards out (``self.dq_seq`` ...), dsinks.
         In explicit mode this is the single ``usp_attn_bwd`` (or
         ``usp_attn_mod_bwd``) call."""
+        if self._mods is not None:
+            if torch.cuda.current_device() != self.lse.device.index:
+                with torch.cuda.device(self.lse.device):
+                    return self.backward_phases(do_seq, sinks, stream)
         if self.fused or self._mods is not None:
             return self.backward_phases(do_seq, sinks, stream)
         s = self.shape
