@@ -399,11 +399,13 @@ int usp_attn_bwd_dq(const usp_attn_params* params, const void* q, const void* k,
  * (t - u <= window_left still holds with a window).
  * ---------------------------------------------------------------------- */
 typedef struct {
-  float softcap;               /* 0: none; else 2^-10 .. 2^10.  The absolute error of z is about
-                                  2.5e-7 softcap (fp32 tanh by one exponential and a reciprocal). */
-  const float* slopes;         /* device fp32 [Hq] (global heads), or NULL: no linear bias */
-  const float* rel_bias;       /* device fp32 [Hq][n_buckets], or NULL: no learned bias.  -inf hides keys
-                                  (only without a cap); a row that then sees nothing has O = 0, LSE = -inf */
+  float softcap;               /* 0: none; else 2^-10 .. 2^10.  The absolute error of z is under
+                                  2.5e-7 softcap and that of x. */
+  const float* slopes;         /* device fp32 [Hq] (global heads), or NULL: no linear bias.  |slope| <= 2^10; a
+                                  biased score is exact to fp32 at the size of 128 slopes */
+  const float* rel_bias;       /* device fp32 [Hq][n_buckets], or NULL: no learned bias.  At most 2^20; an entry
+                                  below -2^20 (-inf, the lowest fp32 value) hides its keys (only without a cap):
+                                  a row that then sees nothing has O = 0, LSE = -inf */
   const int32_t* buckets;      /* device int32 [2*max_distance + 1]: the bucket of distance t - u at index
                                   t - u + max_distance; farther distances take the ends' buckets */
   int n_buckets;               /* 1 .. 4097 */
@@ -427,7 +429,9 @@ int usp_rel_buckets_log(int n_buckets, int max_distance, int bidirectional, int3
 
 /* Forward.  q, k, v, o, lse, dev_status and params as usp_attn_fwd (every
  * io_layout; ring <= 1).
- * dev_status may also get USP_ERR_BAD_MODS (the outputs are then unspecified).
+ * dev_status may also get USP_ERR_BAD_MODS: a bucket id outside the table, a bias or
+ * a slope above its limit or NaN, a negative or missing prefix length (the outputs are
+ * then unspecified).
  * Every element of q, k and v must be finite, hidden keys' too: a tile's products
  * take all its keys, hidden ones with weight 0.
  * Errors: as usp_attn_fwd, and USP_ERR_INVALID_ARG (mods NULL, a softcap that is

@@ -96,7 +96,8 @@ def mod_attention(q, k, v, cu, causal=True, window_left=-1, scale=None, sinks=No
             if slopes is not None:
                 x = x - float(slopes[h]) * np.abs(dist)
             if rel_bias is not None:
-                x = x + np.asarray(rel_bias, dtype=np.float64)[h][bucket]
+                row = np.asarray(rel_bias, dtype=np.float64)[h]
+                x = x + np.where(row < -2.0 ** 20, -np.inf, row)[bucket]
             th = None
             if softcap:
                 th = np.tanh(x / softcap)

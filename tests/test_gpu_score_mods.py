@@ -316,6 +316,113 @@ def test_two_layers_together():
     _f32_close("dsinks", la.dsinks, ra2["dsinks"])
 
 
+def test_masks_of_the_lowest_value_hide_as_infinities_do():
+    """A table's entries far below any score: the same bits whatever their value, rows without a key among them."""
+    c = next(x for x in CASES if x.w.name == "rel_hides")
+    t, pos, kw = _inputs(c)
+    got = []
+    for low in (-np.inf, np.finfo(np.float32).min, -2.0 ** 20 - 1):
+        kx = dict(kw, rel_bias=np.where(np.isneginf(kw["rel_bias"]), low, kw["rel_bias"]))
+        ua = _layer(c, kx)
+        _run(c, ua, t, pos, kx)
+        got.append([x.clone() for x in (ua.o_seq, ua.lse, ua.dq_seq, ua.dk_seq, ua.dv_seq, ua.drel_bias)])
+    assert torch.isneginf(got[0][1]).any()
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n_buckets,R", [(1, 1), (3, 1), (4097, 2048), (5, 160)])
+@pytest.mark.parametrize("S,D", [(1, 64), (1, 128), (129, 128), (257, 64)])
+def test_any_bucket_map(n_buckets, R, S, D):
+    """Bucket maps without order, from one bucket to one for every distance, sequences from one token; with
+    slopes and a prefix of the whole sequence, so that every distance of both signs is met."""
+    rng = np.random.default_rng(R + S)
+    c = Case(_w("map", S=S, Hq=4, Hkv=2, D=D, P=1, sinks=True), slopes=True, rel=(2, 2), prefix=(S,))
+    t, pos, kw = _inputs(c)
+    kw["buckets"] = rng.integers(0, n_buckets, 2 * R + 1).astype(np.int32)
+    kw["rel_bias"] = rng.standard_normal((4, n_buckets)).astype(np.float32).astype(np.float64)
+    ua = _layer(c, kw)
+    _run(c, ua, t, pos, kw)
+    host = {n: W.bf16_to_f64(x) for n, x in t.items()}
+    ref = SM.mod_layer(host["q"], host["k"], host["v"], pos, host["do"], **kw)
+    for n, x in (("o", ua.o_seq), ("dq", ua.dq_seq), ("dk", ua.dk_seq), ("dv", ua.dv_seq)):
+        if S > 1 or n in ("o", "dv"):
+            assert_close(n, _np(x), ref[n])
+        else:
+            # one key and the sink: dX = P (1 - P) dO.v, and D from O's rounding has no part in it here (fp32 pass)
+            assert_close(n, _np(x), ref[n], slack=ref[n + "_slack"])
+    assert_close("lse", _np(ua.lse), ref["lse"], bf16_out=False)
+    _f32_close("dsinks", ua.dsinks, ref["dsinks"])
+    _f32_close("drel_bias", ua.drel_bias, ref["drel_bias"])
+    assert np.all(_np(ua.drel_bias)[ref["drel_bias"] == 0] == 0)
+
+
+@pytest.mark.parametrize("name", ["cap_window", "slope_window_sinks", "rel_many_ranks", "all"])
+def test_keys_and_values_moved_first(name):
+    """What a sequence beyond KV_IN_PLACE_TOKENS takes: k and v in head layout for the forward."""
+    c = next(x for x in CASES if x.w.name == name)
+    t, pos, kw = _inputs(c)
+    ua = _layer(c, kw, fused=True)
+    assert ua._kv_in_place
+    ua._kv_in_place = False
+    _run(c, ua, t, pos, kw)
+    host = {n: W.bf16_to_f64(x) for n, x in t.items()}
+    ref = SM.mod_layer(host["q"], host["k"], host["v"], pos, host["do"], window_left=c.w.window_left, **kw)
+    assert_close("o", _np(ua.o_seq), ref["o"])
+    assert_close("lse", _np(ua.lse), ref["lse"], bf16_out=False)
+    for n, x in (("dq", ua.dq_seq), ("dk", ua.dk_seq), ("dv", ua.dv_seq)):
+        assert_close(n, _np(x), ref[n], slack=ref[n + "_slack"])
+
+
+def test_back_to_back_steps_see_the_step_before():
+    """Steps queued without a wait between them, each on the outputs of the one before and with a table that the
+    step before updates: the same bits as with a wait after every call (the launches overlap their set-up only)."""
+    c = next(x for x in CASES if x.w.name == "all")
+    t, pos, kw = _inputs(c)
+    dpos, sinks = torch.from_numpy(pos).cuda(), torch.tensor(kw["sinks"], dtype=torch.float32).cuda()
+
+    def steps(wait):
+        mods = _device_mods(kw)
+        from ulysses_sequence_long_gb300.pipeline import Shape, UlyssesAttention
+        w = c.w
+        ua = UlyssesAttention(Shape(w.B, w.S, w.Hq, w.Hkv, w.D, w.P, w.causal, w.window_left), mods=mods)
+        d = {n: x.cuda() for n, x in t.items()}
+        for _ in range(8):
+            ua.forward(d["q"], d["k"], d["v"], dpos, sinks)
+            wait()
+            ua.backward(d["do"], sinks)
+            wait()
+            d["q"].copy_(ua.o_seq).add_(ua.dq_seq)
+            d["k"].add_(ua.dk_seq)
+            d["do"].copy_(ua.o_seq)
+            mods.rel_bias.sub_(ua.drel_bias, alpha=1e-3)
+            wait()
+        torch.cuda.synchronize()
+        assert ua.read_status() == 0
+        return [x.clone() for x in (ua.o_seq, ua.lse, d["q"], d["k"], ua.dv_seq, ua.dsinks, mods.rel_bias)]
+
+    for a, b in zip(steps(torch.cuda.synchronize), steps(lambda: None)):
+        assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+
+
+def test_values_beyond_the_limits_are_reported():
+    """Biases and slopes that are too large or NaN: a status, no fault."""
+    from ulysses_sequence_long_gb300 import binding as Bd
+    for name, key, values in (("rel_short", "rel_bias", (np.nan, np.inf, 2.0 ** 21)),
+                              ("slope_rows", "slopes", (np.nan, np.inf, -2.0 ** 11))):
+        c = next(x for x in CASES if x.w.name == name)
+        t, pos, kw = _inputs(c)
+        for v in values:
+            bad = kw[key].copy()
+            bad.reshape(-1)[0] = v
+            ua = _layer(c, dict(kw, **{key: bad}))
+            d = {n: x.cuda() for n, x in t.items()}
+            ua.forward(d["q"], d["k"], d["v"], torch.from_numpy(pos).cuda())
+            torch.cuda.synchronize()
+            assert ua.read_status() == Bd.USP_ERR_BAD_MODS
+
+
 def test_bad_data_is_reported():
     """A bucket id outside the table, a negative prefix length, too few prefix lengths: a status, no fault."""
     from ulysses_sequence_long_gb300 import binding as Bd
@@ -346,6 +453,14 @@ def test_refusals_of_the_binding():
     for bad in (ScoreMods(slopes=f(4).double()), ScoreMods(slopes=torch.zeros(4)), ScoreMods(prefix_lens=f(2))):
         with pytest.raises(TypeError):
             UlyssesAttention(shape, mods=bad)
+    two = UlyssesAttention(shape, mods=ScoreMods(softcap=5.0))
+    q2, kv2 = (torch.zeros((2, 1, 128, h, 64), dtype=torch.bfloat16, device="cuda") for h in (4, 2))
+    for args in ((kv2, kv2, kv2, i(256)), (q2, q2, kv2, i(256)), (q2, kv2, kv2, i(255)), (q2, kv2, kv2, i(256), f(3))):
+        with pytest.raises(ValueError):
+            two.forward(*args)
+    two.forward(q2, kv2, kv2, i(256))
+    with pytest.raises(ValueError):
+        two.backward(kv2)
     cu, n = i(257), i(1)
     x = torch.zeros((2, 1, 128, 4, 64), dtype=torch.bfloat16, device="cuda")
     kv = torch.zeros((2, 1, 128, 2, 64), dtype=torch.bfloat16, device="cuda")

@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
   }
   if constexpr (M::on) {
     if (bias_on<M> && mods.slopes != nullptr && tid < kBN)
-      reinterpret_cast<float*>(smem + C::OFF_RAMP)[tid] = __ldg(mods.slopes + r * p.hq + j) * kLog2E * static_cast<float>(tid);
+      reinterpret_cast<float*>(smem + C::OFF_RAMP)[tid] =
+          checked_slope(mods, r * p.hq + j, p.status) * kLog2E * static_cast<float>(tid);
     if (bias_on<M> && mods.rel_bias != nullptr)
       for (int e = tid; e < tab_len(mods.R); e += C::THREADS)
         reinterpret_cast<float*>(smem + C::OFF_TAB)[e] = table_entry(mods, r * p.hq + j, e, p.status);

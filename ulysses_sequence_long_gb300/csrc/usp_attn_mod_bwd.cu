@@ -408,7 +408,7 @@ Layout mod_layout(const usp_attn_params& p, const usp_score_mods& m) {
     end = L.partial = end + up256(sizeof(float) * p.Hq * tab_len(m.max_distance));
     if (m.rel_bias_grad) {
       end = L.sums = end + up256(sizeof(float) * p.Hq * static_cast<size_t>(L.n_rows) * row);
-      if (L.splits > 1) end += up256(sizeof(float) * p.Hq * static_cast<size_t>(L.splits) * row);
+      end += up256(sizeof(float) * p.Hq * static_cast<size_t>(L.splits) * row);
     }
   }
   L.ds = L.total = end;

@@ -88,10 +88,21 @@ __device__ __forceinline__ int checked_bucket(const ModArgs& m, int i, int32_t* 
   return min(max(b, 0), m.n_buckets - 1);
 }
 
-// Entry e (of tab_len(R)) of head h's row by distance, in the log2 domain.
+// Entry e (of tab_len(R)) of head h's row by distance, in the log2 domain.  Beyond
+// 2^20 a bias leaves nothing of a score in fp32: below it hides the key as -inf does
+// (a mask of the type's lowest value among them), above it is reported.
+constexpr float kMaxBias = 0x1p20f, kMaxSlope = 0x1p10f;
 __device__ __forceinline__ float table_entry(const ModArgs& m, int h, int e, int32_t* status) {
   const int d = min(max(e - (m.R + kTabPad), -m.R), m.R);
-  return __ldg(m.rel_bias + static_cast<size_t>(h) * m.n_buckets + checked_bucket(m, d + m.R, status)) * kLog2E;
+  const float v = __ldg(m.rel_bias + static_cast<size_t>(h) * m.n_buckets + checked_bucket(m, d + m.R, status));
+  if (!(v <= kMaxBias)) set_status(status, USP_ERR_BAD_MODS);
+  return v < -kMaxBias ? -INFINITY : v * kLog2E;
+}
+
+__device__ __forceinline__ float checked_slope(const ModArgs& m, int h, int32_t* status) {
+  const float v = __ldg(m.slopes + h);
+  if (!(fabsf(v) <= kMaxSlope)) set_status(status, USP_ERR_BAD_MODS);
+  return v;
 }
 
 // One past the last prefix token of document d = [a, b).
