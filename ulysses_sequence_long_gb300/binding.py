@@ -175,6 +175,10 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
+def _esize(t) -> int:
+    return (t.tensor if type(t) is Buffer else t).element_size()
+
+
 def _dev(t: Optional[torch.Tensor], name: str, dtype=None):
     if t is None:
         return None
@@ -199,18 +203,18 @@ def _stream(stream) -> ctypes.c_void_p:
 
 def usp_relayout_fwd(x_seq, x_head, B, S, H, D, P, stream=None):
     _check(load().usp_relayout_fwd(_dev(x_seq, "x_seq"), _dev(x_head, "x_head"), B, S, H, D, P,
-                                   x_seq.element_size(), _stream(stream)), "usp_relayout_fwd")
+                                   _esize(x_seq), _stream(stream)), "usp_relayout_fwd")
 
 
 def usp_relayout_bwd(x_head, x_seq, B, S, H, D, P, stream=None):
     _check(load().usp_relayout_bwd(_dev(x_head, "x_head"), _dev(x_seq, "x_seq"), B, S, H, D, P,
-                                   x_head.element_size(), _stream(stream)), "usp_relayout_bwd")
+                                   _esize(x_head), _stream(stream)), "usp_relayout_bwd")
 
 
 def usp_relayout_fwd_qkv(q_seq, k_seq, v_seq, q_head, k_head, v_head, B, S, Hq, Hkv, D, P, stream=None):
     _check(load().usp_relayout_fwd_qkv(_dev(q_seq, "q_seq"), _dev(k_seq, "k_seq"), _dev(v_seq, "v_seq"),
                                        _dev(q_head, "q_head"), _dev(k_head, "k_head"), _dev(v_head, "v_head"),
-                                       B, S, Hq, Hkv, D, P, q_seq.element_size(), _stream(stream)),
+                                       B, S, Hq, Hkv, D, P, _esize(q_seq), _stream(stream)),
            "usp_relayout_fwd_qkv")
 
 

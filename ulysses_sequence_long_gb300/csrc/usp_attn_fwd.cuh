@@ -106,7 +106,7 @@ struct Out {
   int nqb;  // query blocks (NQT tiles of 128 rows) per (rank, head)
 };
 
-// Halves of a row's keys (see Cfg).  A cap lengthens a row's chain from S to P, and 8
+// Halves of a row's keys (see Cfg) where there are tiles enough for CTAs of two.  A cap lengthens a row's chain from S to P, and 8
 // softmax warps do not hide it (8192 packed tokens, D = 128: 225 us with whole rows,
 // 208 with halves).  Without one the exchange of the row's maximum costs more than
 // the shorter chain gains (prefix 123 and 127 us, slopes 211 and 219).
@@ -115,12 +115,12 @@ constexpr int kHalves = 1;
 template <bool BIAS>
 constexpr int kHalves<Mods<true, BIAS>> = 2;
 
-template <int D, int NQT, class M>
-__global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>::CTAS)
+template <int D, int NQT, int NH, class M>
+__global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to, AttnArgs p, Out out,
                     M mods) {
-  constexpr int NH = kHalves<M>, NC = kBN / NH;  // columns of a thread
+  constexpr int NC = kBN / NH;  // columns of a thread
   using C = Cfg<D, NQT, NH>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -643,12 +643,12 @@ __global__ void __launch_bounds__(Cfg<D, NQT, kHalves<M>>::THREADS, Cfg<D, NQT>:
 }  // namespace fwd
 
 // `tab_bytes`: shared memory of the bias row (Mods with a table, else 0).
-template <int D, int NQT, class M>
+template <int D, int NQT, int NH, class M>
 static int run_fwd(const AttnArgs& a, const M& mods, int tab_bytes, const CUtensorMap& tq, const CUtensorMap& tk,
                    const CUtensorMap& tv, void* o, float* lse, cudaStream_t st) {
-  using C = fwd::Cfg<D, NQT, fwd::kHalves<M>>;
+  using C = fwd::Cfg<D, NQT, NH>;
   fwd::Out out{static_cast<__nv_bfloat16*>(o), lse, (a.BS + NQT * kBM - 1) / (NQT * kBM)};
-  auto kern = fwd::attn_fwd_kernel<D, NQT, M>;
+  auto kern = fwd::attn_fwd_kernel<D, NQT, NH, M>;
   const int smem = C::SMEM + tab_bytes;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return USP_ERR_CUDA;
@@ -679,9 +679,18 @@ static int run_fwd(const AttnArgs& a, const M& mods, int tab_bytes, const void* 
   if (!M::on && fwd_window_fits(a, D)) return run_fwd_window(a, tq, tk, tv, o, lse, st);
   if constexpr (D == 64) {
     if (a.window_left >= 0 && a.window_left < 4 * kBN)
-      return run_fwd<D, 1, M>(a, mods, tab_bytes, tq, tk, tv, o, lse, st);
+      return run_fwd<D, 1, fwd::kHalves<M>, M>(a, mods, tab_bytes, tq, tk, tv, o, lse, st);
   }
-  return run_fwd<D, 2, M>(a, mods, tab_bytes, tq, tk, tv, o, lse, st);
+  // Few tiles: a CTA of two would leave SMs empty, and one tile in two halves has the shorter chain from S to P.
+  // Two tiles / one, slopes, D = 128: 256 tokens of 8 heads (8 CTAs of two tiles) 12.9 /
+  // 10.5 us, 2048 of 16 (128) 47.4 / 37.2; two rows of 1500 of 12 (144) 45.3 / 43.3 and at D = 64 39.6 / 41.2; 2048
+  // of 32 (256) 53.6 / 70.0.  Half of the gain is that CTAs of unequal length spread better: where rows see later
+  // keys too, D = 128 (one CTA per SM) keeps two tiles (2048 of 16 with a cap, a table and a prefix: 50 / 59).
+  if constexpr (M::on) {
+    const long long ctas = static_cast<long long>((a.BS + 2 * kBM - 1) / (2 * kBM)) * a.P * a.hq;
+    if (ctas * 8 <= device_sm_count() * (D == 64 || mods.later_hidden ? 7 : 4)) return run_fwd<D, 1, 2, M>(a, mods, tab_bytes, tq, tk, tv, o, lse, st);
+  }
+  return run_fwd<D, 2, fwd::kHalves<M>, M>(a, mods, tab_bytes, tq, tk, tv, o, lse, st);
 }
 
 static inline AttnArgs make_fwd_args(const usp_attn_params& prm, int32_t* status) {

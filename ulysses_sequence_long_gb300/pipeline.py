@@ -275,16 +275,23 @@ class UlyssesAttention:
     def exchange_qkv(self, q_seq, k_seq, v_seq, stream=None):
         s = self.shape
         if self._mods is not None:
-            self._inputs = (self._shards(q_seq, "q", s.Hq), self._shards(k_seq, "k", s.Hkv),
-                            self._shards(v_seq, "v", s.Hkv))
+            q, k, v = self._inputs = (self._shards(q_seq, "q", s.Hq), self._shards(k_seq, "k", s.Hkv),
+                                      self._shards(v_seq, "v", s.Hkv))
             if self._one_rank or self._kv_in_place:
                 return
+            own = self._own
+            if self.fused:
+                B_.usp_relayout_fwd(k, own["k_head"], s.B, s.S, s.Hkv, s.D, s.P, stream)
+                B_.usp_relayout_fwd(v, own["v_head"], s.B, s.S, s.Hkv, s.D, s.P, stream)
+            else:
+                B_.usp_relayout_fwd_qkv(q, k, v, own["q_head"], own["k_head"], own["v_head"],
+                                        s.B, s.S, s.Hq, s.Hkv, s.D, s.P, stream)
+            return
         if self.fused:
             # q stays in its shards; k and v go to head layout for the forward
             B_.usp_relayout_fwd(k_seq, self.k_head, s.B, s.S, s.Hkv, s.D, s.P, stream)
             B_.usp_relayout_fwd(v_seq, self.v_head, s.B, s.S, s.Hkv, s.D, s.P, stream)
-            if self._mods is None:
-                self._inputs = (q_seq, k_seq, v_seq)
+            self._inputs = (q_seq, k_seq, v_seq)
             return
         B_.usp_relayout_fwd_qkv(q_seq, k_seq, v_seq, self.q_head, self.k_head, self.v_head,
                                 s.B, s.S, s.Hq, s.Hkv, s.D, s.P, stream)
@@ -328,7 +335,8 @@ class UlyssesAttention:
         if self._mods is not None and self._one_rank:
             return
         if not self.fused:
-            B_.usp_relayout_bwd(self.o_head, self.o_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
+            o, o_seq = (self.o_head, self.o_seq) if self._mods is None else (self._own["o_head"], self._own["o_seq"])
+            B_.usp_relayout_bwd(o, o_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
 
     def forward(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None):
         """Sequence shards in, sequence shards out (``self.o_seq``)."""
@@ -406,7 +414,7 @@ class UlyssesAttention:
         do = self._shards(do_seq, "do", s.Hq)
         mark(0)
         if not in_place:
-            B_.usp_relayout_fwd(do_seq, self.do_head, s.B, s.S, s.Hq, s.D, s.P, stream)
+            B_.usp_relayout_fwd(do, own["do_head"], s.B, s.S, s.Hq, s.D, s.P, stream)
             do = own["do_head"]
         mark(1)
         if marks is None and len(self.ds_groups) == 1:
@@ -429,9 +437,8 @@ class UlyssesAttention:
                 B_.usp_attn_mod_bwd_rel_bias(prm, mods, drel, ws, stream)
         mark(4)
         if not in_place:
-            B_.usp_relayout_bwd(self.dq_head, self.dq_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
-            B_.usp_relayout_bwd(self.dk_head, self.dk_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
-            B_.usp_relayout_bwd(self.dv_head, self.dv_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
+            for grad, name, H in ((dq, "dq_seq", s.Hq), (dk, "dk_seq", s.Hkv), (dv, "dv_seq", s.Hkv)):
+                B_.usp_relayout_bwd(grad, own[name], s.B, s.S, H, s.D, s.P, stream)
         mark(5)
         return self.dq_seq, self.dk_seq, self.dv_seq
 
