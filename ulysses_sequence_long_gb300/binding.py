@@ -165,8 +165,10 @@ class Buffer:
     __slots__ = ("tensor", "ptr")
 
     def __init__(self, tensor: torch.Tensor, name: str = "buffer", dtype=None):
-        self.ptr = _dev(tensor, name, dtype)
-        self.tensor = tensor
+        if not (type(tensor) is torch.Tensor and tensor.is_cuda and tensor.is_contiguous()
+                and (dtype is None or tensor.dtype is dtype)):
+            _dev(tensor, name, dtype)   # says what is wrong
+        self.tensor, self.ptr = tensor, tensor.data_ptr()
 
 
 def _nbytes(t) -> int:
@@ -193,7 +195,9 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream):
+    if type(stream) is int:
+        return stream
     if stream is None:
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
@@ -431,15 +435,14 @@ class _Call:
         return ptr
 
     def run(self, where, *args):
+        stream = _stream(torch.cuda.current_stream(self.device) if self.stream is None else self.stream)
         if torch.cuda.current_device() == self.device.index:
-            self._launch(where, args)
+            rc = getattr(load(), where)(ctypes.byref(self.prm), ctypes.byref(self.mods), *args, stream)
         else:
             with torch.cuda.device(self.device):
-                self._launch(where, args)
-
-    def _launch(self, where, args):
-        stream = _stream(torch.cuda.current_stream(self.device) if self.stream is None else self.stream)
-        _check(getattr(load(), where)(ctypes.byref(self.prm), ctypes.byref(self.mods), *args, stream), where)
+                rc = getattr(load(), where)(ctypes.byref(self.prm), ctypes.byref(self.mods), *args, stream)
+        if rc != USP_OK:
+            raise UspError(rc, where)
 
 
 _BF, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32

@@ -226,6 +226,7 @@ class UlyssesAttention:
             self._one_rank = P == 1
             # Few tokens: the forward reads k and v from the shards too.
             self._kv_in_place = self.fused and Bb * S <= KV_IN_PLACE_TOKENS
+            self._index = self.lse.get_device()
             self._own = {n: B_.Buffer(t, n) for n, t in vars(self).items() if isinstance(t, torch.Tensor)}
             self._prm = {}
 
@@ -240,7 +241,7 @@ class UlyssesAttention:
                     s.B, s.S, s.Hq, s.Hkv, s.D, s.P, self.cu_seqlens, self.n_docs, s.causal, s.window_left,
                     s.softmax_scale, None, io, head_first=group[0], head_count=group[1])
             prm.sinks = B_._dev(sinks, "sinks", torch.float32)
-            if sinks is not None and (sinks.numel() != s.Hq or sinks.device != self.lse.device):
+            if sinks is not None and (sinks.numel() != s.Hq or sinks.get_device() != self._index):
                 raise ValueError(f"sinks must hold one logit per query head ({s.Hq}) on {self.lse.device}, "
                                  f"got {sinks.numel()} on {sinks.device}")
             return prm
@@ -261,13 +262,13 @@ class UlyssesAttention:
     def _handle(self, stream):
         """The CUDA stream of a whole pass, looked up once."""
         if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.lse.device.index)
+            return torch._C._cuda_getCurrentRawStream(self._index)
         return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
     def _shards(self, t, name, H):
         s = self.shape
         shards = B_.Buffer(t, name, torch.bfloat16)
-        if t.numel() != s.B * s.S * H * s.D or t.device != self.lse.device:
+        if t.numel() != s.B * s.S * H * s.D or t.get_device() != self._index:
             raise ValueError(f"{name} must be the shards [{s.P}][{s.B}][{s.S // s.P}][{H}][{s.D}] on {self.lse.device}")
         return shards
 
@@ -300,11 +301,12 @@ class UlyssesAttention:
     def boundaries(self, pos_shards, stream=None):
         s = self.shape
         if self._mods is not None:
-            if pos_shards.numel() != s.B * s.S or pos_shards.device != self.lse.device:
+            pos = B_.Buffer(pos_shards, "pos", torch.int32)
+            if pos_shards.numel() != s.B * s.S or pos_shards.get_device() != self._index:
                 raise ValueError(f"position ids must cover {s.B} x {s.S} tokens on {self.lse.device}, "
                                  f"got {pos_shards.numel()} on {pos_shards.device}")
             o = self._own
-            B_.usp_cu_seqlens_from_position_ids(pos_shards, s.B, s.S, s.P, o["cu_seqlens"], o["n_docs"], o["max_len"],
+            B_.usp_cu_seqlens_from_position_ids(pos, s.B, s.S, s.P, o["cu_seqlens"], o["n_docs"], o["max_len"],
                                                 o["scan_ws"], o["status"], stream)
             return
         B_.usp_cu_seqlens_from_position_ids(pos_shards, s.B, s.S, s.P, self.cu_seqlens, self.n_docs,
@@ -341,8 +343,8 @@ class UlyssesAttention:
     def forward(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None):
         """Sequence shards in, sequence shards out (``self.o_seq``)."""
         if self._mods is not None:
-            if torch.cuda.current_device() != self.lse.device.index:
-                with torch.cuda.device(self.lse.device):
+            if torch.cuda.current_device() != self._index:
+                with torch.cuda.device(self._index):
                     return self.forward(q_seq, k_seq, v_seq, pos_shards, sinks, stream)
             stream = self._handle(stream)
         self.exchange_qkv(q_seq, k_seq, v_seq, stream)
@@ -447,8 +449,8 @@ class UlyssesAttention:
         In explicit mode this is the single ``usp_attn_bwd`` (or
         ``usp_attn_mod_bwd``) call."""
         if self._mods is not None:
-            if torch.cuda.current_device() != self.lse.device.index:
-                with torch.cuda.device(self.lse.device):
+            if torch.cuda.current_device() != self._index:
+                with torch.cuda.device(self._index):
                     return self.backward_phases(do_seq, sinks, stream)
         if self.fused or self._mods is not None:
             return self.backward_phases(do_seq, sinks, stream)
