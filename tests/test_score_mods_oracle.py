@@ -192,12 +192,3 @@ def test_workspace_sizes(lib):
     assert n(_params(), _mods(**rel))[0] == stats + rows
     part = up(4 * 4 * 32 * 33) + up(4 * 4 * 1 * 33)                       # 8 blocks of 32 keys, 4 quarters; 1 split
     assert n(_params(), _mods(**rel, grad=1))[0] == stats + rows + part
-
-
-def test_head_slices_of_a_rank():
-    import torch
-    from ulysses_sequence_long_gb300.pipeline import ScoreMods
-    m = ScoreMods(slopes=torch.arange(8.0), rel_bias=torch.arange(16.0).view(8, 2), buckets=torch.zeros(3, dtype=torch.int32))
-    s = m.for_heads(2, 2)
-    assert s.slopes.tolist() == [2.0, 3.0] and s.rel_bias.tolist() == [[4.0, 5.0], [6.0, 7.0]]
-    assert s.buckets is m.buckets and s.softcap == m.softcap

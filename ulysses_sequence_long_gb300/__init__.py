@@ -2,7 +2,8 @@
 
 The P sequence-parallel ranks are emulated inside one GPU: the all-to-all is a
 relayout kernel, document boundaries are rebuilt from the gathered
-position_ids, and varlen causal GQA attention (windows, per-head sinks) runs
+position_ids, and varlen causal GQA attention (windows, per-head sinks; scores
+capped by a tanh, biased by distance or opened to a prefix) runs
 forward and backward on the tcgen05 tensor core.  The product is the C library
 ``libusp.so`` (include/usp.h); ``binding`` exposes its calls to Python.
 """

@@ -32,7 +32,7 @@ the library's kernels.
 """
 from __future__ import annotations
 
-from dataclasses import dataclass, replace
+from dataclasses import dataclass
 from typing import Optional
 
 import torch
@@ -94,11 +94,6 @@ class ScoreMods:
     def struct(self, Hq: int, with_backward: bool = True) -> B_.ScoreModsStruct:
         return B_.score_mods(Hq, self.softcap, self.slopes, self.rel_bias, self.buckets,
                              with_backward and self.rel_bias is not None and self.rel_bias_grad, self.prefix_lens)
-
-    def for_heads(self, first: int, count: int) -> "ScoreMods":
-        """The same for the query heads [first, first + count): one rank's slice."""
-        cut = lambda t: None if t is None else t[first:first + count].contiguous()
-        return replace(self, slopes=cut(self.slopes), rel_bias=cut(self.rel_bias))
 
 
 def rel_buckets_log(n_buckets: int, max_distance: int, bidirectional: bool, device="cuda") -> torch.Tensor:
