@@ -19,8 +19,9 @@
 // TMEM: S_q [128q, 128q+128), O_q [128NQT + qD, 128NQT + (q+1)D) (512 columns
 // for NQT = 2).  With two tiles the MMA thread alternates them (PV_0, S_0
 // next, PV_1, S_1 next), so the tensor core works on one tile while the other
-// tile's softmax runs; with one tile (short windows at D = 64) two CTAs share
-// an SM and overlap instead.
+// tile's softmax runs; with one tile (short windows at D = 64; with modified
+// scores where there are few tiles) at D = 64 two CTAs share an SM and overlap
+// instead.
 //
 // Online softmax in the log2 domain with a lazy rescale: the running max only
 // moves when a row's new max exceeds it by more than 8 (a factor 256), and the
@@ -448,10 +449,57 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
       ++xn;
       return true;
     };
+    // Moves the running maximum to the tile's; true when some row of the warp moved,
+    // and then alpha is the row's factor.
+    auto move_max = [&](float m_tile, float& alpha) -> bool {
+      const float m_new = fmaxf(m, m_tile);
+      const bool need = m_new > m + 8.f;
+      const bool any = __any_sync(0xffffffffu, need);
+      alpha = need ? ex2(m - m_new) : 1.f;
+      if (need) {
+        l *= alpha;
+        m = m_new;
+      }
+      return any;
+    };
+    // The O rows times alpha.  PV of the previous tile has finished (S of this tile was
+    // committed after it), and PV of this tile waits for this warp's arrival on p_full.
+    auto scale_o = [&](float alpha) {
+#pragma unroll 1
+      for (int c = half * (D / 32 / NH); c < (half + 1) * (D / 32 / NH); ++c) {
+        uint32_t ov[32];
+        tmem_ld32(o_tm + c * 32, ov);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+        tmem_st32(o_tm + c * 32, ov);
+      }
+    };
     bool ok = tile_ok[q];
     for (int n = 0; n < n_kv && ok; ++n) {
       if (!(ok = mbar_wait(&bars->s_full[q], n & 1, abort, p.status))) break;
       tc_fence_after();
+      if constexpr (NH == 2) {
+        // A half that none of the warp's rows sees (past the diagonal, before a window)
+        // has P = 0: it only follows the other half's maximum.
+        const int k0 = lo + n * kBN + half * NC;
+        if (!__any_sync(0xffffffffu, mvlo <= mvhi && mvlo < k0 + NC && mvhi >= k0)) {
+          if (!fixed_ref) {
+            float other, alpha;
+            if (!(ok = exchange(-INFINITY, other))) break;
+            if (move_max(other, alpha) && n > 0) scale_o(alpha);
+          }
+          uint32_t zero[NC / 2];
+#pragma unroll
+          for (int c = 0; c < NC / 2; ++c) zero[c] = 0u;
+          tmem_st(s_tm + half * NC, zero);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[q]);
+          continue;
+        }
+      }
       uint32_t sr[NC / 32][32];
 #pragma unroll
       for (int c = 0; c < NC / 32; ++c) tmem_ld32(s_tm + half * NC + c * 32, sr[c]);
@@ -511,14 +559,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
           if (!(ok = exchange(m_tile, other))) break;
           m_tile = fmaxf(m_tile, other);
         }
-        const float m_new = fmaxf(m, m_tile);
-        const bool need = m_new > m + 8.f;
-        rescale = __any_sync(0xffffffffu, need);
-        alpha = need ? ex2(m - m_new) : 1.f;
-        if (need) {
-          l *= alpha;
-          m = m_new;
-        }
+        rescale = move_max(m_tile, alpha);
       }
       const float m_use = (m == -INFINITY) ? 0.f : m;
       uint64_t rs2[4] = {0, 0, 0, 0};  // 8 independent partial sums, two per register
@@ -539,20 +580,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
       }
       const float2 r01 = f2_unpack(f2_add(rs2[0], rs2[1])), r23 = f2_unpack(f2_add(rs2[2], rs2[3]));
       l += (r01.x + r01.y) + (r23.x + r23.y);
-      // The running max moved for some row of this warp: rescale the O rows.
-      // PV of the previous tile has finished (S of this tile was committed
-      // after it), and PV of this tile waits for this warp's arrival below.
-      if (rescale && n > 0) {
-#pragma unroll 1
-        for (int c = half * (D / 32 / NH); c < (half + 1) * (D / 32 / NH); ++c) {
-          uint32_t ov[32];
-          tmem_ld32(o_tm + c * 32, ov);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-          tmem_st32(o_tm + c * 32, ov);
-        }
-      }
+      if (rescale && n > 0) scale_o(alpha);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
