@@ -358,6 +358,23 @@ def test_any_bucket_map(n_buckets, R, S, D):
     assert np.all(_np(ua.drel_bias)[ref["drel_bias"] == 0] == 0)
 
 
+@pytest.mark.parametrize("D,P,causal", [(64, 1, True), (128, 2, True), (128, 1, False)])
+@pytest.mark.parametrize("mod", ["cap", "slopes", "none"])
+def test_one_visible_key_has_no_score_gradient(D, P, causal, mod):
+    """A window of 0: every row sees itself alone, so O = v and dQ = dK = 0.  P is exactly 1 in the forward, O = v in
+    bf16, and D = dO.v differs from dP by the orders of two fp32 sums over D terms, each within D 2^-24 sum |dO v| <
+    128 6e-8 200 = 1.6e-3 of the value; P of the backward is 1 to 1e-5.  Times scale |k| < 0.125 * 5, and for dK twice
+    (two query heads)."""
+    c = Case(_w("alone", S=512, Hq=4, Hkv=2, D=D, P=P, causal=causal, window_left=0),
+             softcap=20.0 if mod == "cap" else 0.0, slopes=mod == "slopes")
+    t, pos, kw = _inputs(c)
+    ua = _layer(c, kw)
+    _run(c, ua, t, pos, kw)
+    v = t["v"].repeat_interleave(2, dim=3)
+    assert torch.equal(ua.o_seq.cpu(), v)
+    assert ua.dq_seq.abs().max().item() <= 2e-3 * 0.625 and ua.dk_seq.abs().max().item() <= 4e-3 * 0.625
+
+
 @pytest.mark.parametrize("name", ["cap_window", "slope_window_sinks", "rel_many_ranks", "all"])
 def test_keys_and_values_moved_first(name):
     """What a sequence beyond KV_IN_PLACE_TOKENS takes: k and v in head layout for the forward."""

@@ -85,7 +85,7 @@ struct Bars {
   uint64_t p_full[2];
   uint64_t o_final[2];
   uint64_t mma_done;
-  uint64_t x_full[2];  // NH = 2: both halves of the tile's rows have written their exchange values
+  uint64_t x_full[2][4];  // NH = 2: both halves of 32 rows of the tile have written their exchange values
   // Four stages (KV_ONE): kv_full[s] = K and V of the tile in stage s
   // landed (V has time to land before S, so PV needs no wait of its own).
   // Two stages: K_0 signals k_first, and kv_full[m % 2] = V_m and K_{m+1}
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
       mbar_init(&bars->q_full[q], 1);
       mbar_init(&bars->s_full[q], 1);
       mbar_init(&bars->p_full[q], 4 * NH);
-      mbar_init(&bars->x_full[q], 4 * NH);
+      for (int w = 0; w < 4; ++w) mbar_init(&bars->x_full[q][w], NH);
       mbar_init(&bars->o_final[q], 1);
     }
     mbar_init(&bars->mma_done, 1);
@@ -416,11 +416,14 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
       m = __ldg(p.sinks + gh) * 1.4426950408889634f;
       l = half == 0 ? 1.f : 0.f;  // the sink counts once
     }
-    // Mods: the row's visible keys, its bias row and slope, and whether the
-    // cap bounds the scores tightly enough for a fixed reference of the softmax
-    // (the sink's logit where that is larger, as a cap does not bound it)
-    [[maybe_unused]] int mvlo = 1, mvhi = 0;
+    // Mods: the row's visible keys, its bias row and slope, and whether the cap bounds
+    // the scores tightly enough to leave the softmax's reference where the row's first
+    // tile with keys (`first`) put it: at that tile's maximum, so that P is exact where
+    // one key is all that a row sees (any other reference leaves P's rounding to bf16 in
+    // O alone, and with it in D against dP), and at least at ref_floor.
+    [[maybe_unused]] int mvlo = 1, mvhi = 0, first = -1;
     [[maybe_unused]] bool fixed_ref = false;
+    [[maybe_unused]] float ref_floor = -INFINITY;
     [[maybe_unused]] float slope2 = 0.f;
     [[maybe_unused]] const float* tab = nullptr;
     [[maybe_unused]] const float* ramp = reinterpret_cast<const float*>(smem + C::OFF_RAMP);
@@ -430,21 +433,20 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
       if (bias_on<M> && mods.rel_bias != nullptr) tab = reinterpret_cast<const float*>(smem + C::OFF_TAB) + mods.R + kTabPad;
       fixed_ref = cap_on<M> && mods.cap * kLog2E <= kFixedRefCap2;
       if (fixed_ref) {
-        const float ref = fmaxf(m, 0.f);  // m is the sink's logit or -inf
-        l = half == 0 ? ex2(m - ref) : 0.f;
-        m = ref;
+        if (mvlo <= mvhi) first = (mvlo - lo) / kBN;
+        ref_floor = mods.cap * kLog2E - kFixedRefCap2;
       }
     }
-    // NH = 2: `give` hands this half's value of the row to the other half and returns
-    // the other's.  Two buffers in turn: a thread writes a buffer again only after the
+    // NH = 2: hands this half's value of the row to the other half and gets the other's,
+    // between the two warps of 32 rows.  Two buffers in turn: a thread writes a buffer again only after the
     // next exchange, to which the other half comes after reading it.
     [[maybe_unused]] uint32_t xn = 0;
     [[maybe_unused]] auto exchange = [&](float mine, float& other) -> bool {
       float* x = reinterpret_cast<float*>(smem + C::OFF_X) + ((xn & 1) * NQT + q) * 2 * kBM;
       x[half * kBM + row] = mine;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->x_full[q]);
-      if (!mbar_wait(&bars->x_full[q], xn & 1, abort, p.status)) return false;
+      if (lane == 0) mbar_arrive(&bars->x_full[q][warp & 3]);
+      if (!mbar_wait(&bars->x_full[q][warp & 3], xn & 1, abort, p.status)) return false;
       other = x[(half ^ 1) * kBM + row];
       ++xn;
       return true;
@@ -479,14 +481,17 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
     for (int n = 0; n < n_kv && ok; ++n) {
       if (!(ok = mbar_wait(&bars->s_full[q], n & 1, abort, p.status))) break;
       tc_fence_after();
+      // whether the reference may move at this tile (for both halves of a row alike)
+      const bool track = !fixed_ref || __any_sync(0xffffffffu, n == first);
       if constexpr (NH == 2) {
         // A half that none of the warp's rows sees (past the diagonal, before a window)
         // has P = 0: it only follows the other half's maximum.
         const int k0 = lo + n * kBN + half * NC;
         if (!__any_sync(0xffffffffu, mvlo <= mvhi && mvlo < k0 + NC && mvhi >= k0)) {
-          if (!fixed_ref) {
+          if (track) {
             float other, alpha;
             if (!(ok = exchange(-INFINITY, other))) break;
+            if (fixed_ref && n == first) other = fmaxf(other, ref_floor);
             if (move_max(other, alpha) && n > 0) scale_o(alpha);
           }
           uint32_t zero[NC / 2];
@@ -542,7 +547,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
       }
       float alpha = 1.f;
       bool rescale = false;
-      if (!fixed_ref) {
+      if (track) {
         // row max as 8 independent chains
         float mx8[8];
 #pragma unroll
@@ -559,6 +564,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
           if (!(ok = exchange(m_tile, other))) break;
           m_tile = fmaxf(m_tile, other);
         }
+        if (cap_on<M> && fixed_ref && n == first) m_tile = fmaxf(m_tile, ref_floor);
         rescale = move_max(m_tile, alpha);
       }
       const float m_use = (m == -INFINITY) ? 0.f : m;

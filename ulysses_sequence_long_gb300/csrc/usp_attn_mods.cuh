@@ -549,9 +549,10 @@ __device__ __forceinline__ void f2_scale(float (&p)[N], const float (&g)[N]) {
   }
 }
 
-// A capped score lies in [-c2, c2].  Up to this c2 the softmax takes a fixed
-// reference instead of a running maximum: 2^z2 and sums of up to 2^31 of them
-// stay in fp32 (and bf16, which has its range), with room for O's products.
+// A capped score lies in [-c2, c2].  Up to this c2 the softmax's reference does not
+// follow the running maximum past a row's first keys, as long as it lies no more
+// than this below c2: 2^(z2 - reference) and sums of up to 2^31 of them stay in fp32
+// (and bf16, which has its range), with room for O's products.
 constexpr float kFixedRefCap2 = 80.f;
 
 }  // namespace usp
