@@ -418,12 +418,18 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
     }
     // Mods: the row's visible keys, its bias row and slope, and whether the cap bounds
     // the scores tightly enough to leave the softmax's reference where the row's first
-    // tile with keys (`first`) put it: at that tile's maximum, so that P is exact where
+    // tile with keys (`starts`) put it: at that tile's maximum, so that P is exact where
     // one key is all that a row sees (any other reference leaves P's rounding to bf16 in
-    // O alone, and with it in D against dP), and at least at ref_floor.
-    [[maybe_unused]] int mvlo = 1, mvhi = 0, first = -1;
+    // O alone, and with it in D against dP), and at most kFixedRefCap2 below the cap.
+    [[maybe_unused]] int mvlo = 1, mvhi = 0;
     [[maybe_unused]] bool fixed_ref = false;
-    [[maybe_unused]] float ref_floor = -INFINITY;
+    [[maybe_unused]] auto starts = [&](int n) {
+      return static_cast<uint32_t>(mvlo - (lo + n * kBN)) < static_cast<uint32_t>(kBN);
+    };
+    [[maybe_unused]] auto floored = [&](float ref) {
+      if constexpr (M::on) ref = fmaxf(ref, mods.cap * kLog2E - kFixedRefCap2);
+      return ref;
+    };
     [[maybe_unused]] float slope2 = 0.f;
     [[maybe_unused]] const float* tab = nullptr;
     [[maybe_unused]] const float* ramp = reinterpret_cast<const float*>(smem + C::OFF_RAMP);
@@ -432,10 +438,6 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
       if (bias_on<M> && mods.slopes != nullptr) slope2 = __ldg(mods.slopes + gh) * kLog2E;
       if (bias_on<M> && mods.rel_bias != nullptr) tab = reinterpret_cast<const float*>(smem + C::OFF_TAB) + mods.R + kTabPad;
       fixed_ref = cap_on<M> && mods.cap * kLog2E <= kFixedRefCap2;
-      if (fixed_ref) {
-        if (mvlo <= mvhi) first = (mvlo - lo) / kBN;
-        ref_floor = mods.cap * kLog2E - kFixedRefCap2;
-      }
     }
     // NH = 2: hands this half's value of the row to the other half and gets the other's,
     // between the two warps of 32 rows.  Two buffers in turn: a thread writes a buffer again only after the
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
       if (!(ok = mbar_wait(&bars->s_full[q], n & 1, abort, p.status))) break;
       tc_fence_after();
       // whether the reference may move at this tile (for both halves of a row alike)
-      const bool track = !fixed_ref || __any_sync(0xffffffffu, n == first);
+      const bool track = !fixed_ref || __any_sync(0xffffffffu, starts(n));
       if constexpr (NH == 2) {
         // A half that none of the warp's rows sees (past the diagonal, before a window)
         // has P = 0: it only follows the other half's maximum.
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
           if (track) {
             float other, alpha;
             if (!(ok = exchange(-INFINITY, other))) break;
-            if (fixed_ref && n == first) other = fmaxf(other, ref_floor);
+            if (cap_on<M> && fixed_ref && starts(n)) other = floored(other);
             if (move_max(other, alpha) && n > 0) scale_o(alpha);
           }
           uint32_t zero[NC / 2];
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
           if (!(ok = exchange(m_tile, other))) break;
           m_tile = fmaxf(m_tile, other);
         }
-        if (cap_on<M> && fixed_ref && n == first) m_tile = fmaxf(m_tile, ref_floor);
+        if (cap_on<M> && fixed_ref && starts(n)) m_tile = floored(m_tile);
         rescale = move_max(m_tile, alpha);
       }
       const float m_use = (m == -INFINITY) ? 0.f : m;
