@@ -254,6 +254,29 @@ def test_table_updates_and_a_frozen_table():
     assert_close("dk", _np(frozen.dk_seq), ref["dk"])
 
 
+def test_exchanged_storage_of_a_table():
+    """A parameter whose storage is exchanged between calls is read where it is now; another size is refused."""
+    c = next(x for x in CASES if x.w.name == "rel_short")
+    t, pos, kw = _inputs(c)
+    from ulysses_sequence_long_gb300.pipeline import Shape, UlyssesAttention
+    w = c.w
+    mods = _device_mods(kw)
+    mods.rel_bias = torch.nn.Parameter(mods.rel_bias)
+    ua = UlyssesAttention(Shape(w.B, w.S, w.Hq, w.Hkv, w.D, w.P), mods=mods)
+    _run(c, ua, t, pos, kw)
+    old = mods.rel_bias.data
+    mods.rel_bias.data = old * -2.0
+    old.fill_(5.0)
+    d, _ = _run(c, ua, t, pos, kw)
+    host = {n: W.bf16_to_f64(x) for n, x in t.items()}
+    ref = SM.mod_layer(host["q"], host["k"], host["v"], pos, host["do"], **dict(kw, rel_bias=-2.0 * kw["rel_bias"]))
+    assert_close("o", _np(ua.o_seq), ref["o"])
+    _f32_close("drel_bias", ua.drel_bias, ref["drel_bias"])
+    mods.rel_bias.data = old[:, :-1].contiguous()
+    with pytest.raises(ValueError):
+        ua.forward(d["q"], d["k"], d["v"], torch.from_numpy(pos).cuda())
+
+
 def test_captured_and_replayed_on_another_stream():
     """A captured training step replays on new inputs and gives what the eager calls give."""
     c = next(x for x in CASES if x.w.name == "all")

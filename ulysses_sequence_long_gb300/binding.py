@@ -68,8 +68,8 @@ class AttnParams(ctypes.Structure):
 
 
 class ScoreModsStruct(ctypes.Structure):
-    """usp_score_mods (include/usp.h).  ``tensors`` keeps what its pointers point at, all on ``device`` (None when
-    there is no tensor)."""
+    """usp_score_mods (include/usp.h).  ``tensors`` keeps what its pointers point at, as (field, tensor, elements), all
+    on ``device`` (None when there is no tensor)."""
     _fields_ = [
         ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("rel_bias", ctypes.c_void_p),
         ("buckets", ctypes.c_void_p), ("n_buckets", ctypes.c_int), ("max_distance", ctypes.c_int),
@@ -77,6 +77,13 @@ class ScoreModsStruct(ctypes.Structure):
     ]
     tensors = ()
     device = None
+
+    def point(self):
+        """The tensors' addresses of now: a parameter's storage may have been exchanged since the last call."""
+        for field, t, n in self.tensors:
+            if t.numel() != n or t.device != self.device or not t.is_contiguous():
+                raise ValueError(f"{field} has changed its size, strides or device")
+            setattr(self, field, t.data_ptr())
 
 
 USP_IO_HEAD = 0
@@ -389,8 +396,9 @@ def score_mods(Hq, softcap=0.0, slopes=None, rel_bias=None, buckets=None, rel_bi
     m = ScoreModsStruct(float(softcap), sl, rb, bk, 0 if rel_bias is None else rel_bias.shape[1],
                         0 if buckets is None else (buckets.numel() - 1) // 2, 1 if rel_bias_grad else 0, pl,
                         0 if prefix_lens is None else prefix_lens.numel())
-    m.tensors = tuple(t for t in (slopes, rel_bias, buckets, prefix_lens) if t is not None)
-    for t in m.tensors:
+    m.tensors = tuple((f, t, t.numel()) for f, t in (("slopes", slopes), ("rel_bias", rel_bias), ("buckets", buckets),
+                                                     ("prefix_lens", prefix_lens)) if t is not None)
+    for _, t, _ in m.tensors:
         if m.device is None:
             m.device = t.device
         elif t.device != m.device:
@@ -414,6 +422,7 @@ class _Call:
 
     def __init__(self, prm: AttnParams, mods: ScoreModsStruct, stream):
         self.prm, self.mods, self.stream, self.device, self.sizes = prm, mods, stream, mods.device, None
+        mods.point()
 
     def __call__(self, t, name, dtype, size):
         if t is None:
