@@ -31,27 +31,37 @@ namespace bwd {
 // turn S_n into P_n, behind dP_n, which takes dP's one buffer once they have read
 // dP_{n-1}.  The tile counter n runs over all of the CTA's units.
 // TMEM: S [0,128) and [128,256), dP [256,384), scratch [384,512) (tanh_rare).
-template <int D>
+// Column groups of four warps; a thread takes a row's 128 / kDeltaGroups keys of a tile.
+// A cap's longer chain wants more warps (capped windows of 128, D = 64: 76 us with two
+// groups, 66 with four; cap and table, 2048 tokens, D = 128: 52.5 and 50), a bias alone
+// does not (8192 packed tokens, D = 128: 186 and 198).
+template <class M>
+constexpr int kDeltaGroups = cap_on<M> ? 4 : 2;
+
+template <int D, int NG>
 struct CfgD {
+  static constexpr int THREADS = 128 * NG + 64;
   static constexpr int NCH = D / 64;
   static constexpr int TILE = NCH * kBN * 128;       // 128-row bf16 tile
   static constexpr int QST = D == 128 ? 1 : 2;       // buffers of (Q, dO)
-  static constexpr int KST = D == 128 ? 3 : 5;       // buffers of K; S runs a tile ahead of dP
+  static constexpr int KST = D == 64 ? 5 : NG == 4 ? 2 : 3;  // buffers of K; S runs a tile ahead of dP
   static constexpr int VST = D == 128 ? 2 : 4;       // buffers of V
   static constexpr int OFF_Q = 0;                    // per buffer: Q, then dO
   static constexpr int OFF_K = OFF_Q + QST * 2 * TILE;
   static constexpr int OFF_V = OFF_K + KST * TILE;
   static constexpr int OFF_BAR = OFF_V + VST * TILE;
-  static constexpr int OFF_RED = OFF_BAR + 512;      // [2][128] floats
-  static constexpr int SMEM = OFF_RED + 1024 + 1024;
+  static constexpr int OFF_RED = OFF_BAR + 512;      // [2][groups - 1][128] floats
+  static constexpr int SMEM = OFF_RED + 2 * (NG - 1) * kBM * 4 + 1024;
 };
-static_assert(CfgD<128>::SMEM <= kMaxDynSmem && CfgD<64>::SMEM <= kMaxDynSmem, "delta shared memory");
+static_assert(CfgD<128, 2>::SMEM <= kMaxDynSmem && CfgD<128, 4>::SMEM <= kMaxDynSmem &&
+                  CfgD<64, 2>::SMEM <= kMaxDynSmem && CfgD<64, 4>::SMEM <= kMaxDynSmem,
+              "delta shared memory");
 
 struct BarsD {
   uint64_t qd_full[2], qd_free[2];
   uint64_t k_full[5], k_free[5], v_full[4], v_free[4];
   uint64_t s_full[2], s_free[2], dp_full, dp_free;
-  uint64_t red_full[2];  // the second group's row sums of a unit (two in turn) are in shared memory
+  uint64_t red_full[2];  // the other groups' row sums of a unit (two in turn) are in shared memory
   uint64_t mma_done;
   uint32_t tmem;
   int abort;
@@ -81,11 +91,12 @@ __device__ __forceinline__ DeltaUnit delta_unit(const AttnArgs& p, const M& mods
 }
 
 template <int D, class M>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(CfgD<D, kDeltaGroups<M>>::THREADS, 1)
     delta_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                  const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs p,
                  const float* __restrict__ lse, float* __restrict__ stats, int bsp, int n_tiles, M mods) {
-  using C = CfgD<D>;
+  constexpr int NG = kDeltaGroups<M>;
+  using C = CfgD<D, NG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   BarsD* bars = reinterpret_cast<BarsD*>(smem + C::OFF_BAR);
@@ -111,11 +122,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->s_full[b], 1);
-      mbar_init(&bars->s_free[b], 8);
-      mbar_init(&bars->red_full[b], 4);
+      mbar_init(&bars->s_free[b], 4 * NG);
+      mbar_init(&bars->red_full[b], 4 * (NG - 1));
     }
     mbar_init(&bars->dp_full, 1);
-    mbar_init(&bars->dp_free, 8);
+    mbar_init(&bars->dp_free, 4 * NG);
     mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
     fence_barrier_init();
@@ -134,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // The producer's and the MMA issuer's warps walk the units as a whole (delta_unit);
   // their first lanes act.
-  if (warp == 8) {
+  if (warp == 4 * NG) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       prefetch_tmap(&tq);
@@ -189,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, k - C::QST); i < k; ++i)
         mbar_wait(&bars->qd_full[i % C::QST], (i / C::QST) & 1, abort, p.status);
     }
-  } else if (warp == 9) {
+  } else if (warp == 4 * NG + 1) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc = idesc_bf16(kBM, kBN, false, false);  // [128 rows x 128 keys], K = D
     auto issue = [&](uint32_t t_out, uint32_t a, uint32_t b) {
@@ -242,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ compute
-    const int grp = warp >> 2;  // key columns [64*grp, 64*grp + 64) of every tile
+    constexpr int NC = kBN / NG;
+    const int grp = warp >> 2;  // key columns [NC*grp, NC*grp + NC) of every tile
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lb = tmem + ((static_cast<uint32_t>(warp & 3) * 32) << 16);
     float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
@@ -282,31 +294,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint64_t acc2[4] = {0, 0, 0, 0};  // 8 independent partial sums, two per register
       for (int i = 0; i < w.n_kv && ok; ++i, ++n) {
-        const int k0 = w.lo + i * kBN + grp * 64;  // first key of this group's columns
+        const int k0 = w.lo + i * kBN + grp * NC;  // first key of this group's columns
         if (!(ok = mbar_wait(&bars->s_full[n & 1], (n >> 1) & 1, abort, p.status))) break;
         tc_fence_after();
-        float x[64];
-        tmem_ld_cols<64>(lb + (n & 1) * kBN + grp * 64, x);
+        float x[NC];
+        tmem_ld_cols<NC>(lb + (n & 1) * kBN + grp * NC, x);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->s_free[n & 1]);
         const int d0 = t - k0, dw = d0 - lane;
         Affine f{p.scale_log2, 0.f};
         if constexpr (bias_on<M>)
-          f = add_bias(x, tab, mods.R, slope2, nullptr, d0, dw - 63, dw + 31, mods.later_hidden, p.scale_log2);
+          f = add_bias(x, tab, mods.R, slope2, nullptr, d0, dw - (NC - 1), dw + 31, mods.later_hidden, p.scale_log2);
         if constexpr (cap_on<M>) {
-          cap_scores<1>(x, f, mods.cap, true, lb + T_SCRATCH + grp * 64);
+          cap_scores<1>(x, f, mods.cap, true, lb + T_SCRATCH + grp * NC);
           f = {mods.cap * kLog2E, 0.f};
         }
         const int c_lo = w.vlo - k0, c_hi = w.vhi - k0;
-        if (!(c_lo <= 0 && c_hi >= 63)) {
+        if (!(c_lo <= 0 && c_hi >= NC - 1)) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
+          for (int c = 0; c < NC; ++c)
             if (c < c_lo || c > c_hi) x[c] = -INFINITY;
         }
         const uint64_t sc2 = f2_pack(f.sc, f.sc), nl2 = f2_pack(nlse2 + f.off, nlse2 + f.off);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
+        for (int c = 0; c < NC; c += 2) {
           const float2 e = f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sc2, nl2));
           x[c] = ex2(e.x);
           x[c + 1] = ex2(e.y);
@@ -314,23 +326,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i == 0) next = row_of(u + static_cast<int>(gridDim.x));
         if (!(ok = mbar_wait(&bars->dp_full, n & 1, abort, p.status))) break;
         tc_fence_after();
-        float dp[64];
-        tmem_ld_cols<64>(lb + T_DP + grp * 64, dp);
+        float dp[NC];
+        tmem_ld_cols<NC>(lb + T_DP + grp * NC, dp);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->dp_free);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2)
+        for (int c = 0; c < NC; c += 2)
           acc2[(c >> 1) & 3] = f2_fma(f2_pack(x[c], x[c + 1]), f2_pack(dp[c], dp[c + 1]), acc2[(c >> 1) & 3]);
       }
       if (!ok) break;
       const float2 s01 = f2_unpack(f2_add(acc2[0], acc2[1])), s23 = f2_unpack(f2_add(acc2[2], acc2[3]));
       const float sum = (s01.x + s01.y) + (s23.x + s23.y);
-      // The two key halves of a row meet.  The second group writes a buffer again two
-      // units later, for which it has waited for a dP that the first group's reading of
+      // The parts of a row meet.  The other groups write a buffer again two units
+      // later, for which they have waited for a dP that the first group's reading of
       // the unit between released: the first group has read this one by then.
-      if (grp == 1) {
-        red[(k & 1) * kBM + row] = sum;
+      float* part = red + (k & 1) * (NG - 1) * kBM + row;
+      if (grp > 0) {
+        part[(grp - 1) * kBM] = sum;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->red_full[k & 1]);
       } else {
@@ -338,7 +351,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t < p.BS) {
           float* plane = stats + plane_index(bsp, p.hq, hg / p.hq, hg % p.hq, 0, t);
           plane[0] = nlse2 - slope_of_row(mods, slope2, t);
-          plane[bsp] = sum + red[(k & 1) * kBM + row];
+          float all = sum;
+#pragma unroll
+          for (int e = 0; e < NG - 1; ++e) all += part[e * kBM];
+          plane[bsp] = all;
         }
       }
       ++k;
@@ -360,7 +376,7 @@ namespace {
 template <int D, class M>
 int run_delta(const AttnArgs& a, const M& m, const void* q, const void* k, const void* v, const void* dO,
               const float* lse, float* stats, cudaStream_t st) {
-  using C = bwd::CfgD<D>;
+  using C = bwd::CfgD<D, bwd::kDeltaGroups<M>>;
   CUtensorMap tq, tdo, tk, tv;
   int rc;
   if ((rc = make_rows_tmap(&tq, q, a, a.hq, a.Hq, D, kBM)) != USP_OK) return rc;
@@ -373,7 +389,7 @@ int run_delta(const AttnArgs& a, const M& m, const void* q, const void* k, const
   const int n_tiles = (a.BS + kBM - 1) / kBM;
   const long long units = static_cast<long long>(n_tiles) * a.Hq;
   const int grid = units < device_sm_count() ? static_cast<int>(units) : device_sm_count();
-  return launch_chained(kern, grid, bwd::kThreads, C::SMEM, 1, st, tq, tdo, tk, tv, a, lse, stats,
+  return launch_chained(kern, grid, C::THREADS, C::SMEM, 1, st, tq, tdo, tk, tv, a, lse, stats,
                         stats_row_pitch(a.BS), n_tiles, m);
 }
 
