@@ -236,6 +236,37 @@ __device__ __forceinline__ void row_to_tmem(uint32_t taddr, const __nv_bfloat16*
   tmem_wait_st();
 }
 
+// Diagonal sums of a 32 x 32 block whose row l is lane l's x: below = the sum of
+// x_l[e] over e - l = -lane, above = over e - l = 32 - lane (nothing for lane 0).
+// Lanes join in pairs, pairs in fours and so on.  Lane i of m joined rows holds their
+// sums over the diagonals j = m t - i (j = e - l of the first of the rows), t = 0, 1,
+// ...; joined with the next m rows, T'[j] = T[j] + T_next[j + m], lane i of the 2m takes
+// j = 2m s - i: its own value t = 2s and the odd value 2s + 1 (or 2s - 1, for the upper
+// half) of the lane m away.  So each lane sends its odd values and keeps its even ones:
+// 16 + 8 + 4 + 2 + 1 shuffles, where a sum that moves a lane per column took 64.
+template <int N>
+__device__ __forceinline__ void fold_diagonals(const float (&y)[N], int lane, int m, float (&z)[N / 2 + 1]) {
+  const bool upper = lane & m;
+  float r[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) r[i] = __shfl_xor_sync(0xffffffffu, y[2 * i + 1], m);
+#pragma unroll
+  for (int s = 0; s <= N / 2; ++s) {
+    const float lo = s < N / 2 ? r[s < N / 2 ? s : 0] : 0.f, hi = s > 0 ? r[s > 0 ? s - 1 : 0] : 0.f;
+    z[s] = (2 * s < N ? y[2 * s < N ? 2 * s : 0] : 0.f) + (upper ? hi : lo);
+  }
+}
+__device__ __forceinline__ void diagonal_sums(const float (&x)[32], int lane, float& below, float& above) {
+  float a[17], b[9], c[5], d[3], e[2];
+  fold_diagonals(x, lane, 1, a);
+  fold_diagonals(a, lane, 2, b);
+  fold_diagonals(b, lane, 4, c);
+  fold_diagonals(c, lane, 8, d);
+  fold_diagonals(d, lane, 16, e);
+  below = e[0];
+  above = e[1];
+}
+
 // Write one TMEM row (NCOL fp32 columns at `taddr`) times `mul` as bf16 to `dst` (if `ok`).
 template <int NCOL>
 __device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16* dst, float mul, bool ok) {
@@ -380,7 +411,8 @@ struct Grads {
 // With a bias four groups of four warps share a slice's columns (32 each): the
 // bias and its table's gradient lengthen a warp's chain from S^T to P^T and from
 // dP^T to dS^T, which the tensor core waits for, and half the columns halve it
-// (8192 packed tokens, D = 128: learned bias 361 -> 302 us, slopes 352 -> 295 us).
+// (8192 packed tokens, D = 128: learned bias 361 -> 302 us, slopes 352 -> 295 us; 289
+// and 278 with the diagonal sums folded).
 // Without one the chain is short enough that the fewer registers of 16 warps cost
 // as much as they gain (prefix 209 us with two groups, 214 with four; a cap 356
 // and 348, but a cap over short windows at D = 64 96 and 104).
@@ -724,7 +756,6 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
       // dS^T packed once: into TMEM for the dK MMA (first: the MMA thread
       // waits on it), then, if dS is stored, into the staging buffer
       uint32_t pk[NCK][16];
-      [[maybe_unused]] float run = 0.f, done = 0.f;  // diagonal sums of dX (see below)
 #pragma unroll
       for (int c = 0; c < NCK; ++c) {
         if (!(vis >> c & 1u)) {
@@ -752,16 +783,11 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
         tmem_st16(lb + T_DP + gc + 16 * c, pk[c]);
         if constexpr (bias_on<M>) {
           if (mods.partial != nullptr) {
-            // The table's gradient sums dX along diagonals (t - u = const).
-            // Chunks wholly beyond R add to one sum per key; in the others a
-            // diagonal moves one lane up per query column, so a sum that moves
-            // with it (`run`) collects its whole diagonal over the 32 keys: it
-            // enters at lane 0 and is complete when it leaves lane 31, from
-            // where it moves on through a second chain (`done`) to be stored
-            // 32 at a time.  After the chunk's last column lane l holds the
-            // diagonal at distance dw + 31 - l in `run` and, complete, the one
-            // at dw - 1 - l in `done`.  Every distance is stored at most once
-            // by a warp and head: the group's next columns start 128 later.
+            // The table's gradient sums dX along diagonals (t - u = const): a chunk
+            // wholly beyond R adds to one sum per key, the others are folded
+            // (diagonal_sums).  Every distance is stored at most once by a warp and
+            // head: the group's next columns start 128 later.
+            static_assert(NCK == 1, "a group's chunks of one slice would share diagonals");
             const int dw = q0 + 32 * c - uw;
             auto beyond = [&](int w0) { return w0 - 31 >= mods.R || w0 + 31 <= -mods.R; };
             if (beyond(dw)) {
@@ -775,24 +801,16 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
               }
               (dw > 0 ? far_hi : far_lo) += (s4.x + s4.y) + (s4.z + s4.w);
             } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float r1 = __shfl_sync(0xffffffffu, run, (lane + 31) & 31);
-                const float r2 = __shfl_sync(0xffffffffu, done, (lane + 31) & 31);
-                done = lane == 0 ? r1 : r2;
-                run = (lane == 0 ? 0.f : r1) + x[e];
-              }
+              float below, above;
+              diagonal_sums(x, lane, below, above);
               float* row = rel_row(mods, hg0 + i / n_q, uw, grp) + mods.R;
               auto put = [&](int d, float v) {
                 if (d >= mods.R) far_hi += v;
                 else if (d <= -mods.R) far_lo += v;
                 else if (uw < p.BS) row[d] = v;
               };
-              put(dw - 1 - lane, done);
-              if (c + 1 == NCK || !(vis >> (c + 1) & 1u) || beyond(dw + 32)) {  // no column continues the diagonals
-                put(dw + 31 - lane, run);
-                run = done = 0.f;
-              }
+              put(dw - lane, below);
+              if (lane > 0) put(dw + 32 - lane, above);
             }
           }
         }
