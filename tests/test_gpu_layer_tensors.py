@@ -1,0 +1,69 @@
+"""Tensors that change their storage between a layer's calls, and a layer's own
+buffers exchanged for the caller's: every call reads and writes where they are
+now.  Bits are compared with an undisturbed layer's."""
+import pytest
+import torch
+
+import usp_workloads as W
+from gpu_util import built_lib
+from test_gpu_score_mods import _device_mods, _w
+
+pytestmark = pytest.mark.gpu
+
+# exchanges in place (one rank), fused with k and v read in place, fused with k and v moved first, explicit
+LAYOUTS = [(1, None, True), (2, True, True), (2, True, False), (2, False, True)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    built_lib()
+
+
+def _make(P, fused, in_place, **kw):
+    from ulysses_sequence_long_gb300.pipeline import Shape, UlyssesAttention
+    import numpy as np
+    from oracle import score_mods as SM
+    w = _w("exchange", S=256, Hq=4, Hkv=2, D=64, P=P, sinks=True, doc_lens=(100, 156))
+    rng = np.random.default_rng(1)
+    mods = dict(softcap=20.0, rel_bias=rng.standard_normal((4, 8)), buckets=SM.rel_buckets_log(8, 20, False))
+    ua = UlyssesAttention(Shape(w.B, w.S, w.Hq, w.Hkv, w.D, w.P), fused=fused, mods=_device_mods(mods), **kw)
+    ua._kv_in_place = ua._kv_in_place and in_place
+    d = {n: x.cuda() for n, x in W.qkv_do_shards(w).items()}
+    d["pos"] = torch.from_numpy(W.position_ids_shards(w)).cuda()
+    d["sinks"] = W.sinks(w).cuda()
+    return ua, d
+
+
+OUT = ("o_seq", "lse", "dq_seq", "dk_seq", "dv_seq", "dsinks", "drel_bias")
+
+
+def _forward(ua, d):
+    return ua.forward(d["q"], d["k"], d["v"], d["pos"], d["sinks"])
+
+
+def _results(ua):
+    torch.cuda.synchronize()
+    assert ua.read_status() == 0
+    return [getattr(ua, n).clone() for n in OUT]
+
+
+def _expected(P, fused, in_place):
+    ua, d = _make(P, fused, in_place)
+    _forward(ua, d)
+    ua.backward(d["do"], d["sinks"])
+    return _results(ua)
+
+
+@pytest.mark.parametrize("P,fused,in_place", LAYOUTS)
+def test_inputs_whose_storage_is_exchanged_before_the_backward(P, fused, in_place):
+    """What moving a saved tensor out and in again does: the backward reads it where it is."""
+    ua, d = _make(P, fused, in_place)
+    _forward(ua, d)
+    old = []
+    for n in ("q", "k", "v"):
+        old.append(d[n].data)
+        d[n].data = d[n].data.clone()
+        old[-1].fill_(7.0)           # kept alive: nothing else gets this memory
+    ua.backward(d["do"], d["sinks"])
+    for a, b in zip(_results(ua), _expected(P, fused, in_place)):
+        assert torch.equal(a, b)

@@ -1,0 +1,63 @@
+"""Attention with modified scores at the ends of its parameters' ranges, forward
+and backward, against the fp64 restatement of ``oracle.score_mods``.  Tolerances
+as in ``test_gpu_score_mods``, with the roundings of P, dX and O to bf16 left out
+element by element (`*_slack`): gradients scale with the softmax scale."""
+import numpy as np
+import pytest
+import torch
+
+import usp_workloads as W
+from gpu_util import assert_close, built_lib
+from oracle import score_mods as SM
+from test_gpu_score_mods import _device_mods, _f32_close, _np, _w
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    built_lib()
+
+
+def _layer(w, kw, scale=0.0, **more):
+    from ulysses_sequence_long_gb300.pipeline import Shape, UlyssesAttention
+    return UlyssesAttention(Shape(w.B, w.S, w.Hq, w.Hkv, w.D, w.P, w.causal, w.window_left, scale),
+                            mods=_device_mods(kw), **more)
+
+
+def _step(ua, t, pos, sinks=None):
+    d = {n: x.cuda() for n, x in t.items()}
+    ua.forward(d["q"], d["k"], d["v"], torch.from_numpy(pos).cuda(), sinks)
+    ua.backward(d["do"], sinks)
+    torch.cuda.synchronize()
+    assert ua.read_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("softcap,scale", [(2.0 ** -10, 2.0), (2.0 ** -10, 0.5), (0.25, 1024.0), (4.0, 0.25),
+                                           (2.0 ** 10, 2.0 ** -4), (2.0 ** 10, 8.0), (1.0, 2.0 ** 40),
+                                           (2.0 ** -10, 2.0 ** 100)])
+def test_any_ratio_of_scale_and_cap(D, softcap, scale):
+    """Whatever the cap and the softmax scale are: scores whose deviation is a quarter of the cap (a block's largest
+    lies between half the cap and a little beyond it), or 1 where the cap is far above that."""
+    w = _w("ratio", S=256, Hq=4, Hkv=2, D=D, P=2, doc_mode="explicit", doc_lens=(100, 156))
+    t = W.qkv_do_shards(w)
+    pos = W.position_ids_shards(w)
+    t["q"] = (t["q"].double() * (min(0.25 * softcap, 1.0) / scale / D ** 0.5)).to(torch.bfloat16)
+    t["do"] = (t["do"].double() * min(1.0, 1.0 / scale)).to(torch.bfloat16)   # keeps dQ's values in fp32
+    kw = dict(softcap=softcap)
+    ua = _layer(w, kw, scale)
+    _step(ua, t, pos)
+    host = {n: W.bf16_to_f64(x) for n, x in t.items()}
+    ref = SM.mod_layer(host["q"], host["k"], host["v"], pos, host["do"], scale=scale, **kw)
+    assert_close("o", _np(ua.o_seq), ref["o"])
+    assert_close("lse", _np(ua.lse), ref["lse"], bf16_out=False)
+    # (dq and dk carry the scale and the queries' size: bounds in units of their largest value)
+    for n, x in (("dq", ua.dq_seq), ("dk", ua.dk_seq), ("dv", ua.dv_seq)):
+        top = np.abs(ref[n]).max()
+        if n != "dv" and top / scale < 2.0 ** -126:
+            # sum dX q (or k) before the scale: below the smallest normal fp32 number, as dX (here 2^-100) times q
+            # (2^-115) is under a scale of 2^100.  It may be lost; it adds at most itself.
+            assert np.abs(_np(x)).max() <= 2.0 * top
+            continue
+        assert_close(n, _np(x) / top, ref[n] / top, slack=ref[n + "_slack"] / top)

@@ -13,6 +13,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include "usp_attn_common.cuh"
@@ -494,9 +495,9 @@ __device__ __forceinline__ void tanh_poly(float (&x)[N], float k) {
 // `tmem`: N columns of this warp's lanes, free to write.
 template <int TIERS, int N>
 __device__ __forceinline__ float cap_scores(float (&x)[N], Affine f, float cap, bool biased, uint32_t tmem) {
-  float k = f.sc * (0.6931471805599453f / cap);
-  if (TIERS != 3 || biased || k < 0x1p-9f) {
-    // to y itself: the offset of a bias, or a k whose powers would leave fp32
+  float k = fminf(f.sc * (0.6931471805599453f / cap), FLT_MAX);
+  if (TIERS != 3 || biased || k < 0x1p-9f || k > 0x1p9f) {
+    // to y itself: the offset of a bias, or a k whose powers (up to k^12) would leave fp32
     const float ko = f.off * (0.6931471805599453f / cap);
     const uint64_t k2 = f2_pack(k, k), o2 = f2_pack(ko, ko);
 #pragma unroll
