@@ -61,3 +61,28 @@ def test_any_ratio_of_scale_and_cap(D, softcap, scale):
             assert np.abs(_np(x)).max() <= 2.0 * top
             continue
         assert_close(n, _np(x) / top, ref[n] / top, slack=ref[n + "_slack"] / top)
+
+
+@pytest.mark.parametrize("low", [-np.inf, float(np.finfo(np.float32).min)])
+def test_a_sink_of_no_weight_where_a_row_sees_nothing(low):
+    """Head 0 has a sink of no weight and a table that hides every key of some rows: those rows' weights are all
+    zero, and so is what they add to the sink's gradient."""
+    w = _w("no_sink", S=384, Hq=2, Hkv=1, D=64, P=1, sinks=True, doc_mode="explicit", doc_lens=(150, 234))
+    t = W.qkv_do_shards(w)
+    pos = W.position_ids_shards(w)
+    rb = np.random.default_rng(0).standard_normal((2, 8)).astype(np.float32).astype(np.float64)
+    rb[0, 0] = rb[0, -1] = -np.inf
+    kw = dict(rel_bias=rb, buckets=SM.rel_buckets_log(8, 20, False))
+    sinks = np.array([low, 0.5])
+    ua = _layer(w, kw)
+    _step(ua, t, pos, torch.tensor(sinks, dtype=torch.float32).cuda())
+    host = {n: W.bf16_to_f64(x) for n, x in t.items()}
+    # (-1e30 is a sink without weight too, and keeps the restatement's logarithms finite)
+    ref = SM.mod_layer(host["q"], host["k"], host["v"], pos, host["do"], sinks=np.array([-1e30, 0.5]), **kw)
+    none = ref["lse"] == -1e30
+    assert none.any() and np.array_equal(np.isneginf(_np(ua.lse)), none)
+    assert float(ua.dsinks[0]) == 0.0
+    _f32_close("dsinks", ua.dsinks, ref["dsinks"])
+    _f32_close("drel_bias", ua.drel_bias, ref["drel_bias"])
+    for n, x in (("o", ua.o_seq), ("dq", ua.dq_seq), ("dk", ua.dk_seq), ("dv", ua.dv_seq)):
+        assert_close(n, _np(x), ref[n])

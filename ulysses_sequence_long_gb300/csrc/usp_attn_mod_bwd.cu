@@ -526,8 +526,11 @@ __global__ void __launch_bounds__(kSinkThreads)
   for (int b = 0; b < p.B; ++b) {
     const float* l = lse + (static_cast<size_t>(r * p.B + b) * p.hq + j) * p.S;
 #pragma unroll 4
-    for (int s = threadIdx.x; s < p.S; s += kSinkThreads)
-      acc -= ex2(fmaf(-kLog2E, __ldg(l + s), z2)) * __ldg(dd + b * p.S + s);
+    for (int s = threadIdx.x; s < p.S; s += kSinkThreads) {
+      // a row that sees nothing, beside a sink of no weight (-inf): its weights are zero
+      const float lse_s = __ldg(l + s), w = lse_s == -INFINITY ? 0.f : ex2(fmaf(-kLog2E, lse_s, z2));
+      acc -= w * __ldg(dd + b * p.S + s);
+    }
   }
   red[threadIdx.x] = acc;
   __syncthreads();
