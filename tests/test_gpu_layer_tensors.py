@@ -67,3 +67,25 @@ def test_inputs_whose_storage_is_exchanged_before_the_backward(P, fused, in_plac
     ua.backward(d["do"], d["sinks"])
     for a, b in zip(_results(ua), _expected(P, fused, in_place)):
         assert torch.equal(a, b)
+
+
+def test_a_refused_forward_changes_nothing_for_the_backward():
+    ua, d = _make(2, True, True)
+    _forward(ua, d)
+    with pytest.raises(ValueError):
+        ua.forward(d["q"], d["q"], d["v"], d["pos"], d["sinks"])
+    ua.backward(d["do"], d["sinks"])
+    for a, b in zip(_results(ua), _expected(2, True, True)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("P,fused,in_place", LAYOUTS)
+def test_the_steps_called_one_by_one(P, fused, in_place):
+    ua, d = _make(P, fused, in_place)
+    ua.exchange_qkv(d["q"], d["k"], d["v"])
+    ua.boundaries(d["pos"])
+    ua.attention(d["sinks"])
+    ua.exchange_out()
+    ua.backward_phases(d["do"], d["sinks"], marks=lambda i: None)
+    for a, b in zip(_results(ua), _expected(P, fused, in_place)):
+        assert torch.equal(a, b)

@@ -213,12 +213,15 @@ class UlyssesAttention:
                 self.drel_bias = torch.zeros((s.Hq, self._mods.n_buckets), dtype=torch.float32, device=dev)
         self._bwd_ws = None
         self.ds_groups = [(0, 0)]
-        self._inputs = None  # the forward's q/k/v as the attention kernels read them
+        # the forward's q/k/v: as the attention kernels read them, with modified scores the caller's tensors, whose
+        # addresses are taken at each call
+        self._inputs = None
         if self._mods is not None:
             if self._mods.device not in (None, self.lse.device):
                 raise ValueError(f"the score modifications are on {self._mods.device}, the layer on {self.lse.device}")
             # One rank's shards are its head layout, byte for byte: nothing to exchange.
             self._one_rank = P == 1
+            self._in_place = self.fused or self._one_rank   # the attention kernels read and write the shards
             # Few tokens: the forward reads k and v from the shards too.
             self._kv_in_place = self.fused and Bb * S <= KV_IN_PLACE_TOKENS
             self._index = self.lse.get_device()
@@ -267,21 +270,50 @@ class UlyssesAttention:
             raise ValueError(f"{name} must be the shards [{s.P}][{s.B}][{s.S // s.P}][{H}][{s.D}] on {self.lse.device}")
         return shards
 
+    def _input_shards(self, q_seq, k_seq, v_seq):
+        """q, k and v where they are now (a tensor's storage may have been exchanged since the last call)."""
+        s = self.shape
+        return self._shards(q_seq, "q", s.Hq), self._shards(k_seq, "k", s.Hkv), self._shards(v_seq, "v", s.Hkv)
+
+    def _attention_inputs(self):
+        """The forward's q, k and v as the attention kernels read them."""
+        own = self._own
+        return self._input_shards(*self._inputs) if self._in_place else (own["q_head"], own["k_head"], own["v_head"])
+
+    # -- steps with modified scores --------------------------------------------
+    def _mod_exchange(self, q_seq, k_seq, v_seq, stream):
+        s, own = self.shape, self._own
+        q, k, v = shards = self._input_shards(q_seq, k_seq, v_seq)
+        if self._in_place:
+            self._inputs = (q_seq, k_seq, v_seq)
+        if self._one_rank or self._kv_in_place:
+            return shards
+        if self.fused:
+            B_.usp_relayout_fwd(k, own["k_head"], s.B, s.S, s.Hkv, s.D, s.P, stream)
+            B_.usp_relayout_fwd(v, own["v_head"], s.B, s.S, s.Hkv, s.D, s.P, stream)
+        else:
+            B_.usp_relayout_fwd_qkv(q, k, v, own["q_head"], own["k_head"], own["v_head"],
+                                    s.B, s.S, s.Hq, s.Hkv, s.D, s.P, stream)
+            shards = own["q_head"], own["k_head"], own["v_head"]
+        return shards
+
+    def _mod_attention(self, inputs, sinks, stream):
+        own = self._own
+        q, k, v = inputs
+        o = own["o_seq" if self._in_place else "o_head"]
+        if self._one_rank or not self.fused:
+            io = B_.USP_IO_HEAD
+        elif self._kv_in_place:
+            io = B_.USP_IO_SEQ
+        else:
+            io, k, v = B_.USP_IO_SEQ_KV_HEAD, own["k_head"], own["v_head"]
+        B_.usp_attn_mod_fwd(self.params(sinks, io), self._mods, q, k, v, o, own["lse"], own["status"], stream)
+
     # -- steps ---------------------------------------------------------------
     def exchange_qkv(self, q_seq, k_seq, v_seq, stream=None):
         s = self.shape
         if self._mods is not None:
-            q, k, v = self._inputs = (self._shards(q_seq, "q", s.Hq), self._shards(k_seq, "k", s.Hkv),
-                                      self._shards(v_seq, "v", s.Hkv))
-            if self._one_rank or self._kv_in_place:
-                return
-            own = self._own
-            if self.fused:
-                B_.usp_relayout_fwd(k, own["k_head"], s.B, s.S, s.Hkv, s.D, s.P, stream)
-                B_.usp_relayout_fwd(v, own["v_head"], s.B, s.S, s.Hkv, s.D, s.P, stream)
-            else:
-                B_.usp_relayout_fwd_qkv(q, k, v, own["q_head"], own["k_head"], own["v_head"],
-                                        s.B, s.S, s.Hq, s.Hkv, s.D, s.P, stream)
+            self._mod_exchange(q_seq, k_seq, v_seq, stream)
             return
         if self.fused:
             # q stays in its shards; k and v go to head layout for the forward
@@ -308,20 +340,11 @@ class UlyssesAttention:
                                             self.max_len, self.scan_ws, self.status, stream)
 
     def attention(self, sinks=None, stream=None):
-        q, k, v = self._inputs
         if self._mods is not None:
-            own = self._own
-            o = own["o_seq" if self.fused or self._one_rank else "o_head"]
-            if self._one_rank:
-                io = B_.USP_IO_HEAD
-            elif self._kv_in_place:
-                io = B_.USP_IO_SEQ
-            elif self.fused:
-                io, k, v = B_.USP_IO_SEQ_KV_HEAD, own["k_head"], own["v_head"]
-            else:
-                io, q, k, v = B_.USP_IO_HEAD, own["q_head"], own["k_head"], own["v_head"]
-            B_.usp_attn_mod_fwd(self.params(sinks, io), self._mods, q, k, v, o, own["lse"], own["status"], stream)
-        elif self.fused:
+            self._mod_attention(self._attention_inputs(), sinks, stream)
+            return
+        q, k, v = self._inputs
+        if self.fused:
             B_.usp_attn_fwd(self.params(sinks, B_.USP_IO_SEQ_KV_HEAD), q, self.k_head, self.v_head, self.o_seq,
                             self.lse, self.status, stream)
         else:
@@ -342,6 +365,11 @@ class UlyssesAttention:
                 with torch.cuda.device(self._index):
                     return self.forward(q_seq, k_seq, v_seq, pos_shards, sinks, stream)
             stream = self._handle(stream)
+            inputs = self._mod_exchange(q_seq, k_seq, v_seq, stream)
+            self.boundaries(pos_shards, stream)
+            self._mod_attention(inputs, sinks, stream)
+            self.exchange_out(stream)
+            return self.o_seq
         self.exchange_qkv(q_seq, k_seq, v_seq, stream)
         self.boundaries(pos_shards, stream)
         self.attention(sinks, stream)
@@ -401,9 +429,9 @@ class UlyssesAttention:
         self._ws(prm)
         ws = own["ws"]
         mark = marks or (lambda i: None)
-        in_place = self.fused or self._one_rank      # the tensors of the call are the shards
+        in_place = self._in_place
         lay = "_seq" if in_place else "_head"
-        q, k, v = self._inputs if in_place else (own["q_head"], own["k_head"], own["v_head"])
+        q, k, v = self._attention_inputs()
         o, dq, dk, dv = (own[n + lay] for n in ("o", "dq", "dk", "dv"))
         lse, status = own["lse"], own["status"]
         dsinks = own["dsinks"] if sinks is not None else None
