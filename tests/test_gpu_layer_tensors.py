@@ -89,3 +89,87 @@ def test_the_steps_called_one_by_one(P, fused, in_place):
     ua.backward_phases(d["do"], d["sinks"], marks=lambda i: None)
     for a, b in zip(_results(ua), _expected(P, fused, in_place)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("P,fused,in_place", LAYOUTS)
+def test_own_buffers_that_were_exchanged(P, fused, in_place):
+    """A buffer put in place of a layer's own, or another storage under it, is the one that the calls use."""
+    ua, d = _make(P, fused, in_place)
+    _forward(ua, d)
+    ua.backward(d["do"], d["sinks"])     # (the workspace exists from here on)
+    torch.cuda.synchronize()
+    names = [n for n, x in vars(ua).items() if isinstance(x, torch.Tensor)]
+    assert set(OUT) <= set(names) and "_bwd_ws" in names and "cu_seqlens" in names
+    old = {}
+    for i, n in enumerate(names):
+        x = getattr(ua, n)
+        fresh = torch.zeros_like(x)
+        if i % 2:
+            setattr(ua, n, fresh)
+            old[n] = x
+        else:
+            old[n], x.data = x.data, fresh
+        old[n].view(-1).view(torch.uint8).fill_(0x5A)
+    o = _forward(ua, d)
+    assert o is ua.o_seq
+    ua.backward(d["do"], d["sinks"])
+    for a, b in zip(_results(ua), _expected(P, fused, in_place)):
+        assert torch.equal(a, b)
+    for n, x in old.items():
+        assert (x.view(-1).view(torch.uint8) == 0x5A).all(), n
+
+
+def test_exchanged_tensors_of_another_size_or_type_are_refused():
+    ua, d = _make(2, True, True)
+    _forward(ua, d)
+    before = ua.o_seq.clone()
+    for n in ("q", "k", "v"):
+        keep = d[n].data
+        d[n].data = keep[:1].clone()
+        with pytest.raises(ValueError):
+            ua.backward(d["do"], d["sinks"])
+        d[n].data = keep.float()
+        with pytest.raises(TypeError):
+            ua.backward(d["do"], d["sinks"])
+        d[n].data = keep
+    for n in ("o_seq", "lse", "status", "cu_seqlens", "n_docs"):
+        keep = getattr(ua, n)
+        setattr(ua, n, torch.cat([keep.view(-1)] * 2))
+        with pytest.raises(ValueError):
+            _forward(ua, d)
+        setattr(ua, n, keep.double())
+        with pytest.raises(TypeError):
+            _forward(ua, d)
+        setattr(ua, n, keep)
+    ua.backward(d["do"], d["sinks"])
+    for a, b in zip(_results(ua), _expected(2, True, True)):
+        assert torch.equal(a, b)
+    assert torch.equal(before, ua.o_seq)
+
+
+def test_parameters_of_a_call_belong_to_the_caller():
+    """What params() gives is not changed by later calls and holds the buffers' addresses of now."""
+    ua, d = _make(2, True, True)
+    a = ua.params(d["sinks"])
+    b = ua.params(None)
+    assert a.sinks == d["sinks"].data_ptr() and b.sinks is None
+    _forward(ua, d)
+    assert b.sinks is None and a.cu_seqlens == ua.cu_seqlens.data_ptr()
+    ua.cu_seqlens = ua.cu_seqlens.clone()
+    assert ua.params(None).cu_seqlens == ua.cu_seqlens.data_ptr() != a.cu_seqlens
+
+
+def test_a_layer_frees_its_buffers_when_it_is_dropped():
+    import gc
+    import weakref
+    ua, d = _make(2, True, True)
+    _forward(ua, d)
+    ua.backward(d["do"], d["sinks"])
+    torch.cuda.synchronize()
+    gc.disable()
+    try:
+        gone = weakref.ref(ua.o_seq)
+        del ua
+        assert gone() is None
+    finally:
+        gc.enable()

@@ -166,33 +166,9 @@ def _check(rc: int, where: str) -> None:
         raise UspError(rc, where)
 
 
-class Buffer:
-    """A tensor that was checked once and whose owner keeps it: the calls take it for the tensor and do not look
-    at it again (a layer's own buffers, at every step of a model)."""
-    __slots__ = ("tensor", "ptr")
-
-    def __init__(self, tensor: torch.Tensor, name: str = "buffer", dtype=None):
-        if not (type(tensor) is torch.Tensor and tensor.is_cuda and tensor.is_contiguous()
-                and (dtype is None or tensor.dtype is dtype)):
-            _dev(tensor, name, dtype)   # says what is wrong
-        self.tensor, self.ptr = tensor, tensor.data_ptr()
-
-
-def _nbytes(t) -> int:
-    if type(t) is Buffer:
-        t = t.tensor
-    return t.numel() * t.element_size()
-
-
-def _esize(t) -> int:
-    return (t.tensor if type(t) is Buffer else t).element_size()
-
-
 def _dev(t: Optional[torch.Tensor], name: str, dtype=None):
     if t is None:
         return None
-    if type(t) is Buffer:
-        return t.ptr
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if not t.is_contiguous():
@@ -202,9 +178,7 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
-    if type(stream) is int:
-        return stream
+def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
@@ -214,18 +188,18 @@ def _stream(stream):
 
 def usp_relayout_fwd(x_seq, x_head, B, S, H, D, P, stream=None):
     _check(load().usp_relayout_fwd(_dev(x_seq, "x_seq"), _dev(x_head, "x_head"), B, S, H, D, P,
-                                   _esize(x_seq), _stream(stream)), "usp_relayout_fwd")
+                                   x_seq.element_size(), _stream(stream)), "usp_relayout_fwd")
 
 
 def usp_relayout_bwd(x_head, x_seq, B, S, H, D, P, stream=None):
     _check(load().usp_relayout_bwd(_dev(x_head, "x_head"), _dev(x_seq, "x_seq"), B, S, H, D, P,
-                                   _esize(x_head), _stream(stream)), "usp_relayout_bwd")
+                                   x_head.element_size(), _stream(stream)), "usp_relayout_bwd")
 
 
 def usp_relayout_fwd_qkv(q_seq, k_seq, v_seq, q_head, k_head, v_head, B, S, Hq, Hkv, D, P, stream=None):
     _check(load().usp_relayout_fwd_qkv(_dev(q_seq, "q_seq"), _dev(k_seq, "k_seq"), _dev(v_seq, "v_seq"),
                                        _dev(q_head, "q_head"), _dev(k_head, "k_head"), _dev(v_head, "v_head"),
-                                       B, S, Hq, Hkv, D, P, _esize(q_seq), _stream(stream)),
+                                       B, S, Hq, Hkv, D, P, q_seq.element_size(), _stream(stream)),
            "usp_relayout_fwd_qkv")
 
 
@@ -238,7 +212,7 @@ def usp_cu_seqlens_from_position_ids(pos, B, S, P, cu_seqlens, n_docs, max_len, 
     _check(load().usp_cu_seqlens_from_position_ids(
         _dev(pos, "pos", torch.int32), B, S, P, _dev(cu_seqlens, "cu_seqlens", torch.int32),
         _dev(n_docs, "n_docs", torch.int32), _dev(max_len, "max_len", torch.int32), _dev(ws, "ws"),
-        _nbytes(ws), _dev(dev_status, "dev_status", torch.int32), _stream(stream)),
+        ws.numel() * ws.element_size(), _dev(dev_status, "dev_status", torch.int32), _stream(stream)),
         "usp_cu_seqlens_from_position_ids")
 
 
@@ -427,10 +401,6 @@ class _Call:
     def __call__(self, t, name, dtype, size):
         if t is None:
             return None
-        if type(t) is Buffer:
-            if self.device is None:
-                self.device = t.tensor.device
-            return t.ptr
         ptr = _dev(t, name, dtype)
         if self.device is None:
             self.device = t.device
@@ -477,7 +447,7 @@ def usp_attn_mod_bwd(params: AttnParams, mods: ScoreModsStruct, q, k, v, o, lse,
     c.run("usp_attn_mod_bwd", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"), c(o, "o", _BF, "q"),
           c(lse, "lse", _F32, "lse"), c(dO, "dO", _BF, "q"), c(dq, "dq", _BF, "q"),
           c(dk, "dk", _BF, "kv"), c(dv, "dv", _BF, "kv"), c(dsinks, "dsinks", _F32, "heads"),
-          c(drel_bias, "drel_bias", _F32, "rel"), c(ws, "ws", None, None), _nbytes(ws),
+          c(drel_bias, "drel_bias", _F32, "rel"), c(ws, "ws", None, None), ws.numel() * ws.element_size(),
           c(dev_status, "dev_status", _I32, None))
 
 
@@ -486,7 +456,7 @@ def usp_attn_mod_bwd_preprocess(params: AttnParams, mods: ScoreModsStruct, q, k,
     c = _Call(params, mods, stream)
     c.run("usp_attn_mod_bwd_preprocess", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"),
           c(o, "o", _BF, "q"), c(lse, "lse", _F32, "lse"), c(dO, "dO", _BF, "q"), c(dsinks, "dsinks", _F32, "heads"), c(ws, "ws", None, None),
-          _nbytes(ws), c(dev_status, "dev_status", _I32, None))
+          ws.numel() * ws.element_size(), c(dev_status, "dev_status", _I32, None))
 
 
 def usp_attn_mod_bwd_dkdv(params: AttnParams, mods: ScoreModsStruct, q, k, v, dO, dk, dv, ws, dev_status=None,
@@ -494,17 +464,17 @@ def usp_attn_mod_bwd_dkdv(params: AttnParams, mods: ScoreModsStruct, q, k, v, dO
     c = _Call(params, mods, stream)
     c.run("usp_attn_mod_bwd_dkdv", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"),
           c(dO, "dO", _BF, "q"), c(dk, "dk", _BF, "kv"), c(dv, "dv", _BF, "kv"), c(ws, "ws", None, None),
-          _nbytes(ws), c(dev_status, "dev_status", _I32, None))
+          ws.numel() * ws.element_size(), c(dev_status, "dev_status", _I32, None))
 
 
 def usp_attn_mod_bwd_dq(params: AttnParams, mods: ScoreModsStruct, q, k, v, dO, dq, ws, dev_status=None, stream=None):
     c = _Call(params, mods, stream)
     c.run("usp_attn_mod_bwd_dq", c(q, "q", _BF, "q"), c(k, "k", _BF, "kv"), c(v, "v", _BF, "kv"),
-          c(dO, "dO", _BF, "q"), c(dq, "dq", _BF, "q"), c(ws, "ws", None, None), _nbytes(ws),
+          c(dO, "dO", _BF, "q"), c(dq, "dq", _BF, "q"), c(ws, "ws", None, None), ws.numel() * ws.element_size(),
           c(dev_status, "dev_status", _I32, None))
 
 
 def usp_attn_mod_bwd_rel_bias(params: AttnParams, mods: ScoreModsStruct, drel_bias, ws, stream=None):
     c = _Call(params, mods, stream)
     c.run("usp_attn_mod_bwd_rel_bias", c(drel_bias, "drel_bias", _F32, "rel"), c(ws, "ws", None, None),
-          _nbytes(ws))
+          ws.numel() * ws.element_size())

@@ -32,6 +32,7 @@ the library's kernels.
 """
 from __future__ import annotations
 
+import ctypes
 from dataclasses import dataclass
 from typing import Optional
 
@@ -225,24 +226,14 @@ class UlyssesAttention:
             # Few tokens: the forward reads k and v from the shards too.
             self._kv_in_place = self.fused and Bb * S <= KV_IN_PLACE_TOKENS
             self._index = self.lse.get_device()
-            self._own = {n: B_.Buffer(t, n) for n, t in vars(self).items() if isinstance(t, torch.Tensor)}
+            self._seen = {}
+            for n in [n for n, t in vars(self).items() if isinstance(t, torch.Tensor)]:
+                self._remember(n)
+            self._n_q, self._n_kv = Bb * S * s.Hq * D, Bb * S * s.Hkv * D
             self._prm = {}
 
     def params(self, sinks: Optional[torch.Tensor], io: Optional[int] = None, group=(0, 0)) -> B_.AttnParams:
         s = self.shape
-        if self._mods is not None:   # built once for each layout and group; only the sinks change
-            if io is None:
-                io = B_.USP_IO_SEQ if self.fused else B_.USP_IO_HEAD
-            prm = self._prm.get((io, group))
-            if prm is None:
-                prm = self._prm[io, group] = B_.attn_params(
-                    s.B, s.S, s.Hq, s.Hkv, s.D, s.P, self.cu_seqlens, self.n_docs, s.causal, s.window_left,
-                    s.softmax_scale, None, io, head_first=group[0], head_count=group[1])
-            prm.sinks = B_._dev(sinks, "sinks", torch.float32)
-            if sinks is not None and (sinks.numel() != s.Hq or sinks.get_device() != self._index):
-                raise ValueError(f"sinks must hold one logit per query head ({s.Hq}) on {self.lse.device}, "
-                                 f"got {sinks.numel()} on {sinks.device}")
-            return prm
         if io is None:
             io = B_.USP_IO_SEQ if self.fused else B_.USP_IO_HEAD
         return B_.attn_params(s.B, s.S, s.Hq, s.Hkv, s.D, s.P, self.cu_seqlens, self.n_docs, s.causal,
@@ -254,8 +245,38 @@ class UlyssesAttention:
                 prm, self.lse.device, self.stored_ds, self.shape.Hkv, groups_ok=self.fused,
                 group_size=self.ds_group_size, mods=self._mods)
             if self._mods is not None:
-                self._own["ws"] = B_.Buffer(self._bwd_ws, "ws")
+                self._remember("_bwd_ws")
         return self._bwd_ws
+
+    # -- a layer with modified scores: its calls take the addresses of their tensors, and check them, each time ----
+    def _remember(self, name):
+        t = getattr(self, name)
+        self._seen[name] = (t, t.data_ptr(), t.dtype, t.numel())
+
+    def _at(self, t, name, dtype, n):
+        """The address that ``t`` has now."""
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and t.get_device() == self._index
+                and t.is_contiguous()):
+            return t.data_ptr()
+        if B_._dev(t, name, dtype) is None:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} must have {n} elements on {self.lse.device}, got {t.numel()} on {t.device}")
+
+    def _own(self, *names):
+        """The addresses of the layer's own buffers: the caller may have put another tensor, or another storage under
+        it, in a buffer's place.  It has to have the buffer's type and size and lie on the layer's device."""
+        mine, seen, out = self.__dict__, self._seen, []
+        for name in names:
+            t = mine[name]
+            was, at, dtype, n = seen[name]
+            if not (t is was and t.data_ptr() == at and t.dtype is dtype and t.numel() == n and t.is_contiguous()):
+                at = self._at(t, name, dtype, n)
+                seen[name] = (t, at, dtype, n)
+            out.append(at)
+        return out
+
+    def _shards(self, t, name, H):
+        return self._at(t, name, torch.bfloat16, self._n_q if H == self.shape.Hq else self._n_kv)
 
     def _handle(self, stream):
         """The CUDA stream of a whole pass, looked up once."""
@@ -263,57 +284,137 @@ class UlyssesAttention:
             return torch._C._cuda_getCurrentRawStream(self._index)
         return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
-    def _shards(self, t, name, H):
-        s = self.shape
-        shards = B_.Buffer(t, name, torch.bfloat16)
-        if t.numel() != s.B * s.S * H * s.D or t.get_device() != self._index:
-            raise ValueError(f"{name} must be the shards [{s.P}][{s.B}][{s.S // s.P}][{H}][{s.D}] on {self.lse.device}")
-        return shards
+    def _on_device(self, step, *args, stream=None):
+        """step(*args, stream's handle) with the layer's device current."""
+        if torch.cuda.current_device() == self._index:
+            return step(*args, self._handle(stream))
+        with torch.cuda.device(self._index):
+            return step(*args, self._handle(stream))
+
+    @staticmethod
+    def _launch(where, *args):
+        rc = getattr(B_.load(), where)(*args)
+        if rc != B_.USP_OK:
+            raise B_.UspError(rc, where)
+
+    def _mod_call(self, where, io, group, docs, sinks, *args):
+        """``where(params, mods, *args)``; ``docs``: the addresses of cu_seqlens and n_docs.  The structures of a
+        layout and group are built once, of which the addresses change; a call has read them when it returns."""
+        prm = self._prm.get((io, group))
+        if prm is None:
+            prm = self._prm[io, group] = self.params(None, io, group)
+        prm.cu_seqlens, prm.n_docs = docs
+        prm.sinks = None if sinks is None else self._at(sinks, "sinks", torch.float32, self.shape.Hq)
+        self._mods.point()
+        self._launch(where, ctypes.byref(prm), ctypes.byref(self._mods), *args)
 
     def _input_shards(self, q_seq, k_seq, v_seq):
-        """q, k and v where they are now (a tensor's storage may have been exchanged since the last call)."""
         s = self.shape
         return self._shards(q_seq, "q", s.Hq), self._shards(k_seq, "k", s.Hkv), self._shards(v_seq, "v", s.Hkv)
 
     def _attention_inputs(self):
         """The forward's q, k and v as the attention kernels read them."""
-        own = self._own
-        return self._input_shards(*self._inputs) if self._in_place else (own["q_head"], own["k_head"], own["v_head"])
+        return self._input_shards(*self._inputs) if self._in_place else self._own("q_head", "k_head", "v_head")
 
-    # -- steps with modified scores --------------------------------------------
     def _mod_exchange(self, q_seq, k_seq, v_seq, stream):
-        s, own = self.shape, self._own
-        q, k, v = shards = self._input_shards(q_seq, k_seq, v_seq)
+        s = self.shape
+        q, k, v = inputs = self._input_shards(q_seq, k_seq, v_seq)
         if self._in_place:
             self._inputs = (q_seq, k_seq, v_seq)
         if self._one_rank or self._kv_in_place:
-            return shards
+            return inputs
         if self.fused:
-            B_.usp_relayout_fwd(k, own["k_head"], s.B, s.S, s.Hkv, s.D, s.P, stream)
-            B_.usp_relayout_fwd(v, own["v_head"], s.B, s.S, s.Hkv, s.D, s.P, stream)
-        else:
-            B_.usp_relayout_fwd_qkv(q, k, v, own["q_head"], own["k_head"], own["v_head"],
-                                    s.B, s.S, s.Hq, s.Hkv, s.D, s.P, stream)
-            shards = own["q_head"], own["k_head"], own["v_head"]
-        return shards
+            for x, y in zip((k, v), self._own("k_head", "v_head")):
+                self._launch("usp_relayout_fwd", x, y, s.B, s.S, s.Hkv, s.D, s.P, 2, stream)
+            return inputs
+        inputs = self._own("q_head", "k_head", "v_head")
+        self._launch("usp_relayout_fwd_qkv", q, k, v, *inputs, s.B, s.S, s.Hq, s.Hkv, s.D, s.P, 2, stream)
+        return inputs
 
-    def _mod_attention(self, inputs, sinks, stream):
-        own = self._own
+    def _mod_boundaries(self, pos_shards, stream):
+        s = self.shape
+        pos = self._at(pos_shards, "position ids", torch.int32, s.B * s.S)
+        cu, n_docs, max_len, ws, status = self._own("cu_seqlens", "n_docs", "max_len", "scan_ws", "status")
+        self._launch("usp_cu_seqlens_from_position_ids", pos, s.B, s.S, s.P, cu, n_docs, max_len, ws,
+                     self.scan_ws.numel(), status, stream)
+        return cu, n_docs, status
+
+    def _mod_attention(self, inputs, docs, sinks, stream):
         q, k, v = inputs
-        o = own["o_seq" if self._in_place else "o_head"]
+        cu, n_docs, status = docs
+        o, lse = self._own("o_seq" if self._in_place else "o_head", "lse")
         if self._one_rank or not self.fused:
             io = B_.USP_IO_HEAD
         elif self._kv_in_place:
             io = B_.USP_IO_SEQ
         else:
-            io, k, v = B_.USP_IO_SEQ_KV_HEAD, own["k_head"], own["v_head"]
-        B_.usp_attn_mod_fwd(self.params(sinks, io), self._mods, q, k, v, o, own["lse"], own["status"], stream)
+            io = B_.USP_IO_SEQ_KV_HEAD
+            k, v = self._own("k_head", "v_head")
+        self._mod_call("usp_attn_mod_fwd", io, (0, 0), (cu, n_docs), sinks, q, k, v, o, lse, status, stream)
+
+    def _mod_exchange_out(self, stream):
+        if not self._in_place:
+            s = self.shape
+            self._launch("usp_relayout_bwd", *self._own("o_head", "o_seq"), s.B, s.S, s.Hq, s.D, s.P, 2, stream)
+
+    def _mod_forward(self, q_seq, k_seq, v_seq, pos_shards, sinks, stream):
+        inputs = self._mod_exchange(q_seq, k_seq, v_seq, stream)
+        docs = self._mod_boundaries(pos_shards, stream)
+        self._mod_attention(inputs, docs, sinks, stream)
+        self._mod_exchange_out(stream)
+        return self.o_seq
+
+    def _mod_backward(self, do_seq, sinks, marks, group_marks, stream):
+        """``backward_phases`` with modified scores: one library call where no one asks for its phases and
+        the stored dS holds every head."""
+        s, rel = self.shape, self._mods.rel_bias_grad
+        io = B_.USP_IO_SEQ if self.fused else B_.USP_IO_HEAD
+        self._ws(self.params(None, io) if self._bwd_ws is None else None)
+        mark = marks or (lambda i: None)
+        lay = "_seq" if self._in_place else "_head"
+        q, k, v = self._attention_inputs()
+        o, dq, dk, dv, lse, status, ws, *docs = self._own("o" + lay, "dq" + lay, "dk" + lay, "dv" + lay, "lse", "status",
+                                                          "_bwd_ws", "cu_seqlens", "n_docs")
+        ws = (ws, self._bwd_ws.numel())
+        dsinks = self._own("dsinks")[0] if sinks is not None else None
+        drel = self._own("drel_bias")[0] if rel else None
+        do = self._shards(do_seq, "do", s.Hq)
+        call = lambda where, grp, snk, *args: self._mod_call(where, io, grp, docs, snk, *args)
+        mark(0)
+        if not self._in_place:
+            moved, = self._own("do_head")
+            self._launch("usp_relayout_fwd", do, moved, s.B, s.S, s.Hq, s.D, s.P, 2, stream)
+            do = moved
+        mark(1)
+        if marks is None and len(self.ds_groups) == 1:
+            call("usp_attn_mod_bwd", (0, 0), sinks, q, k, v, o, lse, do, dq, dk, dv, dsinks, drel, *ws, status, stream)
+        else:
+            gmark = group_marks or (lambda g, i: None)
+            call("usp_attn_mod_bwd_preprocess", (0, 0), sinks, q, k, v, o, lse, do, dsinks, *ws, status, stream)
+            mark(2)
+            one = len(self.ds_groups) == 1
+            for gi, grp in enumerate(self.ds_groups):
+                call("usp_attn_mod_bwd_dkdv", grp, sinks if one else None, q, k, v, do, dk, dv, *ws, status, stream)
+                mark(3) if one else gmark(gi, 0)
+                call("usp_attn_mod_bwd_dq", grp, sinks if one else None, q, k, v, do, dq, *ws, status, stream)
+                if not one:
+                    gmark(gi, 1)
+            if not one:
+                mark(3)
+            if rel:
+                call("usp_attn_mod_bwd_rel_bias", (0, 0), sinks, drel, *ws, stream)
+        mark(4)
+        if not self._in_place:
+            for grad, name, H in ((dq, "dq_seq", s.Hq), (dk, "dk_seq", s.Hkv), (dv, "dv_seq", s.Hkv)):
+                self._launch("usp_relayout_bwd", grad, *self._own(name), s.B, s.S, H, s.D, s.P, 2, stream)
+        mark(5)
+        return self.dq_seq, self.dk_seq, self.dv_seq
 
     # -- steps ---------------------------------------------------------------
     def exchange_qkv(self, q_seq, k_seq, v_seq, stream=None):
         s = self.shape
         if self._mods is not None:
-            self._mod_exchange(q_seq, k_seq, v_seq, stream)
+            self._on_device(self._mod_exchange, q_seq, k_seq, v_seq, stream=stream)
             return
         if self.fused:
             # q stays in its shards; k and v go to head layout for the forward
@@ -328,20 +429,15 @@ class UlyssesAttention:
     def boundaries(self, pos_shards, stream=None):
         s = self.shape
         if self._mods is not None:
-            pos = B_.Buffer(pos_shards, "pos", torch.int32)
-            if pos_shards.numel() != s.B * s.S or pos_shards.get_device() != self._index:
-                raise ValueError(f"position ids must cover {s.B} x {s.S} tokens on {self.lse.device}, "
-                                 f"got {pos_shards.numel()} on {pos_shards.device}")
-            o = self._own
-            B_.usp_cu_seqlens_from_position_ids(pos, s.B, s.S, s.P, o["cu_seqlens"], o["n_docs"], o["max_len"],
-                                                o["scan_ws"], o["status"], stream)
+            self._on_device(self._mod_boundaries, pos_shards, stream=stream)
             return
         B_.usp_cu_seqlens_from_position_ids(pos_shards, s.B, s.S, s.P, self.cu_seqlens, self.n_docs,
                                             self.max_len, self.scan_ws, self.status, stream)
 
     def attention(self, sinks=None, stream=None):
         if self._mods is not None:
-            self._mod_attention(self._attention_inputs(), sinks, stream)
+            self._on_device(self._mod_attention, self._attention_inputs(), self._own("cu_seqlens", "n_docs", "status"),
+                            sinks, stream=stream)
             return
         q, k, v = self._inputs
         if self.fused:
@@ -352,24 +448,15 @@ class UlyssesAttention:
 
     def exchange_out(self, stream=None):
         s = self.shape
-        if self._mods is not None and self._one_rank:
-            return
-        if not self.fused:
-            o, o_seq = (self.o_head, self.o_seq) if self._mods is None else (self._own["o_head"], self._own["o_seq"])
-            B_.usp_relayout_bwd(o, o_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
+        if self._mods is not None:
+            self._on_device(self._mod_exchange_out, stream=stream)
+        elif not self.fused:
+            B_.usp_relayout_bwd(self.o_head, self.o_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
 
     def forward(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None):
         """Sequence shards in, sequence shards out (``self.o_seq``)."""
         if self._mods is not None:
-            if torch.cuda.current_device() != self._index:
-                with torch.cuda.device(self._index):
-                    return self.forward(q_seq, k_seq, v_seq, pos_shards, sinks, stream)
-            stream = self._handle(stream)
-            inputs = self._mod_exchange(q_seq, k_seq, v_seq, stream)
-            self.boundaries(pos_shards, stream)
-            self._mod_attention(inputs, sinks, stream)
-            self.exchange_out(stream)
-            return self.o_seq
+            return self._on_device(self._mod_forward, q_seq, k_seq, v_seq, pos_shards, sinks, stream=stream)
         self.exchange_qkv(q_seq, k_seq, v_seq, stream)
         self.boundaries(pos_shards, stream)
         self.attention(sinks, stream)
@@ -385,7 +472,7 @@ class UlyssesAttention:
         after group g's dK/dV and dQ passes."""
         s = self.shape
         if self._mods is not None:
-            return self._mod_backward(do_seq, sinks, self._handle(stream), marks, group_marks)
+            return self._on_device(self._mod_backward, do_seq, sinks, marks, group_marks, stream=stream)
         prm = self.params(sinks)
         ws = self._ws(prm)
         mark = marks or (lambda i: None)
@@ -421,60 +508,10 @@ class UlyssesAttention:
         mark(5)
         return self.dq_seq, self.dk_seq, self.dv_seq
 
-    def _mod_backward(self, do_seq, sinks, stream, marks, group_marks):
-        """``backward_phases`` with modified scores: one library call where no one asks for its phases and
-        the stored dS holds every head."""
-        s, own, mods = self.shape, self._own, self._mods
-        prm = self.params(sinks)
-        self._ws(prm)
-        ws = own["ws"]
-        mark = marks or (lambda i: None)
-        in_place = self._in_place
-        lay = "_seq" if in_place else "_head"
-        q, k, v = self._attention_inputs()
-        o, dq, dk, dv = (own[n + lay] for n in ("o", "dq", "dk", "dv"))
-        lse, status = own["lse"], own["status"]
-        dsinks = own["dsinks"] if sinks is not None else None
-        drel = own["drel_bias"] if mods.rel_bias_grad else None
-        do = self._shards(do_seq, "do", s.Hq)
-        mark(0)
-        if not in_place:
-            B_.usp_relayout_fwd(do, own["do_head"], s.B, s.S, s.Hq, s.D, s.P, stream)
-            do = own["do_head"]
-        mark(1)
-        if marks is None and len(self.ds_groups) == 1:
-            B_.usp_attn_mod_bwd(prm, mods, q, k, v, o, lse, do, dq, dk, dv, dsinks, drel, ws, status, stream)
-        else:
-            gmark = group_marks or (lambda g, i: None)
-            B_.usp_attn_mod_bwd_preprocess(prm, mods, q, k, v, o, lse, do, dsinks, ws, status, stream)
-            mark(2)
-            one = len(self.ds_groups) == 1
-            for gi, grp in enumerate(self.ds_groups):
-                prm_g = prm if one else self.params(None, group=grp)
-                B_.usp_attn_mod_bwd_dkdv(prm_g, mods, q, k, v, do, dk, dv, ws, status, stream)
-                mark(3) if one else gmark(gi, 0)
-                B_.usp_attn_mod_bwd_dq(prm_g, mods, q, k, v, do, dq, ws, status, stream)
-                if not one:
-                    gmark(gi, 1)
-            if not one:
-                mark(3)
-            if drel is not None:
-                B_.usp_attn_mod_bwd_rel_bias(prm, mods, drel, ws, stream)
-        mark(4)
-        if not in_place:
-            for grad, name, H in ((dq, "dq_seq", s.Hq), (dk, "dk_seq", s.Hkv), (dv, "dv_seq", s.Hkv)):
-                B_.usp_relayout_bwd(grad, own[name], s.B, s.S, H, s.D, s.P, stream)
-        mark(5)
-        return self.dq_seq, self.dk_seq, self.dv_seq
-
     def backward(self, do_seq, sinks=None, stream=None):
         """dO shards in; dQ/dK/dV shards out (``self.dq_seq`` ...), dsinks.
         In explicit mode this is the single ``usp_attn_bwd`` (or
         ``usp_attn_mod_bwd``) call."""
-        if self._mods is not None:
-            if torch.cuda.current_device() != self._index:
-                with torch.cuda.device(self._index):
-                    return self.backward_phases(do_seq, sinks, stream)
         if self.fused or self._mods is not None:
             return self.backward_phases(do_seq, sinks, stream)
         s = self.shape
