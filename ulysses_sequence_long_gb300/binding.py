@@ -68,8 +68,8 @@ class AttnParams(ctypes.Structure):
 
 
 class ScoreModsStruct(ctypes.Structure):
-    """usp_score_mods (include/usp.h).  ``tensors`` keeps what its pointers point at, as (field, tensor, elements), all
-    on ``device`` (None when there is no tensor)."""
+    """usp_score_mods (include/usp.h).  ``tensors`` keeps what its pointers point at, as (field, tensor, type, shape),
+    all on ``device`` (None when there is no tensor)."""
     _fields_ = [
         ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("rel_bias", ctypes.c_void_p),
         ("buckets", ctypes.c_void_p), ("n_buckets", ctypes.c_int), ("max_distance", ctypes.c_int),
@@ -79,9 +79,12 @@ class ScoreModsStruct(ctypes.Structure):
     device = None
 
     def point(self):
-        """The tensors' addresses of now: a parameter's storage may have been exchanged since the last call."""
-        for field, t, n in self.tensors:
-            if t.numel() != n or t.device != self.device or not t.is_contiguous():
+        """The tensors' addresses of now: a parameter's storage may have been exchanged since the last call (a module
+        that is moved to another type keeps its parameters' objects)."""
+        for field, t, dtype, shape in self.tensors:
+            if t.dtype is not dtype:
+                raise TypeError(f"{field} must be {dtype}, it has become {t.dtype}")
+            if t.shape != shape or t.device != self.device or not t.is_contiguous():
                 raise ValueError(f"{field} has changed its size, strides or device")
             setattr(self, field, t.data_ptr())
 
@@ -370,9 +373,10 @@ def score_mods(Hq, softcap=0.0, slopes=None, rel_bias=None, buckets=None, rel_bi
     m = ScoreModsStruct(float(softcap), sl, rb, bk, 0 if rel_bias is None else rel_bias.shape[1],
                         0 if buckets is None else (buckets.numel() - 1) // 2, 1 if rel_bias_grad else 0, pl,
                         0 if prefix_lens is None else prefix_lens.numel())
-    m.tensors = tuple((f, t, t.numel()) for f, t in (("slopes", slopes), ("rel_bias", rel_bias), ("buckets", buckets),
-                                                     ("prefix_lens", prefix_lens)) if t is not None)
-    for _, t, _ in m.tensors:
+    m.tensors = tuple((f, t, t.dtype, t.shape) for f, t in (("slopes", slopes), ("rel_bias", rel_bias),
+                                                            ("buckets", buckets), ("prefix_lens", prefix_lens))
+                      if t is not None)
+    for _, t, _, _ in m.tensors:
         if m.device is None:
             m.device = t.device
         elif t.device != m.device:
