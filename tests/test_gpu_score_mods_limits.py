@@ -86,3 +86,37 @@ def test_a_sink_of_no_weight_where_a_row_sees_nothing(low):
     _f32_close("drel_bias", ua.drel_bias, ref["drel_bias"])
     for n, x in (("o", ua.o_seq), ("dq", ua.dq_seq), ("dk", ua.dk_seq), ("dv", ua.dv_seq)):
         assert_close(n, _np(x), ref[n])
+
+
+def test_threads_with_tables_of_different_reach():
+    """Two host threads, each with its own layer, tensors and stream: a table that reaches 5 tokens and one that reaches
+    2048 take the same kernel with different amounts of shared memory.  Neither thread's calls may fail."""
+    import threading
+    w = _w("threads", S=128, Hq=2, Hkv=1, D=64, P=1)
+    t = W.qkv_do_shards(w)
+    pos = torch.from_numpy(W.position_ids_shards(w)).cuda()
+    d = {n: x.cuda() for n, x in t.items()}
+    rng = np.random.default_rng(0)
+    layers = [_layer(w, dict(rel_bias=rng.standard_normal((2, 8)), buckets=SM.rel_buckets_log(8, R, False)))
+              for R in (5, 2048)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(ua):
+        try:
+            stream = torch.cuda.Stream()
+            for i in range(4000):
+                ua.forward(d["q"], d["k"], d["v"], pos, stream=stream)
+                if i % 100 == 99:
+                    stream.synchronize()
+        except Exception as e:  # noqa: BLE001 (reported below, in the test's thread)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(ua,)) for ua in layers]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    assert all(ua.read_status() == 0 for ua in layers)

@@ -52,7 +52,6 @@ constexpr int kThreads = 320;
 constexpr int kSL = 64;                      // queries of a stored dS block
 constexpr int kAtomBytes = kBN * 128;        // 128-row, 128-byte-wide swizzle column
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMaxDynSmem = 227 * 1024;      // opt-in dynamic shared memory per CTA
 
 // index of (rank r, local head j, rank-local token t) in a [P][B][hq][S] array
 __device__ __forceinline__ size_t stat_index(const AttnArgs& p, int r, int j, int t) {
@@ -1505,7 +1504,9 @@ static int run_preprocess(const usp_attn_params& prm, const M& mods, const void*
   const int smem = Hb * tok * static_cast<int>(sizeof(float));
   int grid = n_chunks < device_sm_count() * 8 ? n_chunks : device_sm_count() * 8;
   auto kern = prm.D == 128 ? bwd::preprocess_kernel<128, M> : bwd::preprocess_kernel<64, M>;
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  // (one limit for every call, as in run_fwd: 1024 heads at most)
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               1024 * bwd::kPreTok * static_cast<int>(sizeof(float))) != cudaSuccess)
     return USP_ERR_CUDA;
   if constexpr (M::on)
     return launch_chained(kern, grid, 256, smem, 1, st, static_cast<const uint4*>(o), static_cast<const uint4*>(dO),

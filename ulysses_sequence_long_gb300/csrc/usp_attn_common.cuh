@@ -18,6 +18,7 @@ namespace usp {
 
 constexpr int kBM = 128;  // query rows per tile (TMEM lanes)
 constexpr int kBN = 128;  // keys per tile
+constexpr int kMaxDynSmem = 227 * 1024;  // opt-in dynamic shared memory per CTA
 
 struct AttnArgs {
   int BS;           // tokens per rank: B*S

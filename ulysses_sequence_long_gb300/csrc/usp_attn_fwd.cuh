@@ -686,7 +686,11 @@ static int run_fwd(const AttnArgs& a, const M& mods, int tab_bytes, const CUtens
   fwd::Out out{static_cast<__nv_bfloat16*>(o), lse, (a.BS + NQT * kBM - 1) / (NQT * kBM)};
   auto kern = fwd::attn_fwd_kernel<D, NQT, NH, M>;
   const int smem = C::SMEM + tab_bytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  // the limit is one value per kernel, so one that fits every call: a call of another thread must not lower it
+  // between this call's two steps
+  constexpr int limit = C::SMEM + (bias_on<M> ? tab_len(kMaxBiasDistance) * static_cast<int>(sizeof(float)) : 0);
+  static_assert(limit <= kMaxDynSmem, "forward shared memory");
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, limit) != cudaSuccess)
     return USP_ERR_CUDA;
   const unsigned grid = static_cast<unsigned>(out.nqb) * a.P * a.hq;
   CUtensorMap to;

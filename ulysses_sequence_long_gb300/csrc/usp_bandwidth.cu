@@ -671,9 +671,9 @@ int launch_cu_seqlens(const int32_t* pos, int B, int S, int P, int32_t* cu, int3
   ScanWs w{reinterpret_cast<uint32_t*>(ws),
            reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(ws) + kScanHeaderBytes)};
   const size_t smem = sizeof(uint32_t) * std::min<size_t>(g.range / kScanItems, kScanSmemWords);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-          cudaSuccess)
+  // (one limit for every call: another thread's must not lower it before this one's launch)
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sizeof(uint32_t)) * kScanSmemWords) != cudaSuccess)
     return USP_ERR_CUDA;
   if (launch_chained(scan_init_kernel, 1, 256, 0, 1, st, w, g.nblk, max_len) != USP_OK) return USP_ERR_CUDA;
   return launch_chained(scan_kernel, g.nblk, kScanThreads, static_cast<int>(smem), 1, st, pos, g, w, cu, n_docs, max_len,
