@@ -76,8 +76,8 @@ __device__ __forceinline__ size_t plane_index(int bsp, int hq, int r, int j, int
 constexpr int kPreTok = 32;  // the most tokens of a chunk
 
 template <int D, class M>
-__global__ void __launch_bounds__(256) preprocess_kernel(const uint4* __restrict__ o, const uint4* __restrict__ dO,
-                                                         const float* __restrict__ lse, float* __restrict__ stats,
+__global__ void __launch_bounds__(256) preprocess_kernel(const uint4* o, const uint4* dO,
+                                                         const float* lse, float* __restrict__ stats,
                                                          AttnArgs p, int bsp, int n_chunks, int tok, M mods) {
   constexpr int LPR = D / 8;           // 16-byte lanes per row
   // passes whose loads are issued before any of them is reduced, so that
@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(256) preprocess_kernel(const uint4* __restrict
         a[u] = bq[u] = make_uint4(0, 0, 0, 0);
         if (i < nrows) {
           const size_t e = (base + static_cast<size_t>(i) * D) / 8 + lane_row;
-          a[u] = __ldg(o + e);
-          bq[u] = __ldg(dO + e);
+          a[u] = gld(o + e);
+          bq[u] = gld(dO + e);
         }
       }
 #pragma unroll
@@ -138,10 +138,10 @@ __global__ void __launch_bounds__(256) preprocess_kernel(const uint4* __restrict
       if (k < ntok) {
         const int r = p.seq_io ? h / p.hq : r0, j = p.seq_io ? h - r * p.hq : h, t = t0 + k;
         // a row that sees nothing (LSE = -inf) keeps -inf, so that its weights are 2^-inf = 0
-        const float l = __ldg(lse + stat_index(p, r, j, t));
+        const float l = gld(lse + stat_index(p, r, j, t));
         float nl = l == -INFINITY ? l : l * -kLog2e;
         if constexpr (bias_on<M>) {
-          if (mods.slopes != nullptr) nl -= slope_of_row(mods, __ldg(mods.slopes + r * p.hq + j) * kLog2E, t);
+          if (mods.slopes != nullptr) nl -= slope_of_row(mods, gld(mods.slopes + r * p.hq + j) * kLog2E, t);
         }
         stats[plane_index(bsp, p.hq, r, j, 0, t)] = nl;
         stats[plane_index(bsp, p.hq, r, j, 1, t)] = dsum[idx];
@@ -152,15 +152,15 @@ __global__ void __launch_bounds__(256) preprocess_kernel(const uint4* __restrict
 }
 
 // --------------------------------------------------------------- dsink
-static __global__ void __launch_bounds__(256) dsink_kernel(const float* __restrict__ stats, float* __restrict__ dsinks,
+static __global__ void __launch_bounds__(256) dsink_kernel(const float* stats, float* __restrict__ dsinks,
                                                     AttnArgs p, int bsp) {
   __shared__ float red[256];
   const int r = blockIdx.x / p.hq, j = blockIdx.x % p.hq;
-  const float z2 = __ldg(p.sinks + r * p.hq + j) * kLog2e;
+  const float z2 = gld(p.sinks + r * p.hq + j) * kLog2e;
   const float* l2 = stats + plane_index(bsp, p.hq, r, j, 0, 0);
   const float* dd = stats + plane_index(bsp, p.hq, r, j, 1, 0);
   float acc = 0.f;
-  for (int t = threadIdx.x; t < p.BS; t += blockDim.x) acc -= ex2(z2 + __ldg(l2 + t)) * __ldg(dd + t);
+  for (int t = threadIdx.x; t < p.BS; t += blockDim.x) acc -= ex2(z2 + gld(l2 + t)) * gld(dd + t);
   red[threadIdx.x] = acc;
   __syncthreads();
   for (int s = 128; s > 0; s >>= 1) {
@@ -224,7 +224,7 @@ __device__ __forceinline__ void row_to_tmem(uint32_t taddr, const __nv_bfloat16*
     uint32_t v[32];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(src + c * 64) + e) : make_uint4(0, 0, 0, 0);
+      uint4 w = ok ? gld(reinterpret_cast<const uint4*>(src + c * 64) + e) : make_uint4(0, 0, 0, 0);
       v[4 * e] = w.x;
       v[4 * e + 1] = w.y;
       v[4 * e + 2] = w.z;
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
         if constexpr (bias_on<M>) {
 
           if (mods.table != nullptr) tab = mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad;
-          if (mods.slopes != nullptr) slope2 = __ldg(mods.slopes + hg) * kLog2E;
+          if (mods.slopes != nullptr) slope2 = gld(mods.slopes + hg) * kLog2E;
         }
       }
 #pragma unroll
@@ -1084,11 +1084,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     float nlse2 = -INFINITY, dvt = 0.f;  // -LSE*log2(e) of the row
     if (row_ok) {
       doc_bounds(p, mods, n_docs, t, a, b, pe);
-      nlse2 = __ldg(g.stats + plane_index(g.bsp, p.hq, r, j, 0, t));
+      nlse2 = gld(g.stats + plane_index(g.bsp, p.hq, r, j, 0, t));
       if constexpr (bias_on<M>) {
-        if (mods.slopes != nullptr) nlse2 += slope_of_row(mods, __ldg(mods.slopes + hg) * kLog2E, t);
+        if (mods.slopes != nullptr) nlse2 += slope_of_row(mods, gld(mods.slopes + hg) * kLog2E, t);
       }
-      dvt = __ldg(g.stats + plane_index(g.bsp, p.hq, r, j, 1, t));
+      dvt = gld(g.stats + plane_index(g.bsp, p.hq, r, j, 1, t));
     }
     a = max(a, rk0);  // a ring step: one key/value super-chunk only
     b = min(b, rk1);
@@ -1099,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (M::on) {
       if constexpr (bias_on<M>) {
         if (mods.table != nullptr) tab = mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad;
-        if (mods.slopes != nullptr) slope2 = __ldg(mods.slopes + hg) * kLog2E;
+        if (mods.slopes != nullptr) slope2 = gld(mods.slopes + hg) * kLog2E;
       }
     }
     const uint32_t s_col = T_S + grp * 64, dp_col = T_DP + grp * 64;

@@ -119,21 +119,21 @@ __device__ __forceinline__ void tma_store_rows(const CUtensorMap* m, const void*
 }
 
 // Document index d with cu[d] <= t < cu[d+1] (cu assumed valid, n >= 1).
-__device__ __forceinline__ int find_doc(const int32_t* __restrict__ cu, int n, int t) {
+__device__ __forceinline__ int find_doc(const int32_t* cu, int n, int t) {
   int lo = 0, hi = n;  // invariant: cu[lo] <= t < cu[hi]
   while (hi - lo > 1) {
     int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid;
+    if (gld(cu + mid) <= t) lo = mid; else hi = mid;
   }
   return lo;
 }
 
 // [start, end) of the document holding token t, clamped so that a malformed
 // cu_seqlens (already reported) can never send an index out of [0, BS).
-__device__ __forceinline__ void doc_bounds(const int32_t* __restrict__ cu, int n, int BS, int t, int& a, int& b) {
+__device__ __forceinline__ void doc_bounds(const int32_t* cu, int n, int BS, int t, int& a, int& b) {
   int d = find_doc(cu, n, t);
-  a = __ldg(cu + d);
-  b = __ldg(cu + d + 1);
+  a = gld(cu + d);
+  b = gld(cu + d + 1);
   a = max(0, min(a, t));
   b = min(BS, max(b, t + 1));
 }
@@ -216,16 +216,16 @@ __device__ __forceinline__ void query_range(const AttnArgs& p, int n, int u_firs
 // USP_ERR_BAD_SEQLENS) when it cannot describe the gathered sequence.  Block 0
 // also checks that every document is non-empty.
 __device__ __forceinline__ int checked_docs(const AttnArgs& p) {
-  int n = __ldg(p.n_docs);
+  int n = gld(p.n_docs);
   bool ok = n >= 1 && n <= p.BS;
-  if (ok) ok = __ldg(p.cu) == 0 && __ldg(p.cu + n) == p.BS;
+  if (ok) ok = gld(p.cu) == 0 && gld(p.cu + n) == p.BS;
   if (!ok) {
     if (threadIdx.x == 0) set_status(p.status, USP_ERR_BAD_SEQLENS);
     return 0;
   }
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     for (int d = threadIdx.x; d < n; d += blockDim.x)
-      if (__ldg(p.cu + d + 1) <= __ldg(p.cu + d)) set_status(p.status, USP_ERR_BAD_SEQLENS);
+      if (gld(p.cu + d + 1) <= gld(p.cu + d)) set_status(p.status, USP_ERR_BAD_SEQLENS);
   }
   return n;
 }

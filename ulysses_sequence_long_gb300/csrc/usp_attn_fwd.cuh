@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
         for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0, 0, 0, 0);
         const int bb = t / p.S, ss = t - bb * p.S;
         out.lse[(static_cast<size_t>(r * p.B + bb) * p.hq + j) * p.S + ss] =
-            p.sinks != nullptr ? __ldg(p.sinks + r * p.hq + j) : -INFINITY;
+            p.sinks != nullptr ? gld(p.sinks + r * p.hq + j) : -INFINITY;
       }
     }
     leave_early();
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
     const int gh = r * p.hq + j;  // global query head: the sink slice of this rank
     float m = -INFINITY, l = 0.f;
     if (p.sinks != nullptr) {
-      m = __ldg(p.sinks + gh) * 1.4426950408889634f;
+      m = gld(p.sinks + gh) * 1.4426950408889634f;
       l = half == 0 ? 1.f : 0.f;  // the sink counts once
     }
     // Mods: the row's visible keys, its bias row and slope, and whether the cap bounds
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
     [[maybe_unused]] const float* ramp = reinterpret_cast<const float*>(smem + C::OFF_RAMP);
     if constexpr (M::on) {
       visible_keys(mods, t, a, b, pe, p.causal, p.window_left, row_ok, mvlo, mvhi);
-      if (bias_on<M> && mods.slopes != nullptr) slope2 = __ldg(mods.slopes + gh) * kLog2E;
+      if (bias_on<M> && mods.slopes != nullptr) slope2 = gld(mods.slopes + gh) * kLog2E;
       if (bias_on<M> && mods.rel_bias != nullptr) tab = reinterpret_cast<const float*>(smem + C::OFF_TAB) + mods.R + kTabPad;
       fixed_ref = cap_on<M> && mods.cap * kLog2E <= kFixedRefCap2;
     }

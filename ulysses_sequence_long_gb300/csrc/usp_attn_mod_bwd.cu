@@ -94,7 +94,7 @@ template <int D, class M>
 __global__ void __launch_bounds__(CfgD<D, kDeltaGroups<M>>::THREADS, 1)
     delta_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                  const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs p,
-                 const float* __restrict__ lse, float* __restrict__ stats, int bsp, int n_tiles, M mods) {
+                 const float* lse, float* __restrict__ stats, int bsp, int n_tiles, M mods) {
   constexpr int NG = kDeltaGroups<M>;
   using C = CfgD<D, NG>;
   extern __shared__ uint8_t smem_raw[];
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(CfgD<D, kDeltaGroups<M>>::THREADS, 1)
       const DeltaUnit w = delta_unit(p, mods, n_docs, n_tiles, u);
       const int t = w.t0 + row;
       const bool row_ok = t < p.BS;
-      if (row_ok) x.lse = __ldg(lse + stat_index(p, w.r, w.j, t));
+      if (row_ok) x.lse = gld(lse + stat_index(p, w.r, w.j, t));
       int a = 0, b = 0, pe = 0;
       if (row_ok) doc_bounds(p, mods, w.docs, t, a, b, pe);
       visible_keys(mods, t, a, b, pe, p.causal, p.window_left, row_ok, x.vlo, x.vhi);
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(CfgD<D, kDeltaGroups<M>>::THREADS, 1)
       const float nlse2 = w.lse == -INFINITY || t >= p.BS ? -INFINITY : w.lse * -kLog2e;  // (as in preprocess_kernel)
       const float* tab =
           mods.table != nullptr ? mods.table + static_cast<size_t>(hg) * tab_len(mods.R) + mods.R + kTabPad : nullptr;
-      const float slope2 = mods.slopes != nullptr ? __ldg(mods.slopes + hg) * kLog2E : 0.f;
+      const float slope2 = mods.slopes != nullptr ? gld(mods.slopes + hg) * kLog2E : 0.f;
       if (w.n_kv == 0) {
         next = row_of(u + static_cast<int>(gridDim.x));
         continue;
@@ -458,12 +458,12 @@ __global__ void __launch_bounds__(kRelThreads)
 
 // One column of rows [r0, r1), kRelAhead of them in flight (the last again past the
 // end: a load behind a branch would wait for the one before), joined in a fixed order.
-__device__ __forceinline__ float rel_column(const float* __restrict__ src, int r0, int r1, int step, int row) {
+__device__ __forceinline__ float rel_column(const float* src, int r0, int r1, int step, int row) {
   float acc = 0.f;
   for (int r = r0; r < r1; r += step) {
     float x[kRelAhead];
 #pragma unroll
-    for (int e = 0; e < kRelAhead; ++e) x[e] = __ldg(src + static_cast<size_t>(min(r + e, r1 - 1)) * row);
+    for (int e = 0; e < kRelAhead; ++e) x[e] = gld(src + static_cast<size_t>(min(r + e, r1 - 1)) * row);
 #pragma unroll
     for (int e = 0; e < kRelAhead; ++e) x[e] = r + e < r1 ? x[e] : 0.f;
 #pragma unroll
@@ -477,7 +477,7 @@ __device__ __forceinline__ float rel_column(const float* __restrict__ src, int r
 
 // Many rows: a split's partial rows of a head become one, thread = distance.
 __global__ void __launch_bounds__(1024, 1)
-    rel_sum_kernel(const float* __restrict__ partial, float* __restrict__ sums, int n_rows, int per, int row) {
+    rel_sum_kernel(const float* partial, float* __restrict__ sums, int n_rows, int per, int row) {
   const int h = blockIdx.x, s = blockIdx.y;
   grid_wait();
   const float* src = partial + static_cast<size_t>(h) * n_rows * row;
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(1024, 1)
 // bucket at a time, its lanes the distances, joined by a fixed tree (no atomics: the
 // result does not depend on the schedule).
 __global__ void __launch_bounds__(1024, 1)
-    rel_grad_kernel(ModArgs m, const float* __restrict__ rows, float* __restrict__ drel, int n_rows, int row) {
+    rel_grad_kernel(ModArgs m, const float* rows, float* __restrict__ drel, int n_rows, int row) {
   extern __shared__ float by_dist[];  // [teams][row]
   const int teams = rel_teams(row), width = blockDim.x / teams, team = threadIdx.x / width;
   int* bucket = reinterpret_cast<int*>(by_dist + teams * row);
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(1024, 1)
   const float* src = rows + static_cast<size_t>(h) * n_rows * row;
   for (int c = threadIdx.x - team * width; c < row; c += width)
     by_dist[team * row + c] = rel_column(src + c, team * kRelAhead, n_rows, teams * kRelAhead, row);
-  for (int c = threadIdx.x; c < row; c += blockDim.x) bucket[c] = min(max(__ldg(m.buckets + c), 0), m.n_buckets - 1);
+  for (int c = threadIdx.x; c < row; c += blockDim.x) bucket[c] = min(max(gld(m.buckets + c), 0), m.n_buckets - 1);
   __syncthreads();
   for (int b = threadIdx.x >> 5; b < m.n_buckets; b += blockDim.x / 32) {
     float acc = 0.f;
@@ -515,12 +515,12 @@ __global__ void __launch_bounds__(1024, 1)
 // dsink_h = -sum_t exp(sink_h - LSE_t) D_t: one block per head, fixed-order tree.
 constexpr int kSinkThreads = 512;
 __global__ void __launch_bounds__(kSinkThreads)
-    mod_dsink_kernel(const float* __restrict__ stats, const float* __restrict__ lse, float* __restrict__ dsinks,
+    mod_dsink_kernel(const float* stats, const float* lse, float* __restrict__ dsinks,
                      AttnArgs p, int bsp) {
   __shared__ float red[kSinkThreads];
   const int r = blockIdx.x / p.hq, j = blockIdx.x % p.hq;
   grid_wait();
-  const float z2 = __ldg(p.sinks + blockIdx.x) * kLog2E;
+  const float z2 = gld(p.sinks + blockIdx.x) * kLog2E;
   const float* dd = stats + bwd::plane_index(bsp, p.hq, r, j, 1, 0);
   float acc = 0.f;
   for (int b = 0; b < p.B; ++b) {
@@ -528,8 +528,8 @@ __global__ void __launch_bounds__(kSinkThreads)
 #pragma unroll 4
     for (int s = threadIdx.x; s < p.S; s += kSinkThreads) {
       // a row that sees nothing, beside a sink of no weight (-inf): its weights are zero
-      const float lse_s = __ldg(l + s), w = lse_s == -INFINITY ? 0.f : ex2(fmaf(-kLog2E, lse_s, z2));
-      acc -= w * __ldg(dd + b * p.S + s);
+      const float lse_s = gld(l + s), w = lse_s == -INFINITY ? 0.f : ex2(fmaf(-kLog2E, lse_s, z2));
+      acc -= w * gld(dd + b * p.S + s);
     }
   }
   red[threadIdx.x] = acc;

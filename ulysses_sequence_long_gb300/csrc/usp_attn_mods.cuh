@@ -84,7 +84,7 @@ __device__ __forceinline__ float* rel_row(const ModArgs& m, int hg, int uw, int 
 
 // Bucket of distance index i, clamped into the table; an id outside it is reported.
 __device__ __forceinline__ int checked_bucket(const ModArgs& m, int i, int32_t* status) {
-  const int b = __ldg(m.buckets + i);
+  const int b = gld(m.buckets + i);
   if (b < 0 || b >= m.n_buckets) set_status(status, USP_ERR_BAD_MODS);
   return min(max(b, 0), m.n_buckets - 1);
 }
@@ -95,13 +95,13 @@ __device__ __forceinline__ int checked_bucket(const ModArgs& m, int i, int32_t* 
 constexpr float kMaxBias = 0x1p20f, kMaxSlope = 0x1p10f;
 __device__ __forceinline__ float table_entry(const ModArgs& m, int h, int e, int32_t* status) {
   const int d = min(max(e - (m.R + kTabPad), -m.R), m.R);
-  const float v = __ldg(m.rel_bias + static_cast<size_t>(h) * m.n_buckets + checked_bucket(m, d + m.R, status));
+  const float v = gld(m.rel_bias + static_cast<size_t>(h) * m.n_buckets + checked_bucket(m, d + m.R, status));
   if (!(v <= kMaxBias)) set_status(status, USP_ERR_BAD_MODS);
   return v < -kMaxBias ? -INFINITY : v * kLog2E;
 }
 
 __device__ __forceinline__ float checked_slope(const ModArgs& m, int h, int32_t* status) {
-  const float v = __ldg(m.slopes + h);
+  const float v = gld(m.slopes + h);
   if (!(fabsf(v) <= kMaxSlope)) set_status(status, USP_ERR_BAD_MODS);
   return v;
 }
@@ -113,7 +113,7 @@ __device__ __forceinline__ int prefix_end(const ModArgs& m, int d, int a, int b,
     set_status(status, USP_ERR_BAD_MODS);
     return a;
   }
-  const int len = __ldg(m.prefix + d);
+  const int len = gld(m.prefix + d);
   if (len < 0) set_status(status, USP_ERR_BAD_MODS);
   return a + min(max(len, 0), b - a);
 }
@@ -125,8 +125,8 @@ __device__ __forceinline__ void doc_bounds(const AttnArgs& p, const NoMods&, int
 }
 __device__ __forceinline__ void doc_bounds(const AttnArgs& p, const ModArgs& m, int n, int t, int& a, int& b, int& pe) {
   const int d = find_doc(p.cu, n, t);
-  a = max(0, min(__ldg(p.cu + d), t));
-  b = min(p.BS, max(__ldg(p.cu + d + 1), t + 1));
+  a = max(0, min(gld(p.cu + d), t));
+  b = min(p.BS, max(gld(p.cu + d + 1), t + 1));
   pe = prefix_end(m, d, a, b, p.status);
 }
 
@@ -182,12 +182,12 @@ __device__ __forceinline__ void query_range(const AttnArgs& p, const M& m, int n
 
 // find_doc by a whole warp, for one token: 32 boundaries are looked at at once
 // instead of one after the other.
-__device__ __forceinline__ int find_doc_warp(const int32_t* __restrict__ cu, int n, int t) {
+__device__ __forceinline__ int find_doc_warp(const int32_t* cu, int n, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = n;  // cu[lo] <= t < cu[hi]
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const unsigned at_or_before = __ballot_sync(0xffffffffu, at < hi && __ldg(cu + at) <= t) | 1u;  // (cu[lo] <= t)
+    const unsigned at_or_before = __ballot_sync(0xffffffffu, at < hi && gld(cu + at) <= t) | 1u;  // (cu[lo] <= t)
     lo += (31 - __clz(at_or_before)) * step;
     hi = min(hi, lo + step);
   }
@@ -202,8 +202,8 @@ template <class M>
 __device__ __forceinline__ TileDocs tile_docs(const AttnArgs& p, const M& m, int n, int first, int last) {
   TileDocs w;
   w.d0 = find_doc_warp(p.cu, n, first);
-  w.a0 = max(0, min(__ldg(p.cu + w.d0), first));
-  w.b0 = min(p.BS, max(__ldg(p.cu + w.d0 + 1), first + 1));
+  w.a0 = max(0, min(gld(p.cu + w.d0), first));
+  w.b0 = min(p.BS, max(gld(p.cu + w.d0 + 1), first + 1));
   w.pe0 = prefix_end(m, w.d0, w.a0, w.b0, p.status);
   w.d1 = w.d0;
   w.a1 = w.a0;
@@ -211,8 +211,8 @@ __device__ __forceinline__ TileDocs tile_docs(const AttnArgs& p, const M& m, int
   w.pe1 = w.pe0;
   if (last >= w.b0) {
     w.d1 = find_doc_warp(p.cu, n, last);
-    w.a1 = max(0, min(__ldg(p.cu + w.d1), last));
-    w.b1 = min(p.BS, max(__ldg(p.cu + w.d1 + 1), last + 1));
+    w.a1 = max(0, min(gld(p.cu + w.d1), last));
+    w.b1 = min(p.BS, max(gld(p.cu + w.d1 + 1), last + 1));
     w.pe1 = prefix_end(m, w.d1, w.a1, w.b1, p.status);
   }
   return w;
@@ -224,10 +224,10 @@ __device__ __forceinline__ TileDocs tile_docs(const AttnArgs& p, const M& m, int
 template <class M>
 __device__ __forceinline__ bool checked_tile_docs(const AttnArgs& p, const M& m, int first, int last, int& n,
                                                   TileDocs& w) {
-  n = __ldg(p.n_docs);
+  n = gld(p.n_docs);
   bool ok = n >= 1 && n <= p.BS;
   if (ok) {
-    const int c0 = __ldg(p.cu), cn = __ldg(p.cu + n);
+    const int c0 = gld(p.cu), cn = gld(p.cu + n);
     w = tile_docs(p, m, n, first, last);
     ok = c0 == 0 && cn == p.BS;
   }
@@ -237,7 +237,7 @@ __device__ __forceinline__ bool checked_tile_docs(const AttnArgs& p, const M& m,
   }
   if (blockIdx.x == 0) {
     for (int d = threadIdx.x; d < n; d += blockDim.x)
-      if (__ldg(p.cu + d + 1) <= __ldg(p.cu + d)) set_status(p.status, USP_ERR_BAD_SEQLENS);
+      if (gld(p.cu + d + 1) <= gld(p.cu + d)) set_status(p.status, USP_ERR_BAD_SEQLENS);
   }
   return true;
 }
@@ -257,10 +257,10 @@ __device__ __forceinline__ void doc_bounds(const AttnArgs& p, const M& m, const 
     int lo = w.d0 + 1, hi = w.d1;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(p.cu + mid) <= t) lo = mid; else hi = mid;
+      if (gld(p.cu + mid) <= t) lo = mid; else hi = mid;
     }
-    a = max(0, min(__ldg(p.cu + lo), t));
-    b = min(p.BS, max(__ldg(p.cu + lo + 1), t + 1));
+    a = max(0, min(gld(p.cu + lo), t));
+    b = min(p.BS, max(gld(p.cu + lo + 1), t + 1));
     pe = prefix_end(m, lo, a, b, p.status);
   }
 }

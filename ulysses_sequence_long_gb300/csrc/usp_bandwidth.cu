@@ -60,7 +60,7 @@ constexpr int kRelayoutUnroll = 4;
 // least 128 bytes in every configuration this path is used with.  Towards the
 // head layout a replicated head is simply read by each of its replicas.
 template <bool kToHead>
-__device__ __forceinline__ void relayout_body(const int4* __restrict__ src, int4* __restrict__ dst,
+__device__ __forceinline__ void relayout_body(const int4* src, int4* __restrict__ dst,
                                               const RelayoutGeom& g, uint32_t first, uint32_t stride) {
   for (uint32_t base = first; base < g.n_vec; base += stride * kRelayoutUnroll) {
     int4 val[kRelayoutUnroll];
@@ -73,7 +73,7 @@ __device__ __forceinline__ void relayout_body(const int4* __restrict__ src, int4
         uint32_t run = g.run_vec.div(v);
         uint32_t k = v - run * g.run_vec.d;
         uint32_t srun = kToHead ? head_run_to_seq_run(g, run) : seq_run_to_head_run(g, run, 0);
-        val[u] = __ldg(src + static_cast<size_t>(srun) * g.run_vec.d + k);
+        val[u] = gld(src + static_cast<size_t>(srun) * g.run_vec.d + k);
       }
     }
 #pragma unroll
@@ -83,7 +83,7 @@ __device__ __forceinline__ void relayout_body(const int4* __restrict__ src, int4
 }
 
 template <bool kToHead>
-__global__ void __launch_bounds__(kRelayoutThreads) relayout_kernel(const int4* __restrict__ src,
+__global__ void __launch_bounds__(kRelayoutThreads) relayout_kernel(const int4* src,
                                                                     int4* __restrict__ dst, RelayoutGeom g) {
   grid_wait();
   relayout_body<kToHead>(src, dst, g, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kRelayoutThreads) relayout_kernel(const int4* 
 // Head layout -> seq layout when heads are replicated (bf16 only): the
 // exchange back sums the rep replicas of every head (the adjoint of the
 // replication), in fp32 in replica order, rounded once to bf16.
-__global__ void __launch_bounds__(kRelayoutThreads) relayout_reduce_kernel(const int4* __restrict__ src,
+__global__ void __launch_bounds__(kRelayoutThreads) relayout_reduce_kernel(const int4* src,
                                                                            int4* __restrict__ dst, RelayoutGeom g) {
   const uint32_t stride = gridDim.x * blockDim.x;
   grid_wait();
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kRelayoutThreads) relayout_reduce_kernel(const
     const uint32_t k = v - run * g.run_vec.d;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (uint32_t rr = 0; rr < g.rep_u; ++rr) {
-      const int4 x = __ldg(src + static_cast<size_t>(seq_run_to_head_run(g, run, rr)) * g.run_vec.d + k);
+      const int4 x = gld(src + static_cast<size_t>(seq_run_to_head_run(g, run, rr)) * g.run_vec.d + k);
       const uint32_t w[4] = {static_cast<uint32_t>(x.x), static_cast<uint32_t>(x.y), static_cast<uint32_t>(x.z),
                              static_cast<uint32_t>(x.w)};
 #pragma unroll
@@ -269,16 +269,16 @@ struct ScanWs {
   uint64_t* state;
 };
 
-__device__ __forceinline__ int load_pos(const int32_t* __restrict__ pos, const ScanGeom& g, int gi) {
-  if (g.P == 1 || g.B == 1) return __ldg(pos + gi);  // the shards already sit in gathered order
+__device__ __forceinline__ int load_pos(const int32_t* pos, const ScanGeom& g, int gi) {
+  if (g.P == 1 || g.B == 1) return gld(pos + gi);  // the shards already sit in gathered order
   int b = gi / g.S, s = gi - b * g.S;
   int r = s / g.Sl, sp = s - r * g.Sl;
-  return __ldg(pos + (static_cast<size_t>(r) * g.B + b) * g.Sl + sp);
+  return gld(pos + (static_cast<size_t>(r) * g.B + b) * g.Sl + sp);
 }
 
 // This thread's kScanItems positions starting at gathered index `first`:
 // start flags (bit i) and whether any position was negative.
-__device__ __forceinline__ uint32_t thread_flags(const int32_t* __restrict__ pos, const ScanGeom& g, int first,
+__device__ __forceinline__ uint32_t thread_flags(const int32_t* pos, const ScanGeom& g, int first,
                                                  bool& negative) {
   int v[kScanItems];
   if (g.vec && first + kScanItems <= g.total) {
@@ -291,7 +291,7 @@ __device__ __forceinline__ uint32_t thread_flags(const int32_t* __restrict__ pos
     const int4* p4 = reinterpret_cast<const int4*>(pos + at);
 #pragma unroll
     for (int k = 0; k < kScanItems / 4; ++k) {
-      const int4 x = __ldg(p4 + k);
+      const int4 x = gld(p4 + k);
       v[4 * k] = x.x;
       v[4 * k + 1] = x.y;
       v[4 * k + 2] = x.z;
@@ -324,7 +324,7 @@ __device__ __forceinline__ uint32_t thread_flags(const int32_t* __restrict__ pos
 // 32-position flag word w = 4k + L/8 is assembled from eight lanes' nibbles
 // by a segmented OR over shuffles; lane L ends up holding word (L % 8) * 4 +
 // L / 8 (returned, with that word's index in *wi).
-__device__ __forceinline__ uint32_t warp_flags(const int32_t* __restrict__ pos, const ScanGeom& g, int base,
+__device__ __forceinline__ uint32_t warp_flags(const int32_t* pos, const ScanGeom& g, int base,
                                                bool vec, int& wi, bool& negative) {
   const int lane = threadIdx.x & 31;
   int v[8][4];
@@ -337,7 +337,7 @@ __device__ __forceinline__ uint32_t warp_flags(const int32_t* __restrict__ pos, 
     const int4* p4 = reinterpret_cast<const int4*>(pos + at) + lane;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int4 x = __ldg(p4 + 32 * k);
+      const int4 x = gld(p4 + 32 * k);
       v[k][0] = x.x;
       v[k][1] = x.y;
       v[k][2] = x.z;
@@ -444,7 +444,7 @@ __device__ __forceinline__ void block_scan2(int c, int l, int& ex_c, int& ex_l, 
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const int32_t* __restrict__ pos, ScanGeom g, ScanWs ws,
+__global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const int32_t* pos, ScanGeom g, ScanWs ws,
                                                                int32_t* __restrict__ cu, int32_t* n_docs,
                                                                int32_t* max_len, int32_t* status) {
   extern __shared__ uint32_t flag_words[];  // min(range/32, kScanSmemWords)
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const int32_t* __
 // 10.4; 8192 tokens: 4.2 and 8.4).
 constexpr int kSmallAhead = 8;
 __global__ void __launch_bounds__(kScanThreads, 1)
-    scan_small_kernel(const int32_t* __restrict__ pos, int total, int B, int P, FastDiv S, FastDiv Sl,
+    scan_small_kernel(const int32_t* pos, int total, int B, int P, FastDiv S, FastDiv Sl,
                       int32_t* __restrict__ cu, int32_t* n_docs, int32_t* max_len, int32_t* status) {
   __shared__ uint32_t words[kScanThreads];
   __shared__ int sh_cnt[32], sh_last[32], sh_max[32];
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       v[e] = 1;
       if (gi < total) {
         const uint32_t r = Sl.div(s[e]);
-        v[e] = __ldg(pos + (gathered ? gi : (r * B + b) * Sl.d + (s[e] - r * Sl.d)));
+        v[e] = gld(pos + (gathered ? gi : (r * B + b) * Sl.d + (s[e] - r * Sl.d)));
       }
     }
 #pragma unroll

@@ -27,6 +27,14 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // kernel before it in the stream ends; grid_wait() returns once that one has ended and its
 // writes are visible.  Every thread calls it before it touches global memory.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A load of global memory in such a kernel: an ordinary one.  The read-only path (ld.global.nc,
+// which __ldg and const __restrict__ parameters give) is for memory that nothing writes while
+// the kernel lives; this kernel lives before grid_wait() returns, and loads of memory that is
+// taken for constant may be moved above it.
+template <class T>
+__device__ __forceinline__ T gld(const T* p) {
+  return *p;
+}
 
 __device__ __forceinline__ uint64_t global_ns() {
   uint64_t t;
