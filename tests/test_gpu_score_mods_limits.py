@@ -120,3 +120,42 @@ def test_threads_with_tables_of_different_reach():
     torch.cuda.synchronize()
     assert not failed, failed
     assert all(ua.read_status() == 0 for ua in layers)
+
+
+@pytest.mark.parametrize("D,causal", [(64, True), (128, True), (64, False)])
+def test_slopes_below_zero(D, causal):
+    """Slopes below 0 put the weights on the farthest keys, where the bias is largest.  An exponent carries, in units of
+    2^-24 |slope| d: the rounding of slope log2e, of its product with the distance, of their sum with the score's part,
+    and of the LSE and its product with log2e: 5 half steps, and 1.2e-5 of the rest (see test_gpu_score_mods).  With
+    P' = P (1 + e), |e| <= eps: |dX' - dX| <= eps P (|dP| + |D| + sum_u P |dP|)."""
+    w = _w("below_zero", S=1536, Hq=4, Hkv=2, D=D, P=2, causal=causal, doc_mode="explicit", doc_lens=(1400, 136))
+    t = W.qkv_do_shards(w)
+    pos = W.position_ids_shards(w)
+    slopes = np.array([-0.5, -2.0 ** -5, 2.0 ** -3, -0.125])
+    table = np.random.default_rng(2).standard_normal((4, 32)).astype(np.float32).astype(np.float64)
+    kw = dict(slopes=slopes, rel_bias=table, buckets=SM.rel_buckets_log(32, 128, not causal))
+    ua = _layer(w, kw)
+    _step(ua, t, pos)
+    host = {n: W.bf16_to_f64(x) for n, x in t.items()}
+    ref = SM.mod_layer(host["q"], host["k"], host["v"], pos, host["do"], causal=causal, **kw)
+    assert_close("o", _np(ua.o_seq), ref["o"])
+    assert_close("lse", _np(ua.lse), ref["lse"], bf16_out=False)
+    for n, x in (("dq", ua.dq_seq), ("dk", ua.dk_seq), ("dv", ua.dv_seq)):
+        assert_close(n, _np(x), ref[n], slack=ref[n + "_slack"])
+    flat = {n: np.moveaxis(x, 0, 1).reshape(w.S, -1, D) for n, x in host.items()}
+    lse = np.moveaxis(ref["lse"], 0, 1).reshape(4, w.S)
+    bound = np.zeros_like(table)
+    for h in range(4):
+        for a, b in ((0, 1400), (1400, 1536)):
+            at = np.arange(b - a)
+            dist = at[:, None] - at[None, :]
+            bucket = kw["buckets"][np.clip(dist, -128, 128) + 128]
+            x = flat["q"][a:b, h] @ flat["k"][a:b, h // 2].T / D ** 0.5 - slopes[h] * np.abs(dist) + table[h][bucket]
+            p = np.where((dist >= 0) | (not causal), np.exp(np.minimum(x - lse[h, a:b, None], 0.0)), 0.0)
+            dp = flat["do"][a:b, h] @ flat["v"][a:b, h // 2].T
+            eps = 5 * 2.0 ** -24 * abs(slopes[h]) * (b - a + 128) + 1.2e-5
+            some = p * (np.abs(dp) + np.abs((p * dp).sum(1))[:, None] + (p * np.abs(dp)).sum(1)[:, None])
+            bound[h] += eps * np.bincount(bucket.reshape(-1), some.reshape(-1), 32)
+    err = np.abs(_np(ua.drel_bias) - ref["drel_bias"])
+    print(f"[parity] drel_bias: worst error / bound {np.max(err / np.maximum(bound, 1e-30)):.3f}")
+    assert np.all(err <= bound)

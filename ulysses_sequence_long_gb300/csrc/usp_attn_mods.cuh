@@ -298,7 +298,9 @@ struct Affine {
 // Distances all beyond R cost nothing per element: their bias is one value and
 // goes into `off`.  `later_hidden`: keys after the query are masked anyway, so
 // their slope may have either sign.  `ramp`: slope2 * c for every column in shared
-// memory, or null (computed here).
+// memory, or null (computed here).  A slope's part is split at the block's first column,
+// -slope d0 + slope c, so it is rounded at the size of slope d0: for slopes >= 0 far keys, which
+// have no weight, carry that; for slopes below 0 the keys that have the weight do.
 template <int N>
 __device__ __forceinline__ Affine add_bias(float (&x)[N], const float* row, int R, float slope2, const float* ramp,
                                            int d0, int dmin, int dmax, bool later_hidden, float scale_log2) {
