@@ -403,9 +403,10 @@ typedef struct {
                                   2.5e-7 softcap and that of x. */
   const float* slopes;         /* device fp32 [Hq] (global heads), or NULL: no linear bias.  |slope| <= 2^10.
                                   The score of a key at distance d has fp32's error at the size of |slope| (d + 128):
-                                  up to 5 2^-24 |slope| (d + 128) in an exponent.  Where slopes are >= 0 (and no table hides
-                                  the near keys) a far key has no weight and only 128 slopes count; slopes below 0 put the weights on the farthest
-                                  keys (-0.5 over 32768 tokens: up to 5e-3 of a weight) */
+                                  up to 5 2^-24 |slope| (d + 128) in an exponent.  Where slopes are >= 0 (and no
+                                  table hides the near keys) a far key has no weight and only 128 slopes count;
+                                  slopes below 0 put the weights on the farthest keys (-0.5 over 32768 tokens: up
+                                  to 5e-3 of a weight) */
   const float* rel_bias;       /* device fp32 [Hq][n_buckets], or NULL: no learned bias.  At most 2^20; an entry
                                   below -2^20 (-inf, the lowest fp32 value) hides its keys (only without a cap):
                                   a row that then sees nothing has O = 0, LSE = -inf */

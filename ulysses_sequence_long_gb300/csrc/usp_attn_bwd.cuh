@@ -709,9 +709,11 @@ __global__ void __launch_bounds__(Team<M>::THREADS, 1)
             f = add_bias_of_key(x, tab, mods.R, slope2, !cap_on<M>, d0, dw - 31, dw + 31, mods.later_hidden,
                                 p.scale_log2);
           if constexpr (cap_on<M>) {
-            // (shorter polynomials, 4096 tokens at D = 128, cap 50: 153 -> 138 us; capped
-            // windows at D = 64, whose chunks rarely agree on one: 91 -> 105 us)
-            cap_scores<D == 128 ? 3 : 1>(x, f, mods.cap, true, lb + T_S + gc + 32 * c);
+            // One polynomial for all scores within the cap.  With the shorter ones for blocks of
+            // smaller scores (their deviation / the cap: 0.06, 0.1, 0.15, 0.5): 4096 tokens, 12
+            // heads of 128: 151, 151, 151, 203 us, with them 138, 153, 172, 213; windows of
+            // 128, D = 64: 91, 91, 91, 128 and 86, 93, 105, 134.
+            cap_scores<false>(x, f, mods.cap, true, lb + T_S + gc + 32 * c);
             cap_slope(x, gf);
             f = {mods.cap * kLog2E, 0.f};
           }
@@ -1119,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (bias_on<M>)
           f = add_bias(x, tab, mods.R, slope2, nullptr, d0, dw - 63, dw + 31, mods.later_hidden, p.scale_log2);
         if constexpr (cap_on<M>) {
-          cap_scores<1>(x, f, mods.cap, true, lb + s_col);
+          cap_scores<false>(x, f, mods.cap, true, lb + s_col);
           cap_slope(x, gf);
           f = {mods.cap * kLog2E, 0.f};
         }

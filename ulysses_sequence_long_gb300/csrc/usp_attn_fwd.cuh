@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, NH>::THREADS, Cfg<D, NQT>::CTAS)
         if constexpr (bias_on<M>)
           f = add_bias(s, tab, mods.R, slope2, ramp, d0, dw - (NC - 1), dw + 31, mods.later_hidden, sc);
         if constexpr (cap_on<M>) {
-          const float k = cap_scores<3>(s, f, mods.cap, bias_on<M>, s_tm + half * NC);
+          const float k = cap_scores<true>(s, f, mods.cap, bias_on<M>, s_tm + half * NC);
           f = {k * mods.cap * kLog2E, 0.f};
         }
         sc = f.sc;

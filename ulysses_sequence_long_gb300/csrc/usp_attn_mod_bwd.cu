@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(CfgD<D, kDeltaGroups<M>>::THREADS, 1)
         if constexpr (bias_on<M>)
           f = add_bias(x, tab, mods.R, slope2, nullptr, d0, dw - (NC - 1), dw + 31, mods.later_hidden, p.scale_log2);
         if constexpr (cap_on<M>) {
-          cap_scores<1>(x, f, mods.cap, true, lb + T_SCRATCH + grp * NC);
+          cap_scores<false>(x, f, mods.cap, true, lb + T_SCRATCH + grp * NC);
           f = {mods.cap * kLog2E, 0.f};
         }
         const int c_lo = w.vlo - k0, c_hi = w.vhi - k0;

@@ -491,14 +491,16 @@ __device__ __forceinline__ void tanh_poly(float (&x)[N], float k) {
 
 // x -> w = tanh(y) / k in place, y = x2 ln2 / cap, x2 = x f.sc + f.off, and returns
 // k: the capped score in the log2 domain is then w k cap log2e, and tanh is w k.
-// The kernels are bound by the packed fp32 operations of a score, so a warp takes
-// the shortest polynomial that its largest |y| allows (forward, 8192 packed
-// tokens, D = 128, cap 30: 225 us, and 241 with degree 6 alone).
+// SHORT (the forward): a warp takes the shortest polynomial that its largest |y|
+// allows.  Causal rows of 4096, 8192 tokens, 32 heads of 128, scores' deviation / the
+// cap of 0.06, 0.1, 0.15, 0.5: 294, 316, 341, 563 us, and 322, 322, 322, 568 with
+// degree 6 alone; the same order at D = 64 and in windows.  (0.5 and more: every
+// block has scores beyond the cap, tanh_rare.)  The backward takes degree 6 alone.
 // `tmem`: N columns of this warp's lanes, free to write.
-template <int TIERS, int N>
+template <bool SHORT, int N>
 __device__ __forceinline__ float cap_scores(float (&x)[N], Affine f, float cap, bool biased, uint32_t tmem) {
   float k = fminf(f.sc * (0.6931471805599453f / cap), FLT_MAX);
-  if (TIERS != 3 || biased || k < 0x1p-9f || k > 0x1p9f) {
+  if (!SHORT || biased || k < 0x1p-9f || k > 0x1p9f) {
     // to y itself: the offset of a bias, or a k whose powers (up to k^12) would leave fp32
     const float ko = f.off * (0.6931471805599453f / cap);
     const uint64_t k2 = f2_pack(k, k), o2 = f2_pack(ko, ko);
@@ -515,9 +517,9 @@ __device__ __forceinline__ float cap_scores(float (&x)[N], Affine f, float cap, 
   for (int c = 0; c < N; c += 2) top4[(c >> 1) & 3] = fmax3(top4[(c >> 1) & 3], fabsf(x[c]), fabsf(x[c + 1]));
   // (the max skips a NaN, which every path keeps)
   const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * k;
-  if (TIERS > 1 && !__any_sync(0xffffffffu, top > 0.25f)) {
+  if (SHORT && !__any_sync(0xffffffffu, top > 0.25f)) {
     tanh_poly<2>(x, k);
-  } else if (TIERS > 2 && !__any_sync(0xffffffffu, top > 0.5f)) {
+  } else if (SHORT && !__any_sync(0xffffffffu, top > 0.5f)) {
     tanh_poly<4>(x, k);
   } else if (!__any_sync(0xffffffffu, top > 1.f)) {
     tanh_poly<6>(x, k);
