@@ -173,3 +173,18 @@ def test_a_layer_frees_its_buffers_when_it_is_dropped():
         assert gone() is None
     finally:
         gc.enable()
+
+
+def test_two_layers_at_once_on_two_streams():
+    """Steps of two layers queued in turn on two streams, nothing waiting for anything: each gives what it gives alone."""
+    one, d1 = _make(2, True, True)
+    two, d2 = _make(1, None, True)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for ua, d, st in ((one, d1, streams[0]), (two, d2, streams[1])):
+            ua.forward(d["q"], d["k"], d["v"], d["pos"], d["sinks"], stream=st)
+            ua.backward(d["do"], d["sinks"], stream=st)
+    for ua, want in ((one, _expected(2, True, True)), (two, _expected(1, None, True))):
+        for a, b in zip(_results(ua), want):
+            assert torch.equal(a, b)

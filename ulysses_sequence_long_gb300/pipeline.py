@@ -286,7 +286,7 @@ class UlyssesAttention:
 
     def _on_device(self, step, *args, stream=None):
         """step(*args, stream's handle) with the layer's device current."""
-        if torch.cuda.current_device() == self._index:
+        if torch._C._cuda_getDevice() == self._index:
             return step(*args, self._handle(stream))
         with torch.cuda.device(self._index):
             return step(*args, self._handle(stream))
