@@ -462,6 +462,7 @@ size_t usp_attn_mod_bwd_fast_workspace_bytes(const usp_attn_params* params, cons
  * taken from the bf16 o, or, where a gradient in fp32 would show its rounding
  * (rel_bias_grad, or dsinks with sinks), as sum_u P_tu (dO_t . v_u) in fp32 by a
  * pass of its own over the scores.  drel_bias: fp32 [Hq][n_buckets], given exactly when mods->rel_bias_grad.
+ * Every element of q, k, v and dO must be finite (see the forward).
  * Deterministic.  A workspace belongs to one call at a time: backward calls that
  * may overlap (other streams, graphs launched at once) need one each.
  * Errors: as usp_attn_mod_fwd and usp_attn_bwd. */

@@ -413,8 +413,8 @@ struct Grads {
 // (8192 packed tokens, D = 128: learned bias 361 -> 302 us, slopes 352 -> 295 us; 289
 // and 278 with the diagonal sums folded).
 // Without one the chain is short enough that the fewer registers of 16 warps cost
-// as much as they gain (prefix 209 us with two groups, 214 with four; a cap 356
-// and 348, but a cap over short windows at D = 64 96 and 104).
+// as much as they gain (prefix 209 us with two groups, 214 with four; a cap 355
+// and 371, over short windows at D = 64 92 and 107).
 template <class M>
 struct Team {
   static constexpr int NG = bias_on<M> ? kModGroups : 2;

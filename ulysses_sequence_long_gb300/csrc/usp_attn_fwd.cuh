@@ -108,8 +108,8 @@ struct Out {
 };
 
 // Halves of a row's keys (see Cfg) where there are tiles enough for CTAs of two.  A cap lengthens a row's chain from S to P, and 8
-// softmax warps do not hide it (8192 packed tokens, D = 128: 225 us with whole rows,
-// 208 with halves).  Without one the exchange of the row's maximum costs more than
+// softmax warps do not hide it (8192 packed tokens, D = 128: 214 us with whole rows,
+// 192 with halves).  Without one the exchange of the row's maximum costs more than
 // the shorter chain gains (prefix 123 and 127 us, slopes 211 and 219).
 template <class M>
 constexpr int kHalves = 1;
