@@ -168,6 +168,9 @@ def test_a_layer_frees_its_buffers_when_it_is_dropped():
     torch.cuda.synchronize()
     gc.disable()
     try:
+        gone = weakref.ref(ua.dv_seq)
+        ua.dv_seq = torch.empty_like(ua.dv_seq)     # the replaced one is not kept
+        assert gone() is None
         gone = weakref.ref(ua.o_seq)
         del ua
         assert gone() is None

@@ -251,7 +251,7 @@ class UlyssesAttention:
     # -- a layer with modified scores: its calls take the addresses of their tensors, and check them, each time ----
     def _remember(self, name):
         t = getattr(self, name)
-        self._seen[name] = (t, t.data_ptr(), t.dtype, t.numel())
+        self._seen[name] = (t.data_ptr(), t.dtype, t.numel())   # (no reference: a dropped buffer is freed)
 
     def _at(self, t, name, dtype, n):
         """The address that ``t`` has now."""
@@ -268,10 +268,11 @@ class UlyssesAttention:
         mine, seen, out = self.__dict__, self._seen, []
         for name in names:
             t = mine[name]
-            was, at, dtype, n = seen[name]
-            if not (t is was and t.data_ptr() == at and t.dtype is dtype and t.numel() == n and t.is_contiguous()):
+            at, dtype, n = seen[name]
+            if not (isinstance(t, torch.Tensor) and t.data_ptr() == at and t.dtype is dtype and t.numel() == n
+                    and t.is_contiguous()):
                 at = self._at(t, name, dtype, n)
-                seen[name] = (t, at, dtype, n)
+                seen[name] = (at, dtype, n)
             out.append(at)
         return out
 
