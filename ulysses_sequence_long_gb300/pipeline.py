@@ -269,8 +269,7 @@ class UlyssesAttention:
         for name in names:
             t = mine[name]
             at, dtype, n = seen[name]
-            if not (isinstance(t, torch.Tensor) and t.data_ptr() == at and t.dtype is dtype and t.numel() == n
-                    and t.is_contiguous()):
+            if not (t.data_ptr() == at and t.dtype is dtype and t.numel() == n and t.is_contiguous()):
                 at = self._at(t, name, dtype, n)
                 seen[name] = (at, dtype, n)
             out.append(at)
@@ -352,17 +351,18 @@ class UlyssesAttention:
             io = B_.USP_IO_SEQ_KV_HEAD
             k, v = self._own("k_head", "v_head")
         self._mod_call("usp_attn_mod_fwd", io, (0, 0), (cu, n_docs), sinks, q, k, v, o, lse, status, stream)
+        return o
 
-    def _mod_exchange_out(self, stream):
-        if not self._in_place:
-            s = self.shape
-            self._launch("usp_relayout_bwd", *self._own("o_head", "o_seq"), s.B, s.S, s.Hq, s.D, s.P, 2, stream)
+    def _mod_exchange_out(self, o, stream):
+        s = self.shape
+        self._launch("usp_relayout_bwd", o, *self._own("o_seq"), s.B, s.S, s.Hq, s.D, s.P, 2, stream)
 
     def _mod_forward(self, q_seq, k_seq, v_seq, pos_shards, sinks, stream):
         inputs = self._mod_exchange(q_seq, k_seq, v_seq, stream)
         docs = self._mod_boundaries(pos_shards, stream)
-        self._mod_attention(inputs, docs, sinks, stream)
-        self._mod_exchange_out(stream)
+        o = self._mod_attention(inputs, docs, sinks, stream)
+        if not self._in_place:
+            self._mod_exchange_out(o, stream)
         return self.o_seq
 
     def _mod_backward(self, do_seq, sinks, marks, group_marks, stream):
@@ -450,7 +450,8 @@ class UlyssesAttention:
     def exchange_out(self, stream=None):
         s = self.shape
         if self._mods is not None:
-            self._on_device(self._mod_exchange_out, stream=stream)
+            if not self._in_place:
+                self._on_device(self._mod_exchange_out, *self._own("o_head"), stream=stream)
         elif not self.fused:
             B_.usp_relayout_bwd(self.o_head, self.o_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
 
