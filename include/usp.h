@@ -69,8 +69,11 @@ typedef enum {
   USP_ERR_TIMEOUT = 7,       /* device: a bounded wait inside a kernel gave up */
   USP_ERR_CUDA = 8,          /* a CUDA runtime/driver call or launch failed */
   USP_ERR_WORKSPACE = 9,     /* workspace pointer null/misaligned or smaller than required */
-  USP_ERR_BAD_MODS = 10      /* device: a bucket id outside [0, n_buckets), a negative prefix length, or
+  USP_ERR_BAD_MODS = 10,     /* device: a bucket id outside [0, n_buckets), a negative prefix length, or
                                 fewer prefix lengths than documents */
+  USP_ERR_BAD_ROPE = 11,     /* device: an axis outside [0, n_axes), or a frequency that is not finite or above 1024 */
+  USP_ERR_BAD_PAGES = 12     /* device: a page outside the pool, a length outside the block table, or boundaries of
+                                appended tokens that do not fit their number or their sequences' lengths */
 } usp_status;
 
 /* Static, human-readable name of a status code.  Never NULL. */
@@ -486,6 +489,101 @@ int usp_attn_mod_bwd_dq(const usp_attn_params* params, const usp_score_mods* mod
                         usp_stream_t stream);
 int usp_attn_mod_bwd_rel_bias(const usp_attn_params* params, const usp_score_mods* mods, float* drel_bias, void* ws,
                               size_t ws_bytes, usp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions of one or several axes (a text's position; height and width;
+ * time, height and width), for q and k in one launch.  Pair i of a head turns by
+ * the angle w = positions[axes[i]][t] * freqs[i]:
+ *     y1 = x1 cos w - x2 sin w,  y2 = x1 sin w + x2 cos w
+ * with (x1, x2) = elements (i, i + n_pairs), or (2i, 2i + 1) when interleaved; the
+ * elements behind the 2 n_pairs turned ones pass through.  The layer applies it
+ * to the sequence shards before the exchange, a decoding step to the new tokens.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int tokens;               /* tokens of q and k, in any order: q is [tokens][Hq][D] */
+  int Hq, Hkv, D;           /* D 64 or 128; Hkv 0: no k */
+  int n_axes;               /* 1 .. 8 */
+  int n_pos;                /* divides tokens: token t has the position t mod n_pos (the ranks of a head layout
+                               hold the same tokens) */
+  int n_pairs;              /* a multiple of 8, 8 .. D/2 */
+  int interleaved;
+  const int32_t* positions; /* device int32 [n_axes][n_pos]; negative ones turn backwards */
+  const float* freqs;       /* device fp32 [n_pairs], radians per position, |f| <= 1024 */
+  const int32_t* axes;      /* device int32 [n_pairs], or NULL: axis 0 */
+} usp_rope_params;
+
+/* q, q_out: bf16 [tokens][Hq][D]; k, k_out: bf16 [tokens][Hkv][D] (NULL with Hkv 0).  An output may be its input
+ * (in place), else buffers must not overlap.  usp_rope_bwd takes the gradients of q_out and k_out to those of q
+ * and k: it turns back by the same angles.  The angle is taken modulo a turn in 64-bit fixed point: it is within
+ * 2e-7 (5e-7 for |f| > 1) at any int32 position.  The turned values are rounded once.
+ * dev_status: USP_ERR_BAD_ROPE (such pairs turn by 0).
+ * Errors: USP_ERR_INVALID_ARG, USP_ERR_INDIVISIBLE (tokens % n_pos), USP_ERR_UNSUPPORTED (D, n_pairs, n_axes > 8,
+ * Hq + Hkv > 4096, tokens >= 2^30, tokens (Hq + Hkv) >= 2^34), USP_ERR_ALIGNMENT, USP_ERR_CUDA. */
+int usp_rope_fwd(const usp_rope_params* params, const void* q, const void* k, void* q_out, void* k_out,
+                 int32_t* dev_status, usp_stream_t stream);
+int usp_rope_bwd(const usp_rope_params* params, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                 int32_t* dev_status, usp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A key/value cache in pages, per rank the heads that the rank holds.  Position t
+ * of sequence s is token t % page_size of page block_table[s][t / page_size].  The
+ * heads of a rank are those of the head layout: Hkv/P of them, or with Hkv < P the
+ * one head r / (P/Hkv) on rank r.
+ * With dtype USP_CACHE_E4M3 a token's head has a power of two 2^e, the smallest
+ * with e >= -126 for which every |x| <= 448 2^e (an infinity counts as the largest
+ * finite bf16), stored as the byte e + 127, and its elements are x / 2^e rounded to
+ * the nearest e4m3 value (ties to even).  NaN stays NaN.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int P, Hkv, D;              /* global key/value heads; D 64 or 128 */
+  int n_pages, page_size;     /* page_size a multiple of 16 */
+  int n_seqs, max_pages;      /* the block table's sides */
+  int dtype;                  /* USP_CACHE_BF16 or USP_CACHE_E4M3 */
+  void* k_pages;              /* [P][n_pages][hk][page_size][D], bf16 or e4m3 */
+  void* v_pages;
+  uint8_t* k_scales;          /* [P][n_pages][hk][page_size], e4m3 only (else NULL) */
+  uint8_t* v_scales;
+  const int32_t* block_table; /* device int32 [n_seqs][max_pages]; entries behind a sequence's last page are not read */
+  const int32_t* lens;        /* device int32 [n_seqs]: tokens of each sequence, appended ones included */
+} usp_paged_cache;
+
+enum { USP_CACHE_BF16 = 0, USP_CACHE_E4M3 = 1 };
+
+/* Writes `tokens` new tokens, k and v bf16 [P][tokens][hk][D] (the head layout), as the last ones of their
+ * sequences: with cu_seqlens (device int32 [n_seqs+1], e.g. a packed prompt's document boundaries) tokens
+ * [cu[s], cu[s+1]) end at position lens[s]; a sequence may have none, and tokens behind cu[n_seqs] are not
+ * written.  cu_seqlens NULL: one token each (tokens <= n_seqs: sequence s gets token s; a sequence of length 0,
+ * an empty place of a padded batch, is passed over).  Nothing else in the pool changes.  Pages that two
+ * sequences share may be read by both but not written in one call.
+ * usp_cache_read is the way back: the same tokens out of the cache into k and v, rounded to bf16 (exact for a
+ * bf16 cache; e4m3 values times their power of two are rounded only below bf16's normal range).  Tokens that
+ * are not described (behind cu[n_seqs], or of an empty place) are left as they were.
+ * Either of k and v may be NULL, when it is not wanted.
+ * dev_status: USP_ERR_BAD_PAGES; tokens without a place in the pool are passed over.
+ * Errors: USP_ERR_INVALID_ARG, USP_ERR_INDIVISIBLE, USP_ERR_UNSUPPORTED (D, page_size, dtype; sizes past 2^30
+ * tokens or 2^40 elements), USP_ERR_ALIGNMENT, USP_ERR_CUDA. */
+int usp_cache_append(const usp_paged_cache* cache, const void* k, const void* v, int tokens,
+                     const int32_t* cu_seqlens, int32_t* dev_status, usp_stream_t stream);
+int usp_cache_read(const usp_paged_cache* cache, void* k, void* v, int tokens, const int32_t* cu_seqlens,
+                   int32_t* dev_status, usp_stream_t stream);
+
+/* Attention of one new token per sequence over the cache (which already holds it: the query is at position
+ * lens[s] - 1).  Query head j of a rank reads its key/value head j / (Hq/P / hk):
+ *     s_u = softmax_scale q.k_u for u < lens[s], and lens[s] - 1 - u <= window_left with a window
+ *     LSE = ln( sum_u exp(s_u) + exp(sink) ),  O = sum_u exp(s_u - LSE) v_u
+ * O = 0 where nothing is visible (LSE = -inf, or the sink).
+ * q, o: bf16 [P][n_seqs][Hq/P][D]; lse: fp32 [P][n_seqs][Hq/P]; sinks: fp32 [Hq] or NULL.
+ * The work of all sequences is dealt out evenly in pieces of 64 positions, whatever their lengths, and pieces
+ * of one sequence are joined in the order of their positions: the result does not depend on timing.
+ * ws: usp_attn_decode_workspace_bytes bytes, 256-byte aligned, contents on entry do not matter; it belongs to one
+ * call at a time (calls that may overlap need one each).
+ * dev_status: USP_ERR_BAD_PAGES (the sequence's outputs are then unspecified; nothing outside the pool is read).
+ * Errors: USP_ERR_INVALID_ARG, USP_ERR_INDIVISIBLE, USP_ERR_UNSUPPORTED (as the cache; window_left < -1, Hq > 1024),
+ * USP_ERR_ALIGNMENT, USP_ERR_WORKSPACE, USP_ERR_CUDA. */
+size_t usp_attn_decode_workspace_bytes(const usp_paged_cache* cache, int Hq);
+int usp_attn_decode(const usp_paged_cache* cache, int Hq, int window_left, float softmax_scale, const float* sinks,
+                    const void* q, void* o, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                    usp_stream_t stream);
 
 #ifdef __cplusplus
 }

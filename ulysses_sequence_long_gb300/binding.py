@@ -28,6 +28,8 @@ USP_ERR_TIMEOUT = 7
 USP_ERR_CUDA = 8
 USP_ERR_WORKSPACE = 9
 USP_ERR_BAD_MODS = 10
+USP_ERR_BAD_ROPE = 11
+USP_ERR_BAD_PAGES = 12
 
 EXPORTED = [
     "usp_status_string", "usp_version",
@@ -43,6 +45,8 @@ EXPORTED = [
     "usp_rel_buckets_log", "usp_attn_mod_fwd", "usp_attn_mod_bwd_workspace_bytes",
     "usp_attn_mod_bwd_fast_workspace_bytes", "usp_attn_mod_bwd", "usp_attn_mod_bwd_preprocess",
     "usp_attn_mod_bwd_dkdv", "usp_attn_mod_bwd_dq", "usp_attn_mod_bwd_rel_bias",
+    "usp_rope_fwd", "usp_rope_bwd", "usp_cache_append", "usp_cache_read",
+    "usp_attn_decode_workspace_bytes", "usp_attn_decode",
 ]
 
 USP_RING_FIRST = 1
@@ -88,6 +92,28 @@ class ScoreModsStruct(ctypes.Structure):
                 raise ValueError(f"{field} has changed its size, strides or device")
             setattr(self, field, t.data_ptr())
 
+
+class RopeParams(ctypes.Structure):
+    """usp_rope_params (include/usp.h)."""
+    _fields_ = [
+        ("tokens", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("n_axes", ctypes.c_int), ("n_pos", ctypes.c_int), ("n_pairs", ctypes.c_int), ("interleaved", ctypes.c_int),
+        ("positions", ctypes.c_void_p), ("freqs", ctypes.c_void_p), ("axes", ctypes.c_void_p),
+    ]
+
+
+class PagedCacheStruct(ctypes.Structure):
+    """usp_paged_cache (include/usp.h)."""
+    _fields_ = [
+        ("P", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("n_pages", ctypes.c_int),
+        ("page_size", ctypes.c_int), ("n_seqs", ctypes.c_int), ("max_pages", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+    ]
+
+
+USP_CACHE_BF16 = 0
+USP_CACHE_E4M3 = 1
 
 USP_IO_HEAD = 0
 USP_IO_SEQ = 1
@@ -145,6 +171,16 @@ def load() -> ctypes.CDLL:
     L.usp_attn_mod_bwd_dkdv.argtypes = [prm, mods] + [vp] * 7 + [sz, vp, vp]
     L.usp_attn_mod_bwd_dq.argtypes = [prm, mods] + [vp] * 6 + [sz, vp, vp]
     L.usp_attn_mod_bwd_rel_bias.argtypes = [prm, mods, vp, vp, sz, vp]
+    for name in ("usp_rope_fwd", "usp_rope_bwd"):
+        getattr(L, name).argtypes = [ctypes.POINTER(RopeParams)] + [vp] * 6
+    cache = ctypes.POINTER(PagedCacheStruct)
+    for name in ("usp_cache_append", "usp_cache_read"):
+        getattr(L, name).argtypes = [cache, vp, vp, i32, vp, vp, vp]
+    L.usp_attn_decode_workspace_bytes.restype = sz
+    L.usp_attn_decode_workspace_bytes.argtypes = [cache, i32]
+    L.usp_attn_decode.argtypes = [cache, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, sz, vp, vp]
+    for name in ("usp_rope_fwd", "usp_rope_bwd", "usp_cache_append", "usp_cache_read", "usp_attn_decode"):
+        getattr(L, name).restype = i32
     for name in ("usp_rel_buckets_log", "usp_attn_mod_fwd", "usp_attn_mod_bwd", "usp_attn_mod_bwd_preprocess",
                  "usp_attn_mod_bwd_dkdv", "usp_attn_mod_bwd_dq", "usp_attn_mod_bwd_rel_bias"):
         getattr(L, name).restype = i32
@@ -482,3 +518,109 @@ def usp_attn_mod_bwd_rel_bias(params: AttnParams, mods: ScoreModsStruct, drel_bi
     c = _Call(params, mods, stream)
     c.run("usp_attn_mod_bwd_rel_bias", c(drel_bias, "drel_bias", _F32, "rel"), c(ws, "ws", None, None),
           ws.numel() * ws.element_size())
+
+
+# -- rotary positions, the paged cache and single tokens -----------------------
+def _sized(t, name, dtype, n, like):
+    """_dev, with its number of elements and its device checked (nothing else of a tensor tells the library its size)."""
+    ptr = _dev(t, name, dtype)
+    if ptr is None:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, other tensors of the call on {like.device}")
+    return ptr
+
+
+def call_on(device: torch.device, stream, where, *args):
+    """``where(*args, stream)`` with `device` current, on `stream` or the device's current one."""
+    index = device.index
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        stream = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    fn = getattr(_lib or load(), where)
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, stream)
+    if rc != USP_OK:
+        raise UspError(rc, where)
+
+
+def rope_params(Hq, Hkv, D, positions, freqs, tokens, n_axes=1, axes=None, interleaved=False) -> RopeParams:
+    """usp_rope_params from tensors: positions int32 [n_axes][n_pos], freqs fp32 [n_pairs], axes int32 [n_pairs]."""
+    if positions.numel() % n_axes != 0:
+        raise ValueError(f"positions must be [{n_axes}][n_pos], got {positions.numel()} elements")
+    if axes is not None and axes.numel() != freqs.numel():
+        raise ValueError(f"axes must have an entry for each of the {freqs.numel()} frequencies")
+    return RopeParams(tokens, Hq, Hkv, D, n_axes, positions.numel() // n_axes, freqs.numel(), 1 if interleaved else 0,
+                      _dev(positions, "positions", _I32), _dev(freqs, "freqs", _F32), _dev(axes, "axes", _I32))
+
+
+def _rope(where, params, x, y, names, dev_status, stream):
+    n = (params.tokens * params.Hq * params.D, params.tokens * params.Hkv * params.D)
+    ptrs = [None if t is None else _sized(t, name, _BF, n[i % 2], x[0])
+            for i, (t, name) in enumerate(zip(x + y, names))]
+    call_on(x[0].device, stream, where, ctypes.byref(params), *ptrs, _dev(dev_status, "dev_status", _I32))
+
+
+def usp_rope_fwd(params: RopeParams, q, k, q_out, k_out, dev_status=None, stream=None):
+    _rope("usp_rope_fwd", params, (q, k), (q_out, k_out), ("q", "k", "q_out", "k_out"), dev_status, stream)
+
+
+def usp_rope_bwd(params: RopeParams, dq_out, dk_out, dq, dk, dev_status=None, stream=None):
+    _rope("usp_rope_bwd", params, (dq_out, dk_out), (dq, dk), ("dq_out", "dk_out", "dq", "dk"), dev_status, stream)
+
+
+def paged_cache(Hkv, D, P, k_pages, v_pages, block_table, lens, k_scales=None, v_scales=None) -> PagedCacheStruct:
+    """usp_paged_cache from tensors: pages [P][n_pages][hk][page_size][D] of bf16, or of float8_e4m3fn with scales
+    uint8 [P][n_pages][hk][page_size]; block_table int32 [n_seqs][max_pages], lens int32 [n_seqs]."""
+    if k_pages.dim() != 5 or k_pages.shape[0] != P or k_pages.shape[2] != (Hkv // P if Hkv >= P else 1) or k_pages.shape[4] != D:
+        raise ValueError(f"pages must be [P][n_pages][heads of a rank][page_size][D], got {tuple(k_pages.shape)}")
+    if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"pages must be torch.bfloat16 or torch.float8_e4m3fn, got {k_pages.dtype}")
+    if block_table.dim() != 2 or lens.dim() != 1:
+        raise ValueError("block_table must be [n_seqs][max_pages], lens [n_seqs]")
+    eight = k_pages.dtype is torch.float8_e4m3fn
+    if eight != (k_scales is not None) or eight != (v_scales is not None):
+        raise ValueError("k_scales and v_scales belong to e4m3 pages")
+    n = k_pages.numel()
+    kp, vp = _dev(k_pages, "k_pages"), _sized(v_pages, "v_pages", k_pages.dtype, n, k_pages)
+    ks = _sized(k_scales, "k_scales", torch.uint8, n // D, k_pages) if eight else None
+    vs = _sized(v_scales, "v_scales", torch.uint8, n // D, k_pages) if eight else None
+    return PagedCacheStruct(P, Hkv, D, k_pages.shape[1], k_pages.shape[3], lens.numel(), block_table.shape[1],
+                            USP_CACHE_E4M3 if eight else USP_CACHE_BF16, kp, vp, ks, vs,
+                            _sized(block_table, "block_table", _I32, lens.numel() * block_table.shape[1], k_pages),
+                            _sized(lens, "lens", _I32, lens.numel(), k_pages))
+
+
+def _cache_move(where, cache, k, v, tokens, cu_seqlens, dev_status, stream):
+    like = k if k is not None else v
+    n = cache.P * tokens * (cache.Hkv // cache.P if cache.Hkv >= cache.P else 1) * cache.D
+    kp, vp = (None if t is None else _sized(t, name, _BF, n, like) for t, name in ((k, "k"), (v, "v")))
+    cu = None if cu_seqlens is None else _sized(cu_seqlens[:cache.n_seqs + 1], "cu_seqlens", _I32, cache.n_seqs + 1, like)
+    call_on(like.device, stream, where, ctypes.byref(cache), kp, vp, tokens, cu, _dev(dev_status, "dev_status", _I32))
+
+
+def usp_cache_append(cache: PagedCacheStruct, k, v, tokens, cu_seqlens=None, dev_status=None, stream=None):
+    _cache_move("usp_cache_append", cache, k, v, tokens, cu_seqlens, dev_status, stream)
+
+
+def usp_cache_read(cache: PagedCacheStruct, k, v, tokens, cu_seqlens=None, dev_status=None, stream=None):
+    _cache_move("usp_cache_read", cache, k, v, tokens, cu_seqlens, dev_status, stream)
+
+
+def usp_attn_decode_workspace_bytes(cache: PagedCacheStruct, Hq: int) -> int:
+    return int(load().usp_attn_decode_workspace_bytes(ctypes.byref(cache), Hq))
+
+
+def usp_attn_decode(cache: PagedCacheStruct, Hq, q, o, lse, ws, window_left=-1, softmax_scale=0.0, sinks=None,
+                    dev_status=None, stream=None):
+    rows = cache.n_seqs * Hq
+    call_on(q.device, stream, "usp_attn_decode", ctypes.byref(cache), Hq, window_left, softmax_scale,
+            None if sinks is None else _sized(sinks, "sinks", _F32, Hq, q), _sized(q, "q", _BF, rows * cache.D, q),
+            _sized(o, "o", _BF, rows * cache.D, q), _sized(lse, "lse", _F32, rows, q), _dev(ws, "ws"),
+            ws.numel() * ws.element_size(), _dev(dev_status, "dev_status", _I32))

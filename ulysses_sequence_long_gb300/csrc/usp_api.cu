@@ -242,6 +242,77 @@ int check_mod_bwd(const usp_attn_params* p, const usp_score_mods* m, usp_attn_pa
   return USP_OK;
 }
 
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const char *pa = static_cast<const char*>(a), *pb = static_cast<const char*>(b);
+  return pa < pb + nb && pb < pa + na;
+}
+
+int check_rope(const usp_rope_params* p, const void* q, const void* k, const void* q_out, const void* k_out) {
+  if (p == nullptr || q == nullptr || q_out == nullptr) return USP_ERR_INVALID_ARG;
+  if (p->tokens <= 0 || p->Hq <= 0 || p->Hkv < 0 || p->n_axes <= 0 || p->n_pos <= 0 || p->n_pairs <= 0)
+    return USP_ERR_INVALID_ARG;
+  if (p->interleaved != 0 && p->interleaved != 1) return USP_ERR_INVALID_ARG;
+  if (p->positions == nullptr || p->freqs == nullptr) return USP_ERR_INVALID_ARG;
+  if ((p->Hkv > 0) != (k != nullptr) || (p->Hkv > 0) != (k_out != nullptr)) return USP_ERR_INVALID_ARG;
+  if (p->tokens % p->n_pos != 0) return USP_ERR_INDIVISIBLE;
+  if (p->D != 64 && p->D != 128) return USP_ERR_UNSUPPORTED;
+  if (p->n_pairs % 8 != 0 || p->n_pairs > p->D / 2 || p->n_axes > 8) return USP_ERR_UNSUPPORTED;
+  const int64_t H = static_cast<int64_t>(p->Hq) + p->Hkv;
+  if (H > 4096 || p->tokens >= (1 << 30) || p->tokens * H >= (1ll << 34)) return USP_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return USP_ERR_ALIGNMENT;
+  if (!aligned4(p->positions) || !aligned4(p->freqs) || !aligned4(p->axes)) return USP_ERR_ALIGNMENT;
+  const uint64_t row = 2ull * p->D * p->tokens, nq = row * p->Hq, nk = row * p->Hkv;
+  if ((q_out != q && overlap(q_out, nq, q, nq)) || (p->Hkv > 0 && k_out != k && overlap(k_out, nk, k, nk)))
+    return USP_ERR_INVALID_ARG;
+  if (p->Hkv > 0 && (overlap(q_out, nq, k, nk) || overlap(k_out, nk, q, nq) || overlap(q_out, nq, k_out, nk)))
+    return USP_ERR_INVALID_ARG;
+  return USP_OK;
+}
+
+int check_cache(const usp_paged_cache* c) {
+  if (c == nullptr) return USP_ERR_INVALID_ARG;
+  if (c->P <= 0 || c->Hkv <= 0 || c->D <= 0 || c->n_pages <= 0 || c->page_size <= 0 || c->n_seqs <= 0 ||
+      c->max_pages <= 0)
+    return USP_ERR_INVALID_ARG;
+  if (c->dtype != USP_CACHE_BF16 && c->dtype != USP_CACHE_E4M3) return USP_ERR_INVALID_ARG;
+  const bool e4m3 = c->dtype == USP_CACHE_E4M3;
+  if (c->k_pages == nullptr || c->v_pages == nullptr || c->block_table == nullptr || c->lens == nullptr)
+    return USP_ERR_INVALID_ARG;
+  if (e4m3 != (c->k_scales != nullptr) || e4m3 != (c->v_scales != nullptr)) return USP_ERR_INVALID_ARG;
+  if (c->Hkv >= c->P ? c->Hkv % c->P != 0 : c->P % c->Hkv != 0) return USP_ERR_INDIVISIBLE;
+  if ((c->D != 64 && c->D != 128) || c->page_size % 16 != 0) return USP_ERR_UNSUPPORTED;
+  const int64_t heads = c->Hkv >= c->P ? c->Hkv : c->P;  // of all ranks
+  if (heads > 4096 || c->n_seqs >= (1 << 20) || static_cast<int64_t>(c->n_seqs) * heads >= (1ll << 24))
+    return USP_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(c->n_pages) * c->page_size >= (1ll << 40) / (heads * c->D)) return USP_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(c->max_pages) * c->page_size >= (1ll << 30)) return USP_ERR_UNSUPPORTED;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !aligned16(c->k_scales) || !aligned16(c->v_scales))
+    return USP_ERR_ALIGNMENT;
+  if (!aligned4(c->block_table) || !aligned4(c->lens)) return USP_ERR_ALIGNMENT;
+  return USP_OK;
+}
+
+int move_tokens(const usp_paged_cache* c, const void* k, const void* v, int tokens, const int32_t* cu, bool append,
+                int32_t* status, usp_stream_t stream) {
+  int rc = check_cache(c);
+  if (rc != USP_OK) return rc;
+  if ((k == nullptr && v == nullptr) || tokens <= 0 || (cu == nullptr && tokens > c->n_seqs)) return USP_ERR_INVALID_ARG;
+  const int64_t heads = c->Hkv >= c->P ? c->Hkv : c->P;
+  if (tokens >= (1 << 30) || tokens * heads >= (1ll << 32)) return USP_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v)) return USP_ERR_ALIGNMENT;
+  if (!aligned4(cu)) return USP_ERR_ALIGNMENT;
+  return launch_cache_move(*c, const_cast<void*>(k), const_cast<void*>(v), tokens, cu, append, status,
+                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+int check_decode(const usp_paged_cache* c, int Hq) {
+  int rc = check_cache(c);
+  if (rc != USP_OK) return rc;
+  if (Hq <= 0) return USP_ERR_INVALID_ARG;
+  if (Hq % c->P != 0 || Hq % c->Hkv != 0) return USP_ERR_INDIVISIBLE;
+  return Hq > 1024 ? USP_ERR_UNSUPPORTED : USP_OK;
+}
+
 template <class... T>
 bool any_null(const T*... p) {
   return (... || (p == nullptr));
@@ -268,6 +339,8 @@ const char* usp_status_string(int s) {
     case USP_ERR_CUDA: return "USP_ERR_CUDA: CUDA call or launch failed";
     case USP_ERR_WORKSPACE: return "USP_ERR_WORKSPACE: workspace missing, misaligned or too small";
     case USP_ERR_BAD_MODS: return "USP_ERR_BAD_MODS: bucket id out of range, negative or missing prefix length";
+    case USP_ERR_BAD_ROPE: return "USP_ERR_BAD_ROPE: rotary axis out of range, or frequency not finite or too large";
+    case USP_ERR_BAD_PAGES: return "USP_ERR_BAD_PAGES: page, sequence length or boundaries outside the cache";
     default: return "USP_ERR_UNKNOWN";
   }
 }
@@ -624,6 +697,52 @@ int usp_attn_mod_bwd(const usp_attn_params* params, const usp_score_mods* mods, 
     return rc;
   if (rel && (rc = launch_attn_mod_bwd_rel_bias(prm, *mods, drel_bias, ws, st)) != USP_OK) return rc;
   return launch_attn_mod_bwd_dq(prm, *mods, q, k, v, dO, dq, ws, ws_bytes, dev_status, st);
+}
+
+// ---- rotary positions, the paged cache and single tokens
+
+int usp_rope_fwd(const usp_rope_params* params, const void* q, const void* k, void* q_out, void* k_out,
+                 int32_t* dev_status, usp_stream_t stream) {
+  int rc = check_rope(params, q, k, q_out, k_out);
+  if (rc != USP_OK) return rc;
+  return launch_rope(*params, q, k, q_out, k_out, false, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int usp_rope_bwd(const usp_rope_params* params, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                 int32_t* dev_status, usp_stream_t stream) {
+  int rc = check_rope(params, dq_out, dk_out, dq, dk);
+  if (rc != USP_OK) return rc;
+  return launch_rope(*params, dq_out, dk_out, dq, dk, true, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int usp_cache_append(const usp_paged_cache* cache, const void* k, const void* v, int tokens,
+                     const int32_t* cu_seqlens, int32_t* dev_status, usp_stream_t stream) {
+  return move_tokens(cache, k, v, tokens, cu_seqlens, true, dev_status, stream);
+}
+
+int usp_cache_read(const usp_paged_cache* cache, void* k, void* v, int tokens, const int32_t* cu_seqlens,
+                   int32_t* dev_status, usp_stream_t stream) {
+  return move_tokens(cache, k, v, tokens, cu_seqlens, false, dev_status, stream);
+}
+
+size_t usp_attn_decode_workspace_bytes(const usp_paged_cache* cache, int Hq) {
+  return check_decode(cache, Hq) != USP_OK ? 0 : attn_decode_ws_bytes(*cache);
+}
+
+int usp_attn_decode(const usp_paged_cache* cache, int Hq, int window_left, float softmax_scale, const float* sinks,
+                    const void* q, void* o, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                    usp_stream_t stream) {
+  int rc = check_decode(cache, Hq);
+  if (rc != USP_OK) return rc;
+  if (window_left < -1) return USP_ERR_UNSUPPORTED;
+  if (!(softmax_scale >= 0.f) || isinf(softmax_scale)) return USP_ERR_INVALID_ARG;
+  if (any_null(q, o) || lse == nullptr) return USP_ERR_INVALID_ARG;
+  if (!all_aligned16(q, o) || !aligned4(lse) || !aligned4(sinks)) return USP_ERR_ALIGNMENT;
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < attn_decode_ws_bytes(*cache))
+    return USP_ERR_WORKSPACE;
+  const float scale = softmax_scale != 0.f ? softmax_scale : 1.f / sqrtf(static_cast<float>(cache->D));
+  return launch_attn_decode(*cache, Hq, window_left, scale, sinks, q, o, lse, ws, dev_status,
+                            reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

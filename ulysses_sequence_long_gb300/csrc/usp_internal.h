@@ -53,11 +53,16 @@ struct FastDiv {
     m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - div)) / div + 1);
   }
 #ifdef __CUDACC__
-  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+  __host__ __device__ __forceinline__
+#endif
+  uint32_t div(uint32_t n) const {
+#ifdef __CUDA_ARCH__
     uint32_t hi = __umulhi(n, m);
+#else
+    uint32_t hi = static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> 32);
+#endif
     return static_cast<uint32_t>((static_cast<uint64_t>(hi) + n) >> s);
   }
-#endif
 };
 
 // Ps sequence shards, Ph head blocks (Ps = Ph = P: the Ulysses exchange;
@@ -113,5 +118,14 @@ int launch_attn_mod_bwd_dq(const usp_attn_params& p, const usp_score_mods& m, co
                            cudaStream_t st);
 int launch_attn_mod_bwd_rel_bias(const usp_attn_params& p, const usp_score_mods& m, float* drel_bias, void* ws,
                                  cudaStream_t st);
+
+// Rotary positions, the paged key/value cache and the attention of single tokens over it.
+int launch_rope(const usp_rope_params& p, const void* q, const void* k, void* q_out, void* k_out, bool back,
+                int32_t* status, cudaStream_t st);
+int launch_cache_move(const usp_paged_cache& c, void* k, void* v, int tokens, const int32_t* cu, bool append,
+                      int32_t* status, cudaStream_t st);
+size_t attn_decode_ws_bytes(const usp_paged_cache& c);
+int launch_attn_decode(const usp_paged_cache& c, int Hq, int window_left, float scale, const float* sinks,
+                       const void* q, void* o, float* lse, void* ws, int32_t* status, cudaStream_t st);
 
 }  // namespace usp

@@ -183,10 +183,12 @@ def all_gather(x: torch.Tensor, group=None) -> torch.Tensor:
 
 
 class UlyssesRankAttention:
-    """One rank's attention layer: its sequence chunk in, its sequence chunk out."""
+    """One rank's attention layer: its sequence chunk in, its sequence chunk out.  With ``rope``
+    (``pipeline.Rotary``) q and k of the chunk are turned before the exchange, and their gradients turned back."""
 
-    def __init__(self, shape: RankShape, group=None, device=None, ops=None):
+    def __init__(self, shape: RankShape, group=None, device=None, ops=None, rope=None):
         self.s = shape
+        self.rope = rope
         self.group = group
         self.rank = dist.get_rank(group)
         if dist.get_world_size(group) != shape.P:
@@ -209,10 +211,14 @@ class UlyssesRankAttention:
         hq = self.s.hq
         return sinks[self.rank * hq:(self.rank + 1) * hq].contiguous()
 
-    def forward(self, q_local, k_local, v_local, pos_local, sinks=None):
+    def forward(self, q_local, k_local, v_local, pos_local, sinks=None, rope_positions=None):
         """q/k/v ``[B][S/P][H][D]`` and position_ids ``[B][S/P]`` of this rank's
-        chunk (sinks: the global ``[Hq]`` logits) -> O ``[B][S/P][Hq][D]``."""
+        chunk (sinks: the global ``[Hq]`` logits) -> O ``[B][S/P][Hq][D]``.
+        ``rope_positions``: ``[n_axes][B][S/P]`` for ``rope`` (default: the position ids)."""
         s = self.s
+        self._rope_positions = pos_local if rope_positions is None else rope_positions
+        if self.rope is not None:
+            q_local, k_local = self.rope.forward(q_local, k_local, self._rope_positions)
         self.ops.boundaries(all_gather(pos_local, self.group))
         q_h = self._to_head(q_local, s.Hq)
         k_h = self._to_head(k_local, s.Hkv)
@@ -232,5 +238,7 @@ class UlyssesRankAttention:
         dq = self._to_seq(dq_h, s.Hq)
         dk = self._to_seq(dk_h, s.Hkv)
         dv = self._to_seq(dv_h, s.Hkv)
+        if self.rope is not None:
+            dq, dk = self.rope.backward(dq, dk, self._rope_positions, out=(dq, dk))
         dsinks = None if dz is None else all_gather(dz, self.group).reshape(-1)
         return dq, dk, dv, dsinks

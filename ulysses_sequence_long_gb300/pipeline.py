@@ -102,6 +102,118 @@ def rel_buckets_log(n_buckets: int, max_distance: int, bidirectional: bool, devi
     return B_.usp_rel_buckets_log(n_buckets, max_distance, bidirectional).to(device)
 
 
+class Rotary:
+    """Rotary positions of a model (``usp_rope_fwd``): ``freqs`` fp32
+    ``[pairs]`` in radians per position, ``axes`` int32 ``[pairs]`` the axis of
+    each pair (``n_axes`` of them; None: one axis).  Pair i is elements i and
+    i + pairs of a head, or 2i and 2i + 1 (``interleaved``); elements behind
+    the pairs pass through."""
+
+    def __init__(self, freqs: torch.Tensor, axes: Optional[torch.Tensor] = None, n_axes: int = 1,
+                 interleaved: bool = False):
+        if B_._dev(freqs, "freqs", torch.float32) is None:
+            raise TypeError("freqs must be a CUDA tensor")
+        B_._dev(axes, "axes", torch.int32)
+        if axes is None and n_axes != 1:
+            raise ValueError("several axes need the axis of each pair")
+        if axes is not None and (axes.numel() != freqs.numel() or axes.device != freqs.device):
+            raise ValueError(f"axes must have an entry for each of the {freqs.numel()} frequencies, on their device")
+        self.freqs, self.axes, self.n_axes, self.interleaved = freqs, axes, int(n_axes), bool(interleaved)
+        self.status = torch.zeros((1,), dtype=torch.int32, device=freqs.device)
+        self.device, self._index = freqs.device, freqs.get_device()
+        self._seen = {}
+
+    def _check(self, t, name, like):
+        if like is not None and t.shape != like.shape:
+            raise ValueError(f"{name} must have the shape {tuple(like.shape)}, got {tuple(t.shape)}")
+        if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == self._index
+                and t.is_contiguous()):
+            if B_._dev(t, name, torch.bfloat16) is None:
+                raise TypeError(f"{name} must be a CUDA tensor")
+            raise ValueError(f"{name} is on {t.device}, the frequencies on {self.device}")
+        return t.data_ptr()
+
+    def _params(self, q, k, positions):
+        """This call's own structure (threads may share a Rotary): sizes that go by the shapes, addresses of now."""
+        key = (q.shape, None if k is None else k.shape, positions.numel())
+        p = self._seen.get(key)
+        if p is None:
+            if q.dim() < 2 or (k is not None and (k.dim() < 2 or k.shape[-1] != q.shape[-1])):
+                raise ValueError("q and k must be [..., heads, D]")
+            Hq, D = q.shape[-2:]
+            tokens, Hkv = q.numel() // max(1, Hq * D), 0 if k is None else k.shape[-2]
+            if k is not None and k.numel() != tokens * Hkv * D:
+                raise ValueError(f"q has {tokens} tokens, k {k.numel() // max(1, Hkv * D)}")
+            if positions.numel() == 0 or positions.numel() % self.n_axes or tokens % (positions.numel() // self.n_axes):
+                raise ValueError(f"positions must be [{self.n_axes}][n] with n tokens or a divisor of their {tokens}, "
+                                 f"got {positions.numel()} elements")
+            p = B_.RopeParams(tokens, Hq, Hkv, D, self.n_axes, positions.numel() // self.n_axes, self.freqs.numel(),
+                              int(self.interleaved))
+            if len(self._seen) < 1024:
+                self._seen[key] = p
+        p = B_.RopeParams.from_buffer_copy(p)
+        pos, freqs, axes = positions, self.freqs, self.axes
+        for t, name, dtype in ((pos, "positions", torch.int32), (freqs, "freqs", torch.float32)) + (
+                () if axes is None else ((axes, "axes", torch.int32),)):
+            if not (t.dtype is dtype and t.get_device() == self._index and t.is_contiguous()):
+                B_._dev(t, name, dtype)
+                raise ValueError(f"{name} is on {t.device}, the frequencies on {self.device}")
+        if freqs.numel() != p.n_pairs or (axes is not None and axes.numel() != p.n_pairs):
+            raise ValueError("freqs or axes have changed their size")
+        p.positions, p.freqs, p.axes = pos.data_ptr(), freqs.data_ptr(), None if axes is None else axes.data_ptr()
+        return p
+
+    def _turn(self, where, q, k, positions, out, stream):
+        if out is None:
+            out = (torch.empty_like(q, memory_format=torch.contiguous_format),
+                   None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format))
+        p = self._params(q, k, positions)
+        ptrs = [self._check(q, "q", None), None if k is None else self._check(k, "k", None),
+                self._check(out[0], "the output of q", q), None if k is None else self._check(out[1], "the output of k", k)]
+        B_.call_on(self.device, stream, where, ctypes.byref(p), *ptrs, self.status.data_ptr())
+        return out
+
+    def forward(self, q, k, positions, out=None, stream=None):
+        """(q, k) turned: bf16 ``[..., H, D]`` each (k may be None), positions int32 ``[n_axes][tokens]``, or of a
+        divisor of the tokens, over which they repeat.  ``out``: the tensors to write, which may be q and k."""
+        return self._turn("usp_rope_fwd", q, k, positions, out, stream)
+
+    def backward(self, dq, dk, positions, out=None, stream=None):
+        """The gradients of ``forward``'s outputs to those of its inputs (``out`` may be dq and dk)."""
+        return self._turn("usp_rope_bwd", dq, dk, positions, out, stream)
+
+    def read_status(self) -> int:
+        return int(self.status.item())
+
+
+class _Turned:
+    """A layer's rotary positions: buffers for the turned shards, and the positions of the forward for the backward."""
+
+    def _init_rope(self, rope, dev, seq_q, seq_kv):
+        self.rope = rope
+        if rope is None:
+            return
+        self.q_rot = torch.empty(seq_q, dtype=torch.bfloat16, device=dev)
+        self.k_rot = torch.empty(seq_kv, dtype=torch.bfloat16, device=dev)
+        if rope.device != self.q_rot.device:
+            raise ValueError(f"the rotary frequencies are on {rope.device}, the layer on {self.q_rot.device}")
+        self._rope_positions = None
+
+    def rotate(self, q_seq, k_seq, positions, stream=None):
+        """The layer's first step: q and k shards turned (as they are without ``rope``), for ``exchange_qkv``."""
+        if self.rope is None:
+            return q_seq, k_seq
+        self.rope.forward(q_seq, k_seq, positions, out=(self.q_rot, self.k_rot), stream=stream)
+        self._rope_positions = positions
+        return self.q_rot, self.k_rot
+
+    def _rotate_back(self, stream):
+        """dQ and dK shards to the gradients of q and k before they were turned, in place."""
+        if self.rope is not None:
+            self.rope.backward(self.dq_seq, self.dk_seq, self._rope_positions, out=(self.dq_seq, self.dk_seq),
+                               stream=stream)
+
+
 def plan_backward(prm: B_.AttnParams, free_bytes: int, stored_ds: Optional[bool] = None, Hkv: int = 0,
                   groups_ok: bool = False, group_size: Optional[int] = None,
                   mods: Optional[B_.ScoreModsStruct] = None):
@@ -166,14 +278,15 @@ def backward_workspace(prm: B_.AttnParams, device, stored_ds: Optional[bool] = N
     return torch.empty((max(n, 256),), dtype=torch.uint8, device=device), stored_ds, groups
 
 
-class UlyssesAttention:
+class UlyssesAttention(_Turned):
     """Buffers and calls for one shape on one device.  With ``mods`` the scores
     are modified (``ScoreMods``): the same calls, and ``drel_bias`` after a
-    backward."""
+    backward.  With ``rope`` (``Rotary``) q and k are turned before the
+    exchange, and the gradients turned back."""
 
     def __init__(self, shape: Shape, device="cuda", with_backward: bool = True, fused: Optional[bool] = None,
                  stored_ds: Optional[bool] = None, ds_group_size: Optional[int] = None,
-                 mods: Optional[ScoreMods] = None):
+                 mods: Optional[ScoreMods] = None, rope: Optional[Rotary] = None):
         s = self.shape = shape
         self._mods = None if mods is None else mods.struct(s.Hq, with_backward)
         self.stored_ds = stored_ds
@@ -212,6 +325,7 @@ class UlyssesAttention:
             self.dsinks = torch.zeros((s.Hq,), dtype=torch.float32, device=dev)
             if self._mods is not None and self._mods.rel_bias_grad:
                 self.drel_bias = torch.zeros((s.Hq, self._mods.n_buckets), dtype=torch.float32, device=dev)
+        self._init_rope(rope, dev, seq_q, seq_kv)
         self._bwd_ws = None
         self.ds_groups = [(0, 0)]
         # the forward's q/k/v: as the attention kernels read them, with modified scores the caller's tensors, whose
@@ -455,8 +569,14 @@ class UlyssesAttention:
         elif not self.fused:
             B_.usp_relayout_bwd(self.o_head, self.o_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
 
-    def forward(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None):
-        """Sequence shards in, sequence shards out (``self.o_seq``)."""
+    def forward(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None, rope_positions=None):
+        """Sequence shards in, sequence shards out (``self.o_seq``).  ``rope_positions``: int32
+        ``[n_axes][P][B][S/P]`` for the layer's ``rope`` (default: the position ids, one axis)."""
+        if self.rope is not None:
+            if self._mods is not None:  # a call that is refused leaves what the backward reads
+                self._shards(v_seq, "v", self.shape.Hkv)
+                self._at(pos_shards, "position ids", torch.int32, self.shape.B * self.shape.S)
+            q_seq, k_seq = self.rotate(q_seq, k_seq, pos_shards if rope_positions is None else rope_positions, stream)
         if self._mods is not None:
             return self._on_device(self._mod_forward, q_seq, k_seq, v_seq, pos_shards, sinks, stream=stream)
         self.exchange_qkv(q_seq, k_seq, v_seq, stream)
@@ -468,10 +588,16 @@ class UlyssesAttention:
     def backward_phases(self, do_seq, sinks=None, stream=None, marks=None, group_marks=None):
         """The backward as its separate library calls; `marks(i)` is called
         between them (for timing): 0 before, 1 after the dO exchange, 2 after
-        the preprocess, 3 after dK/dV, 4 after dQ, 5 after the output exchanges.
+        the preprocess, 3 after dK/dV, 4 after dQ, 5 after the output exchanges
+        (with ``rope`` the gradients are turned back after that).
         When the passes run in key/value head groups, marks 3 and 4 both come
         after the last group and `group_marks(g, 0)` / `group_marks(g, 1)`
         after group g's dK/dV and dQ passes."""
+        self._backward_phases(do_seq, sinks, stream, marks, group_marks)
+        self._rotate_back(stream)
+        return self.dq_seq, self.dk_seq, self.dv_seq
+
+    def _backward_phases(self, do_seq, sinks, stream, marks, group_marks):
         s = self.shape
         if self._mods is not None:
             return self._on_device(self._mod_backward, do_seq, sinks, marks, group_marks, stream=stream)
@@ -526,13 +652,14 @@ class UlyssesAttention:
         B_.usp_relayout_bwd(self.dq_head, self.dq_seq, s.B, s.S, s.Hq, s.D, s.P, stream)
         B_.usp_relayout_bwd(self.dk_head, self.dk_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
         B_.usp_relayout_bwd(self.dv_head, self.dv_seq, s.B, s.S, s.Hkv, s.D, s.P, stream)
+        self._rotate_back(stream)
         return self.dq_seq, self.dk_seq, self.dv_seq
 
     def read_status(self) -> int:
-        return int(self.status.item())
+        return int(self.status.item()) or (0 if self.rope is None else self.rope.read_status())
 
 
-class HybridAttention:
+class HybridAttention(_Turned):
     """Ring x Ulysses (USP) over P = ring * ulysses emulated ranks.
 
     The Ulysses exchange runs inside each ring group; then ``ring`` steps
@@ -549,10 +676,14 @@ class HybridAttention:
     intermediate is in that layout, so no exchange kernel runs.  Explicit:
     ``usp_hybrid_relayout_*`` move tensors to and from the hybrid head layout
     [U][B][S][H/U][D].
+
+    With ``rope`` (``Rotary``) q and k are turned before the exchange, and the
+    gradients turned back.
     """
 
     def __init__(self, shape: Shape, ring: int, device="cuda", with_backward: bool = True,
-                 stored_ds: Optional[bool] = None, fused: Optional[bool] = None, ds_group_size: Optional[int] = None):
+                 stored_ds: Optional[bool] = None, fused: Optional[bool] = None, ds_group_size: Optional[int] = None,
+                 rope: Optional[Rotary] = None):
         s = self.shape = shape
         self.stored_ds = stored_ds
         self.ds_group_size = ds_group_size
@@ -606,6 +737,7 @@ class HybridAttention:
             self.dk_seq = torch.empty(seq_kv, dtype=bf, device=dev)
             self.dv_seq = torch.empty(seq_kv, dtype=bf, device=dev)
             self.dsinks = torch.zeros((s.Hq,), dtype=torch.float32, device=dev)
+        self._init_rope(rope, dev, seq_q, seq_kv)
         self._bwd_ws = None
         self.ds_groups = [(0, 0)]
         self._inputs = None
@@ -620,11 +752,13 @@ class HybridAttention:
     def _flags(self, step: int) -> int:
         return (B_.USP_RING_FIRST if step == 0 else 0) | (B_.USP_RING_LAST if step == self.ring - 1 else 0)
 
-    def forward_phases(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None, marks=None):
-        """marks(i): 0 before, 1 after the q/k/v exchange, 2 after the document
+    def forward_phases(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None, marks=None,
+                       rope_positions=None):
+        """marks(i): 0 before (with ``rope``, after q and k are turned), 1 after the q/k/v exchange, 2 after the document
         boundaries, 3 after the ring steps and merges, 4 after the O exchange."""
         s = self.shape
         mark = marks or (lambda i: None)
+        q_seq, k_seq = self.rotate(q_seq, k_seq, pos_shards if rope_positions is None else rope_positions, stream)
         mark(0)
         if self.fused:
             # q stays in its shards; k and v go to the hybrid head layout for the forward
@@ -654,13 +788,14 @@ class HybridAttention:
         mark(4)
         return self.o_seq
 
-    def forward(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None):
-        return self.forward_phases(q_seq, k_seq, v_seq, pos_shards, sinks, stream)
+    def forward(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None, rope_positions=None):
+        return self.forward_phases(q_seq, k_seq, v_seq, pos_shards, sinks, stream, rope_positions=rope_positions)
 
     def backward_phases(self, do_seq, sinks=None, stream=None, marks=None):
         """marks(i): 0 before, 1 after the dO exchange, 2 after the
         statistics, 3 after the dK/dV ring steps, 4 after the dQ ring steps,
-        5 after the dQ/dK/dV exchanges."""
+        5 after the dQ/dK/dV exchanges (with ``rope`` the gradients are
+        turned back after that)."""
         s = self.shape
         mark = marks or (lambda i: None)
         prm = self.params(sinks, 0)
@@ -709,10 +844,11 @@ class HybridAttention:
             B_.usp_hybrid_relayout_bwd(self.dk_head, self.dk_seq, s.B, s.S, s.Hkv, s.D, self.ring, self.U, stream)
             B_.usp_hybrid_relayout_bwd(self.dv_head, self.dv_seq, s.B, s.S, s.Hkv, s.D, self.ring, self.U, stream)
         mark(5)
+        self._rotate_back(stream)
         return self.dq_seq, self.dk_seq, self.dv_seq
 
     def backward(self, do_seq, sinks=None, stream=None):
         return self.backward_phases(do_seq, sinks, stream)
 
     def read_status(self) -> int:
-        return int(self.status.item())
+        return int(self.status.item()) or (0 if self.rope is None else self.rope.read_status())

@@ -1,0 +1,189 @@
+"""Serving: a key/value cache in pages and the attention of one new token per
+sequence over it.
+
+A prompt runs through ``UlyssesAttention``; its keys and values in head layout
+go into the cache (``PagedCache.append``), document by document of a packed
+batch.  From there on each step has one new token per sequence:
+``DecodeAttention.step`` turns its query and key (``Rotary``), appends key and
+value and attends over the sequence's pages.  Tensors have the head layout of
+one token per sequence, ``[P][sequences][H/P][D]``: every rank holds every
+sequence for its heads, so nothing is exchanged.
+
+Everything that grows or changes between steps (lengths, block tables) is read
+from device memory, so a captured step replays for longer sequences.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import binding as B_
+
+_BF, _F8, _I32, _F32, _U8 = torch.bfloat16, torch.float8_e4m3fn, torch.int32, torch.float32, torch.uint8
+
+
+def _where(t, name, dtype, n, index):
+    """The address of `t`, which has to be contiguous, of `n` elements of `dtype`, on device `index`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and t.get_device() == index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if B_._dev(t, name, dtype) is None:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} must have {n} elements on cuda:{index}, got {tuple(t.shape)} on {t.device}")
+
+
+class PagedCache:
+    """The pool of pages of one layer: ``k_pages``, ``v_pages``
+    ``[P][n_pages][heads of a rank][page_size][D]`` in bf16, or in e4m3
+    (``dtype=torch.float8_e4m3fn``) with ``k_scales``, ``v_scales`` bytes
+    ``[P][n_pages][heads of a rank][page_size]``.  ``block_table`` is int32
+    ``[sequences][max_pages]``, ``lens`` int32 ``[sequences]`` counts each
+    sequence's tokens, appended ones included."""
+
+    def __init__(self, n_pages: int, page_size: int, Hkv: int, D: int, P: int = 1, dtype=torch.bfloat16,
+                 device="cuda"):
+        if dtype not in (_BF, _F8):
+            raise TypeError(f"a cache holds torch.bfloat16 or torch.float8_e4m3fn, not {dtype}")
+        if (Hkv % P if Hkv >= P else P % Hkv) != 0:
+            raise ValueError(f"{P} ranks and {Hkv} key/value heads: neither divides the other")
+        self.n_pages, self.page_size, self.Hkv, self.D, self.P, self.dtype = n_pages, page_size, Hkv, D, P, dtype
+        self.hk = Hkv // P if Hkv >= P else 1
+        dev = torch.device(device)
+        shape = (P, n_pages, self.hk, page_size, D)
+        self.k_pages, self.v_pages = (torch.zeros(shape, dtype=_U8 if dtype is _F8 else _BF, device=dev).view(dtype)
+                                      for _ in range(2))
+        eight = dtype is _F8
+        self.k_scales, self.v_scales = (torch.ones(shape[:-1], dtype=_U8, device=dev) if eight else None
+                                        for _ in range(2))
+        self.status = torch.zeros((1,), dtype=_I32, device=dev)
+        self.device = self.status.device
+        self._index = self.status.get_device()
+        self._fixed = B_.PagedCacheStruct(P, Hkv, D, n_pages, page_size, 0, 0,
+                                          B_.USP_CACHE_E4M3 if eight else B_.USP_CACHE_BF16)
+
+    def _struct(self, block_table, lens) -> B_.PagedCacheStruct:
+        """This call's own structure: threads may use one cache at once, and buffers may have been exchanged."""
+        c = B_.PagedCacheStruct.from_buffer_copy(self._fixed)
+        index, n = self._index, self.P * self.n_pages * self.hk * self.page_size
+        if block_table.dim() != 2 or lens.dim() != 1:
+            raise ValueError("block_table must be [sequences][max_pages], lens [sequences]")
+        c.n_seqs, c.max_pages = lens.shape[0], block_table.shape[1]
+        c.k_pages = _where(self.k_pages, "k_pages", self.dtype, n * self.D, index)
+        c.v_pages = _where(self.v_pages, "v_pages", self.dtype, n * self.D, index)
+        if self.dtype is _F8:
+            c.k_scales = _where(self.k_scales, "k_scales", _U8, n, index)
+            c.v_scales = _where(self.v_scales, "v_scales", _U8, n, index)
+        c.block_table = _where(block_table, "block_table", _I32, c.n_seqs * c.max_pages, index)
+        c.lens = _where(lens, "lens", _I32, c.n_seqs, index)
+        return c
+
+    def _move(self, where, k, v, block_table, lens, cu_seqlens, stream):
+        c = self._struct(block_table, lens)
+        per = self.P * self.hk * self.D
+        n = k.numel()
+        if n == 0 or n % per != 0:
+            raise ValueError(f"k must be [{self.P}][tokens][{self.hk}][{self.D}], got {tuple(k.shape)}")
+        kp, vp = _where(k, "k", _BF, n, self._index), _where(v, "v", _BF, n, self._index)
+        cu = None
+        if cu_seqlens is not None:  # (the boundaries of a packed batch have room for more documents)
+            if cu_seqlens.numel() <= c.n_seqs:
+                raise ValueError(f"cu_seqlens must have at least {c.n_seqs + 1} elements, got {cu_seqlens.numel()}")
+            cu = _where(cu_seqlens, "cu_seqlens", _I32, cu_seqlens.numel(), self._index)
+        B_.call_on(self.device, stream, where, ctypes.byref(c), kp, vp, n // per, cu,
+                   _where(self.status, "status", _I32, 1, self._index))
+
+    def append(self, k, v, block_table, lens, cu_seqlens=None, stream=None):
+        """Write the last tokens of each sequence: k, v bf16 ``[P][tokens][heads of a rank][D]`` (head layout), tokens
+        ``[cu_seqlens[s], cu_seqlens[s+1])`` of sequence s, or one of each sequence without ``cu_seqlens``.
+        ``cu_seqlens`` and ``k_head``, ``v_head`` of a layer that ran a packed batch are these."""
+        self._move("usp_cache_append", k, v, block_table, lens, cu_seqlens, stream)
+
+    def read(self, block_table, lens, cu_seqlens=None, out=None, tokens: Optional[int] = None, stream=None):
+        """The way back: (k, v) of the last tokens of each sequence, into ``out``, or into new tensors of ``tokens``
+        tokens (places without a token are zero there, and left alone in ``out``)."""
+        if out is None:
+            if tokens is None:
+                if cu_seqlens is not None:
+                    raise ValueError("read needs out or tokens beside cu_seqlens (their sum is on the device)")
+                tokens = lens.shape[0]
+            out = tuple(torch.zeros((self.P, tokens, self.hk, self.D), dtype=_BF, device=self.device) for _ in range(2))
+        self._move("usp_cache_read", out[0], out[1], block_table, lens, cu_seqlens, stream)
+        return out
+
+    def read_status(self) -> int:
+        return int(self.status.item())
+
+
+class DecodeAttention:
+    """Attention of one new token per sequence over a ``PagedCache``, with the
+    window, scale and sinks of the layer; ``rope``: the layer's ``Rotary``,
+    for ``step``.  Outputs are views of the layer's own buffers, which hold up
+    to ``max_seqs`` sequences; the workspace is the layer's too, so calls that
+    may overlap (other streams, captured graphs) need a layer each."""
+
+    def __init__(self, cache: PagedCache, Hq: int, max_seqs: int, window_left: int = -1, softmax_scale: float = 0.0,
+                 rope=None):
+        self.cache, self.Hq, self.max_seqs = cache, Hq, max_seqs
+        self.window_left, self.softmax_scale, self.rope = int(window_left), float(softmax_scale), rope
+        if Hq % cache.P != 0 or Hq % cache.Hkv != 0:
+            raise ValueError(f"{Hq} query heads over {cache.P} ranks and {cache.Hkv} key/value heads")
+        dev = cache.device
+        self.hq = Hq // cache.P
+        rows = max_seqs * Hq
+        self._o = torch.empty((rows * cache.D,), dtype=_BF, device=dev)
+        self._lse = torch.empty((rows,), dtype=_F32, device=dev)
+        self._turned = None if rope is None else (
+            torch.empty((rows * cache.D,), dtype=_BF, device=dev),
+            torch.empty((cache.P * max_seqs * cache.hk * cache.D,), dtype=_BF, device=dev))
+        one = torch.zeros((1, 1), dtype=_I32, device=dev)
+        with torch.cuda.device(dev):
+            n = B_.usp_attn_decode_workspace_bytes(cache._struct(one, one[0]), Hq)
+        if n == 0:
+            raise ValueError("the library has no such attention: D 64 or 128, page_size a multiple of 16, Hq <= 1024")
+        self._ws = torch.empty((n,), dtype=_U8, device=dev)
+        self._views = {}
+        self.lse = None
+
+    def _out(self, n):
+        v = self._views.get(n)
+        if v is None:
+            c = self.cache
+            if not 0 < n <= self.max_seqs:
+                raise ValueError(f"{n} sequences, the layer has room for 1 to {self.max_seqs}")
+            v = self._views[n] = (self._o[:n * self.Hq * c.D].view(c.P, n, self.hq, c.D),
+                                  self._lse[:n * self.Hq].view(c.P, n, self.hq))
+        return v
+
+    def forward(self, q, block_table, lens, sinks=None, stream=None):
+        """q bf16 ``[P][sequences][Hq/P][D]``, already turned -> O of the same shape (and ``self.lse``)."""
+        c = self.cache
+        index = c._index
+        prm = c._struct(block_table, lens)
+        n = prm.n_seqs
+        o, lse = self._out(n)
+        B_.call_on(c.device, stream, "usp_attn_decode", ctypes.byref(prm), self.Hq, self.window_left,
+                   self.softmax_scale, None if sinks is None else _where(sinks, "sinks", _F32, self.Hq, index),
+                   _where(q, "q", _BF, n * self.Hq * c.D, index), o.data_ptr(), lse.data_ptr(), self._ws.data_ptr(),
+                   self._ws.numel(), _where(c.status, "status", _I32, 1, index))
+        self.lse = lse
+        return o
+
+    def step(self, q, k, v, block_table, lens, sinks=None, positions=None, stream=None):
+        """One token of each sequence through the layer: turn q and k (``rope``; positions int32
+        ``[n_axes][sequences]``), append k and v, attend.  ``lens`` counts the new token."""
+        if self.rope is not None:
+            if positions is None:
+                raise ValueError("a layer with rope needs the new tokens' positions")
+            n = lens.shape[0]
+            self._out(n)  # (checks n)
+            c = self.cache
+            out = (self._turned[0][:n * self.Hq * c.D].view(c.P, n, self.hq, c.D),
+                   self._turned[1][:n * c.P * c.hk * c.D].view(c.P, n, c.hk, c.D))
+            q, k = self.rope.forward(q, k, positions, out=out, stream=stream)
+        self.cache.append(k, v, block_table, lens, stream=stream)
+        return self.forward(q, block_table, lens, sinks, stream)
+
+    def read_status(self) -> int:
+        return self.cache.read_status() or (0 if self.rope is None else self.rope.read_status())
