@@ -15,12 +15,12 @@
 // Loads.  A warp has 16 positions of each tile.  The products are arranged so that the
 // positions are the rows of the matrix instruction and the query heads its 8 columns
 // (S^T = K q^T, O^T = V^T P^T): rows of 16 query heads would be half empty for groups up to 8.
-// Sums over d may take d in any order, so a thread's operands are whole 16-byte pieces of its rows:
-// each thread copies its own pieces into shared memory (cp.async, several tiles ahead)
-// and takes them from there itself.  No barrier, no swizzle, no other thread's data; only the pairs of
-// positions that V^T's operands want next to each other are interleaved, by byte permutations.  (Matrix
-// instructions with operands from shared memory and results in tensor memory want 64 rows of queries; here there are
-// G.)
+// Sums over d may take d in any order, so a thread's operands are whole 16-byte pieces of its rows.  A warp copies
+// its own 16 rows into shared memory (cp.async, 512 consecutive bytes an instruction, tiles ahead) and no barrier but
+// the warp's own is needed; only the pairs of positions that V^T's operands want next to each other are
+// interleaved, by byte permutations.  Copying each thread's own pieces, in segments of 64 bytes of a
+// K row, kept loads at 5.2 TB/s, consecutive rows at 7.0.  (Matrix instructions with operands from shared memory and
+// results in tensor memory want 64 rows of queries; here there are G.)
 //
 // e4m3: an element is exactly an f16, so products run in f16; a token's scales are powers of two
 // and act on its score (keys) and on its weight (values).  The reference M of a column is near the maximum of
@@ -58,10 +58,11 @@ constexpr int ctas_per_sm(int row_bytes) { return row_bytes == 256 ? 2 : row_byt
 template <int D, bool kE4m3>
 struct Cfg {
   static constexpr int kRow = D * (kE4m3 ? 1 : 2);               // bytes of a token's head
-  static constexpr int kKPieces = kRow / 64;                     // 16-byte pieces of a K row per thread (4 threads a row)
+  static constexpr int kCopies = kRow / 32;                      // 16-byte copies of a thread for 16 rows
+  static constexpr int kKPieces = kRow / 64;                     // 16-byte pieces of a K row that a thread takes (4 threads a row)
   static constexpr int kVBytes = kRow / 8 >= 16 ? 16 : 8;        // a thread's piece of a V row (8 threads a row)
   static constexpr int kVPieces = kRow / 8 / kVBytes;
-  static constexpr int kScaleBytes = kE4m3 ? 32 : 0;             // 16 tokens' key and value scales
+  static constexpr int kScaleBytes = kE4m3 ? 128 : 0;            // 16 tokens' key and value scales (and up to whole lines)
   static constexpr int kStage = 2 * 16 * kRow + kScaleBytes;     // one warp's share of a tile
   static constexpr int kCtas = ctas_per_sm(kRow);
   static constexpr int kStages = kRow == 64 ? 4 : 3;
@@ -88,20 +89,12 @@ __device__ __forceinline__ int tiles_of(const Args& a, int seq, bool& bad) {
   return paged::Span(a.pool, a.window, seq, bad).tiles();
 }
 
-// N bytes from global memory to shared memory, past L1 where it can be (16 bytes)
-template <int N>
+// 16 bytes from global memory to shared memory, past L1
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-template <int N>
 __device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool ok) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(ok ? N : 0) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -272,51 +265,42 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
   };
   enter_unit();
   find_page();
-  const int koff = g * C::kRow + qd * 16, voff = 2 * qd * C::kRow + g * C::kVBytes;
+  // Shared memory holds rows as they are, 16-byte pieces turned over within 128 bytes so that both the copies (512 bytes
+  // of consecutive rows an instruction) and the reads below meet all banks: a K row's by 4 where it is odd, a V row's by
+  // twice its pair's number mod 4 (rows of 64 bytes: K not at all, V by 2 where the pair is odd).
+  constexpr int R = C::kRow;
+  const int kput = (lane ^ (R == 256 ? lane >> 4 << 2 : R == 128 ? (lane >> 3 & 1) << 2 : 0)) * 16;
+  const int vput = (lane ^ (R == 256 ? 0 : R == 128 ? lane >> 4 << 1 : (lane >> 3 & 1) << 1)) * 16;
+  const int kget = g * R + qd * 16 + (R == 64 ? 0 : (g & 1) * 64);
+  const int vget = 2 * qd * R + (R == 64 ? ((g >> 1) ^ ((qd & 1) << 1)) * 16 + (g & 1) * 8 : (g ^ (2 * qd)) * 16);
   auto load = [&]() {
     if (left > 0) {
       const int t0 = ld.tile * kTile + 16 * w;
       if (t0 < ld.len && t0 + 16 > ld.lo) {
         const bool ok = page >= 0 && page < a.pool.n_pages;
         const int64_t row = unit_row + (ok ? page : 0) * page_rows + (t0 - static_cast<int>(col) * a.pool.page_size);
-        const unsigned char* kp = static_cast<const unsigned char*>(a.pool.k) + row * C::kRow + koff;
-        const unsigned char* vp = static_cast<const unsigned char*>(a.pool.v) + row * C::kRow + voff;
-        const uint32_t kdst = ring + slot + lane * 16, vdst = ring + slot + 16 * C::kRow + lane * C::kVBytes;
+        const unsigned char* kp = static_cast<const unsigned char*>(a.pool.k) + row * R + lane * 16;
+        const unsigned char* vp = static_cast<const unsigned char*>(a.pool.v) + row * R + lane * 16;
+        const uint32_t kdst = ring + slot + kput, vdst = ring + slot + 16 * R + vput;
+        const auto vturn = [](int i) { return R == 256 ? (i & 3) << 5 : R == 128 ? (i & 1) << 6 : 0; };
         if (ok && t0 >= ld.lo && t0 + 16 <= ld.len) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < C::kCopies; ++i) cp_async(kdst + i * 512, kp + i * 512);
 #pragma unroll
-            for (int p = 0; p < C::kKPieces; ++p)
-              cp_async<16>(kdst + (i * C::kKPieces + p) * 512, kp + 8 * i * C::kRow + p * 64);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int p = 0; p < C::kVPieces; ++p)
-              cp_async<C::kVBytes>(vdst + (i * C::kVPieces + p) * 32 * C::kVBytes,
-                                   vp + ((i & 1) + 8 * (i >> 1)) * C::kRow + p * 8 * C::kVBytes);
+          for (int i = 0; i < C::kCopies; ++i) cp_async((vdst ^ vturn(i)) + i * 512, vp + i * 512);
         } else {  // zeros for what is not seen: a weight of 0 does not undo a value that is not finite
           if (!ok) set_status(a.status, USP_ERR_BAD_PAGES);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int t = t0 + g + 8 * i;
+          for (int i = 0; i < C::kCopies; ++i) {
+            const int t = t0 + (i * 512 + lane * 16) / R;
             const bool in = ok && t < ld.len && t >= ld.lo;
-#pragma unroll
-            for (int p = 0; p < C::kKPieces; ++p)
-              cp_async_or_zero<16>(kdst + (i * C::kKPieces + p) * 512, kp + 8 * i * C::kRow + p * 64, in);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = t0 + 2 * qd + (i & 1) + 8 * (i >> 1);
-            const bool in = ok && t < ld.len && t >= ld.lo;
-#pragma unroll
-            for (int p = 0; p < C::kVPieces; ++p)
-              cp_async_or_zero<C::kVBytes>(vdst + (i * C::kVPieces + p) * 32 * C::kVBytes,
-                                           vp + ((i & 1) + 8 * (i >> 1)) * C::kRow + p * 8 * C::kVBytes, in);
+            cp_async_or_zero(kdst + i * 512, kp + i * 512, in);
+            cp_async_or_zero((vdst ^ vturn(i)) + i * 512, vp + i * 512, in);
           }
         }
         if constexpr (kE4m3) {
           if (lane < 2)
-            cp_async<16>(ring + slot + 32 * C::kRow + 16 * lane, (lane == 0 ? a.pool.k_scales : a.pool.v_scales) + row);
+            cp_async(ring + slot + 32 * R + 16 * lane, (lane == 0 ? a.pool.k_scales : a.pool.v_scales) + row);
         }
       }
       if (--left > 0) {
@@ -389,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
     int t0 = cur.tile * kTile + 16 * w;
     for (int it = 0; it < tiles; ++it, t0 += kTile) {
       cp_async_wait<C::kStages - 2>();
-      if constexpr (kE4m3) __syncwarp();  // (the scales are another lane's copies)
+      __syncwarp();  // every lane's copies are here, and its reads of the place that is filled next are done
       load();
       const uint32_t src = ring + read;
       read = read == (C::kStages - 1) * C::kStage ? 0 : read + C::kStage;
@@ -398,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
       float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int p = 0; p < C::kKPieces; ++p) {
-        const uint4 x = lds16(src + lane * 16 + p * 512), y = lds16(src + lane * 16 + (C::kKPieces + p) * 512);
+        const uint32_t from = ((src + kget) ^ (p & 1) * 64) + (p >> 1) * 128;
+        const uint4 x = lds16(from), y = lds16(from + 8 * R);
         if constexpr (!kE4m3) {
           mma<false>(s, x.x, y.x, x.y, y.y, qf[2 * p][0], qf[2 * p][1]);
           mma<false>(s2, x.z, y.z, x.w, y.w, qf[2 * p + 1][0], qf[2 * p + 1][1]);
@@ -416,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
       if constexpr (kE4m3) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int kb = lds1(src + 32 * C::kRow + g + 8 * i), vb = lds1(src + 32 * C::kRow + 16 + g + 8 * i);
+          const int kb = lds1(src + 32 * R + g + 8 * i), vb = lds1(src + 32 * R + 16 + g + 8 * i);
           ks[i] = kb ? __uint_as_float(static_cast<uint32_t>(kb) << 23) : 0x1p-127f;
           ve[i] = static_cast<float>(vb - 127);
         }
@@ -480,14 +465,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
         c1 = transpose8(pack_bf16x2(p[2] - bf16lo(h1), p[3] - bf16hi(h1)));
       }
       // O^T += V^T P^T
-      const uint32_t vsrc = src + 16 * C::kRow + lane * C::kVBytes;
+      const uint32_t vsrc = src + 16 * R + vget;
       constexpr int W4 = C::kVBytes / 4;  // words of a piece
 #pragma unroll
       for (int pc = 0; pc < C::kVPieces; ++pc) {
         uint32_t v[4][W4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t from = vsrc + (i * C::kVPieces + pc) * 32 * C::kVBytes;
+          const uint32_t from = vsrc + ((i & 1) + 8 * (i >> 1)) * R + pc * 128;
           if constexpr (W4 == 4) {
             const uint4 y = lds16(from);
             v[i][0] = y.x;
