@@ -575,8 +575,8 @@ int usp_cache_read(const usp_paged_cache* cache, void* k, void* v, int tokens, c
  * q, o: bf16 [P][n_seqs][Hq/P][D]; lse: fp32 [P][n_seqs][Hq/P]; sinks: fp32 [Hq] or NULL.
  * The work of all sequences is dealt out evenly in pieces of 64 positions, whatever their lengths, and pieces
  * of one sequence are joined in the order of their positions: the result does not depend on timing.
- * ws: usp_attn_decode_workspace_bytes bytes, 256-byte aligned, contents on entry do not matter; it belongs to one
- * call at a time (calls that may overlap need one each).
+ * ws: usp_attn_decode_workspace_bytes bytes, 256-byte aligned, all zero before its first call; a call leaves zero
+ * what has to be.  It belongs to one call at a time (calls that may overlap need one each).
  * dev_status: USP_ERR_BAD_PAGES (the sequence's outputs are then unspecified; nothing outside the pool is read).
  * Errors: USP_ERR_INVALID_ARG, USP_ERR_INDIVISIBLE, USP_ERR_UNSUPPORTED (as the cache; window_left < -1, Hq > 1024),
  * USP_ERR_ALIGNMENT, USP_ERR_WORKSPACE, USP_ERR_CUDA. */

@@ -126,6 +126,7 @@ static void deal(int it) {
   const long long ctas = std::min<long long>(pick(1, 400), W);
   std::map<std::pair<int, int>, std::vector<int>> seen;            // unit -> tiles in order
   std::map<std::pair<int, int>, std::vector<int>> holders;         // unit -> CTAs that have a part
+  const int warps = 4;
   std::map<int, std::pair<std::pair<int, int>, int>> named;        // CTA -> (unit that it begins and does not end, parts)
   for (int k = 0; k < ctas; ++k) {
     const long long a = stretch(W, ctas, k), b = stretch(W, ctas, k + 1);
@@ -135,6 +136,19 @@ static void deal(int it) {
     Cursor cur;
     cur.seek(p, window, s, a - begins[s], bad);
     int part = cur.tile == cur.first;
+    // the warps' stretches follow one another, and a warp that has one finds its begin as the CTA does
+    CHECK(stretch(b - a, warps, 0) == 0 && stretch(b - a, warps, warps) == b - a);
+    for (int w = 0; w < warps; ++w) {
+      const long long x = a + stretch(b - a, warps, w), y = a + stretch(b - a, warps, w + 1);
+      CHECK(x <= y);
+      if (x == y) continue;
+      int q = 0;
+      while (!(x >= begins[q] && x < begins[q] + static_cast<long long>(Span(p, window, q, bad).tiles()) * units)) ++q;
+      Cursor c2, c3 = cur;
+      c2.seek(p, window, q, x - begins[q], bad);
+      for (long long t = a; t < x; ++t) c3.next(p, window, units, bad);
+      CHECK(c2.b == c3.b && c2.u == c3.u && c2.tile == c3.tile && c2.end == c3.end);
+    }
     for (long long t = a; t < b; ++t) {
       const std::pair<int, int> unit(cur.b, cur.u);
       seen[unit].push_back(cur.tile);

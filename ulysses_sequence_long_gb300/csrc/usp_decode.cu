@@ -6,13 +6,15 @@
 // for each of the G query heads of their group, G a few: far below the card's ratio.  So
 // what counts is that loads never pause and that all SMs have the same share of them.
 //
-// Shares.  The work of all sequences is one line of tiles of 64 positions (of a sequence, a rank
-// and a key/value head: a "unit"); each CTA takes an equal stretch of the line, found from the
-// lengths on the device, whatever they are.  A unit that lies in one CTA is finished there.  One
-// that several CTAs share leaves partial results (O, maximum, sum in fp32) which a second
-// kernel joins in the order of the positions.
+// Shares.  The work of all sequences is one line of tiles of 16 positions (of a sequence, a rank
+// and a key/value head: a "unit"); each CTA takes an equal stretch of the line and each of its warps
+// a part of that, found from the lengths on the device, whatever they are.  A warp runs through its tiles
+// without waiting for the others.  A unit that lies in one warp is finished there.  Of one that several share
+// each leaves a partial result (O, maximum, sum in fp32): the CTA puts its warps' together once,
+// when all are done, and what crosses CTAs goes through the workspace.  Parts are joined in the order of the
+// positions.
 //
-// Loads.  A warp has 16 positions of each tile.  The products are arranged so that the
+// Loads.  The products are arranged so that the
 // positions are the rows of the matrix instruction and the query heads its 8 columns
 // (S^T = K q^T, O^T = V^T P^T): rows of 16 query heads would be half empty for groups up to 8.
 // Sums over d may take d in any order, so a thread's operands are whole 16-byte pieces of its rows.  A warp copies
@@ -41,19 +43,17 @@
 namespace usp {
 namespace decode {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 using paged::Cursor;
 using paged::kTile;
-static_assert(kTile == 16 * kWarps, "a warp has 16 positions of a tile");
+static_assert(kTile == 16, "the rows of a matrix instruction");
+constexpr int kFan = 48;            // parts that a CTA puts together at once
+constexpr int kLeastTiles = 1;      // tiles of a warp, where there are few
 constexpr int kHeads = 8;           // query heads of a unit (more of them in a group: more units)
-constexpr int kMaxCtas = 1024;
+constexpr int kMaxCtas = 1024, kTicketBytes = kMaxCtas * 12;
 // A column's reference may stay this far (log2) below a weight; e4m3: weights go into f16 kUp higher (2^15 at most), and
 // a token's value exponent counts from kLeast up in the reference.
 constexpr float kAbove = 8.f, kUp = 7.f, kDown = 0x1p-7f, kLeast = -60.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-// What fits into an SM's shared memory with the stages below (64 to 96 KB of loads in flight).
-constexpr int ctas_per_sm(int row_bytes) { return row_bytes == 256 ? 2 : row_bytes == 128 ? 3 : 4; }
 
 template <int D, bool kE4m3>
 struct Cfg {
@@ -64,10 +64,14 @@ struct Cfg {
   static constexpr int kVPieces = kRow / 8 / kVBytes;
   static constexpr int kScaleBytes = kE4m3 ? 128 : 0;            // 16 tokens' key and value scales (and up to whole lines)
   static constexpr int kStage = 2 * 16 * kRow + kScaleBytes;     // one warp's share of a tile
-  static constexpr int kCtas = ctas_per_sm(kRow);
-  static constexpr int kStages = kRow == 64 ? 4 : 3;
-  static constexpr int kMerge = kWarps * kHeads * D * 4;         // the warps' O
-  static constexpr int kSmem = kStages * kStage * kWarps + kMerge;
+  // One CTA per SM, of as many warps as its registers and shared memory hold: few CTAs leave few parts to join.
+  static constexpr int kWarps = kRow == 256 ? 8 : kRow == 128 ? 12 : 16, kThreads = 32 * kWarps;
+  static constexpr int kSlices = kThreads / 128;                 // (16 threads for each of 8 heads)
+  static constexpr int kStages = kRow == 64 ? 4 : 3;             // 100 to 130 KB of loads in flight per SM
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kKept = kHeads * D * 4;                   // a partial O of a warp
+  static constexpr int kSmem = kWarps * (kRing + kKept);
+  static_assert(kRing >= kKept && kWarps * kRing >= kSlices * kKept, "partial Os fit into rings that are done with");
 };
 
 struct Args {
@@ -81,7 +85,7 @@ struct Args {
   float* lse;
   float* parts;                         // [2 * ctas][kHeads][D] then [2 * ctas][kHeads][2]
   float* stats;
-  int32_t* desc;                        // [ctas][2]: the unit that begins in this CTA and ends in another (or -1), its parts
+  int32_t* tickets;                     // [ctas][3], zero between calls
   int32_t* status;
 };
 
@@ -144,13 +148,48 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// The matrix row pair mt of V^T that thread group g has: elements d, d + 1 with
-// d = value_column(mt, g) (its 16-byte pieces, two elements a row pair).
+// The matrix row pair mt of V^T has elements d, d + 1 of thread group g's pieces, in order: row pairs 4 x .. 4 x + 3 are
+// the eight elements from first_column(x, g) on.
 template <int D, bool kE4m3>
-__device__ __forceinline__ int value_column(int mt, int g) {
-  if constexpr (!kE4m3) return 64 * (mt >> 2) + 8 * g + 2 * (mt & 3);
-  return (D / 8) * g + 2 * mt;
+__device__ __forceinline__ int first_column(int x, int g) {
+  return kE4m3 ? (D / 8) * g + 8 * x : 64 * x + 8 * g;
 }
+
+// A warp's part of a unit that it shares with others.
+struct Part {
+  int unit;           // sequence * units + unit, -1: none
+  int begins, ends;   // the unit begins, ends in it
+  int tiles;          // of the whole unit
+  long long stop;     // where the unit ends on the line
+};
+
+// The query heads of a unit: row of the first among [P][n_seqs][hq], how many, its sink.
+struct Heads {
+  int64_t row;
+  int n, sink;
+  __device__ __forceinline__ Heads(const Args& a, int b, int r, int j, int chunk) {
+    const int h0 = j * a.G + chunk * kHeads;
+    row = (static_cast<int64_t>(r) * a.n_seqs + b) * a.hq + h0;
+    n = min(kHeads, a.G - chunk * kHeads);
+    sink = r * a.hq + h0;
+  }
+};
+
+// From a head's reference (log2, finite) and sum: what its weighted values are multiplied by, and its LSE.
+struct Finish {
+  float scale, lse;
+  __device__ __forceinline__ Finish(const Args& a, const Heads& hd, int h, float ref, float sum) {
+    float f = 1.f;
+    if (a.sinks != nullptr) {  // the sink joins the sum once, with no value
+      const float z = gld(a.sinks + hd.sink + h) * kLog2e, m = fmaxf(ref, z);
+      f = ex2(ref - m);
+      sum = sum * f + ex2(z - m);
+      ref = m;
+    }
+    scale = sum > 0.f ? f / sum : sum;  // (0 stays 0, NaN NaN)
+    lse = (ref + log2f(sum)) * kLn2;
+  }
+};
 
 // A stretch's place with the unit's parts spelt out.
 struct Place : Cursor {
@@ -168,82 +207,22 @@ struct Place : Cursor {
   }
 };
 
+// A warp's stretch: `count` tiles from `at` of the line, which is `rest` tiles into sequence `seq`.
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(Args a) {
+__device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, Part* parts, float2 (*stats)[kHeads], int seq,
+                                            long long rest, long long at, int count) {
   using C = Cfg<D, kE4m3>;
   constexpr int MT = D / 16, KS = D / 16, QV = D / 32;  // QV: 16-byte pieces of a query head that a thread has
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long scan[kWarps];
-  __shared__ int at_seq;
-  __shared__ long long at_rest;
-  __shared__ float wm[kWarps][kHeads], wl[kWarps][kHeads];
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
-  grid_wait();
-
-  // ---- the CTA's stretch of the line
-  const int per = (a.n_seqs + kThreads - 1) / kThreads, s0 = tid * per, s1 = min(a.n_seqs, s0 + per);
-  long long mine = 0;
-  bool bad = false;
-  for (int s = s0; s < s1; ++s) mine += tiles_of(a, s, bad);
-  if (bad) set_status(a.status, USP_ERR_BAD_PAGES);
-  long long before = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, before, d);
-    if (lane >= d) before += x;
-  }
-  if (lane == 31) scan[w] = before;
-  __syncthreads();
-  long long all = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < w) before += scan[i];
-    all += scan[i];
-  }
-  before = (before - mine) * a.units;
-  const long long W = all * a.units;
-  const long long n_ctas = min(static_cast<long long>(gridDim.x), W);
-  const int cta = blockIdx.x;
-  if (tid == 0) {
-    a.desc[2 * cta] = -1;
-    a.desc[2 * cta + 1] = 0;
-  }
-  // sequences without a visible token have no tile: their outputs are written here
-  for (int s = cta; s < a.n_seqs; s += gridDim.x)
-    if (tiles_of(a, s, bad) == 0) {
-      for (int i = tid; i < a.P * a.hq; i += kThreads) {
-        const int r = i / a.hq, h = i - r * a.hq;
-        a.lse[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq + h] = a.sinks ? gld(a.sinks + r * a.hq + h) : -INFINITY;
-      }
-      for (int i = tid; i < a.P * a.hq * (D / 8); i += kThreads) {
-        const int r = i / (a.hq * (D / 8)), x = i - r * (a.hq * (D / 8));
-        reinterpret_cast<uint4*>(a.o)[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq * (D / 8) + x] = make_uint4(0, 0, 0, 0);
-      }
-    }
-  if (cta >= n_ctas) return;
-  const long long begin = paged::stretch(W, n_ctas, cta), finish = paged::stretch(W, n_ctas, cta + 1);
-  if (begin >= before && begin < before + mine * a.units) {
-    long long rest = begin - before;
-    int s = s0;
-    for (;; ++s) {
-      const long long n = static_cast<long long>(tiles_of(a, s, bad)) * a.units;
-      if (rest < n) break;
-      rest -= n;
-    }
-    at_seq = s;
-    at_rest = rest;
-  }
-  __syncthreads();
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, qd = lane & 3;
+  float* kept = reinterpret_cast<float*>(smem + C::kWarps * C::kRing + w * C::kKept);
+  bool bad = false;  // (reported when the lengths were added up)
   Place cur;
-  cur.seek(a.pool, a.window, at_seq, at_rest, bad);
+  cur.seek(a.pool, a.window, seq, rest, bad);
   cur.split(a);
-  int count = static_cast<int>(finish - begin);
-  long long at = begin;                 // the tile of the line that is next
-  int part = cur.tile == cur.first;     // 0: of a unit that began in an earlier CTA; 1: of one that begins here
+  bool begins = cur.tile == cur.first;  // the unit at hand begins in this warp
 
   // ---- loads, kStages - 1 tiles ahead
-  const uint32_t ring = smem_u32(smem) + w * (C::kStages * C::kStage);
-  float* merge = reinterpret_cast<float*>(smem + C::kStages * C::kStage * kWarps);
+  const uint32_t ring = smem_u32(smem) + w * C::kRing;
   Place ld = cur;
   int left = count;                     // tiles not asked for yet
   int page = 0;                         // of the tile at ld; looked up a tile ahead
@@ -257,11 +236,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
     unit_row = static_cast<int64_t>(ld.r) * a.pool.n_pages * page_rows + ld.j * a.pool.page_size;
   };
   auto find_page = [&]() {
-    const int t0 = ld.tile * kTile + 16 * w;
-    if (t0 < ld.len && t0 + 16 > ld.lo) {
-      col = a.pool.by_page.div(t0);
-      page = gld(table + col);
-    }
+    col = a.pool.by_page.div(ld.tile * kTile);
+    page = gld(table + col);
   };
   enter_unit();
   find_page();
@@ -275,33 +251,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
   const int vget = 2 * qd * R + (R == 64 ? ((g >> 1) ^ ((qd & 1) << 1)) * 16 + (g & 1) * 8 : (g ^ (2 * qd)) * 16);
   auto load = [&]() {
     if (left > 0) {
-      const int t0 = ld.tile * kTile + 16 * w;
-      if (t0 < ld.len && t0 + 16 > ld.lo) {
-        const bool ok = page >= 0 && page < a.pool.n_pages;
-        const int64_t row = unit_row + (ok ? page : 0) * page_rows + (t0 - static_cast<int>(col) * a.pool.page_size);
-        const unsigned char* kp = static_cast<const unsigned char*>(a.pool.k) + row * R + lane * 16;
-        const unsigned char* vp = static_cast<const unsigned char*>(a.pool.v) + row * R + lane * 16;
-        const uint32_t kdst = ring + slot + kput, vdst = ring + slot + 16 * R + vput;
-        const auto vturn = [](int i) { return R == 256 ? (i & 3) << 5 : R == 128 ? (i & 1) << 6 : 0; };
-        if (ok && t0 >= ld.lo && t0 + 16 <= ld.len) {
+      const int t0 = ld.tile * kTile;
+      const bool ok = page >= 0 && page < a.pool.n_pages;
+      const int64_t row = unit_row + (ok ? page : 0) * page_rows + (t0 - static_cast<int>(col) * a.pool.page_size);
+      const unsigned char* kp = static_cast<const unsigned char*>(a.pool.k) + row * R + lane * 16;
+      const unsigned char* vp = static_cast<const unsigned char*>(a.pool.v) + row * R + lane * 16;
+      const uint32_t kdst = ring + slot + kput, vdst = ring + slot + 16 * R + vput;
+      const auto vturn = [](int i) { return R == 256 ? (i & 3) << 5 : R == 128 ? (i & 1) << 6 : 0; };
+      if (ok && t0 >= ld.lo && t0 + 16 <= ld.len) {
 #pragma unroll
-          for (int i = 0; i < C::kCopies; ++i) cp_async(kdst + i * 512, kp + i * 512);
+        for (int i = 0; i < C::kCopies; ++i) cp_async(kdst + i * 512, kp + i * 512);
 #pragma unroll
-          for (int i = 0; i < C::kCopies; ++i) cp_async((vdst ^ vturn(i)) + i * 512, vp + i * 512);
-        } else {  // zeros for what is not seen: a weight of 0 does not undo a value that is not finite
-          if (!ok) set_status(a.status, USP_ERR_BAD_PAGES);
+        for (int i = 0; i < C::kCopies; ++i) cp_async((vdst ^ vturn(i)) + i * 512, vp + i * 512);
+      } else {  // zeros for what is not seen: a weight of 0 does not undo a value that is not finite
+        if (!ok) set_status(a.status, USP_ERR_BAD_PAGES);
 #pragma unroll
-          for (int i = 0; i < C::kCopies; ++i) {
-            const int t = t0 + (i * 512 + lane * 16) / R;
-            const bool in = ok && t < ld.len && t >= ld.lo;
-            cp_async_or_zero(kdst + i * 512, kp + i * 512, in);
-            cp_async_or_zero((vdst ^ vturn(i)) + i * 512, vp + i * 512, in);
-          }
+        for (int i = 0; i < C::kCopies; ++i) {
+          const int t = t0 + (i * 512 + lane * 16) / R;
+          const bool in = ok && t < ld.len && t >= ld.lo;
+          cp_async_or_zero(kdst + i * 512, kp + i * 512, in);
+          cp_async_or_zero((vdst ^ vturn(i)) + i * 512, vp + i * 512, in);
         }
-        if constexpr (kE4m3) {
-          if (lane < 2)
-            cp_async(ring + slot + 32 * R + 16 * lane, (lane == 0 ? a.pool.k_scales : a.pool.v_scales) + row);
-        }
+      }
+      if constexpr (kE4m3) {
+        if (lane < 2)
+          cp_async(ring + slot + 32 * R + 16 * lane, (lane == 0 ? a.pool.k_scales : a.pool.v_scales) + row);
       }
       if (--left > 0) {
         if (++ld.tile == ld.end) {
@@ -370,14 +344,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
     for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     bool none = true;  // no visible position yet
     const int tiles = min(count, cur.end - cur.tile);
-    int t0 = cur.tile * kTile + 16 * w;
+    int t0 = cur.tile * kTile;
     for (int it = 0; it < tiles; ++it, t0 += kTile) {
       cp_async_wait<C::kStages - 2>();
       __syncwarp();  // every lane's copies are here, and its reads of the place that is filled next are done
       load();
       const uint32_t src = ring + read;
       read = read == (C::kStages - 1) * C::kStage ? 0 : read + C::kStage;
-      if (t0 >= cur.len || t0 + 16 <= cur.lo) continue;
       // S^T: rows g and g + 8 are positions, columns 2 qd and 2 qd + 1 query heads
       float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -506,149 +479,341 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3>::kCtas) decode_kernel(
       }
     }
 
-    // ---- the unit (or its part in this CTA) ends
-    const bool ends = cur.tile + tiles == cur.end;
-    const int unit = cur.b * a.units + cur.u, heads = min(kHeads, a.G - cur.chunk * kHeads);
-    const int64_t head0 = (static_cast<int64_t>(cur.r) * a.n_seqs + cur.b) * a.hq + cur.j * a.G + cur.chunk * kHeads;
-    const int sink0 = cur.r * a.hq + cur.j * a.G + cur.chunk * kHeads;
+    // ---- the unit, or its part in this warp, ends
+    const bool ends = cur.tile + tiles == cur.end, own = begins;
+    const int unit = cur.b * a.units + cur.u;
+    const Heads hd(a, cur.b, cur.r, cur.j, cur.chunk);
+    const int unit_tiles = cur.end - cur.first;
     const long long stop = at + (cur.end - cur.tile);  // where the unit ends on the line
     count -= tiles;
     at += tiles;
-    if (count > 0) {  // the next unit's query is on its way while the warps' results are put together
+    if (count > 0) {  // the next unit's query is on its way meanwhile
       cur.next_unit(a, bad);
+      begins = true;
       fetch_q();
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
-    if (g == 0) {
-      wm[w][2 * qd] = m[0];
-      wm[w][2 * qd + 1] = m[1];
-      wl[w][2 * qd] = l[0];
-      wl[w][2 * qd + 1] = l[1];
-    }
-    // [warp][head][d], d with bits 1 and 2 turned over by the head's place so that the stores meet all banks
+    // a thread has the elements d .. d + 7 of two heads, d = first_column(x, g)
+    if (own && ends) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int d = value_column<D, kE4m3>(i, g) ^ (2 * qd);
-      float* to = merge + (w * kHeads + 2 * qd) * D + d;
-      *reinterpret_cast<float2*>(to) = make_float2(acc[i][0], acc[i][2]);
-      *reinterpret_cast<float2*>(to + D) = make_float2(acc[i][1], acc[i][3]);
-    }
-    __syncthreads();
-    // 16 threads a head, D/16 elements each
-    constexpr int E = D / 16;
-    const int h = tid >> 4, d0 = (tid & 15) * E;
-    float M = -INFINITY;
+      for (int c = 0; c < 2; ++c) {
+        const int h = 2 * qd + c;
+        if (h < hd.n) {
+          const Finish f(a, hd, h, ref[c], l[c]);
+          const float by = f.scale * (kE4m3 ? kDown : 1.f);
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) M = fmaxf(M, wm[i][h]);
-    const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f, o[E] = {};
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const float f = ex2(wm[i][h] - base);
-      L += wl[i][h] * f;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 y = *reinterpret_cast<const float2*>(merge + (i * kHeads + h) * D + ((d0 + e) ^ (2 * (h >> 1))));
-        o[e] += y.x * f;
-        o[e + 1] += y.y * f;
-      }
-    }
-    if constexpr (kE4m3) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= kDown;
-    }
-    if (ends && part == 1) {
-      if (h < heads) {
-        M = base;
-        if (a.sinks != nullptr) {
-          const float z = gld(a.sinks + sink0 + h) * kLog2e;
-          M = fmaxf(base, z);
-          const float f = ex2(base - M);
-          L = L * f + ex2(z - M);
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] *= f;
+          for (int x = 0; x < D / 64; ++x)
+            *reinterpret_cast<uint4*>(a.o + (hd.row + h) * D + first_column<D, kE4m3>(x, g)) =
+                make_uint4(pack_bf16x2(acc[4 * x][c] * by, acc[4 * x][2 + c] * by),
+                           pack_bf16x2(acc[4 * x + 1][c] * by, acc[4 * x + 1][2 + c] * by),
+                           pack_bf16x2(acc[4 * x + 2][c] * by, acc[4 * x + 2][2 + c] * by),
+                           pack_bf16x2(acc[4 * x + 3][c] * by, acc[4 * x + 3][2 + c] * by));
+          if (g == 0) a.lse[hd.row + h] = f.lse;
         }
-        const float inv = L > 0.f ? 1.f / L : L;  // (0 stays 0, NaN NaN)
-        uint32_t out[E / 2];
-#pragma unroll
-        for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-        uint16_t* to = a.o + (head0 + h) * D + d0;
-        if constexpr (E == 8)
-          *reinterpret_cast<uint4*>(to) = make_uint4(out[0], out[1], out[2], out[3]);
-        else
-          *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
-        if ((tid & 15) == 0) a.lse[head0 + h] = (M + log2f(L)) * kLn2;
       }
     } else {
-      const int64_t place = static_cast<int64_t>(2 * cta + part) * kHeads + h;
-      float* to = a.parts + place * D + d0;
+      // [head][d] in shared memory: of a unit that began earlier in the place kept for it, of one that goes on in the
+      // warp's ring, whose last tile has been read
+      __syncwarp();
+      const int k = 2 * w + own;
+      float* to = own ? reinterpret_cast<float*>(smem + w * C::kRing) : kept;
 #pragma unroll
-      for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-      if ((tid & 15) == 0) *reinterpret_cast<float2*>(a.stats + place * 2) = make_float2(M, L);
-      if (!ends && part == 1 && tid == 0) {
-        a.desc[2 * cta] = unit;
-        a.desc[2 * cta + 1] = static_cast<int>(paged::cta_of_last(W, n_ctas, stop)) - cta + 1;
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+          float* at8 = to + (2 * qd + c) * D + first_column<D, kE4m3>(x, g);
+          reinterpret_cast<float4*>(at8)[0] = make_float4(acc[4 * x][c], acc[4 * x][2 + c], acc[4 * x + 1][c], acc[4 * x + 1][2 + c]);
+          reinterpret_cast<float4*>(at8)[1] =
+              make_float4(acc[4 * x + 2][c], acc[4 * x + 2][2 + c], acc[4 * x + 3][c], acc[4 * x + 3][2 + c]);
+        }
+        if (g == 0) stats[k][2 * qd + c] = make_float2(m[c], l[c]);
       }
+      if (lane == 0) parts[k] = Part{unit, own, ends, unit_tiles, stop};
     }
-    if (count == 0) return;
-    part = 1;
-    __syncthreads();
+    if (count == 0) break;
   }
 }
 
-// The parts of the unit that begins in CTA blockIdx.x and ends in a later one, head blockIdx.y of the unit.
+// Thread (h, d0)'s D/16 elements of a unit's head h.
 template <int D>
-__global__ void __launch_bounds__(kThreads) join_kernel(Args a) {
-  __shared__ float so[kWarps][D], sl[kWarps];
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, h = blockIdx.y;
-  constexpr int E = D / 32;
-  grid_wait();
-  const int cta = blockIdx.x, unit = gld(a.desc + 2 * cta), n = gld(a.desc + 2 * cta + 1);
-  if (unit < 0) return;
-  const int b = unit / a.units, u = unit - b * a.units, rj = u / a.chunks, chunk = u - rj * a.chunks;
-  const int r = rj / a.pool.hk, j = rj - r * a.pool.hk, heads = min(kHeads, a.G - chunk * kHeads);
-  if (h >= heads) return;
-  // part 0 is the second of the first CTA's two places, the others the first of theirs
-  auto place = [&](int i) { return static_cast<int64_t>(2 * (cta + i) + (i == 0)) * kHeads + h; };
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, gld(a.stats + 2 * place(i)));
+__device__ __forceinline__ void write_out(const Args& a, int unit, int h, int d0, float M, float L, const float (&o)[D / 16]) {
+  constexpr int E = D / 16;
+  const int b = unit / a.units, u = unit - b * a.units, rj = u / a.chunks, r = rj / a.pool.hk;
+  const Heads hd(a, b, r, rj - r * a.pool.hk, u - rj * a.chunks);
+  if (h >= hd.n) return;
+  const Finish f(a, hd, h, M == -INFINITY ? 0.f : M, L);
+  uint32_t out[E / 2];
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  const float z = a.sinks != nullptr ? gld(a.sinks + r * a.hq + j * a.G + chunk * kHeads + h) * kLog2e : -INFINITY;
-  M = fmaxf(M, z);
-  if (M == -INFINITY) M = 0.f;
-  float L = 0.f, o[E] = {};
-#pragma unroll 4
-  for (int i = w; i < n; i += kWarps) {
-    const int64_t at = place(i);
-    const float2 ml = *reinterpret_cast<const float2*>(a.stats + 2 * at);
-    const float f = ex2(ml.x - M);
-    L += ml.y * f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += gld(a.parts + at * D + e * 32 + lane) * f;
+  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(o[e] * f.scale, o[e + 1] * f.scale);
+  uint16_t* to = a.o + (hd.row + h) * D + d0;
+  if constexpr (E == 8)
+    *reinterpret_cast<uint4*>(to) = make_uint4(out[0], out[1], out[2], out[3]);
+  else
+    *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
+  if (d0 == 0) a.lse[hd.row + h] = f.lse;
+}
+
+// A CTA's part of a unit that crosses CTAs: it is part i of the n in CTAs first .. first + n - 1.
+struct Crossing {
+  int unit, first, n, i;  // unit -1: none
+};
+
+// Parts in the workspace.  A CTA has two places: the first for a unit that began in an earlier CTA, the second for one
+// that begins in it.  (Loads and stores past L1: other CTAs' data.)
+template <int D>
+struct Parts {
+  static constexpr int E = D / 16;
+  const Args& a;
+  int first, h, d0;
+  __device__ __forceinline__ int64_t place(int x) const {
+    return static_cast<int64_t>(2 * (first + x) + (x == 0)) * kHeads + h;
   }
-  if (lane == 0) sl[w] = L;
+  __device__ __forceinline__ void leave(int x, float M, float L, const float (&o)[E]) const {
+    float* to = a.parts + place(x) * D + d0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[w][e * 32 + lane] = o[e];
-  __syncthreads();
-  float total = ex2(z - M);
+    for (int e = 0; e < E; e += 4) __stcg(reinterpret_cast<float4*>(to + e), make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+    if (d0 == 0) __stcg(reinterpret_cast<float2*>(a.stats) + place(x), make_float2(M, L));
+  }
+  // x, x + step, ... below stop, put together
+  __device__ __forceinline__ void gather(int x, int stop, int step, float& M, float& L, float (&o)[E]) const {
+    M = -INFINITY;
+    L = 0.f;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) total += sl[i];
-  const int64_t head = (static_cast<int64_t>(r) * a.n_seqs + b) * a.hq + j * a.G + chunk * kHeads + h;
-  const float inv = total > 0.f ? 1.f / total : total;  // (0 stays 0, NaN NaN)
-  if (tid < D / 2) {
-    float x = 0.f, y = 0.f;
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    constexpr int kAtOnce = 8;
+#pragma unroll 1
+    for (; x < stop; x += kAtOnce * step) {
+      float2 ml[kAtOnce];
+      float4 y[kAtOnce][E / 4];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      x += so[i][2 * tid];
-      y += so[i][2 * tid + 1];
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int p = x + k * step;
+        ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e) y[k][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p < stop) {
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(a.stats) + place(p));
+#pragma unroll
+          for (int e = 0; e < E / 4; ++e) y[k][e] = __ldcg(reinterpret_cast<const float4*>(a.parts + place(p) * D + d0) + e);
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
+      const float ref = top == -INFINITY ? 0.f : top, f = ex2(M - ref);
+      M = top;
+      L *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float by = ex2(ml[k].x - ref);
+        L += ml[k].y * by;
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e) {
+          o[4 * e] += y[k][e].x * by;
+          o[4 * e + 1] += y[k][e].y * by;
+          o[4 * e + 2] += y[k][e].z * by;
+          o[4 * e + 3] += y[k][e].w * by;
+        }
+      }
     }
-    reinterpret_cast<uint32_t*>(a.o)[head * (D / 2) + tid] = pack_bf16x2(x * inv, y * inv);
   }
-  if (tid == 0) a.lse[head] = (M + log2f(total)) * kLn2;
+};
+
+// One of several partial results in shared memory joins (M, L, o).
+template <int E>
+__device__ __forceinline__ void add_part(float2 ml, const float* from, float& M, float& L, float (&o)[E]) {
+  const float top = fmaxf(M, ml.x), ref = top == -INFINITY ? 0.f : top, f = ex2(M - ref), by = ex2(ml.x - ref);
+  M = top;
+  L = L * f + ml.y * by;
+#pragma unroll
+  for (int e = 0; e < E; e += 4) {
+    const float4 y = *reinterpret_cast<const float4*>(from + e);
+    o[e] = o[e] * f + y.x * by;
+    o[e + 1] = o[e + 1] * f + y.y * by;
+    o[e + 2] = o[e + 2] * f + y.z * by;
+    o[e + 3] = o[e + 3] * f + y.w * by;
+  }
+}
+
+// The units that cross CTAs, in the CTAs that come last: every CTA leaves its part in the workspace and takes a ticket; of
+// kFan parts in a row the last CTA puts them together, and of these sums again the last one.  The
+// order of the additions goes by the positions, whoever is last.
+template <int D, bool kE4m3>
+__device__ __forceinline__ void join(const Args& a, unsigned char* smem, const Crossing* crossing) {
+  using C = Cfg<D, kE4m3>;
+  constexpr int E = D / 16;
+  __shared__ int last[2];
+  __shared__ float2 stats[C::kSlices][kHeads];
+  const int tid = threadIdx.x, slice = tid >> 7, h = (tid >> 4) & 7, d0 = (tid & 15) * E;
+  float* sums = reinterpret_cast<float*>(smem);  // [slice][head][d]
+  __syncthreads();  // the CTA's parts are written
+  if (tid < 2) {
+    int is_last = 0;
+    if (crossing[tid].unit >= 0) {
+      const int x0 = crossing[tid].i / kFan * kFan, x1 = min(crossing[tid].n, x0 + kFan);
+      // tickets of the CTA that has a group's first part: [0] of a unit that began earlier, [1] of one that begins there,
+      // [2] of the groups of that one.  The last to come leaves 0.
+      int32_t* ticket = a.tickets + 3 * (crossing[tid].first + x0) + (x0 == 0);
+      __threadfence();
+      is_last = atomicAdd(ticket, 1) == x1 - x0 - 1;
+      __threadfence();
+      if (is_last) *ticket = 0;
+    }
+    last[tid] = is_last;
+  }
+  __syncthreads();
+  for (int c = 0; c < 2; ++c) {
+    if (!last[c]) continue;
+    const int n = crossing[c].n, unit = crossing[c].unit, groups = (n + kFan - 1) / kFan;
+    const Parts<D> parts{a, crossing[c].first, h, d0};
+    int x = crossing[c].i / kFan * kFan, stop = min(n, x + kFan), step = 1;
+    while (true) {
+      float M, L, o[E];
+      parts.gather(x + slice * step, stop, C::kSlices * step, M, L, o);
+#pragma unroll
+      for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<float4*>(sums + (slice * kHeads + h) * D + d0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      if (d0 == 0) stats[slice][h] = make_float2(M, L);
+      __syncthreads();
+      if (slice == 0) {
+#pragma unroll
+        for (int k = 1; k < C::kSlices; ++k) add_part(stats[k][h], sums + (k * kHeads + h) * D + d0, M, L, o);
+        if (step == 1 && groups > 1)
+          parts.leave(x, M, L, o);
+        else
+          write_out<D>(a, unit, h, d0, M, L, o);
+      }
+      __syncthreads();
+      if (step > 1 || groups == 1) break;
+      if (tid == 0) {
+        int32_t* ticket = a.tickets + 3 * crossing[c].first + 2;
+        __threadfence();
+        last[c] = atomicAdd(ticket, 1) == groups - 1;
+        __threadfence();
+        if (last[c]) *ticket = 0;
+      }
+      __syncthreads();
+      if (!last[c]) break;
+      x = 0;
+      stop = n;
+      step = kFan;
+    }
+  }
+}
+
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args a) {
+  using C = Cfg<D, kE4m3>;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long scan[kWarps];
+  __shared__ int at_seq[kWarps];
+  __shared__ long long at_rest[kWarps];
+  __shared__ Part parts[2 * kWarps];
+  __shared__ float2 stats[2 * kWarps][kHeads];  // reference, sum
+  __shared__ Crossing crossing[2];              // of a unit that began in an earlier CTA, of one that begins here
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  grid_wait();
+
+  // ---- the CTA's stretch of the line
+  const int per = (a.n_seqs + kThreads - 1) / kThreads, s0 = tid * per, s1 = min(a.n_seqs, s0 + per);
+  long long mine = 0;
+  bool bad = false;
+  for (int s = s0; s < s1; ++s) mine += tiles_of(a, s, bad);
+  if (bad) set_status(a.status, USP_ERR_BAD_PAGES);
+  long long before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before += x;
+  }
+  if (lane == 31) scan[w] = before;
+  __syncthreads();
+  long long all = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < w) before += scan[i];
+    all += scan[i];
+  }
+  before = (before - mine) * a.units;
+  const long long W = all * a.units;
+  const long long n_ctas = min(static_cast<long long>(gridDim.x), (W + kWarps * kLeastTiles - 1) / (kWarps * kLeastTiles));
+  const int cta = blockIdx.x;
+  // sequences without a visible token have no tile: their outputs are written here
+  for (int s = cta; s < a.n_seqs; s += gridDim.x)
+    if (tiles_of(a, s, bad) == 0) {
+      for (int i = tid; i < a.P * a.hq; i += kThreads) {
+        const int r = i / a.hq, h = i - r * a.hq;
+        a.lse[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq + h] = a.sinks ? gld(a.sinks + r * a.hq + h) : -INFINITY;
+      }
+      for (int i = tid; i < a.P * a.hq * (D / 8); i += kThreads) {
+        const int r = i / (a.hq * (D / 8)), x = i - r * (a.hq * (D / 8));
+        reinterpret_cast<uint4*>(a.o)[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq * (D / 8) + x] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  if (cta >= n_ctas) return;
+  const long long begin = paged::stretch(W, n_ctas, cta), total = paged::stretch(W, n_ctas, cta + 1) - begin;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {  // where the warps' stretches begin
+    const long long x = begin + paged::stretch(total, kWarps, i);
+    if (x >= before && x < before + mine * a.units) {
+      long long rest = x - before;
+      int s = s0;
+      for (;; ++s) {
+        const long long n = static_cast<long long>(tiles_of(a, s, bad)) * a.units;
+        if (rest < n) break;
+        rest -= n;
+      }
+      at_seq[i] = s;
+      at_rest[i] = rest;
+    }
+  }
+  if (tid < 2 * kWarps) parts[tid].unit = -1;
+  if (tid < 2) crossing[tid].unit = -1;
+  __syncthreads();
+  const long long at = begin + paged::stretch(total, kWarps, w);
+  const int count = static_cast<int>(begin + paged::stretch(total, kWarps, w + 1) - at);
+  if (count > 0) run_stretch<D, kE4m3>(a, smem, parts, stats, at_seq[w], at_rest[w], at, count);
+
+  // ---- the warps' parts, in order: those of one unit next to each other
+  __syncthreads();
+  constexpr int E = D / 16;  // a slice has 16 threads for each head, D/16 elements each
+  const int slice = tid >> 7, h = (tid >> 4) & 7, d0 = (tid & 15) * E;
+  for (int i = 0, group = 0; i < 2 * kWarps; ++group) {
+    const int unit = parts[i].unit;
+    int last = i;
+    for (int k = i + 1; k < 2 * kWarps; ++k)
+      if (unit >= 0 && parts[k].unit == unit) last = k;
+    if (unit >= 0 && group % C::kSlices == slice) {
+      float M = -INFINITY, L = 0.f, o[E] = {};
+      for (int k = i; k <= last; ++k)
+        if (parts[k].unit == unit)
+          add_part(stats[k][h],
+                   reinterpret_cast<const float*>(smem + (k & 1 ? k / 2 * C::kRing : kWarps * C::kRing + k / 2 * C::kKept)) + h * D + d0,
+                   M, L, o);
+      if constexpr (kE4m3) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= kDown;
+      }
+      const bool begins = parts[i].begins;
+      if (begins && parts[last].ends) {
+        write_out<D>(a, unit, h, d0, M, L, o);
+      } else {
+        const long long stop = parts[last].stop;
+        const int first = begins ? cta : static_cast<int>(paged::cta_of_last(W, n_ctas, stop - parts[last].tiles + 1));
+        Parts<D>{a, first, h, d0}.leave(cta - first, M, L, o);
+        if (h == 0 && d0 == 0)
+          crossing[begins] = Crossing{unit, first, static_cast<int>(paged::cta_of_last(W, n_ctas, stop)) - first + 1, cta - first};
+      }
+    }
+    i = last + 1;
+  }
+  join<D, kE4m3>(a, smem, crossing);
 }
 
 template <int D, bool kE4m3>
@@ -659,22 +824,17 @@ int launch(const Args& a, int ctas, cudaStream_t st) {
     cudaGetLastError();
     return USP_ERR_CUDA;
   }
-  const int rc = launch_chained(kern, dim3(ctas), kThreads, smem, 1, st, a);
-  if (rc != USP_OK) return rc;
-  return launch_chained(join_kernel<D>, dim3(ctas, std::min(kHeads, a.G)), kThreads, 0, 1, st, a);
+  return launch_chained(kern, dim3(ctas), Cfg<D, kE4m3>::kThreads, smem, 1, st, a);
 }
 
-int grid_of(const usp_paged_cache& c) {
-  const int row = c.D * (c.dtype == USP_CACHE_E4M3 ? 1 : 2);
-  return std::min(kMaxCtas, device_sm_count() * ctas_per_sm(row));
-}
+int grid_of() { return std::min(kMaxCtas, device_sm_count()); }
 
 }  // namespace decode
 
-// parts, then statistics, then descriptors
+// Tickets (of kMaxCtas, so that they lie at the same place for every cache), then parts, then statistics.
 size_t attn_decode_ws_bytes(const usp_paged_cache& c) {
-  const size_t ctas = decode::grid_of(c), rows = 2 * ctas * decode::kHeads;
-  return rows * c.D * 4 + rows * 8 + ctas * 8;
+  const size_t ctas = decode::grid_of(), rows = 2 * ctas * decode::kHeads;
+  return decode::kTicketBytes + rows * c.D * 4 + rows * 8;
 }
 
 int launch_attn_decode(const usp_paged_cache& c, int Hq, int window_left, float scale, const float* sinks,
@@ -694,11 +854,11 @@ int launch_attn_decode(const usp_paged_cache& c, int Hq, int window_left, float 
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
   a.status = status;
-  const int ctas = decode::grid_of(c);
+  const int ctas = decode::grid_of();
   const size_t rows = 2 * static_cast<size_t>(ctas) * decode::kHeads;
-  a.parts = static_cast<float*>(ws);
+  a.tickets = static_cast<int32_t*>(ws);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + decode::kTicketBytes);
   a.stats = a.parts + rows * c.D;
-  a.desc = reinterpret_cast<int32_t*>(a.stats + rows * 2);
   const bool e = c.dtype == USP_CACHE_E4M3;
   if (c.D == 64) return e ? decode::launch<64, true>(a, ctas, st) : decode::launch<64, false>(a, ctas, st);
   return e ? decode::launch<128, true>(a, ctas, st) : decode::launch<128, false>(a, ctas, st);

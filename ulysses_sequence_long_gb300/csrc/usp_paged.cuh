@@ -91,8 +91,8 @@ struct Pool {
 };
 
 // ---- the attention's work: one line of tiles of kTile positions, sequence by sequence, within
-// a sequence unit by unit (a rank's key/value head and up to 8 of its query heads)
-constexpr int kTile = 64;
+// a sequence unit by unit (a rank's key/value head and up to 8 of its query heads).  A tile lies in one page.
+constexpr int kTile = 16;
 
 // What a sequence's token sees: positions lo .. len - 1, tiles first .. end - 1.
 struct Span {
@@ -106,7 +106,7 @@ struct Span {
   USP_HD int tiles() const { return end - first; }
 };
 
-// CTA c of n takes tiles [stretch(c), stretch(c + 1)) of W >= n.
+// CTA c of n takes tiles [stretch(c), stretch(c + 1)) of W >= n; its warps share them the same way.
 USP_HD long long stretch(long long W, long long n, long long c) { return W * c / n; }
 // The CTA that has tile stop - 1: the smallest c with stretch(c + 1) >= stop.
 USP_HD long long cta_of_last(long long W, long long n, long long stop) { return (stop * n + W - 1) / W - 1; }

@@ -142,7 +142,7 @@ class DecodeAttention:
             n = B_.usp_attn_decode_workspace_bytes(cache._struct(one, one[0]), Hq)
         if n == 0:
             raise ValueError("the library has no such attention: D 64 or 128, page_size a multiple of 16, Hq <= 1024")
-        self._ws = torch.empty((n,), dtype=_U8, device=dev)
+        self._ws = torch.zeros((n,), dtype=_U8, device=dev)
         self._views = {}
         self.lse = None
 
