@@ -129,17 +129,20 @@ static void deal(int it) {
   const int warps = 4;
   std::map<int, std::pair<std::pair<int, int>, int>> named;        // CTA -> (unit that it begins and does not end, parts)
   for (int k = 0; k < ctas; ++k) {
-    const long long a = stretch(W, ctas, k), b = stretch(W, ctas, k + 1);
-    CHECK(a < b);
+    const Deal line(W, ctas);
+    const long long a = line.begin(k), b = line.begin(k + 1);
+    CHECK(a < b && line.owner(a) == static_cast<uint32_t>(k) && line.owner(b - 1) == static_cast<uint32_t>(k));
+    CHECK(line.begin(0) == 0 && line.begin(ctas) == W);
     int s = 0;
     while (!(a >= begins[s] && a < begins[s] + static_cast<long long>(Span(p, window, s, bad).tiles()) * units)) ++s;
     Cursor cur;
     cur.seek(p, window, s, a - begins[s], bad);
     int part = cur.tile == cur.first;
     // the warps' stretches follow one another, and a warp that has one finds its begin as the CTA does
-    CHECK(stretch(b - a, warps, 0) == 0 && stretch(b - a, warps, warps) == b - a);
+    const Deal own(b - a, warps);
+    CHECK(own.begin(0) == 0 && own.begin(warps) == b - a);
     for (int w = 0; w < warps; ++w) {
-      const long long x = a + stretch(b - a, warps, w), y = a + stretch(b - a, warps, w + 1);
+      const long long x = a + own.begin(w), y = a + own.begin(w + 1);
       CHECK(x <= y);
       if (x == y) continue;
       int q = 0;
@@ -154,7 +157,7 @@ static void deal(int it) {
       seen[unit].push_back(cur.tile);
       if (holders[unit].empty() || holders[unit].back() != k) holders[unit].push_back(k);
       const bool ends = cur.tile + 1 == cur.end;
-      if (!ends && t + 1 == b && part) named[k] = {unit, static_cast<int>(cta_of_last(W, ctas, t + (cur.end - cur.tile))) - k + 1};
+      if (!ends && t + 1 == b && part) named[k] = {unit, static_cast<int>(line.owner(t + (cur.end - cur.tile) - 1)) - k + 1};
       if (ends) part = 1;
       cur.next(p, window, units, bad);
     }

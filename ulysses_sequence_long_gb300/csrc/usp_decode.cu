@@ -44,10 +44,11 @@ namespace usp {
 namespace decode {
 
 using paged::Cursor;
+using paged::Deal;
 using paged::kTile;
 static_assert(kTile == 16, "the rows of a matrix instruction");
 constexpr int kFan = 48;            // parts that a CTA puts together at once
-constexpr int kLeastTiles = 1;      // tiles of a warp, where there are few
+constexpr int kJoinTiles = 3;       // tiles that a warp works through in the time that joining parts takes
 constexpr int kHeads = 8;           // query heads of a unit (more of them in a group: more units)
 constexpr int kMaxCtas = 1024, kTicketBytes = kMaxCtas * 12;
 // A column's reference may stay this far (log2) below a weight; e4m3: weights go into f16 kUp higher (2^15 at most), and
@@ -79,6 +80,7 @@ struct Args {
   int n_seqs, P, hq, G, chunks, units;  // chunks of 8 heads in a group of G; units = P * hk * chunks per sequence
   int window;                           // -1: none
   float scale;                          // softmax scale
+  FastDiv by_units, by_chunks, by_hk;
   const float* sinks;
   const uint16_t* q;
   uint16_t* o;
@@ -160,7 +162,7 @@ struct Part {
   int unit;           // sequence * units + unit, -1: none
   int begins, ends;   // the unit begins, ends in it
   int tiles;          // of the whole unit
-  long long stop;     // where the unit ends on the line
+  uint32_t stop;      // where the unit ends on the line
 };
 
 // The query heads of a unit: row of the first among [P][n_seqs][hq], how many, its sink.
@@ -195,9 +197,9 @@ struct Finish {
 struct Place : Cursor {
   int r, j, chunk;  // rank, its key/value head, chunk of 8 query heads
   __device__ __forceinline__ void split(const Args& a) {
-    const int rj = u / a.chunks;
+    const int rj = a.by_chunks.div(u);
     chunk = u - rj * a.chunks;
-    r = rj / a.pool.hk;
+    r = a.by_hk.div(rj);
     j = rj - r * a.pool.hk;
   }
   __device__ __forceinline__ void next_unit(const Args& a, bool& bad) {
@@ -207,17 +209,31 @@ struct Place : Cursor {
   }
 };
 
-// A warp's stretch: `count` tiles from `at` of the line, which is `rest` tiles into sequence `seq`.
+// A warp's stretch: `count` tiles from `at` of the line, or `count` whole units; it begins start.y tiles (units) into
+// sequence start.x.
 template <int D, bool kE4m3>
-__device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, Part* parts, float2 (*stats)[kHeads], int seq,
-                                            long long rest, long long at, int count) {
+__device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, Part* parts, float2 (*stats)[kHeads],
+                                            int2 start, bool by_unit, uint32_t at, int count) {
   using C = Cfg<D, kE4m3>;
   constexpr int MT = D / 16, KS = D / 16, QV = D / 32;  // QV: 16-byte pieces of a query head that a thread has
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, qd = lane & 3;
   float* kept = reinterpret_cast<float*>(smem + C::kWarps * C::kRing + w * C::kKept);
   bool bad = false;  // (reported when the lengths were added up)
   Place cur;
-  cur.seek(a.pool, a.window, seq, rest, bad);
+  if (by_unit) {
+    cur.sequence(a.pool, a.window, start.x, bad);
+    cur.u = start.y;
+    Cursor c = cur;
+    int tiles = 0;
+    for (int i = 0; i < count; ++i) {
+      tiles += c.end - c.first;
+      c.tile = c.end - 1;
+      c.next(a.pool, a.window, a.units, bad);
+    }
+    count = tiles;
+  } else {
+    cur.seek(a.pool, a.window, start.x, start.y, bad);
+  }
   cur.split(a);
   bool begins = cur.tile == cur.first;  // the unit at hand begins in this warp
 
@@ -484,7 +500,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
     const int unit = cur.b * a.units + cur.u;
     const Heads hd(a, cur.b, cur.r, cur.j, cur.chunk);
     const int unit_tiles = cur.end - cur.first;
-    const long long stop = at + (cur.end - cur.tile);  // where the unit ends on the line
+    const uint32_t stop = at + (cur.end - cur.tile);  // where the unit ends on the line
     count -= tiles;
     at += tiles;
     if (count > 0) {  // the next unit's query is on its way meanwhile
@@ -541,7 +557,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
 template <int D>
 __device__ __forceinline__ void write_out(const Args& a, int unit, int h, int d0, float M, float L, const float (&o)[D / 16]) {
   constexpr int E = D / 16;
-  const int b = unit / a.units, u = unit - b * a.units, rj = u / a.chunks, r = rj / a.pool.hk;
+  const int b = a.by_units.div(unit), u = unit - b * a.units, rj = a.by_chunks.div(u), r = a.by_hk.div(rj);
   const Heads hd(a, b, r, rj - r * a.pool.hk, u - rj * a.chunks);
   if (h >= hd.n) return;
   const Finish f(a, hd, h, M == -INFINITY ? 0.f : M, L);
@@ -554,6 +570,13 @@ __device__ __forceinline__ void write_out(const Args& a, int unit, int h, int d0
   else
     *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
   if (d0 == 0) a.lse[hd.row + h] = f.lse;
+}
+
+// A ticket: what this CTA's threads wrote before (a barrier lies between) is visible to whoever takes a later one.
+__device__ __forceinline__ int take(int32_t* ticket) {
+  int t;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(t) : "l"(ticket) : "memory");
+  return t;
 }
 
 // A CTA's part of a unit that crosses CTAs: it is part i of the n in CTAs first .. first + n - 1.
@@ -659,9 +682,7 @@ __device__ __forceinline__ void join(const Args& a, unsigned char* smem, const C
       // tickets of the CTA that has a group's first part: [0] of a unit that began earlier, [1] of one that begins there,
       // [2] of the groups of that one.  The last to come leaves 0.
       int32_t* ticket = a.tickets + 3 * (crossing[tid].first + x0) + (x0 == 0);
-      __threadfence();
-      is_last = atomicAdd(ticket, 1) == x1 - x0 - 1;
-      __threadfence();
+      is_last = take(ticket) == x1 - x0 - 1;
       if (is_last) *ticket = 0;
     }
     last[tid] = is_last;
@@ -692,9 +713,7 @@ __device__ __forceinline__ void join(const Args& a, unsigned char* smem, const C
       if (step > 1 || groups == 1) break;
       if (tid == 0) {
         int32_t* ticket = a.tickets + 3 * crossing[c].first + 2;
-        __threadfence();
-        last[c] = atomicAdd(ticket, 1) == groups - 1;
-        __threadfence();
+        last[c] = take(ticket) == groups - 1;
         if (last[c]) *ticket = 0;
       }
       __syncthreads();
@@ -712,106 +731,147 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
   constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long scan[kWarps];
-  __shared__ int at_seq[kWarps];
-  __shared__ long long at_rest[kWarps];
+  __shared__ int2 scan_any[kWarps];             // sequences with tiles, the most tiles of one
+  __shared__ int2 starts[kWarps];               // sequence, tiles (or units) into it
   __shared__ Part parts[2 * kWarps];
   __shared__ float2 stats[2 * kWarps][kHeads];  // reference, sum
   __shared__ Crossing crossing[2];              // of a unit that began in an earlier CTA, of one that begins here
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   grid_wait();
 
-  // ---- the CTA's stretch of the line
+  // ---- the line: tiles, sequences that have any, the most of one
+  const int cta = blockIdx.x;
   const int per = (a.n_seqs + kThreads - 1) / kThreads, s0 = tid * per, s1 = min(a.n_seqs, s0 + per);
   long long mine = 0;
+  int mine_any = 0, most = 0;
   bool bad = false;
-  for (int s = s0; s < s1; ++s) mine += tiles_of(a, s, bad);
+  for (int s = s0; s < s1; ++s) {
+    const int n = tiles_of(a, s, bad);
+    mine += n;
+    mine_any += n > 0;
+    most = max(most, n);
+  }
   if (bad) set_status(a.status, USP_ERR_BAD_PAGES);
   long long before = mine;
+  int before_any = mine_any;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, before, d);
-    if (lane >= d) before += x;
-  }
-  if (lane == 31) scan[w] = before;
-  __syncthreads();
-  long long all = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < w) before += scan[i];
-    all += scan[i];
-  }
-  before = (before - mine) * a.units;
-  const long long W = all * a.units;
-  const long long n_ctas = min(static_cast<long long>(gridDim.x), (W + kWarps * kLeastTiles - 1) / (kWarps * kLeastTiles));
-  const int cta = blockIdx.x;
-  // sequences without a visible token have no tile: their outputs are written here
-  for (int s = cta; s < a.n_seqs; s += gridDim.x)
-    if (tiles_of(a, s, bad) == 0) {
-      for (int i = tid; i < a.P * a.hq; i += kThreads) {
-        const int r = i / a.hq, h = i - r * a.hq;
-        a.lse[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq + h] = a.sinks ? gld(a.sinks + r * a.hq + h) : -INFINITY;
-      }
-      for (int i = tid; i < a.P * a.hq * (D / 8); i += kThreads) {
-        const int r = i / (a.hq * (D / 8)), x = i - r * (a.hq * (D / 8));
-        reinterpret_cast<uint4*>(a.o)[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq * (D / 8) + x] = make_uint4(0, 0, 0, 0);
-      }
+    const int y = __shfl_up_sync(0xffffffffu, before_any, d);
+    if (lane >= d) {
+      before += x;
+      before_any += y;
     }
-  if (cta >= n_ctas) return;
-  const long long begin = paged::stretch(W, n_ctas, cta), total = paged::stretch(W, n_ctas, cta + 1) - begin;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {  // where the warps' stretches begin
-    const long long x = begin + paged::stretch(total, kWarps, i);
-    if (x >= before && x < before + mine * a.units) {
-      long long rest = x - before;
-      int s = s0;
-      for (;; ++s) {
-        const long long n = static_cast<long long>(tiles_of(a, s, bad)) * a.units;
-        if (rest < n) break;
-        rest -= n;
-      }
-      at_seq[i] = s;
-      at_rest[i] = rest;
-    }
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    scan[w] = before;
+    scan_any[w] = make_int2(before_any, most);
   }
   if (tid < 2 * kWarps) parts[tid].unit = -1;
   if (tid < 2) crossing[tid].unit = -1;
   __syncthreads();
-  const long long at = begin + paged::stretch(total, kWarps, w);
-  const int count = static_cast<int>(begin + paged::stretch(total, kWarps, w + 1) - at);
-  if (count > 0) run_stretch<D, kE4m3>(a, smem, parts, stats, at_seq[w], at_rest[w], at, count);
+  long long all = 0;
+  int any = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < w) {
+      before += scan[i];
+      before_any += scan_any[i].x;
+    }
+    all += scan[i];
+    any += scan_any[i].x;
+    most = max(most, scan_any[i].y);
+  }
+  before -= mine;
+  before_any -= mine_any;
+  // sequences without a visible token have no tile: their outputs are written here
+  if (any < a.n_seqs)
+    for (int s = cta; s < a.n_seqs; s += gridDim.x)
+      if (tiles_of(a, s, bad) == 0) {
+        for (int i = tid; i < a.P * a.hq; i += kThreads) {
+          const int r = i / a.hq, h = i - r * a.hq;
+          a.lse[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq + h] = a.sinks ? gld(a.sinks + r * a.hq + h) : -INFINITY;
+        }
+        for (int i = tid; i < a.P * a.hq * (D / 8); i += kThreads) {
+          const int r = i / (a.hq * (D / 8)), x = i - r * (a.hq * (D / 8));
+          reinterpret_cast<uint4*>(a.o)[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq * (D / 8) + x] = make_uint4(0, 0, 0, 0);
+        }
+      }
+  if (all * a.units >= (1ll << 31)) {
+    set_status(a.status, USP_ERR_UNSUPPORTED);
+    return;
+  }
+  // Dealt out by tiles, or whole units to the warps where that makes the longest share kJoinTiles longer at
+  // most: then nothing is to be joined.
+  const uint32_t W = static_cast<uint32_t>(all) * a.units, U = static_cast<uint32_t>(any) * a.units;
+  if (W == 0) return;
+  const uint32_t warps = gridDim.x * kWarps;
+  const bool by_unit = static_cast<uint64_t>((U + warps - 1) / warps) * most <= (W + warps - 1) / warps + kJoinTiles;
+  const uint32_t things = by_unit ? U : W, n_ctas = min(gridDim.x, (things + kWarps - 1) / kWarps);
+  if (cta >= n_ctas) return;
+  const Deal line(things, n_ctas);
+  const uint32_t begin = line.begin(cta);
+  const Deal own(line.begin(cta + 1) - begin, kWarps);
+  const uint32_t lo = (by_unit ? before_any : static_cast<uint32_t>(before)) * a.units;
+  const uint32_t hi = lo + (by_unit ? mine_any : static_cast<uint32_t>(mine)) * a.units;
+#pragma unroll 1
+  for (int i = 0; i < kWarps; ++i) {  // where the warps' stretches begin
+    const uint32_t x = begin + own.begin(i);
+    if (x >= lo && x < hi) {
+      uint32_t rest = x - lo;
+      int s = s0;
+      for (;; ++s) {
+        const int tiles = tiles_of(a, s, bad);
+        const uint32_t n = (by_unit ? tiles > 0 : tiles) * a.units;
+        if (rest < n) break;
+        rest -= n;
+      }
+      starts[i] = make_int2(s, static_cast<int>(rest));
+    }
+  }
+  __syncthreads();
+  const uint32_t at = begin + own.begin(w), count = begin + own.begin(w + 1) - at;
+  if (count > 0) run_stretch<D, kE4m3>(a, smem, parts, stats, starts[w], by_unit, at, count);
+  if (by_unit) return;
 
   // ---- the warps' parts, in order: those of one unit next to each other
   __syncthreads();
   constexpr int E = D / 16;  // a slice has 16 threads for each head, D/16 elements each
   const int slice = tid >> 7, h = (tid >> 4) & 7, d0 = (tid & 15) * E;
-  for (int i = 0, group = 0; i < 2 * kWarps; ++group) {
+  // part k of lane k: which there are, and which begin another unit than the one before
+  const int unit_k = lane < 2 * kWarps ? parts[lane].unit : -1;
+  const uint32_t there = __ballot_sync(0xffffffffu, unit_k >= 0), below = there & ((1u << lane) - 1);
+  const int unit_before = __shfl_sync(0xffffffffu, unit_k, below ? 31 - __clz(below) : 0);
+  uint32_t starters = __ballot_sync(0xffffffffu, unit_k >= 0 && (below == 0 || unit_before != unit_k));
+  for (int group = 0; starters != 0; ++group) {
+    const int i = __ffs(starters) - 1;
+    starters &= starters - 1;
+    uint32_t members = there & ~((1u << i) - 1) & (starters ? (starters & -starters) - 1 : 0xffffffffu);
+    if (group % C::kSlices != slice) continue;
     const int unit = parts[i].unit;
+    float M = -INFINITY, L = 0.f, o[E] = {};
     int last = i;
-    for (int k = i + 1; k < 2 * kWarps; ++k)
-      if (unit >= 0 && parts[k].unit == unit) last = k;
-    if (unit >= 0 && group % C::kSlices == slice) {
-      float M = -INFINITY, L = 0.f, o[E] = {};
-      for (int k = i; k <= last; ++k)
-        if (parts[k].unit == unit)
-          add_part(stats[k][h],
-                   reinterpret_cast<const float*>(smem + (k & 1 ? k / 2 * C::kRing : kWarps * C::kRing + k / 2 * C::kKept)) + h * D + d0,
-                   M, L, o);
-      if constexpr (kE4m3) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= kDown;
-      }
-      const bool begins = parts[i].begins;
-      if (begins && parts[last].ends) {
-        write_out<D>(a, unit, h, d0, M, L, o);
-      } else {
-        const long long stop = parts[last].stop;
-        const int first = begins ? cta : static_cast<int>(paged::cta_of_last(W, n_ctas, stop - parts[last].tiles + 1));
-        Parts<D>{a, first, h, d0}.leave(cta - first, M, L, o);
-        if (h == 0 && d0 == 0)
-          crossing[begins] = Crossing{unit, first, static_cast<int>(paged::cta_of_last(W, n_ctas, stop)) - first + 1, cta - first};
-      }
+    for (; members != 0; members &= members - 1) {
+      last = __ffs(members) - 1;
+      add_part(stats[last][h],
+               reinterpret_cast<const float*>(smem + (last & 1 ? last / 2 * C::kRing : kWarps * C::kRing + last / 2 * C::kKept)) +
+                   h * D + d0,
+               M, L, o);
     }
-    i = last + 1;
+    if constexpr (kE4m3) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= kDown;
+    }
+    const bool begins = parts[i].begins;
+    if (begins && parts[last].ends) {
+      write_out<D>(a, unit, h, d0, M, L, o);
+    } else {
+      const uint32_t stop = parts[last].stop;
+      const int first = begins ? cta : static_cast<int>(line.owner(stop - parts[last].tiles));
+      Parts<D>{a, first, h, d0}.leave(cta - first, M, L, o);
+      if (h == 0 && d0 == 0) crossing[begins] = Crossing{unit, first, static_cast<int>(line.owner(stop - 1)) - first + 1, cta - first};
+    }
   }
   join<D, kE4m3>(a, smem, crossing);
 }
@@ -847,6 +907,9 @@ int launch_attn_decode(const usp_paged_cache& c, int Hq, int window_left, float 
   a.G = a.hq / a.pool.hk;
   a.chunks = (a.G + decode::kHeads - 1) / decode::kHeads;
   a.units = c.P * a.pool.hk * a.chunks;
+  a.by_units = FastDiv(static_cast<uint32_t>(a.units));
+  a.by_chunks = FastDiv(static_cast<uint32_t>(a.chunks));
+  a.by_hk = FastDiv(static_cast<uint32_t>(a.pool.hk));
   a.window = window_left;
   a.scale = scale;
   a.sinks = sinks;

@@ -106,10 +106,17 @@ struct Span {
   USP_HD int tiles() const { return end - first; }
 };
 
-// CTA c of n takes tiles [stretch(c), stretch(c + 1)) of W >= n; its warps share them the same way.
-USP_HD long long stretch(long long W, long long n, long long c) { return W * c / n; }
-// The CTA that has tile stop - 1: the smallest c with stretch(c + 1) >= stop.
-USP_HD long long cta_of_last(long long W, long long n, long long stop) { return (stop * n + W - 1) / W - 1; }
+// `all` things in a row dealt out to n: c has those from begin(c) to begin(c + 1), `each` or one more of them.
+struct Deal {
+  uint32_t each, more;
+  USP_HD Deal(uint32_t all, uint32_t n) : each(all / n), more(all - all / n * n) {}
+  USP_HD uint32_t begin(uint32_t c) const { return c * each + (c < more ? c : more); }
+  // who has thing x (of all >= n)
+  USP_HD uint32_t owner(uint32_t x) const {
+    const uint32_t head = more * (each + 1);
+    return x < head ? x / (each + 1) : more + (x - head) / each;
+  }
+};
 
 // A place on the line: tile `tile` of unit u of sequence b.
 struct Cursor {
@@ -124,11 +131,11 @@ struct Cursor {
     end = s.end;
   }
   // `rest` tiles into sequence `seq`
-  USP_HD void seek(const Pool& p, int window, int seq, long long rest, bool& bad) {
+  USP_HD void seek(const Pool& p, int window, int seq, uint32_t rest, bool& bad) {
     sequence(p, window, seq, bad);
-    const int n = end - first;
+    const uint32_t n = end - first;
     u = static_cast<int>(rest / n);
-    tile = first + static_cast<int>(rest - static_cast<long long>(u) * n);
+    tile = first + static_cast<int>(rest - u * n);
   }
   USP_HD void next(const Pool& p, int window, int units, bool& bad) {
     if (++tile < end) return;
