@@ -67,12 +67,11 @@ struct Cfg {
   static constexpr int kStage = 2 * 16 * kRow + kScaleBytes;     // one warp's share of a tile
   // One CTA per SM, of as many warps as its registers and shared memory hold: few CTAs leave few parts to join.
   static constexpr int kWarps = kRow == 256 ? 8 : kRow == 128 ? 12 : 16, kThreads = 32 * kWarps;
-  static constexpr int kSlices = kThreads / 128;                 // (16 threads for each of 8 heads)
   static constexpr int kStages = kRow == 64 ? 4 : 3;             // 100 to 130 KB of loads in flight per SM
   static constexpr int kRing = kStages * kStage;
   static constexpr int kKept = kHeads * D * 4;                   // a partial O of a warp
   static constexpr int kSmem = kWarps * (kRing + kKept);
-  static_assert(kRing >= kKept && kWarps * kRing >= kSlices * kKept, "partial Os fit into rings that are done with");
+  static_assert(kRing >= kKept && kSmem >= kFan * (kKept + kHeads * 8), "partial Os fit into shared memory that is done with");
 };
 
 struct Args {
@@ -155,6 +154,23 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 template <int D, bool kE4m3>
 __device__ __forceinline__ int first_column(int x, int g) {
   return kE4m3 ? (D / 8) * g + 8 * x : 64 * x + 8 * g;
+}
+
+// O and LSE of the sequences that see nothing.
+template <int D, int kThreads>
+__device__ __noinline__ void write_empty(const Args& a) {
+  bool bad = false;
+  for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
+    if (tiles_of(a, s, bad) != 0) continue;
+    for (int i = threadIdx.x; i < a.P * a.hq; i += kThreads) {
+      const int r = i / a.hq, h = i - r * a.hq;
+      a.lse[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq + h] = a.sinks ? gld(a.sinks + r * a.hq + h) : -INFINITY;
+    }
+    for (int i = threadIdx.x; i < a.P * a.hq * (D / 8); i += kThreads) {
+      const int r = i / (a.hq * (D / 8)), x = i - r * (a.hq * (D / 8));
+      reinterpret_cast<uint4*>(a.o)[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq * (D / 8) + x] = make_uint4(0, 0, 0, 0);
+    }
+  }
 }
 
 // A warp's part of a unit that it shares with others.
@@ -553,23 +569,46 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
   }
 }
 
-// Thread (h, d0)'s D/16 elements of a unit's head h.
+// A head's partial result in a warp: reference and sum, and D/32 elements of each lane.
 template <int D>
-__device__ __forceinline__ void write_out(const Args& a, int unit, int h, int d0, float M, float L, const float (&o)[D / 16]) {
-  constexpr int E = D / 16;
-  const int b = a.by_units.div(unit), u = unit - b * a.units, rj = a.by_chunks.div(u), r = a.by_hk.div(rj);
+struct Partial {
+  static constexpr int E = D / 32;
+  float M = -INFINITY, L = 0.f, o[E] = {};
+  __device__ __forceinline__ void add(float2 ml, const float* from) {
+    const float top = fmaxf(M, ml.x), ref = top == -INFINITY ? 0.f : top, f = ex2(M - ref), by = ex2(ml.x - ref);
+    M = top;
+    L = L * f + ml.y * by;
+    float y[E];
+    load(from, y);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * f + y[e] * by;
+  }
+  static __device__ __forceinline__ void load(const float* from, float (&y)[E]) {
+    if constexpr (E == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(from);
+      y[0] = x.x, y[1] = x.y, y[2] = x.z, y[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(from);
+      y[0] = x.x, y[1] = x.y;
+    }
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void write_out(const Args& a, int unit, int h, const Partial<D>& p) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, b = a.by_units.div(unit), u = unit - b * a.units, rj = a.by_chunks.div(u);
+  const int r = a.by_hk.div(rj);
   const Heads hd(a, b, r, rj - r * a.pool.hk, u - rj * a.chunks);
   if (h >= hd.n) return;
-  const Finish f(a, hd, h, M == -INFINITY ? 0.f : M, L);
-  uint32_t out[E / 2];
-#pragma unroll
-  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(o[e] * f.scale, o[e + 1] * f.scale);
-  uint16_t* to = a.o + (hd.row + h) * D + d0;
-  if constexpr (E == 8)
-    *reinterpret_cast<uint4*>(to) = make_uint4(out[0], out[1], out[2], out[3]);
+  const Finish f(a, hd, h, p.M == -INFINITY ? 0.f : p.M, p.L);
+  uint32_t* to = reinterpret_cast<uint32_t*>(a.o + (hd.row + h) * D) + lane * (E / 2);
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(p.o[0] * f.scale, p.o[1] * f.scale),
+                                               pack_bf16x2(p.o[2] * f.scale, p.o[3] * f.scale));
   else
-    *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
-  if (d0 == 0) a.lse[hd.row + h] = f.lse;
+    *to = pack_bf16x2(p.o[0] * f.scale, p.o[1] * f.scale);
+  if (lane == 0) a.lse[hd.row + h] = f.lse;
 }
 
 // A ticket: what this CTA's threads wrote before (a barrier lies between) is visible to whoever takes a later one.
@@ -584,96 +623,33 @@ struct Crossing {
   int unit, first, n, i;  // unit -1: none
 };
 
-// Parts in the workspace.  A CTA has two places: the first for a unit that began in an earlier CTA, the second for one
-// that begins in it.  (Loads and stores past L1: other CTAs' data.)
-template <int D>
-struct Parts {
-  static constexpr int E = D / 16;
-  const Args& a;
-  int first, h, d0;
-  __device__ __forceinline__ int64_t place(int x) const {
-    return static_cast<int64_t>(2 * (first + x) + (x == 0)) * kHeads + h;
-  }
-  __device__ __forceinline__ void leave(int x, float M, float L, const float (&o)[E]) const {
-    float* to = a.parts + place(x) * D + d0;
-#pragma unroll
-    for (int e = 0; e < E; e += 4) __stcg(reinterpret_cast<float4*>(to + e), make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
-    if (d0 == 0) __stcg(reinterpret_cast<float2*>(a.stats) + place(x), make_float2(M, L));
-  }
-  // x, x + step, ... below stop, put together
-  __device__ __forceinline__ void gather(int x, int stop, int step, float& M, float& L, float (&o)[E]) const {
-    M = -INFINITY;
-    L = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    constexpr int kAtOnce = 8;
-#pragma unroll 1
-    for (; x < stop; x += kAtOnce * step) {
-      float2 ml[kAtOnce];
-      float4 y[kAtOnce][E / 4];
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const int p = x + k * step;
-        ml[k] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int e = 0; e < E / 4; ++e) y[k][e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p < stop) {
-          ml[k] = __ldcg(reinterpret_cast<const float2*>(a.stats) + place(p));
-#pragma unroll
-          for (int e = 0; e < E / 4; ++e) y[k][e] = __ldcg(reinterpret_cast<const float4*>(a.parts + place(p) * D + d0) + e);
-        }
-      }
-      float top = M;
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
-      const float ref = top == -INFINITY ? 0.f : top, f = ex2(M - ref);
-      M = top;
-      L *= f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= f;
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const float by = ex2(ml[k].x - ref);
-        L += ml[k].y * by;
-#pragma unroll
-        for (int e = 0; e < E / 4; ++e) {
-          o[4 * e] += y[k][e].x * by;
-          o[4 * e + 1] += y[k][e].y * by;
-          o[4 * e + 2] += y[k][e].z * by;
-          o[4 * e + 3] += y[k][e].w * by;
-        }
-      }
-    }
-  }
-};
+// Part x of a unit that begins in CTA `first`: its place in the workspace.  A CTA has two: the first for a unit that began
+// in an earlier CTA, the second for one that begins in it.
+__device__ __forceinline__ int64_t place_of(int first, int x) { return 2 * (first + x) + (x == 0); }
 
-// One of several partial results in shared memory joins (M, L, o).
-template <int E>
-__device__ __forceinline__ void add_part(float2 ml, const float* from, float& M, float& L, float (&o)[E]) {
-  const float top = fmaxf(M, ml.x), ref = top == -INFINITY ? 0.f : top, f = ex2(M - ref), by = ex2(ml.x - ref);
-  M = top;
-  L = L * f + ml.y * by;
-#pragma unroll
-  for (int e = 0; e < E; e += 4) {
-    const float4 y = *reinterpret_cast<const float4*>(from + e);
-    o[e] = o[e] * f + y.x * by;
-    o[e + 1] = o[e + 1] * f + y.y * by;
-    o[e + 2] = o[e + 2] * f + y.z * by;
-    o[e + 3] = o[e + 3] * f + y.w * by;
-  }
+template <int D>
+__device__ __forceinline__ void leave(const Args& a, int first, int x, int h, const Partial<D>& p) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = place_of(first, x) * kHeads + h;
+  float* to = a.parts + row * D + lane * E;
+  if constexpr (E == 4)
+    __stcg(reinterpret_cast<float4*>(to), make_float4(p.o[0], p.o[1], p.o[2], p.o[3]));
+  else
+    __stcg(reinterpret_cast<float2*>(to), make_float2(p.o[0], p.o[1]));
+  if (lane == 0) __stcg(reinterpret_cast<float2*>(a.stats) + row, make_float2(p.M, p.L));
 }
 
 // The units that cross CTAs, in the CTAs that come last: every CTA leaves its part in the workspace and takes a ticket; of
 // kFan parts in a row the last CTA puts them together, and of these sums again the last one.  The
-// order of the additions goes by the positions, whoever is last.
+// order of the additions goes by the positions, whoever is last.  (All of this runs once: it is kept
+// short, for its instructions come from L2.)
 template <int D, bool kE4m3>
 __device__ __forceinline__ void join(const Args& a, unsigned char* smem, const Crossing* crossing) {
   using C = Cfg<D, kE4m3>;
-  constexpr int E = D / 16;
   __shared__ int last[2];
-  __shared__ float2 stats[C::kSlices][kHeads];
-  const int tid = threadIdx.x, slice = tid >> 7, h = (tid >> 4) & 7, d0 = (tid & 15) * E;
-  float* sums = reinterpret_cast<float*>(smem);  // [slice][head][d]
+  float2* stats = reinterpret_cast<float2*>(smem + kFan * C::kKept);  // [part][head], behind the parts
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   __syncthreads();  // the CTA's parts are written
   if (tid < 2) {
     int is_last = 0;
@@ -688,39 +664,44 @@ __device__ __forceinline__ void join(const Args& a, unsigned char* smem, const C
     last[tid] = is_last;
   }
   __syncthreads();
+#pragma unroll 1
   for (int c = 0; c < 2; ++c) {
-    if (!last[c]) continue;
-    const int n = crossing[c].n, unit = crossing[c].unit, groups = (n + kFan - 1) / kFan;
-    const Parts<D> parts{a, crossing[c].first, h, d0};
-    int x = crossing[c].i / kFan * kFan, stop = min(n, x + kFan), step = 1;
-    while (true) {
-      float M, L, o[E];
-      parts.gather(x + slice * step, stop, C::kSlices * step, M, L, o);
-#pragma unroll
-      for (int e = 0; e < E; e += 4)
-        *reinterpret_cast<float4*>(sums + (slice * kHeads + h) * D + d0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-      if (d0 == 0) stats[slice][h] = make_float2(M, L);
+    const int n = crossing[c].n, first = crossing[c].first, groups = (n + kFan - 1) / kFan;
+    int x0 = crossing[c].i / kFan * kFan, step = 1, parts = min(n - x0, kFan);
+    while (last[c]) {
+      // parts x0, x0 + step, ... into shared memory, past L1 (other CTAs wrote them)
+      constexpr int kPieces = kHeads * D / 4;
+      for (int i = tid; i < parts * kPieces; i += C::kThreads) {
+        const int p = i / kPieces;
+        cp_async(smem_u32(smem) + i * 16, a.parts + (place_of(first, x0 + p * step) * kPieces + (i - p * kPieces)) * 4);
+      }
+      cp_async_commit();
+      for (int i = tid; i < parts * kHeads; i += C::kThreads)
+        stats[i] =
+            __ldcg(reinterpret_cast<const float2*>(a.stats) + place_of(first, x0 + i / kHeads * step) * kHeads + i % kHeads);
+      cp_async_wait<0>();
       __syncthreads();
-      if (slice == 0) {
-#pragma unroll
-        for (int k = 1; k < C::kSlices; ++k) add_part(stats[k][h], sums + (k * kHeads + h) * D + d0, M, L, o);
-        if (step == 1 && groups > 1)
-          parts.leave(x, M, L, o);
+      const bool done = step > 1 || groups == 1;
+      if (w < kHeads) {
+        Partial<D> sum;
+        for (int p = 0; p < parts; ++p)
+          sum.add(stats[p * kHeads + w], reinterpret_cast<const float*>(smem) + (p * kHeads + w) * D + lane * (D / 32));
+        if (done)
+          write_out<D>(a, crossing[c].unit, w, sum);
         else
-          write_out<D>(a, unit, h, d0, M, L, o);
+          leave<D>(a, first, x0, w, sum);
       }
       __syncthreads();
-      if (step > 1 || groups == 1) break;
+      if (done) break;
       if (tid == 0) {
-        int32_t* ticket = a.tickets + 3 * crossing[c].first + 2;
+        int32_t* ticket = a.tickets + 3 * first + 2;
         last[c] = take(ticket) == groups - 1;
         if (last[c]) *ticket = 0;
       }
       __syncthreads();
-      if (!last[c]) break;
-      x = 0;
-      stop = n;
+      x0 = 0;
       step = kFan;
+      parts = groups;
     }
   }
 }
@@ -730,147 +711,105 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
   using C = Cfg<D, kE4m3>;
   constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long scan[kWarps];
-  __shared__ int2 scan_any[kWarps];             // sequences with tiles, the most tiles of one
-  __shared__ int2 starts[kWarps];               // sequence, tiles (or units) into it
   __shared__ Part parts[2 * kWarps];
   __shared__ float2 stats[2 * kWarps][kHeads];  // reference, sum
   __shared__ Crossing crossing[2];              // of a unit that began in an earlier CTA, of one that begins here
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  if (lane < 2) parts[2 * w + lane].unit = -1;
+  if (tid < 2) crossing[tid].unit = -1;
   grid_wait();
 
-  // ---- the line: tiles, sequences that have any, the most of one
-  const int cta = blockIdx.x;
-  const int per = (a.n_seqs + kThreads - 1) / kThreads, s0 = tid * per, s1 = min(a.n_seqs, s0 + per);
-  long long mine = 0;
-  int mine_any = 0, most = 0;
+  // ---- the line, in each warp: a lane adds up n_seqs / 32 sequences' tiles, and how many have any
+  constexpr uint32_t kMost = 1u << 26;  // of a lane (a table's row has less)
+  const int per = (a.n_seqs + 31) / 32, s0 = min(a.n_seqs, lane * per), s1 = min(a.n_seqs, s0 + per);
+  uint32_t mine = 0, mine_any = 0, most = 0;
   bool bad = false;
+#pragma unroll 4
   for (int s = s0; s < s1; ++s) {
-    const int n = tiles_of(a, s, bad);
-    mine += n;
+    const uint32_t n = tiles_of(a, s, bad);
+    mine = min(mine + n, kMost + 1);
     mine_any += n > 0;
     most = max(most, n);
   }
   if (bad) set_status(a.status, USP_ERR_BAD_PAGES);
-  long long before = mine;
-  int before_any = mine_any;
+  uint32_t before = mine, before_any = mine_any;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, before, d);
-    const int y = __shfl_up_sync(0xffffffffu, before_any, d);
+    const uint32_t x = __shfl_up_sync(0xffffffffu, before, d), y = __shfl_up_sync(0xffffffffu, before_any, d);
     if (lane >= d) {
       before += x;
       before_any += y;
     }
   }
+  const uint32_t all = __shfl_sync(0xffffffffu, before, 31), any = __shfl_sync(0xffffffffu, before_any, 31);
   most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 31) {
-    scan[w] = before;
-    scan_any[w] = make_int2(before_any, most);
-  }
-  if (tid < 2 * kWarps) parts[tid].unit = -1;
-  if (tid < 2) crossing[tid].unit = -1;
-  __syncthreads();
-  long long all = 0;
-  int any = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < w) {
-      before += scan[i];
-      before_any += scan_any[i].x;
-    }
-    all += scan[i];
-    any += scan_any[i].x;
-    most = max(most, scan_any[i].y);
-  }
-  before -= mine;
-  before_any -= mine_any;
   // sequences without a visible token have no tile: their outputs are written here
-  if (any < a.n_seqs)
-    for (int s = cta; s < a.n_seqs; s += gridDim.x)
-      if (tiles_of(a, s, bad) == 0) {
-        for (int i = tid; i < a.P * a.hq; i += kThreads) {
-          const int r = i / a.hq, h = i - r * a.hq;
-          a.lse[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq + h] = a.sinks ? gld(a.sinks + r * a.hq + h) : -INFINITY;
-        }
-        for (int i = tid; i < a.P * a.hq * (D / 8); i += kThreads) {
-          const int r = i / (a.hq * (D / 8)), x = i - r * (a.hq * (D / 8));
-          reinterpret_cast<uint4*>(a.o)[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq * (D / 8) + x] = make_uint4(0, 0, 0, 0);
-        }
-      }
-  if (all * a.units >= (1ll << 31)) {
+  if (any < a.n_seqs) write_empty<D, kThreads>(a);
+  const uint64_t tiles = static_cast<uint64_t>(all) * a.units;
+  if (__any_sync(0xffffffffu, mine > kMost) || tiles >= (1ull << 31)) {
     set_status(a.status, USP_ERR_UNSUPPORTED);
     return;
   }
+  if (tiles == 0) return;
   // Dealt out by tiles, or whole units to the warps where that makes the longest share kJoinTiles longer at
   // most: then nothing is to be joined.
-  const uint32_t W = static_cast<uint32_t>(all) * a.units, U = static_cast<uint32_t>(any) * a.units;
-  if (W == 0) return;
-  const uint32_t warps = gridDim.x * kWarps;
+  const uint32_t W = static_cast<uint32_t>(tiles), U = any * a.units, warps = gridDim.x * kWarps;
   const bool by_unit = static_cast<uint64_t>((U + warps - 1) / warps) * most <= (W + warps - 1) / warps + kJoinTiles;
   const uint32_t things = by_unit ? U : W, n_ctas = min(gridDim.x, (things + kWarps - 1) / kWarps);
   if (cta >= n_ctas) return;
-  const Deal line(things, n_ctas);
-  const uint32_t begin = line.begin(cta);
-  const Deal own(line.begin(cta + 1) - begin, kWarps);
-  const uint32_t lo = (by_unit ? before_any : static_cast<uint32_t>(before)) * a.units;
-  const uint32_t hi = lo + (by_unit ? mine_any : static_cast<uint32_t>(mine)) * a.units;
-#pragma unroll 1
-  for (int i = 0; i < kWarps; ++i) {  // where the warps' stretches begin
-    const uint32_t x = begin + own.begin(i);
-    if (x >= lo && x < hi) {
-      uint32_t rest = x - lo;
-      int s = s0;
-      for (;; ++s) {
-        const int tiles = tiles_of(a, s, bad);
-        const uint32_t n = (by_unit ? tiles > 0 : tiles) * a.units;
-        if (rest < n) break;
-        rest -= n;
-      }
-      starts[i] = make_int2(s, static_cast<int>(rest));
+  const Deal line(things, n_ctas * kWarps);
+  const uint32_t at = line.begin(cta * kWarps + w), count = line.begin(cta * kWarps + w + 1) - at;
+  if (count > 0) {
+    const uint32_t hi = (by_unit ? before_any : before) * a.units, lo = hi - (by_unit ? mine_any : mine) * a.units;
+    const bool here = at >= lo && at < hi;
+    int s = s0;
+    uint32_t rest = at - lo;
+    while (here) {
+      const uint32_t n = tiles_of(a, s, bad), things_of = (by_unit ? n > 0 : n) * a.units;
+      if (rest < things_of) break;
+      rest -= things_of;
+      ++s;
     }
+    const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    const int2 start = make_int2(__shfl_sync(0xffffffffu, s, from), __shfl_sync(0xffffffffu, rest, from));
+    run_stretch<D, kE4m3>(a, smem, parts, stats, start, by_unit, at, count);
   }
-  __syncthreads();
-  const uint32_t at = begin + own.begin(w), count = begin + own.begin(w + 1) - at;
-  if (count > 0) run_stretch<D, kE4m3>(a, smem, parts, stats, starts[w], by_unit, at, count);
   if (by_unit) return;
 
   // ---- the warps' parts, in order: those of one unit next to each other
   __syncthreads();
-  constexpr int E = D / 16;  // a slice has 16 threads for each head, D/16 elements each
-  const int slice = tid >> 7, h = (tid >> 4) & 7, d0 = (tid & 15) * E;
   // part k of lane k: which there are, and which begin another unit than the one before
   const int unit_k = lane < 2 * kWarps ? parts[lane].unit : -1;
   const uint32_t there = __ballot_sync(0xffffffffu, unit_k >= 0), below = there & ((1u << lane) - 1);
   const int unit_before = __shfl_sync(0xffffffffu, unit_k, below ? 31 - __clz(below) : 0);
   uint32_t starters = __ballot_sync(0xffffffffu, unit_k >= 0 && (below == 0 || unit_before != unit_k));
+  constexpr int kSets = kWarps / kHeads;  // a warp for each head of a unit
   for (int group = 0; starters != 0; ++group) {
     const int i = __ffs(starters) - 1;
     starters &= starters - 1;
     uint32_t members = there & ~((1u << i) - 1) & (starters ? (starters & -starters) - 1 : 0xffffffffu);
-    if (group % C::kSlices != slice) continue;
-    const int unit = parts[i].unit;
-    float M = -INFINITY, L = 0.f, o[E] = {};
+    if (w / kHeads != group % kSets) continue;
+    const int unit = parts[i].unit, h = w % kHeads;
+    Partial<D> sum;
     int last = i;
     for (; members != 0; members &= members - 1) {
       last = __ffs(members) - 1;
-      add_part(stats[last][h],
-               reinterpret_cast<const float*>(smem + (last & 1 ? last / 2 * C::kRing : kWarps * C::kRing + last / 2 * C::kKept)) +
-                   h * D + d0,
-               M, L, o);
+      sum.add(stats[last][h],
+              reinterpret_cast<const float*>(smem + (last & 1 ? last / 2 * C::kRing : kWarps * C::kRing + last / 2 * C::kKept)) +
+                  h * D + lane * (D / 32));
     }
     if constexpr (kE4m3) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= kDown;
+      for (int e = 0; e < D / 32; ++e) sum.o[e] *= kDown;
     }
     const bool begins = parts[i].begins;
     if (begins && parts[last].ends) {
-      write_out<D>(a, unit, h, d0, M, L, o);
+      write_out<D>(a, unit, h, sum);
     } else {
       const uint32_t stop = parts[last].stop;
-      const int first = begins ? cta : static_cast<int>(line.owner(stop - parts[last].tiles));
-      Parts<D>{a, first, h, d0}.leave(cta - first, M, L, o);
-      if (h == 0 && d0 == 0) crossing[begins] = Crossing{unit, first, static_cast<int>(line.owner(stop - 1)) - first + 1, cta - first};
+      const int first = begins ? cta : static_cast<int>(line.owner(stop - parts[last].tiles)) / kWarps;
+      leave<D>(a, first, cta - first, h, sum);
+      if (h == 0 && lane == 0) crossing[begins] = Crossing{unit, first, static_cast<int>(line.owner(stop - 1)) / kWarps - first + 1, cta - first};
     }
   }
   join<D, kE4m3>(a, smem, crossing);
