@@ -156,19 +156,20 @@ __device__ __forceinline__ int first_column(int x, int g) {
   return kE4m3 ? (D / 8) * g + 8 * x : 64 * x + 8 * g;
 }
 
-// O and LSE of the sequences that see nothing.
-template <int D, int kThreads>
-__device__ __noinline__ void write_empty(const Args& a) {
+// O and LSE of the sequences first, first + step, ... that see nothing, in a warp.
+template <int D>
+__device__ __noinline__ void write_empty(const Args& a, int first, int step) {
+  const int lane = threadIdx.x & 31;
   bool bad = false;
-  for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
+  for (int s = first; s < a.n_seqs; s += step) {
     if (tiles_of(a, s, bad) != 0) continue;
-    for (int i = threadIdx.x; i < a.P * a.hq; i += kThreads) {
-      const int r = i / a.hq, h = i - r * a.hq;
-      a.lse[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq + h] = a.sinks ? gld(a.sinks + r * a.hq + h) : -INFINITY;
+    for (int r = 0; r < a.P; ++r) {
+      uint4* o = reinterpret_cast<uint4*>(a.o + (static_cast<int64_t>(r) * a.n_seqs + s) * a.hq * D);
+      for (int i = lane; i < a.hq * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
     }
-    for (int i = threadIdx.x; i < a.P * a.hq * (D / 8); i += kThreads) {
-      const int r = i / (a.hq * (D / 8)), x = i - r * (a.hq * (D / 8));
-      reinterpret_cast<uint4*>(a.o)[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq * (D / 8) + x] = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < a.P * a.hq; i += 32) {
+      const int r = i / a.hq;
+      a.lse[(static_cast<int64_t>(r) * a.n_seqs + s) * a.hq + (i - r * a.hq)] = a.sinks ? gld(a.sinks + i) : -INFINITY;
     }
   }
 }
@@ -743,20 +744,21 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
   }
   const uint32_t all = __shfl_sync(0xffffffffu, before, 31), any = __shfl_sync(0xffffffffu, before_any, 31);
   most = __reduce_max_sync(0xffffffffu, most);
-  // sequences without a visible token have no tile: their outputs are written here
-  if (any < a.n_seqs) write_empty<D, kThreads>(a);
   const uint64_t tiles = static_cast<uint64_t>(all) * a.units;
   if (__any_sync(0xffffffffu, mine > kMost) || tiles >= (1ull << 31)) {
     set_status(a.status, USP_ERR_UNSUPPORTED);
     return;
   }
-  if (tiles == 0) return;
   // Dealt out by tiles, or whole units to the warps where that makes the longest share kJoinTiles longer at
   // most: then nothing is to be joined.
   const uint32_t W = static_cast<uint32_t>(tiles), U = any * a.units, warps = gridDim.x * kWarps;
   const bool by_unit = static_cast<uint64_t>((U + warps - 1) / warps) * most <= (W + warps - 1) / warps + kJoinTiles;
   const uint32_t things = by_unit ? U : W, n_ctas = min(gridDim.x, (things + kWarps - 1) / kWarps);
-  if (cta >= n_ctas) return;
+  // sequences that see nothing have no tile: CTAs without work write their outputs, or all when they are done
+  if (cta >= n_ctas) {
+    if (any < a.n_seqs) write_empty<D>(a, (cta - n_ctas) * kWarps + w, (gridDim.x - n_ctas) * kWarps);
+    return;
+  }
   const Deal line(things, n_ctas * kWarps);
   const uint32_t at = line.begin(cta * kWarps + w), count = line.begin(cta * kWarps + w + 1) - at;
   if (count > 0) {
@@ -774,6 +776,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
     const int2 start = make_int2(__shfl_sync(0xffffffffu, s, from), __shfl_sync(0xffffffffu, rest, from));
     run_stretch<D, kE4m3>(a, smem, parts, stats, start, by_unit, at, count);
   }
+  if (any < a.n_seqs && n_ctas == gridDim.x) write_empty<D>(a, cta * kWarps + w, warps);
   if (by_unit) return;
 
   // ---- the warps' parts, in order: those of one unit next to each other
