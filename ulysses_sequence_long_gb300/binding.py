@@ -533,14 +533,12 @@ def _sized(t, name, dtype, n, like):
     return ptr
 
 
-def call_on(device: torch.device, stream, where, *args):
-    """``where(*args, stream)`` with `device` current, on `stream` or the device's current one."""
-    index = device.index
+def run_on(index: int, stream, fn, where, *args):
+    """``fn(*args, stream)`` (the library's ``where``) with device `index` current, on `stream` or its current one."""
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(index)
     else:
         stream = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    fn = getattr(_lib or load(), where)
     if torch._C._cuda_getDevice() == index:
         rc = fn(*args, stream)
     else:
@@ -548,6 +546,10 @@ def call_on(device: torch.device, stream, where, *args):
             rc = fn(*args, stream)
     if rc != USP_OK:
         raise UspError(rc, where)
+
+
+def call_on(device: torch.device, stream, where, *args):
+    run_on(device.index, stream, getattr(load(), where), where, *args)
 
 
 def rope_params(Hq, Hkv, D, positions, freqs, tokens, n_axes=1, axes=None, interleaved=False) -> RopeParams:

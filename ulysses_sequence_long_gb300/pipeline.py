@@ -121,66 +121,80 @@ class Rotary:
         self.freqs, self.axes, self.n_axes, self.interleaved = freqs, axes, int(n_axes), bool(interleaved)
         self.status = torch.zeros((1,), dtype=torch.int32, device=freqs.device)
         self.device, self._index = freqs.device, freqs.get_device()
+        lib = B_.load()
+        self._fwd, self._bwd = lib.usp_rope_fwd, lib.usp_rope_bwd
         self._seen = {}
+        self._n_pairs = freqs.numel()
+        self._find()
 
-    def _check(self, t, name, like):
-        if like is not None and t.shape != like.shape:
-            raise ValueError(f"{name} must have the shape {tuple(like.shape)}, got {tuple(t.shape)}")
-        if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == self._index
-                and t.is_contiguous()):
-            if B_._dev(t, name, torch.bfloat16) is None:
-                raise TypeError(f"{name} must be a CUDA tensor")
-            raise ValueError(f"{name} is on {t.device}, the frequencies on {self.device}")
-        return t.data_ptr()
+    def _find(self):
+        """The addresses of the rotation's tensors, for the calls to come."""
+        at, n = self._at, self._n_pairs
+        self._tables = (at(self.freqs, "freqs", torch.float32, n),
+                        None if self.axes is None else at(self.axes, "axes", torch.int32, n))
+        self._status = at(self.status, "status", torch.int32, 1)
+        self._found = tuple((name, getattr(self, name), getattr(self, name).data_ptr())
+                            for name in ("freqs", "axes", "status") if getattr(self, name) is not None)
 
-    def _params(self, q, k, positions):
-        """This call's own structure (threads may share a Rotary): sizes that go by the shapes, addresses of now."""
-        key = (q.shape, None if k is None else k.shape, positions.numel())
-        p = self._seen.get(key)
+    def _plan(self, q, k, positions):
+        """Sizes of a call, by the shapes."""
+        if q.dim() < 2 or (k is not None and (k.dim() < 2 or k.shape[-1] != q.shape[-1])):
+            raise ValueError("q and k must be [..., heads, D]")
+        Hq, D = q.shape[-2:]
+        tokens, Hkv = q.numel() // max(1, Hq * D), 0 if k is None else k.shape[-2]
+        if k is not None and k.numel() != tokens * Hkv * D:
+            raise ValueError(f"q has {tokens} tokens, k {k.numel() // max(1, Hkv * D)}")
+        n = positions.numel()
+        if n == 0 or n % self.n_axes or tokens % (n // self.n_axes):
+            raise ValueError(f"positions must be [{self.n_axes}][n] with n tokens or a divisor of their {tokens}, "
+                             f"got {n} elements")
+        return B_.RopeParams(tokens, Hq, Hkv, D, self.n_axes, n // self.n_axes, self._n_pairs, int(self.interleaved))
+
+    def _at(self, t, name, dtype, n):
+        if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and t.get_device() == self._index and t.is_contiguous():
+            return t.data_ptr()
+        if B_._dev(t, name, dtype) is None:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} must have {n} elements on {self.device}, got {tuple(t.shape)} on {t.device}")
+
+    def _turn(self, fn, where, q, k, positions, out, stream):
+        shapes = (q.shape, None if k is None else k.shape, positions.numel())
+        p = self._seen.get(shapes)
         if p is None:
-            if q.dim() < 2 or (k is not None and (k.dim() < 2 or k.shape[-1] != q.shape[-1])):
-                raise ValueError("q and k must be [..., heads, D]")
-            Hq, D = q.shape[-2:]
-            tokens, Hkv = q.numel() // max(1, Hq * D), 0 if k is None else k.shape[-2]
-            if k is not None and k.numel() != tokens * Hkv * D:
-                raise ValueError(f"q has {tokens} tokens, k {k.numel() // max(1, Hkv * D)}")
-            if positions.numel() == 0 or positions.numel() % self.n_axes or tokens % (positions.numel() // self.n_axes):
-                raise ValueError(f"positions must be [{self.n_axes}][n] with n tokens or a divisor of their {tokens}, "
-                                 f"got {positions.numel()} elements")
-            p = B_.RopeParams(tokens, Hq, Hkv, D, self.n_axes, positions.numel() // self.n_axes, self.freqs.numel(),
-                              int(self.interleaved))
+            p = self._plan(q, k, positions)
             if len(self._seen) < 1024:
-                self._seen[key] = p
-        p = B_.RopeParams.from_buffer_copy(p)
-        pos, freqs, axes = positions, self.freqs, self.axes
-        for t, name, dtype in ((pos, "positions", torch.int32), (freqs, "freqs", torch.float32)) + (
-                () if axes is None else ((axes, "axes", torch.int32),)):
-            if not (t.dtype is dtype and t.get_device() == self._index and t.is_contiguous()):
-                B_._dev(t, name, dtype)
-                raise ValueError(f"{name} is on {t.device}, the frequencies on {self.device}")
-        if freqs.numel() != p.n_pairs or (axes is not None and axes.numel() != p.n_pairs):
-            raise ValueError("freqs or axes have changed their size")
-        p.positions, p.freqs, p.axes = pos.data_ptr(), freqs.data_ptr(), None if axes is None else axes.data_ptr()
-        return p
-
-    def _turn(self, where, q, k, positions, out, stream):
+                self._seen[shapes] = p
+        p = B_.RopeParams.from_buffer_copy(p)   # this call's own (threads may share a Rotary)
+        mine, bf, index, at = self.__dict__, torch.bfloat16, self._index, self._at
+        for name, t, was in self._found:
+            if mine[name] is not t or t.data_ptr() != was:   # a tensor, or the storage under one, was exchanged
+                self._find()
+                break
+        p.freqs, p.axes = self._tables
+        p.positions = at(positions, "positions", torch.int32, shapes[2])
         if out is None:
             out = (torch.empty_like(q, memory_format=torch.contiguous_format),
                    None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format))
-        p = self._params(q, k, positions)
-        ptrs = [self._check(q, "q", None), None if k is None else self._check(k, "k", None),
-                self._check(out[0], "the output of q", q), None if k is None else self._check(out[1], "the output of k", k)]
-        B_.call_on(self.device, stream, where, ctypes.byref(p), *ptrs, self.status.data_ptr())
+        y, yk = out
+        if (k is not None and q.dtype is bf and k.dtype is bf and y.dtype is bf and yk.dtype is bf
+                and q.get_device() == index and k.get_device() == index and y.get_device() == index
+                and yk.get_device() == index and q.is_contiguous() and k.is_contiguous() and y.is_contiguous()
+                and yk.is_contiguous() and y.numel() == q.numel() and yk.numel() == k.numel()):
+            x, xk, y, yk = q.data_ptr(), k.data_ptr(), y.data_ptr(), yk.data_ptr()
+        else:
+            x, y = at(q, "q", bf, q.numel()), at(y, "the output of q", bf, q.numel())
+            xk, yk = (None, None) if k is None else (at(k, "k", bf, k.numel()), at(yk, "the output of k", bf, k.numel()))
+        B_.run_on(index, stream, fn, where, ctypes.byref(p), x, xk, y, yk, self._status)
         return out
 
     def forward(self, q, k, positions, out=None, stream=None):
         """(q, k) turned: bf16 ``[..., H, D]`` each (k may be None), positions int32 ``[n_axes][tokens]``, or of a
         divisor of the tokens, over which they repeat.  ``out``: the tensors to write, which may be q and k."""
-        return self._turn("usp_rope_fwd", q, k, positions, out, stream)
+        return self._turn(self._fwd, "usp_rope_fwd", q, k, positions, out, stream)
 
     def backward(self, dq, dk, positions, out=None, stream=None):
         """The gradients of ``forward``'s outputs to those of its inputs (``out`` may be dq and dk)."""
-        return self._turn("usp_rope_bwd", dq, dk, positions, out, stream)
+        return self._turn(self._bwd, "usp_rope_bwd", dq, dk, positions, out, stream)
 
     def read_status(self) -> int:
         return int(self.status.item())

@@ -26,8 +26,7 @@ _BF, _F8, _I32, _F32, _U8 = torch.bfloat16, torch.float8_e4m3fn, torch.int32, to
 
 def _where(t, name, dtype, n, index):
     """The address of `t`, which has to be contiguous, of `n` elements of `dtype`, on device `index`."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and t.get_device() == index
-            and t.is_contiguous()):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
     if B_._dev(t, name, dtype) is None:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -62,43 +61,62 @@ class PagedCache:
         self._index = self.status.get_device()
         self._fixed = B_.PagedCacheStruct(P, Hkv, D, n_pages, page_size, 0, 0,
                                           B_.USP_CACHE_E4M3 if eight else B_.USP_CACHE_BF16)
+        lib = B_.load()
+        self._append, self._read = lib.usp_cache_append, lib.usp_cache_read
+        self._find()
 
-    def _struct(self, block_table, lens) -> B_.PagedCacheStruct:
-        """This call's own structure: threads may use one cache at once, and buffers may have been exchanged."""
-        c = B_.PagedCacheStruct.from_buffer_copy(self._fixed)
-        index, n = self._index, self.P * self.n_pages * self.hk * self.page_size
-        if block_table.dim() != 2 or lens.dim() != 1:
-            raise ValueError("block_table must be [sequences][max_pages], lens [sequences]")
-        c.n_seqs, c.max_pages = lens.shape[0], block_table.shape[1]
+    def _find(self):
+        """The addresses of the pool's tensors, which have to be of their sizes and types, for the calls to come."""
+        c, index, n = self._fixed, self._index, self.P * self.n_pages * self.hk * self.page_size
         c.k_pages = _where(self.k_pages, "k_pages", self.dtype, n * self.D, index)
         c.v_pages = _where(self.v_pages, "v_pages", self.dtype, n * self.D, index)
         if self.dtype is _F8:
             c.k_scales = _where(self.k_scales, "k_scales", _U8, n, index)
             c.v_scales = _where(self.v_scales, "v_scales", _U8, n, index)
-        c.block_table = _where(block_table, "block_table", _I32, c.n_seqs * c.max_pages, index)
-        c.lens = _where(lens, "lens", _I32, c.n_seqs, index)
-        return c
+        self._status = _where(self.status, "status", _I32, 1, index)
+        names = ("k_pages", "v_pages", "status") + (("k_scales", "v_scales") if self.dtype is _F8 else ())
+        self._found = tuple((name, getattr(self, name), getattr(self, name).data_ptr()) for name in names)
 
-    def _move(self, where, k, v, block_table, lens, cu_seqlens, stream):
+    def _struct(self, block_table, lens) -> B_.PagedCacheStruct:
+        """This call's own structure (threads may use one cache at once), with the addresses that the tensors have now."""
+        mine = self.__dict__
+        for name, t, at in self._found:
+            if mine[name] is not t or t.data_ptr() != at:   # a tensor, or the storage under one, was exchanged
+                self._find()
+                break
+        c = B_.PagedCacheStruct.from_buffer_copy(self._fixed)
+        index = self._index
+        if (block_table.dtype is _I32 and lens.dtype is _I32 and block_table.get_device() == index
+                and lens.get_device() == index and block_table.is_contiguous() and lens.is_contiguous()
+                and block_table.dim() == 2 and lens.dim() == 1 and block_table.size(0) == lens.size(0)):
+            c.n_seqs, c.max_pages = lens.size(0), block_table.size(1)
+            c.block_table, c.lens = block_table.data_ptr(), lens.data_ptr()
+            return c
+        if block_table.dim() != 2 or lens.dim() != 1:
+            raise ValueError("block_table must be [sequences][max_pages], lens [sequences]")
+        _where(lens, "lens", _I32, lens.numel(), index)
+        _where(block_table, "block_table", _I32, lens.numel() * block_table.shape[1], index)
+        raise ValueError(f"block_table has {block_table.shape[0]} rows, lens {lens.shape[0]} sequences")
+
+    def _move(self, fn, where, k, v, block_table, lens, cu_seqlens, stream):
         c = self._struct(block_table, lens)
-        per = self.P * self.hk * self.D
+        per, index = self.P * self.hk * self.D, self._index
         n = k.numel()
         if n == 0 or n % per != 0:
             raise ValueError(f"k must be [{self.P}][tokens][{self.hk}][{self.D}], got {tuple(k.shape)}")
-        kp, vp = _where(k, "k", _BF, n, self._index), _where(v, "v", _BF, n, self._index)
+        kp, vp = _where(k, "k", _BF, n, index), _where(v, "v", _BF, n, index)
         cu = None
         if cu_seqlens is not None:  # (the boundaries of a packed batch have room for more documents)
             if cu_seqlens.numel() <= c.n_seqs:
                 raise ValueError(f"cu_seqlens must have at least {c.n_seqs + 1} elements, got {cu_seqlens.numel()}")
-            cu = _where(cu_seqlens, "cu_seqlens", _I32, cu_seqlens.numel(), self._index)
-        B_.call_on(self.device, stream, where, ctypes.byref(c), kp, vp, n // per, cu,
-                   _where(self.status, "status", _I32, 1, self._index))
+            cu = _where(cu_seqlens, "cu_seqlens", _I32, cu_seqlens.numel(), index)
+        B_.run_on(index, stream, fn, where, ctypes.byref(c), kp, vp, n // per, cu, self._status)
 
     def append(self, k, v, block_table, lens, cu_seqlens=None, stream=None):
         """Write the last tokens of each sequence: k, v bf16 ``[P][tokens][heads of a rank][D]`` (head layout), tokens
         ``[cu_seqlens[s], cu_seqlens[s+1])`` of sequence s, or one of each sequence without ``cu_seqlens``.
         ``cu_seqlens`` and ``k_head``, ``v_head`` of a layer that ran a packed batch are these."""
-        self._move("usp_cache_append", k, v, block_table, lens, cu_seqlens, stream)
+        self._move(self._append, "usp_cache_append", k, v, block_table, lens, cu_seqlens, stream)
 
     def read(self, block_table, lens, cu_seqlens=None, out=None, tokens: Optional[int] = None, stream=None):
         """The way back: (k, v) of the last tokens of each sequence, into ``out``, or into new tensors of ``tokens``
@@ -109,7 +127,7 @@ class PagedCache:
                     raise ValueError("read needs out or tokens beside cu_seqlens (their sum is on the device)")
                 tokens = lens.shape[0]
             out = tuple(torch.zeros((self.P, tokens, self.hk, self.D), dtype=_BF, device=self.device) for _ in range(2))
-        self._move("usp_cache_read", out[0], out[1], block_table, lens, cu_seqlens, stream)
+        self._move(self._read, "usp_cache_read", out[0], out[1], block_table, lens, cu_seqlens, stream)
         return out
 
     def read_status(self) -> int:
@@ -143,6 +161,8 @@ class DecodeAttention:
         if n == 0:
             raise ValueError("the library has no such attention: D 64 or 128, page_size a multiple of 16, Hq <= 1024")
         self._ws = torch.zeros((n,), dtype=_U8, device=dev)
+        self._ws_bytes = n
+        self._decode = B_.load().usp_attn_decode
         self._views = {}
         self.lse = None
 
@@ -163,10 +183,10 @@ class DecodeAttention:
         prm = c._struct(block_table, lens)
         n = prm.n_seqs
         o, lse = self._out(n)
-        B_.call_on(c.device, stream, "usp_attn_decode", ctypes.byref(prm), self.Hq, self.window_left,
-                   self.softmax_scale, None if sinks is None else _where(sinks, "sinks", _F32, self.Hq, index),
-                   _where(q, "q", _BF, n * self.Hq * c.D, index), o.data_ptr(), lse.data_ptr(), self._ws.data_ptr(),
-                   self._ws.numel(), _where(c.status, "status", _I32, 1, index))
+        B_.run_on(index, stream, self._decode, "usp_attn_decode", ctypes.byref(prm), self.Hq, self.window_left,
+                  self.softmax_scale, None if sinks is None else _where(sinks, "sinks", _F32, self.Hq, index),
+                  _where(q, "q", _BF, n * self.Hq * c.D, index), o.data_ptr(), lse.data_ptr(), self._ws.data_ptr(),
+                  self._ws_bytes, c._status)
         self.lse = lse
         return o
 
