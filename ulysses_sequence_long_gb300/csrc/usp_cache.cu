@@ -20,13 +20,14 @@
 namespace usp {
 namespace cache {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 struct Geom {
   paged::Pool pool;
   int tokens;
   uint32_t chunks;         // groups of 32 / (D/16) tokens
   uint32_t items;          // P * chunks * hk
+  FastDiv by_hk, by_chunks;
   const int32_t* cu;       // nullptr: token i is sequence i's last
 };
 
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_kernel(Geom g, uint4* k, ui
   check_boundaries(g, status);
   const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (item >= g.items) return;
-  const uint32_t rc = item / g.pool.hk, j = item - rc * g.pool.hk, r = rc / g.chunks, c = rc - r * g.chunks;
+  const uint32_t rc = g.by_hk.div(item), j = item - rc * g.pool.hk, r = g.by_chunks.div(rc), c = rc - r * g.chunks;
   const int i = static_cast<int>(c) * TPW + lane / LPR;
   const bool have = i < g.tokens;
   const int64_t tok = ((static_cast<int64_t>(r) * g.tokens + i) * g.pool.hk + j) * V + 2 * t;
@@ -201,6 +202,8 @@ int launch_cache_move(const usp_paged_cache& c, void* k, void* v, int tokens, co
   const int per_warp = 32 / (c.D / 16);
   g.chunks = static_cast<uint32_t>((static_cast<int64_t>(tokens) + per_warp - 1) / per_warp);
   g.items = static_cast<uint32_t>(c.P) * g.chunks * static_cast<uint32_t>(g.pool.hk);
+  g.by_hk = FastDiv(static_cast<uint32_t>(g.pool.hk));
+  g.by_chunks = FastDiv(g.chunks);
   const unsigned ctas = (g.items + cache::kWarps - 1) / cache::kWarps;
   void (*kern)(cache::Geom, uint4*, uint4*, int32_t*) = nullptr;
   const bool e = c.dtype == USP_CACHE_E4M3;
