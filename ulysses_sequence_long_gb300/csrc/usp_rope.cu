@@ -58,19 +58,13 @@ template <int D, bool kInterleaved, bool kBack>
 __global__ void __launch_bounds__(32 * kWarps) rope_kernel(Geom g, const uint4* q, const uint4* k, uint4* q_out,
                                                            uint4* k_out, int32_t* status) {
   constexpr int LPR = D / 16, RPW = 32 / LPR, PPL = 8 / RPW;  // lanes per row, rows at once, pairs a lane prepares
-  __shared__ float2 turns[kWarps][LPR * 8];
+  __shared__ __align__(16) float2 turns[kWarps][LPR * 8];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, t = lane % LPR, rg = lane / LPR;
   const int rot_lanes = g.n_pairs / 8;
   const bool rot = t < rot_lanes;
-  // the lane's two vectors within a row
-  int va, vb;
-  if (kInterleaved || !rot) {
-    va = 2 * t;
-    vb = 2 * t + 1;
-  } else {
-    va = t;
-    vb = t + rot_lanes;
-  }
+  // the lane's two vectors within a row: neighbouring lanes have neighbouring ones (half a row's vectors apart, so that a
+  // pair's two elements meet, and pairs of neighbours do anyway)
+  const int va = rot ? t : rot_lanes + t, vb = rot ? t + rot_lanes : LPR + t;
   grid_wait();
   // the pairs whose angles this lane prepares: rg * PPL .. of its row position t
   unsigned long long frac[PPL];
@@ -126,7 +120,8 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(Geom g, const uint4* 
     float2 cs[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 x = reinterpret_cast<const float4*>(&turns[w][t * 8])[i];
+      const int p = kInterleaved ? 4 * (i < 2 ? va : vb) + 2 * (i & 1) : 8 * t + 2 * i;
+      const float4 x = *reinterpret_cast<const float4*>(&turns[w][p]);
       cs[2 * i] = make_float2(x.x, x.y);
       cs[2 * i + 1] = make_float2(x.z, x.w);
     }
@@ -164,7 +159,7 @@ template <int D>
 int launch(const Geom& g, const void* q, const void* k, void* q_out, void* k_out, bool interleaved, bool back,
            int32_t* status, cudaStream_t st) {
   const int ctas = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(g.items) + kWarps - 1) / kWarps,
-                                                      static_cast<int64_t>(device_sm_count()) * 16));
+                                                      static_cast<int64_t>(device_sm_count()) * 64));
   auto* kern = interleaved ? (back ? rope_kernel<D, true, true> : rope_kernel<D, true, false>)
                            : (back ? rope_kernel<D, false, true> : rope_kernel<D, false, false>);
   return launch_chained(kern, dim3(ctas), 32 * kWarps, 0, 1, st, g, static_cast<const uint4*>(q),
