@@ -203,7 +203,7 @@ def _decode_case(lens, G, Hkv, D, P, page, dtype, window=-1, sinks=False, seed=0
     return c, table, ln, k, v, q, z, att
 
 
-def _check_decode(c, lens, k, v, q, z, att, o, lse, scale=0.0):
+def _check_decode(c, lens, k, v, q, z, att, o, lse, scale=0.0, only=None):
     """Against the oracle over the values that the cache holds.  Bounds, per output, with n visible keys:
     a score's fp32 sum of D products (2 D 2^-24 of their sizes' sum; tensor cores cut, so a whole step each) and the
     arithmetic behind it (2^-20); a weight's relative error is twice that, and its own rounding (bf16 in two parts:
@@ -218,6 +218,8 @@ def _check_decode(c, lens, k, v, q, z, att, o, lse, scale=0.0):
     got, gl = o.double().cpu().numpy(), lse.double().cpu().numpy()
     begin = np.cumsum([0] + list(lens))
     for s, m in enumerate(lens):
+        if only is not None and s not in only:
+            continue
         a = begin[s] + (0 if att.window_left < 0 else max(0, m - 1 - att.window_left))
         for r in range(P):
             for h in range(hq):
@@ -304,7 +306,7 @@ def test_decode_bad_pages_and_lengths_are_reported_and_others_are_right():
     from ulysses_sequence_long_gb300 import binding as B
     lens = [100, 200, 0, 50]
     c, table, ln, k, v, q, z, att = _decode_case(lens, 2, 2, 64, 1, 32, F8)
-    good = att.forward(q, table, ln, z).clone()
+    att.forward(q, table, ln, z)
     assert att.read_status() == 0
     for what in ("page", "negative page", "long", "negative"):
         t2, l2 = table.clone(), ln.clone()
@@ -319,10 +321,10 @@ def test_decode_bad_pages_and_lengths_are_reported_and_others_are_right():
         got = att.forward(q, t2, l2, z)
         assert att.read_status() == B.USP_ERR_BAD_PAGES, what
         c.status.zero_()
-        for s in (0, 2, 3):
-            # (another length deals the work out in other pieces, whose sums round otherwise: one step)
-            d = (got[:, s].double() - good[:, s].double()).abs()
-            assert (d <= 2.0 ** -7 * good[:, s].double().abs() + 1e-5).all(), what
+        # Another length deals the work out in other pieces, with other references, against which the weights round
+        # to f16 (2^-11 of each): two right results are apart by more than their own roundings (2 2^-8 of them, a
+        # first form of this test), by up to 2 2^-11 sum p |v|.  Each is within the oracle's bound.
+        _check_decode(c, lens, k, v, q, z, att, got, att.lse, only=(0, 2, 3))
 
 
 def test_tokens_behind_the_last_sequence_and_pages_of_others_do_not_matter():
@@ -336,6 +338,63 @@ def test_tokens_behind_the_last_sequence_and_pages_of_others_do_not_matter():
             c.v_pages[:, p] = float("nan")
     table[table == 2 ** 31 - 1] = -7
     assert torch.equal(o, att.forward(q, table, ln, z)) and att.read_status() == 0
+
+
+def test_sequences_that_share_a_prefix_and_places_of_the_table():
+    """Pages that several sequences read: each is what it is alone."""
+    c, table, ln, k, v, q, z, att = _decode_case([200, 0, 0], 4, 2, 64, 1, 64, F8, seed=3)
+    table[1] = table[0]
+    table[2] = table[0]
+    ln[1:] = torch.tensor([130, 200])
+    q[:, 2] = q[:, 0]
+    o = att.forward(q, table, ln, z)
+    assert att.read_status() == 0
+    _check_decode(c, [200], k, v, q[:, :1].contiguous(), z, att, o[:, :1], att.lse[:, :1])
+    _check_decode(c, [200], k, v, q[:, 2:].contiguous(), z, att, o[:, 2:], att.lse[:, 2:])
+    _check_decode(c, [130], k[:, :130].contiguous(), v[:, :130].contiguous(), q[:, 1:2].contiguous(), z, att, o[:, 1:2], att.lse[:, 1:2])
+
+
+def test_more_work_than_the_line_holds_is_reported():
+    """64 sequences of 2^30 positions, all of them in the same page: refused on the device before anything is read."""
+    from ulysses_sequence_long_gb300 import binding as B
+    from ulysses_sequence_long_gb300.serving import DecodeAttention, PagedCache
+    c = PagedCache(1, 2 ** 20, 1, 64, 1, dtype=F8)
+    table = torch.zeros((64, 1000), dtype=torch.int32).cuda()
+    att = DecodeAttention(c, 1, 64)
+    att.forward(_tokens((1, 64, 1, 64)), table, torch.full((64,), 1000 * 2 ** 20, dtype=torch.int32).cuda())
+    assert att.read_status() == B.USP_ERR_UNSUPPORTED
+    c.status.zero_()
+    o = att.forward(_tokens((1, 64, 1, 64)), table, torch.full((64,), 3, dtype=torch.int32).cuda())
+    assert att.read_status() == 0 and not o.any()       # (zeros in the pool)
+
+
+def test_scores_and_sums_that_are_not_finite_stay_in_their_sequence():
+    lens = [40, 40, 40]
+    c, table, ln, k, v, q, z, att = _decode_case(lens, 2, 1, 64, 1, 16, BF, sinks=True)
+    want = att.forward(q, table, ln, z).clone()
+    c.v_pages[0, table[1, 1].item(), 0, 3, 5] = float("nan")      # one value of one token
+    c.k_pages[0, table[2, 0].item(), 0, 0] = float("nan")         # a key
+    o = att.forward(q, table, ln, z)
+    assert torch.equal(o[:, 0], want[:, 0])
+    assert o[:, 1, :, 5].isnan().all() and torch.equal(o[:, 1, :, :5], want[:, 1, :, :5]) and torch.equal(o[:, 1, :, 6:], want[:, 1, :, 6:])
+    assert o[:, 2].isnan().all() and att.lse[:, 2].isnan().all()
+
+
+def test_a_workspace_is_as_it_was_found_and_serves_caches_of_all_kinds():
+    """What has to be zero is zero after every call, whatever the split; so calls of different caches may follow one
+    another in one workspace."""
+    from ulysses_sequence_long_gb300 import binding as B
+    ws = torch.zeros((8 << 20,), dtype=torch.uint8).cuda()
+    for i, (lens, D, dt, P, Hkv) in enumerate([([5000], 128, BF, 1, 1), ([300] * 40, 64, F8, 2, 4), ([20001, 7], 64, BF, 1, 1),
+                                               ([30000, 0, 9], 128, F8, 1, 2), ([100] * 200, 128, BF, 1, 8)]):
+        c, table, ln, k, v, q, z, att = _decode_case(lens, 2, Hkv, D, P, 64, dt, seed=i)
+        want, lse = att.forward(q, table, ln).clone(), att.lse.clone()
+        o, l2 = torch.empty_like(want), torch.empty_like(lse)
+        prm = B.paged_cache(Hkv, D, P, c.k_pages, c.v_pages, table, ln, c.k_scales, c.v_scales)
+        assert B.usp_attn_decode_workspace_bytes(prm, 2 * Hkv) <= ws.numel()
+        B.usp_attn_decode(prm, 2 * Hkv, q, o, l2, ws, dev_status=c.status)
+        assert c.read_status() == 0 and torch.equal(o, want) and torch.equal(l2, lse)
+        assert not ws[:1024 * 12].any()
 
 
 def test_a_pool_beyond_32_bits():

@@ -221,12 +221,13 @@ def test_the_hybrid_layer():
     assert a.read_status() == 0
 
 
-def test_a_refused_forward_leaves_the_turned_shards():
+@pytest.mark.parametrize("capped", [False, True])
+def test_a_refused_forward_leaves_the_turned_shards(capped):
     from ulysses_sequence_long_gb300.pipeline import ScoreMods
     w = W.Workload("rope", B=1, S=256, Hq=4, Hkv=2, D=64, P=2, doc_mode="explicit", doc_lens=(256,))
     dev, _ = device_inputs(w)
     rope, _, _ = _rotary(32)
-    a = _layer(w, rope, mods=ScoreMods(softcap=20.0))
+    a = _layer(w, rope, mods=ScoreMods(softcap=20.0) if capped else None)
     a.forward(dev["q"], dev["k"], dev["v"], dev["pos"])
     kept = [x.clone() for x in a.backward(dev["do"])]
     for bad in (dict(v=dev["q"]), dict(pos=dev["pos"].long()), dict(q=dev["k"])):

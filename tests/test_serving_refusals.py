@@ -59,20 +59,24 @@ def test_cache_refusals(lib):
     from ulysses_sequence_long_gb300 import binding as B
     e = dict(dtype=B.USP_CACHE_E4M3, k_scales=1 << 20, v_scales=1 << 21)
 
-    def rc(k=A, v=Bq, tokens=3, cu=None, Hq=8, ws=Cq, ws_bytes=None, **kw):
+    def rc(k=A, v=Dq, tokens=3, cu=None, Hq=8, ws=Cq, ws_bytes=None, **kw):
         c = _cache(**kw)
         codes = [f(ctypes.byref(c), k, v, tokens, cu, None, None) for f in (lib.usp_cache_append, lib.usp_cache_read)]
         n = lib.usp_attn_decode_workspace_bytes(ctypes.byref(c), Hq)
-        codes.append(lib.usp_attn_decode(ctypes.byref(c), Hq, -1, 0.0, None, A, Bq, Dq, ws, n - 1, None, None))
+        codes.append(lib.usp_attn_decode(ctypes.byref(c), Hq, -1, 0.0, None, A, Cq, Dq, ws, n - 1, None, None))
         assert (n == 0) == (codes[2] != B.USP_ERR_WORKSPACE)
         return codes
     for f in (lib.usp_cache_append, lib.usp_cache_read):
         assert f(None, A, Bq, 3, None, None, None) == B.USP_ERR_INVALID_ARG
-        for args in ((None, None, 3, None), (A, Bq, 0, None), (A, Bq, -1, P(16)), (A, Bq, 4, None)):
+        for args in ((None, None, 3, None), (A, Dq, 0, None), (A, Dq, -1, P(16)), (A, Dq, 4, None)):
             assert f(ctypes.byref(_cache()), *args, None, None) == B.USP_ERR_INVALID_ARG, args
         assert f(ctypes.byref(_cache()), P(8), Bq, 3, None, None, None) == B.USP_ERR_ALIGNMENT
         assert f(ctypes.byref(_cache()), A, Bq, 3, P(6), None, None) == B.USP_ERR_ALIGNMENT
         assert f(ctypes.byref(_cache()), A, Bq, 1 << 30, P(16), None, None) == B.USP_ERR_UNSUPPORTED
+        inside = P((1 << 31) + 2 * 4 * 64 * 10 * 16 - 16)         # the last bytes of the values' pool
+        assert f(ctypes.byref(_cache()), inside, Bq, 3, None, None, None) == B.USP_ERR_INVALID_ARG
+        assert f(ctypes.byref(_cache()), A, inside, 3, None, None, None) == B.USP_ERR_INVALID_ARG
+    assert lib.usp_cache_read(ctypes.byref(_cache()), A, P((1 << 20) + 16), 3, None, None, None) == B.USP_ERR_INVALID_ARG
     for kw in (dict(P=0), dict(Hkv=0), dict(D=0), dict(n_pages=0), dict(page_size=0), dict(n_seqs=0), dict(max_pages=0),
                dict(dtype=2), dict(k_pages=None), dict(v_pages=None), dict(block_table=None), dict(lens=None),
                dict(k_scales=1 << 20), dict(dtype=B.USP_CACHE_E4M3), dict(e, v_scales=None)):
@@ -95,7 +99,7 @@ def test_decode_refusals(lib):
     def rc(Hq=8, window=-1, scale=0.0, sinks=None, q=A, o=Bq, lse=Dq, ws=Cq, n=n):
         return lib.usp_attn_decode(ctypes.byref(c), Hq, window, scale, sinks, q, o, lse, ws, n, None, None)
     for kw in (dict(Hq=0), dict(q=None), dict(o=None), dict(lse=None), dict(scale=-1.0), dict(scale=float("nan")),
-               dict(scale=float("inf"))):
+               dict(scale=float("inf")), dict(o=A), dict(o=P((1 << 20) + 64)), dict(lse=A), dict(lse=Bq)):
         assert rc(**kw) == B.USP_ERR_INVALID_ARG, kw
     for h in (6, 7, 2):
         assert rc(Hq=h) == B.USP_ERR_INDIVISIBLE and lib.usp_attn_decode_workspace_bytes(ctypes.byref(c), h) == 0
@@ -147,3 +151,17 @@ def test_oracle_gradient_of_the_rotation_is_that_of_differences(interleaved):
         up[i] += 1.0
         diff = ((OS.rope(up, pos, f, ax, interleaved)[0] - OS.rope(x, pos, f, ax, interleaved)[0]) * dy).sum()
         assert abs(diff - dx[i]) < 1e-12
+
+
+def test_kernels_that_are_launched_early_wait_first():
+    """As the library's other chained kernels: grid_wait before any load (of global memory), no read-only loads."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "ulysses_sequence_long_gb300", "csrc")
+    for name, kernel in (("usp_rope.cu", "rope_kernel"), ("usp_cache.cu", "cache_kernel"), ("usp_decode.cu", "decode_kernel")):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(csrc, name)).read())
+        bodies = text.split("__global__")[1:]
+        assert len(bodies) == 1 and kernel in bodies[0] and "launch_chained(" in text
+        before, wait, _ = bodies[0].partition("grid_wait()")
+        assert wait and "gld(" not in before and "atom" not in before
+        assert "__ldg(" not in text and not re.search(r"const\s+\w+\s*\*\s*__restrict__", text)

@@ -301,6 +301,11 @@ int move_tokens(const usp_paged_cache* c, const void* k, const void* v, int toke
   if (tokens >= (1 << 30) || tokens * heads >= (1ll << 32)) return USP_ERR_UNSUPPORTED;
   if (!aligned16(k) || !aligned16(v)) return USP_ERR_ALIGNMENT;
   if (!aligned4(cu)) return USP_ERR_ALIGNMENT;
+  const uint64_t elems = static_cast<uint64_t>(heads) * c->D, n = 2 * elems * tokens;
+  const uint64_t pool = elems * c->n_pages * c->page_size * (c->dtype == USP_CACHE_E4M3 ? 1 : 2);
+  for (const void* x : {k, v})
+    if (x != nullptr && (overlap(x, n, c->k_pages, pool) || overlap(x, n, c->v_pages, pool))) return USP_ERR_INVALID_ARG;
+  if (!append && k != nullptr && v != nullptr && overlap(k, n, v, n)) return USP_ERR_INVALID_ARG;
   return launch_cache_move(*c, const_cast<void*>(k), const_cast<void*>(v), tokens, cu, append, status,
                            reinterpret_cast<cudaStream_t>(stream));
 }
@@ -740,6 +745,8 @@ int usp_attn_decode(const usp_paged_cache* cache, int Hq, int window_left, float
   if (!all_aligned16(q, o) || !aligned4(lse) || !aligned4(sinks)) return USP_ERR_ALIGNMENT;
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < attn_decode_ws_bytes(*cache))
     return USP_ERR_WORKSPACE;
+  const uint64_t rows = static_cast<uint64_t>(cache->n_seqs) * Hq, n = 2 * rows * cache->D;
+  if (overlap(q, n, o, n) || overlap(o, n, lse, 4 * rows) || overlap(q, n, lse, 4 * rows)) return USP_ERR_INVALID_ARG;
   const float scale = softmax_scale != 0.f ? softmax_scale : 1.f / sqrtf(static_cast<float>(cache->D));
   return launch_attn_decode(*cache, Hq, window_left, scale, sinks, q, o, lse, ws, dev_status,
                             reinterpret_cast<cudaStream_t>(stream));

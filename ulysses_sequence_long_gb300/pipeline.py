@@ -587,9 +587,11 @@ class UlyssesAttention(_Turned):
         """Sequence shards in, sequence shards out (``self.o_seq``).  ``rope_positions``: int32
         ``[n_axes][P][B][S/P]`` for the layer's ``rope`` (default: the position ids, one axis)."""
         if self.rope is not None:
-            if self._mods is not None:  # a call that is refused leaves what the backward reads
-                self._shards(v_seq, "v", self.shape.Hkv)
-                self._at(pos_shards, "position ids", torch.int32, self.shape.B * self.shape.S)
+            # (a call that is refused leaves the turned shards, which the backward reads)
+            B_._sized(v_seq, "v", torch.bfloat16, self.k_rot.numel(), self.k_rot)
+            B_._sized(pos_shards, "position ids", torch.int32, self.shape.B * self.shape.S, self.k_rot)
+            if sinks is not None:
+                B_._sized(sinks, "sinks", torch.float32, self.shape.Hq, self.k_rot)
             q_seq, k_seq = self.rotate(q_seq, k_seq, pos_shards if rope_positions is None else rope_positions, stream)
         if self._mods is not None:
             return self._on_device(self._mod_forward, q_seq, k_seq, v_seq, pos_shards, sinks, stream=stream)
