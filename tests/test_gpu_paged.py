@@ -528,6 +528,30 @@ def test_two_streams_and_two_layers_at_once():
         assert torch.equal(att._out(2)[0], o) and torch.equal(att.lse, lse)
 
 
+def test_a_pool_whose_tensors_were_exchanged():
+    """Every call reads and writes the tensors where they are then; one of another size or type is refused."""
+    lens = [70, 33]
+    c, table, ln, k, v, q, z, att = _decode_case(lens, 4, 2, 64, 1, 16, F8)
+    want = att.forward(q, table, ln, z).clone()
+    for name in ("k_pages", "v_pages", "k_scales", "v_scales", "status"):
+        old = getattr(c, name)
+        setattr(c, name, old.clone())                      # another tensor
+        old.view(torch.uint8).fill_(0x5A)
+        assert torch.equal(att.forward(q, table, ln, z), want), name
+        t = getattr(c, name)
+        keep = t.data
+        t.data = keep.clone()                              # another storage under it
+        keep.view(torch.uint8).fill_(0x5A)
+        assert torch.equal(att.forward(q, table, ln, z), want), name
+        t = getattr(c, name)
+        for bad in (torch.cat([t.view(torch.uint8).view(-1)] * 2), t.view(torch.uint8).double(), t.cpu()):
+            setattr(c, name, bad)
+            with pytest.raises((TypeError, ValueError)):
+                att.forward(q, table, ln, z)
+            setattr(c, name, t)
+    assert torch.equal(att.forward(q, table, ln, z), want) and att.read_status() == 0
+
+
 def test_refused_tensors():
     from ulysses_sequence_long_gb300.binding import UspError
     lens = [40, 3]

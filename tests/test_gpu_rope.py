@@ -158,6 +158,16 @@ def test_streams_graphs_and_exchanged_storage():
     half, _ = rope.forward(x, None, pos * 2)
     rope.freqs.data = old
     assert torch.equal(half, want)
+    for name in ("freqs", "axes", "status"):
+        t = getattr(rope, name)
+        setattr(rope, name, t.clone())
+        assert torch.equal(rope.forward(x, None, pos)[0], want)
+        for bad in (t.double(), t[:-1].clone() if name != "status" else t.cpu()):
+            setattr(rope, name, bad)
+            with pytest.raises((TypeError, ValueError)):
+                rope.forward(x, None, pos)
+        setattr(rope, name, t)
+    assert torch.equal(rope.forward(x, None, pos)[0], want) and rope.read_status() == 0
 
 
 def _layer(w, rope, **kw):

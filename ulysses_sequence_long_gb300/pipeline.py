@@ -123,18 +123,18 @@ class Rotary:
         self.device, self._index = freqs.device, freqs.get_device()
         lib = B_.load()
         self._fwd, self._bwd = lib.usp_rope_fwd, lib.usp_rope_bwd
-        self._seen = {}
         self._n_pairs = freqs.numel()
         self._find()
 
     def _find(self):
-        """The addresses of the rotation's tensors, for the calls to come."""
+        """The addresses of the rotation's tensors, for the calls to come (which see by them when one was exchanged; a
+        reference keeps another tensor from getting the same one meanwhile)."""
         at, n = self._at, self._n_pairs
-        self._tables = (at(self.freqs, "freqs", torch.float32, n),
-                        None if self.axes is None else at(self.axes, "axes", torch.int32, n))
-        self._status = at(self.status, "status", torch.int32, 1)
-        self._found = tuple((name, getattr(self, name), getattr(self, name).data_ptr())
-                            for name in ("freqs", "axes", "status") if getattr(self, name) is not None)
+        self._held = (self.freqs, self.axes, self.status)
+        self._found = (at(self.freqs, "freqs", torch.float32, n),
+                       None if self.axes is None else at(self.axes, "axes", torch.int32, n),
+                       at(self.status, "status", torch.int32, 1))
+        self._seen = {}
 
     def _plan(self, q, k, positions):
         """Sizes of a call, by the shapes."""
@@ -148,7 +148,8 @@ class Rotary:
         if n == 0 or n % self.n_axes or tokens % (n // self.n_axes):
             raise ValueError(f"positions must be [{self.n_axes}][n] with n tokens or a divisor of their {tokens}, "
                              f"got {n} elements")
-        return B_.RopeParams(tokens, Hq, Hkv, D, self.n_axes, n // self.n_axes, self._n_pairs, int(self.interleaved))
+        return B_.RopeParams(tokens, Hq, Hkv, D, self.n_axes, n // self.n_axes, self._n_pairs, int(self.interleaved),
+                             None, self._found[0], self._found[1])
 
     def _at(self, t, name, dtype, n):
         if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and t.get_device() == self._index and t.is_contiguous():
@@ -158,20 +159,22 @@ class Rotary:
         raise ValueError(f"{name} must have {n} elements on {self.device}, got {tuple(t.shape)} on {t.device}")
 
     def _turn(self, fn, where, q, k, positions, out, stream):
-        shapes = (q.shape, None if k is None else k.shape, positions.numel())
+        freqs, axes, status = self._found
+        mine = self.axes
+        if (self.freqs.data_ptr() != freqs or self.status.data_ptr() != status
+                or (mine is not None and mine.data_ptr()) != (axes is not None and axes)):
+            self._find()
+            status = self._found[2]
+        n_pos = positions.numel()
+        shapes = (q.shape, None if k is None else k.shape, n_pos)
         p = self._seen.get(shapes)
         if p is None:
             p = self._plan(q, k, positions)
             if len(self._seen) < 1024:
                 self._seen[shapes] = p
         p = B_.RopeParams.from_buffer_copy(p)   # this call's own (threads may share a Rotary)
-        mine, bf, index, at = self.__dict__, torch.bfloat16, self._index, self._at
-        for name, t, was in self._found:
-            if mine[name] is not t or t.data_ptr() != was:   # a tensor, or the storage under one, was exchanged
-                self._find()
-                break
-        p.freqs, p.axes = self._tables
-        p.positions = at(positions, "positions", torch.int32, shapes[2])
+        bf, index, at = torch.bfloat16, self._index, self._at
+        p.positions = at(positions, "positions", torch.int32, n_pos)
         if out is None:
             out = (torch.empty_like(q, memory_format=torch.contiguous_format),
                    None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format))
@@ -184,7 +187,7 @@ class Rotary:
         else:
             x, y = at(q, "q", bf, q.numel()), at(y, "the output of q", bf, q.numel())
             xk, yk = (None, None) if k is None else (at(k, "k", bf, k.numel()), at(yk, "the output of k", bf, k.numel()))
-        B_.run_on(index, stream, fn, where, ctypes.byref(p), x, xk, y, yk, self._status)
+        B_.run_on(index, stream, fn, where, ctypes.byref(p), x, xk, y, yk, status)
         return out
 
     def forward(self, q, k, positions, out=None, stream=None):

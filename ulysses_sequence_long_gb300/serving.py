@@ -66,7 +66,8 @@ class PagedCache:
         self._find()
 
     def _find(self):
-        """The addresses of the pool's tensors, which have to be of their sizes and types, for the calls to come."""
+        """The addresses of the pool's tensors, which have to be of their sizes and types, for the calls to come (which
+        see by them when one was exchanged; a reference keeps another tensor from getting the same one meanwhile)."""
         c, index, n = self._fixed, self._index, self.P * self.n_pages * self.hk * self.page_size
         c.k_pages = _where(self.k_pages, "k_pages", self.dtype, n * self.D, index)
         c.v_pages = _where(self.v_pages, "v_pages", self.dtype, n * self.D, index)
@@ -74,16 +75,15 @@ class PagedCache:
             c.k_scales = _where(self.k_scales, "k_scales", _U8, n, index)
             c.v_scales = _where(self.v_scales, "v_scales", _U8, n, index)
         self._status = _where(self.status, "status", _I32, 1, index)
-        names = ("k_pages", "v_pages", "status") + (("k_scales", "v_scales") if self.dtype is _F8 else ())
-        self._found = tuple((name, getattr(self, name), getattr(self, name).data_ptr()) for name in names)
+        self._held = (self.k_pages, self.v_pages, self.k_scales, self.v_scales, self.status)
+        self._found = (c.k_pages, c.v_pages, c.k_scales, c.v_scales, self._status)
 
     def _struct(self, block_table, lens) -> B_.PagedCacheStruct:
         """This call's own structure (threads may use one cache at once), with the addresses that the tensors have now."""
-        mine = self.__dict__
-        for name, t, at in self._found:
-            if mine[name] is not t or t.data_ptr() != at:   # a tensor, or the storage under one, was exchanged
-                self._find()
-                break
+        k, v, ks, vs, status = self._found
+        if (self.k_pages.data_ptr() != k or self.v_pages.data_ptr() != v or self.status.data_ptr() != status
+                or (ks is not None and (self.k_scales.data_ptr() != ks or self.v_scales.data_ptr() != vs))):
+            self._find()
         c = B_.PagedCacheStruct.from_buffer_copy(self._fixed)
         index = self._index
         if (block_table.dtype is _I32 and lens.dtype is _I32 and block_table.get_device() == index
