@@ -531,7 +531,7 @@ int usp_rope_bwd(const usp_rope_params* params, const void* dq_out, const void* 
  * one head r / (P/Hkv) on rank r.
  * With dtype USP_CACHE_E4M3 a token's head has a power of two 2^e, the smallest
  * with e >= -126 for which every |x| <= 448 2^e (an infinity counts as the largest
- * finite bf16), stored as the byte e + 127, and its elements are x / 2^e rounded to
+ * finite bf16), stored as the byte e + 127 (1 to 247), and its elements are x / 2^e rounded to
  * the nearest e4m3 value (ties to even).  NaN stays NaN.
  * ---------------------------------------------------------------------- */
 typedef struct {

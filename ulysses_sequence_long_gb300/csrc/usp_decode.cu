@@ -257,22 +257,27 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
   const uint32_t ring = smem_u32(smem) + w * C::kRing;
   Place ld = cur;
   int left = count;                     // tiles not asked for yet
-  int page = 0;                         // of the tile at ld; looked up a tile ahead
-  uint32_t col = 0;
-  uint32_t slot = 0;                    // where it goes in the ring
+  uint32_t slot = 0;                    // where the next one goes in the ring
   const int64_t page_rows = static_cast<int64_t>(a.pool.hk) * a.pool.page_size;
-  const int32_t* table;                 // the sequence's row of the table
+  const int32_t* table;                 // the entry of the page at hand
   int64_t unit_row;                     // the unit's first row in a page 0
+  int page, off;                        // the page at hand (looked up a tile ahead), where in it the next tile begins
+  bool new_page = true, ok = false;     // it has not been entered yet; it is one of the pool's
+  int full, full_end;                   // tiles of which every position is visible
+  const unsigned char *kp, *vp;         // the lane's first pieces of the next tile
+  const uint8_t* sp;                    // its scales, keys' in lane 0, values' in lane 1
   auto enter_unit = [&]() {
-    table = a.pool.table + static_cast<int64_t>(ld.b) * a.pool.max_pages;
+    const int t0 = ld.tile * kTile;
+    const uint32_t col = a.pool.by_page.div(t0);
+    table = a.pool.table + static_cast<int64_t>(ld.b) * a.pool.max_pages + col;
+    page = gld(table);
+    off = t0 - static_cast<int>(col) * a.pool.page_size;
     unit_row = static_cast<int64_t>(ld.r) * a.pool.n_pages * page_rows + ld.j * a.pool.page_size;
-  };
-  auto find_page = [&]() {
-    col = a.pool.by_page.div(ld.tile * kTile);
-    page = gld(table + col);
+    full = (ld.lo + kTile - 1) / kTile;
+    full_end = ld.len / kTile;
+    new_page = true;
   };
   enter_unit();
-  find_page();
   // Shared memory holds rows as they are, 16-byte pieces turned over within 128 bytes so that both the copies (512 bytes
   // of consecutive rows an instruction) and the reads below meet all banks: a K row's by 4 where it is odd, a V row's by
   // twice its pair's number mod 4 (rows of 64 bytes: K not at all, V by 2 where the pair is odd).
@@ -283,38 +288,47 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
   const int vget = 2 * qd * R + (R == 64 ? ((g >> 1) ^ ((qd & 1) << 1)) * 16 + (g & 1) * 8 : (g ^ (2 * qd)) * 16);
   auto load = [&]() {
     if (left > 0) {
-      const int t0 = ld.tile * kTile;
-      const bool ok = page >= 0 && page < a.pool.n_pages;
-      const int64_t row = unit_row + (ok ? page : 0) * page_rows + (t0 - static_cast<int>(col) * a.pool.page_size);
-      const unsigned char* kp = static_cast<const unsigned char*>(a.pool.k) + row * R + lane * 16;
-      const unsigned char* vp = static_cast<const unsigned char*>(a.pool.v) + row * R + lane * 16;
+      if (new_page) {
+        new_page = false;
+        ok = page >= 0 && page < a.pool.n_pages;
+        if (!ok) set_status(a.status, USP_ERR_BAD_PAGES);
+        const int64_t row = unit_row + (ok ? page : 0) * page_rows + off;
+        kp = static_cast<const unsigned char*>(a.pool.k) + row * R + lane * 16;
+        vp = static_cast<const unsigned char*>(a.pool.v) + row * R + lane * 16;
+        if constexpr (kE4m3) sp = (lane == 0 ? a.pool.k_scales : a.pool.v_scales) + row;
+      }
       const uint32_t kdst = ring + slot + kput, vdst = ring + slot + 16 * R + vput;
       const auto vturn = [](int i) { return R == 256 ? (i & 3) << 5 : R == 128 ? (i & 1) << 6 : 0; };
-      if (ok && t0 >= ld.lo && t0 + 16 <= ld.len) {
+      if (ok && ld.tile >= full && ld.tile < full_end) {
 #pragma unroll
         for (int i = 0; i < C::kCopies; ++i) cp_async(kdst + i * 512, kp + i * 512);
 #pragma unroll
         for (int i = 0; i < C::kCopies; ++i) cp_async((vdst ^ vturn(i)) + i * 512, vp + i * 512);
       } else {  // zeros for what is not seen: a weight of 0 does not undo a value that is not finite
-        if (!ok) set_status(a.status, USP_ERR_BAD_PAGES);
 #pragma unroll
         for (int i = 0; i < C::kCopies; ++i) {
-          const int t = t0 + (i * 512 + lane * 16) / R;
+          const int t = ld.tile * kTile + (i * 512 + lane * 16) / R;
           const bool in = ok && t < ld.len && t >= ld.lo;
           cp_async_or_zero(kdst + i * 512, kp + i * 512, in);
           cp_async_or_zero((vdst ^ vturn(i)) + i * 512, vp + i * 512, in);
         }
       }
       if constexpr (kE4m3) {
-        if (lane < 2)
-          cp_async(ring + slot + 32 * R + 16 * lane, (lane == 0 ? a.pool.k_scales : a.pool.v_scales) + row);
+        if (lane < 2) cp_async(ring + slot + 32 * R + 16 * lane, sp);
+        sp += kTile;
       }
+      kp += kTile * R;
+      vp += kTile * R;
+      off += kTile;
       if (--left > 0) {
         if (++ld.tile == ld.end) {
           ld.next_unit(a, bad);
           enter_unit();
+        } else if (off == a.pool.page_size) {
+          off = 0;
+          page = gld(++table);
+          new_page = true;
         }
-        find_page();
       }
     }
     slot = slot == (C::kStages - 1) * C::kStage ? 0 : slot + C::kStage;
@@ -384,6 +398,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
       const uint32_t src = ring + read;
       read = read == (C::kStages - 1) * C::kStage ? 0 : read + C::kStage;
       // S^T: rows g and g + 8 are positions, columns 2 qd and 2 qd + 1 query heads
+      constexpr bool kTwo = C::kWarps <= 8;  // two chains of products where few warps hide one's latency
       float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int p = 0; p < C::kKPieces; ++p) {
@@ -391,63 +406,73 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
         const uint4 x = lds16(from), y = lds16(from + 8 * R);
         if constexpr (!kE4m3) {
           mma<false>(s, x.x, y.x, x.y, y.y, qf[2 * p][0], qf[2 * p][1]);
-          mma<false>(s2, x.z, y.z, x.w, y.w, qf[2 * p + 1][0], qf[2 * p + 1][1]);
+          mma<false>(kTwo ? s2 : s, x.z, y.z, x.w, y.w, qf[2 * p + 1][0], qf[2 * p + 1][1]);
         } else {
           const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            mma<true>(e & 1 ? s2 : s, paged::e4m3x2_to_f16x2(xw[e] & 0xffff), paged::e4m3x2_to_f16x2(yw[e] & 0xffff),
+            mma<true>(s, paged::e4m3x2_to_f16x2(xw[e] & 0xffff), paged::e4m3x2_to_f16x2(yw[e] & 0xffff),
                       paged::e4m3x2_to_f16x2(xw[e] >> 16), paged::e4m3x2_to_f16x2(yw[e] >> 16), qf[4 * p + e][0],
                       qf[4 * p + e][1]);
         }
       }
-      float ve[2] = {0.f, 0.f};  // exponents of the two positions' values
-      float ks[2] = {1.f, 1.f};
+      float f[4] = {qs[0], qs[1], qs[0], qs[1]};  // what makes scores of log2 of the products
+      float ve[2] = {0.f, 0.f};                  // exponents of the two positions' values, and kUp
       if constexpr (kE4m3) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int kb = lds1(src + 32 * R + g + 8 * i), vb = lds1(src + 32 * R + 16 + g + 8 * i);
-          ks[i] = kb ? __uint_as_float(static_cast<uint32_t>(kb) << 23) : 0x1p-127f;
-          ve[i] = static_cast<float>(vb - 127);
+          const float by = __uint_as_float(static_cast<uint32_t>(kb) << 23);
+          f[2 * i] *= by;
+          f[2 * i + 1] *= by;
+          ve[i] = static_cast<float>(vb) + (kUp - 127.f);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[i] = (s[i] + s2[i]) * qs[i & 1];
-        if constexpr (kE4m3) s[i] *= ks[i >> 1];
-      }
-      if (t0 + 16 > cur.len || t0 < cur.lo) {
+      const bool edge = t0 + 16 > cur.len || t0 < cur.lo;
+      auto hide = [&](float (&y)[4]) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (t0 + g + 8 * i >= cur.len || t0 + g + 8 * i < cur.lo) s[2 * i] = s[2 * i + 1] = -INFINITY;
-      }
-      // The reference of a column follows its scores only when one is 2^8 above it.
-      float x[4];
-      bool above = none;
+          if (t0 + g + 8 * i >= cur.len || t0 + g + 8 * i < cur.lo) y[2 * i] = y[2 * i + 1] = -INFINITY;
+      };
+      // x: weights over the column's reference; y: those of the products, with the values' exponents.  The reference
+      // follows its scores only when one is 2^kAbove above it.
+      float x[4], y[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[i] = s[i] - ref[i & 1];
-        above |= (kE4m3 ? x[i] + fmaxf(ve[i >> 1], kLeast) : x[i]) > kAbove;
+        if (kTwo) s[i] += s2[i];
+        x[i] = fmaf(s[i], f[i], -ref[i & 1]);
       }
+      if (edge) hide(x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = x[i] + ve[i >> 1];
+      bool above = none || fmaxf(fmax3(y[0], y[1], y[2]), y[3]) > kAbove + (kE4m3 ? kUp : 0.f);
+      if constexpr (kE4m3) above |= fmaxf(fmax3(x[0], x[1], x[2]), x[3]) > kAbove - kLeast;
       if (__any_sync(0xffffffffu, above)) {
         none = false;
+        float z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = s[i] * f[i];
+        if (edge) hide(z);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float top = kE4m3 ? fmaxf(s[c] + fmaxf(ve[0], kLeast), s[2 + c] + fmaxf(ve[1], kLeast)) : fmaxf(s[c], s[2 + c]);
+          float top = kE4m3 ? fmaxf(z[c] + fmaxf(ve[0] - kUp, kLeast), z[2 + c] + fmaxf(ve[1] - kUp, kLeast)) : fmaxf(z[c], z[2 + c]);
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           const float mn = fmaxf(m[c], top);
-          const float f = m[c] == -INFINITY ? 0.f : ex2(m[c] - mn);
+          const float by = m[c] == -INFINITY ? 0.f : ex2(m[c] - mn);
           m[c] = mn;
           ref[c] = mn == -INFINITY ? 0.f : mn;
-          l[c] *= f;
+          l[c] *= by;
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            acc[i][c] *= f;
-            acc[i][2 + c] *= f;
+            acc[i][c] *= by;
+            acc[i][2 + c] *= by;
           }
-          x[c] = s[c] - ref[c];
-          x[2 + c] = s[2 + c] - ref[c];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            x[2 * i + c] = z[2 * i + c] - ref[c];
+            y[2 * i + c] = x[2 * i + c] + ve[i];
+          }
         }
       }
       float p[4];
@@ -459,7 +484,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
       uint32_t b0, b1, c0 = 0, c1 = 0;
       if constexpr (kE4m3) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = ex2(x[i] + (ve[i >> 1] + kUp));
+        for (int i = 0; i < 4; ++i) p[i] = ex2(y[i]);
         b0 = transpose8(pack_f16x2(p[0], p[1]));
         b1 = transpose8(pack_f16x2(p[2], p[3]));
       } else {
@@ -709,7 +734,7 @@ __device__ __forceinline__ void join(const Args& a, unsigned char* smem, const C
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args a) {
   using C = Cfg<D, kE4m3>;
-  constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
+  constexpr int kWarps = C::kWarps;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Part parts[2 * kWarps];
   __shared__ float2 stats[2 * kWarps][kHeads];  // reference, sum
