@@ -456,7 +456,7 @@ def test_prompts_then_tokens(dtype, P, Hkv, window):
     ua.forward(shards(q), shards(k), shards(v), pos.view(P, 1, Sp // P), dev["sinks"])
     c, table, ln = _pool([n for n in whole], page, Hkv, D, P, dtype)
     lens = torch.tensor(docs, dtype=torch.int32).cuda()
-    c.append(ua.k_head, ua.v_head, table, lens, ua.cu_seqlens)
+    c.append(*ua.head_kv(), table, lens, ua.cu_seqlens)
     att = DecodeAttention(c, Hq, len(docs), window_left=window, rope=rope)
     hq, hk = Hq // P, c.hk
     rank_kv = [list(range(r * hk, (r + 1) * hk)) if Hkv >= P else [r * Hkv // P] for r in range(P)]

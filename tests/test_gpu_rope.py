@@ -213,6 +213,29 @@ def test_the_layer_turns_q_and_k_and_their_gradients(kind):
     assert torch.equal(o, c.o_seq)
 
 
+@pytest.mark.parametrize("kind", ["fused", "explicit", "one rank", "mods", "mods in shards", "mods on one rank", "mods moved"])
+def test_keys_and_values_in_head_layout(kind):
+    """What a cache takes from a layer: the exchange of the turned keys and of the values."""
+    from ulysses_sequence_long_gb300 import binding as B
+    from ulysses_sequence_long_gb300.pipeline import ScoreMods
+    P = 1 if "one rank" in kind else 2
+    w = W.Workload("rope", B=2, S=512, Hq=4, Hkv=2, D=64, P=P, doc_mode="explicit", doc_lens=(200, 1, 311))
+    dev, _ = device_inputs(w)
+    rope, _, _ = _rotary(32)
+    kw = dict(fused=kind in ("fused", "mods in shards", "mods moved"))
+    if kind.startswith("mods"):
+        kw["mods"] = ScoreMods(softcap=20.0)
+    a = _layer(w, rope, **kw)
+    if kind == "mods moved":
+        a._kv_in_place = False
+    a.forward(dev["q"], dev["k"], dev["v"], dev["pos"])
+    k, v = a.head_kv()
+    for got, x in ((k, rope.forward(dev["k"], None, dev["pos"])[0]), (v, dev["v"])):
+        want = torch.empty_like(a.k_head)
+        B.usp_relayout_fwd(x, want, w.B, w.S, w.Hkv, w.D, w.P)
+        assert got.shape == want.shape and torch.equal(got, want)
+
+
 def test_the_hybrid_layer():
     from ulysses_sequence_long_gb300.pipeline import HybridAttention, Shape
     w = W.Workload("rope", B=1, S=1024, Hq=4, Hkv=2, D=64, P=4, sinks=True, doc_mode="explicit", doc_lens=(600, 424))

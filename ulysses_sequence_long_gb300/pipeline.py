@@ -604,6 +604,23 @@ class UlyssesAttention(_Turned):
         self.exchange_out(stream)
         return self.o_seq
 
+    def head_kv(self, stream=None):
+        """The last forward's keys (turned, with ``rope``) and values in head layout ``[P][B][S][heads of a rank][D]``:
+        what ``serving.PagedCache.append`` takes, with ``cu_seqlens``.  The forward has left them there but for a layer with
+        modified scores that read them from their shards."""
+        if self._mods is None or not (self._one_rank or self._kv_in_place):
+            return self.k_head, self.v_head
+        k, v = self._inputs[1:]
+        if self._one_rank:   # its shards are its head layout
+            return k.view(self.k_head.shape), v.view(self.v_head.shape)
+        self._on_device(self._mod_exchange_kv, k, v, stream=stream)
+        return self.k_head, self.v_head
+
+    def _mod_exchange_kv(self, k, v, stream):
+        s = self.shape
+        for t, name, y in zip((k, v), ("k", "v"), self._own("k_head", "v_head")):
+            self._launch("usp_relayout_fwd", self._shards(t, name, s.Hkv), y, s.B, s.S, s.Hkv, s.D, s.P, 2, stream)
+
     def backward_phases(self, do_seq, sinks=None, stream=None, marks=None, group_marks=None):
         """The backward as its separate library calls; `marks(i)` is called
         between them (for timing): 0 before, 1 after the dO exchange, 2 after

@@ -115,7 +115,7 @@ class PagedCache:
     def append(self, k, v, block_table, lens, cu_seqlens=None, stream=None):
         """Write the last tokens of each sequence: k, v bf16 ``[P][tokens][heads of a rank][D]`` (head layout), tokens
         ``[cu_seqlens[s], cu_seqlens[s+1])`` of sequence s, or one of each sequence without ``cu_seqlens``.
-        ``cu_seqlens`` and ``k_head``, ``v_head`` of a layer that ran a packed batch are these."""
+        A layer that ran a packed batch has these in ``head_kv()`` and ``cu_seqlens``."""
         self._move(self._append, "usp_cache_append", k, v, block_table, lens, cu_seqlens, stream)
 
     def read(self, block_table, lens, cu_seqlens=None, out=None, tokens: Optional[int] = None, stream=None):
