@@ -289,6 +289,18 @@ def test_decode_many_sequences_more_than_threads():
     _check_decode(c, lens, k, v, q, z, att, o, att.lse)
 
 
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, F8)], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n,most", [(40, 1500), (120, 1500), (300, 40), (150, 300)])
+def test_decode_ragged_batches(D, dtype, n, most):
+    """Units that lie in a warp, in a CTA, across warps and across CTAs, some sequences empty."""
+    rng = np.random.default_rng(n + most)
+    lens = [0 if i % 7 == 3 else int(x) for i, x in enumerate(rng.integers(1, most + 1, n))]
+    c, table, ln, k, v, q, z, att = _decode_case(lens, 2, 4, D, 2, 16, dtype, seed=n, sinks=True)
+    o = att.forward(q, table, ln, z)
+    assert att.read_status() == 0
+    _check_decode(c, lens, k, v, q, z, att, o, att.lse)
+
+
 @pytest.mark.parametrize("dtype", [BF, F8], ids=["bf16", "e4m3"])
 def test_decode_one_long_sequence(dtype):
     """Split over all SMs and joined; every head of one rank against fp64 on the device."""

@@ -54,9 +54,11 @@ using paged::Deal;
 using paged::kTile;
 static_assert(kTile == 16, "the rows of a matrix instruction");
 constexpr int kFan = 48;            // parts that a CTA puts together at once
-// Tiles that a warp works through in the time that joining parts takes: 64 sequences of up to 100 tokens, 8 heads, 10.5 us
-// with 0 or 3, 8.4 with 8; 30 of up to 300, 2 heads, 8.9 with 0 to 8, 15.0 with 20.
-constexpr int kJoinTiles = 8;
+// Tiles that a warp works through in the time that putting a CTA's parts together takes, and joining those of CTAs too.
+// (us; 8 heads, D 128, bf16.  64 sequences of up to 100 tokens: tiles to the warps 10.5, units to the warps 8.2; 8 of up to
+// 200: tiles 8.4, units to the CTAs 5.8, to the warps 11.5; 16 of 1000: 12.7, 10.1; 200 of up to 500, D 64, e4m3: 22.9,
+// units to the CTAs 23.4, to the warps 26.8.)
+constexpr int kWarpsTiles = 3, kCtasTiles = 8;
 constexpr int kHeads = 8;           // query heads of a unit (more of them in a group: more units)
 constexpr int kMaxCtas = 1024, kTicketBytes = kMaxCtas * 12;
 // A column's reference may stay this far (log2) below a weight; e4m3: weights go into f16 kUp higher (2^15 at most), and
@@ -217,6 +219,10 @@ struct Finish {
   }
 };
 
+// How the work is dealt out: the line's tiles to the warps, whole units to the CTAs, whose warps share them, or to the
+// warps.
+enum class Split { kTiles, kUnitsToCtas, kUnitsToWarps };
+
 // A stretch's place with the unit's parts spelt out.
 struct Place : Cursor {
   int r, j, chunk;  // rank, its key/value head, chunk of 8 query heads
@@ -227,34 +233,44 @@ struct Place : Cursor {
     j = rj - r * a.pool.hk;
   }
   __device__ __forceinline__ void next_unit(const Args& a, bool& bad) {
-    tile = end - 1;
-    next(a.pool, a.window, a.units, bad);
+    Cursor::next_unit(a.pool, a.window, a.units, bad);
     split(a);
   }
 };
 
-// A warp's stretch: `count` tiles from `at` of the line, or `count` whole units; it begins start.y tiles (units) into
-// sequence start.x.
+// A warp's stretch: `count` tiles from `at` of the line, `count` whole units, or its share of the CTA's `count` units; it
+// (for a share, they) begins start.y tiles, or units, into sequence start.x.
 template <int D, bool kE4m3>
 __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, Part* parts, float2 (*stats)[kHeads],
-                                            int2 start, bool by_unit, uint32_t at, int count) {
+                                            int2 start, Split split, uint32_t at, int count) {
   using C = Cfg<D, kE4m3>;
   constexpr int MT = D / 16, KS = D / 16, QV = D / 32;  // QV: 16-byte pieces of a query head that a thread has
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, qd = lane & 3;
   float* kept = reinterpret_cast<float*>(smem + C::kWarps * C::kRing + w * C::kKept);
   bool bad = false;  // (reported when the lengths were added up)
   Place cur;
-  if (by_unit) {
+  if (split != Split::kTiles) {
     cur.sequence(a.pool, a.window, start.x, bad);
     cur.u = start.y;
     Cursor c = cur;
-    int tiles = 0;
+    uint32_t tiles = 0;
     for (int i = 0; i < count; ++i) {
       tiles += c.end - c.first;
-      c.tile = c.end - 1;
-      c.next(a.pool, a.window, a.units, bad);
+      c.next_unit(a.pool, a.window, a.units, bad);
     }
     count = tiles;
+    if (split == Split::kUnitsToCtas) {
+      const Deal own(tiles, C::kWarps);
+      at = own.begin(w);
+      count = own.begin(w + 1) - at;
+      if (count == 0) return;
+      int skip = at;
+      while (skip >= cur.end - cur.first) {
+        skip -= cur.end - cur.first;
+        cur.Cursor::next_unit(a.pool, a.window, a.units, bad);
+      }
+      cur.tile = cur.first + skip;
+    }
   } else {
     cur.seek(a.pool, a.window, start.x, start.y, bad);
   }
@@ -781,18 +797,25 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
     set_status(a.status, USP_ERR_UNSUPPORTED);
     return;
   }
-  // Dealt out by tiles, or whole units to the warps where that makes the longest share kJoinTiles longer at
-  // most: then nothing is to be joined.
-  const uint32_t W = static_cast<uint32_t>(tiles), U = any * a.units, warps = gridDim.x * kWarps;
-  const bool by_unit = static_cast<uint64_t>((U + warps - 1) / warps) * most <= (W + warps - 1) / warps + kJoinTiles;
-  const uint32_t things = by_unit ? U : W, n_ctas = min(gridDim.x, (things + kWarps - 1) / kWarps);
+  // The longest share of a warp, in tiles: of whole units dealt out to the warps (nothing is to be joined then), to
+  // the CTAs (nothing across them), of tiles.
+  const uint32_t W = static_cast<uint32_t>(tiles), U = any * a.units, warps = gridDim.x * kWarps, even = (W + warps - 1) / warps;
+  const uint64_t to_warp = static_cast<uint64_t>((U + warps - 1) / warps) * most;
+  const uint64_t to_cta = (static_cast<uint64_t>((U + gridDim.x - 1) / gridDim.x) * most + kWarps - 1) / kWarps;
+  const Split split = to_warp <= min(to_cta + kWarpsTiles, static_cast<uint64_t>(even) + kCtasTiles) ? Split::kUnitsToWarps
+                      : to_cta + kWarpsTiles <= even + kCtasTiles                                     ? Split::kUnitsToCtas
+                                                                                                      : Split::kTiles;
+  const bool by_unit = split != Split::kTiles;
+  const uint32_t things = by_unit ? U : W, takers = split == Split::kUnitsToCtas ? 1 : kWarps;  // of a CTA
+  const uint32_t n_ctas = min(gridDim.x, (things + takers - 1) / takers);
   // sequences that see nothing have no tile: CTAs without work write their outputs, or all when they are done
   if (cta >= n_ctas) {
     if (any < a.n_seqs) write_empty<D>(a, (cta - n_ctas) * kWarps + w, (gridDim.x - n_ctas) * kWarps);
     return;
   }
-  const Deal line(things, n_ctas * kWarps);
-  const uint32_t at = line.begin(cta * kWarps + w), count = line.begin(cta * kWarps + w + 1) - at;
+  const Deal line(things, n_ctas * takers);
+  const uint32_t taker = cta * takers + (takers > 1 ? w : 0);
+  const uint32_t at = line.begin(taker), count = line.begin(taker + 1) - at;
   if (count > 0) {
     const uint32_t hi = (by_unit ? before_any : before) * a.units, lo = hi - (by_unit ? mine_any : mine) * a.units;
     const bool here = at >= lo && at < hi;
@@ -806,10 +829,10 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
     }
     const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
     const int2 start = make_int2(__shfl_sync(0xffffffffu, s, from), __shfl_sync(0xffffffffu, rest, from));
-    run_stretch<D, kE4m3>(a, smem, parts, stats, start, by_unit, at, count);
+    run_stretch<D, kE4m3>(a, smem, parts, stats, start, split, at, count);
   }
   if (any < a.n_seqs && n_ctas == gridDim.x) write_empty<D>(a, cta * kWarps + w, warps);
-  if (by_unit) return;
+  if (split == Split::kUnitsToWarps) return;
 
   // ---- the warps' parts, in order: those of one unit next to each other
   __syncthreads();
@@ -847,7 +870,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
       if (h == 0 && lane == 0) crossing[begins] = Crossing{unit, first, static_cast<int>(line.owner(stop - 1)) / kWarps - first + 1, cta - first};
     }
   }
-  join<D, kE4m3>(a, smem, crossing);
+  if (split == Split::kTiles) join<D, kE4m3>(a, smem, crossing);
 }
 
 template <int D, bool kE4m3>

@@ -138,7 +138,10 @@ struct Cursor {
     tile = first + static_cast<int>(rest - u * n);
   }
   USP_HD void next(const Pool& p, int window, int units, bool& bad) {
-    if (++tile < end) return;
+    if (++tile == end) next_unit(p, window, units, bad);
+  }
+  // to the begin of the next unit; behind the last one it is no place
+  USP_HD void next_unit(const Pool& p, int window, int units, bool& bad) {
     tile = first;
     if (++u < units) return;
     int s = b;
