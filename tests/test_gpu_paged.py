@@ -241,7 +241,7 @@ DECODE_LENS = [[1], [2, 16, 0, 17], [64, 65, 63, 1, 0, 200], [1000, 3], [0, 0], 
 @pytest.mark.parametrize("lens", DECODE_LENS, ids=str)
 @pytest.mark.parametrize("dtype", [BF, F8], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("D,Hkv,P,page,G", [(64, 2, 1, 16, 1), (128, 4, 2, 64, 4), (64, 1, 4, 48, 8), (128, 1, 1, 256, 7),
-                                            (64, 2, 2, 32, 12), (128, 1, 1, 64, 17)])
+                                            (64, 2, 2, 32, 12), (128, 1, 1, 64, 17), (64, 1, 1, 16, 130)])
 def test_decode(lens, dtype, D, Hkv, P, page, G):
     c, table, ln, k, v, q, z, att = _decode_case(lens, G, Hkv, D, P, page, dtype, seed=G, sinks=G % 4 == 0, gain=1.5)
     o = att.forward(q, table, ln, z)

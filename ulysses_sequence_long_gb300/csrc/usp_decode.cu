@@ -16,12 +16,12 @@
 //
 // Loads.  The products are arranged so that the positions are the rows of the matrix
 // instruction and the query heads its 8 columns (S^T = K q^T, O^T = V^T P^T): rows of 16 query heads would be
-// half empty for groups up to 8.  Sums over d may take d in any order, so a thread's operands are whole 16-byte pieces of its rows.  A warp copies
-// its own 16 rows into shared memory (cp.async, 512 consecutive bytes an instruction, tiles ahead) and no barrier but
-// the warp's own is needed; only the pairs of positions that V^T's operands want next to each other are
-// interleaved, by byte permutations.  Copying each thread's own pieces, in segments of 64 bytes of a
-// K row, kept loads at 5.2 TB/s, consecutive rows at 7.0.  (Matrix instructions with operands from shared memory and
-// results in tensor memory want 64 rows of queries; here there are G.)
+// half empty for groups up to 8.  Sums over d may take d in any order, so a thread's operands are whole 16-byte
+// pieces of its rows.  A warp copies its own 16 rows into shared memory (cp.async, 512 consecutive bytes an
+// instruction, tiles ahead) and no barrier but the warp's own is needed; only the pairs of positions that V^T's
+// operands want next to each other are interleaved, by byte permutations.  Copying each thread's own pieces, in
+// segments of 64 bytes of a K row, kept loads at 5.2 TB/s, consecutive rows at 7.0.  (Matrix instructions with operands
+// from shared memory and results in tensor memory want 64 rows of queries; here there are G.)
 //
 // e4m3: an element is exactly an f16, so products run in f16; a token's scales are powers of two
 // and act on its score (keys) and on its weight (values).  The reference M of a column is near the maximum of
