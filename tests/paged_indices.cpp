@@ -136,7 +136,7 @@ static void deal(int it) {
     int s = 0;
     while (!(a >= begins[s] && a < begins[s] + static_cast<long long>(Span(p, window, s, bad).tiles()) * units)) ++s;
     Cursor cur;
-    cur.seek(p, window, s, a - begins[s], bad);
+    cur.seek(p, window, units, s, a - begins[s], bad);
     int part = cur.tile == cur.first;
     // the warps' stretches follow one another, and a warp that has one finds its begin as the CTA does
     const Deal own(b - a, warps);
@@ -148,7 +148,7 @@ static void deal(int it) {
       int q = 0;
       while (!(x >= begins[q] && x < begins[q] + static_cast<long long>(Span(p, window, q, bad).tiles()) * units)) ++q;
       Cursor c2, c3 = cur;
-      c2.seek(p, window, q, x - begins[q], bad);
+      c2.seek(p, window, units, q, x - begins[q], bad);
       for (long long t = a; t < x; ++t) c3.next(p, window, units, bad);
       CHECK(c2.b == c3.b && c2.u == c3.u && c2.tile == c3.tile && c2.end == c3.end);
     }
@@ -181,11 +181,37 @@ static void deal(int it) {
   CHECK(shared == named.size());
 }
 
+// lengths that are others at every look: places stay on the line, and a walk of so many steps ends
+static void changing_lengths(int it) {
+  usp_paged_cache c = sizes();
+  const int n = pick(1, 12), units = pick(1, 9), window = pick(0, 1) ? -1 : pick(0, 300);
+  std::vector<int32_t> lens(n), table(n * c.max_pages, 0);
+  const Pool p = pool_of(c, table, lens);
+  auto change = [&]() {
+    for (auto& x : lens) x = pick(0, 2) ? pick(0, c.max_pages * c.page_size) : pick(0, 1) ? 0 : static_cast<int>(rng());
+  };
+  bool bad = false;
+  change();
+  Cursor cur;
+  cur.seek(p, window, units, pick(0, n - 1), rng() >> pick(0, 31), bad);
+  for (int k = 0; k < 200; ++k) {
+    CHECK(cur.b >= 0 && cur.b < n && cur.u >= 0 && cur.u < units && cur.tiles() >= 1 && cur.left() >= 1);
+    change();
+    if (pick(0, 1))
+      cur.next_unit(p, window, units, bad);
+    else if (cur.tile < cur.end)
+      cur.next(p, window, units, bad);
+    CHECK(cur.tile >= cur.first || cur.first >= cur.end);
+    CHECK(int64_t(cur.first) * kTile <= p.capacity && int64_t(cur.end) * kTile <= p.capacity);
+  }
+}
+
 int main() {
   for (int it = 0; it < 3000; ++it) {
     valid(it);
     any_content(it);
     deal(it);
+    changing_lengths(it);
   }
   puts("ok");
 }

@@ -251,11 +251,12 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
   Place cur;
   if (split != Split::kTiles) {
     cur.sequence(a.pool, a.window, start.x, bad);
-    cur.u = start.y;
+    cur.u = min(start.y, a.units - 1);
     Cursor c = cur;
     uint32_t tiles = 0;
-    for (int i = 0; i < count; ++i) {
-      tiles += c.end - c.first;
+    const int units = count;
+    for (int i = 0; i < units; ++i) {
+      tiles += c.tiles();
       c.next_unit(a.pool, a.window, a.units, bad);
     }
     count = tiles;
@@ -265,14 +266,14 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
       count = own.begin(w + 1) - at;
       if (count == 0) return;
       int skip = at;
-      while (skip >= cur.end - cur.first) {
-        skip -= cur.end - cur.first;
+      for (int i = 1; i < units && skip >= cur.tiles(); ++i) {
+        skip -= cur.tiles();
         cur.Cursor::next_unit(a.pool, a.window, a.units, bad);
       }
       cur.tile = cur.first + skip;
     }
   } else {
-    cur.seek(a.pool, a.window, start.x, start.y, bad);
+    cur.seek(a.pool, a.window, a.units, start.x, start.y, bad);
   }
   cur.split(a);
   bool begins = cur.tile == cur.first;  // the unit at hand begins in this warp
@@ -292,10 +293,10 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
   const uint8_t* sp;                    // its scales, keys' in lane 0, values' in lane 1
   auto enter_unit = [&]() {
     const int t0 = ld.tile * kTile;
-    const uint32_t col = a.pool.by_page.div(t0);
+    const uint32_t col = min(a.pool.by_page.div(t0), static_cast<uint32_t>(a.pool.max_pages - 1));
     table = a.pool.table + static_cast<int64_t>(ld.b) * a.pool.max_pages + col;
     page = gld(table);
-    off = t0 - static_cast<int>(col) * a.pool.page_size;
+    off = min(t0 - static_cast<int>(col) * a.pool.page_size, a.pool.page_size - kTile);
     unit_row = static_cast<int64_t>(ld.r) * a.pool.n_pages * page_rows + ld.j * a.pool.page_size;
     full = (ld.lo + kTile - 1) / kTile;
     full_end = ld.len / kTile;
@@ -345,7 +346,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
       vp += kTile * R;
       off += kTile;
       if (--left > 0) {
-        if (++ld.tile == ld.end) {
+        if (++ld.tile >= ld.end) {
           ld.next_unit(a, bad);
           enter_unit();
         } else if (off == a.pool.page_size) {
@@ -413,7 +414,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     bool none = true;  // no visible position yet
-    const int tiles = min(count, cur.end - cur.tile);
+    const int tiles = min(count, cur.left());
     int t0 = cur.tile * kTile;
     for (int it = 0; it < tiles; ++it, t0 += kTile) {
       cp_async_wait<C::kStages - 2>();
@@ -561,11 +562,11 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
     }
 
     // ---- the unit, or its part in this warp, ends
-    const bool ends = cur.tile + tiles == cur.end, own = begins;
+    const bool ends = cur.tile + tiles >= cur.end, own = begins;
     const int unit = cur.b * a.units + cur.u;
     const Heads hd(a, cur.b, cur.r, cur.j, cur.chunk);
-    const int unit_tiles = cur.end - cur.first;
-    const uint32_t stop = at + (cur.end - cur.tile);  // where the unit ends on the line
+    const int unit_tiles = cur.tiles();
+    const uint32_t stop = at + cur.left();  // where the unit ends on the line
     count -= tiles;
     at += tiles;
     if (count > 0) {  // the next unit's query is on its way meanwhile
@@ -821,7 +822,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
     const bool here = at >= lo && at < hi;
     int s = s0;
     uint32_t rest = at - lo;
-    while (here) {
+    while (here && s + 1 < s1) {
       const uint32_t n = tiles_of(a, s, bad), things_of = (by_unit ? n > 0 : n) * a.units;
       if (rest < things_of) break;
       rest -= things_of;
@@ -865,9 +866,12 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
       write_out<D>(a, unit, h, sum);
     } else {
       const uint32_t stop = parts[last].stop;
-      const int first = begins ? cta : static_cast<int>(line.owner(stop - parts[last].tiles)) / kWarps;
+      // (n_ctas and the bounds hold whatever the lengths have become meanwhile)
+      const uint32_t me = cta, first_of = line.owner(stop - parts[last].tiles) / kWarps, last_of = line.owner(stop - 1) / kWarps;
+      const int first = begins ? cta : static_cast<int>(min(first_of, me));
+      const int end = static_cast<int>(min(max(last_of, me), n_ctas - 1)) + 1;
       leave<D>(a, first, cta - first, h, sum);
-      if (h == 0 && lane == 0) crossing[begins] = Crossing{unit, first, static_cast<int>(line.owner(stop - 1)) / kWarps - first + 1, cta - first};
+      if (h == 0 && lane == 0) crossing[begins] = Crossing{unit, first, end - first, cta - first};
     }
   }
   if (split == Split::kTiles) join<D, kE4m3>(a, smem, crossing);

@@ -118,7 +118,8 @@ struct Deal {
   }
 };
 
-// A place on the line: tile `tile` of unit u of sequence b.
+// A place on the line: tile `tile` of unit u of sequence b.  It stays on the line whatever the lengths are when they are
+// read: where they change while a kernel runs its results mean nothing, but it reads no place that is none and it ends.
 struct Cursor {
   int b, u, tile, first, end, len, lo;
   USP_HD void sequence(const Pool& p, int window, int seq, bool& bad) {
@@ -131,24 +132,30 @@ struct Cursor {
     end = s.end;
   }
   // `rest` tiles into sequence `seq`
-  USP_HD void seek(const Pool& p, int window, int seq, uint32_t rest, bool& bad) {
+  USP_HD void seek(const Pool& p, int window, int units, int seq, uint32_t rest, bool& bad) {
     sequence(p, window, seq, bad);
-    const uint32_t n = end - first;
-    u = static_cast<int>(rest / n);
-    tile = first + static_cast<int>(rest - u * n);
+    const uint32_t n = tiles(), at = rest / n;
+    u = at < static_cast<uint32_t>(units) ? static_cast<int>(at) : units - 1;
+    tile = first + static_cast<int>(rest - at * n);
   }
+  // of the unit, and from the tile on: one at least
+  USP_HD int tiles() const { return end > first ? end - first : 1; }
+  USP_HD int left() const { return end > tile ? end - tile : 1; }
   USP_HD void next(const Pool& p, int window, int units, bool& bad) {
-    if (++tile == end) next_unit(p, window, units, bad);
+    if (++tile >= end) next_unit(p, window, units, bad);
   }
-  // to the begin of the next unit; behind the last one it is no place
+  // to the begin of the next unit; behind the line's end it stays at the last one
   USP_HD void next_unit(const Pool& p, int window, int units, bool& bad) {
     tile = first;
     if (++u < units) return;
-    int s = b;
-    do {
-      if (++s >= p.n_seqs) return;
-      sequence(p, window, s, bad);
-    } while (first >= end);
+    u = units - 1;
+    for (int s = b + 1; s < p.n_seqs; ++s) {
+      const Span next(p, window, s, bad);
+      if (next.first < next.end) {
+        sequence(p, window, s, bad);
+        return;
+      }
+    }
   }
 };
 
