@@ -558,7 +558,8 @@ enum { USP_CACHE_BF16 = 0, USP_CACHE_E4M3 = 1 };
  * usp_cache_read is the way back: the same tokens out of the cache into k and v, rounded to bf16 (exact for a
  * bf16 cache; e4m3 values times their power of two are rounded only below bf16's normal range).  Tokens that
  * are not described (behind cu[n_seqs], or of an empty place) are left as they were.
- * Either of k and v may be NULL, when it is not wanted.  Neither may overlap the pool, nor, when read, the other.
+ * Either of k and v may be NULL, when it is not wanted.  Neither may overlap the cache's arrays, nor, when read, the
+ * other or cu_seqlens.
  * dev_status: USP_ERR_BAD_PAGES; tokens without a place in the pool are passed over.
  * Errors: USP_ERR_INVALID_ARG, USP_ERR_INDIVISIBLE, USP_ERR_UNSUPPORTED (D, page_size, dtype; sizes past 2^30
  * tokens or 2^40 elements), USP_ERR_ALIGNMENT, USP_ERR_CUDA. */
@@ -572,7 +573,8 @@ int usp_cache_read(const usp_paged_cache* cache, void* k, void* v, int tokens, c
  *     s_u = softmax_scale q.k_u for u < lens[s], and lens[s] - 1 - u <= window_left with a window
  *     LSE = ln( sum_u exp(s_u) + exp(sink) ),  O = sum_u exp(s_u - LSE) v_u
  * O = 0 where nothing is visible (LSE = -inf, or the sink).
- * q, o: bf16 [P][n_seqs][Hq/P][D]; lse: fp32 [P][n_seqs][Hq/P]; sinks: fp32 [Hq] or NULL.  No two may overlap.
+ * q, o: bf16 [P][n_seqs][Hq/P][D]; lse: fp32 [P][n_seqs][Hq/P]; sinks: fp32 [Hq] or NULL.  What is written
+ * (o, lse, ws) may overlap nothing else of the call.
  * The work of all sequences is dealt out evenly in pieces of 16 positions, whatever their lengths, and pieces
  * of one sequence are joined in the order of their positions: the result does not depend on timing (on the other
  * sequences' lengths it does, within its roundings).

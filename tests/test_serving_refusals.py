@@ -77,6 +77,11 @@ def test_cache_refusals(lib):
         assert f(ctypes.byref(_cache()), inside, Bq, 3, None, None, None) == B.USP_ERR_INVALID_ARG
         assert f(ctypes.byref(_cache()), A, inside, 3, None, None, None) == B.USP_ERR_INVALID_ARG
     assert lib.usp_cache_read(ctypes.byref(_cache()), A, P((1 << 20) + 16), 3, None, None, None) == B.USP_ERR_INVALID_ARG
+    eight = _cache(**e)
+    for f in (lib.usp_cache_append, lib.usp_cache_read):          # 640 scales each; table and lengths
+        for p in ((1 << 20) + 624, 1 << 21, 16):
+            assert f(ctypes.byref(eight), P(p), None, 3, None, None, None) == B.USP_ERR_INVALID_ARG
+    assert lib.usp_cache_read(ctypes.byref(_cache()), Dq, None, 3, P((1 << 41) + 4), None, None) == B.USP_ERR_INVALID_ARG
     for kw in (dict(P=0), dict(Hkv=0), dict(D=0), dict(n_pages=0), dict(page_size=0), dict(n_seqs=0), dict(max_pages=0),
                dict(dtype=2), dict(k_pages=None), dict(v_pages=None), dict(block_table=None), dict(lens=None),
                dict(k_scales=1 << 20), dict(dtype=B.USP_CACHE_E4M3), dict(e, v_scales=None)):
@@ -106,6 +111,19 @@ def test_decode_refusals(lib):
     assert rc(Hq=1028) == B.USP_ERR_UNSUPPORTED and rc(window=-2) == B.USP_ERR_UNSUPPORTED
     assert rc(q=P((1 << 20) + 2)) == B.USP_ERR_ALIGNMENT and rc(sinks=P(2)) == B.USP_ERR_ALIGNMENT
     assert rc(lse=P((1 << 41) + 2)) == B.USP_ERR_ALIGNMENT
+    # what is written lies on nothing else (rows: 24 of 64)
+    table, lens, sinks = c.block_table, c.lens, P(1 << 22)
+    c.block_table, c.lens = 1 << 23, 1 << 24
+    far = dict(q=P(1 << 42), o=P(1 << 43), lse=P(1 << 44), ws=P(1 << 45), sinks=sinks)
+    for name, at in (("o", 24 * 64 * 2), ("lse", 24 * 4), ("ws", n)):
+        ends_in = [p - (at + 15) // 16 * 16 + 16 for p in (c.k_pages, c.v_pages, c.block_table, c.lens, 1 << 22, 1 << 42)]
+        begins_in = [c.v_pages + 2 * 4 * 64 * 10 * 16 - 16, c.block_table + 32, (1 << 42) + 24 * 64 * 2 - 16]
+        if name == "ws":
+            ends_in, begins_in = [(p + 255) // 256 * 256 for p in ends_in], [p // 256 * 256 for p in begins_in]
+        for p in ends_in + begins_in:
+            assert rc(**dict(far, **{name: P(p)})) == B.USP_ERR_INVALID_ARG, (name, hex(p))
+    assert rc(**dict(far, ws=P((1 << 43) - n // 512 * 256))) == rc(**dict(far, ws=P((1 << 44) - n // 512 * 256))) == B.USP_ERR_INVALID_ARG
+    c.block_table, c.lens = table, lens
     assert rc(ws=None) == rc(ws=P((1 << 40) + 16)) == rc(n=n - 1) == B.USP_ERR_WORKSPACE
 
 

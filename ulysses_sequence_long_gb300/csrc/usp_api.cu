@@ -292,6 +292,15 @@ int check_cache(const usp_paged_cache* c) {
   return USP_OK;
 }
 
+// whether n bytes at x lie on one of the cache's arrays
+bool meets_cache(const void* x, uint64_t n, const usp_paged_cache* c) {
+  const uint64_t rows = static_cast<uint64_t>(c->Hkv >= c->P ? c->Hkv : c->P) * c->n_pages * c->page_size;
+  const uint64_t pool = rows * c->D * (c->dtype == USP_CACHE_E4M3 ? 1 : 2);
+  if (overlap(x, n, c->k_pages, pool) || overlap(x, n, c->v_pages, pool)) return true;
+  if (c->dtype == USP_CACHE_E4M3 && (overlap(x, n, c->k_scales, rows) || overlap(x, n, c->v_scales, rows))) return true;
+  return overlap(x, n, c->block_table, 4ull * c->n_seqs * c->max_pages) || overlap(x, n, c->lens, 4ull * c->n_seqs);
+}
+
 int move_tokens(const usp_paged_cache* c, const void* k, const void* v, int tokens, const int32_t* cu, bool append,
                 int32_t* status, usp_stream_t stream) {
   int rc = check_cache(c);
@@ -301,10 +310,12 @@ int move_tokens(const usp_paged_cache* c, const void* k, const void* v, int toke
   if (tokens >= (1 << 30) || tokens * heads >= (1ll << 32)) return USP_ERR_UNSUPPORTED;
   if (!aligned16(k) || !aligned16(v)) return USP_ERR_ALIGNMENT;
   if (!aligned4(cu)) return USP_ERR_ALIGNMENT;
-  const uint64_t elems = static_cast<uint64_t>(heads) * c->D, n = 2 * elems * tokens;
-  const uint64_t pool = elems * c->n_pages * c->page_size * (c->dtype == USP_CACHE_E4M3 ? 1 : 2);
-  for (const void* x : {k, v})
-    if (x != nullptr && (overlap(x, n, c->k_pages, pool) || overlap(x, n, c->v_pages, pool))) return USP_ERR_INVALID_ARG;
+  const uint64_t n = 2ull * heads * c->D * tokens;
+  for (const void* x : {k, v}) {
+    if (x == nullptr) continue;
+    if (meets_cache(x, n, c)) return USP_ERR_INVALID_ARG;
+    if (!append && cu != nullptr && overlap(x, n, cu, 4ull * (c->n_seqs + 1))) return USP_ERR_INVALID_ARG;
+  }
   if (!append && k != nullptr && v != nullptr && overlap(k, n, v, n)) return USP_ERR_INVALID_ARG;
   return launch_cache_move(*c, const_cast<void*>(k), const_cast<void*>(v), tokens, cu, append, status,
                            reinterpret_cast<cudaStream_t>(stream));
@@ -745,8 +756,15 @@ int usp_attn_decode(const usp_paged_cache* cache, int Hq, int window_left, float
   if (!all_aligned16(q, o) || !aligned4(lse) || !aligned4(sinks)) return USP_ERR_ALIGNMENT;
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < attn_decode_ws_bytes(*cache))
     return USP_ERR_WORKSPACE;
+  // what is written lies on nothing else
   const uint64_t rows = static_cast<uint64_t>(cache->n_seqs) * Hq, n = 2 * rows * cache->D;
-  if (overlap(q, n, o, n) || overlap(o, n, lse, 4 * rows) || overlap(q, n, lse, 4 * rows)) return USP_ERR_INVALID_ARG;
+  const struct { const void* at; uint64_t n; } out[3] = {{o, n}, {lse, 4 * rows}, {ws, ws_bytes}};
+  for (int i = 0; i < 3; ++i) {
+    const auto& x = out[i];
+    if (overlap(x.at, x.n, q, n) || overlap(x.at, x.n, out[(i + 1) % 3].at, out[(i + 1) % 3].n) ||
+        (sinks != nullptr && overlap(x.at, x.n, sinks, 4ull * Hq)) || meets_cache(x.at, x.n, cache))
+      return USP_ERR_INVALID_ARG;
+  }
   const float scale = softmax_scale != 0.f ? softmax_scale : 1.f / sqrtf(static_cast<float>(cache->D));
   return launch_attn_decode(*cache, Hq, window_left, scale, sinks, q, o, lse, ws, dev_status,
                             reinterpret_cast<cudaStream_t>(stream));
