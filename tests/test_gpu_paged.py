@@ -540,6 +540,25 @@ def test_two_streams_and_two_layers_at_once():
         assert torch.equal(att._out(2)[0], o) and torch.equal(att.lse, lse)
 
 
+def test_tokens_read_on_another_stream_into_new_tensors():
+    lens = [70, 33]
+    c, table, ln, k, v, q, z, att = _decode_case(lens, 4, 2, 64, 1, 16, BF)
+    cu = _cu(lens)
+    want = c.read(table, ln, cu, tokens=sum(lens) + 5)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        for _ in range(20):
+            y = torch.empty_like(want[0]), torch.empty_like(want[1])
+            torch.cuda._sleep(200_000)   # the current stream is behind: its zeros would come after the tokens
+            for t in y:
+                t.fill_(7)
+            del y, t
+            got = c.read(table, ln, cu, tokens=sum(lens) + 5, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_a_pool_whose_tensors_were_exchanged():
     """Every call reads and writes the tensors where they are then; one of another size or type is refused."""
     lens = [70, 33]
@@ -556,12 +575,49 @@ def test_a_pool_whose_tensors_were_exchanged():
         keep.view(torch.uint8).fill_(0x5A)
         assert torch.equal(att.forward(q, table, ln, z), want), name
         t = getattr(c, name)
-        for bad in (torch.cat([t.view(torch.uint8).view(-1)] * 2), t.view(torch.uint8).double(), t.cpu()):
+        for bad in (torch.cat([t.view(torch.uint8).view(-1)] * 2), t[:0],
+                    t.view(torch.int16 if name == "status" else torch.int8), t.view(torch.uint8).double(), t.cpu()):
             setattr(c, name, bad)
-            with pytest.raises((TypeError, ValueError)):
-                att.forward(q, table, ln, z)
+            for _ in range(2):
+                with pytest.raises((TypeError, ValueError)):
+                    att.forward(q, table, ln, z)
             setattr(c, name, t)
+    t, other, s = c.k_pages, c.k_pages.clone(), c.status   # one that is good beside one that is not: neither is taken
+    other.view(torch.uint8).fill_(0x5A)
+    c.k_pages, c.status = other, s.cpu()
+    with pytest.raises(TypeError):
+        att.forward(q, table, ln, z)
+    c.k_pages, c.status = t, s
     assert torch.equal(att.forward(q, table, ln, z), want) and att.read_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_the_binding_itself(dtype):
+    from ulysses_sequence_long_gb300 import binding as B
+    lens = [40, 3]
+    c, table, ln, k, v, q, z, att = _decode_case(lens, 2, 2, 64, 1, 16, dtype, sinks=True)
+    cu = _cu(lens)
+    pools = [None if t is None else torch.zeros_like(t) for t in (c.k_pages, c.v_pages, c.k_scales, c.v_scales)]
+    prm = B.paged_cache(2, 64, 1, *pools[:2], table, ln, *pools[2:])
+    B.usp_cache_append(prm, k, None, 43, cu, c.status)
+    B.usp_cache_append(prm, None, v, 43, cu, c.status)
+    got, want = (torch.empty_like(k), torch.empty_like(v)), c.read(table, ln, cu, tokens=43)
+    B.usp_cache_read(prm, got[0], got[1], 43, cu)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    ws = torch.zeros((B.usp_attn_decode_workspace_bytes(prm, 4),), dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty((2, 4), device="cuda")
+    B.usp_attn_decode(prm, 4, q, o, lse, ws, sinks=z, dev_status=c.status)
+    assert torch.equal(o, att.forward(q, table, ln, z)) and torch.equal(lse.view(-1), att.lse.view(-1))
+    bad = [lambda: B.usp_cache_append(prm, None, None, 43, cu), lambda: B.usp_cache_append(prm, k, v, 43, cu, c.status.cpu()),
+           lambda: B.usp_cache_read(prm, got[0], got[1][:, :5], 43, cu), lambda: B.usp_cache_read(prm, got[0], got[0], 43, cu),
+           lambda: B.usp_attn_decode(prm, 4, q, o, lse, ws[:256]), lambda: B.usp_attn_decode(prm, 4, q, q, lse, ws),
+           lambda: B.usp_attn_decode(prm, 4, q, o, lse, ws.cpu()), lambda: B.usp_attn_decode(prm, 4, q, o, lse[:1], ws),
+           lambda: B.paged_cache(2, 64, 1, *pools[:2], table, ln.cpu(), *pools[2:]),
+           lambda: B.paged_cache(2, 64, 1, pools[0], pools[1][:, :1], table, ln, *pools[2:])]
+    for f in bad:
+        with pytest.raises((TypeError, ValueError, B.UspError)):
+            f()
+    assert c.read_status() == 0 and not ws[:12288].any()
 
 
 def test_refused_tensors():

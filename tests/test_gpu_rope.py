@@ -147,6 +147,17 @@ def test_streams_graphs_and_exchanged_storage():
     rope.forward(x, None, pos, out=(out, None), stream=s)
     s.synchronize()
     assert torch.equal(out, want)
+    # new outputs are memory of the stream, given as an object or as its handle: what the current stream has just let go
+    # of and still writes is not theirs
+    for stream in (s, s.cuda_stream):
+        for _ in range(20):
+            y = torch.empty_like(x)
+            torch.cuda._sleep(200_000)
+            y.zero_()
+            del y
+            got, _ = rope.forward(x, None, pos, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         rope.forward(x, None, pos, out=(out, None))
@@ -158,6 +169,17 @@ def test_streams_graphs_and_exchanged_storage():
     half, _ = rope.forward(x, None, pos * 2)
     rope.freqs.data = old
     assert torch.equal(half, want)
+    for name in ("freqs", "axes"):   # at the same place, but fewer
+        t = getattr(rope, name)
+        setattr(rope, name, t[:8])
+        for _ in range(2):
+            with pytest.raises(ValueError):
+                rope.forward(x, None, pos)
+        setattr(rope, name, t)
+    rope.interleaved = True
+    other = rope.forward(x, None, pos)[0]
+    rope.interleaved = False
+    assert torch.equal(rope.forward(x, None, pos)[0], want) and not torch.equal(other, want)
     for name in ("freqs", "axes", "status"):
         t = getattr(rope, name)
         setattr(rope, name, t.clone())
@@ -168,6 +190,25 @@ def test_streams_graphs_and_exchanged_storage():
                 rope.forward(x, None, pos)
         setattr(rope, name, t)
     assert torch.equal(rope.forward(x, None, pos)[0], want) and rope.read_status() == 0
+
+
+def test_the_binding_itself():
+    from ulysses_sequence_long_gb300 import binding as B
+    rope, f, ax = _rotary(64)
+    x = torch.randn((300, 8, 128), generator=torch.Generator().manual_seed(7)).to(torch.bfloat16).cuda()
+    k = x[:, :2].contiguous()
+    pos = torch.arange(150 * rope.n_axes, dtype=torch.int32).cuda()
+    prm = B.rope_params(8, 2, 128, pos.clone(), rope.freqs.clone(), 300, rope.n_axes, rope.axes.clone())
+    torch.full((150 * rope.n_axes,), 9, dtype=torch.int32, device="cuda")   # (the parameters keep their tensors)
+    for fn, turn in ((B.usp_rope_fwd, rope.forward), (B.usp_rope_bwd, rope.backward)):
+        y, yk = torch.empty_like(x), torch.empty_like(k)
+        fn(prm, x, k, y, yk, rope.status)
+        want = turn(x, k, pos)
+        assert torch.equal(y, want[0]) and torch.equal(yk, want[1])
+        for args in ((x, k, y, yk[:1], rope.status), (x, k, y, yk, rope.status.cpu()), (x.float(), k, y, yk),
+                     (x.cpu(), k, y, yk), (x, k, y, None)):
+            with pytest.raises((TypeError, ValueError, B.UspError)):
+                fn(prm, *args)
 
 
 def _layer(w, rope, **kw):
@@ -254,13 +295,17 @@ def test_the_hybrid_layer():
     assert a.read_status() == 0
 
 
-@pytest.mark.parametrize("capped", [False, True])
-def test_a_refused_forward_leaves_the_turned_shards(capped):
-    from ulysses_sequence_long_gb300.pipeline import ScoreMods
-    w = W.Workload("rope", B=1, S=256, Hq=4, Hkv=2, D=64, P=2, doc_mode="explicit", doc_lens=(256,))
+@pytest.mark.parametrize("kind", ["layer", "capped", "hybrid"])
+def test_a_refused_forward_leaves_the_turned_shards(kind):
+    from ulysses_sequence_long_gb300.pipeline import HybridAttention, ScoreMods
+    S, P = (1024, 4) if kind == "hybrid" else (256, 2)   # (a ring step has S/ring keys, a multiple of 256)
+    w = W.Workload("rope", B=1, S=S, Hq=4, Hkv=2, D=64, P=P, doc_mode="explicit", doc_lens=(S,))
     dev, _ = device_inputs(w)
     rope, _, _ = _rotary(32)
-    a = _layer(w, rope, mods=ScoreMods(softcap=20.0) if capped else None)
+    if kind == "hybrid":
+        a = HybridAttention(shape_of(w), 2, rope=rope)
+    else:
+        a = _layer(w, rope, mods=ScoreMods(softcap=20.0) if kind == "capped" else None)
     a.forward(dev["q"], dev["k"], dev["v"], dev["pos"])
     kept = [x.clone() for x in a.backward(dev["do"])]
     for bad in (dict(v=dev["q"]), dict(pos=dev["pos"].long()), dict(q=dev["k"])):

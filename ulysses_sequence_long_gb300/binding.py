@@ -7,6 +7,7 @@ is no CPU fallback, and a missing library or a CPU tensor is an error.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -548,6 +549,16 @@ def run_on(index: int, stream, fn, where, *args):
         raise UspError(rc, where)
 
 
+def memory_of(index: int, stream):
+    """Tensors made within belong to `stream` (None: device `index`'s current one): what they are filled with, and who had
+    their memory before, comes before the call that takes them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
+    return torch.cuda.stream(stream)
+
+
 def call_on(device: torch.device, stream, where, *args):
     run_on(device.index, stream, getattr(load(), where), where, *args)
 
@@ -558,11 +569,22 @@ def rope_params(Hq, Hkv, D, positions, freqs, tokens, n_axes=1, axes=None, inter
         raise ValueError(f"positions must be [{n_axes}][n_pos], got {positions.numel()} elements")
     if axes is not None and axes.numel() != freqs.numel():
         raise ValueError(f"axes must have an entry for each of the {freqs.numel()} frequencies")
-    return RopeParams(tokens, Hq, Hkv, D, n_axes, positions.numel() // n_axes, freqs.numel(), 1 if interleaved else 0,
-                      _dev(positions, "positions", _I32), _dev(freqs, "freqs", _F32), _dev(axes, "axes", _I32))
+    p = RopeParams(tokens, Hq, Hkv, D, n_axes, positions.numel() // n_axes, freqs.numel(), 1 if interleaved else 0,
+                   _dev(positions, "positions", _I32), _sized(freqs, "freqs", _F32, freqs.numel(), positions),
+                   None if axes is None else _sized(axes, "axes", _I32, freqs.numel(), positions))
+    p.tensors = positions, freqs, axes   # (they live as long as their addresses here)
+    return p
+
+
+def _same_device(struct, t, *others):
+    """The tensors that `struct` was made of, `t` and the others of a call (or None) are on one device."""
+    for x in (*getattr(struct, "tensors", ())[:1], *others):
+        if x is not None and x.device != t.device:
+            raise ValueError(f"tensors of one call are on {x.device} and {t.device}")
 
 
 def _rope(where, params, x, y, names, dev_status, stream):
+    _same_device(params, x[0], dev_status)
     n = (params.tokens * params.Hq * params.D, params.tokens * params.Hkv * params.D)
     ptrs = [None if t is None else _sized(t, name, _BF, n[i % 2], x[0])
             for i, (t, name) in enumerate(zip(x + y, names))]
@@ -593,14 +615,19 @@ def paged_cache(Hkv, D, P, k_pages, v_pages, block_table, lens, k_scales=None, v
     kp, vp = _dev(k_pages, "k_pages"), _sized(v_pages, "v_pages", k_pages.dtype, n, k_pages)
     ks = _sized(k_scales, "k_scales", torch.uint8, n // D, k_pages) if eight else None
     vs = _sized(v_scales, "v_scales", torch.uint8, n // D, k_pages) if eight else None
-    return PagedCacheStruct(P, Hkv, D, k_pages.shape[1], k_pages.shape[3], lens.numel(), block_table.shape[1],
-                            USP_CACHE_E4M3 if eight else USP_CACHE_BF16, kp, vp, ks, vs,
-                            _sized(block_table, "block_table", _I32, lens.numel() * block_table.shape[1], k_pages),
-                            _sized(lens, "lens", _I32, lens.numel(), k_pages))
+    c = PagedCacheStruct(P, Hkv, D, k_pages.shape[1], k_pages.shape[3], lens.numel(), block_table.shape[1],
+                         USP_CACHE_E4M3 if eight else USP_CACHE_BF16, kp, vp, ks, vs,
+                         _sized(block_table, "block_table", _I32, lens.numel() * block_table.shape[1], k_pages),
+                         _sized(lens, "lens", _I32, lens.numel(), k_pages))
+    c.tensors = k_pages, v_pages, k_scales, v_scales, block_table, lens
+    return c
 
 
 def _cache_move(where, cache, k, v, tokens, cu_seqlens, dev_status, stream):
     like = k if k is not None else v
+    if like is None:
+        raise TypeError("k or v must be given")
+    _same_device(cache, like, dev_status)
     n = cache.P * tokens * (cache.Hkv // cache.P if cache.Hkv >= cache.P else 1) * cache.D
     kp, vp = (None if t is None else _sized(t, name, _BF, n, like) for t, name in ((k, "k"), (v, "v")))
     cu = None if cu_seqlens is None else _sized(cu_seqlens[:cache.n_seqs + 1], "cu_seqlens", _I32, cache.n_seqs + 1, like)
@@ -622,6 +649,7 @@ def usp_attn_decode_workspace_bytes(cache: PagedCacheStruct, Hq: int) -> int:
 def usp_attn_decode(cache: PagedCacheStruct, Hq, q, o, lse, ws, window_left=-1, softmax_scale=0.0, sinks=None,
                     dev_status=None, stream=None):
     rows = cache.n_seqs * Hq
+    _same_device(cache, q, ws, dev_status)
     call_on(q.device, stream, "usp_attn_decode", ctypes.byref(cache), Hq, window_left, softmax_scale,
             None if sinks is None else _sized(sinks, "sinks", _F32, Hq, q), _sized(q, "q", _BF, rows * cache.D, q),
             _sized(o, "o", _BF, rows * cache.D, q), _sized(lse, "lse", _F32, rows, q), _dev(ws, "ws"),

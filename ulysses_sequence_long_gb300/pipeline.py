@@ -127,14 +127,14 @@ class Rotary:
         self._find()
 
     def _find(self):
-        """The addresses of the rotation's tensors, for the calls to come (which see by them when one was exchanged; a
-        reference keeps another tensor from getting the same one meanwhile)."""
+        """The addresses of the rotation's tensors, for the calls to come (which see when a tensor or its storage was
+        exchanged; references keep others from getting the same places meanwhile)."""
         at, n = self._at, self._n_pairs
-        self._held = (self.freqs, self.axes, self.status)
-        self._found = (at(self.freqs, "freqs", torch.float32, n),
-                       None if self.axes is None else at(self.axes, "axes", torch.int32, n),
-                       at(self.status, "status", torch.int32, 1))
-        self._seen = {}
+        held = self.freqs, self.axes, self.status
+        self._found = (at(held[0], "freqs", torch.float32, n),
+                       None if held[1] is None else at(held[1], "axes", torch.int32, n),
+                       at(held[2], "status", torch.int32, 1))
+        self._held, self._seen = held, {}
 
     def _plan(self, q, k, positions):
         """Sizes of a call, by the shapes."""
@@ -160,13 +160,14 @@ class Rotary:
 
     def _turn(self, fn, where, q, k, positions, out, stream):
         freqs, axes, status = self._found
-        mine = self.axes
-        if (self.freqs.data_ptr() != freqs or self.status.data_ptr() != status
-                or (mine is not None and mine.data_ptr()) != (axes is not None and axes)):
+        mine, mine_axes, mine_status = self._held
+        if (self.freqs is not mine or self.axes is not mine_axes or self.status is not mine_status
+                or mine.data_ptr() != freqs or mine_status.data_ptr() != status
+                or (axes is not None and mine_axes.data_ptr() != axes)):
             self._find()
             status = self._found[2]
         n_pos = positions.numel()
-        shapes = (q.shape, None if k is None else k.shape, n_pos)
+        shapes = (q.shape, None if k is None else k.shape, n_pos, self.n_axes, self.interleaved)
         p = self._seen.get(shapes)
         if p is None:
             p = self._plan(q, k, positions)
@@ -176,8 +177,9 @@ class Rotary:
         bf, index, at = torch.bfloat16, self._index, self._at
         p.positions = at(positions, "positions", torch.int32, n_pos)
         if out is None:
-            out = (torch.empty_like(q, memory_format=torch.contiguous_format),
-                   None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format))
+            with B_.memory_of(index, stream):
+                out = (torch.empty_like(q, memory_format=torch.contiguous_format),
+                       None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format))
         y, yk = out
         if (k is not None and q.dtype is bf and k.dtype is bf and y.dtype is bf and yk.dtype is bf
                 and q.get_device() == index and k.get_device() == index and y.get_device() == index
@@ -192,7 +194,8 @@ class Rotary:
 
     def forward(self, q, k, positions, out=None, stream=None):
         """(q, k) turned: bf16 ``[..., H, D]`` each (k may be None), positions int32 ``[n_axes][tokens]``, or of a
-        divisor of the tokens, over which they repeat.  ``out``: the tensors to write, which may be q and k."""
+        divisor of the tokens, over which they repeat.  ``out``: the tensors to write, which may be q and k (new ones are
+        memory of ``stream``)."""
         return self._turn(self._fwd, "usp_rope_fwd", q, k, positions, out, stream)
 
     def backward(self, dq, dk, positions, out=None, stream=None):
@@ -215,6 +218,16 @@ class _Turned:
         if rope.device != self.q_rot.device:
             raise ValueError(f"the rotary frequencies are on {rope.device}, the layer on {self.q_rot.device}")
         self._rope_positions = None
+
+    def _check_turned(self, v_seq, pos_shards, sinks):
+        """A forward that is refused leaves the turned shards, which the backward reads: what else it takes is looked at
+        before they are written."""
+        if self.rope is None:
+            return
+        B_._sized(v_seq, "v", torch.bfloat16, self.k_rot.numel(), self.k_rot)
+        B_._sized(pos_shards, "position ids", torch.int32, self.shape.B * self.shape.S, self.k_rot)
+        if sinks is not None:
+            B_._sized(sinks, "sinks", torch.float32, self.shape.Hq, self.k_rot)
 
     def rotate(self, q_seq, k_seq, positions, stream=None):
         """The layer's first step: q and k shards turned (as they are without ``rope``), for ``exchange_qkv``."""
@@ -590,11 +603,7 @@ class UlyssesAttention(_Turned):
         """Sequence shards in, sequence shards out (``self.o_seq``).  ``rope_positions``: int32
         ``[n_axes][P][B][S/P]`` for the layer's ``rope`` (default: the position ids, one axis)."""
         if self.rope is not None:
-            # (a call that is refused leaves the turned shards, which the backward reads)
-            B_._sized(v_seq, "v", torch.bfloat16, self.k_rot.numel(), self.k_rot)
-            B_._sized(pos_shards, "position ids", torch.int32, self.shape.B * self.shape.S, self.k_rot)
-            if sinks is not None:
-                B_._sized(sinks, "sinks", torch.float32, self.shape.Hq, self.k_rot)
+            self._check_turned(v_seq, pos_shards, sinks)
             q_seq, k_seq = self.rotate(q_seq, k_seq, pos_shards if rope_positions is None else rope_positions, stream)
         if self._mods is not None:
             return self._on_device(self._mod_forward, q_seq, k_seq, v_seq, pos_shards, sinks, stream=stream)
@@ -794,6 +803,7 @@ class HybridAttention(_Turned):
         boundaries, 3 after the ring steps and merges, 4 after the O exchange."""
         s = self.shape
         mark = marks or (lambda i: None)
+        self._check_turned(v_seq, pos_shards, sinks)
         q_seq, k_seq = self.rotate(q_seq, k_seq, pos_shards if rope_positions is None else rope_positions, stream)
         mark(0)
         if self.fused:

@@ -67,22 +67,27 @@ class PagedCache:
 
     def _find(self):
         """The addresses of the pool's tensors, which have to be of their sizes and types, for the calls to come (which
-        see by them when one was exchanged; a reference keeps another tensor from getting the same one meanwhile)."""
+        see when a tensor or its storage was exchanged; references keep others from getting the same places meanwhile)."""
         c, index, n = self._fixed, self._index, self.P * self.n_pages * self.hk * self.page_size
-        c.k_pages = _where(self.k_pages, "k_pages", self.dtype, n * self.D, index)
-        c.v_pages = _where(self.v_pages, "v_pages", self.dtype, n * self.D, index)
+        held = self.k_pages, self.v_pages, self.k_scales, self.v_scales, self.status
+        ks = vs = None
+        k = _where(held[0], "k_pages", self.dtype, n * self.D, index)
+        v = _where(held[1], "v_pages", self.dtype, n * self.D, index)
         if self.dtype is _F8:
-            c.k_scales = _where(self.k_scales, "k_scales", _U8, n, index)
-            c.v_scales = _where(self.v_scales, "v_scales", _U8, n, index)
-        self._status = _where(self.status, "status", _I32, 1, index)
-        self._held = (self.k_pages, self.v_pages, self.k_scales, self.v_scales, self.status)
-        self._found = (c.k_pages, c.v_pages, c.k_scales, c.v_scales, self._status)
+            ks = _where(held[2], "k_scales", _U8, n, index)
+            vs = _where(held[3], "v_scales", _U8, n, index)
+        status = _where(held[4], "status", _I32, 1, index)
+        # (all of them are in order)
+        c.k_pages, c.v_pages, c.k_scales, c.v_scales, self._status = k, v, ks, vs, status
+        self._held, self._found = held, (k, v, ks, vs, status)
 
     def _struct(self, block_table, lens) -> B_.PagedCacheStruct:
         """This call's own structure (threads may use one cache at once), with the addresses that the tensors have now."""
         k, v, ks, vs, status = self._found
-        if (self.k_pages.data_ptr() != k or self.v_pages.data_ptr() != v or self.status.data_ptr() != status
-                or (ks is not None and (self.k_scales.data_ptr() != ks or self.v_scales.data_ptr() != vs))):
+        hk, hv, hks, hvs, hstatus = self._held
+        if (self.k_pages is not hk or self.v_pages is not hv or self.status is not hstatus or self.k_scales is not hks
+                or self.v_scales is not hvs or hk.data_ptr() != k or hv.data_ptr() != v or hstatus.data_ptr() != status
+                or (ks is not None and (hks.data_ptr() != ks or hvs.data_ptr() != vs))):
             self._find()
         c = B_.PagedCacheStruct.from_buffer_copy(self._fixed)
         index = self._index
@@ -120,13 +125,14 @@ class PagedCache:
 
     def read(self, block_table, lens, cu_seqlens=None, out=None, tokens: Optional[int] = None, stream=None):
         """The way back: (k, v) of the last tokens of each sequence, into ``out``, or into new tensors of ``tokens``
-        tokens (places without a token are zero there, and left alone in ``out``)."""
+        tokens (places without a token are zero there, and left alone in ``out``); the new ones are memory of ``stream``."""
         if out is None:
             if tokens is None:
                 if cu_seqlens is not None:
                     raise ValueError("read needs out or tokens beside cu_seqlens (their sum is on the device)")
                 tokens = lens.shape[0]
-            out = tuple(torch.zeros((self.P, tokens, self.hk, self.D), dtype=_BF, device=self.device) for _ in range(2))
+            with B_.memory_of(self._index, stream):
+                out = tuple(torch.zeros((self.P, tokens, self.hk, self.D), dtype=_BF, device=self.device) for _ in range(2))
         self._move(self._read, "usp_cache_read", out[0], out[1], block_table, lens, cu_seqlens, stream)
         return out
 
