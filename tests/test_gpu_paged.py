@@ -301,6 +301,38 @@ def test_decode_ragged_batches(D, dtype, n, most):
     _check_decode(c, lens, k, v, q, z, att, o, att.lse)
 
 
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, BF), (64, F8), (128, F8)], ids=str)
+@pytest.mark.parametrize("G", [9, 16, 24, 40])
+@pytest.mark.parametrize("lens,Hkv", [([9000, 3, 0, 17], 1), ([20001], 1), ([300] * 12 + [0, 1], 3), ([40, 0, 7] * 60, 2)],
+                         ids=["long", "one", "middle", "short"])
+def test_decode_groups_of_several_warps(lens, Hkv, G, D, dtype):
+    """More query heads of a key/value head than a warp has: teams of warps, some of them without heads."""
+    c, table, ln, k, v, q, z, att = _decode_case(lens, G, Hkv, D, 1, 48, dtype, seed=G, sinks=G == 24, gain=1.5,
+                                                 window=-1 if G < 40 else 1000)
+    o = att.forward(q, table, ln, z).clone()
+    lse = att.lse.clone()
+    assert att.read_status() == 0 and not att._ws[:12 * 1024].any()
+    _check_decode(c, lens, k, v, q, z, att, o, lse)
+    assert torch.equal(att.forward(q, table, ln, z), o) and torch.equal(att.lse, lse)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, BF), (64, F8), (128, F8)], ids=str)
+@pytest.mark.parametrize("lens,Hkv,G,window", [([160001, 0, 5, 300], 2, 24, -1), ([150000], 1, 40, 147003),
+                                               ([1297] * 38 + [0, 0], 8, 16, -1), ([310] * 150 + [0, 309], 5, 33, -1),
+                                               ([310, 33, 0, 2001] * 40, 4, 9, -1)],
+                         ids=["long", "one", "units to CTAs", "units to teams", "ragged"])
+def test_decode_long_lines_of_large_groups(lens, Hkv, G, window, D, dtype):
+    """Lines long enough (in most of the cases) for two warps to share a ring, on every way to deal them out."""
+    c, table, ln, k, v, q, z, att = _decode_case(lens, G, Hkv, D, 1, 64, dtype, seed=G, sinks=G % 2 == 0)
+    att.window_left = window
+    o = att.forward(q, table, ln, z).clone()
+    lse = att.lse.clone()
+    assert att.read_status() == 0 and not att._ws[:12 * 1024].any()
+    _check_decode(c, lens, k, v, q, z, att, o, lse, only=range(0, len(lens), 1 + len(lens) // 7))
+    for _ in range(3):
+        assert torch.equal(att.forward(q, table, ln, z), o) and torch.equal(att.lse, lse)
+
+
 @pytest.mark.parametrize("dtype", [BF, F8], ids=["bf16", "e4m3"])
 def test_decode_one_long_sequence(dtype):
     """Split over all SMs and joined; every head of one rank against fp64 on the device."""

@@ -742,7 +742,7 @@ int usp_cache_read(const usp_paged_cache* cache, void* k, void* v, int tokens, c
 }
 
 size_t usp_attn_decode_workspace_bytes(const usp_paged_cache* cache, int Hq) {
-  return check_decode(cache, Hq) != USP_OK ? 0 : attn_decode_ws_bytes(*cache);
+  return check_decode(cache, Hq) != USP_OK ? 0 : attn_decode_ws_bytes(*cache, Hq);
 }
 
 int usp_attn_decode(const usp_paged_cache* cache, int Hq, int window_left, float softmax_scale, const float* sinks,
@@ -754,7 +754,7 @@ int usp_attn_decode(const usp_paged_cache* cache, int Hq, int window_left, float
   if (!(softmax_scale >= 0.f) || isinf(softmax_scale)) return USP_ERR_INVALID_ARG;
   if (any_null(q, o) || lse == nullptr) return USP_ERR_INVALID_ARG;
   if (!all_aligned16(q, o) || !aligned4(lse) || !aligned4(sinks)) return USP_ERR_ALIGNMENT;
-  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < attn_decode_ws_bytes(*cache))
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < attn_decode_ws_bytes(*cache, Hq))
     return USP_ERR_WORKSPACE;
   // what is written lies on nothing else
   const uint64_t rows = static_cast<uint64_t>(cache->n_seqs) * Hq, n = 2 * rows * cache->D;

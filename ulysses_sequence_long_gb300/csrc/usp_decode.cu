@@ -12,7 +12,8 @@
 // without waiting for the others.  A unit that lies in one warp is finished there.  Of one that several share
 // each leaves a partial result (O, maximum, sum in fp32): the CTA puts its warps' together once,
 // when all are done, and what crosses CTAs goes through the workspace.  Parts are joined in the order of the
-// positions.
+// positions.  A warp has 8 query heads.  Where a group has more and the line is long, two warps make a team: they go through
+// the same tiles, which one ring of twice the size holds, each for 8 heads, so that tiles are read once for 16 of them.
 //
 // Loads.  The products are arranged so that the positions are the rows of the matrix
 // instruction and the query heads its 8 columns (S^T = K q^T, O^T = V^T P^T): rows of 16 query heads would be
@@ -41,6 +42,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "usp_internal.h"
 #include "usp_paged.cuh"
@@ -59,7 +61,12 @@ constexpr int kFan = 48;            // parts that a CTA puts together at once
 // 200: tiles 8.4, units to the CTAs 5.8, to the warps 11.5; 16 of 1000: 12.7, 10.1; 200 of up to 500, D 64, e4m3: 22.9,
 // units to the CTAs 23.4, to the warps 26.8.)
 constexpr int kWarpsTiles = 3, kCtasTiles = 8;
-constexpr int kHeads = 8;           // query heads of a unit (more of them in a group: more units)
+constexpr int kHeads = 8;           // query heads of a warp
+// Groups of more than 8 query heads: teams of two warps where each team of the grid would have this many tiles, else a unit
+// for each 8 heads.  (us, as teams and as units of 8, D 128: 32 sequences of 8000, 8 groups of 16 heads, bf16 173, 305, e4m3
+// 119, 165; of 2000, bf16 55, 85; of 1000, 26 tiles a team: 29.7, 29.5; one of 32768, 4 groups, 14 tiles: 28.5, 20.5; of
+// 131072, 54 tiles: 59, 82; e4m3, 36 tiles: 51, 49.  Teams of four for 32 heads a group were slower than two of two.)
+constexpr int kTeamTiles = 32;
 constexpr int kMaxCtas = 1024, kTicketBytes = kMaxCtas * 12;
 // A column's reference may stay this far (log2) below a weight; e4m3: weights go into f16 kUp higher (2^15 at most), and
 // a token's value exponent counts from kLeast up in the reference.
@@ -86,17 +93,24 @@ struct Cfg {
   static_assert(kRing >= kKept && kSmem >= kFan * (kKept + kHeads * 8), "partial Os fit into shared memory that is done with");
 };
 
+// The units of a sequence: P * hk * chunks, chunks of the G query heads of a group.
+struct Units {
+  int chunks, all;
+  FastDiv by_all, by_chunks;
+};
+
 struct Args {
   paged::Pool pool;
-  int n_seqs, P, hq, G, chunks, units;  // chunks of 8 heads in a group of G; units = P * hk * chunks per sequence
+  int n_seqs, P, hq, G;
+  Units one, team;                      // with chunks of a warp's heads, of a team's
   int window;                           // -1: none
   float scale;                          // softmax scale
-  FastDiv by_units, by_chunks, by_hk;
+  FastDiv by_hk;
   const float* sinks;
   const uint16_t* q;
   uint16_t* o;
   float* lse;
-  float* parts;                         // [2 * ctas][kHeads][D] then [2 * ctas][kHeads][2]
+  float* parts;                         // [2 * ctas][team's warps][kHeads][D], then [2 * ctas][team's warps][kHeads][2]
   float* stats;
   int32_t* tickets;                     // [ctas][3], zero between calls
   int32_t* status;
@@ -186,15 +200,15 @@ __device__ __noinline__ void write_empty(const Args& a, int first, int step) {
   }
 }
 
-// A warp's part of a unit that it shares with others.
+// A warp's part of a unit that its team shares with others.
 struct Part {
-  int unit;           // sequence * units + unit, -1: none
+  int unit;           // (sequence * units + unit) * the team's warps + which of them, -1: none
   int begins, ends;   // the unit begins, ends in it
   int tiles;          // of the whole unit
   uint32_t stop;      // where the unit ends on the line
 };
 
-// The query heads of a unit: row of the first among [P][n_seqs][hq], how many, its sink.
+// The query heads of a warp in a unit: row of the first among [P][n_seqs][hq], how many (none: <= 0), its sink.
 struct Heads {
   int64_t row;
   int n, sink;
@@ -219,67 +233,88 @@ struct Finish {
   }
 };
 
-// How the work is dealt out: the line's tiles to the warps, whole units to the CTAs, whose warps share them, or to the
-// warps.
-enum class Split { kTiles, kUnitsToCtas, kUnitsToWarps };
+// How the work is dealt out: the line's tiles to the teams, whole units to the CTAs, whose teams share them, or to the
+// teams.
+enum class Split { kTiles, kUnitsToCtas, kUnitsToTeams };
 
 // A stretch's place with the unit's parts spelt out.
 struct Place : Cursor {
-  int r, j, chunk;  // rank, its key/value head, chunk of 8 query heads
-  __device__ __forceinline__ void split(const Args& a) {
-    const int rj = a.by_chunks.div(u);
-    chunk = u - rj * a.chunks;
+  int r, j, chunk;  // rank, its key/value head, chunk of a team's query heads
+  __device__ __forceinline__ void split(const Args& a, const Units& un) {
+    const int rj = un.by_chunks.div(u);
+    chunk = u - rj * un.chunks;
     r = a.by_hk.div(rj);
     j = rj - r * a.pool.hk;
   }
-  __device__ __forceinline__ void next_unit(const Args& a, bool& bad) {
-    Cursor::next_unit(a.pool, a.window, a.units, bad);
-    split(a);
+  __device__ __forceinline__ void next_unit(const Args& a, const Units& un, bool& bad) {
+    Cursor::next_unit(a.pool, a.window, un.all, bad);
+    split(a, un);
   }
 };
 
-// A warp's stretch: `count` tiles from `at` of the line, `count` whole units, or its share of the CTA's `count` units; it
+// The barrier of a team of T warps.
+template <int T>
+__device__ __forceinline__ void team_sync(int team) {
+  if constexpr (T == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * T) : "memory");
+}
+
+// (Whatever the lengths have become since, each of a team's warps comes to its barrier once a tile and once behind the
+// last one, of as many tiles as its first warp found: what decides on that has been read once, in the CTA or the team.)
+//
+// A team's stretch: `count` tiles from `at` of the line, `count` whole units, or its share of the CTA's `count` units; it
 // (for a share, they) begins start.y tiles, or units, into sequence start.x.
-template <int D, bool kE4m3>
+template <int D, bool kE4m3, int T>
 __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, Part* parts, float2 (*stats)[kHeads],
-                                            int2 start, Split split, uint32_t at, int count) {
+                                            volatile uint32_t* shared, int2 start, Split split, uint32_t at,
+                                            int count) {
   using C = Cfg<D, kE4m3>;
   constexpr int MT = D / 16, KS = D / 16, QV = D / 32;  // QV: 16-byte pieces of a query head that a thread has
+  const Units& un = T > 1 ? a.team : a.one;
+  constexpr int kTeams = C::kWarps / T, kSlots = T * C::kStages;  // (of the CTA; tiles that the team's ring holds)
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, qd = lane & 3;
+  const int team = w / T, mem = w % T;
   float* kept = reinterpret_cast<float*>(smem + C::kWarps * C::kRing + w * C::kKept);
   bool bad = false;  // (reported when the lengths were added up)
   Place cur;
   if (split != Split::kTiles) {
     cur.sequence(a.pool, a.window, start.x, bad);
-    cur.u = min(start.y, a.units - 1);
+    cur.u = static_cast<int>(min(static_cast<uint32_t>(start.y), static_cast<uint32_t>(un.all - 1)));
     Cursor c = cur;
     uint32_t tiles = 0;
     const int units = count;
     for (int i = 0; i < units; ++i) {
       tiles += c.tiles();
-      c.next_unit(a.pool, a.window, a.units, bad);
+      c.next_unit(a.pool, a.window, un.all, bad);
+    }
+    if constexpr (T > 1) {
+      if (mem == 0 && lane == 0) *shared = tiles;
+      team_sync<T>(team);
+      tiles = *shared;
     }
     count = tiles;
     if (split == Split::kUnitsToCtas) {
-      const Deal own(tiles, C::kWarps);
-      at = own.begin(w);
-      count = own.begin(w + 1) - at;
+      const Deal own(tiles, kTeams);
+      at = own.begin(team);
+      count = own.begin(team + 1) - at;
       if (count == 0) return;
       int skip = at;
       for (int i = 1; i < units && skip >= cur.tiles(); ++i) {
         skip -= cur.tiles();
-        cur.Cursor::next_unit(a.pool, a.window, a.units, bad);
+        cur.Cursor::next_unit(a.pool, a.window, un.all, bad);
       }
       cur.tile = cur.first + skip;
     }
   } else {
-    cur.seek(a.pool, a.window, a.units, start.x, start.y, bad);
+    cur.seek(a.pool, a.window, un.all, start.x, start.y, bad);
   }
-  cur.split(a);
-  bool begins = cur.tile == cur.first;  // the unit at hand begins in this warp
+  cur.split(a, un);
+  bool begins = cur.tile == cur.first;  // the unit at hand begins in this team
 
-  // ---- loads, kStages - 1 tiles ahead
-  const uint32_t ring = smem_u32(smem) + w * C::kRing;
+  // ---- loads, kSlots - 1 tiles ahead
+  const uint32_t ring = smem_u32(smem) + team * T * C::kRing;
   Place ld = cur;
   int left = count;                     // tiles not asked for yet
   uint32_t slot = 0;                    // where the next one goes in the ring
@@ -289,7 +324,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
   int page, off;                        // the page at hand (looked up a tile ahead), where in it the next tile begins
   bool new_page = true, ok = false;     // it has not been entered yet; it is one of the pool's
   int full, full_end;                   // tiles of which every position is visible
-  const unsigned char *kp, *vp;         // the lane's first pieces of the next tile
+  const unsigned char *kp, *vp;         // the lane's first pieces of the next tile (in a team kp: keys' or values')
   const uint8_t* sp;                    // its scales, keys' in lane 0, values' in lane 1
   auto enter_unit = [&]() {
     const int t0 = ld.tile * kTile;
@@ -311,6 +346,9 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
   const int vput = (lane ^ (R == 256 ? 0 : R == 128 ? lane >> 4 << 1 : (lane >> 3 & 1) << 1)) * 16;
   const int kget = g * R + qd * 16 + (R == 64 ? 0 : (g & 1) * 64);
   const int vget = 2 * qd * R + (R == 64 ? ((g >> 1) ^ ((qd & 1) << 1)) * 16 + (g & 1) * 8 : (g ^ (2 * qd)) * 16);
+  // In a team one warp copies the keys, the other the values.
+  const bool values = mem != 0;
+  const int put = values ? 16 * R + vput : kput, turned = values ? -1 : 0;
   auto load = [&]() {
     if (left > 0) {
       if (new_page) {
@@ -318,13 +356,25 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
         ok = page >= 0 && page < a.pool.n_pages;
         if (!ok) set_status(a.status, USP_ERR_BAD_PAGES);
         const int64_t row = unit_row + (ok ? page : 0) * page_rows + off;
-        kp = static_cast<const unsigned char*>(a.pool.k) + row * R + lane * 16;
-        vp = static_cast<const unsigned char*>(a.pool.v) + row * R + lane * 16;
+        kp = static_cast<const unsigned char*>(values ? a.pool.v : a.pool.k) + row * R + lane * 16;
+        if constexpr (T == 1) vp = static_cast<const unsigned char*>(a.pool.v) + row * R + lane * 16;
         if constexpr (kE4m3) sp = (lane == 0 ? a.pool.k_scales : a.pool.v_scales) + row;
       }
       const uint32_t kdst = ring + slot + kput, vdst = ring + slot + 16 * R + vput;
       const auto vturn = [](int i) { return R == 256 ? (i & 3) << 5 : R == 128 ? (i & 1) << 6 : 0; };
-      if (ok && ld.tile >= full && ld.tile < full_end) {
+      if constexpr (T > 1) {
+        const uint32_t dst = ring + slot + put;
+        if (ok && ld.tile >= full && ld.tile < full_end) {
+#pragma unroll
+          for (int i = 0; i < C::kCopies; ++i) cp_async((dst ^ (vturn(i) & turned)) + i * 512, kp + i * 512);
+        } else {
+#pragma unroll
+          for (int i = 0; i < C::kCopies; ++i) {
+            const int t = ld.tile * kTile + (i * 512 + lane * 16) / R;
+            cp_async_or_zero((dst ^ (vturn(i) & turned)) + i * 512, kp + i * 512, ok && t < ld.len && t >= ld.lo);
+          }
+        }
+      } else if (ok && ld.tile >= full && ld.tile < full_end) {
 #pragma unroll
         for (int i = 0; i < C::kCopies; ++i) cp_async(kdst + i * 512, kp + i * 512);
 #pragma unroll
@@ -339,15 +389,15 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
         }
       }
       if constexpr (kE4m3) {
-        if (lane < 2) cp_async(ring + slot + 32 * R + 16 * lane, sp);
+        if (lane < 2 && mem == 0) cp_async(ring + slot + 32 * R + 16 * lane, sp);
         sp += kTile;
       }
       kp += kTile * R;
-      vp += kTile * R;
+      if constexpr (T == 1) vp += kTile * R;
       off += kTile;
       if (--left > 0) {
         if (++ld.tile >= ld.end) {
-          ld.next_unit(a, bad);
+          ld.next_unit(a, un, bad);
           enter_unit();
         } else if (off == a.pool.page_size) {
           off = 0;
@@ -356,18 +406,18 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
         }
       }
     }
-    slot = slot == (C::kStages - 1) * C::kStage ? 0 : slot + C::kStage;
+    slot = slot == (kSlots - 1) * C::kStage ? 0 : slot + C::kStage;
     cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) load();
+#pragma unroll(T == 1 ? C::kStages - 1 : 1)
+  for (int i = 0; i < kSlots - 1; ++i) load();
 
   // ---- the tiles, unit by unit
   uint4 qx[QV];                        // the thread's pieces of its query head, of the unit that comes
   auto fetch_q = [&]() {
-    const int64_t head0 = (static_cast<int64_t>(cur.r) * a.n_seqs + cur.b) * a.hq + cur.j * a.G + cur.chunk * kHeads;
-    const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (head0 + g) * D);
-    const bool have = cur.chunk * kHeads + g < a.G;
+    const Heads hd(a, cur.b, cur.r, cur.j, cur.chunk * T + mem);
+    const uint4* qrow = reinterpret_cast<const uint4*>(a.q + (hd.row + g) * D);
+    const bool have = g < hd.n;
 #pragma unroll
     for (int p = 0; p < QV; ++p) {
       // the elements d that meet the thread's pieces of K
@@ -417,11 +467,11 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
     const int tiles = min(count, cur.left());
     int t0 = cur.tile * kTile;
     for (int it = 0; it < tiles; ++it, t0 += kTile) {
-      cp_async_wait<C::kStages - 2>();
-      __syncwarp();  // every lane's copies are here, and its reads of the place that is filled next are done
+      cp_async_wait<kSlots - 2>();
+      team_sync<T>(team);  // every lane's copies are here, and its reads of the place that is filled next are done
       load();
       const uint32_t src = ring + read;
-      read = read == (C::kStages - 1) * C::kStage ? 0 : read + C::kStage;
+      read = read == (kSlots - 1) * C::kStage ? 0 : read + C::kStage;
       // S^T: rows g and g + 8 are positions, columns 2 qd and 2 qd + 1 query heads
       constexpr bool kTwo = C::kWarps <= 8;  // two chains of products where few warps hide one's latency
       float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
@@ -561,16 +611,17 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
       }
     }
 
-    // ---- the unit, or its part in this warp, ends
+    // ---- the unit, or its part in this team, ends
     const bool ends = cur.tile + tiles >= cur.end, own = begins;
-    const int unit = cur.b * a.units + cur.u;
-    const Heads hd(a, cur.b, cur.r, cur.j, cur.chunk);
+    const int unit = (cur.b * un.all + cur.u) * T + mem;
+    const Heads hd(a, cur.b, cur.r, cur.j, cur.chunk * T + mem);
     const int unit_tiles = cur.tiles();
     const uint32_t stop = at + cur.left();  // where the unit ends on the line
     count -= tiles;
     at += tiles;
+    if (T > 1 && count == 0) team_sync<T>(team);
     if (count > 0) {  // the next unit's query is on its way meanwhile
-      cur.next_unit(a, bad);
+      cur.next_unit(a, un, bad);
       begins = true;
       fetch_q();
     }
@@ -598,7 +649,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
       }
     } else {
       // [head][d] in shared memory: of a unit that began earlier in the place kept for it, of one that goes on in the
-      // warp's ring, whose last tile has been read
+      // warp's part of the ring, whose last tile has been read
       __syncwarp();
       const int k = 2 * w + own;
       float* to = own ? reinterpret_cast<float*>(smem + w * C::kRing) : kept;
@@ -613,7 +664,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
         }
         if (g == 0) stats[k][2 * qd + c] = make_float2(m[c], l[c]);
       }
-      if (lane == 0) parts[k] = Part{unit, own, ends, unit_tiles, stop};
+      if (lane == 0 && hd.n > 0) parts[k] = Part{unit, own, ends, unit_tiles, stop};
     }
     if (count == 0) break;
   }
@@ -644,12 +695,12 @@ struct Partial {
   }
 };
 
-template <int D>
-__device__ __forceinline__ void write_out(const Args& a, int unit, int h, const Partial<D>& p) {
+template <int D, int TM>
+__device__ __forceinline__ void write_out(const Args& a, const Units& un, bool teams, int unit, int h, const Partial<D>& p) {
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, b = a.by_units.div(unit), u = unit - b * a.units, rj = a.by_chunks.div(u);
-  const int r = a.by_hk.div(rj);
-  const Heads hd(a, b, r, rj - r * a.pool.hk, u - rj * a.chunks);
+  const int lane = threadIdx.x & 31, bu = teams ? unit / TM : unit, b = un.by_all.div(bu), u = bu - b * un.all;
+  const int rj = un.by_chunks.div(u), r = a.by_hk.div(rj), chunk = u - rj * un.chunks;
+  const Heads hd(a, b, r, rj - r * a.pool.hk, teams ? chunk * TM + unit % TM : chunk);
   if (h >= hd.n) return;
   const Finish f(a, hd, h, p.M, p.L);
   uint32_t* to = reinterpret_cast<uint32_t*>(a.o + (hd.row + h) * D) + lane * (E / 2);
@@ -670,7 +721,7 @@ __device__ __forceinline__ int take(int32_t* ticket) {
 
 // A CTA's part of a unit that crosses CTAs: it is part i of the n in CTAs first .. first + n - 1.
 struct Crossing {
-  int unit, first, n, i;  // unit -1: none
+  int unit, first, n, i;  // unit: as a Part's of the team's first warp, -1: none
 };
 
 // Part x of a unit that begins in CTA `first`: its place in the workspace.  A CTA has two: the first for a unit that began
@@ -678,10 +729,10 @@ struct Crossing {
 __device__ __forceinline__ int64_t place_of(int first, int x) { return 2 * (first + x) + (x == 0); }
 
 template <int D>
-__device__ __forceinline__ void leave(const Args& a, int first, int x, int h, const Partial<D>& p) {
+__device__ __forceinline__ void leave(const Args& a, int T, int first, int x, int mem, int h, const Partial<D>& p) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
-  const int64_t row = place_of(first, x) * kHeads + h;
+  const int64_t row = (place_of(first, x) * T + mem) * kHeads + h;
   float* to = a.parts + row * D + lane * E;
   if constexpr (E == 4)
     __stcg(reinterpret_cast<float4*>(to), make_float4(p.o[0], p.o[1], p.o[2], p.o[3]));
@@ -694,12 +745,12 @@ __device__ __forceinline__ void leave(const Args& a, int first, int x, int h, co
 // kFan parts in a row the last CTA puts them together, and of these sums again the last one.  The
 // order of the additions goes by the positions, whoever is last.  (All of this runs once: it is kept
 // short, for its instructions come from L2.)
-template <int D, bool kE4m3>
-__device__ __forceinline__ void join(const Args& a, unsigned char* smem, const Crossing* crossing) {
+template <int D, bool kE4m3, int TM>
+__device__ __forceinline__ void join(const Args& a, const Units& un, bool teams, unsigned char* smem, const Crossing* crossing) {
   using C = Cfg<D, kE4m3>;
   __shared__ int last[2];
   float2* stats = reinterpret_cast<float2*>(smem + kFan * C::kKept);  // [part][head], behind the parts
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, T = teams ? TM : 1;
   __syncthreads();  // the CTA's parts are written
   if (tid < 2) {
     int is_last = 0;
@@ -719,29 +770,33 @@ __device__ __forceinline__ void join(const Args& a, unsigned char* smem, const C
     const int n = crossing[c].n, first = crossing[c].first, groups = (n + kFan - 1) / kFan;
     int x0 = crossing[c].i / kFan * kFan, step = 1, parts = min(n - x0, kFan);
     while (last[c]) {
-      // parts x0, x0 + step, ... into shared memory, past L1 (other CTAs wrote them)
-      constexpr int kPieces = kHeads * D / 4;
-      for (int i = tid; i < parts * kPieces; i += C::kThreads) {
-        const int p = i / kPieces;
-        cp_async(smem_u32(smem) + i * 16, a.parts + (place_of(first, x0 + p * step) * kPieces + (i - p * kPieces)) * 4);
-      }
-      cp_async_commit();
-      for (int i = tid; i < parts * kHeads; i += C::kThreads)
-        stats[i] =
-            __ldcg(reinterpret_cast<const float2*>(a.stats) + place_of(first, x0 + i / kHeads * step) * kHeads + i % kHeads);
-      cp_async_wait<0>();
-      __syncthreads();
       const bool done = step > 1 || groups == 1;
-      if (w < kHeads) {
-        Partial<D> sum;
-        for (int p = 0; p < parts; ++p)
-          sum.add(stats[p * kHeads + w], reinterpret_cast<const float*>(smem) + (p * kHeads + w) * D + lane * (D / 32));
-        if (done)
-          write_out<D>(a, crossing[c].unit, w, sum);
-        else
-          leave<D>(a, first, x0, w, sum);
+#pragma unroll 1
+      for (int m = 0; m < T; ++m) {  // the team's warps
+        // parts x0, x0 + step, ... into shared memory, past L1 (other CTAs wrote them)
+        constexpr int kPieces = kHeads * D / 4;
+        for (int i = tid; i < parts * kPieces; i += C::kThreads) {
+          const int p = i / kPieces;
+          cp_async(smem_u32(smem) + i * 16,
+                   a.parts + ((place_of(first, x0 + p * step) * T + m) * kPieces + (i - p * kPieces)) * 4);
+        }
+        cp_async_commit();
+        for (int i = tid; i < parts * kHeads; i += C::kThreads)
+          stats[i] = __ldcg(reinterpret_cast<const float2*>(a.stats) +
+                            (place_of(first, x0 + i / kHeads * step) * T + m) * kHeads + i % kHeads);
+        cp_async_wait<0>();
+        __syncthreads();
+        if (w < kHeads) {
+          Partial<D> sum;
+          for (int p = 0; p < parts; ++p)
+            sum.add(stats[p * kHeads + w], reinterpret_cast<const float*>(smem) + (p * kHeads + w) * D + lane * (D / 32));
+          if (done)
+            write_out<D, TM>(a, un, teams, crossing[c].unit + m, w, sum);
+          else
+            leave<D>(a, T, first, x0, m, w, sum);
+        }
+        __syncthreads();
       }
-      __syncthreads();
       if (done) break;
       if (tid == 0) {
         int32_t* ticket = a.tickets + 3 * first + 2;
@@ -756,12 +811,14 @@ __device__ __forceinline__ void join(const Args& a, unsigned char* smem, const C
   }
 }
 
-template <int D, bool kE4m3>
+template <int D, bool kE4m3, int TM>
 __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args a) {
   using C = Cfg<D, kE4m3>;
   constexpr int kWarps = C::kWarps;
+  static_assert(TM <= 2 && kWarps % TM == 0, "one warp of a team copies the keys, the other the values");
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Part parts[2 * kWarps];
+  __shared__ uint32_t team_tiles[kWarps];
   __shared__ float2 stats[2 * kWarps][kHeads];  // reference, sum
   __shared__ Crossing crossing[2];              // of a unit that began in an earlier CTA, of one that begins here
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, cta = blockIdx.x;
@@ -791,23 +848,36 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
       before_any += y;
     }
   }
-  const uint32_t all = __shfl_sync(0xffffffffu, before, 31), any = __shfl_sync(0xffffffffu, before_any, 31);
+  uint32_t all = __shfl_sync(0xffffffffu, before, 31), any = __shfl_sync(0xffffffffu, before_any, 31);
   most = __reduce_max_sync(0xffffffffu, most);
-  const uint64_t tiles = static_cast<uint64_t>(all) * a.units;
-  if (__any_sync(0xffffffffu, mine > kMost) || tiles >= (1ull << 31)) {
+  bool over = __any_sync(0xffffffffu, mine > kMost);
+  if constexpr (TM > 1) {  // warps that wait for each other go by one reading of the lengths
+    __shared__ uint4 line_of;
+    if (tid == 0) line_of = make_uint4(all, any, most, over);
+    __syncthreads();
+    all = line_of.x, any = line_of.y, most = line_of.z, over = line_of.w;
+  }
+  const bool teams =
+      TM > 1 && static_cast<uint64_t>(all) * a.team.all >= static_cast<uint64_t>(kTeamTiles) * gridDim.x * (kWarps / TM);
+  const Units& un = teams ? a.team : a.one;
+  const int T = teams ? TM : 1;
+  const uint32_t n_teams = teams ? kWarps / TM : kWarps;  // of a CTA
+  const uint64_t tiles = static_cast<uint64_t>(all) * un.all;
+  if (over || tiles >= (1ull << 31)) {
     set_status(a.status, USP_ERR_UNSUPPORTED);
     return;
   }
-  // The longest share of a warp, in tiles: of whole units dealt out to the warps (nothing is to be joined then), to
+  // The longest share of a team, in tiles: of whole units dealt out to the teams (nothing is to be joined then), to
   // the CTAs (nothing across them), of tiles.
-  const uint32_t W = static_cast<uint32_t>(tiles), U = any * a.units, warps = gridDim.x * kWarps, even = (W + warps - 1) / warps;
-  const uint64_t to_warp = static_cast<uint64_t>((U + warps - 1) / warps) * most;
-  const uint64_t to_cta = (static_cast<uint64_t>((U + gridDim.x - 1) / gridDim.x) * most + kWarps - 1) / kWarps;
-  const Split split = to_warp <= min(to_cta + kWarpsTiles, static_cast<uint64_t>(even) + kCtasTiles) ? Split::kUnitsToWarps
+  const uint32_t W = static_cast<uint32_t>(tiles), U = any * un.all, grid_teams = gridDim.x * n_teams;
+  const uint32_t even = (W + grid_teams - 1) / grid_teams;
+  const uint64_t to_team = static_cast<uint64_t>((U + grid_teams - 1) / grid_teams) * most;
+  const uint64_t to_cta = (static_cast<uint64_t>((U + gridDim.x - 1) / gridDim.x) * most + n_teams - 1) / n_teams;
+  const Split split = to_team <= min(to_cta + kWarpsTiles, static_cast<uint64_t>(even) + kCtasTiles) ? Split::kUnitsToTeams
                       : to_cta + kWarpsTiles <= even + kCtasTiles                                     ? Split::kUnitsToCtas
                                                                                                       : Split::kTiles;
   const bool by_unit = split != Split::kTiles;
-  const uint32_t things = by_unit ? U : W, takers = split == Split::kUnitsToCtas ? 1 : kWarps;  // of a CTA
+  const uint32_t things = by_unit ? U : W, takers = split == Split::kUnitsToCtas ? 1 : n_teams;  // of a CTA
   const uint32_t n_ctas = min(gridDim.x, (things + takers - 1) / takers);
   // sequences that see nothing have no tile: CTAs without work write their outputs, or all when they are done
   if (cta >= n_ctas) {
@@ -815,30 +885,38 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
     return;
   }
   const Deal line(things, n_ctas * takers);
-  const uint32_t taker = cta * takers + (takers > 1 ? w : 0);
+  const uint32_t taker = cta * takers + (takers > 1 ? (teams ? w / TM : w) : 0);
   const uint32_t at = line.begin(taker), count = line.begin(taker + 1) - at;
   if (count > 0) {
-    const uint32_t hi = (by_unit ? before_any : before) * a.units, lo = hi - (by_unit ? mine_any : mine) * a.units;
+    const uint32_t hi = (by_unit ? before_any : before) * un.all, lo = hi - (by_unit ? mine_any : mine) * un.all;
     const bool here = at >= lo && at < hi;
     int s = s0;
     uint32_t rest = at - lo;
     while (here && s + 1 < s1) {
-      const uint32_t n = tiles_of(a, s, bad), things_of = (by_unit ? n > 0 : n) * a.units;
+      const uint32_t n = tiles_of(a, s, bad), things_of = (by_unit ? n > 0 : n) * un.all;
       if (rest < things_of) break;
       rest -= things_of;
       ++s;
     }
     const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-    const int2 start = make_int2(__shfl_sync(0xffffffffu, s, from), __shfl_sync(0xffffffffu, rest, from));
-    run_stretch<D, kE4m3>(a, smem, parts, stats, start, split, at, count);
+    const int2 start = make_int2(min(__shfl_sync(0xffffffffu, s, from & 31), a.n_seqs - 1),
+                                 __shfl_sync(0xffffffffu, rest, from & 31));
+    if (teams)
+      run_stretch<D, kE4m3, TM>(a, smem, parts, stats, team_tiles + w / TM, start, split, at, count);
+    else
+      run_stretch<D, kE4m3, 1>(a, smem, parts, stats, nullptr, start, split, at, count);
   }
-  if (any < a.n_seqs && n_ctas == gridDim.x) write_empty<D>(a, cta * kWarps + w, warps);
-  if (split == Split::kUnitsToWarps) return;
+  if (any < a.n_seqs && n_ctas == gridDim.x) write_empty<D>(a, cta * kWarps + w, gridDim.x * kWarps);
+  if (split == Split::kUnitsToTeams) return;
 
-  // ---- the warps' parts, in order: those of one unit next to each other
+  // ---- the warps' parts, in order: those of one unit next to each other, a team's first warps' before its second ones'
   __syncthreads();
-  // part k of lane k: which there are, and which begin another unit than the one before
-  const int unit_k = lane < 2 * kWarps ? parts[lane].unit : -1;
+  const auto part_of = [&](int i) {
+    constexpr int n = kWarps / TM;
+    return teams ? 2 * ((i >> 1) % n * TM + i / (2 * n)) + (i & 1) : i;
+  };
+  // a lane's part: which there are, and which begin another unit than the one before
+  const int unit_k = lane < 2 * kWarps ? parts[part_of(lane)].unit : -1;
   const uint32_t there = __ballot_sync(0xffffffffu, unit_k >= 0), below = there & ((1u << lane) - 1);
   const int unit_before = __shfl_sync(0xffffffffu, unit_k, below ? 31 - __clz(below) : 0);
   uint32_t starters = __ballot_sync(0xffffffffu, unit_k >= 0 && (below == 0 || unit_before != unit_k));
@@ -848,11 +926,11 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
     starters &= starters - 1;
     uint32_t members = there & ~((1u << i) - 1) & (starters ? (starters & -starters) - 1 : 0xffffffffu);
     if (h >= kHeads) continue;
-    const int unit = parts[i].unit;
+    const int unit = parts[part_of(i)].unit;
     Partial<D> sum;
-    int last = i;
+    int last = part_of(i);
     for (; members != 0; members &= members - 1) {
-      last = __ffs(members) - 1;
+      last = part_of(__ffs(members) - 1);
       sum.add(stats[last][h],
               reinterpret_cast<const float*>(smem + (last & 1 ? last / 2 * C::kRing : kWarps * C::kRing + last / 2 * C::kKept)) +
                   h * D + lane * (D / 32));
@@ -861,25 +939,26 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) sum.o[e] *= kDown;
     }
-    const bool begins = parts[i].begins;
+    const bool begins = parts[part_of(i)].begins;
     if (begins && parts[last].ends) {
-      write_out<D>(a, unit, h, sum);
+      write_out<D, TM>(a, un, teams, unit, h, sum);
     } else {
       const uint32_t stop = parts[last].stop;
       // (n_ctas and the bounds hold whatever the lengths have become meanwhile)
-      const uint32_t me = cta, first_of = line.owner(stop - parts[last].tiles) / kWarps, last_of = line.owner(stop - 1) / kWarps;
+      const uint32_t me = cta, first_of = line.owner(stop - parts[last].tiles) / n_teams, last_of = line.owner(stop - 1) / n_teams;
       const int first = begins ? cta : static_cast<int>(min(first_of, me));
       const int end = static_cast<int>(min(max(last_of, me), n_ctas - 1)) + 1;
-      leave<D>(a, first, cta - first, h, sum);
-      if (h == 0 && lane == 0) crossing[begins] = Crossing{unit, first, end - first, cta - first};
+      const int mem = teams ? unit % TM : 0;
+      leave<D>(a, T, first, cta - first, mem, h, sum);
+      if (h == 0 && lane == 0 && mem == 0) crossing[begins] = Crossing{unit, first, end - first, cta - first};
     }
   }
-  if (split == Split::kTiles) join<D, kE4m3>(a, smem, crossing);
+  if (split == Split::kTiles) join<D, kE4m3, TM>(a, un, teams, smem, crossing);
 }
 
-template <int D, bool kE4m3>
+template <int D, bool kE4m3, int TM>
 int launch(const Args& a, int ctas, cudaStream_t st) {
-  auto* kern = decode_kernel<D, kE4m3>;
+  auto* kern = decode_kernel<D, kE4m3, TM>;
   constexpr int smem = Cfg<D, kE4m3>::kSmem;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
     cudaGetLastError();
@@ -888,13 +967,24 @@ int launch(const Args& a, int ctas, cudaStream_t st) {
   return launch_chained(kern, dim3(ctas), Cfg<D, kE4m3>::kThreads, smem, 1, st, a);
 }
 
+template <int D, bool kE4m3>
+int launch_team(const Args& a, int warps, int ctas, cudaStream_t st) {
+  return warps == 1 ? launch<D, kE4m3, 1>(a, ctas, st) : launch<D, kE4m3, 2>(a, ctas, st);
+}
+
 int grid_of() { return std::min(kMaxCtas, device_sm_count()); }
+
+// Warps of a team, 8 query heads each.
+int team_of(const usp_paged_cache& c, int Hq) {
+  const int G = Hq / std::max(c.P, c.Hkv);
+  return G <= kHeads ? 1 : 2;
+}
 
 }  // namespace decode
 
 // Tickets (of kMaxCtas, so that they lie at the same place for every cache), then parts, then statistics.
-size_t attn_decode_ws_bytes(const usp_paged_cache& c) {
-  const size_t ctas = decode::grid_of(), rows = 2 * ctas * decode::kHeads;
+size_t attn_decode_ws_bytes(const usp_paged_cache& c, int Hq) {
+  const size_t ctas = decode::grid_of(), rows = 2 * ctas * decode::team_of(c, Hq) * decode::kHeads;
   return decode::kTicketBytes + rows * c.D * 4 + rows * 8;
 }
 
@@ -906,10 +996,13 @@ int launch_attn_decode(const usp_paged_cache& c, int Hq, int window_left, float 
   a.P = c.P;
   a.hq = Hq / c.P;
   a.G = a.hq / a.pool.hk;
-  a.chunks = (a.G + decode::kHeads - 1) / decode::kHeads;
-  a.units = c.P * a.pool.hk * a.chunks;
-  a.by_units = FastDiv(static_cast<uint32_t>(a.units));
-  a.by_chunks = FastDiv(static_cast<uint32_t>(a.chunks));
+  const int team = decode::team_of(c, Hq);
+  for (auto [un, heads] : {std::pair(&a.one, decode::kHeads), std::pair(&a.team, team * decode::kHeads)}) {
+    un->chunks = (a.G + heads - 1) / heads;
+    un->all = c.P * a.pool.hk * un->chunks;
+    un->by_all = FastDiv(static_cast<uint32_t>(un->all));
+    un->by_chunks = FastDiv(static_cast<uint32_t>(un->chunks));
+  }
   a.by_hk = FastDiv(static_cast<uint32_t>(a.pool.hk));
   a.window = window_left;
   a.scale = scale;
@@ -919,13 +1012,13 @@ int launch_attn_decode(const usp_paged_cache& c, int Hq, int window_left, float 
   a.lse = lse;
   a.status = status;
   const int ctas = decode::grid_of();
-  const size_t rows = 2 * static_cast<size_t>(ctas) * decode::kHeads;
+  const size_t rows = 2 * static_cast<size_t>(ctas) * team * decode::kHeads;
   a.tickets = static_cast<int32_t*>(ws);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + decode::kTicketBytes);
   a.stats = a.parts + rows * c.D;
   const bool e = c.dtype == USP_CACHE_E4M3;
-  if (c.D == 64) return e ? decode::launch<64, true>(a, ctas, st) : decode::launch<64, false>(a, ctas, st);
-  return e ? decode::launch<128, true>(a, ctas, st) : decode::launch<128, false>(a, ctas, st);
+  if (c.D == 64) return e ? decode::launch_team<64, true>(a, team, ctas, st) : decode::launch_team<64, false>(a, team, ctas, st);
+  return e ? decode::launch_team<128, true>(a, team, ctas, st) : decode::launch_team<128, false>(a, team, ctas, st);
 }
 
 }  // namespace usp

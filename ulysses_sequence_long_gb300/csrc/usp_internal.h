@@ -124,7 +124,7 @@ int launch_rope(const usp_rope_params& p, const void* q, const void* k, void* q_
                 int32_t* status, cudaStream_t st);
 int launch_cache_move(const usp_paged_cache& c, void* k, void* v, int tokens, const int32_t* cu, bool append,
                       int32_t* status, cudaStream_t st);
-size_t attn_decode_ws_bytes(const usp_paged_cache& c);
+size_t attn_decode_ws_bytes(const usp_paged_cache& c, int Hq);
 int launch_attn_decode(const usp_paged_cache& c, int Hq, int window_left, float scale, const float* sinks,
                        const void* q, void* o, float* lse, void* ws, int32_t* status, cudaStream_t st);
 
