@@ -581,8 +581,8 @@ int usp_cache_read(const usp_paged_cache* cache, void* k, void* v, int tokens, c
  * ws: usp_attn_decode_workspace_bytes bytes, 256-byte aligned, all zero before its first call; a call leaves zero
  * what has to be.  It belongs to one call at a time (calls that may overlap need one each).
  * dev_status: USP_ERR_BAD_PAGES (the sequence's outputs are then unspecified; nothing outside the pool is read);
- * USP_ERR_UNSUPPORTED (2^31 pieces of all sequences, ranks and key/value heads, or 2^30 positions in one of
- * every 32 sequences: no output is written).
+ * USP_ERR_UNSUPPORTED (2^31 pieces of all sequences, ranks, key/value heads and, of a head's group, 8 or 16 query
+ * heads each; or 2^30 positions in one of every 32 sequences: no output is written).
  * Errors: USP_ERR_INVALID_ARG, USP_ERR_INDIVISIBLE, USP_ERR_UNSUPPORTED (as the cache; window_left < -1, Hq > 1024),
  * USP_ERR_ALIGNMENT, USP_ERR_WORKSPACE, USP_ERR_CUDA. */
 size_t usp_attn_decode_workspace_bytes(const usp_paged_cache* cache, int Hq);
