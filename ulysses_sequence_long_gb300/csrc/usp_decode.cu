@@ -463,7 +463,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
     float l[2] = {0.f, 0.f}, acc[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    bool none = true;  // no visible position yet
+    bool none = true;  // a column has no weight yet (every score so far hidden or -inf): its reference is to be set
     const int tiles = min(count, cur.left());
     int t0 = cur.tile * kTile;
     for (int it = 0; it < tiles; ++it, t0 += kTile) {
@@ -523,7 +523,6 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
       bool above = none || fmaxf(fmax3(y[0], y[1], y[2]), y[3]) > kAbove + (kE4m3 ? kUp : 0.f);
       if constexpr (kE4m3) above |= fmaxf(fmax3(x[0], x[1], x[2]), x[3]) > kAbove - kLeast;
       if (__any_sync(0xffffffffu, above)) {
-        none = false;
         float z[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = s[i] * f[i];
@@ -549,6 +548,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
             y[2 * i + c] = x[2 * i + c] + ve[i];
           }
         }
+        none = m[0] == -INFINITY || m[1] == -INFINITY;
       }
       float p[4];
 #pragma unroll
