@@ -318,7 +318,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
   Place ld = cur;
   int left = count;                     // tiles not asked for yet
   uint32_t slot = 0;                    // where the next one goes in the ring
-  const int64_t page_rows = static_cast<int64_t>(a.pool.hk) * a.pool.page_size;
+  const int64_t page_rows = a.pool.page_rows();
   const int32_t* table;                 // the entry of the page at hand
   int64_t unit_row;                     // the unit's first row in a page 0
   int page, off;                        // the page at hand (looked up a tile ahead), where in it the next tile begins
@@ -332,7 +332,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
     table = a.pool.table + static_cast<int64_t>(ld.b) * a.pool.max_pages + col;
     page = gld(table);
     off = min(t0 - static_cast<int>(col) * a.pool.page_size, a.pool.page_size - kTile);
-    unit_row = static_cast<int64_t>(ld.r) * a.pool.n_pages * page_rows + ld.j * a.pool.page_size;
+    unit_row = a.pool.unit_row(ld.r, ld.j);
     full = (ld.lo + kTile - 1) / kTile;
     full_end = ld.len / kTile;
     new_page = true;

@@ -53,6 +53,11 @@ struct Pool {
     return ((static_cast<int64_t>(r) * n_pages + page) * hk + j) * page_size +
            (pos - static_cast<int>(col) * page_size);
   }
+  // Row of position 0 of a rank's head j in page 0, and rows from a page to the next (a head's rows of a page may be 2^30).
+  USP_HD int64_t unit_row(int r, int j) const {
+    return static_cast<int64_t>(r) * n_pages * page_rows() + static_cast<int64_t>(j) * page_size;
+  }
+  USP_HD int64_t page_rows() const { return static_cast<int64_t>(hk) * page_size; }
   // Sequence and position of token i of `tokens` appended ones; false if it has no place.  cu: their boundaries
   // [n_seqs + 1] (whatever they hold, nothing else is read), or nullptr: token i is sequence i's last.
   USP_HD bool place(const int32_t* cu, int i, int& seq, int& pos, bool& bad) const {
