@@ -29,6 +29,10 @@
 // score + value exponent (log2), so that the weights of the products, 2^(s + e - M + 7), stay within f16: below
 // 2^15, and whole down to 2^-21 of the largest (less than 2^-31 of it is lost).  q is scaled by a power of two into
 // f16's range.  The reference moves only when a weight would pass 2^8: no reduction over the warp in most tiles.
+// The same reference would flush the sum of the weights 2^(s - M) where values are near the largest bf16, and the
+// products' weights where they are near the smallest: a unit whose sum shows that goes through the warp once more, its
+// references near the scores' maximum and those of the products' weights kept beside them.  (That look at the sums costs
+// groups of 16 heads 1.7%; finding such values on the way, in one pass for all, 4 to 8%.)
 // bf16: the weights are rounded to bf16 in two parts (high and the rest), 16 bits of them in all: one part alone would
 // make the output's error 1.4 times that of its own rounding.
 //
@@ -42,6 +46,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 #include <utility>
 
 #include "usp_internal.h"
@@ -68,9 +73,14 @@ constexpr int kHeads = 8;           // query heads of a warp
 // 131072, 54 tiles: 59, 82; e4m3, 36 tiles: 51, 49.  Teams of four for 32 heads a group were slower than two of two.)
 constexpr int kTeamTiles = 32;
 constexpr int kMaxCtas = 1024, kTicketBytes = kMaxCtas * 12;
-// A column's reference may stay this far (log2) below a weight; e4m3: weights go into f16 kUp higher (2^15 at most), and
-// a token's value exponent counts from kLeast up in the reference.
+// A column's reference may stay this far (log2) below a weight; e4m3: weights of the products go into f16 kUp higher
+// (2^15 at most), and a token's value exponent counts from kLeast up in the reference.
 constexpr float kAbove = 8.f, kUp = 7.f, kDown = 0x1p-7f, kLeast = -60.f;
+// e4m3: a sum of weights within these has its reference at most 2^44 below the scores' maximum (kLeast has had no effect)
+// and 2^30 a position above it, so that nothing that counts is flushed here or beside other parts (values from about
+// 2^-20 to 2^30 are within them, however many); scores up to kHuge have roundings that are small beside an exponent.
+// Else the unit goes once more, its references within kFar of the maximum.
+constexpr float kSumLeast = 0x1p-30f, kSumMost = 0x1p44f, kHuge = 0x1p22f, kFar = 20.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D, bool kE4m3>
@@ -89,8 +99,11 @@ struct Cfg {
   static constexpr int kStages = kRow == 64 ? 4 : 3;
   static constexpr int kRing = kStages * kStage;
   static constexpr int kKept = kHeads * D * 4;                   // a partial O of a warp
-  static constexpr int kSmem = kWarps * (kRing + kKept);
-  static_assert(kRing >= kKept && kSmem >= kFan * (kKept + kHeads * 8), "partial Os fit into shared memory that is done with");
+  // Of a partial result: reference and sum of its weights; e4m3: how far above that reference the values' one is, too.
+  using Stat = std::conditional_t<kE4m3, float4, float2>;
+  static constexpr int kRings = kWarps * (kRing + kKept), kJoin = kFan * (kKept + kHeads * static_cast<int>(sizeof(Stat)));
+  static constexpr int kSmem = kRings > kJoin ? kRings : kJoin;  // (the join takes shared memory that is done with)
+  static_assert(kRing >= kKept, "a partial O fits into a ring that is done with");
 };
 
 // The units of a sequence: P * hk * chunks, chunks of the G query heads of a group.
@@ -110,8 +123,8 @@ struct Args {
   const uint16_t* q;
   uint16_t* o;
   float* lse;
-  float* parts;                         // [2 * ctas][team's warps][kHeads][D], then [2 * ctas][team's warps][kHeads][2]
-  float* stats;
+  float* parts;                         // [2 * ctas][team's warps][kHeads][D], then [2 * ctas][team's warps][kHeads] Stats
+  void* stats;
   int32_t* tickets;                     // [ctas][3], zero between calls
   int32_t* status;
 };
@@ -220,17 +233,22 @@ struct Heads {
   }
 };
 
-// From a head's reference (log2; -inf: no weight) and sum: what its weighted values are multiplied by, and its LSE.
+// From a head's reference M (log2; -inf: no weight), how far V the values' one is above it (e4m3) and the sum: its LSE,
+// and what makes outputs of its weighted values, x half scale (e4m3: 2^(M + V) in two halves, either of which is in
+// fp32's range) or x scale.
+template <bool kE4m3>
 struct Finish {
-  float scale, lse;
-  __device__ __forceinline__ Finish(const Args& a, const Heads& hd, int h, float M, float sum) {
+  float half, scale, lse;
+  __device__ __forceinline__ Finish(const Args& a, const Heads& hd, int h, float M, float V, float sum) {
     // the sink joins the sum once, with no value
     const float z = a.sinks != nullptr ? gld(a.sinks + hd.sink + h) * kLog2e : -INFINITY, top = fmaxf(M, z);
     const float ref = top == -INFINITY ? 0.f : top, f = ex2(M - ref);
     sum = sum * f + ex2(z - ref);
-    scale = sum > 0.f ? f / sum : sum;  // (0 stays 0, NaN NaN)
+    half = kE4m3 ? ex2(0.5f * (M - ref + V)) : 1.f;
+    scale = sum > 0.f ? (kE4m3 ? half : f) / sum : sum;  // (0 stays 0, NaN NaN)
     lse = (ref + log2f(sum)) * kLn2;
   }
+  __device__ __forceinline__ float operator()(float x) const { return (kE4m3 ? x * half : x) * scale; }
 };
 
 // How the work is dealt out: the line's tiles to the teams, whole units to the CTAs, whose teams share them, or to the
@@ -252,6 +270,35 @@ struct Place : Cursor {
   }
 };
 
+// The largest value of a column (in the lanes of the same place in their four).
+__device__ __forceinline__ float column_max(float v) {
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+
+// The reference of a column whose value exponents are far from 0 moves: to m, within kFar of the scores' maximum, with
+// the products' weights raised beside it; (log2) drop is what their earlier ones have less.  kept: the scores' maximum and
+// the raise; was, m: the reference so far (-inf: none), and at least; z, e: the lane's scores and their values' exponents.
+struct Moved {
+  float m, drop, raise;
+};
+__device__ __noinline__ Moved far_reference(float4* kept, float was, float m, float z0, float z1, float e0,
+                                            float e1) {
+  const bool first = was == -INFINITY;
+  const float raised = first ? 0.f : kept->y;
+  const float most = fmaxf(first ? -INFINITY : kept->x, column_max(fmaxf(z0, z1)));
+  m = fminf(fmaxf(m, most - kFar), most + kFar);
+  const float ref = m == -INFINITY ? 0.f : m;
+  // above the reference, that of the values: near 0 unless the one is at an end or scores are huge
+  float over = column_max(fmaxf(z0 - ref + e0, z1 - ref + e1));
+  if (!first) over = fmaxf(over, was - m - raised);
+  const float raise = fabsf(over) > 1.f && over != -INFINITY ? -over : 0.f;
+  __syncwarp();
+  if ((threadIdx.x & 31) < 4) *kept = make_float4(most, raise, 0.f, 0.f);
+  return Moved{m, was - m - raised + raise, raise};
+}
+
 // The barrier of a team of T warps.
 template <int T>
 __device__ __forceinline__ void team_sync(int team) {
@@ -261,13 +308,28 @@ __device__ __forceinline__ void team_sync(int team) {
     asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * T) : "memory");
 }
 
+// Whether p holds in one of a team's lanes; a barrier.
+template <int T>
+__device__ __forceinline__ bool team_any(int team, bool p) {
+  if constexpr (T == 1) return __any_sync(0xffffffffu, p);
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(1 + team), "n"(32 * T), "r"(static_cast<int>(p))
+      : "memory");
+  return any != 0;
+}
+
 // (Whatever the lengths have become since, each of a team's warps comes to its barrier once a tile and once behind the
-// last one, of as many tiles as its first warp found: what decides on that has been read once, in the CTA or the team.)
+// last one, e4m3 at each end of a unit too, of as many tiles as its first warp found: what decides on that has been read
+// once, in the CTA or the team.)
 //
 // A team's stretch: `count` tiles from `at` of the line, `count` whole units, or its share of the CTA's `count` units; it
 // (for a share, they) begins start.y tiles, or units, into sequence start.x.
 template <int D, bool kE4m3, int T>
-__device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, Part* parts, float2 (*stats)[kHeads],
+__device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, Part* parts,
+                                            typename Cfg<D, kE4m3>::Stat (*stats)[kHeads],
                                             volatile uint32_t* shared, int2 start, Split split, uint32_t at,
                                             int count) {
   using C = Cfg<D, kE4m3>;
@@ -290,9 +352,9 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
       c.next_unit(a.pool, a.window, un.all, bad);
     }
     if constexpr (T > 1) {
-      if (mem == 0 && lane == 0) *shared = tiles;
+      if (mem == 0 && lane == 0) shared[0] = tiles;
       team_sync<T>(team);
-      tiles = *shared;
+      tiles = shared[0];
     }
     count = tiles;
     if (split == Split::kUnitsToCtas) {
@@ -427,6 +489,7 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
   };
   fetch_q();
   uint32_t read = 0;
+  bool far = false;  // e4m3: the unit goes through once more, with references for value exponents far from 0
   while (true) {
     uint32_t qf[KS][2];
     float qs[2];  // log2(e) scale q's power of two, of the thread's two columns
@@ -463,8 +526,15 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
     float l[2] = {0.f, 0.f}, acc[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    bool none = true;  // a column has no weight yet (every score so far hidden or -inf): its reference is to be set
-    const int tiles = min(count, cur.left());
+    // a column has no weight yet (every score so far hidden or -inf): its reference is to be set; or far
+    bool none = true;
+    const int kept_at = 2 * w + begins;
+    int tiles = min(count, cur.left());
+    if constexpr (T > 1 && kE4m3) {
+      if (mem == 0 && lane == 0) shared[1] = tiles;
+      team_sync<T>(team);
+      tiles = shared[1];
+    }
     int t0 = cur.tile * kTile;
     for (int it = 0; it < tiles; ++it, t0 += kTile) {
       cp_async_wait<kSlots - 2>();
@@ -527,28 +597,37 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = s[i] * f[i];
         if (edge) hide(z);
+        float raise[2] = {0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float top = kE4m3 ? fmaxf(z[c] + fmaxf(ve[0] - kUp, kLeast), z[2 + c] + fmaxf(ve[1] - kUp, kLeast)) : fmaxf(z[c], z[2 + c]);
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          const float mn = fmaxf(m[c], top);
-          const float by = m[c] == -INFINITY ? 0.f : ex2(m[c] - mn);
+          const bool first = m[c] == -INFINITY;  // (what there is has no weight)
+          const float top = kE4m3 ? fmaxf(z[c] + fmaxf(ve[0] - kUp, kLeast), z[2 + c] + fmaxf(ve[1] - kUp, kLeast)) : fmaxf(z[c], z[2 + c]);
+          float mn = fmaxf(m[c], column_max(top)), drop = m[c] - mn;  // (log2) what the values' sum is lowered by
+          if constexpr (kE4m3) {
+            if (__builtin_expect(far, 0)) {
+              const Moved to = far_reference(&stats[kept_at][2 * qd + c], m[c], mn, z[c], z[2 + c], ve[0] - kUp, ve[1] - kUp);
+              mn = to.m;
+              drop = to.drop;
+              raise[c] = to.raise;
+            }
+          }
+          const float by = first ? 0.f : ex2(drop);
+          l[c] *= first ? 0.f : ex2(m[c] - mn);
           m[c] = mn;
           ref[c] = mn == -INFINITY ? 0.f : mn;
-          l[c] *= by;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            x[2 * i + c] = z[2 * i + c] - ref[c];
+            y[2 * i + c] = x[2 * i + c] + ve[i];
+            if (kE4m3) y[2 * i + c] += raise[c];
+          }
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             acc[i][c] *= by;
             acc[i][2 + c] *= by;
           }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            x[2 * i + c] = z[2 * i + c] - ref[c];
-            y[2 * i + c] = x[2 * i + c] + ve[i];
-          }
         }
-        none = m[0] == -INFINITY || m[1] == -INFINITY;
+        none = far || m[0] == -INFINITY || m[1] == -INFINITY;
       }
       float p[4];
 #pragma unroll
@@ -611,6 +690,34 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
       }
     }
 
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
+    float over[2] = {0.f, 0.f};  // how far the values' references are above the columns'
+    if constexpr (kE4m3) {
+      const auto lost = [&](int c) {
+        return m[c] > -INFINITY && (l[c] < kSumLeast || l[c] > kSumMost || fabsf(m[c]) > kHuge);
+      };
+      if (__builtin_expect(far, 0)) {
+        __syncwarp();
+        over[0] = -stats[kept_at][2 * qd].y;
+        over[1] = -stats[kept_at][2 * qd + 1].y;
+        far = false;
+      } else if (__builtin_expect(team_any<T>(team, lost(0) || lost(1)), 0)) {
+        cp_async_wait<0>();
+        team_sync<T>(team);
+        ld = cur;
+        left = count;
+        slot = read;
+        enter_unit();
+#pragma unroll 1
+        for (int i = 0; i < kSlots - 1; ++i) load();
+        far = true;
+        continue;
+      }
+    }
+
     // ---- the unit, or its part in this team, ends
     const bool ends = cur.tile + tiles >= cur.end, own = begins;
     const int unit = (cur.b * un.all + cur.u) * T + mem;
@@ -625,25 +732,21 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
       begins = true;
       fetch_q();
     }
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
     // a thread has the elements d .. d + 7 of two heads, d = first_column(x, g)
     if (own && ends) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int h = 2 * qd + c;
         if (h < hd.n) {
-          const Finish f(a, hd, h, m[c], l[c]);
-          const float by = f.scale * (kE4m3 ? kDown : 1.f);
+          Finish<kE4m3> f(a, hd, h, m[c], over[c], l[c]);
+          if constexpr (kE4m3) f.scale *= kDown;
 #pragma unroll
           for (int x = 0; x < D / 64; ++x)
             *reinterpret_cast<uint4*>(a.o + (hd.row + h) * D + first_column<D, kE4m3>(x, g)) =
-                make_uint4(pack_bf16x2(acc[4 * x][c] * by, acc[4 * x][2 + c] * by),
-                           pack_bf16x2(acc[4 * x + 1][c] * by, acc[4 * x + 1][2 + c] * by),
-                           pack_bf16x2(acc[4 * x + 2][c] * by, acc[4 * x + 2][2 + c] * by),
-                           pack_bf16x2(acc[4 * x + 3][c] * by, acc[4 * x + 3][2 + c] * by));
+                make_uint4(pack_bf16x2(f(acc[4 * x][c]), f(acc[4 * x][2 + c])),
+                           pack_bf16x2(f(acc[4 * x + 1][c]), f(acc[4 * x + 1][2 + c])),
+                           pack_bf16x2(f(acc[4 * x + 2][c]), f(acc[4 * x + 2][2 + c])),
+                           pack_bf16x2(f(acc[4 * x + 3][c]), f(acc[4 * x + 3][2 + c])));
           if (g == 0) a.lse[hd.row + h] = f.lse;
         }
       }
@@ -662,7 +765,12 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
           reinterpret_cast<float4*>(at8)[1] =
               make_float4(acc[4 * x + 2][c], acc[4 * x + 2][2 + c], acc[4 * x + 3][c], acc[4 * x + 3][2 + c]);
         }
-        if (g == 0) stats[k][2 * qd + c] = make_float2(m[c], l[c]);
+        if (g == 0) {
+          if constexpr (kE4m3)
+            stats[k][2 * qd + c] = make_float4(m[c], l[c], over[c], 0.f);
+          else
+            stats[k][2 * qd + c] = make_float2(m[c], l[c]);
+        }
       }
       if (lane == 0 && hd.n > 0) parts[k] = Part{unit, own, ends, unit_tiles, stop};
     }
@@ -670,19 +778,34 @@ __device__ __forceinline__ void run_stretch(const Args& a, unsigned char* smem, 
   }
 }
 
-// A head's partial result in a warp: reference and sum, and D/32 elements of each lane.
-template <int D>
+// A head's partial result in a warp: reference and sum, how far the values' reference is above it (e4m3), and D/32
+// elements of each lane.
+template <int D, bool kE4m3>
 struct Partial {
   static constexpr int E = D / 32;
-  float M = -INFINITY, L = 0.f, o[E] = {};
-  __device__ __forceinline__ void add(float2 ml, const float* from) {
-    const float top = fmaxf(M, ml.x), ref = top == -INFINITY ? 0.f : top, f = ex2(M - ref), by = ex2(ml.x - ref);
+  using Stat = typename Cfg<D, kE4m3>::Stat;
+  float M = -INFINITY, L = 0.f, V = 0.f, o[E] = {};
+  __device__ __forceinline__ void add(Stat st, const float* from) {
+    const float top = fmaxf(M, st.x), ref = top == -INFINITY ? 0.f : top;
+    float f = ex2(M - ref), by = ex2(st.x - ref);
+    L = L * f + st.y * by;
+    if constexpr (kE4m3) {
+      const float mine = M - ref + V, its = st.x - ref + st.z, over = fmaxf(mine, its);
+      V = over == -INFINITY ? 0.f : over;
+      f = ex2(mine - V);
+      by = ex2(its - V);
+    }
     M = top;
-    L = L * f + ml.y * by;
     float y[E];
     load(from, y);
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = o[e] * f + y[e] * by;
+  }
+  __device__ __forceinline__ Stat stat() const {
+    if constexpr (kE4m3)
+      return make_float4(M, L, V, 0.f);
+    else
+      return make_float2(M, L);
   }
   static __device__ __forceinline__ void load(const float* from, float (&y)[E]) {
     if constexpr (E == 4) {
@@ -695,20 +818,20 @@ struct Partial {
   }
 };
 
-template <int D, int TM>
-__device__ __forceinline__ void write_out(const Args& a, const Units& un, bool teams, int unit, int h, const Partial<D>& p) {
+template <int D, bool kE4m3, int TM>
+__device__ __forceinline__ void write_out(const Args& a, const Units& un, bool teams, int unit, int h,
+                                          const Partial<D, kE4m3>& p) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, bu = teams ? unit / TM : unit, b = un.by_all.div(bu), u = bu - b * un.all;
   const int rj = un.by_chunks.div(u), r = a.by_hk.div(rj), chunk = u - rj * un.chunks;
   const Heads hd(a, b, r, rj - r * a.pool.hk, teams ? chunk * TM + unit % TM : chunk);
   if (h >= hd.n) return;
-  const Finish f(a, hd, h, p.M, p.L);
+  const Finish<kE4m3> f(a, hd, h, p.M, p.V, p.L);
   uint32_t* to = reinterpret_cast<uint32_t*>(a.o + (hd.row + h) * D) + lane * (E / 2);
   if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(p.o[0] * f.scale, p.o[1] * f.scale),
-                                               pack_bf16x2(p.o[2] * f.scale, p.o[3] * f.scale));
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(f(p.o[0]), f(p.o[1])), pack_bf16x2(f(p.o[2]), f(p.o[3])));
   else
-    *to = pack_bf16x2(p.o[0] * f.scale, p.o[1] * f.scale);
+    *to = pack_bf16x2(f(p.o[0]), f(p.o[1]));
   if (lane == 0) a.lse[hd.row + h] = f.lse;
 }
 
@@ -728,8 +851,8 @@ struct Crossing {
 // in an earlier CTA, the second for one that begins in it.
 __device__ __forceinline__ int64_t place_of(int first, int x) { return 2 * (first + x) + (x == 0); }
 
-template <int D>
-__device__ __forceinline__ void leave(const Args& a, int T, int first, int x, int mem, int h, const Partial<D>& p) {
+template <int D, bool kE4m3>
+__device__ __forceinline__ void leave(const Args& a, int T, int first, int x, int mem, int h, const Partial<D, kE4m3>& p) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int64_t row = (place_of(first, x) * T + mem) * kHeads + h;
@@ -738,7 +861,7 @@ __device__ __forceinline__ void leave(const Args& a, int T, int first, int x, in
     __stcg(reinterpret_cast<float4*>(to), make_float4(p.o[0], p.o[1], p.o[2], p.o[3]));
   else
     __stcg(reinterpret_cast<float2*>(to), make_float2(p.o[0], p.o[1]));
-  if (lane == 0) __stcg(reinterpret_cast<float2*>(a.stats) + row, make_float2(p.M, p.L));
+  if (lane == 0) __stcg(static_cast<typename Cfg<D, kE4m3>::Stat*>(a.stats) + row, p.stat());
 }
 
 // The units that cross CTAs, in the CTAs that come last: every CTA leaves its part in the workspace and takes a ticket; of
@@ -749,7 +872,8 @@ template <int D, bool kE4m3, int TM>
 __device__ __forceinline__ void join(const Args& a, const Units& un, bool teams, unsigned char* smem, const Crossing* crossing) {
   using C = Cfg<D, kE4m3>;
   __shared__ int last[2];
-  float2* stats = reinterpret_cast<float2*>(smem + kFan * C::kKept);  // [part][head], behind the parts
+  using Stat = typename C::Stat;
+  Stat* stats = reinterpret_cast<Stat*>(smem + kFan * C::kKept);  // [part][head], behind the parts
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, T = teams ? TM : 1;
   __syncthreads();  // the CTA's parts are written
   if (tid < 2) {
@@ -782,18 +906,18 @@ __device__ __forceinline__ void join(const Args& a, const Units& un, bool teams,
         }
         cp_async_commit();
         for (int i = tid; i < parts * kHeads; i += C::kThreads)
-          stats[i] = __ldcg(reinterpret_cast<const float2*>(a.stats) +
+          stats[i] = __ldcg(static_cast<const Stat*>(a.stats) +
                             (place_of(first, x0 + i / kHeads * step) * T + m) * kHeads + i % kHeads);
         cp_async_wait<0>();
         __syncthreads();
         if (w < kHeads) {
-          Partial<D> sum;
+          Partial<D, kE4m3> sum;
           for (int p = 0; p < parts; ++p)
             sum.add(stats[p * kHeads + w], reinterpret_cast<const float*>(smem) + (p * kHeads + w) * D + lane * (D / 32));
           if (done)
-            write_out<D, TM>(a, un, teams, crossing[c].unit + m, w, sum);
+            write_out<D, kE4m3, TM>(a, un, teams, crossing[c].unit + m, w, sum);
           else
-            leave<D>(a, T, first, x0, m, w, sum);
+            leave<D, kE4m3>(a, T, first, x0, m, w, sum);
         }
         __syncthreads();
       }
@@ -818,8 +942,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
   static_assert(TM <= 2 && kWarps % TM == 0, "one warp of a team copies the keys, the other the values");
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Part parts[2 * kWarps];
-  __shared__ uint32_t team_tiles[kWarps];
-  __shared__ float2 stats[2 * kWarps][kHeads];  // reference, sum
+  __shared__ uint32_t team_tiles[kWarps / TM][2];  // what a team goes by: of its units, of the one at hand
+  __shared__ typename C::Stat stats[2 * kWarps][kHeads];
   __shared__ Crossing crossing[2];              // of a unit that began in an earlier CTA, of one that begins here
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   if (lane < 2) parts[2 * w + lane].unit = -1;
@@ -902,7 +1026,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
     const int2 start = make_int2(min(__shfl_sync(0xffffffffu, s, from & 31), a.n_seqs - 1),
                                  __shfl_sync(0xffffffffu, rest, from & 31));
     if (teams)
-      run_stretch<D, kE4m3, TM>(a, smem, parts, stats, team_tiles + w / TM, start, split, at, count);
+      run_stretch<D, kE4m3, TM>(a, smem, parts, stats, team_tiles[w / TM], start, split, at, count);
     else
       run_stretch<D, kE4m3, 1>(a, smem, parts, stats, nullptr, start, split, at, count);
   }
@@ -927,7 +1051,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
     uint32_t members = there & ~((1u << i) - 1) & (starters ? (starters & -starters) - 1 : 0xffffffffu);
     if (h >= kHeads) continue;
     const int unit = parts[part_of(i)].unit;
-    Partial<D> sum;
+    Partial<D, kE4m3> sum;
     int last = part_of(i);
     for (; members != 0; members &= members - 1) {
       last = part_of(__ffs(members) - 1);
@@ -941,7 +1065,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
     }
     const bool begins = parts[part_of(i)].begins;
     if (begins && parts[last].ends) {
-      write_out<D, TM>(a, un, teams, unit, h, sum);
+      write_out<D, kE4m3, TM>(a, un, teams, unit, h, sum);
     } else {
       const uint32_t stop = parts[last].stop;
       // (n_ctas and the bounds hold whatever the lengths have become meanwhile)
@@ -949,7 +1073,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1) decode_kernel(Args
       const int first = begins ? cta : static_cast<int>(min(first_of, me));
       const int end = static_cast<int>(min(max(last_of, me), n_ctas - 1)) + 1;
       const int mem = teams ? unit % TM : 0;
-      leave<D>(a, T, first, cta - first, mem, h, sum);
+      leave<D, kE4m3>(a, T, first, cta - first, mem, h, sum);
       if (h == 0 && lane == 0 && mem == 0) crossing[begins] = Crossing{unit, first, end - first, cta - first};
     }
   }
@@ -985,7 +1109,7 @@ int team_of(const usp_paged_cache& c, int Hq) {
 // Tickets (of kMaxCtas, so that they lie at the same place for every cache), then parts, then statistics.
 size_t attn_decode_ws_bytes(const usp_paged_cache& c, int Hq) {
   const size_t ctas = decode::grid_of(), rows = 2 * ctas * decode::team_of(c, Hq) * decode::kHeads;
-  return decode::kTicketBytes + rows * c.D * 4 + rows * 8;
+  return decode::kTicketBytes + rows * c.D * 4 + rows * (c.dtype == USP_CACHE_E4M3 ? sizeof(float4) : sizeof(float2));
 }
 
 int launch_attn_decode(const usp_paged_cache& c, int Hq, int window_left, float scale, const float* sinks,
