@@ -36,6 +36,7 @@ import torch
 import torch.distributed as dist
 
 from . import binding as B_
+from .pipeline import layer_positions
 
 
 @dataclass
@@ -214,10 +215,10 @@ class UlyssesRankAttention:
     def forward(self, q_local, k_local, v_local, pos_local, sinks=None, rope_positions=None):
         """q/k/v ``[B][S/P][H][D]`` and position_ids ``[B][S/P]`` of this rank's
         chunk (sinks: the global ``[Hq]`` logits) -> O ``[B][S/P][Hq][D]``.
-        ``rope_positions``: ``[n_axes][B][S/P]`` for ``rope`` (default: the position ids)."""
+        ``rope_positions``: ``[n_axes][B][S/P]`` for ``rope`` (default, for one axis: the position ids)."""
         s = self.s
-        self._rope_positions = pos_local if rope_positions is None else rope_positions
         if self.rope is not None:
+            self._rope_positions = layer_positions(self.rope, rope_positions, pos_local, s.B * s.Sl)
             q_local, k_local = self.rope.forward(q_local, k_local, self._rope_positions)
         self.ops.boundaries(all_gather(pos_local, self.group))
         q_h = self._to_head(q_local, s.Hq)

@@ -206,6 +206,19 @@ class Rotary:
         return int(self.status.item())
 
 
+def layer_positions(rope, given, ids, tokens: int):
+    """The positions by which a layer turns its `tokens` tokens: `given`, or the position ids of a ``rope`` of one axis.  A
+    layer takes one for each of its tokens and axes (``Rotary`` itself repeats those of a divisor of the tokens: fewer
+    would be taken for another axis' or another rank's)."""
+    if given is None:
+        if ids is None or rope.n_axes != 1:
+            raise ValueError(f"a layer whose rope has {rope.n_axes} axes needs its tokens' positions")
+        given = ids
+    if given.numel() != rope.n_axes * tokens:
+        raise ValueError(f"positions must be [{rope.n_axes}] axes of {tokens} tokens, got {tuple(given.shape)}")
+    return given
+
+
 class _Turned:
     """A layer's rotary positions: buffers for the turned shards, and the positions of the forward for the backward."""
 
@@ -222,8 +235,6 @@ class _Turned:
     def _check_turned(self, v_seq, pos_shards, sinks):
         """A forward that is refused leaves the turned shards, which the backward reads: what else it takes is looked at
         before they are written."""
-        if self.rope is None:
-            return
         B_._sized(v_seq, "v", torch.bfloat16, self.k_rot.numel(), self.k_rot)
         B_._sized(pos_shards, "position ids", torch.int32, self.shape.B * self.shape.S, self.k_rot)
         if sinks is not None:
@@ -233,6 +244,7 @@ class _Turned:
         """The layer's first step: q and k shards turned (as they are without ``rope``), for ``exchange_qkv``."""
         if self.rope is None:
             return q_seq, k_seq
+        layer_positions(self.rope, positions, None, self.shape.B * self.shape.S)
         self.rope.forward(q_seq, k_seq, positions, out=(self.q_rot, self.k_rot), stream=stream)
         self._rope_positions = positions
         return self.q_rot, self.k_rot
@@ -601,10 +613,11 @@ class UlyssesAttention(_Turned):
 
     def forward(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None, rope_positions=None):
         """Sequence shards in, sequence shards out (``self.o_seq``).  ``rope_positions``: int32
-        ``[n_axes][P][B][S/P]`` for the layer's ``rope`` (default: the position ids, one axis)."""
+        ``[n_axes][P][B][S/P]`` for the layer's ``rope`` (default, for one axis: the position ids)."""
         if self.rope is not None:
             self._check_turned(v_seq, pos_shards, sinks)
-            q_seq, k_seq = self.rotate(q_seq, k_seq, pos_shards if rope_positions is None else rope_positions, stream)
+            rope_positions = layer_positions(self.rope, rope_positions, pos_shards, self.shape.B * self.shape.S)
+            q_seq, k_seq = self.rotate(q_seq, k_seq, rope_positions, stream)
         if self._mods is not None:
             return self._on_device(self._mod_forward, q_seq, k_seq, v_seq, pos_shards, sinks, stream=stream)
         self.exchange_qkv(q_seq, k_seq, v_seq, stream)
@@ -800,11 +813,14 @@ class HybridAttention(_Turned):
     def forward_phases(self, q_seq, k_seq, v_seq, pos_shards, sinks=None, stream=None, marks=None,
                        rope_positions=None):
         """marks(i): 0 before (with ``rope``, after q and k are turned), 1 after the q/k/v exchange, 2 after the document
-        boundaries, 3 after the ring steps and merges, 4 after the O exchange."""
+        boundaries, 3 after the ring steps and merges, 4 after the O exchange.  ``rope_positions``: int32
+        ``[n_axes][P][B][S/P]`` for ``rope`` (default, for one axis: the position ids)."""
         s = self.shape
         mark = marks or (lambda i: None)
-        self._check_turned(v_seq, pos_shards, sinks)
-        q_seq, k_seq = self.rotate(q_seq, k_seq, pos_shards if rope_positions is None else rope_positions, stream)
+        if self.rope is not None:
+            self._check_turned(v_seq, pos_shards, sinks)
+            rope_positions = layer_positions(self.rope, rope_positions, pos_shards, s.B * s.S)
+            q_seq, k_seq = self.rotate(q_seq, k_seq, rope_positions, stream)
         mark(0)
         if self.fused:
             # q stays in its shards; k and v go to the hybrid head layout for the forward

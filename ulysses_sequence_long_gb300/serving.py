@@ -20,6 +20,7 @@ from typing import Optional
 import torch
 
 from . import binding as B_
+from .pipeline import layer_positions
 
 _BF, _F8, _I32, _F32, _U8 = torch.bfloat16, torch.float8_e4m3fn, torch.int32, torch.float32, torch.uint8
 
@@ -200,9 +201,8 @@ class DecodeAttention:
         """One token of each sequence through the layer: turn q and k (``rope``; positions int32
         ``[n_axes][sequences]``), append k and v, attend.  ``lens`` counts the new token."""
         if self.rope is not None:
-            if positions is None:
-                raise ValueError("a layer with rope needs the new tokens' positions")
             n = lens.shape[0]
+            layer_positions(self.rope, positions, None, n)
             self._out(n)  # (checks n)
             c = self.cache
             out = (self._turned[0][:n * self.Hq * c.D].view(c.P, n, self.hq, c.D),
