@@ -217,15 +217,23 @@ class UlyssesRankAttention:
         chunk (sinks: the global ``[Hq]`` logits) -> O ``[B][S/P][Hq][D]``.
         ``rope_positions``: ``[n_axes][B][S/P]`` for ``rope`` (default, for one axis: the position ids)."""
         s = self.s
+        # (a refused forward leaves the boundaries and what the backward reads)
+        for x, name, n in ((q_local, "q", s.Hq * s.D), (k_local, "k", s.Hkv * s.D), (v_local, "v", s.Hkv * s.D),
+                           (pos_local, "position ids", 1)):
+            if x.numel() != s.B * s.Sl * n:
+                raise ValueError(f"{name} must have {s.B * s.Sl * n} elements, got {tuple(x.shape)}")
+        if not q_local.dtype == k_local.dtype == v_local.dtype:
+            raise TypeError(f"q, k and v must have one type, got {q_local.dtype}, {k_local.dtype} and {v_local.dtype}")
         if self.rope is not None:
-            self._rope_positions = layer_positions(self.rope, rope_positions, pos_local, s.B * s.Sl)
-            q_local, k_local = self.rope.forward(q_local, k_local, self._rope_positions)
+            rope_positions = layer_positions(self.rope, rope_positions, pos_local, s.B * s.Sl)
+            q_local, k_local = self.rope.forward(q_local, k_local, rope_positions)
         self.ops.boundaries(all_gather(pos_local, self.group))
         q_h = self._to_head(q_local, s.Hq)
         k_h = self._to_head(k_local, s.Hkv)
         v_h = self._to_head(v_local, s.Hkv)
         o_h, lse = self.ops.attention_fwd(q_h, k_h, v_h, self._sinks_slice(sinks))
         self._saved = (q_h, k_h, v_h, o_h, lse)
+        self._rope_positions = rope_positions
         self.lse = lse
         return self._to_seq(o_h, s.Hq)
 
@@ -243,3 +251,6 @@ class UlyssesRankAttention:
             dq, dk = self.rope.backward(dq, dk, self._rope_positions, out=(dq, dk))
         dsinks = None if dz is None else all_gather(dz, self.group).reshape(-1)
         return dq, dk, dv, dsinks
+
+    def read_status(self) -> int:
+        return self.ops.read_status() or (0 if self.rope is None else self.rope.read_status())
