@@ -183,33 +183,63 @@ class DecodeAttention:
                                   self._lse[:n * self.Hq].view(c.P, n, self.hq))
         return v
 
+    def _query(self, q, sinks, n):
+        """The addresses of the queries and sinks."""
+        c = self.cache
+        return (_where(q, "q", _BF, n * self.Hq * c.D, c._index),
+                None if sinks is None else _where(sinks, "sinks", _F32, self.Hq, c._index))
+
+    def _attend(self, prm, q, sinks, o, lse, stream):
+        c = self.cache
+        B_.run_on(c._index, stream, self._decode, "usp_attn_decode", ctypes.byref(prm), self.Hq, self.window_left,
+                  self.softmax_scale, sinks, q, o.data_ptr(), lse.data_ptr(), self._ws.data_ptr(), self._ws_bytes, c._status)
+        self.lse = lse
+        return o
+
     def forward(self, q, block_table, lens, sinks=None, stream=None):
         """q bf16 ``[P][sequences][Hq/P][D]``, already turned -> O of the same shape (and ``self.lse``)."""
+        prm = self.cache._struct(block_table, lens)
+        o, lse = self._out(prm.n_seqs)
+        return self._attend(prm, *self._query(q, sinks, prm.n_seqs), o, lse, stream)
+
+    def _check_attend(self, prm, q, sinks, o, lse):
+        """What the library refuses of the attention, by addresses, before the step's tokens are in the pool."""
+        if q % 16 != 0:
+            raise B_.UspError(B_.USP_ERR_ALIGNMENT, "usp_attn_decode")
+        if self.window_left < -1:
+            raise B_.UspError(B_.USP_ERR_UNSUPPORTED, "usp_attn_decode")
+        n, D = prm.n_seqs, prm.D
+        o0, l0 = o.data_ptr(), lse.data_ptr()
+        o1, l1 = o0 + 2 * n * self.Hq * D, l0 + 4 * n * self.Hq
+        bad = not 0.0 <= self.softmax_scale < float("inf")
+        for at, size in ((q, o1 - o0), (sinks, 4 * self.Hq), (prm.block_table, 4 * n * prm.max_pages), (prm.lens, 4 * n)):
+            bad |= at is not None and (at < o1 and o0 < at + size or at < l1 and l0 < at + size)
+        if bad:
+            raise B_.UspError(B_.USP_ERR_INVALID_ARG, "usp_attn_decode")
+
+    def step(self, q, k, v, block_table, lens, sinks=None, positions=None, stream=None):
+        """One token of each sequence through the layer: turn q and k (``rope``; positions int32
+        ``[n_axes][sequences]``), append k and v (bf16 ``[P][sequences][heads of a rank][D]``), attend.  ``lens`` counts the
+        new token.  A step that is refused leaves the cache as it was."""
         c = self.cache
         index = c._index
         prm = c._struct(block_table, lens)
         n = prm.n_seqs
         o, lse = self._out(n)
-        B_.run_on(index, stream, self._decode, "usp_attn_decode", ctypes.byref(prm), self.Hq, self.window_left,
-                  self.softmax_scale, None if sinks is None else _where(sinks, "sinks", _F32, self.Hq, index),
-                  _where(q, "q", _BF, n * self.Hq * c.D, index), o.data_ptr(), lse.data_ptr(), self._ws.data_ptr(),
-                  self._ws_bytes, c._status)
-        self.lse = lse
-        return o
-
-    def step(self, q, k, v, block_table, lens, sinks=None, positions=None, stream=None):
-        """One token of each sequence through the layer: turn q and k (``rope``; positions int32
-        ``[n_axes][sequences]``), append k and v, attend.  ``lens`` counts the new token."""
-        if self.rope is not None:
-            n = lens.shape[0]
+        rows = n * c.P * c.hk * c.D
+        qp, sp = self._query(q, sinks, n)
+        kp, vp = _where(k, "k", _BF, rows, index), _where(v, "v", _BF, rows, index)
+        if self.rope is None:
+            self._check_attend(prm, qp, sp, o, lse)
+        else:
             layer_positions(self.rope, positions, None, n)
-            self._out(n)  # (checks n)
-            c = self.cache
             out = (self._turned[0][:n * self.Hq * c.D].view(c.P, n, self.hq, c.D),
-                   self._turned[1][:n * c.P * c.hk * c.D].view(c.P, n, c.hk, c.D))
-            q, k = self.rope.forward(q, k, positions, out=out, stream=stream)
-        self.cache.append(k, v, block_table, lens, stream=stream)
-        return self.forward(q, block_table, lens, sinks, stream)
+                   self._turned[1][:rows].view(c.P, n, c.hk, c.D))
+            qp, kp = out[0].data_ptr(), out[1].data_ptr()
+            self._check_attend(prm, qp, sp, o, lse)
+            self.rope.forward(q, k, positions, out=out, stream=stream)
+        B_.run_on(index, stream, c._append, "usp_cache_append", ctypes.byref(prm), kp, vp, n, None, c._status)
+        return self._attend(prm, qp, sp, o, lse, stream)
 
     def read_status(self) -> int:
         return self.cache.read_status() or (0 if self.rope is None else self.rope.read_status())
