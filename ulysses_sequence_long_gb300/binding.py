@@ -559,6 +559,14 @@ def memory_of(index: int, stream):
     return torch.cuda.stream(stream)
 
 
+def settle(index: int):
+    """Waits for what device `index`'s current stream has been given: tensors that an object has just made and filled are
+    ready for calls on any stream.  (Not within a capture: its calls follow in it.)"""
+    with torch.cuda.device(index):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+
+
 def call_on(device: torch.device, stream, where, *args):
     run_on(device.index, stream, getattr(load(), where), where, *args)
 

@@ -125,6 +125,7 @@ class Rotary:
         self._fwd, self._bwd = lib.usp_rope_fwd, lib.usp_rope_bwd
         self._n_pairs = freqs.numel()
         self._find()
+        B_.settle(self._index)
 
     def _find(self):
         """The addresses of the rotation's tensors, for the calls to come (which see when a tensor or its storage was

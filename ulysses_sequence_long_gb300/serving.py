@@ -65,6 +65,7 @@ class PagedCache:
         lib = B_.load()
         self._append, self._read = lib.usp_cache_append, lib.usp_cache_read
         self._find()
+        B_.settle(self._index)
 
     def _find(self):
         """The addresses of the pool's tensors, which have to be of their sizes and types, for the calls to come (which
@@ -172,6 +173,7 @@ class DecodeAttention:
         self._decode = B_.load().usp_attn_decode
         self._views = {}
         self.lse = None
+        B_.settle(cache._index)
 
     def _out(self, n):
         v = self._views.get(n)
