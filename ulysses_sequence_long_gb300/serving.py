@@ -185,24 +185,19 @@ class DecodeAttention:
                                   self._lse[:n * self.Hq].view(c.P, n, self.hq))
         return v
 
-    def _query(self, q, sinks, n):
-        """The addresses of the queries and sinks."""
-        c = self.cache
-        return (_where(q, "q", _BF, n * self.Hq * c.D, c._index),
-                None if sinks is None else _where(sinks, "sinks", _F32, self.Hq, c._index))
-
-    def _attend(self, prm, q, sinks, o, lse, stream):
-        c = self.cache
-        B_.run_on(c._index, stream, self._decode, "usp_attn_decode", ctypes.byref(prm), self.Hq, self.window_left,
-                  self.softmax_scale, sinks, q, o.data_ptr(), lse.data_ptr(), self._ws.data_ptr(), self._ws_bytes, c._status)
-        self.lse = lse
-        return o
-
     def forward(self, q, block_table, lens, sinks=None, stream=None):
         """q bf16 ``[P][sequences][Hq/P][D]``, already turned -> O of the same shape (and ``self.lse``)."""
-        prm = self.cache._struct(block_table, lens)
-        o, lse = self._out(prm.n_seqs)
-        return self._attend(prm, *self._query(q, sinks, prm.n_seqs), o, lse, stream)
+        c = self.cache
+        index = c._index
+        prm = c._struct(block_table, lens)
+        n = prm.n_seqs
+        o, lse = self._out(n)
+        B_.run_on(index, stream, self._decode, "usp_attn_decode", ctypes.byref(prm), self.Hq, self.window_left,
+                  self.softmax_scale, None if sinks is None else _where(sinks, "sinks", _F32, self.Hq, index),
+                  _where(q, "q", _BF, n * self.Hq * c.D, index), o.data_ptr(), lse.data_ptr(), self._ws.data_ptr(),
+                  self._ws_bytes, c._status)
+        self.lse = lse
+        return o
 
     def _check_attend(self, prm, q, sinks, o, lse):
         """What the library refuses of the attention, by addresses, before the step's tokens are in the pool."""
@@ -229,7 +224,8 @@ class DecodeAttention:
         n = prm.n_seqs
         o, lse = self._out(n)
         rows = n * c.P * c.hk * c.D
-        qp, sp = self._query(q, sinks, n)
+        qp = _where(q, "q", _BF, n * self.Hq * c.D, index)
+        sp = None if sinks is None else _where(sinks, "sinks", _F32, self.Hq, index)
         kp, vp = _where(k, "k", _BF, rows, index), _where(v, "v", _BF, rows, index)
         if self.rope is None:
             self._check_attend(prm, qp, sp, o, lse)
@@ -241,7 +237,10 @@ class DecodeAttention:
             self._check_attend(prm, qp, sp, o, lse)
             self.rope.forward(q, k, positions, out=out, stream=stream)
         B_.run_on(index, stream, c._append, "usp_cache_append", ctypes.byref(prm), kp, vp, n, None, c._status)
-        return self._attend(prm, qp, sp, o, lse, stream)
+        B_.run_on(index, stream, self._decode, "usp_attn_decode", ctypes.byref(prm), self.Hq, self.window_left,
+                  self.softmax_scale, sp, qp, o.data_ptr(), lse.data_ptr(), self._ws.data_ptr(), self._ws_bytes, c._status)
+        self.lse = lse
+        return o
 
     def read_status(self) -> int:
         return self.cache.read_status() or (0 if self.rope is None else self.rope.read_status())
