@@ -125,3 +125,31 @@ def test_scores_and_values_that_make_up_for_one_another():
     c.append(k, v, table, ln, _cu(lens))
     att.forward(q, table, ln, z)
     _check(c, lens, k, v, q, z, att)
+
+
+@pytest.mark.parametrize("e", ["any", 120, -120, 0])
+def test_teams_of_warps_of_long_rows(e):
+    """Rows of 128 bytes: two warps share a ring, and go through a unit once more together (e = 0: they do not)."""
+    lens = [120001, 300]
+    exps = np.random.default_rng(1).integers(-120, 121, sum(lens)) if e == "any" else [e] * sum(lens)
+    c, table, ln, k, v, q, z, att = _case(lens, 16, 4, 128, exps, seed=3, sinks=True)
+    assert sum(-(-n // 16) for n in lens) * 4 >= 32 * 152 * 6       # (tiles of a team)
+    o = att.forward(q, table, ln, z).clone()
+    lse = att.lse.clone()
+    assert att.read_status() == 0 and not att._ws[:12 * 1024].any()
+    _check(c, lens, k, v, q, z, att, heads=9)
+    assert torch.equal(att.forward(q, table, ln, z), o) and torch.equal(att.lse, lse)
+
+
+def test_one_warp_of_a_team_finds_values_that_are_far():
+    """Heads 0 to 7 of a group see only ordinary values, heads 8 to 15 large ones: both of its warps go once more."""
+    lens = [120001]
+    e = np.zeros(lens[0])
+    e[::2] = 100
+    c, table, ln, k, v, q, z, att = _case(lens, 16, 4, 128, e, seed=4)
+    k[0, ::2, :, 0], k[0, 1::2, :, 0] = -60.0, 0.0
+    q[..., 0] = torch.tensor([64.0] * 8 + [0.0] * 8, dtype=BF).repeat(4).cuda()   # 2^-490 for every second token
+    c.append(k, v, table, ln, _cu(lens))
+    att.forward(q, table, ln, z)
+    assert att.read_status() == 0
+    _check(c, lens, k, v, q, z, att, heads=5)

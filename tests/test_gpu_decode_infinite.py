@@ -134,3 +134,25 @@ def test_scores_above_all_others_stay_in_their_head(dtype):
         rel = 2 * ds + (2.0 ** -16 if dtype is BF else 2.0 ** -11) + 100 * 2.0 ** -23 + 2.0 ** -20
         assert (np.abs(o[0, s, h].numpy() - want) <= 2.0 ** -8 * np.abs(want) + (1 + 2.0 ** -8) * rel * size).all()
         assert abs(float(lse[0, s, h]) - wl) <= ds + 2.0 ** -21 * (1 + abs(wl)) + 100 * 2.0 ** -23
+
+
+def test_teams_of_warps_of_8_bit_rows():
+    lens = [120001, 300]
+    off = np.random.default_rng(5).random((2, 7501)) < 0.5
+    hidden = _tiles(lens, lambda s, t: off[s, t])
+    c, table, ln, k, v, q, z, att = _case(lens, 16, 4, 128, F8, hidden, seed=6)
+    att.forward(q, table, ln, z)
+    assert att.read_status() == 0
+    _check(c, lens, k, v, q, z, att, hidden, heads=9)
+
+
+def test_an_infinite_value_stays_in_its_element():
+    lens = [300, 40]
+    c, table, ln, k, v, q, z, att = _decode_case(lens, 4, 1, 64, 1, 64, BF, seed=8)
+    want, lse = att.forward(q, table, ln, z).clone(), att.lse.clone()
+    v[0, 5, 0, 9], v[0, 320, 0, 33] = float("inf"), float("-inf")
+    c.append(k, v, table, ln, _cu(lens))
+    o = att.forward(q, table, ln, z)
+    odd = torch.zeros_like(o, dtype=torch.bool)
+    odd[:, 0, :, 9] = odd[:, 1, :, 33] = True
+    assert not o[odd].isfinite().any() and torch.equal(o[~odd], want[~odd]) and torch.equal(att.lse, lse)

@@ -67,10 +67,14 @@ constexpr int kFan = 48;            // parts that a CTA puts together at once
 // units to the CTAs 23.4, to the warps 26.8.)
 constexpr int kWarpsTiles = 3, kCtasTiles = 8;
 constexpr int kHeads = 8;           // query heads of a warp
-// Groups of more than 8 query heads: teams of two warps where each team of the grid would have this many tiles, else a unit
-// for each 8 heads.  (us, as teams and as units of 8, D 128: 32 sequences of 8000, 8 groups of 16 heads, bf16 173, 305, e4m3
-// 119, 165; of 2000, bf16 55, 85; of 1000, 26 tiles a team: 29.7, 29.5; one of 32768, 4 groups, 14 tiles: 28.5, 20.5; of
-// 131072, 54 tiles: 59, 82; e4m3, 36 tiles: 51, 49.  Teams of four for 32 heads a group were slower than two of two.)
+// Groups of more than 8 query heads: teams of two warps where each team of the grid would have this many tiles and a
+// token's row has 128 bytes or more, else a unit for each 8 heads.  (us, as teams / as units of 8; groups of 16 heads.
+// bf16, D 128: 32 sequences of 8000, 8 groups 172 / 305; of 2000, 53 tiles a team, 56 / 86; 8 of 4000, 26 tiles, 36 / 27; one of
+// 131072, 4 groups, 54 tiles, 61 / 82.  D 64: 32 of 2000, 35 tiles, 35 / 46; 16 of 4000, 35 tiles, 35.3 / 33.6; 8 of 4000, 18
+// tiles, 26 / 18.  e4m3, D 128: 32 of 8000 121 / 165; of 2000, 35 tiles, 45 / 50; one of 131072, 36 tiles, 54 / 49; of 262144,
+// 72 tiles, 80 / 88.  e4m3, D 64, whose codes are converted once a warp and bound it: 32 of 2000, 26 tiles, 33 / 31; of 4000,
+// 53 tiles, 54 / 48; of 16000, 211 tiles, 163 / 167; 4 of 262144, 431 tiles, 317 / 289: no teams.  Teams of four for 32
+// heads a group were slower than two of two.)
 constexpr int kTeamTiles = 32;
 constexpr int kMaxCtas = 1024, kTicketBytes = kMaxCtas * 12;
 // A column's reference may stay this far (log2) below a weight; e4m3: weights of the products go into f16 kUp higher
@@ -1093,15 +1097,18 @@ int launch(const Args& a, int ctas, cudaStream_t st) {
 
 template <int D, bool kE4m3>
 int launch_team(const Args& a, int warps, int ctas, cudaStream_t st) {
-  return warps == 1 ? launch<D, kE4m3, 1>(a, ctas, st) : launch<D, kE4m3, 2>(a, ctas, st);
+  if constexpr (Cfg<D, kE4m3>::kRow >= 128) {
+    if (warps == 2) return launch<D, kE4m3, 2>(a, ctas, st);
+  }
+  return launch<D, kE4m3, 1>(a, ctas, st);
 }
 
 int grid_of() { return std::min(kMaxCtas, device_sm_count()); }
 
-// Warps of a team, 8 query heads each.
+// Warps of a team, 8 query heads each (see kTeamTiles).
 int team_of(const usp_paged_cache& c, int Hq) {
-  const int G = Hq / std::max(c.P, c.Hkv);
-  return G <= kHeads ? 1 : 2;
+  const int G = Hq / std::max(c.P, c.Hkv), row = c.D * (c.dtype == USP_CACHE_E4M3 ? 1 : 2);
+  return G <= kHeads || row < 128 ? 1 : 2;
 }
 
 }  // namespace decode
