@@ -532,7 +532,7 @@ int usp_rope_bwd(const usp_rope_params* params, const void* dq_out, const void* 
  * With dtype USP_CACHE_E4M3 a token's head has a power of two 2^e, the smallest
  * with e >= -126 for which every |x| <= 448 2^e (an infinity counts as the largest
  * finite bf16), stored as the byte e + 127 (1 to 247), and its elements are x / 2^e rounded to
- * the nearest e4m3 value (ties to even).  NaN stays NaN.
+ * the nearest e4m3 value (ties to even; an infinity is held as 448 2^120).  NaN stays NaN.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int P, Hkv, D;              /* global key/value heads; D 64 or 128 */
@@ -556,8 +556,9 @@ enum { USP_CACHE_BF16 = 0, USP_CACHE_E4M3 = 1 };
  * an empty place of a padded batch, is passed over).  Nothing else in the pool changes.  Pages that two
  * sequences share may be read by both but not written in one call.
  * usp_cache_read is the way back: the same tokens out of the cache into k and v, rounded to bf16 (exact for a
- * bf16 cache; e4m3 values times their power of two are rounded only below bf16's normal range).  Tokens that
- * are not described (behind cu[n_seqs], or of an empty place) are left as they were.
+ * bf16 cache; e4m3 values times their power of two are rounded only below bf16's normal range, and infinite from
+ * 2^128 on, where |x| >= 248 2^120 has gone).  Tokens that are not described
+ * (behind cu[n_seqs], or of an empty place) are left as they were.
  * Either of k and v may be NULL, when it is not wanted.  Neither may overlap the cache's arrays, nor, when read, the
  * other or cu_seqlens.
  * dev_status: USP_ERR_BAD_PAGES; tokens without a place in the pool are passed over.
@@ -575,6 +576,12 @@ int usp_cache_read(const usp_paged_cache* cache, void* k, void* v, int tokens, c
  * O = 0 where nothing is visible (LSE = -inf, or the sink).
  * q, o: bf16 [P][n_seqs][Hq/P][D]; lse: fp32 [P][n_seqs][Hq/P]; sinks: fp32 [Hq] or NULL.  What is written
  * (o, lse, ws) may overlap nothing else of the call.
+ * Products, sums and partial results are fp32.  For the products with the values a weight is rounded to 16 bits over a
+ * bf16 cache, to 11 over an e4m3 one (their sum in the LSE is of unrounded weights); over an e4m3 one q is scaled by a
+ * power of two into f16, which takes elements below 2^-39 of a head's largest for 0.  A score of -inf has no weight, one
+ * of +inf or NaN (also where q and k are so large that fp32 does not hold their product) leaves a head no finite output.
+ * A visible value that is not finite leaves its element of O none (over a bf16 cache it may be NaN for an infinity).  Over a
+ * bf16 cache values are summed before they are divided: |v| 2^8 lens[s] has to stay below 2^128.
  * The work of all sequences is dealt out evenly in pieces of 16 positions, whatever their lengths, and pieces
  * of one sequence are joined in the order of their positions: the result does not depend on timing (on the other
  * sequences' lengths it does, within its roundings).

@@ -8,8 +8,9 @@
 // A power of two as the scale: x / 2^e and its way back are exact, so the one rounding
 // is that to e4m3, and the attention moves the scale from the elements to the scores.
 //
-// Measured (one GB300): 31153 tokens of 8 heads, D 128, into e4m3 pages 29.2 us (floor at 6.69 TB/s 28.7); 25478 of
-// them back 24.4 us (23.5); 7400 tokens of 8 heads, D 64, bf16 4.6 us (4.5); one token of 64 sequences 1.9 us.
+// Measured (one GB300, several states in turn, larger than L2 together): 31153 tokens of 8 heads, D 128, into e4m3 pages
+// 30.1 us (floor at 6.69 TB/s 28.7); 25478 of them back 26.2 us (23.5); 7400 tokens of 8 heads, D 64, bf16 6.6 us (4.5); one
+// token of 64 sequences 1.8 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

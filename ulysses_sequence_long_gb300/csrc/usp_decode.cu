@@ -21,8 +21,11 @@
 // pieces of its rows.  A warp copies its own 16 rows into shared memory (cp.async, 512 consecutive bytes an
 // instruction, tiles ahead) and no barrier but the warp's own is needed; only the pairs of positions that V^T's
 // operands want next to each other are interleaved, by byte permutations.  Copying each thread's own pieces, in
-// segments of 64 bytes of a K row, kept loads at 5.2 TB/s, consecutive rows at 7.0.  (Matrix instructions with operands
-// from shared memory and results in tensor memory want 64 rows of queries; here there are G.)
+// segments of 64 bytes of a K row, kept loads at 5.2 TB/s, consecutive rows at 7.0.
+// (The matrix instruction with operands in shared memory and results in tensor memory takes this arrangement too,
+// positions as its 64 or 128 rows and 8 heads or more as columns.  Up to 8 heads a group it has nothing to give: HBM
+// bounds them, with the tensor pipe 12% busy.  Larger groups are bound by instructions here; it is not tried for them:
+// weights would go through shared or tensor memory, and e4m3 codes be made f16 first, or weights and queries 8 bits.)
 //
 // e4m3: an element is exactly an f16, so products run in f16; a token's scales are powers of two
 // and act on its score (keys) and on its weight (values).  The reference M of a column is near the maximum of
@@ -32,16 +35,17 @@
 // The same reference would flush the sum of the weights 2^(s - M) where values are near the largest bf16, and the
 // products' weights where they are near the smallest: a unit whose sum shows that goes through the warp once more, its
 // references near the scores' maximum and those of the products' weights kept beside them.  (That look at the sums costs
-// groups of 16 heads 1.7%; finding such values on the way, in one pass for all, 4 to 8%.)
+// groups of 16 heads 1.9%, up to 6% of them over one sequence, 0.4 us of the smallest calls and 1% of others; finding such
+// values on the way, in one pass for all, 4 to 8% of 16 heads.)
 // bf16: the weights are rounded to bf16 in two parts (high and the rest), 16 bits of them in all: one part alone would
 // make the output's error 1.4 times that of its own rounding.
 //
-// Measured (one GB300, inputs larger than L2 or three of them in turn; the floor is the cache's visible bytes at the
-// measured copy rate of 6.69 TB/s): 32 sequences of up to 8192, 32/8 heads, D 128, bf16: 108 us, floor 104; one of
-// 131072, 28/4 heads, e4m3: 31 us, floor 20; windows of 128 over 256 sequences, 64/8 heads, D 64, bf16: 14.6 us,
-// floor 8.7; one of 500: 7 us.  What is above the floor is the begin (lengths, table and first rows: a chain of loads, 2 us)
-// and the end (a sum over the warps, a ticket, the parts of other CTAs: round trips that wait behind the loads of the SMs
-// that still work, 3 to 6 us).
+// Measured (one GB300, the GPU's time in a captured graph of calls on several states in turn, larger than L2 together; the
+// floor is the cache's visible bytes at the measured copy rate of 6.69 TB/s): 32 sequences of up to 8192, 32/8 heads, D
+// 128, bf16: 109 us, floor 104; one of 131072, 28/4 heads, e4m3: 32 to 33 us, floor 20; windows of 128 over 256 sequences,
+// 64/8 heads, D 64, bf16: 15.1 us, floor 8.7; one of 500: 7.3 us.  What is above the floor is the begin (lengths, table
+// and first rows: a chain of loads, 2 us) and the end (a sum over the warps, a ticket, the parts of other CTAs: round trips
+// that wait behind the loads of the SMs that still work, 3 to 6 us).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -62,9 +66,10 @@ using paged::kTile;
 static_assert(kTile == 16, "the rows of a matrix instruction");
 constexpr int kFan = 48;            // parts that a CTA puts together at once
 // Tiles that a warp works through in the time that putting a CTA's parts together takes, and joining those of CTAs too.
-// (us; 8 heads, D 128, bf16.  64 sequences of up to 100 tokens: tiles to the warps 10.5, units to the warps 8.2; 8 of up to
-// 200: tiles 8.4, units to the CTAs 5.8, to the warps 11.5; 16 of 1000: 12.7, 10.1; 200 of up to 500, D 64, e4m3: 22.9,
-// units to the CTAs 23.4, to the warps 26.8.)
+// (us, of one state, which L2 holds; 8 heads, D 128, bf16 unless stated: the rule counts tiles, whatever their bytes.  64
+// sequences of up to 100 tokens: tiles to the warps 10.5, units to the warps 8.2; 8 of up to 200: tiles 8.4, units to the
+// CTAs 5.8, to the warps 11.5; 16 of 1000: 12.7, 10.1; 200 of up to 500, D 64, e4m3: 22.9, units to the CTAs 23.4, to the
+// warps 26.8.)
 constexpr int kWarpsTiles = 3, kCtasTiles = 8;
 constexpr int kHeads = 8;           // query heads of a warp
 // Groups of more than 8 query heads: teams of two warps where each team of the grid would have this many tiles and a

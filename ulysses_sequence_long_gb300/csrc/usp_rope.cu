@@ -10,8 +10,9 @@
 // to 64 bits, by integers); position * F modulo 2^64 then drops the whole turns exactly,
 // where an fp32 product has no digits behind the point left for far positions.
 //
-// Measured (one GB300): 32768 tokens, 32 + 8 heads, D 128, forward and backward 197 us (6.8 TB/s); 3000 tokens, 12 + 12
-// heads, D 64, half of each head turned: 3.5 us a pass (floor 2.8); one token of four sequences: 2.5 us.
+// Measured (one GB300, several states in turn, larger than L2 together): 32768 tokens, 32 + 8 heads, D 128, forward and
+// backward 197 us (6.8 TB/s); 3000 tokens, 12 + 12 heads, D 64, half of each head turned: 5.2 us a pass (floor 2.8; 3.5
+// where L2 has them); one token of four sequences: 2.3 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
