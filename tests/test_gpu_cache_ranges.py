@@ -16,7 +16,7 @@ def _lib():
     built_lib()
 
 
-def _check(c, lens, k, v, q, z, att, heads=1):
+def _check(c, lens, k, v, q, z, att, heads=1, only=None):
     """Bounds as for values around 1: a score's fp32 sum of D products (2 D 2^-24 of their sizes' sum) and 2^-20, twice that
     for a weight, 2^-11 for its rounding to f16, n 2^-23 for a sum of n, 2^-8 for the output's rounding.  Beside them the
     references' difference, up to 2^8, which scales the values' sum with an error of a few 2^-17 (four roundings of half a
@@ -27,7 +27,7 @@ def _check(c, lens, k, v, q, z, att, heads=1):
     o, lse = att._out(len(lens))
     o, lse = o.double().cpu().numpy()[0], lse.double().cpu().numpy()[0]
     begin = np.cumsum([0] + list(lens))
-    for s in range(len(lens)):
+    for s in range(len(lens)) if only is None else only:
         for h in range(0, qs.shape[1], heads):
             kk, vv = ks[begin[s]:begin[s + 1], h // G], vs[begin[s]:begin[s + 1], h // G]
             want, wl, size, qk = OS.decode(qs[s, h], kk, vv, 1 / np.sqrt(D), None if zz is None else zz[h])
@@ -153,3 +153,24 @@ def test_one_warp_of_a_team_finds_values_that_are_far():
     att.forward(q, table, ln, z)
     assert att.read_status() == 0
     _check(c, lens, k, v, q, z, att, heads=5)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,G", [([40, 0, 90, 17, 1] * 120, 3), ([300] * 100, 2), ([1000, 30] * 30, 5),
+                                    ([310, 33, 0, 2001] * 40, 16)], ids=["short", "middle", "ragged", "groups"])
+def test_some_sequences_of_a_warp(lens, G, D):
+    """Sequences with values far from 1 between others: a warp, or team, that goes through one once more has others before
+    and behind it, on every way to deal them out.  The others are what they are among sequences of ordinary values."""
+    kind = np.arange(len(lens)) % 4
+    e = np.concatenate([np.full(n, (0, 115, 0, -115)[k]) for n, k in zip(lens, kind)])
+    hkv = 4 if G == 16 else 2
+    c, table, ln, k, v, q, z, att = _decode_case(lens, G, hkv, D, 1, 64, F8, seed=9, sinks=True)
+    o, lse = att.forward(q, table, ln, z).clone(), att.lse.clone()
+    v = (v.double() * torch.exp2(torch.from_numpy(e.astype(float)).cuda())[None, :, None, None]).to(BF)
+    c.append(k, v, table, ln, _cu(lens))
+    att.forward(q, table, ln, z)
+    assert att.read_status() == 0
+    same = torch.from_numpy(kind % 2 == 0).cuda()
+    assert torch.equal(att._out(len(lens))[0][:, same], o[:, same]) and torch.equal(att.lse[:, same], lse[:, same])
+    only = [s for s in range(len(lens)) if s % 4 != 0][::1 + len(lens) // 40]
+    _check(c, lens, k, v, q, z, att, only=only)

@@ -122,7 +122,8 @@ class PagedCache:
     def append(self, k, v, block_table, lens, cu_seqlens=None, stream=None):
         """Write the last tokens of each sequence: k, v bf16 ``[P][tokens][heads of a rank][D]`` (head layout), tokens
         ``[cu_seqlens[s], cu_seqlens[s+1])`` of sequence s, or one of each sequence without ``cu_seqlens``.
-        A layer that ran a packed batch has these in ``head_kv()`` and ``cu_seqlens``."""
+        A layer that ran a packed batch has these in ``head_kv()`` and ``cu_seqlens``; ``block_table`` and ``lens`` have a
+        row for each of its first documents then, but none beyond its last (where its ``cu_seqlens`` hold nothing)."""
         self._move(self._append, "usp_cache_append", k, v, block_table, lens, cu_seqlens, stream)
 
     def read(self, block_table, lens, cu_seqlens=None, out=None, tokens: Optional[int] = None, stream=None):
