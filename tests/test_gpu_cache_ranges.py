@@ -174,3 +174,27 @@ def test_some_sequences_of_a_warp(lens, G, D):
     assert torch.equal(att._out(len(lens))[0][:, same], o[:, same]) and torch.equal(att.lse[:, same], lse[:, same])
     only = [s for s in range(len(lens)) if s % 4 != 0][::1 + len(lens) // 40]
     _check(c, lens, k, v, q, z, att, only=only)
+
+
+@pytest.mark.parametrize("window", [0, 20, 300])
+@pytest.mark.parametrize("e", [-118, 110])
+def test_windows(window, e):
+    """What a window hides and what lies behind a sequence's end (scales of 2^128 among them) moves no reference."""
+    lens = [400, 16, 0, 33, 1, 700] * 20
+    exps = np.where(np.arange(sum(lens)) % 3 == 0, 0, e)
+    c, table, ln, k, v, q, z, att = _case(lens, 3, 2, 64, exps, seed=11, window=window, sinks=True)
+    for s, m in enumerate(lens):        # (again: the values were appended anew)
+        for t in range(0, max(0, m - 1 - window)):
+            pg = int(table[s, t // 64])
+            for x in (c.k_pages, c.v_pages):
+                x.view(torch.uint8)[:, pg, :, t % 64] = 255
+            c.k_scales[:, pg, :, t % 64] = c.v_scales[:, pg, :, t % 64] = 255
+        if s == 5:
+            break
+    att.forward(q, table, ln, z)
+    assert att.read_status() == 0
+    begin = np.cumsum([0] + lens)
+    seen = [np.arange(max(0, m - 1 - window), m) for m in lens[:6]]
+    kk = torch.cat([k[:, begin[s] + torch.from_numpy(t).cuda()] for s, t in enumerate(seen)], 1)
+    vv = torch.cat([v[:, begin[s] + torch.from_numpy(t).cuda()] for s, t in enumerate(seen)], 1)
+    _check(c, [len(t) for t in seen], kk, vv, q[:, :6], z, att)
